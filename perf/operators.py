@@ -468,15 +468,14 @@ def work(case):
             return {"bytes": 2 * live * h + 2 * v * h + teacher + 4 * r * k,
                     "flops": 2 * live * h * v}
         return {"bytes": 2 * live * h + 2 * r * h + 4 * v * h + teacher, "flops": 6 * live * h * v}
-    v = case["vocab"]
-    tensors = 2 if op == "process_fwd" else 3
+    v = case["vocab"]   # forward: logits and results; backward: both gradients (logits at few ids)
     if case["shared"]:
         tokens = case["history"] + r
     else:
         tokens = 0.625 * case["history"] * r
     grammar = (max(1, r // 2) * ((v + 31) // 32) * 4 + 4 * r) if case["grammar"] else 0
     biases = 8 * case["biases"] * r if op == "process_fwd" else 0
-    return {"bytes": tensors * r * v * b + 4 * tokens + 36 * r + grammar + biases,
+    return {"bytes": 2 * r * v * b + 4 * tokens + 36 * r + grammar + biases,
             "flops": 2 * r * v}
 
 
