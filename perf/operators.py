@@ -296,7 +296,7 @@ def _plain_lse(z):
 def _plain_loss(s, z):
     p, logp, live = _plain_teacher(s)
     lse = _plain_lse(z)
-    zt = torch.gather(z, 1, s["ids"].long())
+    zt = torch.where(live, torch.gather(z, 1, s["ids"].long()), 0.0)   # absent entries: 0
     loss = (p * torch.where(live, logp - (zt - lse[:, None]), 0.0)).sum(1)
     if s["mask"] is not None:
         on = s["mask"] != 0
@@ -516,7 +516,7 @@ def _exact_rows(s, z, g, lse_given, tau):
         q = torch.exp(z - use.unsqueeze(1))
         onehots = torch.zeros_like(z).scatter_add_(1, ids, p)
         dz = (p.sum(1, keepdim=True) * q - onehots) * (g / tau).unsqueeze(1)
-    return loss, lse, zt, dz
+    return loss, lse, torch.where(torch.isneginf(a), 0.0, zt), dz
 
 
 def _part(s, rows, names):
