@@ -26,6 +26,13 @@ __all__ = [
     "lmhead_selftest_bounded_wait", "lmhead_logps_fwd_shard", "lmhead_logps_bwd_shard",
     "lmhead_combine_shards",
     "forward", "backward",
+    "LMHEAD_F32", "LMHEAD_BF16", "LMHEAD_F16",
+    "lmhead_distill_workspace_size", "lmhead_distill_fwd", "lmhead_distill_bwd",
+    "lmhead_distill_logits_fwd", "lmhead_distill_logits_bwd",
+    "lmhead_layernorm_workspace_size", "lmhead_layernorm_fwd", "lmhead_layernorm_bwd",
+    "lmhead_process_logits_fwd", "lmhead_process_logits_bwd",
+    "distill_forward", "distill_backward", "distill_logits_forward", "distill_logits_backward",
+    "layernorm_forward", "layernorm_backward", "process_logits", "process_logits_backward",
 ]
 
 LMHEAD_OP_FWD = 0
@@ -34,6 +41,9 @@ LMHEAD_OP_FWD_BWD = 2
 LMHEAD_STRATEGY_AUTO = 0
 LMHEAD_STRATEGY_RECOMPUTE = 1
 LMHEAD_STRATEGY_KEEP_LOGITS = 2
+LMHEAD_F32 = 0
+LMHEAD_BF16 = 1
+LMHEAD_F16 = 2
 NOALLOC_SCRATCH_BYTES = 64 << 20   # LMHEAD_NOALLOC_SCRATCH_BYTES in include/lmhead.h
 STATUS_NAMES = {
     0: "LMHEAD_OK", 1: "LMHEAD_ERR_INVALID_ARG", 2: "LMHEAD_ERR_UNSUPPORTED",
@@ -87,6 +97,32 @@ _SIGNATURES = {
     "lmhead_logps_bwd_shard": (ctypes.c_int, [_VP, _VP, _VP, _VP, _I64, _I32, _I32, _I32, _I32,
                                               ctypes.c_float, _I32, _VP, _VP, _VP, _VP, _VP, _VP,
                                               ctypes.c_int, _VP, _SZ, _VP]),
+    "lmhead_distill_workspace_size": (_SZ, [ctypes.c_int, _I64, _I32, _I32, _I32, _I32]),
+    "lmhead_distill_fwd": (ctypes.c_int, [_VP, _VP, _VP, _VP, _VP, _VP, _I64, _I32, _I32, _I32,
+                                          ctypes.c_float, ctypes.c_float, _I32, _VP, _VP, _VP,
+                                          _VP, _SZ, _VP]),
+    "lmhead_distill_bwd": (ctypes.c_int, [_VP, _VP, _VP, _VP, _VP, _VP, _I64, _I32, _I32, _I32,
+                                          ctypes.c_float, ctypes.c_float, _I32, _VP, _VP, _VP,
+                                          _VP, _VP, ctypes.c_int, _VP, _SZ, _VP]),
+    "lmhead_distill_logits_fwd": (ctypes.c_int, [_VP, ctypes.c_int, _I64, _VP, _VP, _VP, _VP, _I64,
+                                                 _I32, _I32, ctypes.c_float, ctypes.c_float, _VP,
+                                                 _VP, _VP]),
+    "lmhead_distill_logits_bwd": (ctypes.c_int, [_VP, ctypes.c_int, _I64, _VP, _VP, _VP, _VP, _I64,
+                                                 _I32, _I32, ctypes.c_float, ctypes.c_float, _VP,
+                                                 _VP, _VP, _I64, _VP]),
+    "lmhead_layernorm_workspace_size": (_SZ, [_I64, _I32]),
+    "lmhead_layernorm_fwd": (ctypes.c_int, [_VP, ctypes.c_int, _I64, _VP, _VP, ctypes.c_int, _I64,
+                                            _I32, ctypes.c_float, _VP, ctypes.c_int, _I64, _VP,
+                                            _VP, _VP]),
+    "lmhead_layernorm_bwd": (ctypes.c_int, [_VP, ctypes.c_int, _I64, _VP, ctypes.c_int, _I64, _VP,
+                                            ctypes.c_int, _VP, _VP, _I64, _I32, _VP, _I64, _VP,
+                                            _VP, ctypes.c_int, _VP, _SZ, _VP]),
+    "lmhead_process_logits_fwd": (ctypes.c_int, [_VP, ctypes.c_int, _I64, _I64, _I32, _VP, _I64,
+                                                 _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I64, _VP,
+                                                 _I64, _VP, _VP, _I64, _VP]),
+    "lmhead_process_logits_bwd": (ctypes.c_int, [_VP, _I64, _VP, ctypes.c_int, _I64, _I64, _I32,
+                                                 _VP, _I64, _VP, _VP, _VP, _I64, _VP, _VP, _I64,
+                                                 _VP]),
 }
 
 
@@ -168,6 +204,41 @@ def _on_device(tensors, stream, fn):
 def _check_workspace(ws):
     if ws is None or not ws.is_cuda or not ws.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
+
+
+def _element_types():
+    import torch
+    return {torch.float32: LMHEAD_F32, torch.bfloat16: LMHEAD_BF16, torch.float16: LMHEAD_F16}
+
+
+def _check_rows(t, name, shape, dtypes=None):
+    """A CUDA matrix whose rows are contiguous but may lie further apart than their
+    length; returns (element type, elements between rows)."""
+    if t is None:
+        raise ValueError("%s is required" % name)
+    types = _element_types()
+    if t.dtype not in types or (dtypes is not None and t.dtype not in dtypes):
+        raise TypeError("%s must be %s, got %s" % (name, " or ".join(
+            str(d) for d in (dtypes if dtypes is not None else types)), t.dtype))
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    rows, cols = t.shape
+    ld = t.stride(0) if rows > 1 else max(cols, t.stride(0))
+    if (cols > 1 and t.stride(1) != 1) or ld < cols:
+        raise ValueError("%s must have contiguous rows that do not overlap" % name)
+    return types[t.dtype], ld
+
+
+def _check_teacher(top_ids, top_logits, teacher_lse, loss_mask, T):
+    import torch
+    K = top_ids.shape[1] if top_ids.dim() == 2 else -1
+    _check_tensor(top_ids, "top_ids", torch.int32, (T, K))
+    _check_tensor(top_logits, "top_logits", torch.float32, (T, K))
+    _check_tensor(teacher_lse, "teacher_lse", torch.float32, (T,), allow_none=True)
+    _check_tensor(loss_mask, "loss_mask", torch.uint8, (T,), allow_none=True)
+    return K
 
 
 def lmhead_workspace_size(op, T, H, V, chunk_size):
@@ -383,6 +454,197 @@ def lmhead_logps_bwd_shard(hidden, weight_shard, targets, loss_mask, vocab_offse
         workspace.numel() * workspace.element_size(), _stream(stream))))
 
 
+def lmhead_distill_workspace_size(op, T, H, V, K, chunk_size):
+    return int(library().lmhead_distill_workspace_size(op, T, H, V, K, chunk_size))
+
+
+def lmhead_distill_fwd(hidden, weight, top_ids, top_logits, teacher_lse, loss_mask, temperature,
+                       teacher_temperature, chunk_size, loss, lse, z_top, workspace, stream=None):
+    """C ``lmhead_distill_fwd`` on torch tensors; returns the status code."""
+    import torch
+    T, H = hidden.shape
+    V = weight.shape[0]
+    _check_tensor(hidden, "hidden", torch.bfloat16, (T, H))
+    _check_tensor(weight, "weight", torch.bfloat16, (V, H))
+    K = _check_teacher(top_ids, top_logits, teacher_lse, loss_mask, T)
+    _check_tensor(loss, "loss", torch.float32, (T,))
+    _check_tensor(lse, "lse", torch.float32, (T,))
+    _check_tensor(z_top, "z_top", torch.float32, (T, K))
+    _check_workspace(workspace)
+    tensors = [hidden, weight, top_ids, top_logits, teacher_lse, loss_mask, loss, lse, z_top,
+               workspace]
+    return _on_device(tensors, stream, lambda: int(library().lmhead_distill_fwd(
+        _ptr(hidden), _ptr(weight), _ptr(top_ids), _ptr(top_logits), _ptr(teacher_lse),
+        _ptr(loss_mask), T, H, V, K, float(temperature), float(teacher_temperature),
+        int(chunk_size), _ptr(loss), _ptr(lse), _ptr(z_top), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream))))
+
+
+def lmhead_distill_bwd(hidden, weight, top_ids, top_logits, teacher_lse, loss_mask, temperature,
+                       teacher_temperature, chunk_size, grad_loss, lse, z_top, d_hidden, d_weight,
+                       accumulate_dweight, workspace, stream=None):
+    """C ``lmhead_distill_bwd`` on torch tensors; returns the status code."""
+    import torch
+    T, H = hidden.shape
+    V = weight.shape[0]
+    _check_tensor(hidden, "hidden", torch.bfloat16, (T, H))
+    _check_tensor(weight, "weight", torch.bfloat16, (V, H))
+    K = _check_teacher(top_ids, top_logits, teacher_lse, loss_mask, T)
+    _check_tensor(grad_loss, "grad_loss", torch.float32, (T,))
+    _check_tensor(lse, "lse", torch.float32, (T,))
+    _check_tensor(z_top, "z_top", torch.float32, (T, K))
+    _check_tensor(d_hidden, "d_hidden", torch.float32, (T, H))
+    _check_tensor(d_weight, "d_weight", torch.float32, (V, H))
+    _check_workspace(workspace)
+    tensors = [hidden, weight, top_ids, top_logits, teacher_lse, loss_mask, grad_loss, lse, z_top,
+               d_hidden, d_weight, workspace]
+    return _on_device(tensors, stream, lambda: int(library().lmhead_distill_bwd(
+        _ptr(hidden), _ptr(weight), _ptr(top_ids), _ptr(top_logits), _ptr(teacher_lse),
+        _ptr(loss_mask), T, H, V, K, float(temperature), float(teacher_temperature),
+        int(chunk_size), _ptr(grad_loss), _ptr(lse), _ptr(z_top), _ptr(d_hidden),
+        _ptr(d_weight), int(bool(accumulate_dweight)), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream))))
+
+
+def lmhead_distill_logits_fwd(logits, top_ids, top_logits, teacher_lse, loss_mask, temperature,
+                              teacher_temperature, loss, lse, stream=None):
+    """C ``lmhead_distill_logits_fwd`` on torch tensors; returns the status code."""
+    import torch
+    T, V = logits.shape
+    kind, ld = _check_rows(logits, "logits", (T, V))
+    K = _check_teacher(top_ids, top_logits, teacher_lse, loss_mask, T)
+    _check_tensor(loss, "loss", torch.float32, (T,))
+    _check_tensor(lse, "lse", torch.float32, (T,))
+    tensors = [logits, top_ids, top_logits, teacher_lse, loss_mask, loss, lse]
+    return _on_device(tensors, stream, lambda: int(library().lmhead_distill_logits_fwd(
+        _ptr(logits), kind, ld, _ptr(top_ids), _ptr(top_logits), _ptr(teacher_lse),
+        _ptr(loss_mask), T, V, K, float(temperature), float(teacher_temperature), _ptr(loss),
+        _ptr(lse), _stream(stream))))
+
+
+def lmhead_distill_logits_bwd(logits, top_ids, top_logits, teacher_lse, loss_mask, temperature,
+                              teacher_temperature, grad_loss, lse, d_logits, stream=None):
+    """C ``lmhead_distill_logits_bwd`` on torch tensors; returns the status code."""
+    import torch
+    T, V = logits.shape
+    kind, ld = _check_rows(logits, "logits", (T, V))
+    K = _check_teacher(top_ids, top_logits, teacher_lse, loss_mask, T)
+    _check_tensor(grad_loss, "grad_loss", torch.float32, (T,))
+    _check_tensor(lse, "lse", torch.float32, (T,))
+    _, d_ld = _check_rows(d_logits, "d_logits", (T, V), (logits.dtype,))
+    tensors = [logits, top_ids, top_logits, teacher_lse, loss_mask, grad_loss, lse, d_logits]
+    return _on_device(tensors, stream, lambda: int(library().lmhead_distill_logits_bwd(
+        _ptr(logits), kind, ld, _ptr(top_ids), _ptr(top_logits), _ptr(teacher_lse),
+        _ptr(loss_mask), T, V, K, float(temperature), float(teacher_temperature),
+        _ptr(grad_loss), _ptr(lse), _ptr(d_logits), d_ld, _stream(stream))))
+
+
+def lmhead_layernorm_workspace_size(N, H):
+    return int(library().lmhead_layernorm_workspace_size(N, H))
+
+
+def _check_norm_params(x, weight, bias, H):
+    import torch
+    if weight is None or weight.dtype not in (torch.float32, x.dtype):
+        raise TypeError("weight must be torch.float32 or %s" % x.dtype)
+    _check_tensor(weight, "weight", weight.dtype, (H,))
+    _check_tensor(bias, "bias", weight.dtype, (H,), allow_none=True)
+    return _element_types()[weight.dtype]
+
+
+def lmhead_layernorm_fwd(x, weight, bias, eps, y, mean, rstd, stream=None):
+    """C ``lmhead_layernorm_fwd`` on torch tensors; returns the status code."""
+    import torch
+    N, H = x.shape
+    x_type, x_ld = _check_rows(x, "x", (N, H))
+    param_type = _check_norm_params(x, weight, bias, H)
+    y_type, y_ld = _check_rows(y, "y", (N, H), (x.dtype, torch.bfloat16)
+                               if x.dtype == torch.float32 else (x.dtype,))
+    _check_tensor(mean, "mean", torch.float32, (N,), allow_none=True)
+    _check_tensor(rstd, "rstd", torch.float32, (N,), allow_none=True)
+    return _on_device([x, weight, bias, y, mean, rstd], stream, lambda: int(
+        library().lmhead_layernorm_fwd(
+            _ptr(x), x_type, x_ld, _ptr(weight), _ptr(bias), param_type, N, H, float(eps), _ptr(y),
+            y_type, y_ld, _ptr(mean), _ptr(rstd), _stream(stream))))
+
+
+def lmhead_layernorm_bwd(dy, x, weight, mean, rstd, dx, d_weight, d_bias, accumulate, workspace,
+                         stream=None):
+    """C ``lmhead_layernorm_bwd`` on torch tensors; returns the status code."""
+    import torch
+    N, H = x.shape
+    x_type, x_ld = _check_rows(x, "x", (N, H))
+    dy_type, dy_ld = _check_rows(dy, "dy", (N, H), (torch.float32, torch.bfloat16)
+                                 if x.dtype == torch.float32 else (torch.float32, x.dtype))
+    param_type = _check_norm_params(x, weight, None, H)
+    _check_tensor(mean, "mean", torch.float32, (N,))
+    _check_tensor(rstd, "rstd", torch.float32, (N,))
+    dx_ld = 0 if dx is None else _check_rows(dx, "dx", (N, H), (x.dtype,))[1]
+    _check_tensor(d_weight, "d_weight", torch.float32, (H,), allow_none=True)
+    _check_tensor(d_bias, "d_bias", torch.float32, (H,), allow_none=True)
+    if workspace is not None or d_weight is not None or d_bias is not None:
+        _check_workspace(workspace)
+    tensors = [dy, x, weight, mean, rstd, dx, d_weight, d_bias, workspace]
+    return _on_device(tensors, stream, lambda: int(library().lmhead_layernorm_bwd(
+        _ptr(dy), dy_type, dy_ld, _ptr(x), x_type, x_ld, _ptr(weight), param_type, _ptr(mean),
+        _ptr(rstd), N, H, _ptr(dx), dx_ld, _ptr(d_weight), _ptr(d_bias), int(bool(accumulate)),
+        _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
+        _stream(stream))))
+
+
+def _check_rules(R, V, tokens, spans, repetition, frequency, presence, allowed, allowed_rows):
+    import torch
+    if tokens is not None:
+        _check_tensor(tokens, "tokens", torch.int32, (tokens.numel(),))
+    _check_tensor(spans, "spans", torch.int64, (R, 3), allow_none=True)
+    _check_tensor(repetition, "repetition", torch.float32, (R,), allow_none=True)
+    _check_tensor(frequency, "frequency", torch.float32, (R,), allow_none=True)
+    _check_tensor(presence, "presence", torch.float32, (R,), allow_none=True)
+    if allowed is not None:
+        _check_tensor(allowed, "allowed", torch.int32, (allowed.shape[0], (V + 31) // 32))
+    _check_tensor(allowed_rows, "allowed_rows", torch.int32, (R,), allow_none=True)
+
+
+def lmhead_process_logits_fwd(logits, tokens, spans, repetition, frequency, presence,
+                              bias_offsets, bias_ids, bias_values, allowed, allowed_rows, out,
+                              stream=None):
+    """C ``lmhead_process_logits_fwd`` on torch tensors; returns the status code."""
+    import torch
+    R, V = logits.shape
+    kind, ld = _check_rows(logits, "logits", (R, V))
+    _check_rules(R, V, tokens, spans, repetition, frequency, presence, allowed, allowed_rows)
+    _check_tensor(bias_offsets, "bias_offsets", torch.int64, (R + 1,), allow_none=True)
+    n_bias = 0 if bias_ids is None else bias_ids.numel()
+    _check_tensor(bias_ids, "bias_ids", torch.int32, (n_bias,), allow_none=bias_offsets is None)
+    _check_tensor(bias_values, "bias_values", torch.float32, (n_bias,),
+                  allow_none=bias_offsets is None)
+    _, out_ld = _check_rows(out, "out", (R, V), (logits.dtype,))
+    tensors = [logits, tokens, spans, repetition, frequency, presence, bias_offsets, bias_ids,
+               bias_values, allowed, allowed_rows, out]
+    return _on_device(tensors, stream, lambda: int(library().lmhead_process_logits_fwd(
+        _ptr(logits), kind, ld, R, V, _ptr(tokens), 0 if tokens is None else tokens.numel(),
+        _ptr(spans), _ptr(repetition), _ptr(frequency), _ptr(presence), _ptr(bias_offsets),
+        _ptr(bias_ids), _ptr(bias_values), n_bias, _ptr(allowed),
+        0 if allowed is None else allowed.shape[0], _ptr(allowed_rows), _ptr(out), out_ld,
+        _stream(stream))))
+
+
+def lmhead_process_logits_bwd(grad_out, logits, tokens, spans, repetition, allowed, allowed_rows,
+                              d_logits, stream=None):
+    """C ``lmhead_process_logits_bwd`` on torch tensors; returns the status code."""
+    R, V = logits.shape
+    kind, ld = _check_rows(logits, "logits", (R, V))
+    _, grad_ld = _check_rows(grad_out, "grad_out", (R, V), (logits.dtype,))
+    _check_rules(R, V, tokens, spans, repetition, None, None, allowed, allowed_rows)
+    _, d_ld = _check_rows(d_logits, "d_logits", (R, V), (logits.dtype,))
+    tensors = [grad_out, logits, tokens, spans, repetition, allowed, allowed_rows, d_logits]
+    return _on_device(tensors, stream, lambda: int(library().lmhead_process_logits_bwd(
+        _ptr(grad_out), grad_ld, _ptr(logits), kind, ld, R, V, _ptr(tokens),
+        0 if tokens is None else tokens.numel(), _ptr(spans), _ptr(repetition), _ptr(allowed),
+        0 if allowed is None else allowed.shape[0], _ptr(allowed_rows), _ptr(d_logits), d_ld,
+        _stream(stream))))
+
+
 def lmhead_selftest_bounded_wait(workspace, limit_ms, stream=None):
     """C ``lmhead_selftest_bounded_wait``; returns the status code of the launch."""
     _check_workspace(workspace)
@@ -486,3 +748,150 @@ def backward(hidden, weight, targets, loss_mask, temperature, chunk_size, grad_l
     if rc:
         raise LmheadError(rc, "lmhead_logps_bwd")
     return d_hidden, d_weight
+
+
+def _distill_workspace(op, T, H, V, K, chunk_size, device):
+    import torch
+    n = lmhead_distill_workspace_size(op, T, H, V, K, chunk_size)
+    if n == 0:
+        raise LmheadError(1, "lmhead_distill_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def distill_forward(hidden, weight, top_ids, top_logits, loss_mask=None, temperature=1.0,
+                    teacher_temperature=1.0, chunk_size=512, teacher_lse=None, workspace=None,
+                    stream=None):
+    """Distillation loss through the head.  Returns (loss [T], lse [T], z_top [T, K]), fp32;
+    keep lse and z_top for ``distill_backward``."""
+    import torch
+    T, H = hidden.shape
+    V = weight.shape[0]
+    K = top_ids.shape[1]
+    dev = hidden.device
+    loss = torch.empty(T, dtype=torch.float32, device=dev)
+    lse = torch.empty(T, dtype=torch.float32, device=dev)
+    z_top = torch.empty((T, K), dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = _distill_workspace(LMHEAD_OP_FWD, T, H, V, K, chunk_size, dev)
+    rc = lmhead_distill_fwd(hidden, weight, top_ids, top_logits, teacher_lse, loss_mask,
+                            temperature, teacher_temperature, chunk_size, loss, lse, z_top,
+                            workspace, stream)
+    if rc:
+        raise LmheadError(rc, "lmhead_distill_fwd")
+    return loss, lse, z_top
+
+
+def distill_backward(hidden, weight, top_ids, top_logits, loss_mask, temperature,
+                     teacher_temperature, chunk_size, grad_loss, lse, z_top, teacher_lse=None,
+                     d_weight=None, accumulate_dweight=False, workspace=None, stream=None):
+    """Returns (d_hidden [T, H] fp32, d_weight [V, H] fp32)."""
+    import torch
+    T, H = hidden.shape
+    V = weight.shape[0]
+    dev = hidden.device
+    d_hidden = torch.empty((T, H), dtype=torch.float32, device=dev)
+    if d_weight is None:
+        d_weight = torch.empty((V, H), dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = _distill_workspace(LMHEAD_OP_BWD, T, H, V, top_ids.shape[1], chunk_size, dev)
+    rc = lmhead_distill_bwd(hidden, weight, top_ids, top_logits, teacher_lse, loss_mask,
+                            temperature, teacher_temperature, chunk_size, grad_loss, lse, z_top,
+                            d_hidden, d_weight, accumulate_dweight, workspace, stream)
+    if rc:
+        raise LmheadError(rc, "lmhead_distill_bwd")
+    return d_hidden, d_weight
+
+
+def distill_logits_forward(logits, top_ids, top_logits, loss_mask=None, temperature=1.0,
+                           teacher_temperature=1.0, teacher_lse=None, stream=None):
+    """Distillation loss on held logits [T, V] (fp32, bf16 or fp16, rows may be padded).
+    Returns (loss [T], lse [T]), fp32."""
+    import torch
+    T = logits.shape[0]
+    loss = torch.empty(T, dtype=torch.float32, device=logits.device)
+    lse = torch.empty(T, dtype=torch.float32, device=logits.device)
+    rc = lmhead_distill_logits_fwd(logits, top_ids, top_logits, teacher_lse, loss_mask,
+                                   temperature, teacher_temperature, loss, lse, stream)
+    if rc:
+        raise LmheadError(rc, "lmhead_distill_logits_fwd")
+    return loss, lse
+
+
+def distill_logits_backward(logits, top_ids, top_logits, loss_mask, temperature,
+                            teacher_temperature, grad_loss, lse, teacher_lse=None, d_logits=None,
+                            stream=None):
+    """Returns d_logits [T, V] of the logits' type (``d_logits=logits`` overwrites them)."""
+    import torch
+    if d_logits is None:
+        d_logits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    rc = lmhead_distill_logits_bwd(logits, top_ids, top_logits, teacher_lse, loss_mask,
+                                   temperature, teacher_temperature, grad_loss, lse, d_logits,
+                                   stream)
+    if rc:
+        raise LmheadError(rc, "lmhead_distill_logits_bwd")
+    return d_logits
+
+
+def layernorm_forward(x, weight, bias=None, eps=1e-5, out_dtype=None, stream=None):
+    """Layer norm of x [N, H].  Returns (y [N, H] of x's type or out_dtype, mean [N] fp32,
+    rstd [N] fp32)."""
+    import torch
+    N = x.shape[0]
+    y = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
+    mean = torch.empty(N, dtype=torch.float32, device=x.device)
+    rstd = torch.empty(N, dtype=torch.float32, device=x.device)
+    rc = lmhead_layernorm_fwd(x, weight, bias, eps, y, mean, rstd, stream)
+    if rc:
+        raise LmheadError(rc, "lmhead_layernorm_fwd")
+    return y, mean, rstd
+
+
+def layernorm_backward(dy, x, weight, mean, rstd, with_bias=True, d_weight=None, d_bias=None,
+                       accumulate=False, dx=None, workspace=None, stream=None):
+    """Returns (dx [N, H] of x's type, d_weight [H] fp32, d_bias [H] fp32 or None)."""
+    import torch
+    N, H = x.shape
+    dev = x.device
+    if dx is None:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    if d_weight is None:
+        d_weight = torch.empty(H, dtype=torch.float32, device=dev)
+    if d_bias is None and with_bias:
+        d_bias = torch.empty(H, dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = torch.empty(lmhead_layernorm_workspace_size(N, H), dtype=torch.uint8,
+                                device=dev)
+    rc = lmhead_layernorm_bwd(dy, x, weight, mean, rstd, dx, d_weight, d_bias, accumulate,
+                              workspace, stream)
+    if rc:
+        raise LmheadError(rc, "lmhead_layernorm_bwd")
+    return dx, d_weight, d_bias
+
+
+def process_logits(logits, tokens=None, spans=None, repetition=None, frequency=None,
+                   presence=None, bias_offsets=None, bias_ids=None, bias_values=None,
+                   allowed=None, allowed_rows=None, out=None, stream=None):
+    """Penalties, biases and a grammar mask on logits [R, V]; returns the processed logits
+    (``out=logits`` processes them in place)."""
+    import torch
+    if out is None:
+        out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    rc = lmhead_process_logits_fwd(logits, tokens, spans, repetition, frequency, presence,
+                                   bias_offsets, bias_ids, bias_values, allowed, allowed_rows,
+                                   out, stream)
+    if rc:
+        raise LmheadError(rc, "lmhead_process_logits_fwd")
+    return out
+
+
+def process_logits_backward(grad_out, logits, tokens=None, spans=None, repetition=None,
+                            allowed=None, allowed_rows=None, d_logits=None, stream=None):
+    """Cotangent of the original logits (``d_logits=grad_out`` overwrites the cotangent)."""
+    import torch
+    if d_logits is None:
+        d_logits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    rc = lmhead_process_logits_bwd(grad_out, logits, tokens, spans, repetition, allowed,
+                                   allowed_rows, d_logits, stream)
+    if rc:
+        raise LmheadError(rc, "lmhead_process_logits_bwd")
+    return d_logits

@@ -21,8 +21,11 @@ parameters.
 """
 import torch
 
-from . import LMHEAD_OP_BWD, LMHEAD_OP_FWD, LmheadError, lmhead_logps_bwd, lmhead_logps_fwd, \
-    lmhead_workspace_size
+from . import LMHEAD_OP_BWD, LMHEAD_OP_FWD, LmheadError, distill_logits_backward, \
+    distill_logits_forward, layernorm_backward, layernorm_forward, lmhead_distill_bwd, \
+    lmhead_distill_fwd, lmhead_distill_workspace_size, lmhead_layernorm_workspace_size, \
+    lmhead_logps_bwd, lmhead_logps_fwd, lmhead_workspace_size, process_logits_backward
+from . import process_logits as _process_logits
 
 # (device index, stream handle) -> uint8 workspace, grown on demand.  Work on one
 # stream runs in order, so every call on that stream can reuse one buffer; the
@@ -35,6 +38,10 @@ def _workspace(T, H, V, chunk_size, device):
             lmhead_workspace_size(LMHEAD_OP_BWD, T, H, V, chunk_size))
     if n == 0:
         raise LmheadError(1, "lmhead_workspace_size")
+    return _stream_workspace(n, device)
+
+
+def _stream_workspace(n, device):
     key = (device.index, torch.cuda.current_stream(device).cuda_stream)
     buf = _workspaces.get(key)
     if buf is None or buf.numel() < n:
@@ -111,6 +118,13 @@ def lmhead_logps(hidden, weight, targets, loss_mask=None, temperature=1.0, chunk
     main_grad: an fp32 [V, H] CUDA tensor that the backward adds the weight's
     gradient to (in fp32, in place); defaults to ``weight.main_grad`` when the
     weight has one.  With it, ``weight.grad`` is not produced."""
+    return LMHeadLogps.apply(hidden, weight, targets, loss_mask, float(temperature),
+                             int(chunk_size), _main_grad(weight, main_grad))
+
+
+def _main_grad(weight, main_grad):
+    """The fp32 buffer the weight's gradient is added to: the argument, the weight's own, or
+    None."""
     if main_grad is None:
         main_grad = getattr(weight, "main_grad", None)
     if main_grad is not None:
@@ -119,5 +133,148 @@ def lmhead_logps(hidden, weight, targets, loss_mask=None, temperature=1.0, chunk
                 or not main_grad.is_contiguous() or main_grad.device != weight.device):
             raise ValueError("main_grad must be a contiguous fp32 [V, H] tensor on the "
                              "weight's device")
-    return LMHeadLogps.apply(hidden, weight, targets, loss_mask, float(temperature),
-                             int(chunk_size), main_grad)
+    return main_grad
+
+
+class LMHeadDistill(torch.autograd.Function):
+    """(hidden [T,H] bf16, weight [V,H] bf16, top_ids [T,K] int32, top_logits [T,K] fp32,
+    loss_mask, temperature, teacher_temperature, chunk_size, teacher_lse [T] fp32 or None,
+    main_grad) -> loss [T] fp32."""
+
+    @staticmethod
+    def forward(ctx, hidden, weight, top_ids, top_logits, loss_mask, temperature,
+                teacher_temperature, chunk_size, teacher_lse, main_grad):
+        T, H = hidden.shape
+        V = weight.shape[0]
+        K = top_ids.shape[1]
+        dev = hidden.device
+        loss = torch.empty(T, dtype=torch.float32, device=dev)
+        lse = torch.empty(T, dtype=torch.float32, device=dev)
+        z_top = torch.empty((T, K), dtype=torch.float32, device=dev)
+        sizes = [lmhead_distill_workspace_size(op, T, H, V, K, chunk_size)
+                 for op in (LMHEAD_OP_FWD, LMHEAD_OP_BWD)]
+        if 0 in sizes:
+            raise LmheadError(1, "lmhead_distill_workspace_size")
+        ws = _stream_workspace(max(sizes), dev)
+        rc = lmhead_distill_fwd(hidden, weight, top_ids, top_logits, teacher_lse, loss_mask,
+                                temperature, teacher_temperature, chunk_size, loss, lse, z_top, ws)
+        if rc:
+            raise LmheadError(rc, "lmhead_distill_fwd")
+        ctx.save_for_backward(hidden, weight, top_ids, top_logits, loss_mask, teacher_lse, lse,
+                              z_top)
+        ctx.temperatures = temperature, teacher_temperature
+        ctx.chunk_size = chunk_size
+        ctx.workspace_bytes = max(sizes)
+        ctx.main_grad = main_grad
+        return loss
+
+    @staticmethod
+    def backward(ctx, g_loss):
+        hidden, weight, top_ids, top_logits, loss_mask, teacher_lse, lse, z_top = ctx.saved_tensors
+        need_h, need_w = ctx.needs_input_grad[0], ctx.needs_input_grad[1]
+        if not (need_h or need_w):
+            return (None,) * 10
+        main = ctx.main_grad if need_w else None
+        T, H = hidden.shape
+        V = weight.shape[0]
+        dev = hidden.device
+        d_hidden = torch.empty((T, H), dtype=torch.float32, device=dev)
+        d_weight = main if main is not None else torch.empty((V, H), dtype=torch.float32,
+                                                             device=dev)
+        ws = _stream_workspace(ctx.workspace_bytes, dev)
+        rc = lmhead_distill_bwd(hidden, weight, top_ids, top_logits, teacher_lse, loss_mask,
+                                *ctx.temperatures, ctx.chunk_size,
+                                g_loss.to(torch.float32).contiguous(), lse, z_top, d_hidden,
+                                d_weight, main is not None, ws)
+        if rc:
+            raise LmheadError(rc, "lmhead_distill_bwd")
+        return (d_hidden if need_h else None, d_weight if need_w and main is None else None,
+                *(None,) * 8)
+
+
+def lmhead_distill(hidden, weight, top_ids, top_logits, loss_mask=None, temperature=1.0,
+                   teacher_temperature=1.0, chunk_size=512, teacher_lse=None, main_grad=None):
+    """Per-token distillation loss from a teacher's top logits through the head (the [T, V]
+    logits never exist), differentiable in hidden and weight.  main_grad as in
+    ``lmhead_logps``."""
+    return LMHeadDistill.apply(hidden, weight, top_ids, top_logits, loss_mask, float(temperature),
+                               float(teacher_temperature), int(chunk_size), teacher_lse,
+                               _main_grad(weight, main_grad))
+
+
+class DistillLogits(torch.autograd.Function):
+    """(logits [T,V], top_ids, top_logits, loss_mask, temperature, teacher_temperature,
+    teacher_lse) -> loss [T] fp32."""
+
+    @staticmethod
+    def forward(ctx, logits, top_ids, top_logits, loss_mask, temperature, teacher_temperature,
+                teacher_lse):
+        loss, lse = distill_logits_forward(logits, top_ids, top_logits, loss_mask, temperature,
+                                           teacher_temperature, teacher_lse)
+        ctx.save_for_backward(logits, top_ids, top_logits, loss_mask, teacher_lse, lse)
+        ctx.temperatures = temperature, teacher_temperature
+        return loss
+
+    @staticmethod
+    def backward(ctx, g_loss):
+        logits, top_ids, top_logits, loss_mask, teacher_lse, lse = ctx.saved_tensors
+        d = distill_logits_backward(logits, top_ids, top_logits, loss_mask, *ctx.temperatures,
+                                    g_loss.to(torch.float32).contiguous(), lse, teacher_lse)
+        return (d, *(None,) * 6)
+
+
+def distill_logits(logits, top_ids, top_logits, loss_mask=None, temperature=1.0,
+                   teacher_temperature=1.0, teacher_lse=None):
+    """Per-token distillation loss on held logits, differentiable in the logits."""
+    return DistillLogits.apply(logits, top_ids, top_logits, loss_mask, float(temperature),
+                               float(teacher_temperature), teacher_lse)
+
+
+class LayerNorm(torch.autograd.Function):
+    """(x [N,H], weight [H], bias [H] or None, eps, out_dtype) -> y [N,H]."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps, out_dtype):
+        y, mean, rstd = layernorm_forward(x, weight, bias, eps, out_dtype)
+        ctx.save_for_backward(x, weight, mean, rstd)
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, weight, mean, rstd = ctx.saved_tensors
+        if dy.stride(1) != 1 or (dy.shape[0] > 1 and dy.stride(0) < dy.shape[1]):
+            dy = dy.contiguous()
+        need_b = ctx.needs_input_grad[2]
+        ws = _stream_workspace(lmhead_layernorm_workspace_size(*x.shape), x.device)
+        dx, dw, db = layernorm_backward(dy, x, weight, mean, rstd, with_bias=need_b, workspace=ws)
+        return (dx, dw, db, None, None)
+
+
+def layer_norm(x, weight, bias=None, eps=1e-5, out_dtype=None):
+    """Layer norm of x [N, H] (fp32, bf16 or fp16; out_dtype bf16 for fp32 rows),
+    differentiable in x, weight and bias."""
+    return LayerNorm.apply(x, weight, bias, float(eps), out_dtype)
+
+
+class ProcessLogits(torch.autograd.Function):
+    """(logits [R,V], rules as keyword arguments of ``process_logits``) -> processed [R,V]."""
+
+    @staticmethod
+    def forward(ctx, logits, rules):
+        ctx.save_for_backward(logits)
+        ctx.rules = {k: rules.get(k) for k in ("tokens", "spans", "repetition", "allowed",
+                                               "allowed_rows")}
+        return _process_logits(logits, **rules)
+
+    @staticmethod
+    def backward(ctx, g):
+        logits, = ctx.saved_tensors
+        if g.stride(1) != 1 or (g.shape[0] > 1 and g.stride(0) < g.shape[1]):
+            g = g.contiguous()
+        return process_logits_backward(g, logits, **ctx.rules), None
+
+
+def process_logits(logits, **rules):
+    """``chunked_lm_head_tcgen05_gb300.process_logits`` (the same keyword arguments, without
+    ``out`` and ``stream``), differentiable in the logits."""
+    return ProcessLogits.apply(logits, rules)

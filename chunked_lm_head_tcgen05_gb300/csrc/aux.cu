@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kCompactThreads)
     if (live & (1u << c)) {
       const int t = static_cast<int>(base) + c * kCompactThreads + threadIdx.x;
       const int pos = before + round_warp[c][w] + rank[c];
-      const int y = shard_target(targets[t], v0, Vs, Vt);
+      const int y = targets ? shard_target(targets[t], v0, Vs, Vt) : kTargetElsewhere;
       bad |= y == kTargetInvalid;
       idx[pos] = t;
       y_c[pos] = y;
@@ -166,7 +166,7 @@ __global__ void targets_dense_kernel(const int32_t* __restrict__ targets, int T,
   if (r >= T_alloc) return;
   int y = kTargetInvalid;
   if (r < T) {
-    y = shard_target(targets[r], v0, Vs, Vt);
+    y = targets ? shard_target(targets[r], v0, Vs, Vt) : kTargetElsewhere;
     if (y == kTargetInvalid) atomicCAS(&st->status, 0, STATUS_BAD_TARGET);
   }
   y_c[r] = y;

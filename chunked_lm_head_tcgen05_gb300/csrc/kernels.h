@@ -166,6 +166,7 @@ int compact_chunks(int T);
 // [v0, v0 + Vs) of it (the whole vocabulary: v0 = 0, Vs = Vt).  y_c gets the
 // local row of each scored target, -2 for a valid id held by another
 // vocabulary shard, -1 for an invalid id (which also sets the status word).
+// targets may be NULL: -2 for every scored token (losses without a target).
 cudaError_t launch_compact(const uint8_t* mask, const int32_t* targets, int T, int v0, int Vs,
                            int Vt, int T_alloc, int* counts, int* idx, int* y_c, DeviceState* st,
                            cudaStream_t s);

@@ -15,6 +15,7 @@
 #include <vector>
 
 #include "kernels.h"
+#include "operators.h"
 
 using namespace lmh;
 
@@ -52,26 +53,38 @@ cudaEvent_t pooled_event() {
 
 template <class F>
 cudaError_t launch(const char* name, cudaStream_t s, F&& f) {
-  cudaEvent_t a = nullptr, b = nullptr;
+  return traced_launch(name, s, std::forward<F>(f));
+}
+
+}  // namespace
+
+namespace lmh {
+
+LaunchTrace trace_start(cudaStream_t s) {
+  LaunchTrace t{nullptr, nullptr};
   {
     std::lock_guard<std::mutex> lk(g_prof_mu);
     if (g_prof_on) {
-      a = pooled_event();
-      b = pooled_event();
+      t.start = pooled_event();
+      t.stop = pooled_event();
     }
   }
-  if (a && b) cudaEventRecord(a, s);
-  const cudaError_t e = f();
-  if (a && b) {
-    cudaEventRecord(b, s);
-    std::lock_guard<std::mutex> lk(g_prof_mu);
-    g_prof.push_back({name, a, b});
-  }
-  if (e == cudaSuccess) g_launches.fetch_add(1, std::memory_order_relaxed);
-  return e;
+  if (t.start && t.stop) cudaEventRecord(t.start, s);
+  return t;
 }
 
-// ------------------------------------------------------------------ device facts
+void trace_stop(const char* name, cudaStream_t s, const LaunchTrace& t, bool launched) noexcept {
+  if (t.start && t.stop) {
+    cudaEventRecord(t.stop, s);
+    try {
+      std::lock_guard<std::mutex> lk(g_prof_mu);
+      g_prof.push_back({name, t.start, t.stop});
+    } catch (...) {   // out of host memory: this launch goes unrecorded
+    }
+  }
+  if (launched) g_launches.fetch_add(1, std::memory_order_relaxed);
+}
+
 int sm_count() {
   static std::atomic<int> cache[64];   // per device; 0 = not yet known
   int dev = 0;
@@ -85,6 +98,11 @@ int sm_count() {
   return n;
 }
 
+}  // namespace lmh
+
+namespace {
+
+// ------------------------------------------------------------------ device facts
 // Tiles run on CTA pairs (tcgen05 cta_group::2) unless the environment sets
 // LMHEAD_CTA_PAIR=0 (single-CTA tiles; a diagnostic fallback).
 bool use_pair() {
@@ -558,7 +576,8 @@ lmhead_status fwd_impl(const uint16_t* hidden, const uint16_t* weight, const int
   lmhead_status rc = check_sizes(T, H, V, temperature, chunk_size);
   if (rc != LMHEAD_OK) return rc;
   if (T == 0) return LMHEAD_OK;
-  if (!hidden || !weight || !targets || !workspace || (!shard_part && (!logp || !lse)))
+  // targets may be NULL when only the statistics are wanted (distillation)
+  if (!hidden || !weight || !workspace || (!shard_part && (!targets || !logp || !lse)))
     return LMHEAD_ERR_INVALID_ARG;
   if (!aligned16(hidden) || !aligned16(weight) || (reinterpret_cast<uintptr_t>(workspace) & 255))
     return LMHEAD_ERR_UNSUPPORTED;
@@ -613,16 +632,30 @@ lmhead_status fwd_impl(const uint16_t* hidden, const uint16_t* weight, const int
   return LMHEAD_OK;
 }
 
+// What the distillation backward puts in place of the log-prob / entropy
+// cotangent: the row coefficients come from launch_distill_prep, and each dz
+// block gets the exact cotangents at the teacher's ids before the gradient
+// contractions read it.
+struct DistillCotangent {
+  Teacher teacher;
+  const float* grad_loss;
+  const float* z_top;
+  int32_t* patch_ids;       // workspace [T_alloc, K]
+  uint16_t* patch_values;   // workspace [T_alloc, K]
+};
+
 // Backward over vocabulary rows [v0, v0 + V) of a vocabulary of Vt ids, given
 // the whole vocabulary's lse (and entropy): d_hidden gets these rows' share of
-// the gradient, d_weight the gradient of these rows.
+// the gradient, d_weight the gradient of these rows.  With `distill` (whole
+// vocabulary only) there are no targets, and grad_logp, grad_entropy and
+// entropy are NULL.
 lmhead_status bwd_impl(const uint16_t* hidden, const uint16_t* weight, const int32_t* targets,
                        const uint8_t* loss_mask, int64_t T, int32_t H, int32_t V, int32_t v0,
                        int32_t Vt, float temperature, int32_t chunk_size,
                        const float* grad_logp, const float* grad_entropy, const float* lse,
                        const float* entropy, float* d_hidden, float* d_weight,
-                       int accumulate_dweight, void* workspace, size_t workspace_bytes,
-                       lmhead_stream_t stream) {
+                       int accumulate_dweight, const DistillCotangent* distill, void* workspace,
+                       size_t workspace_bytes, lmhead_stream_t stream) {
   lmhead_status rc = check_sizes(T, H, V, temperature, chunk_size);
   if (rc != LMHEAD_OK) return rc;
   if (!weight || !d_weight) return LMHEAD_ERR_INVALID_ARG;
@@ -634,7 +667,8 @@ lmhead_status bwd_impl(const uint16_t* hidden, const uint16_t* weight, const int
       return LMHEAD_ERR_CUDA;
     return LMHEAD_OK;
   }
-  if (!hidden || !targets || !lse || !d_hidden || !workspace || (grad_entropy && !entropy))
+  if (!hidden || (!targets && !distill) || !lse || !d_hidden || !workspace ||
+      (grad_entropy && !entropy))
     return LMHEAD_ERR_INVALID_ARG;
   if (!aligned16(hidden) || !aligned16(d_hidden) || (reinterpret_cast<uintptr_t>(workspace) & 255))
     return LMHEAD_ERR_UNSUPPORTED;
@@ -650,10 +684,19 @@ lmhead_status bwd_impl(const uint16_t* hidden, const uint16_t* weight, const int
 
   float4* coef = reinterpret_cast<float4*>(ws + L.coef);
   uint16_t* dz = reinterpret_cast<uint16_t*>(ws + L.dz);
-  LMH_TRY(launch("bwd_prep", s, [&] {
-    return launch_bwd_prep(f.idx, f.st, 0, static_cast<int>(f.T_alloc), lse, entropy, grad_logp,
-                           grad_entropy, temperature, coef, s);
-  }));
+  if (distill) {
+    LMH_TRY(launch("distill_prep", s, [&] {
+      return launch_distill_prep(distill->teacher, V, temperature, f.idx,
+                                 static_cast<int>(f.T_alloc), distill->grad_loss, lse,
+                                 distill->z_top, f.st, coef, distill->patch_ids,
+                                 distill->patch_values, s);
+    }));
+  } else {
+    LMH_TRY(launch("bwd_prep", s, [&] {
+      return launch_bwd_prep(f.idx, f.st, 0, static_cast<int>(f.T_alloc), lse, entropy, grad_logp,
+                             grad_entropy, temperature, coef, s);
+    }));
+  }
   if (loss_mask) {
     LMH_TRY(launch("zero_masked_rows", s, [&] {
       return launch_zero_masked_rows(loss_mask, static_cast<int>(T), H, d_hidden, s);
@@ -668,6 +711,7 @@ lmhead_status bwd_impl(const uint16_t* hidden, const uint16_t* weight, const int
 
   int mode = bwd_mode();
   if (mode < 0) mode = persistent_pays(bp.Tb, bp.Vb, H) ? 1 : 0;
+  if (distill) mode = 0;   // its dz blocks are completed between the launches
   if (pair && mode != 0 && bp.n_tb <= BWD_ALL_MAX_TOKEN_BLOCKS) {
     // every block's dz, dh and dW tiles in one launch, ordered by tile flags
     BwdAllArgs a;
@@ -756,6 +800,14 @@ lmhead_status bwd_impl(const uint16_t* hidden, const uint16_t* weight, const int
       const int gz = static_cast<int>(
           std::min<int64_t>(ceil_div(m_cap, um) * ceil_div(vact, BN) * ctas, sms));
       LMH_TRY(launch("bwd_dz_gemm", s, [&] { return launch_gemm_bwd_dz(lz, gz, pair, s); }));
+      if (distill) {
+        LMH_TRY(launch("distill_patch", s, [&] {
+          return launch_distill_patch(distill->patch_ids, distill->patch_values,
+                                      distill->teacher.K, f.st, static_cast<int>(t0),
+                                      static_cast<int>(m_cap), static_cast<int>(v0),
+                                      static_cast<int>(vact), dz, bp.Vb, s);
+        }));
+      }
 
       // one launch for both gradient contractions of the block
       LaunchArgs lg;
@@ -848,7 +900,7 @@ lmhead_status lmhead_logps_bwd(const uint16_t* hidden, const uint16_t* weight,
                                size_t workspace_bytes, lmhead_stream_t stream) {
   return bwd_impl(hidden, weight, targets, loss_mask, T, H, V, 0, V, temperature, chunk_size,
                   grad_logp, grad_entropy, lse, entropy, d_hidden, d_weight, accumulate_dweight,
-                  workspace, workspace_bytes, stream);
+                  nullptr, workspace, workspace_bytes, stream);
 }
 
 lmhead_status lmhead_logps_fwd_shard(const uint16_t* hidden, const uint16_t* weight_shard,
@@ -859,7 +911,7 @@ lmhead_status lmhead_logps_fwd_shard(const uint16_t* hidden, const uint16_t* wei
                                      lmhead_stream_t stream) {
   lmhead_status rc = check_shard(V_shard, vocab_offset, vocab_total);
   if (rc != LMHEAD_OK) return rc;
-  if (T > 0 && !partials) return LMHEAD_ERR_INVALID_ARG;
+  if (T > 0 && (!partials || !targets)) return LMHEAD_ERR_INVALID_ARG;
   if (!aligned16(partials)) return LMHEAD_ERR_UNSUPPORTED;
   return fwd_impl(hidden, weight_shard, targets, loss_mask, T, H, V_shard, vocab_offset,
                   vocab_total, temperature, chunk_size, nullptr, nullptr, nullptr,
@@ -879,8 +931,8 @@ lmhead_status lmhead_logps_bwd_shard(const uint16_t* hidden, const uint16_t* wei
   if (rc != LMHEAD_OK) return rc;
   return bwd_impl(hidden, weight_shard, targets, loss_mask, T, H, V_shard, vocab_offset,
                   vocab_total, temperature, chunk_size, grad_logp, grad_entropy, lse, entropy,
-                  d_hidden, d_weight_shard, accumulate_dweight, workspace, workspace_bytes,
-                  stream);
+                  d_hidden, d_weight_shard, accumulate_dweight, nullptr, workspace,
+                  workspace_bytes, stream);
 }
 
 lmhead_status lmhead_combine_shards(const float* partials, int32_t n_shards,
@@ -1074,6 +1126,129 @@ lmhead_status lmhead_logps_fwd_bwd(const uint16_t* hidden, const uint16_t* weigh
     LMH_TRY(launch("bwd_grad_gemm", s, [&] { return launch_gemm_bwd_grad(lg, gg, pair, s); }));
   }
   return LMHEAD_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+// Workspace of the distillation calls: that of the head's forward or backward
+// (256-byte multiples), then the statistics of the forward, or the ids and
+// cotangents of the teacher's entries.
+bool distill_extra(int op, int64_t T, int32_t K, size_t* first, size_t* second) {
+  if (K <= 0 || K > kMaxTeacher) return false;
+  const int64_t T_alloc = round_up(T, BM);
+  *second = 0;
+  if (op == LMHEAD_OP_FWD) {
+    *first = align256(16 * static_cast<size_t>(T));
+  } else if (op == LMHEAD_OP_BWD) {
+    *first = align256(4 * static_cast<size_t>(T_alloc) * static_cast<size_t>(K));
+    *second = align256(2 * static_cast<size_t>(T_alloc) * static_cast<size_t>(K));
+  } else {
+    return false;
+  }
+  return true;
+}
+
+// The planner keeps small host tables; out of host memory there must not leave
+// a C entry as an exception.
+template <class F>
+lmhead_status no_throw(F&& f) noexcept {
+  try {
+    return f();
+  } catch (...) {
+    return LMHEAD_ERR_CUDA;
+  }
+}
+
+lmhead_status check_teacher(int32_t K, float tau) {
+  if (K <= 0 || !std::isfinite(tau) || !(tau > 0.f)) return LMHEAD_ERR_INVALID_ARG;
+  return K > kMaxTeacher ? LMHEAD_ERR_UNSUPPORTED : LMHEAD_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t lmhead_distill_workspace_size(int op, int64_t T, int32_t H, int32_t V, int32_t K,
+                                     int32_t chunk_size) {
+  size_t a = 0, b = 0;
+  if (check_sizes(T, H, V, 1.0f, chunk_size) != LMHEAD_OK || !distill_extra(op, T, K, &a, &b))
+    return 0;
+  return layout(op, T, H, V, chunk_size).total + a + b;
+}
+
+lmhead_status lmhead_distill_fwd(const uint16_t* hidden, const uint16_t* weight,
+                                 const int32_t* top_ids, const float* top_logits,
+                                 const float* teacher_lse, const uint8_t* loss_mask, int64_t T,
+                                 int32_t H, int32_t V, int32_t K, float temperature,
+                                 float teacher_temperature, int32_t chunk_size, float* loss,
+                                 float* lse, float* z_top, void* workspace,
+                                 size_t workspace_bytes, lmhead_stream_t stream) {
+  lmhead_status rc = check_sizes(T, H, V, temperature, chunk_size);
+  if (rc == LMHEAD_OK) rc = check_teacher(K, teacher_temperature);
+  if (rc != LMHEAD_OK) return rc;
+  if (T == 0) return LMHEAD_OK;
+  if (!hidden || !weight || !top_ids || !top_logits || !loss || !lse || !z_top || !workspace)
+    return LMHEAD_ERR_INVALID_ARG;
+  if (!aligned16(hidden) || !aligned16(weight) || (reinterpret_cast<uintptr_t>(workspace) & 255))
+    return LMHEAD_ERR_UNSUPPORTED;
+  size_t extra = 0, none = 0;
+  distill_extra(LMHEAD_OP_FWD, T, K, &extra, &none);
+  const size_t base = layout(LMHEAD_OP_FWD, T, H, V, chunk_size).total;
+  if (workspace_bytes < base + extra) return LMHEAD_ERR_WORKSPACE_TOO_SMALL;
+  float4* stats = reinterpret_cast<float4*>(static_cast<char*>(workspace) + base);
+  rc = no_throw([&] {
+    return fwd_impl(hidden, weight, nullptr, loss_mask, T, H, V, 0, V, temperature, chunk_size,
+                    nullptr, nullptr, nullptr, stats, workspace, base, stream);
+  });
+  if (rc != LMHEAD_OK) return rc;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const Teacher teacher{top_ids, top_logits, teacher_lse, K, teacher_temperature};
+  LMH_TRY(launch("distill_head_loss", s, [&] {
+    return launch_distill_head_loss(hidden, weight, H, V, teacher, loss_mask, static_cast<int>(T),
+                                    temperature, stats, static_cast<DeviceState*>(workspace), loss,
+                                    lse, z_top, s);
+  }));
+  return LMHEAD_OK;
+}
+
+lmhead_status lmhead_distill_bwd(const uint16_t* hidden, const uint16_t* weight,
+                                 const int32_t* top_ids, const float* top_logits,
+                                 const float* teacher_lse, const uint8_t* loss_mask, int64_t T,
+                                 int32_t H, int32_t V, int32_t K, float temperature,
+                                 float teacher_temperature, int32_t chunk_size,
+                                 const float* grad_loss, const float* lse, const float* z_top,
+                                 float* d_hidden, float* d_weight, int accumulate_dweight,
+                                 void* workspace, size_t workspace_bytes, lmhead_stream_t stream) {
+  lmhead_status rc = check_sizes(T, H, V, temperature, chunk_size);
+  if (rc == LMHEAD_OK) rc = check_teacher(K, teacher_temperature);
+  if (rc != LMHEAD_OK) return rc;
+  size_t base = 0, ids = 0, values = 0;
+  DistillCotangent d{};
+  if (T > 0) {
+    if (!top_ids || !top_logits || !grad_loss || !lse || !z_top || !workspace)
+      return LMHEAD_ERR_INVALID_ARG;
+    base = layout(LMHEAD_OP_BWD, T, H, V, chunk_size).total;
+    distill_extra(LMHEAD_OP_BWD, T, K, &ids, &values);
+    // pointers and alignment come before the size, as in lmhead_logps_bwd
+    if (!weight || !d_weight || !hidden || !d_hidden) return LMHEAD_ERR_INVALID_ARG;
+    if (!aligned16(weight) || !aligned16(d_weight) || !aligned16(hidden) || !aligned16(d_hidden) ||
+        (reinterpret_cast<uintptr_t>(workspace) & 255))
+      return LMHEAD_ERR_UNSUPPORTED;
+    if (workspace_bytes < base + ids + values) return LMHEAD_ERR_WORKSPACE_TOO_SMALL;
+    char* ws = static_cast<char*>(workspace) + base;
+    d = {{top_ids, top_logits, teacher_lse, K, teacher_temperature},
+         grad_loss,
+         z_top,
+         reinterpret_cast<int32_t*>(ws),
+         reinterpret_cast<uint16_t*>(ws + ids)};
+  }
+  return no_throw([&] {
+    return bwd_impl(hidden, weight, nullptr, loss_mask, T, H, V, 0, V, temperature, chunk_size,
+                    nullptr, nullptr, lse, nullptr, d_hidden, d_weight, accumulate_dweight, &d,
+                    workspace, base, stream);
+  });
 }
 
 lmhead_status lmhead_score_logits_fwd(const float* logits, const int32_t* targets,

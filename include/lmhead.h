@@ -329,6 +329,184 @@ lmhead_status lmhead_score_logits_bwd(const float* logits, const int32_t* target
                                       const float* entropy, float* d_logits,
                                       lmhead_stream_t stream);
 
+/* Element types of the calls on caller-held tensors below. */
+enum { LMHEAD_F32 = 0, LMHEAD_BF16 = 1, LMHEAD_F16 = 2 };
+
+/*
+ * Distillation from a teacher's top logits.  Token t has K teacher entries:
+ * vocabulary ids top_ids [T, K] int32 and the teacher's logits top_logits
+ * [T, K] fp32 at them.  With tau' = teacher_temperature,
+ *
+ *   L_t     = teacher_lse_t, or log sum_k exp(a_k / tau') when teacher_lse is NULL
+ *   p_k     = exp(a_k / tau' - L_t),  P_t = sum_k p_k
+ *   loss_t  = sum_k p_k (log p_k - z_{id_k} + lse_t)
+ *   d loss_t / d z_v = P_t softmax(z)_v - sum_{k: id_k = v} p_k
+ *
+ * where z = logits / temperature is the student's row and lse_t its
+ * log-sum-exp over the whole vocabulary: the teacher's cross-entropy minus its
+ * entropy over the K entries (a KL divergence when P_t = 1).  teacher_lse is
+ * the teacher's own log-sum-exp of a / tau' over its whole vocabulary; pass it
+ * to keep the mass outside the K entries out of the loss instead of spreading
+ * it over them.
+ *  - a_k = -inf marks an absent entry: its id is not looked at.  A token whose
+ *    entries are all absent (P_t = 0) has loss +0.0 and a zero gradient.
+ *  - Ids in [-V, 0) wrap to id + V.  An id outside [-V, V) makes the token's
+ *    loss NaN and takes no part in its gradient; the calls through the head
+ *    also set LMHEAD_ERR_BAD_TARGET in the device status.
+ *  - An id that a token names more than once gets the sum of its entries.
+ *  - loss_mask as elsewhere: unscored tokens give +0.0 outputs and gradients.
+ *  - 1 <= K <= 1024 (LMHEAD_ERR_INVALID_ARG below, LMHEAD_ERR_UNSUPPORTED above);
+ *    teacher_temperature is checked like temperature.
+ *
+ * Through the head: z = hidden . weight^T / temperature, never materialised.
+ * Arguments not named here are those of lmhead_logps_fwd / _bwd, and so are the
+ * errors, the order of the checks and the determinism.
+ *  loss   [T] fp32 out
+ *  lse    [T] fp32 out; keep it for the backward
+ *  z_top  [T, K] fp32 out: z at the teacher's ids (0 at absent entries and
+ *         unscored tokens, NaN at an invalid id); keep it for the backward
+ *  grad_loss [T] fp32: the loss's cotangent
+ *  workspace  lmhead_distill_workspace_size(LMHEAD_OP_FWD or LMHEAD_OP_BWD, ...)
+ * The forward is the head's statistics GEMM and one pass that forms the K
+ * products per token; the backward forms the dense part of the cotangent in the
+ * recompute GEMM's epilogue and replaces it at the K ids before both gradient
+ * contractions read it.
+ */
+size_t lmhead_distill_workspace_size(int op, int64_t T, int32_t H, int32_t V, int32_t K,
+                                     int32_t chunk_size);
+
+lmhead_status lmhead_distill_fwd(const uint16_t* hidden, const uint16_t* weight,
+                                 const int32_t* top_ids, const float* top_logits,
+                                 const float* teacher_lse, const uint8_t* loss_mask, int64_t T,
+                                 int32_t H, int32_t V, int32_t K, float temperature,
+                                 float teacher_temperature, int32_t chunk_size, float* loss,
+                                 float* lse, float* z_top, void* workspace,
+                                 size_t workspace_bytes, lmhead_stream_t stream);
+
+lmhead_status lmhead_distill_bwd(const uint16_t* hidden, const uint16_t* weight,
+                                 const int32_t* top_ids, const float* top_logits,
+                                 const float* teacher_lse, const uint8_t* loss_mask, int64_t T,
+                                 int32_t H, int32_t V, int32_t K, float temperature,
+                                 float teacher_temperature, int32_t chunk_size,
+                                 const float* grad_loss, const float* lse, const float* z_top,
+                                 float* d_hidden, float* d_weight, int accumulate_dweight,
+                                 void* workspace, size_t workspace_bytes, lmhead_stream_t stream);
+
+/*
+ * Distillation on logits the caller holds: logits [T, V] of element type `type`,
+ * rows `ld` >= V elements apart (a table padded past V keeps its padding out of
+ * the softmax).  d_logits (type, rows d_ld apart) is overwritten and may be the
+ * logits buffer itself, with the same ld.  Sums are fp32; d_logits is rounded
+ * once.  Non-finite student logits as in lmhead_score_logits_fwd: -inf has
+ * probability 0 (and makes the loss +inf where p_k > 0), NaN or +inf makes the
+ * row's lse and loss NaN, a row with no finite logit has lse = -inf and a NaN
+ * loss; non-finite logits get a zero cotangent.  HBM-bound: one read of the
+ * logits; one read and one write backward.  A pointer that is not aligned to
+ * its element returns LMHEAD_ERR_UNSUPPORTED; any other alignment works.
+ */
+lmhead_status lmhead_distill_logits_fwd(const void* logits, int type, int64_t ld,
+                                        const int32_t* top_ids, const float* top_logits,
+                                        const float* teacher_lse, const uint8_t* loss_mask,
+                                        int64_t T, int32_t V, int32_t K, float temperature,
+                                        float teacher_temperature, float* loss, float* lse,
+                                        lmhead_stream_t stream);
+
+lmhead_status lmhead_distill_logits_bwd(const void* logits, int type, int64_t ld,
+                                        const int32_t* top_ids, const float* top_logits,
+                                        const float* teacher_lse, const uint8_t* loss_mask,
+                                        int64_t T, int32_t V, int32_t K, float temperature,
+                                        float teacher_temperature, const float* grad_loss,
+                                        const float* lse, void* d_logits, int64_t d_ld,
+                                        lmhead_stream_t stream);
+
+/*
+ * Layer norm of the rows that the head reads.  Row t of x [N, H]:
+ *   mean_t = mean(x),  rstd_t = 1 / sqrt(mean((x - mean_t)^2) + eps)
+ *   y = (x - mean_t) rstd_t weight + bias
+ *  x_type, y_type  y has x's type, or bf16 for fp32 rows (an fp32 residual
+ *                  stream feeding a bf16 head)
+ *  x_ld, y_ld      elements between rows, >= H
+ *  weight, bias    [H] of param_type, which is x_type or LMHEAD_F32; bias may be NULL
+ *  mean, rstd      [N] fp32 out, each may be NULL; the backward needs both
+ * Backward, h = dy weight, xh = (x - mean_t) rstd_t:
+ *   dx = rstd_t (h - mean(h) - xh mean(h xh))
+ *   d_weight (+)= sum_t dy xh,  d_bias (+)= sum_t dy
+ *  dy_type         x_type or LMHEAD_F32 (the head's d_hidden), or bf16 for fp32 rows
+ *  dx              [N, H] of x_type, rows dx_ld apart; may be NULL, and may be x or
+ *                  (same type and ld) dy itself
+ *  d_weight, d_bias  [H] fp32, each may be NULL; overwritten, or added to when
+ *                  accumulate != 0
+ *  workspace       lmhead_layernorm_workspace_size(N, H) bytes, 256-byte aligned;
+ *                  needed with d_weight or d_bias
+ * Statistics and sums are fp32, the variance is taken about the mean, and column
+ * sums are added in a fixed order: same inputs, same bits.  N == 0 is a no-op
+ * (the backward still zeroes d_weight / d_bias unless accumulate is set).
+ */
+size_t lmhead_layernorm_workspace_size(int64_t N, int32_t H);
+
+lmhead_status lmhead_layernorm_fwd(const void* x, int x_type, int64_t x_ld, const void* weight,
+                                   const void* bias, int param_type, int64_t N, int32_t H,
+                                   float eps, void* y, int y_type, int64_t y_ld, float* mean,
+                                   float* rstd, lmhead_stream_t stream);
+
+lmhead_status lmhead_layernorm_bwd(const void* dy, int dy_type, int64_t dy_ld, const void* x,
+                                   int x_type, int64_t x_ld, const void* weight, int param_type,
+                                   const float* mean, const float* rstd, int64_t N, int32_t H,
+                                   void* dx, int64_t dx_ld, float* d_weight, float* d_bias,
+                                   int accumulate, void* workspace, size_t workspace_bytes,
+                                   lmhead_stream_t stream);
+
+/*
+ * A sampler's rules on logits [R, V] of element type `type` (rows ld apart):
+ * penalties for repeated tokens, biases and a grammar mask, in this order and
+ * in fp32, rounded once.  For row r and id v, with `met` whether v occurs in the
+ * row's prompt or outputs and c its occurrences in the outputs:
+ *   x1  = met ? (x > 0 ? x / repetition_r : x * repetition_r) : x
+ *   x2  = c > 0 ? x1 - (frequency_r c + presence_r) : x1
+ *   x3  = x2 + bias_v
+ *   out = v allowed ? x3 : -inf
+ *  tokens        [n_tokens] int32, all rows' histories; spans [R, 3] int64: row r's
+ *                prompt is tokens[spans[r][0] : spans[r][1]], its outputs
+ *                tokens[spans[r][1] : spans[r][2]].  Rows may share tokens: the
+ *                positions of one sequence are rows whose spans end one token later
+ *                each.  Ends are cut to [0, n_tokens] and to be in order; ids
+ *                outside [0, V) (padding) are skipped.  Both NULL: no history
+ *                (then the three penalties must be NULL too).
+ *  repetition, frequency, presence  [R] fp32, each may be NULL (1, 0, 0)
+ *  bias_offsets  [R + 1] int64: row r's biases are entries
+ *                [bias_offsets[r], bias_offsets[r + 1]) of bias_ids int32 and
+ *                bias_values fp32 (n_bias entries); the last entry of a repeated id
+ *                counts, ids outside [0, V) are skipped.  NULL: no biases.
+ *  allowed       [n_allowed, (V + 31) / 32] 32-bit words, bit v % 32 of word v / 32
+ *                set = id v allowed; row r uses mask allowed_rows[r] ([R] int32), or
+ *                r when allowed_rows is NULL; an index outside [0, n_allowed) (-1)
+ *                leaves the row unmasked.  A mask with no bit set gives a row of -inf.
+ *  out           [R, V] of the same type, rows out_ld apart; may be the logits
+ *                buffer itself, with the same ld
+ * The backward takes the ORIGINAL logits and grad_out (the cotangent of out):
+ *   d_logits = v allowed ? (met ? (x > 0 ? 1 / repetition_r : repetition_r) : 1)
+ *              * grad_out : 0
+ * d_logits may be grad_out itself, with the same ld.  Masked logits are not
+ * read, nor, in the backward, logits of ids that were never met.
+ */
+lmhead_status lmhead_process_logits_fwd(const void* logits, int type, int64_t ld, int64_t R,
+                                        int32_t V, const int32_t* tokens, int64_t n_tokens,
+                                        const int64_t* spans, const float* repetition,
+                                        const float* frequency, const float* presence,
+                                        const int64_t* bias_offsets, const int32_t* bias_ids,
+                                        const float* bias_values, int64_t n_bias,
+                                        const uint32_t* allowed, int64_t n_allowed,
+                                        const int32_t* allowed_rows, void* out, int64_t out_ld,
+                                        lmhead_stream_t stream);
+
+lmhead_status lmhead_process_logits_bwd(const void* grad_out, int64_t grad_ld, const void* logits,
+                                        int type, int64_t ld, int64_t R, int32_t V,
+                                        const int32_t* tokens, int64_t n_tokens,
+                                        const int64_t* spans, const float* repetition,
+                                        const uint32_t* allowed, int64_t n_allowed,
+                                        const int32_t* allowed_rows, void* d_logits, int64_t d_ld,
+                                        lmhead_stream_t stream);
+
 /*
  * Self-test of failure detection (the pages have no counterpart; the
  * kernels need it on shared GPUs): launches one CTA that allocates tensor
