@@ -155,49 +155,74 @@ def library():
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+# Bound on first use (importing this package does not import torch).
+_torch = None
+_types = None
+_raw_stream = None
+
+
+def _bind_torch():
+    global _torch, _types, _raw_stream
+    import torch
+    _types = {torch.float32: LMHEAD_F32, torch.bfloat16: LMHEAD_BF16, torch.float16: LMHEAD_F16}
+    # the handle without a Stream object around it (about 2 us a call less)
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    _torch = torch
 
 
 def _stream(stream):
     if stream is None:
-        import torch
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        if _torch is None:
+            _bind_torch()
+        if _raw_stream is not None:
+            return _raw_stream(_torch.cuda.current_device())
+        return _torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
-        return ctypes.c_void_p(stream)
-    return ctypes.c_void_p(stream.cuda_stream)
+        return stream
+    return stream.cuda_stream
 
 
 def _check_tensor(t, name, dtype, shape, allow_none=False):
-    import torch
     if t is None:
         if allow_none:
             return
         raise ValueError("%s is required" % name)
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    del torch
 
 
 def _on_device(tensors, stream, fn):
     """Run fn() with the tensors' CUDA device current.  The library launches
     on the current device, so a call whose tensors (or stream) live on
     another device, or on several, is refused here instead of launched."""
-    import torch
-    devs = {t.device for t in tensors if t is not None}
+    if _torch is None:
+        _bind_torch()
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError("all tensors and the stream of one call must be on one CUDA device, "
+                             "got %s" % sorted({str(t.device) for t in tensors if t is not None}))
     if stream is not None and not isinstance(stream, int) and hasattr(stream, "device"):
-        devs.add(stream.device)
-    if len(devs) > 1:
-        raise ValueError("all tensors and the stream of one call must be on one CUDA device, "
-                         "got %s" % sorted(str(d) for d in devs))
-    if not devs:
+        if dev is not None and stream.device != dev:
+            raise ValueError("all tensors and the stream of one call must be on one CUDA device, "
+                             "got %s" % sorted({str(dev), str(stream.device)}))
+        dev = stream.device
+    if dev is None or dev.index == _torch.cuda.current_device():
         return fn()
-    with torch.cuda.device(devs.pop()):
+    with _torch.cuda.device(dev):
         return fn()
 
 
@@ -206,29 +231,28 @@ def _check_workspace(ws):
         raise ValueError("workspace must be a contiguous CUDA tensor")
 
 
-def _element_types():
-    import torch
-    return {torch.float32: LMHEAD_F32, torch.bfloat16: LMHEAD_BF16, torch.float16: LMHEAD_F16}
-
-
 def _check_rows(t, name, shape, dtypes=None):
     """A CUDA matrix whose rows are contiguous but may lie further apart than their
     length; returns (element type, elements between rows)."""
     if t is None:
         raise ValueError("%s is required" % name)
-    types = _element_types()
-    if t.dtype not in types or (dtypes is not None and t.dtype not in dtypes):
+    if _torch is None:
+        _bind_torch()
+    kind = _types.get(t.dtype)
+    if kind is None or (dtypes is not None and t.dtype not in dtypes):
         raise TypeError("%s must be %s, got %s" % (name, " or ".join(
-            str(d) for d in (dtypes if dtypes is not None else types)), t.dtype))
+            str(d) for d in (dtypes if dtypes is not None else _types)), t.dtype))
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    rows, cols = t.shape
-    ld = t.stride(0) if rows > 1 else max(cols, t.stride(0))
-    if (cols > 1 and t.stride(1) != 1) or ld < cols:
+    rows, cols = shape
+    ld, step = t.stride()
+    if rows <= 1:
+        ld = max(cols, ld)
+    if (cols > 1 and step != 1) or ld < cols:
         raise ValueError("%s must have contiguous rows that do not overlap" % name)
-    return types[t.dtype], ld
+    return kind, ld
 
 
 def _check_teacher(top_ids, top_logits, teacher_lse, loss_mask, T):
@@ -544,12 +568,11 @@ def lmhead_layernorm_workspace_size(N, H):
 
 
 def _check_norm_params(x, weight, bias, H):
-    import torch
-    if weight is None or weight.dtype not in (torch.float32, x.dtype):
+    if weight is None or (weight.dtype is not _torch.float32 and weight.dtype is not x.dtype):
         raise TypeError("weight must be torch.float32 or %s" % x.dtype)
     _check_tensor(weight, "weight", weight.dtype, (H,))
     _check_tensor(bias, "bias", weight.dtype, (H,), allow_none=True)
-    return _element_types()[weight.dtype]
+    return _types[weight.dtype]
 
 
 def lmhead_layernorm_fwd(x, weight, bias, eps, y, mean, rstd, stream=None):

@@ -29,9 +29,9 @@ __device__ __forceinline__ __half from_f32<__half>(float x) {
   return __float2half_rn(x);
 }
 
-// VEC elements moved by one access (aligned to their size).
+// VEC elements moved by one 16-byte access or less (two for 8 fp32), aligned to it.
 template <typename T, int VEC>
-struct alignas(sizeof(T) * VEC) Pack {
+struct alignas(sizeof(T) * VEC > 16 ? 16 : sizeof(T) * VEC) Pack {
   T v[VEC];
 };
 

@@ -14,6 +14,9 @@
 namespace lmh {
 namespace {
 
+constexpr int kFwdMaxThreads = 1024;   // forward, one CTA per row
+constexpr int kFwdWarpRows = 4;        // forward, one warp per row: rows per CTA
+constexpr int kBwdThreads = 512;       // backward: most threads per CTA
 constexpr int kRowThreads = 256;
 constexpr int kColThreads = 256;   // 32 columns x 8 row lanes
 constexpr int kFinishRows = 8;
@@ -22,6 +25,31 @@ __device__ __forceinline__ float load_param(const void* p, int type, int64_t i) 
   if (type == kF32) return static_cast<const float*>(p)[i];
   if (type == kBF16) return to_f32(static_cast<const __nv_bfloat16*>(p)[i]);
   return to_f32(static_cast<const __half*>(p)[i]);
+}
+
+// VEC parameters from index i (a multiple of VEC; 16-byte aligned base if VEC > 1).
+template <int VEC>
+__device__ __forceinline__ void load_params(const void* p, int type, int i, float (&v)[VEC]) {
+  if (type == kF32) {
+    constexpr int N = VEC < 4 ? VEC : 4;
+#pragma unroll
+    for (int j = 0; j < VEC; j += N) {
+      const Pack<float, N> q = *reinterpret_cast<const Pack<float, N>*>(
+          static_cast<const float*>(p) + i + j);
+#pragma unroll
+      for (int e = 0; e < N; ++e) v[j + e] = q.v[e];
+    }
+  } else if (type == kBF16) {
+    const Pack<__nv_bfloat16, VEC> q = *reinterpret_cast<const Pack<__nv_bfloat16, VEC>*>(
+        static_cast<const __nv_bfloat16*>(p) + i);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) v[e] = to_f32(q.v[e]);
+  } else {
+    const Pack<__half, VEC> q =
+        *reinterpret_cast<const Pack<__half, VEC>*>(static_cast<const __half*>(p) + i);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) v[e] = to_f32(q.v[e]);
+  }
 }
 
 // Sum over the CTA, returned to every thread.
@@ -64,6 +92,219 @@ __global__ void __launch_bounds__(kRowThreads)
       if (mean) mean[t] = mu;
       if (rstd) rstd[t] = r;
     }
+  }
+}
+
+// A row in the registers of one warp (kPerWarp) or one CTA: read once, NV packs
+// of VEC elements per thread.  Warps form mean and squared deviations about
+// their own mean; with one CTA per row those are joined by
+//   M2 = sum_w M2_w + n_w (mean_w - mean)^2
+// after a single barrier.
+template <typename X, typename Y, int VEC, int NV, bool kPerWarp>
+__global__ void __launch_bounds__(kPerWarp ? 32 * kFwdWarpRows : kFwdMaxThreads)
+    norm_fwd_kernel(const X* __restrict__ x, int64_t x_ld, const void* __restrict__ w,
+                    const void* __restrict__ b, int param_type, int64_t N, int H, float eps,
+                    Y* __restrict__ y, int64_t y_ld, float* mean, float* rstd) {
+  pdl_wait_prerequisites();
+  pdl_launch_dependents();
+  __shared__ float red[3][kPerWarp ? 1 : kFwdMaxThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = kPerWarp ? 32 : blockDim.x;
+  const int i = kPerWarp ? lane : threadIdx.x;
+  const int64_t t = kPerWarp ? static_cast<int64_t>(blockIdx.x) * kFwdWarpRows + warp
+                             : static_cast<int64_t>(blockIdx.x);
+  if (t >= N) return;   // whole warps, and only where warps work alone
+  const X* row = x + t * x_ld;
+  const int n = H / VEC;
+  Pack<X, VEC> raw[NV];
+#pragma unroll
+  for (int k = 0; k < NV; ++k)
+    if (i + k * g < n) raw[k] = *reinterpret_cast<const Pack<X, VEC>*>(row + (i + k * g) * VEC);
+  float s = 0.f;
+  int cnt = 0;
+#pragma unroll
+  for (int k = 0; k < NV; ++k)
+    if (i + k * g < n) {
+      cnt += VEC;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) s += to_f32(raw[k].v[e]);
+    }
+  cnt = __reduce_add_sync(0xffffffffu, cnt);
+  float mu = cnt ? warp_sum(s) / static_cast<float>(cnt) : 0.f;
+  float m2 = 0.f;
+#pragma unroll
+  for (int k = 0; k < NV; ++k)
+    if (i + k * g < n) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float d = to_f32(raw[k].v[e]) - mu;
+        m2 = fmaf(d, d, m2);
+      }
+    }
+  m2 = warp_sum(m2);
+  if (!kPerWarp && blockDim.x > 32) {
+    if (lane == 0) {
+      red[0][warp] = static_cast<float>(cnt);
+      red[1][warp] = mu;
+      red[2][warp] = m2;
+    }
+    __syncthreads();
+    const int warps = blockDim.x >> 5;
+    const float c = lane < warps ? red[0][lane] : 0.f;
+    const float mw = lane < warps ? red[1][lane] : 0.f;
+    mu = warp_sum(c * mw) / static_cast<float>(H);
+    const float d = mw - mu;
+    m2 = warp_sum(lane < warps ? fmaf(c * d, d, red[2][lane]) : 0.f);
+  }
+  const float r = 1.f / sqrtf(m2 / static_cast<float>(H) + eps);
+  Y* out = y + t * y_ld;
+#pragma unroll
+  for (int k = 0; k < NV; ++k)
+    if (i + k * g < n) {
+      const int c = (i + k * g) * VEC;
+      float wv[VEC], bv[VEC];
+      load_params<VEC>(w, param_type, c, wv);
+      if (b) load_params<VEC>(b, param_type, c, bv);
+      Pack<Y, VEC> o;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float v = (to_f32(raw[k].v[e]) - mu) * r * wv[e];
+        o.v[e] = from_f32<Y>(b ? v + bv[e] : v);
+      }
+      *reinterpret_cast<Pack<Y, VEC>*>(out + c) = o;
+    }
+  if (i == 0) {
+    if (mean) mean[t] = mu;
+    if (rstd) rstd[t] = r;
+  }
+}
+
+// Both gradients in one pass over x and dy.  A group of g threads (g a multiple
+// of 32) owns a row at a time and its threads fixed columns, so dw and db gather
+// in registers over the group's rows; the CTA's groups are joined in shared
+// memory at the end, and the CTA writes one partial row.  The next row's loads
+// are issued before this row's two sums are reduced.
+template <typename X, typename D, int VEC, int NV>
+__global__ void __launch_bounds__(kBwdThreads)
+    norm_bwd_kernel(const D* __restrict__ dy, int64_t dy_ld, const X* x, int64_t x_ld,
+                    const void* __restrict__ w, int param_type, const float* __restrict__ mean,
+                    const float* __restrict__ rstd, int64_t N, int H, X* dx, int64_t dx_ld,
+                    float* __restrict__ part_w, float* __restrict__ part_b, int g) {
+  extern __shared__ float joined[];   // [2][H] when the CTA has several groups
+  __shared__ float red[2][2][kBwdThreads / 32];
+  constexpr bool kKeep = VEC * NV <= 16 && NV <= 8;   // room to keep w and the next row in registers
+  pdl_wait_prerequisites();
+  pdl_launch_dependents();
+  const int groups = blockDim.x / g;
+  const int grp = threadIdx.x / g, i = threadIdx.x - grp * g;
+  const int lane = threadIdx.x & 31, warps = g >> 5;
+  const int n = H / VEC;
+  const float inv = 1.f / static_cast<float>(H);
+  float aw[NV][VEC] = {}, ab[NV][VEC] = {}, wv[kKeep ? NV : 1][VEC];
+  if constexpr (kKeep) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+      if (i + k * g < n) load_params<VEC>(w, param_type, (i + k * g) * VEC, wv[k]);
+  }
+  Pack<X, VEC> xn[NV];
+  Pack<D, VEC> gn[NV];
+  float mn = 0.f, rn = 0.f;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+  int64_t t = static_cast<int64_t>(blockIdx.x) * groups + grp;
+  auto fetch = [&](int64_t row) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+      if (i + k * g < n) {
+        xn[k] = *reinterpret_cast<const Pack<X, VEC>*>(x + row * x_ld + (i + k * g) * VEC);
+        gn[k] = *reinterpret_cast<const Pack<D, VEC>*>(dy + row * dy_ld + (i + k * g) * VEC);
+      }
+    mn = mean[row];
+    rn = rstd[row];
+  };
+  if (t < N) fetch(t);
+  int flip = 0;
+  for (; t < N; t += step, flip ^= 1) {
+    Pack<X, VEC> xr[NV];
+    Pack<D, VEC> gr[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      xr[k] = xn[k];
+      gr[k] = gn[k];
+    }
+    const float mu = mn, r = rn;
+    if (kKeep && t + step < N) fetch(t + step);
+    float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+      if (i + k * g < n) {
+        float wl[VEC];
+        if constexpr (!kKeep) load_params<VEC>(w, param_type, (i + k * g) * VEC, wl);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float xh = (to_f32(xr[k].v[e]) - mu) * r, d = to_f32(gr[k].v[e]);
+          const float h = d * (kKeep ? wv[kKeep ? k : 0][e] : wl[e]);
+          s1 = fmaf(h, xh, s1);
+          s2 += h;
+          aw[k][e] = fmaf(d, xh, aw[k][e]);
+          ab[k][e] += d;
+        }
+      }
+    if (dx) {
+      s1 = warp_sum(s1);
+      s2 = warp_sum(s2);
+      if (warps > 1) {
+        const int w0 = grp * warps;
+        if (lane == 0) {
+          red[flip][0][threadIdx.x >> 5] = s1;
+          red[flip][1][threadIdx.x >> 5] = s2;
+        }
+        named_bar_sync(1 + grp, g);
+        s1 = warp_sum(lane < warps ? red[flip][0][w0 + lane] : 0.f);
+        s2 = warp_sum(lane < warps ? red[flip][1][w0 + lane] : 0.f);
+      }
+      const float c1 = s1 * inv, c2 = s2 * inv;
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+        if (i + k * g < n) {
+          const int c = (i + k * g) * VEC;
+          float wl[VEC];
+          if constexpr (!kKeep) load_params<VEC>(w, param_type, c, wl);
+          Pack<X, VEC> o;
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            const float xh = (to_f32(xr[k].v[e]) - mu) * r;
+            const float h = to_f32(gr[k].v[e]) * (kKeep ? wv[kKeep ? k : 0][e] : wl[e]);
+            o.v[e] = from_f32<X>((h - c2 - xh * c1) * r);
+          }
+          *reinterpret_cast<Pack<X, VEC>*>(dx + t * dx_ld + c) = o;
+        }
+    }
+    if (!kKeep && t + step < N) fetch(t + step);
+  }
+  if (!part_w) return;
+  // groups join in order
+  for (int q = 0; q < groups; ++q) {
+    if (groups > 1 && q > 0) __syncthreads();
+    if (grp != q) continue;
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+      if (i + k * g < n) {
+        const int c = (i + k * g) * VEC;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          if (q > 0) {
+            aw[k][e] += joined[c + e];
+            ab[k][e] += joined[H + c + e];
+          }
+          if (q + 1 < groups) {
+            joined[c + e] = aw[k][e];
+            joined[H + c + e] = ab[k][e];
+          } else {
+            part_w[static_cast<int64_t>(blockIdx.x) * H + c + e] = aw[k][e];
+            part_b[static_cast<int64_t>(blockIdx.x) * H + c + e] = ab[k][e];
+          }
+        }
+      }
   }
 }
 
@@ -156,8 +397,40 @@ __global__ void __launch_bounds__(32 * kFinishRows)
   }
 }
 
+bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+int round32(int n) { return (n + 31) / 32 * 32; }
+
+template <typename X, typename Y, int VEC, int NV, bool kPerWarp>
+cudaError_t fwd_rows(const NormFwd& a, cudaStream_t s) {
+  const int n = a.H / VEC;
+  const int threads = kPerWarp ? 32 * kFwdWarpRows : round32((n + NV - 1) / NV);
+  const int64_t grid = kPerWarp ? (a.N + kFwdWarpRows - 1) / kFwdWarpRows : a.N;
+  return launch_dependent(norm_fwd_kernel<X, Y, VEC, NV, kPerWarp>,
+                          dim3(static_cast<unsigned>(grid)), threads, 0, 1, s, static_cast<const X*>(a.x), a.x_ld, a.weight, a.bias,
+                          a.param_type, a.N, a.H, a.eps, static_cast<Y*>(a.y), a.y_ld, a.mean,
+                          a.rstd);
+}
+
 template <typename X, typename Y>
 cudaError_t fwd_typed(const NormFwd& a, cudaStream_t s) {
+  constexpr int VEC = kVec<X>;
+  const bool packs = a.H % VEC == 0 && a.x_ld % VEC == 0 && a.y_ld % VEC == 0 &&
+                     aligned(a.x, 16) && aligned(a.y, sizeof(Y) * VEC) && aligned(a.weight, 16) &&
+                     aligned(a.bias, 16);
+  if (packs) {
+    const int n = a.H / VEC;
+    if (a.N >= 4ll * sm_count()) {   // enough rows to give every warp its own
+      if (n <= 32 * 2) return fwd_rows<X, Y, VEC, 2, true>(a, s);
+      if (n <= 32 * 4) return fwd_rows<X, Y, VEC, 4, true>(a, s);
+      if (n <= 32 * 8) return fwd_rows<X, Y, VEC, 8, true>(a, s);
+      if (n <= 32 * 12) return fwd_rows<X, Y, VEC, 12, true>(a, s);
+    }
+    if (n <= kFwdMaxThreads) return fwd_rows<X, Y, VEC, 1, false>(a, s);
+    if (n <= 4 * kFwdMaxThreads) return fwd_rows<X, Y, VEC, 4, false>(a, s);
+  }
+  if (a.H <= kFwdMaxThreads) return fwd_rows<X, Y, 1, 4, false>(a, s);
+  if (a.H <= 8 * kFwdMaxThreads) return fwd_rows<X, Y, 1, 8, false>(a, s);
   const int64_t cap = static_cast<int64_t>(sm_count()) * 8;
   const int grid = static_cast<int>(a.N < cap ? a.N : cap);
   return launch_dependent(norm_fwd_any_kernel<X, Y>, dim3(grid), kRowThreads, 0, 1, s,
@@ -165,8 +438,52 @@ cudaError_t fwd_typed(const NormFwd& a, cudaStream_t s) {
                           a.H, a.eps, static_cast<Y*>(a.y), a.y_ld, a.mean, a.rstd);
 }
 
+cudaError_t finish(const NormBwd& a, int P, cudaStream_t s) {
+  return launch_dependent(norm_finish_kernel, dim3((a.H + 31) / 32, 2), 32 * kFinishRows, 0, 1, s,
+                          static_cast<const float*>(a.partials),
+                          static_cast<const float*>(a.partials + static_cast<int64_t>(P) * a.H), P,
+                          a.H, a.d_weight, a.d_bias, a.accumulate);
+}
+
+template <typename X, typename D, int VEC, int NV>
+cudaError_t bwd_rows(const NormBwd& a, cudaStream_t s) {
+  const int n = a.H / VEC;
+  const int g = round32((n + NV - 1) / NV);
+  const int sms = sm_count();
+  int groups = kBwdThreads / g;
+  const int64_t per_cta = (a.N + sms - 1) / sms;
+  if (groups > per_cta) groups = static_cast<int>(per_cta);
+  const int64_t ctas = (a.N + groups - 1) / groups;
+  const int P = static_cast<int>(ctas < sms ? ctas : sms);
+  const bool params = a.d_weight || a.d_bias;
+  static std::atomic<int> ready[64];
+  auto* kern = norm_bwd_kernel<X, D, VEC, NV>;
+  constexpr size_t kMost = 2 * sizeof(float) * kBwdThreads / 2 * VEC * NV;   // two groups or more
+  cudaError_t e = allow_shared(ready, reinterpret_cast<const void*>(kern), kMost);
+  if (e != cudaSuccess) return e;
+  const size_t smem = groups > 1 && params ? 2 * sizeof(float) * static_cast<size_t>(a.H) : 0;
+  float* part_w = params ? a.partials : nullptr;
+  float* part_b = params ? a.partials + static_cast<int64_t>(P) * a.H : nullptr;
+  e = launch_dependent(kern, dim3(P), g * groups, smem, 1, s, static_cast<const D*>(a.dy), a.dy_ld,
+                       static_cast<const X*>(a.x), a.x_ld, a.weight, a.param_type, a.mean, a.rstd,
+                       a.N, a.H, static_cast<X*>(a.dx), a.dx_ld, part_w, part_b, g);
+  if (e != cudaSuccess || !params) return e;
+  return finish(a, P, s);
+}
+
 template <typename X, typename D>
 cudaError_t bwd_typed(const NormBwd& a, cudaStream_t s) {
+  constexpr int VEC = kVec<X>;
+  const bool packs = a.H % VEC == 0 && a.x_ld % VEC == 0 && a.dy_ld % VEC == 0 &&
+                     a.dx_ld % VEC == 0 && aligned(a.x, 16) && aligned(a.dx, 16) &&
+                     aligned(a.dy, sizeof(D) * VEC > 16 ? 16 : sizeof(D) * VEC) &&
+                     aligned(a.weight, 16);
+  if (packs) {
+    if (a.H <= kBwdThreads * 16) return bwd_rows<X, D, VEC, 16 / VEC>(a, s);
+    if (a.H <= kBwdThreads * 32) return bwd_rows<X, D, VEC, 32 / VEC>(a, s);
+  }
+  if (a.H <= kBwdThreads * 8) return bwd_rows<X, D, 1, 8>(a, s);
+  if (a.H <= kBwdThreads * 16) return bwd_rows<X, D, 1, 16>(a, s);
   const X* x = static_cast<const X*>(a.x);
   const D* dy = static_cast<const D*>(a.dy);
   cudaError_t e = cudaSuccess;
@@ -180,9 +497,7 @@ cudaError_t bwd_typed(const NormBwd& a, cudaStream_t s) {
                                    s, dy, a.dy_ld, x, a.x_ld, a.mean, a.rstd, a.N, a.H, part_w,
                                    part_b);
   if (e != cudaSuccess) return e;
-  e = launch_dependent(norm_finish_kernel, dim3(cols, 2), 32 * kFinishRows, 0, 1, s,
-                       static_cast<const float*>(part_w), static_cast<const float*>(part_b), P,
-                       a.H, a.d_weight, a.d_bias, a.accumulate);
+  e = finish(a, P, s);
   if (e != cudaSuccess) return e;
   }
   if (a.dx) {
