@@ -6,10 +6,22 @@
 //   x3 = x2 + bias_v
 //   out = allowed ? x3 : -inf
 //   d x = allowed ? (met ? (x > 0 ? 1 / rho : rho) : 1) g : 0
-// Each CTA owns a range of one row's columns and counts the row's history into
-// a table in shared memory that covers just this range, so there is no
-// counting workspace and no global atomic; integer counts do not depend on the
-// order they are added in.
+// HBM-bound: one read and one write of the logits (or gradients).  Two kernels:
+//  1. copy_kernel copies the rows, 16 bytes per access, with the mask applied; a
+//     copy leaves every allowed element as it was, in its own type.  In place it
+//     touches masked packs only, and without a mask it does not run.
+//  2. rewrite_kernel, one CTA per row, finds the distinct ids of the row's
+//     history and biases, counts them, and rewrites those elements from what the
+//     copy left (in L2): in fp32 from the exact logit, rounded once.
+// The distinct ids live in a bitmap over the vocabulary in shared memory.  Ranks
+// (set bits before an id) number them without gaps, so counts take four bytes per
+// distinct id and not per column, and ascending ranks are ascending columns.
+// Integer counts do not depend on the order they are added in.
+// One kernel that counted into a table over each CTA's column range before or
+// after copying it took 127 to 225 us where these two take 72 (256 rows of
+// 151,936 bf16, 5,100 tokens each): every range's CTA reads the row's whole
+// history, and clearing and searching a table as large as the vocabulary costs
+// more instructions than the copy.
 #include "element.cuh"
 #include "operators.h"
 #include "ptx.cuh"
@@ -17,98 +29,273 @@
 namespace lmh {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kRange = 8192;   // columns per CTA: 32 KB of counts, 32 KB of bias slots
+constexpr int kCopyThreads = 256;
+constexpr int kUnroll = 4;             // 16-byte accesses in flight per thread
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMostColumns = 1 << 18;  // per CTA of rewrite_kernel: 32 KB of bitmap, 32 KB of ranks
+constexpr int kWindow = 4096;          // distinct ids handled at a time
 
+// Bits [c, c + n) of a mask row, n <= 32; bits past the row's V are not read.
+__device__ __forceinline__ uint32_t mask_bits(const uint32_t* mask, int c, int n, int V) {
+  const int w = c >> 5, sh = c & 31;
+  uint32_t lo = mask[w];
+  if (sh == 0) return lo;
+  const uint32_t hi = (sh + n > 32 && ((w + 1) << 5) < V) ? mask[w + 1] : 0u;
+  return __funnelshift_r(lo, hi, sh);
+}
+
+// `on` = one bit per element of the pack: elements whose bit is clear become off.
+template <typename T, int VEC>
+__device__ __forceinline__ void keep_allowed(Pack<T, VEC>& q, uint32_t on, T off) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e)
+      if (!(on >> e & 1u)) q.v[e] = off;
+  } else {
+    // two elements per 32-bit word: a 0xffff mask for each bit, one select per word
+    uint32_t* w = reinterpret_cast<uint32_t*>(&q);
+    const uint32_t both = static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(&off)) * 0x10001u;
+#pragma unroll
+    for (int e = 0; e < VEC / 2; ++e) {
+      const uint32_t m = (on >> (2 * e) & 1u) * 0xffffu | (on >> (2 * e + 1) & 1u) * 0xffff0000u;
+      w[e] = (w[e] & m) | (both & ~m);
+    }
+  }
+}
+
+// Grid (chunks of kUnroll * kCopyThreads packs, rows).
 template <typename T, bool kBackward>
-__global__ void __launch_bounds__(kThreads) process_kernel(ProcessLogits a, int parts) {
-  extern __shared__ uint32_t table[];   // [kRange] 2 * outputs + met, then [kRange] bias slots
+__global__ void __launch_bounds__(kCopyThreads) copy_kernel(ProcessLogits a) {
   pdl_wait_prerequisites();
   pdl_launch_dependents();
-  uint32_t* count = table;
-  int* slot = reinterpret_cast<int*>(table + kRange);
+  constexpr int VEC = kVec<T>;
+  constexpr uint32_t kAll = (1u << VEC) - 1u;
+  const T off = from_f32<T>(kBackward ? 0.f : -INFINITY);
   const int words = (a.V + 31) / 32;
-  for (int64_t item = blockIdx.x; item < a.R * parts; item += gridDim.x) {
-    const int64_t r = item / parts;
-    const int c0 = static_cast<int>(item - r * parts) * kRange;
-    const int n = min(kRange, a.V - c0);
-    // history of the row inside this range
+  for (int64_t r = blockIdx.y; r < a.R; r += gridDim.y) {
+    const uint32_t* mask = nullptr;
+    if (a.allowed) {
+      const int64_t m = a.allowed_rows ? a.allowed_rows[r] : r;
+      if (m >= 0 && m < a.M) mask = a.allowed + m * words;
+    }
+    const T* const src = kBackward ? static_cast<const T*>(a.grad) + r * a.grad_ld
+                                   : static_cast<const T*>(a.logits) + r * a.ld;
+    T* const dst = static_cast<T*>(a.out) + r * a.out_ld;
+    const bool in_place = src == dst;
+    if (in_place && !mask) continue;
+    auto allowed = [&](int c) { return !mask || (mask[c >> 5] >> (c & 31) & 1u); };
+    if (!same_offset16(src, static_cast<const T*>(dst))) {
+      constexpr int kChunk = kUnroll * kCopyThreads * VEC;
+      const int64_t end = min(static_cast<int64_t>(blockIdx.x + 1) * kChunk, static_cast<int64_t>(a.V));
+#pragma unroll 4
+      for (int64_t c = static_cast<int64_t>(blockIdx.x) * kChunk + threadIdx.x; c < end; c += kCopyThreads)
+        dst[c] = allowed(static_cast<int>(c)) ? src[c] : off;
+      continue;
+    }
+    const int head = min(to_boundary(src), a.V), packs = (a.V - head) / VEC;
+    const int tail = head + packs * VEC;
+    if (blockIdx.x == 0) {   // what lies before the first and after the last pack
+      const int i = threadIdx.x < head ? threadIdx.x : tail + static_cast<int>(threadIdx.x) - head;
+      if (i < a.V && static_cast<int>(threadIdx.x) < 2 * VEC) dst[i] = allowed(i) ? src[i] : off;
+    }
+    const Pack<T, VEC>* const from = reinterpret_cast<const Pack<T, VEC>*>(src + head);
+    Pack<T, VEC>* const to = reinterpret_cast<Pack<T, VEC>*>(dst + head);
+    const int k0 = blockIdx.x * (kUnroll * kCopyThreads) + threadIdx.x;
+    Pack<T, VEC> q[kUnroll];
+    uint32_t on[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int k = k0 + u * kCopyThreads;
+      on[u] = kAll;
+      if (k >= packs) continue;
+      if (mask) on[u] = mask_bits(mask, head + k * VEC, VEC, a.V) & kAll;
+      if (on[u] && !(in_place && on[u] == kAll)) q[u] = from[k];
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int k = k0 + u * kCopyThreads;
+      if (k >= packs || (in_place && on[u] == kAll)) continue;
+      if (mask) keep_allowed<T, VEC>(q[u], on[u], off);
+      to[k] = q[u];
+    }
+  }
+}
+
+// Shared memory: bitmap [range / 32], rank of each word's first bit [range / 32],
+// then per id of the window: column, 2 * outputs + met, and with biases 1 + the
+// last entry's index.  Grid (column ranges, rows).
+template <typename T, bool kBackward>
+__global__ void __launch_bounds__(kThreads) rewrite_kernel(ProcessLogits a, int range) {
+  extern __shared__ __align__(16) uint32_t bitmap[];
+  __shared__ int red[kWarps], carry;
+  pdl_wait_prerequisites();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t* const rank = bitmap + range / 32;
+  uint32_t* const column = rank + range / 32;
+  uint32_t* const count = column + kWindow;
+  uint32_t* const slot = count + kWindow;
+  const int c0 = range * static_cast<int>(blockIdx.x), n = min(range, a.V - c0);
+  const int map_words = (n + 31) / 32, mask_words = (a.V + 31) / 32;
+  for (int64_t r = blockIdx.y; r < a.R; r += gridDim.y) {
     int64_t p0 = 0, p1 = 0, p2 = 0;
     if (a.tokens) {
       p0 = min(max(a.spans[3 * r], int64_t{0}), a.n_tokens);
       p1 = min(max(a.spans[3 * r + 1], p0), a.n_tokens);
       p2 = min(max(a.spans[3 * r + 2], p1), a.n_tokens);
     }
-    int64_t b0 = 0, b1 = 0;
+    int64_t b0 = 0, biases = 0;
     if (!kBackward && a.bias_offsets) {
       b0 = min(max(a.bias_offsets[r], int64_t{0}), a.n_bias);
-      b1 = min(max(a.bias_offsets[r + 1], b0), a.n_bias);
+      biases = min(max(a.bias_offsets[r + 1], b0), a.n_bias) - b0;
     }
-    const bool history = p2 > p0, biased = b1 > b0;
-    __syncthreads();   // the previous item's table is no longer read
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-      count[i] = 0;
-      if (biased) slot[i] = 0;
-    }
+    if (p2 == p0 && biases == 0) continue;
+    const int32_t* const bias_ids = a.bias_ids + b0;
+    // each(id) for the tokens [from, to), 16 bytes per load
+    auto scan = [&](int64_t from, int64_t to, auto&& each) {
+      const int64_t q0 = min(from + to_boundary(a.tokens + from), to), q1 = q0 + (to - q0) / 4 * 4;
+      if (from + threadIdx.x < q0) each(a.tokens[from + threadIdx.x]);
+      if (q1 + threadIdx.x < to) each(a.tokens[q1 + threadIdx.x]);
+      const int4* const v4 = reinterpret_cast<const int4*>(a.tokens + q0);
+      const int64_t packs = (q1 - q0) / 4;
+#pragma unroll 4
+      for (int64_t i = threadIdx.x; i < packs; i += kThreads) {
+        const int4 v = v4[i];
+        each(v.x);
+        each(v.y);
+        each(v.z);
+        each(v.w);
+      }
+    };
+    // column of an id in this range; an id of another range, or none, gives >= n
+    auto at = [&](int id) { return static_cast<uint32_t>(id) - static_cast<uint32_t>(c0); };
+
+    // the distinct ids
+    __syncthreads();   // the previous row's readers are done
+    for (int i = threadIdx.x; i < map_words; i += kThreads) bitmap[i] = 0;
     __syncthreads();
-    for (int64_t i = p0 + threadIdx.x; i < p2; i += kThreads) {
-      const int64_t v = static_cast<int64_t>(a.tokens[i]) - c0;
-      if (v < 0 || v >= n) continue;
-      if (i < p1)
-        atomicOr(&count[v], 1u);
-      else
-        atomicAdd(&count[v], 2u);
-    }
-    // the last entry of an id wins
-    for (int64_t i = b0 + threadIdx.x; i < b1; i += kThreads) {
-      const int64_t v = static_cast<int64_t>(a.bias_ids[i]) - c0;
-      if (v >= 0 && v < n) atomicMax(&slot[v], static_cast<int>(i - b0) + 1);
-    }
+    auto mark = [&](int id) {
+      const uint32_t e = at(id);
+      if (e < static_cast<uint32_t>(n)) atomicOr(&bitmap[e >> 5], 1u << (e & 31));
+    };
+    if (p2 > p0) scan(p0, p2, mark);
+    for (int64_t j = threadIdx.x; j < biases; j += kThreads) mark(bias_ids[j]);
+    if (threadIdx.x == 0) carry = 0;
     __syncthreads();
+    // ranks: 512 words at a time
+    for (int base = 0; base < map_words; base += kThreads) {
+      const int i = base + threadIdx.x;
+      const int ones = i < map_words ? __popc(bitmap[i]) : 0;
+      int upto = ones;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
+      }
+      if (lane == 31) red[warp] = upto;
+      const int before = carry;
+      __syncthreads();
+      int sum = lane < kWarps ? red[lane] : 0;
+#pragma unroll
+      for (int o = 1; o < kWarps; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += x;
+      }
+      const int warps_before = warp ? __shfl_sync(0xffffffffu, sum, warp - 1) : 0;
+      const int all = __shfl_sync(0xffffffffu, sum, kWarps - 1);
+      if (i < map_words) rank[i] = before + warps_before + upto - ones;
+      if (threadIdx.x == 0) carry = before + all;
+      __syncthreads();
+    }
+    const int distinct = carry;
+    auto rank_of = [&](uint32_t e) {
+      return rank[e >> 5] + __popc(bitmap[e >> 5] & ((1u << (e & 31)) - 1u));
+    };
+
     const uint32_t* mask = nullptr;
     if (a.allowed) {
       const int64_t m = a.allowed_rows ? a.allowed_rows[r] : r;
-      if (m >= 0 && m < a.M) mask = a.allowed + m * words;
+      if (m >= 0 && m < a.M) mask = a.allowed + m * mask_words;
     }
     const float rho = a.repetition ? a.repetition[r] : 1.f;
     const float fr = a.frequency ? a.frequency[r] : 0.f;
     const float pr = a.presence ? a.presence[r] : 0.f;
-    const T* x = static_cast<const T*>(a.logits) + r * a.ld + c0;
-    const T* g = static_cast<const T*>(a.grad) + r * a.grad_ld + c0;
-    T* out = static_cast<T*>(a.out) + r * a.out_ld + c0;
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-      const int c = c0 + i;
-      const bool on = !mask || (mask[c >> 5] >> (c & 31) & 1u);
-      float v;
-      if (!on) {
-        v = kBackward ? 0.f : -INFINITY;
-      } else {
-        v = to_f32(kBackward ? g[i] : x[i]);
-        const uint32_t met = history ? count[i] : 0u;
+    const T* const xr = static_cast<const T*>(a.logits) + r * a.ld;
+    T* const dst = static_cast<T*>(a.out) + r * a.out_ld;
+    for (int first = 0; first < distinct; first += kWindow) {
+      const uint32_t here = min(kWindow, distinct - first);
+      if (first) __syncthreads();
+      for (uint32_t i = threadIdx.x; i < here; i += kThreads) {
+        count[i] = 0;
+        if (biases) slot[i] = 0;
+      }
+      for (int i = threadIdx.x; i < map_words; i += kThreads) {
+        uint32_t bits = bitmap[i];
+        for (uint32_t k = rank[i] - first; bits; bits &= bits - 1, ++k)
+          if (k < here) column[k] = 32 * i + __ffs(bits) - 1;
+      }
+      __syncthreads();
+      auto count_in = [&](int id, bool output) {
+        const uint32_t e = at(id);
+        if (e >= static_cast<uint32_t>(n)) return;
+        const uint32_t k = rank_of(e) - first;
+        if (k >= here) return;
+        if (output)
+          atomicAdd(&count[k], 2u);
+        else
+          atomicOr(&count[k], 1u);
+      };
+      if (p1 > p0) scan(p0, p1, [&](int id) { count_in(id, false); });
+      if (p2 > p1) scan(p1, p2, [&](int id) { count_in(id, true); });
+      for (int64_t j = threadIdx.x; j < biases; j += kThreads) {   // the last entry counts
+        const uint32_t e = at(bias_ids[j]);
+        if (e >= static_cast<uint32_t>(n)) continue;
+        const uint32_t k = rank_of(e) - first;
+        if (k < here) atomicMax(&slot[k], static_cast<uint32_t>(j) + 1u);
+      }
+      __syncthreads();
+#pragma unroll 4
+      for (uint32_t k = threadIdx.x; k < here; k += kThreads) {
+        const int c = c0 + static_cast<int>(column[k]);
+        if (mask && !(mask[c >> 5] >> (c & 31) & 1u)) continue;
+        const uint32_t met = count[k];
+        float v = to_f32(dst[c]);
         if (met) {
-          const bool positive = (kBackward ? to_f32(x[i]) : v) > 0.f;
+          const bool positive = (kBackward ? to_f32(xr[c]) : v) > 0.f;
           v = positive ? v / rho : v * rho;
           if (!kBackward && met > 1u) v -= fmaf(fr, static_cast<float>(met >> 1), pr);
         }
-        if (!kBackward && biased && slot[i]) v += a.bias_values[b0 + slot[i] - 1];
+        if (!kBackward && biases && slot[k]) v += a.bias_values[b0 + slot[k] - 1];
+        dst[c] = from_f32<T>(v);
       }
-      out[i] = from_f32<T>(v);
     }
   }
 }
 
 template <typename T, bool kBackward>
 cudaError_t run(const ProcessLogits& a, cudaStream_t s) {
+  const unsigned rows = static_cast<unsigned>(a.R < 32768 ? a.R : 32768);
+  const void* in = kBackward ? a.grad : a.logits;
+  const bool in_place = in == a.out && (kBackward ? a.grad_ld : a.ld) == a.out_ld;
+  if (!in_place || a.allowed) {
+    constexpr int kChunk = kUnroll * kCopyThreads * kVec<T>;
+    const unsigned chunks = static_cast<unsigned>((static_cast<int64_t>(a.V) + kChunk - 1) / kChunk);
+    const cudaError_t e = launch_dependent(copy_kernel<T, kBackward>, dim3(chunks, rows),
+                                           kCopyThreads, 0, 1, s, a);
+    if (e != cudaSuccess) return e;
+  }
+  if (!a.tokens && !a.bias_offsets) return cudaSuccess;
   static std::atomic<int> ready[64];
-  auto* kern = process_kernel<T, kBackward>;
+  auto* kern = rewrite_kernel<T, kBackward>;
   const cudaError_t e = allow_shared(ready, reinterpret_cast<const void*>(kern),
-                                     2 * kRange * sizeof(uint32_t));
+                                     2 * kMostColumns / 8 + 3 * 4 * kWindow);
   if (e != cudaSuccess) return e;
-  const int parts = (a.V + kRange - 1) / kRange;
-  const int64_t items = a.R * parts;
-  const int grid = static_cast<int>(items < (1 << 20) ? items : (1 << 20));
-  const size_t smem = (a.bias_offsets ? 2 : 1) * kRange * sizeof(uint32_t);
-  return launch_dependent(kern, dim3(grid), kThreads, smem, 1, s, a, parts);
+  const int64_t padded = (static_cast<int64_t>(a.V) + 31) / 32 * 32;
+  const int range = static_cast<int>(padded < kMostColumns ? padded : kMostColumns);
+  const unsigned ranges = static_cast<unsigned>((padded + range - 1) / range);
+  const size_t smem = 2 * static_cast<size_t>(range) / 8 + (a.bias_offsets ? 3 : 2) * 4 * kWindow;
+  return launch_dependent(kern, dim3(ranges, rows), kThreads, smem, 1, s, a, range);
 }
 
 template <typename T>
