@@ -18,7 +18,12 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBwdCols = 16384;   // columns per CTA in the backward
+constexpr int kUnroll = 4;         // backward: 16-byte accesses in flight per thread
+constexpr int kBwdBytes = 32768;   // backward: logits per CTA
+constexpr int kFwdThreads = 512;   // forward on held logits
+constexpr int kFwdUnroll = 4;
+constexpr int kMaxCluster = 8;
+constexpr int kMaxWarps = kFwdThreads / 32;
 
 // Row of the student's table that an entry names: negative ids wrap; -1 for
 // an id outside [-V, V).
@@ -33,8 +38,7 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
   float t = 0.f;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) t += red[w];
+  for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) t += red[w];
   return t;
 }
 
@@ -44,8 +48,7 @@ __device__ __forceinline__ float block_max(float v, float* red) {
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
   float t = red[0];
-#pragma unroll
-  for (int w = 1; w < kWarps; ++w) t = fmaxf(t, red[w]);
+  for (int w = 1; w < static_cast<int>(blockDim.x >> 5); ++w) t = fmaxf(t, red[w]);
   return t;
 }
 
@@ -60,15 +63,15 @@ __device__ float teacher_row(const Teacher& te, int64_t t, float* p, float* logp
     base = te.lse[t];
   } else {
     float m = -INFINITY;
-    for (int k = threadIdx.x; k < te.K; k += kThreads) m = fmaxf(m, a[k] / te.tau);
+    for (int k = threadIdx.x; k < te.K; k += static_cast<int>(blockDim.x)) m = fmaxf(m, a[k] / te.tau);
     m = block_max(m, red);
     float s = 0.f;
     base = m == -INFINITY ? 0.f : m;
-    for (int k = threadIdx.x; k < te.K; k += kThreads) s += expf(a[k] / te.tau - base);
+    for (int k = threadIdx.x; k < te.K; k += static_cast<int>(blockDim.x)) s += expf(a[k] / te.tau - base);
     rest = logf(block_sum(s, red));
   }
   float P = 0.f;
-  for (int k = threadIdx.x; k < te.K; k += kThreads) {
+  for (int k = threadIdx.x; k < te.K; k += static_cast<int>(blockDim.x)) {
     const bool absent = a[k] == -INFINITY;   // L is -inf where every entry is
     const float lp = absent ? -INFINITY : (a[k] / te.tau - base) - rest;
     const float q = absent ? 0.f : expf(lp);
@@ -85,110 +88,205 @@ __device__ __forceinline__ float loss_term(float p, float logp, float z_rel) {
   return p == 0.f && z_rel == z_rel ? 0.f : p * (logp - z_rel);
 }
 
-// One CTA per row.
+// Running maximum m of the unscaled logits and s = sum 2^((x - m) c), over a
+// chunk of N values: one maximum, one rescale, then the exponentials.  -inf adds
+// exactly nothing; NaN and +inf turn s into NaN.
+template <int N>
+__device__ __forceinline__ void fold(float& m, float& s, const float (&x)[N], float c) {
+  float top = m;
+#pragma unroll
+  for (int j = 0; j < N; ++j) top = fmaxf(top, x[j]);
+  const float base = top == -INFINITY ? 0.f : top;
+  if (top > m) {
+    s *= ex2_approx((m - base) * c);
+    m = top;
+  }
+  // subtracted first: x c and base c overflow for a mask of the type's lowest value
+#pragma unroll
+  for (int j = 0; j < N; ++j) s += ex2_approx((x[j] - base) * c);
+}
+
+// A cluster of CTAs per row (one CTA when there are rows enough), each with a
+// range of its columns; ranks above 0 hand their maximum and sum to rank 0 in
+// distributed shared memory, and rank 0 adds the teacher's side.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) logits_fwd_kernel(DistillLogits a) {
+__global__ void __launch_bounds__(kFwdThreads) logits_fwd_kernel(DistillLogits a) {
+  extern __shared__ float teacher[];   // p [K], log p [K]
+  __shared__ float red[kMaxWarps], red_m[kMaxWarps];
+  __shared__ float joined[2][2 * kMaxCluster];   // by row parity: maxima, sums
   pdl_wait_prerequisites();
   pdl_launch_dependents();
-  __shared__ float red[kWarps], red_m[kWarps];
-  __shared__ float p[kMaxTeacher], logp[kMaxTeacher];
+  constexpr int VEC = kVec<T>;
+  uint32_t size;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(size));
+  const uint32_t rank = cluster_cta_rank();
+  const int K = a.teacher.K;
+  float* const p = teacher;
+  float* const logp = teacher + K;
   const float c = kLog2e / a.tau;
-  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+  int flip = 0;
+  for (int64_t t = blockIdx.x / size; t < a.T; t += gridDim.x / size, flip ^= 1) {
     if (a.mask && !a.mask[t]) {
-      if (threadIdx.x == 0) {
+      if (rank == 0 && threadIdx.x == 0) {
         a.loss[t] = 0.f;
         a.lse[t] = 0.f;
       }
       continue;
     }
     const T* row = static_cast<const T*>(a.logits) + t * a.ld;
-    const float P = teacher_row(a.teacher, t, p, logp, red);
-    // running maximum m (of the unscaled logits) and s = sum 2^((x - m) c)
+    const float P = rank == 0 ? teacher_row(a.teacher, t, p, logp, red) : 0.f;
     float m = -INFINITY, s = 0.f;
-    for (int i = threadIdx.x; i < a.V; i += kThreads) {
-      const float x = to_f32(row[i]);
-      const float mn = fmaxf(m, x);
-      const float base = mn == -INFINITY ? 0.f : mn;
-      s = s * ex2_approx((m - base) * c) + ex2_approx((x - base) * c);
-      m = mn;
+    const int head = min(to_boundary(row), a.V), packs = (a.V - head) / VEC;
+    const int k1 = static_cast<int>(static_cast<int64_t>(packs) * (rank + 1) / size);
+    if (rank == 0) {   // before the first and after the last pack
+      const int tail = head + packs * VEC;
+      const int i = threadIdx.x < head ? threadIdx.x : tail + static_cast<int>(threadIdx.x) - head;
+      if (i < a.V && static_cast<int>(threadIdx.x) < 2 * VEC) {
+        const float x[1] = {to_f32(row[i])};
+        fold(m, s, x, c);
+      }
     }
-    const float M = block_max(m, red_m);
-    const float base = M == -INFINITY ? 0.f : M;
-    const float S = block_sum(s * ex2_approx((m - base) * c), red);
+    const Pack<T, VEC>* const from = reinterpret_cast<const Pack<T, VEC>*>(row + head);
+    int k = static_cast<int>(static_cast<int64_t>(packs) * rank / size) + threadIdx.x;
+    for (; k + (kFwdUnroll - 1) * kFwdThreads < k1; k += kFwdUnroll * kFwdThreads) {
+      Pack<T, VEC> q[kFwdUnroll];
+#pragma unroll
+      for (int u = 0; u < kFwdUnroll; ++u) q[u] = from[k + u * kFwdThreads];
+#pragma unroll
+      for (int u = 0; u < kFwdUnroll; u += 8 / VEC > 1 ? 2 : 1) {
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = to_f32(q[u + j / VEC].v[j % VEC]);
+        fold(m, s, x, c);
+      }
+    }
+    for (; k < k1; k += kFwdThreads) {
+      const Pack<T, VEC> q = from[k];
+      float x[VEC];
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) x[j] = to_f32(q.v[j]);
+      fold(m, s, x, c);
+    }
+    float M = block_max(m, red_m);
+    float base = M == -INFINITY ? 0.f : M;
+    float S = block_sum(s * ex2_approx((m - base) * c), red);
+    if (size > 1) {
+      if (threadIdx.x == 0) {
+        const uint32_t to = map_to_cta(smem_addr(&joined[flip][rank]), 0);
+        st_shared_remote(to, __float_as_int(M));
+        st_shared_remote(to + 4 * kMaxCluster, __float_as_int(S));
+      }
+      cluster_sync();
+      if (rank) continue;
+      M = -INFINITY;
+      for (uint32_t j = 0; j < size; ++j) M = fmaxf(M, joined[flip][j]);
+      base = M == -INFINITY ? 0.f : M;
+      S = 0.f;
+      for (uint32_t j = 0; j < size; ++j)
+        S = fmaf(joined[flip][kMaxCluster + j], ex2_approx((joined[flip][j] - base) * c), S);
+    }
     // loss relative to the maximum, so that large logits do not cancel
-    const float mz = M / a.tau, ln_s = logf(S);
+    const float ln_s = logf(S);
     float term = 0.f;
-    for (int k = threadIdx.x; k < a.teacher.K; k += kThreads) {
-      if (logp[k] == -INFINITY) continue;
-      const int v = wrap_id(a.teacher.ids[t * a.teacher.K + k], a.V);
-      term += loss_term(p[k], logp[k], v < 0 ? __int_as_float(0x7fc00000)
+    for (int j = threadIdx.x; j < K; j += kFwdThreads) {
+      if (logp[j] == -INFINITY) continue;
+      const int v = wrap_id(a.teacher.ids[t * K + j], a.V);
+      term += loss_term(p[j], logp[j], v < 0 ? __int_as_float(0x7fc00000)
                                              : (to_f32(row[v]) - M) / a.tau);
     }
     const float A = block_sum(term, red);
     if (threadIdx.x == 0) {
-      a.lse[t] = mz + ln_s;
+      a.lse[t] = M / a.tau + ln_s;
       a.loss[t] = P == 0.f ? 0.f : fmaf(P, ln_s, A);
     }
-    __syncthreads();
   }
 }
 
-// g (P q_v - taken) / tau for one logit; non-finite logits get zero.
-__device__ __forceinline__ float cotangent(float x, float inv_tau, float lse, float gP,
-                                           float taken) {
-  if (!isfinite(x)) return 0.f;
-  const float q = ex2_approx(fmaf(x, inv_tau, -lse) * kLog2e);
-  return fmaf(gP, q, -taken);
-}
-
-// CTA (row, column range).  The K places of the range are computed from the
+// CTA (column range, row).  The K places of the range are computed from the
 // logits before the dense pass (d_logits may be the logits buffer) and
 // written after it.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) logits_bwd_kernel(DistillLogits a, int parts) {
+__global__ void __launch_bounds__(kThreads, 6) logits_bwd_kernel(DistillLogits a, int range) {
+  extern __shared__ float teacher[];   // p [K], log p [K], id [K]
+  __shared__ float red[kWarps];
   pdl_wait_prerequisites();
   pdl_launch_dependents();
-  __shared__ float red[kWarps];
-  __shared__ float p[kMaxTeacher], logp[kMaxTeacher];
-  __shared__ int id[kMaxTeacher];
+  constexpr int VEC = kVec<T>;
   const int K = a.teacher.K;
+  float* const p = teacher;
+  float* const logp = teacher + K;
+  int* const id = reinterpret_cast<int*>(teacher + 2 * K);
   const float inv_tau = 1.f / a.tau;
-  for (int64_t w = blockIdx.x; w < a.T * parts; w += gridDim.x) {
-    const int64_t t = w / parts;
-    const int c0 = static_cast<int>(w - t * parts) * kBwdCols;
-    const int c1 = min(a.V, c0 + kBwdCols);
-    const T* row = static_cast<const T*>(a.logits) + t * a.ld;
-    T* out = static_cast<T*>(a.d_logits) + t * a.d_ld;
+  // 1 / tau = inv_tau + inv_lo to 48 bits: the exponent is off by its own rounding only
+  const float inv_lo = fmaf(-a.tau, inv_tau, 1.f) * inv_tau;
+  const int c0 = blockIdx.x * range, n = min(range, a.V - c0);
+  for (int64_t t = blockIdx.y; t < a.T; t += gridDim.y) {
+    const T* const src = static_cast<const T*>(a.logits) + t * a.ld + c0;
+    T* const dst = static_cast<T*>(a.d_logits) + t * a.d_ld + c0;
     const bool scored = !a.mask || a.mask[t];
     const float P = scored ? teacher_row(a.teacher, t, p, logp, red) : 0.f;
-    if (P == 0.f) {
-      for (int i = c0 + threadIdx.x; i < c1; i += kThreads) out[i] = from_f32<T>(0.f);
-      __syncthreads();
-      continue;
-    }
-    for (int k = threadIdx.x; k < K; k += kThreads)
-      id[k] = logp[k] == -INFINITY ? -1 : wrap_id(a.teacher.ids[t * K + k], a.V);
-    __syncthreads();
-    const float g = a.grad[t] * inv_tau, lse = a.lse[t], gP = g * P;
+    const bool some = P != 0.f;   // NaN counts as some
+    const float g = some ? a.grad[t] * inv_tau : 0.f, lse = some ? a.lse[t] : 0.f, gP = g * P;
+    auto dense = [&](float x) {
+      if (!(fabsf(x) < INFINITY)) return 0.f;   // NaN and infinities
+      return gP * ex2_approx(fmaf(x, inv_tau, fmaf(x, inv_lo, -lse)) * kLog2e);
+    };
     float fixed[kMaxTeacher / kThreads];
+    if (some) {
+      for (int k = threadIdx.x; k < K; k += kThreads) {
+        const int v = logp[k] == -INFINITY ? -1 : wrap_id(a.teacher.ids[t * K + k], a.V);
+        id[k] = v < c0 || v >= c0 + n ? -1 : v - c0;
+      }
+      __syncthreads();
 #pragma unroll
-    for (int j = 0; j < kMaxTeacher / kThreads; ++j) {
-      const int k = threadIdx.x + j * kThreads;
-      fixed[j] = 0.f;
-      if (k < K && id[k] >= c0 && id[k] < c1) {
+      for (int j = 0; j < kMaxTeacher / kThreads; ++j) {
+        const int k = threadIdx.x + j * kThreads;
+        if (k >= K || id[k] < 0) continue;
         float taken = 0.f;   // repeated ids add up; each writes the same value
         for (int i = 0; i < K; ++i) taken += id[i] == id[k] ? p[i] : 0.f;
-        fixed[j] = cotangent(to_f32(row[id[k]]), inv_tau, lse, gP, g * taken);
+        const float x = to_f32(src[id[k]]);
+        fixed[j] = fabsf(x) < INFINITY ? fmaf(-g, taken, dense(x)) : 0.f;
       }
+      __syncthreads();   // in place, the dense pass overwrites what was read
     }
-    __syncthreads();
-    for (int i = c0 + threadIdx.x; i < c1; i += kThreads)
-      out[i] = from_f32<T>(cotangent(to_f32(row[i]), inv_tau, lse, gP, 0.f));
-    __syncthreads();
+    if (same_offset16(src, static_cast<const T*>(dst))) {
+      const int head = min(to_boundary(src), n), packs = (n - head) / VEC;
+      const int tail = head + packs * VEC;
+      const int i = threadIdx.x < head ? threadIdx.x : tail + static_cast<int>(threadIdx.x) - head;
+      if (i < n && static_cast<int>(threadIdx.x) < 2 * VEC)
+        dst[i] = from_f32<T>(some ? dense(to_f32(src[i])) : 0.f);
+      const Pack<T, VEC>* const from = reinterpret_cast<const Pack<T, VEC>*>(src + head);
+      Pack<T, VEC>* const to = reinterpret_cast<Pack<T, VEC>*>(dst + head);
+      if (!some) {
+        Pack<T, VEC> zero;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) zero.v[e] = from_f32<T>(0.f);
+        for (int k = threadIdx.x; k < packs; k += kThreads) to[k] = zero;
+      } else {
+        for (int k0 = threadIdx.x; k0 < packs; k0 += kUnroll * kThreads) {
+          Pack<T, VEC> q[kUnroll];
+#pragma unroll
+          for (int u = 0; u < kUnroll; ++u)
+            if (k0 + u * kThreads < packs) q[u] = from[k0 + u * kThreads];
+#pragma unroll
+          for (int u = 0; u < kUnroll; ++u) {
+            if (k0 + u * kThreads >= packs) continue;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) q[u].v[e] = from_f32<T>(dense(to_f32(q[u].v[e])));
+            to[k0 + u * kThreads] = q[u];
+          }
+        }
+      }
+    } else {
+      for (int i = threadIdx.x; i < n; i += kThreads)
+        dst[i] = from_f32<T>(some ? dense(to_f32(src[i])) : 0.f);
+    }
+    __syncthreads();   // also: the teacher's arrays are free again
+    if (!some) continue;
 #pragma unroll
     for (int j = 0; j < kMaxTeacher / kThreads; ++j) {
       const int k = threadIdx.x + j * kThreads;
-      if (k < K && id[k] >= c0 && id[k] < c1) out[id[k]] = from_f32<T>(fixed[j]);
+      if (k < K && id[k] >= 0) dst[id[k]] = from_f32<T>(fixed[j]);
     }
     __syncthreads();
   }
@@ -327,17 +425,25 @@ __global__ void __launch_bounds__(kThreads)
 
 template <typename T>
 cudaError_t logits_fwd(const DistillLogits& a, cudaStream_t s) {
-  const int64_t cap = static_cast<int64_t>(sm_count()) * 8;
-  return launch_dependent(logits_fwd_kernel<T>, dim3(static_cast<int>(a.T < cap ? a.T : cap)),
-                          kThreads, 0, 1, s, a);
+  // Split rows while they are few: two CTAs per SM or more, and 8 KB or more of a
+  // row for each.
+  const int64_t bytes = static_cast<int64_t>(a.V) * static_cast<int64_t>(sizeof(T));
+  int size = 1;
+  while (size < kMaxCluster && a.T * size < 4ll * sm_count() && bytes / (2 * size) >= 8192) size *= 2;
+  const int64_t rows = a.T < (1 << 20) ? a.T : (1 << 20);
+  return launch_dependent(logits_fwd_kernel<T>, dim3(static_cast<unsigned>(rows * size)), kFwdThreads,
+                          2 * sizeof(float) * a.teacher.K, size, s, a);
 }
 
 template <typename T>
 cudaError_t logits_bwd(const DistillLogits& a, cudaStream_t s) {
-  const int parts = (a.V + kBwdCols - 1) / kBwdCols;
-  const int64_t cap = static_cast<int64_t>(sm_count()) * 16, items = a.T * parts;
-  return launch_dependent(logits_bwd_kernel<T>, dim3(static_cast<int>(items < cap ? items : cap)),
-                          kThreads, 0, 1, s, a, parts);
+  const int most = kBwdBytes / static_cast<int>(sizeof(T));
+  const int ranges = static_cast<int>((static_cast<int64_t>(a.V) + most - 1) / most);
+  const int range = ((a.V + ranges - 1) / ranges + 63) / 64 * 64;
+  const unsigned rows = static_cast<unsigned>(a.T < 32768 ? a.T : 32768);
+  return launch_dependent(logits_bwd_kernel<T>,
+                          dim3(static_cast<unsigned>((a.V + range - 1) / range), rows), kThreads,
+                          3 * sizeof(float) * a.teacher.K, 1, s, a, range);
 }
 
 }  // namespace
