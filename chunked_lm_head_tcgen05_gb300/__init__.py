@@ -825,6 +825,15 @@ def distill_backward(hidden, weight, top_ids, top_logits, loss_mask, temperature
     return d_hidden, d_weight
 
 
+def _rows_like(t):
+    """A new matrix with t's rows as far apart as t's are (so both sides of a call have the
+    same alignment, padded rows included)."""
+    import torch
+    rows, cols = t.shape
+    return torch.empty_strided((rows, cols), (max(t.stride(0), cols), 1), dtype=t.dtype,
+                               device=t.device)
+
+
 def distill_logits_forward(logits, top_ids, top_logits, loss_mask=None, temperature=1.0,
                            teacher_temperature=1.0, teacher_lse=None, stream=None):
     """Distillation loss on held logits [T, V] (fp32, bf16 or fp16, rows may be padded).
@@ -843,10 +852,10 @@ def distill_logits_forward(logits, top_ids, top_logits, loss_mask=None, temperat
 def distill_logits_backward(logits, top_ids, top_logits, loss_mask, temperature,
                             teacher_temperature, grad_loss, lse, teacher_lse=None, d_logits=None,
                             stream=None):
-    """Returns d_logits [T, V] of the logits' type (``d_logits=logits`` overwrites them)."""
-    import torch
+    """Returns d_logits [T, V] of the logits' type, laid out like the logits
+    (``d_logits=logits`` overwrites them)."""
     if d_logits is None:
-        d_logits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        d_logits = _rows_like(logits)
     rc = lmhead_distill_logits_bwd(logits, top_ids, top_logits, teacher_lse, loss_mask,
                                    temperature, teacher_temperature, grad_loss, lse, d_logits,
                                    stream)
@@ -894,11 +903,10 @@ def layernorm_backward(dy, x, weight, mean, rstd, with_bias=True, d_weight=None,
 def process_logits(logits, tokens=None, spans=None, repetition=None, frequency=None,
                    presence=None, bias_offsets=None, bias_ids=None, bias_values=None,
                    allowed=None, allowed_rows=None, out=None, stream=None):
-    """Penalties, biases and a grammar mask on logits [R, V]; returns the processed logits
-    (``out=logits`` processes them in place)."""
-    import torch
+    """Penalties, biases and a grammar mask on logits [R, V]; returns the processed logits, laid
+    out like the logits (``out=logits`` processes them in place)."""
     if out is None:
-        out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        out = _rows_like(logits)
     rc = lmhead_process_logits_fwd(logits, tokens, spans, repetition, frequency, presence,
                                    bias_offsets, bias_ids, bias_values, allowed, allowed_rows,
                                    out, stream)
@@ -909,10 +917,10 @@ def process_logits(logits, tokens=None, spans=None, repetition=None, frequency=N
 
 def process_logits_backward(grad_out, logits, tokens=None, spans=None, repetition=None,
                             allowed=None, allowed_rows=None, d_logits=None, stream=None):
-    """Cotangent of the original logits (``d_logits=grad_out`` overwrites the cotangent)."""
-    import torch
+    """Cotangent of the original logits, laid out like grad_out (``d_logits=grad_out``
+    overwrites it)."""
     if d_logits is None:
-        d_logits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        d_logits = _rows_like(grad_out)
     rc = lmhead_process_logits_bwd(grad_out, logits, tokens, spans, repetition, allowed,
                                    allowed_rows, d_logits, stream)
     if rc:

@@ -52,6 +52,74 @@ __device__ __forceinline__ bool same_offset16(const T* a, const T* b) {
   return ((reinterpret_cast<uintptr_t>(a) ^ reinterpret_cast<uintptr_t>(b)) & 15u) == 0;
 }
 
+// Two fp32 operations in one instruction (sm_100 and later), each rounded on its own.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(r))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return r;
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(r))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return r;
+}
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(r))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)),
+        "l"(reinterpret_cast<uint64_t&>(c)));
+  return r;
+}
+
+// Elements 2 i and 2 i + 1 of a pack.
+template <int VEC>
+__device__ __forceinline__ float2 pair_of(const Pack<float, VEC>& q, int i) {
+  return make_float2(q.v[2 * i], q.v[2 * i + 1]);
+}
+template <int VEC>
+__device__ __forceinline__ float2 pair_of(const Pack<__nv_bfloat16, VEC>& q, int i) {
+  const uint32_t w = reinterpret_cast<const uint32_t*>(&q)[i];   // bf16 is the upper half of fp32
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+template <int VEC>
+__device__ __forceinline__ float2 pair_of(const Pack<__half, VEC>& q, int i) {
+  return __half22float2(reinterpret_cast<const __half2*>(&q)[i]);
+}
+
+template <int VEC>
+__device__ __forceinline__ void set_pair(Pack<float, VEC>& q, int i, float2 x) {
+  q.v[2 * i] = x.x;
+  q.v[2 * i + 1] = x.y;
+}
+template <int VEC>
+__device__ __forceinline__ void set_pair(Pack<__nv_bfloat16, VEC>& q, int i, float2 x) {
+  reinterpret_cast<__nv_bfloat162*>(&q)[i] = __floats2bfloat162_rn(x.x, x.y);
+}
+template <int VEC>
+__device__ __forceinline__ void set_pair(Pack<__half, VEC>& q, int i, float2 x) {
+  reinterpret_cast<__half2*>(&q)[i] = __floats2half2_rn(x.x, x.y);
+}
+
+// Asynchronous 16-byte copy into shared memory; a thread that reads back only
+// what it copied itself needs no barrier.
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void copy_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
