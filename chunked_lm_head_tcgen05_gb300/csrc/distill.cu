@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kFwdThreads) logits_fwd_kernel(DistillLogits a
     const int k1 = static_cast<int>(static_cast<int64_t>(packs) * (rank + 1) / size);
     auto fetch = [&](int i) {   // the thread's i-th pack, if there is one
       const int k = k0 + i * threads;
-      if (k < k1) copy_async16(ring_addr + (i % kFwdDepth) * 16 * threads, from + k);
+      if (k < k1) copy_async<16>(ring_addr + (i % kFwdDepth) * 16 * threads, from + k);
       copy_async_commit();
     };
 #pragma unroll
@@ -195,8 +195,6 @@ __global__ void __launch_bounds__(kFwdThreads) logits_fwd_kernel(DistillLogits a
       const Pack<T, VEC> q0 = ring[(i % kFwdDepth) * threads];
       if (i + 1 < mine) {
         const Pack<T, VEC> q1 = ring[((i + 1) % kFwdDepth) * threads];
-        fetch(i + kFwdDepth);
-        fetch(i + kFwdDepth + 1);
         float2 x[VEC];
 #pragma unroll
         for (int j = 0; j < VEC / 2; ++j) {
@@ -204,6 +202,8 @@ __global__ void __launch_bounds__(kFwdThreads) logits_fwd_kernel(DistillLogits a
           x[VEC / 2 + j] = pair_of(q1, j);
         }
         fold(m, s2, x, c);
+        fetch(i + kFwdDepth);   // into the slots just read
+        fetch(i + kFwdDepth + 1);
       } else {
         float2 x[VEC / 2];
 #pragma unroll

@@ -107,10 +107,15 @@ __device__ __forceinline__ void set_pair(Pack<__half, VEC>& q, int i, float2 x) 
   reinterpret_cast<__half2*>(&q)[i] = __floats2half2_rn(x.x, x.y);
 }
 
-// Asynchronous 16-byte copy into shared memory; a thread that reads back only
-// what it copied itself needs no barrier.
-__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// Asynchronous copy of 4, 8 or 16 bytes into shared memory; a thread that reads
+// back only what it copied itself needs no barrier.
+template <int kBytes>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+  if constexpr (kBytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(kBytes)
+                 : "memory");
 }
 __device__ __forceinline__ void copy_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
@@ -119,6 +124,38 @@ template <int N>
 __device__ __forceinline__ void copy_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+
+// Packs of VEC elements in flight, one column of slots per thread: slot s of
+// thread i lies at unit (s kParts + part) threads + i, so that a warp's accesses
+// are contiguous.
+template <typename T, int VEC>
+struct PackRing {
+  static constexpr int kBytes = static_cast<int>(sizeof(T)) * VEC;
+  static constexpr int kUnit = kBytes > 16 ? 16 : kBytes;
+  static constexpr int kParts = kBytes / kUnit;
+  static constexpr bool kAsync = kUnit >= 4;   // smaller units cannot be copied asynchronously
+  char* mine;
+  int stride;
+  __device__ __forceinline__ PackRing(void* base, int threads, int thread)
+      : mine(static_cast<char*>(base) + thread * kUnit), stride(threads * kUnit) {}
+  __device__ __forceinline__ void fetch(int slot, const T* src) const {
+#pragma unroll
+    for (int q = 0; q < kParts; ++q)
+      copy_async<kUnit>(static_cast<uint32_t>(__cvta_generic_to_shared(mine + (slot * kParts + q) * stride)),
+                        reinterpret_cast<const char*>(src) + q * kUnit);
+  }
+  __device__ __forceinline__ Pack<T, VEC> read(int slot) const {
+    constexpr int N = VEC / kParts;
+    Pack<T, VEC> out;
+#pragma unroll
+    for (int q = 0; q < kParts; ++q) {
+      const Pack<T, N> x = *reinterpret_cast<const Pack<T, N>*>(mine + (slot * kParts + q) * stride);
+#pragma unroll
+      for (int e = 0; e < N; ++e) out.v[q * N + e] = x.v[e];
+    }
+    return out;
+  }
+};
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll

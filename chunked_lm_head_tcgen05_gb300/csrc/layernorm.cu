@@ -16,10 +16,11 @@ namespace {
 
 constexpr int kFwdMaxThreads = 1024;   // forward, one CTA per row
 constexpr int kFwdWarpRows = 4;        // forward, one warp per row: rows per CTA
+constexpr int kStreamThreads = 512;    // forward with many rows: most threads per CTA
 constexpr int kBwdThreads = 512;       // backward: most threads per CTA
 constexpr int kRowThreads = 256;
 constexpr int kColThreads = 256;   // 32 columns x 8 row lanes
-constexpr int kFinishRows = 8;
+constexpr int kFinishRows = 16;
 
 __device__ __forceinline__ float load_param(const void* p, int type, int64_t i) {
   if (type == kF32) return static_cast<const float*>(p)[i];
@@ -179,20 +180,152 @@ __global__ void __launch_bounds__(kPerWarp ? 32 * kFwdWarpRows : kFwdMaxThreads)
   }
 }
 
-// Both gradients in one pass over x and dy.  A group of g threads (g a multiple
-// of 32) owns a row at a time and its threads fixed columns, so dw and db gather
-// in registers over the group's rows; the CTA's groups are joined in shared
-// memory at the end, and the CTA writes one partial row.  The next row's loads
-// are issued before this row's two sums are reduced.
-template <typename X, typename D, int VEC, int NV>
+// Many rows: a group of g threads (a multiple of 32) takes row after row, each
+// thread always the same columns, so that weight and bias stay in registers and
+// rows arrive through a ring of asynchronous copies kDepth rows deep.  One barrier
+// per row and group.  The statistics join by
+//   mean = ref + sum n_j (m_j - ref) / n,  M2 = sum M2_j + n_j (m_j - ref)^2 - n (mean - ref)^2
+// over threads and then warps, with one part's own mean as ref: both sums at once,
+// and what cancels is no larger than that part's share of M2 times the parts.
+template <typename X, typename Y, int VEC, int NV, int kDepth>
+__global__ void __launch_bounds__(kStreamThreads)
+    norm_fwd_stream_kernel(const X* __restrict__ x, int64_t x_ld, const void* __restrict__ w,
+                           const void* __restrict__ b, int param_type, int64_t N, int H, float eps,
+                           Y* __restrict__ y, int64_t y_ld, float* mean, float* rstd, int g) {
+  extern __shared__ __align__(16) char ring_bytes[];
+  __shared__ float red[2][2][kStreamThreads / 32];
+  pdl_wait_prerequisites();
+  pdl_launch_dependents();
+  const int groups = blockDim.x / g;
+  const int grp = threadIdx.x / g, i = threadIdx.x - grp * g;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = g >> 5, w0 = grp * warps;
+  const int n = H / VEC;
+  const PackRing<X, VEC> ring(ring_bytes, blockDim.x, threadIdx.x);
+  float wv[NV][VEC], bv[NV][VEC];
+  int cnt = 0;
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) wv[k][e] = bv[k][e] = 0.f;
+    if (i + k * g >= n) continue;
+    cnt += VEC;
+    load_params<VEC>(w, param_type, (i + k * g) * VEC, wv[k]);
+    if (b) load_params<VEC>(b, param_type, (i + k * g) * VEC, bv[k]);
+  }
+  const float own_cnt = static_cast<float>(cnt), own_inv = cnt ? 1.f / own_cnt : 0.f;
+  cnt = __reduce_add_sync(0xffffffffu, cnt);   // columns of this warp
+  const float inv = cnt ? 1.f / static_cast<float>(cnt) : 0.f, inv_H = 1.f / static_cast<float>(H);
+  // columns of the group's lane-th warp: the warp fills NV rounds of 32 packs, cut off at n
+  float lane_share = 0.f;
+  for (int k = 0; k < NV; ++k)
+    lane_share += static_cast<float>(VEC * min(max(n - (lane * 32 + k * g), 0), 32));
+  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+  int64_t t = static_cast<int64_t>(blockIdx.x) * groups + grp, next = t;
+  int put = 0, get = 0;
+  auto fetch = [&] {
+    if (next < N) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+        if (i + k * g < n) ring.fetch(put * NV + k, x + next * x_ld + (i + k * g) * VEC);
+    }
+    copy_async_commit();
+    next += step;
+    put = put + 1 == kDepth ? 0 : put + 1;
+  };
+#pragma unroll
+  for (int d = 0; d < kDepth; ++d) fetch();
+  for (int flip = 0; t < N; t += step, flip ^= 1) {
+    copy_async_wait<kDepth - 1>();
+    // the thread's mean and squared deviations about it
+    float2 v[NV][VEC / 2];
+    float2 s2 = make_float2(0.f, 0.f), q2 = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const bool in = i + k * g < n;
+      const Pack<X, VEC> q = ring.read(get * NV + k);
+#pragma unroll
+      for (int e = 0; e < VEC / 2; ++e) {
+        v[k][e] = in ? pair_of(q, e) : make_float2(0.f, 0.f);
+        s2 = add2(s2, v[k][e]);
+      }
+    }
+    get = get + 1 == kDepth ? 0 : get + 1;
+    const float own = (s2.x + s2.y) * own_inv;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      if (i + k * g >= n) continue;
+#pragma unroll
+      for (int e = 0; e < VEC / 2; ++e) {
+        const float2 d = add2(v[k][e], make_float2(-own, -own));
+        q2 = fma2(d, d, q2);
+      }
+    }
+    // the warp's, about lane 0's mean
+    float ref = __shfl_sync(0xffffffffu, own, 0);
+    float d = own - ref, d1 = own_cnt * d, d2 = fmaf(d1, d, q2.x + q2.y);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      d1 += __shfl_xor_sync(0xffffffffu, d1, o);
+      d2 += __shfl_xor_sync(0xffffffffu, d2, o);
+    }
+    fetch();   // into the slots just read, all of whose values are in d1 and d2
+    if (warps > 1) {   // the group's, about its first warp's mean
+      if (lane == 0) {
+        red[flip][0][warp] = fmaf(d1, inv, ref);
+        red[flip][1][warp] = fmaf(-d1 * inv, d1, d2);
+      }
+      named_bar_sync(1 + grp, g);
+      const bool have = lane < warps;
+      ref = red[flip][0][w0];
+      d = have ? red[flip][0][w0 + lane] - ref : 0.f;
+      d1 = lane_share * d;
+      d2 = have ? fmaf(d1, d, red[flip][1][w0 + lane]) : 0.f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        d1 += __shfl_xor_sync(0xffffffffu, d1, o);
+        d2 += __shfl_xor_sync(0xffffffffu, d2, o);
+      }
+    }
+    const float mu = fmaf(d1, inv_H, ref);
+    const float r = rsqrtf(fmaf(fmaf(-d1 * inv_H, d1, d2), inv_H, eps));
+    Y* out = y + t * y_ld;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      if (i + k * g >= n) continue;
+      Pack<Y, VEC> o;
+#pragma unroll
+      for (int e = 0; e < VEC / 2; ++e) {
+        const float2 xh = mul2(add2(v[k][e], make_float2(-mu, -mu)), make_float2(r, r));
+        set_pair(o, e, fma2(xh, make_float2(wv[k][2 * e], wv[k][2 * e + 1]),
+                            make_float2(bv[k][2 * e], bv[k][2 * e + 1])));
+      }
+      *reinterpret_cast<Pack<Y, VEC>*>(out + (i + k * g) * VEC) = o;
+    }
+    if (i == 0) {
+      if (mean) mean[t] = mu;
+      if (rstd) rstd[t] = r;
+    }
+  }
+  copy_async_wait<0>();
+}
+
+// Both gradients in one pass over x and dy.  A group of g threads (a multiple of
+// 32) owns a row at a time and its threads fixed columns, so dw and db gather in
+// registers over the group's rows; the CTA's groups are joined in shared memory
+// at the end, and the CTA writes one partial row.  Rows arrive through a ring of
+// asynchronous copies kDepth rows deep (kDepth = 0: units too small for such
+// copies; a row's loads are then issued before the previous row's sums).
+template <typename X, typename D, int VEC, int NV, int kDepth>
 __global__ void __launch_bounds__(kBwdThreads)
     norm_bwd_kernel(const D* __restrict__ dy, int64_t dy_ld, const X* x, int64_t x_ld,
                     const void* __restrict__ w, int param_type, const float* __restrict__ mean,
                     const float* __restrict__ rstd, int64_t N, int H, X* dx, int64_t dx_ld,
                     float* __restrict__ part_w, float* __restrict__ part_b, int g) {
-  extern __shared__ float joined[];   // [2][H] when the CTA has several groups
+  extern __shared__ __align__(16) char ring_bytes[];   // x and dy in flight; then [2][H] sums
   __shared__ float red[2][2][kBwdThreads / 32];
-  constexpr bool kKeep = VEC * NV <= 16 && NV <= 8;   // room to keep w and the next row in registers
+  constexpr bool kRing = kDepth > 0;
+  constexpr int kRegs = kRing ? 1 : NV;
+  constexpr bool kKeep = VEC * NV <= 16 && NV <= 8;   // room to keep w in registers
   pdl_wait_prerequisites();
   pdl_launch_dependents();
   const int groups = blockDim.x / g;
@@ -200,39 +333,70 @@ __global__ void __launch_bounds__(kBwdThreads)
   const int lane = threadIdx.x & 31, warps = g >> 5;
   const int n = H / VEC;
   const float inv = 1.f / static_cast<float>(H);
+  const PackRing<X, VEC> x_ring(ring_bytes, blockDim.x, threadIdx.x);
+  const PackRing<D, VEC> g_ring(ring_bytes + kDepth * NV * sizeof(X) * VEC * blockDim.x, blockDim.x,
+                                threadIdx.x);
   float aw[NV][VEC] = {}, ab[NV][VEC] = {}, wv[kKeep ? NV : 1][VEC];
   if constexpr (kKeep) {
 #pragma unroll
     for (int k = 0; k < NV; ++k)
       if (i + k * g < n) load_params<VEC>(w, param_type, (i + k * g) * VEC, wv[k]);
   }
-  Pack<X, VEC> xn[NV];
-  Pack<D, VEC> gn[NV];
-  float mn = 0.f, rn = 0.f;
+  Pack<X, VEC> xn[kRegs];
+  Pack<D, VEC> gn[kRegs];
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
-  int64_t t = static_cast<int64_t>(blockIdx.x) * groups + grp;
-  auto fetch = [&](int64_t row) {
+  int64_t t = static_cast<int64_t>(blockIdx.x) * groups + grp, next = t;
+  int put = 0, get = 0;
+  float mn = 0.f, rn = 0.f;
+  auto fetch = [&] {
+    if (next < N) {
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
-      if (i + k * g < n) {
-        xn[k] = *reinterpret_cast<const Pack<X, VEC>*>(x + row * x_ld + (i + k * g) * VEC);
-        gn[k] = *reinterpret_cast<const Pack<D, VEC>*>(dy + row * dy_ld + (i + k * g) * VEC);
+      for (int k = 0; k < NV; ++k) {
+        if (i + k * g >= n) continue;
+        const X* xs = x + next * x_ld + (i + k * g) * VEC;
+        const D* gs = dy + next * dy_ld + (i + k * g) * VEC;
+        if constexpr (kRing) {
+          x_ring.fetch(put * NV + k, xs);
+          g_ring.fetch(put * NV + k, gs);
+        } else {
+          xn[k] = *reinterpret_cast<const Pack<X, VEC>*>(xs);
+          gn[k] = *reinterpret_cast<const Pack<D, VEC>*>(gs);
+        }
       }
-    mn = mean[row];
-    rn = rstd[row];
+    }
+    if constexpr (kRing) {
+      copy_async_commit();
+      put = put + 1 == kDepth ? 0 : put + 1;
+    }
+    next += step;
   };
-  if (t < N) fetch(t);
-  int flip = 0;
-  for (; t < N; t += step, flip ^= 1) {
+#pragma unroll
+  for (int d = 0; d < (kRing ? kDepth : 1); ++d) fetch();
+  if (t < N) {
+    mn = mean[t];
+    rn = rstd[t];
+  }
+  for (int flip = 0; t < N; t += step, flip ^= 1) {
     Pack<X, VEC> xr[NV];
     Pack<D, VEC> gr[NV];
+    if constexpr (kRing) copy_async_wait<kRing ? kDepth - 1 : 0>();
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      xr[k] = xn[k];
-      gr[k] = gn[k];
+      if constexpr (kRing) {
+        xr[k] = x_ring.read(get * NV + k);
+        gr[k] = g_ring.read(get * NV + k);
+      } else {
+        xr[k] = xn[k];
+        gr[k] = gn[k];
+      }
     }
+    if constexpr (kRing) get = get + 1 == kDepth ? 0 : get + 1;
     const float mu = mn, r = rn;
-    if (kKeep && t + step < N) fetch(t + step);
+    if constexpr (!kRing) fetch();
+    if (t + step < N) {
+      mn = mean[t + step];
+      rn = rstd[t + step];
+    }
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
     for (int k = 0; k < NV; ++k)
@@ -249,9 +413,10 @@ __global__ void __launch_bounds__(kBwdThreads)
           ab[k][e] += d;
         }
       }
+    s1 = warp_sum(s1);
+    s2 = warp_sum(s2);
+    if constexpr (kRing) fetch();   // into the slots just read, all of whose values are in the sums
     if (dx) {
-      s1 = warp_sum(s1);
-      s2 = warp_sum(s2);
       if (warps > 1) {
         const int w0 = grp * warps;
         if (lane == 0) {
@@ -279,30 +444,36 @@ __global__ void __launch_bounds__(kBwdThreads)
           *reinterpret_cast<Pack<X, VEC>*>(dx + t * dx_ld + c) = o;
         }
     }
-    if (!kKeep && t + step < N) fetch(t + step);
   }
+  if constexpr (kRing) copy_async_wait<0>();
   if (!part_w) return;
-  // groups join in order
+  // groups join in order, in the memory of the ring
+  float* const joined = reinterpret_cast<float*>(ring_bytes);
   for (int q = 0; q < groups; ++q) {
-    if (groups > 1 && q > 0) __syncthreads();
+    if (groups > 1) __syncthreads();
     if (grp != q) continue;
 #pragma unroll
     for (int k = 0; k < NV; ++k)
       if (i + k * g < n) {
         const int c = (i + k * g) * VEC;
+        constexpr int N = VEC < 4 ? VEC : 4;
+        using Some = Pack<float, N>;
+        float* const to_w = q + 1 < groups ? joined : part_w + static_cast<int64_t>(blockIdx.x) * H;
+        float* const to_b = q + 1 < groups ? joined + H : part_b + static_cast<int64_t>(blockIdx.x) * H;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
+        for (int e = 0; e < VEC; e += N) {
+          Some a, b;
           if (q > 0) {
-            aw[k][e] += joined[c + e];
-            ab[k][e] += joined[H + c + e];
+            a = *reinterpret_cast<const Some*>(joined + c + e);
+            b = *reinterpret_cast<const Some*>(joined + H + c + e);
           }
-          if (q + 1 < groups) {
-            joined[c + e] = aw[k][e];
-            joined[H + c + e] = ab[k][e];
-          } else {
-            part_w[static_cast<int64_t>(blockIdx.x) * H + c + e] = aw[k][e];
-            part_b[static_cast<int64_t>(blockIdx.x) * H + c + e] = ab[k][e];
+#pragma unroll
+          for (int j = 0; j < N; ++j) {
+            a.v[j] = q > 0 ? a.v[j] + aw[k][e + j] : aw[k][e + j];
+            b.v[j] = q > 0 ? b.v[j] + ab[k][e + j] : ab[k][e + j];
           }
+          *reinterpret_cast<Some*>(to_w + c + e) = a;
+          *reinterpret_cast<Some*>(to_b + c + e) = b;
         }
       }
   }
@@ -387,8 +558,10 @@ __global__ void __launch_bounds__(32 * kFinishRows)
   const int lane = threadIdx.x & 31, sub = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float a = 0.f;
-  if (c < H)
+  if (c < H) {
+#pragma unroll 8
     for (int p = sub; p < P; p += kFinishRows) a += part[static_cast<int64_t>(p) * H + c];
+  }
   red[sub][lane] = a;
   __syncthreads();
   if (sub == 0 && c < H) {
@@ -412,6 +585,22 @@ cudaError_t fwd_rows(const NormFwd& a, cudaStream_t s) {
                           a.rstd);
 }
 
+template <typename X, typename Y, int VEC, int NV, int kDepth>
+cudaError_t fwd_stream(const NormFwd& a, cudaStream_t s) {
+  static std::atomic<int> ready[64];
+  auto* kern = norm_fwd_stream_kernel<X, Y, VEC, NV, kDepth>;
+  constexpr size_t kPerThread = static_cast<size_t>(kDepth) * NV * sizeof(X) * VEC;
+  const cudaError_t e = allow_shared(ready, reinterpret_cast<const void*>(kern),
+                                     kPerThread * kStreamThreads);
+  if (e != cudaSuccess) return e;
+  const int g = round32((a.H / VEC + NV - 1) / NV), groups = kStreamThreads / g;
+  const int64_t ctas = (a.N + groups - 1) / groups, sms = sm_count();
+  return launch_dependent(kern, dim3(static_cast<unsigned>(ctas < sms ? ctas : sms)), g * groups,
+                          kPerThread * g * groups, 1, s, static_cast<const X*>(a.x), a.x_ld,
+                          a.weight, a.bias, a.param_type, a.N, a.H, a.eps, static_cast<Y*>(a.y),
+                          a.y_ld, a.mean, a.rstd, g);
+}
+
 template <typename X, typename Y>
 cudaError_t fwd_typed(const NormFwd& a, cudaStream_t s) {
   constexpr int VEC = kVec<X>;
@@ -423,8 +612,8 @@ cudaError_t fwd_typed(const NormFwd& a, cudaStream_t s) {
     if (a.N >= 4ll * sm_count()) {   // enough rows to give every warp its own
       if (n <= 32 * 2) return fwd_rows<X, Y, VEC, 2, true>(a, s);
       if (n <= 32 * 4) return fwd_rows<X, Y, VEC, 4, true>(a, s);
-      if (n <= 32 * 8) return fwd_rows<X, Y, VEC, 8, true>(a, s);
-      if (n <= 32 * 12) return fwd_rows<X, Y, VEC, 12, true>(a, s);
+      constexpr int NV = 16 / VEC;
+      if (n <= kStreamThreads * NV) return fwd_stream<X, Y, VEC, NV, NV == 2 ? 6 : 4>(a, s);
     }
     if (n <= kFwdMaxThreads) return fwd_rows<X, Y, VEC, 1, false>(a, s);
     if (n <= 4 * kFwdMaxThreads) return fwd_rows<X, Y, VEC, 4, false>(a, s);
@@ -447,6 +636,9 @@ cudaError_t finish(const NormBwd& a, int P, cudaStream_t s) {
 
 template <typename X, typename D, int VEC, int NV>
 cudaError_t bwd_rows(const NormBwd& a, cudaStream_t s) {
+  constexpr bool kRing = PackRing<X, VEC>::kAsync && PackRing<D, VEC>::kAsync;
+  constexpr size_t kRow = NV * VEC * (sizeof(X) + sizeof(D));   // a thread's bytes of one row
+  constexpr int kDepth = !kRing ? 0 : kRow <= 96 ? 4 : kRow <= 128 ? 3 : kRow <= 192 ? 2 : 1;
   const int n = a.H / VEC;
   const int g = round32((n + NV - 1) / NV);
   const int sms = sm_count();
@@ -457,16 +649,20 @@ cudaError_t bwd_rows(const NormBwd& a, cudaStream_t s) {
   const int P = static_cast<int>(ctas < sms ? ctas : sms);
   const bool params = a.d_weight || a.d_bias;
   static std::atomic<int> ready[64];
-  auto* kern = norm_bwd_kernel<X, D, VEC, NV>;
-  constexpr size_t kMost = 2 * sizeof(float) * kBwdThreads / 2 * VEC * NV;   // two groups or more
-  cudaError_t e = allow_shared(ready, reinterpret_cast<const void*>(kern), kMost);
+  auto* kern = norm_bwd_kernel<X, D, VEC, NV, kDepth>;
+  constexpr size_t kMostRing = kDepth * kRow * kBwdThreads;
+  constexpr size_t kMostJoin = 2 * sizeof(float) * kBwdThreads / 2 * VEC * NV;   // two groups or more
+  cudaError_t e = allow_shared(ready, reinterpret_cast<const void*>(kern),
+                               kMostRing > kMostJoin ? kMostRing : kMostJoin);
   if (e != cudaSuccess) return e;
-  const size_t smem = groups > 1 && params ? 2 * sizeof(float) * static_cast<size_t>(a.H) : 0;
+  const size_t ring = kDepth * kRow * g * groups;
+  const size_t join = groups > 1 && params ? 2 * sizeof(float) * static_cast<size_t>(a.H) : 0;
   float* part_w = params ? a.partials : nullptr;
   float* part_b = params ? a.partials + static_cast<int64_t>(P) * a.H : nullptr;
-  e = launch_dependent(kern, dim3(P), g * groups, smem, 1, s, static_cast<const D*>(a.dy), a.dy_ld,
-                       static_cast<const X*>(a.x), a.x_ld, a.weight, a.param_type, a.mean, a.rstd,
-                       a.N, a.H, static_cast<X*>(a.dx), a.dx_ld, part_w, part_b, g);
+  e = launch_dependent(kern, dim3(P), g * groups, ring > join ? ring : join, 1, s,
+                       static_cast<const D*>(a.dy), a.dy_ld, static_cast<const X*>(a.x), a.x_ld,
+                       a.weight, a.param_type, a.mean, a.rstd, a.N, a.H, static_cast<X*>(a.dx),
+                       a.dx_ld, part_w, part_b, g);
   if (e != cudaSuccess || !params) return e;
   return finish(a, P, s);
 }
