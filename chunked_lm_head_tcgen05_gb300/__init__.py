@@ -226,6 +226,35 @@ def _on_device(tensors, stream, fn):
         return fn()
 
 
+def _one_device(first, *others):
+    """Index of the CUDA device all of these tensors are on."""
+    dev = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("all tensors and the stream of one call must be on one CUDA device, "
+                             "got %s" % sorted({str(x.device) for x in (first,) + others
+                                                if x is not None}))
+    return dev
+
+
+def _call(fn, dev, stream, *args):
+    """fn(*args, stream handle) with CUDA device `dev` current."""
+    if stream is None:
+        handle = (_raw_stream(dev) if _raw_stream is not None
+                  else _torch.cuda.current_stream(dev).cuda_stream)
+    elif isinstance(stream, int):
+        handle = stream
+    else:
+        if stream.device.index != dev:
+            raise ValueError("all tensors and the stream of one call must be on one CUDA device, "
+                             "got %s" % sorted({"cuda:%d" % dev, str(stream.device)}))
+        handle = stream.cuda_stream
+    if dev == _torch.cuda.current_device():
+        return fn(*args, handle)
+    with _torch.cuda.device(dev):
+        return fn(*args, handle)
+
+
 def _check_workspace(ws):
     if ws is None or not ws.is_cuda or not ws.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
@@ -256,7 +285,7 @@ def _check_rows(t, name, shape, dtypes=None):
 
 
 def _check_teacher(top_ids, top_logits, teacher_lse, loss_mask, T):
-    import torch
+    torch = _torch
     K = top_ids.shape[1] if top_ids.dim() == 2 else -1
     _check_tensor(top_ids, "top_ids", torch.int32, (T, K))
     _check_tensor(top_logits, "top_logits", torch.float32, (T, K))
@@ -530,37 +559,46 @@ def lmhead_distill_bwd(hidden, weight, top_ids, top_logits, teacher_lse, loss_ma
         workspace.numel() * workspace.element_size(), _stream(stream))))
 
 
-def lmhead_distill_logits_fwd(logits, top_ids, top_logits, teacher_lse, loss_mask, temperature,
-                              teacher_temperature, loss, lse, stream=None):
-    """C ``lmhead_distill_logits_fwd`` on torch tensors; returns the status code."""
-    import torch
+def _distill_logits_fwd(logits, top_ids, top_logits, teacher_lse, loss_mask, temperature,
+                        teacher_temperature, out, stream):
     T, V = logits.shape
     kind, ld = _check_rows(logits, "logits", (T, V))
     K = _check_teacher(top_ids, top_logits, teacher_lse, loss_mask, T)
-    _check_tensor(loss, "loss", torch.float32, (T,))
-    _check_tensor(lse, "lse", torch.float32, (T,))
-    tensors = [logits, top_ids, top_logits, teacher_lse, loss_mask, loss, lse]
-    return _on_device(tensors, stream, lambda: int(library().lmhead_distill_logits_fwd(
-        _ptr(logits), kind, ld, _ptr(top_ids), _ptr(top_logits), _ptr(teacher_lse),
-        _ptr(loss_mask), T, V, K, float(temperature), float(teacher_temperature), _ptr(loss),
-        _ptr(lse), _stream(stream))))
+    if out is None:
+        new = dict(dtype=_torch.float32, device=logits.device)
+        out = _torch.empty(T, **new), _torch.empty(T, **new)
+        dev = _one_device(logits, top_ids, top_logits, teacher_lse, loss_mask)
+    else:
+        _check_tensor(out[0], "loss", _torch.float32, (T,))
+        _check_tensor(out[1], "lse", _torch.float32, (T,))
+        dev = _one_device(logits, top_ids, top_logits, teacher_lse, loss_mask, *out)
+    rc = _call(library().lmhead_distill_logits_fwd, dev, stream, logits.data_ptr(), kind, ld,
+               top_ids.data_ptr(), top_logits.data_ptr(), _ptr(teacher_lse), _ptr(loss_mask), T, V,
+               K, temperature, teacher_temperature, out[0].data_ptr(), out[1].data_ptr())
+    return rc, out
+
+
+def lmhead_distill_logits_fwd(logits, top_ids, top_logits, teacher_lse, loss_mask, temperature,
+                              teacher_temperature, loss, lse, stream=None):
+    """C ``lmhead_distill_logits_fwd`` on torch tensors; returns the status code."""
+    return _distill_logits_fwd(logits, top_ids, top_logits, teacher_lse, loss_mask, temperature,
+                               teacher_temperature, (loss, lse), stream)[0]
 
 
 def lmhead_distill_logits_bwd(logits, top_ids, top_logits, teacher_lse, loss_mask, temperature,
                               teacher_temperature, grad_loss, lse, d_logits, stream=None):
     """C ``lmhead_distill_logits_bwd`` on torch tensors; returns the status code."""
-    import torch
     T, V = logits.shape
     kind, ld = _check_rows(logits, "logits", (T, V))
     K = _check_teacher(top_ids, top_logits, teacher_lse, loss_mask, T)
-    _check_tensor(grad_loss, "grad_loss", torch.float32, (T,))
-    _check_tensor(lse, "lse", torch.float32, (T,))
+    _check_tensor(grad_loss, "grad_loss", _torch.float32, (T,))
+    _check_tensor(lse, "lse", _torch.float32, (T,))
     _, d_ld = _check_rows(d_logits, "d_logits", (T, V), (logits.dtype,))
-    tensors = [logits, top_ids, top_logits, teacher_lse, loss_mask, grad_loss, lse, d_logits]
-    return _on_device(tensors, stream, lambda: int(library().lmhead_distill_logits_bwd(
-        _ptr(logits), kind, ld, _ptr(top_ids), _ptr(top_logits), _ptr(teacher_lse),
-        _ptr(loss_mask), T, V, K, float(temperature), float(teacher_temperature),
-        _ptr(grad_loss), _ptr(lse), _ptr(d_logits), d_ld, _stream(stream))))
+    dev = _one_device(logits, top_ids, top_logits, teacher_lse, loss_mask, grad_loss, lse, d_logits)
+    return _call(library().lmhead_distill_logits_bwd, dev, stream, logits.data_ptr(), kind, ld,
+                 top_ids.data_ptr(), top_logits.data_ptr(), _ptr(teacher_lse), _ptr(loss_mask), T,
+                 V, K, temperature, teacher_temperature, grad_loss.data_ptr(), lse.data_ptr(),
+                 d_logits.data_ptr(), d_ld)
 
 
 def lmhead_layernorm_workspace_size(N, H):
@@ -575,81 +613,93 @@ def _check_norm_params(x, weight, bias, H):
     return _types[weight.dtype]
 
 
-def lmhead_layernorm_fwd(x, weight, bias, eps, y, mean, rstd, stream=None):
-    """C ``lmhead_layernorm_fwd`` on torch tensors; returns the status code."""
-    import torch
+def _layernorm_fwd(x, weight, bias, eps, out, out_dtype, stream):
     N, H = x.shape
     x_type, x_ld = _check_rows(x, "x", (N, H))
     param_type = _check_norm_params(x, weight, bias, H)
+    torch = _torch
+    if out is None:
+        where = x.device
+        y = torch.empty((N, H), dtype=x.dtype if out_dtype is None else out_dtype, device=where)
+        mean = torch.empty(N, dtype=torch.float32, device=where)
+        rstd = torch.empty(N, dtype=torch.float32, device=where)
+        dev = _one_device(x, weight, bias)
+    else:
+        y, mean, rstd = out
+        _check_tensor(mean, "mean", torch.float32, (N,), allow_none=True)
+        _check_tensor(rstd, "rstd", torch.float32, (N,), allow_none=True)
+        dev = _one_device(x, weight, bias, y, mean, rstd)
     y_type, y_ld = _check_rows(y, "y", (N, H), (x.dtype, torch.bfloat16)
-                               if x.dtype == torch.float32 else (x.dtype,))
-    _check_tensor(mean, "mean", torch.float32, (N,), allow_none=True)
-    _check_tensor(rstd, "rstd", torch.float32, (N,), allow_none=True)
-    return _on_device([x, weight, bias, y, mean, rstd], stream, lambda: int(
-        library().lmhead_layernorm_fwd(
-            _ptr(x), x_type, x_ld, _ptr(weight), _ptr(bias), param_type, N, H, float(eps), _ptr(y),
-            y_type, y_ld, _ptr(mean), _ptr(rstd), _stream(stream))))
+                               if x_type == LMHEAD_F32 else (x.dtype,))
+    rc = _call(library().lmhead_layernorm_fwd, dev, stream, x.data_ptr(), x_type, x_ld,
+               weight.data_ptr(), _ptr(bias), param_type, N, H, eps, y.data_ptr(), y_type, y_ld,
+               _ptr(mean), _ptr(rstd))
+    return rc, (y, mean, rstd)
+
+
+def lmhead_layernorm_fwd(x, weight, bias, eps, y, mean, rstd, stream=None):
+    """C ``lmhead_layernorm_fwd`` on torch tensors; returns the status code."""
+    return _layernorm_fwd(x, weight, bias, eps, (y, mean, rstd), None, stream)[0]
 
 
 def lmhead_layernorm_bwd(dy, x, weight, mean, rstd, dx, d_weight, d_bias, accumulate, workspace,
                          stream=None):
     """C ``lmhead_layernorm_bwd`` on torch tensors; returns the status code."""
-    import torch
     N, H = x.shape
     x_type, x_ld = _check_rows(x, "x", (N, H))
-    dy_type, dy_ld = _check_rows(dy, "dy", (N, H), (torch.float32, torch.bfloat16)
-                                 if x.dtype == torch.float32 else (torch.float32, x.dtype))
+    f32 = _torch.float32
+    dy_type, dy_ld = _check_rows(dy, "dy", (N, H), (f32, _torch.bfloat16)
+                                 if x_type == LMHEAD_F32 else (f32, x.dtype))
     param_type = _check_norm_params(x, weight, None, H)
-    _check_tensor(mean, "mean", torch.float32, (N,))
-    _check_tensor(rstd, "rstd", torch.float32, (N,))
+    _check_tensor(mean, "mean", f32, (N,))
+    _check_tensor(rstd, "rstd", f32, (N,))
     dx_ld = 0 if dx is None else _check_rows(dx, "dx", (N, H), (x.dtype,))[1]
-    _check_tensor(d_weight, "d_weight", torch.float32, (H,), allow_none=True)
-    _check_tensor(d_bias, "d_bias", torch.float32, (H,), allow_none=True)
+    _check_tensor(d_weight, "d_weight", f32, (H,), allow_none=True)
+    _check_tensor(d_bias, "d_bias", f32, (H,), allow_none=True)
     if workspace is not None or d_weight is not None or d_bias is not None:
         _check_workspace(workspace)
-    tensors = [dy, x, weight, mean, rstd, dx, d_weight, d_bias, workspace]
-    return _on_device(tensors, stream, lambda: int(library().lmhead_layernorm_bwd(
-        _ptr(dy), dy_type, dy_ld, _ptr(x), x_type, x_ld, _ptr(weight), param_type, _ptr(mean),
-        _ptr(rstd), N, H, _ptr(dx), dx_ld, _ptr(d_weight), _ptr(d_bias), int(bool(accumulate)),
-        _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
-        _stream(stream))))
+    dev = _one_device(x, dy, weight, mean, rstd, dx, d_weight, d_bias, workspace)
+    return _call(library().lmhead_layernorm_bwd, dev, stream, dy.data_ptr(), dy_type, dy_ld,
+                 x.data_ptr(), x_type, x_ld, weight.data_ptr(), param_type, mean.data_ptr(),
+                 rstd.data_ptr(), N, H, _ptr(dx), dx_ld, _ptr(d_weight), _ptr(d_bias),
+                 1 if accumulate else 0, _ptr(workspace),
+                 0 if workspace is None else workspace.nbytes)
 
 
 def _check_rules(R, V, tokens, spans, repetition, frequency, presence, allowed, allowed_rows):
-    import torch
+    f32, i32 = _torch.float32, _torch.int32
     if tokens is not None:
-        _check_tensor(tokens, "tokens", torch.int32, (tokens.numel(),))
-    _check_tensor(spans, "spans", torch.int64, (R, 3), allow_none=True)
-    _check_tensor(repetition, "repetition", torch.float32, (R,), allow_none=True)
-    _check_tensor(frequency, "frequency", torch.float32, (R,), allow_none=True)
-    _check_tensor(presence, "presence", torch.float32, (R,), allow_none=True)
+        _check_tensor(tokens, "tokens", i32, (tokens.numel(),))
+    _check_tensor(spans, "spans", _torch.int64, (R, 3), allow_none=True)
+    _check_tensor(repetition, "repetition", f32, (R,), allow_none=True)
+    _check_tensor(frequency, "frequency", f32, (R,), allow_none=True)
+    _check_tensor(presence, "presence", f32, (R,), allow_none=True)
     if allowed is not None:
-        _check_tensor(allowed, "allowed", torch.int32, (allowed.shape[0], (V + 31) // 32))
-    _check_tensor(allowed_rows, "allowed_rows", torch.int32, (R,), allow_none=True)
+        _check_tensor(allowed, "allowed", i32, (allowed.shape[0], (V + 31) // 32))
+    _check_tensor(allowed_rows, "allowed_rows", i32, (R,), allow_none=True)
 
 
 def lmhead_process_logits_fwd(logits, tokens, spans, repetition, frequency, presence,
                               bias_offsets, bias_ids, bias_values, allowed, allowed_rows, out,
                               stream=None):
     """C ``lmhead_process_logits_fwd`` on torch tensors; returns the status code."""
-    import torch
     R, V = logits.shape
     kind, ld = _check_rows(logits, "logits", (R, V))
     _check_rules(R, V, tokens, spans, repetition, frequency, presence, allowed, allowed_rows)
-    _check_tensor(bias_offsets, "bias_offsets", torch.int64, (R + 1,), allow_none=True)
+    _check_tensor(bias_offsets, "bias_offsets", _torch.int64, (R + 1,), allow_none=True)
     n_bias = 0 if bias_ids is None else bias_ids.numel()
-    _check_tensor(bias_ids, "bias_ids", torch.int32, (n_bias,), allow_none=bias_offsets is None)
-    _check_tensor(bias_values, "bias_values", torch.float32, (n_bias,),
+    _check_tensor(bias_ids, "bias_ids", _torch.int32, (n_bias,), allow_none=bias_offsets is None)
+    _check_tensor(bias_values, "bias_values", _torch.float32, (n_bias,),
                   allow_none=bias_offsets is None)
     _, out_ld = _check_rows(out, "out", (R, V), (logits.dtype,))
-    tensors = [logits, tokens, spans, repetition, frequency, presence, bias_offsets, bias_ids,
-               bias_values, allowed, allowed_rows, out]
-    return _on_device(tensors, stream, lambda: int(library().lmhead_process_logits_fwd(
-        _ptr(logits), kind, ld, R, V, _ptr(tokens), 0 if tokens is None else tokens.numel(),
-        _ptr(spans), _ptr(repetition), _ptr(frequency), _ptr(presence), _ptr(bias_offsets),
-        _ptr(bias_ids), _ptr(bias_values), n_bias, _ptr(allowed),
-        0 if allowed is None else allowed.shape[0], _ptr(allowed_rows), _ptr(out), out_ld,
-        _stream(stream))))
+    dev = _one_device(logits, tokens, spans, repetition, frequency, presence, bias_offsets,
+                      bias_ids, bias_values, allowed, allowed_rows, out)
+    return _call(library().lmhead_process_logits_fwd, dev, stream, logits.data_ptr(), kind, ld, R,
+                 V, _ptr(tokens), 0 if tokens is None else tokens.numel(), _ptr(spans),
+                 _ptr(repetition), _ptr(frequency), _ptr(presence), _ptr(bias_offsets),
+                 _ptr(bias_ids), _ptr(bias_values), n_bias, _ptr(allowed),
+                 0 if allowed is None else allowed.shape[0], _ptr(allowed_rows), out.data_ptr(),
+                 out_ld)
 
 
 def lmhead_process_logits_bwd(grad_out, logits, tokens, spans, repetition, allowed, allowed_rows,
@@ -660,12 +710,12 @@ def lmhead_process_logits_bwd(grad_out, logits, tokens, spans, repetition, allow
     _, grad_ld = _check_rows(grad_out, "grad_out", (R, V), (logits.dtype,))
     _check_rules(R, V, tokens, spans, repetition, None, None, allowed, allowed_rows)
     _, d_ld = _check_rows(d_logits, "d_logits", (R, V), (logits.dtype,))
-    tensors = [grad_out, logits, tokens, spans, repetition, allowed, allowed_rows, d_logits]
-    return _on_device(tensors, stream, lambda: int(library().lmhead_process_logits_bwd(
-        _ptr(grad_out), grad_ld, _ptr(logits), kind, ld, R, V, _ptr(tokens),
-        0 if tokens is None else tokens.numel(), _ptr(spans), _ptr(repetition), _ptr(allowed),
-        0 if allowed is None else allowed.shape[0], _ptr(allowed_rows), _ptr(d_logits), d_ld,
-        _stream(stream))))
+    dev = _one_device(logits, grad_out, tokens, spans, repetition, allowed, allowed_rows, d_logits)
+    return _call(library().lmhead_process_logits_bwd, dev, stream, grad_out.data_ptr(), grad_ld,
+                 logits.data_ptr(), kind, ld, R, V, _ptr(tokens),
+                 0 if tokens is None else tokens.numel(), _ptr(spans), _ptr(repetition),
+                 _ptr(allowed), 0 if allowed is None else allowed.shape[0], _ptr(allowed_rows),
+                 d_logits.data_ptr(), d_ld)
 
 
 def lmhead_selftest_bounded_wait(workspace, limit_ms, stream=None):
@@ -828,25 +878,22 @@ def distill_backward(hidden, weight, top_ids, top_logits, loss_mask, temperature
 def _rows_like(t):
     """A new matrix with t's rows as far apart as t's are (so both sides of a call have the
     same alignment, padded rows included)."""
-    import torch
+    if _torch is None:
+        _bind_torch()
     rows, cols = t.shape
-    return torch.empty_strided((rows, cols), (max(t.stride(0), cols), 1), dtype=t.dtype,
-                               device=t.device)
+    return _torch.empty_strided((rows, cols), (max(t.stride(0), cols), 1), dtype=t.dtype,
+                                device=t.device)
 
 
 def distill_logits_forward(logits, top_ids, top_logits, loss_mask=None, temperature=1.0,
                            teacher_temperature=1.0, teacher_lse=None, stream=None):
     """Distillation loss on held logits [T, V] (fp32, bf16 or fp16, rows may be padded).
     Returns (loss [T], lse [T]), fp32."""
-    import torch
-    T = logits.shape[0]
-    loss = torch.empty(T, dtype=torch.float32, device=logits.device)
-    lse = torch.empty(T, dtype=torch.float32, device=logits.device)
-    rc = lmhead_distill_logits_fwd(logits, top_ids, top_logits, teacher_lse, loss_mask,
-                                   temperature, teacher_temperature, loss, lse, stream)
+    rc, out = _distill_logits_fwd(logits, top_ids, top_logits, teacher_lse, loss_mask, temperature,
+                                  teacher_temperature, None, stream)
     if rc:
         raise LmheadError(rc, "lmhead_distill_logits_fwd")
-    return loss, lse
+    return out
 
 
 def distill_logits_backward(logits, top_ids, top_logits, loss_mask, temperature,
@@ -867,25 +914,22 @@ def distill_logits_backward(logits, top_ids, top_logits, loss_mask, temperature,
 def layernorm_forward(x, weight, bias=None, eps=1e-5, out_dtype=None, stream=None):
     """Layer norm of x [N, H].  Returns (y [N, H] of x's type or out_dtype, mean [N] fp32,
     rstd [N] fp32)."""
-    import torch
-    N = x.shape[0]
-    y = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
-    mean = torch.empty(N, dtype=torch.float32, device=x.device)
-    rstd = torch.empty(N, dtype=torch.float32, device=x.device)
-    rc = lmhead_layernorm_fwd(x, weight, bias, eps, y, mean, rstd, stream)
+    rc, out = _layernorm_fwd(x, weight, bias, eps, None, out_dtype, stream)
     if rc:
         raise LmheadError(rc, "lmhead_layernorm_fwd")
-    return y, mean, rstd
+    return out
 
 
 def layernorm_backward(dy, x, weight, mean, rstd, with_bias=True, d_weight=None, d_bias=None,
                        accumulate=False, dx=None, workspace=None, stream=None):
     """Returns (dx [N, H] of x's type, d_weight [H] fp32, d_bias [H] fp32 or None)."""
-    import torch
+    if _torch is None:
+        _bind_torch()
+    torch = _torch
     N, H = x.shape
     dev = x.device
     if dx is None:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        dx = torch.empty((N, H), dtype=x.dtype, device=dev)
     if d_weight is None:
         d_weight = torch.empty(H, dtype=torch.float32, device=dev)
     if d_bias is None and with_bias:
