@@ -124,12 +124,15 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(ProcessLogits a) {
 
 // Shared memory: bitmap [range / 32], rank of each word's first bit [range / 32],
 // then per id of the window: column, 2 * outputs + met, and with biases 1 + the
-// last entry's index.  Grid (column ranges, rows).
+// last entry's index.  Grid (column ranges, rows).  With after_copy the kernel
+// follows copy_kernel, whose CTAs let it start once they know that what came
+// before is complete; only the last step waits for the copy itself.
 template <typename T, bool kBackward>
-__global__ void __launch_bounds__(kThreads) rewrite_kernel(ProcessLogits a, int range) {
+__global__ void __launch_bounds__(kThreads, 2)
+    rewrite_kernel(ProcessLogits a, int range, int after_copy) {
   extern __shared__ __align__(16) uint32_t bitmap[];
-  __shared__ int red[kWarps], carry;
-  pdl_wait_prerequisites();
+  __shared__ int red[kWarps];
+  if (!after_copy) pdl_wait_prerequisites();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint32_t* const rank = bitmap + range / 32;
@@ -159,7 +162,7 @@ __global__ void __launch_bounds__(kThreads) rewrite_kernel(ProcessLogits a, int 
       if (q1 + threadIdx.x < to) each(a.tokens[q1 + threadIdx.x]);
       const int4* const v4 = reinterpret_cast<const int4*>(a.tokens + q0);
       const int64_t packs = (q1 - q0) / 4;
-#pragma unroll 4
+#pragma unroll 2
       for (int64_t i = threadIdx.x; i < packs; i += kThreads) {
         const int4 v = v4[i];
         each(v.x);
@@ -173,7 +176,8 @@ __global__ void __launch_bounds__(kThreads) rewrite_kernel(ProcessLogits a, int 
 
     // the distinct ids
     __syncthreads();   // the previous row's readers are done
-    for (int i = threadIdx.x; i < map_words; i += kThreads) bitmap[i] = 0;
+    for (int i = threadIdx.x; i < (map_words + 3) / 4; i += kThreads)
+      reinterpret_cast<uint4*>(bitmap)[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
     auto mark = [&](int id) {
       const uint32_t e = at(id);
@@ -181,34 +185,26 @@ __global__ void __launch_bounds__(kThreads) rewrite_kernel(ProcessLogits a, int 
     };
     if (p2 > p0) scan(p0, p2, mark);
     for (int64_t j = threadIdx.x; j < biases; j += kThreads) mark(bias_ids[j]);
-    if (threadIdx.x == 0) carry = 0;
     __syncthreads();
-    // ranks: 512 words at a time
-    for (int base = 0; base < map_words; base += kThreads) {
-      const int i = base + threadIdx.x;
-      const int ones = i < map_words ? __popc(bitmap[i]) : 0;
-      int upto = ones;
+    // ranks: each thread sums a run of words, the runs are scanned once
+    const int run = (map_words + kThreads - 1) / kThreads, w0 = threadIdx.x * run;
+    int ones = 0;
+    for (int i = w0; i < min(w0 + run, map_words); ++i) ones += __popc(bitmap[i]);
+    int upto = ones;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += x;
-      }
-      if (lane == 31) red[warp] = upto;
-      const int before = carry;
-      __syncthreads();
-      int sum = lane < kWarps ? red[lane] : 0;
-#pragma unroll
-      for (int o = 1; o < kWarps; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += x;
-      }
-      const int warps_before = warp ? __shfl_sync(0xffffffffu, sum, warp - 1) : 0;
-      const int all = __shfl_sync(0xffffffffu, sum, kWarps - 1);
-      if (i < map_words) rank[i] = before + warps_before + upto - ones;
-      if (threadIdx.x == 0) carry = before + all;
-      __syncthreads();
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += x;
     }
-    const int distinct = carry;
+    if (lane == 31) red[warp] = upto;
+    __syncthreads();
+    const int mine = lane < kWarps ? red[lane] : 0;
+    const int distinct = __reduce_add_sync(0xffffffffu, mine);
+    int before = __reduce_add_sync(0xffffffffu, lane < warp ? mine : 0) + upto - ones;
+    for (int i = w0; i < min(w0 + run, map_words); ++i) {
+      rank[i] = before;
+      before += __popc(bitmap[i]);
+    }
     auto rank_of = [&](uint32_t e) {
       return rank[e >> 5] + __popc(bitmap[e >> 5] & ((1u << (e & 31)) - 1u));
     };
@@ -230,31 +226,32 @@ __global__ void __launch_bounds__(kThreads) rewrite_kernel(ProcessLogits a, int 
         count[i] = 0;
         if (biases) slot[i] = 0;
       }
-      for (int i = threadIdx.x; i < map_words; i += kThreads) {
-        uint32_t bits = bitmap[i];
-        for (uint32_t k = rank[i] - first; bits; bits &= bits - 1, ++k)
-          if (k < here) column[k] = 32 * i + __ffs(bits) - 1;
-      }
-      __syncthreads();
-      auto count_in = [&](int id, bool output) {
+      __syncthreads();   // also: the ranks are there
+      // index of an id in the window; every occurrence notes the column
+      auto place = [&](int id) -> uint32_t {
         const uint32_t e = at(id);
-        if (e >= static_cast<uint32_t>(n)) return;
+        if (e >= static_cast<uint32_t>(n)) return ~0u;
         const uint32_t k = rank_of(e) - first;
-        if (k >= here) return;
-        if (output)
-          atomicAdd(&count[k], 2u);
-        else
-          atomicOr(&count[k], 1u);
+        if (k >= here) return ~0u;
+        column[k] = e;
+        return k;
       };
-      if (p1 > p0) scan(p0, p1, [&](int id) { count_in(id, false); });
-      if (p2 > p1) scan(p1, p2, [&](int id) { count_in(id, true); });
+      if (p1 > p0)
+        scan(p0, p1, [&](int id) {
+          const uint32_t k = place(id);
+          if (k != ~0u) atomicOr(&count[k], 1u);
+        });
+      if (p2 > p1)
+        scan(p1, p2, [&](int id) {
+          const uint32_t k = place(id);
+          if (k != ~0u) atomicAdd(&count[k], 2u);
+        });
       for (int64_t j = threadIdx.x; j < biases; j += kThreads) {   // the last entry counts
-        const uint32_t e = at(bias_ids[j]);
-        if (e >= static_cast<uint32_t>(n)) continue;
-        const uint32_t k = rank_of(e) - first;
-        if (k < here) atomicMax(&slot[k], static_cast<uint32_t>(j) + 1u);
+        const uint32_t k = place(bias_ids[j]);
+        if (k != ~0u) atomicMax(&slot[k], static_cast<uint32_t>(j) + 1u);
       }
       __syncthreads();
+      if (after_copy) pdl_wait_prerequisites();
 #pragma unroll 4
       for (uint32_t k = threadIdx.x; k < here; k += kThreads) {
         const int c = c0 + static_cast<int>(column[k]);
@@ -271,6 +268,7 @@ __global__ void __launch_bounds__(kThreads) rewrite_kernel(ProcessLogits a, int 
       }
     }
   }
+  if (after_copy) pdl_wait_prerequisites();   // rows without history: still after the copy
 }
 
 template <typename T, bool kBackward>
@@ -278,7 +276,8 @@ cudaError_t run(const ProcessLogits& a, cudaStream_t s) {
   const unsigned rows = static_cast<unsigned>(a.R < 32768 ? a.R : 32768);
   const void* in = kBackward ? a.grad : a.logits;
   const bool in_place = in == a.out && (kBackward ? a.grad_ld : a.ld) == a.out_ld;
-  if (!in_place || a.allowed) {
+  const bool copy = !in_place || a.allowed;
+  if (copy) {
     constexpr int kChunk = kUnroll * kCopyThreads * kVec<T>;
     const unsigned chunks = static_cast<unsigned>((static_cast<int64_t>(a.V) + kChunk - 1) / kChunk);
     const cudaError_t e = launch_dependent(copy_kernel<T, kBackward>, dim3(chunks, rows),
@@ -291,11 +290,11 @@ cudaError_t run(const ProcessLogits& a, cudaStream_t s) {
   const cudaError_t e = allow_shared(ready, reinterpret_cast<const void*>(kern),
                                      2 * kMostColumns / 8 + 3 * 4 * kWindow);
   if (e != cudaSuccess) return e;
-  const int64_t padded = (static_cast<int64_t>(a.V) + 31) / 32 * 32;
+  const int64_t padded = (static_cast<int64_t>(a.V) + 127) / 128 * 128;   // whole 16-byte words of bitmap
   const int range = static_cast<int>(padded < kMostColumns ? padded : kMostColumns);
   const unsigned ranges = static_cast<unsigned>((padded + range - 1) / range);
   const size_t smem = 2 * static_cast<size_t>(range) / 8 + (a.bias_offsets ? 3 : 2) * 4 * kWindow;
-  return launch_dependent(kern, dim3(ranges, rows), kThreads, smem, 1, s, a, range);
+  return launch_dependent(kern, dim3(ranges, rows), kThreads, smem, 1, s, a, range, copy ? 1 : 0);
 }
 
 template <typename T>
