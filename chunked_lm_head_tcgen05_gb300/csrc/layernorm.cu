@@ -53,6 +53,12 @@ __device__ __forceinline__ void load_params(const void* p, int type, int i, floa
   }
 }
 
+// Element e of a row of pairs (e known at compile time).
+template <int N>
+__device__ __forceinline__ float& at(float2 (&v)[N], int e) {
+  return e & 1 ? v[e >> 1].y : v[e >> 1].x;
+}
+
 // Sum over the CTA, returned to every thread.
 __device__ __forceinline__ float block_sum(float v, float* red) {
   v = warp_sum(v);
@@ -336,12 +342,28 @@ __global__ void __launch_bounds__(kBwdThreads)
   const PackRing<X, VEC> x_ring(ring_bytes, blockDim.x, threadIdx.x);
   const PackRing<D, VEC> g_ring(ring_bytes + kDepth * NV * sizeof(X) * VEC * blockDim.x, blockDim.x,
                                 threadIdx.x);
-  float aw[NV][VEC] = {}, ab[NV][VEC] = {}, wv[kKeep ? NV : 1][VEC];
+  // pairs of columns: within a pack, or of neighbouring packs of one element
+  constexpr int kPairs = NV * VEC / 2;
+  float2 aw[kPairs] = {}, ab[kPairs] = {}, wv[kKeep ? kPairs : 1] = {};
   if constexpr (kKeep) {
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
-      if (i + k * g < n) load_params<VEC>(w, param_type, (i + k * g) * VEC, wv[k]);
+    for (int k = 0; k < NV; ++k) {
+      float one[VEC] = {};
+      if (i + k * g < n) load_params<VEC>(w, param_type, (i + k * g) * VEC, one);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) at(wv, k * VEC + e) = one[e];
+    }
   }
+  auto weight_of = [&](int j) {
+    if constexpr (kKeep) {
+      return wv[j];
+    } else {   // no room: from L1 each time
+      const int e0 = 2 * j, e1 = 2 * j + 1;
+      const int c0 = (i + e0 / VEC * g) * VEC + e0 % VEC, c1 = (i + e1 / VEC * g) * VEC + e1 % VEC;
+      return make_float2(c0 < H ? load_param(w, param_type, c0) : 0.f,
+                         c1 < H ? load_param(w, param_type, c1) : 0.f);
+    }
+  };
   Pack<X, VEC> xn[kRegs];
   Pack<D, VEC> gn[kRegs];
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
@@ -377,72 +399,69 @@ __global__ void __launch_bounds__(kBwdThreads)
     rn = rstd[t];
   }
   for (int flip = 0; t < N; t += step, flip ^= 1) {
-    Pack<X, VEC> xr[NV];
-    Pack<D, VEC> gr[NV];
     if constexpr (kRing) copy_async_wait<kRing ? kDepth - 1 : 0>();
+    float2 xv[kPairs], gv[kPairs];   // columns past H count as zeros in dy
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
+      Pack<X, VEC> xq;
+      Pack<D, VEC> gq;
       if constexpr (kRing) {
-        xr[k] = x_ring.read(get * NV + k);
-        gr[k] = g_ring.read(get * NV + k);
+        xq = x_ring.read(get * NV + k);
+        gq = g_ring.read(get * NV + k);
       } else {
-        xr[k] = xn[k];
-        gr[k] = gn[k];
+        xq = xn[k];
+        gq = gn[k];
+      }
+      const bool in = i + k * g < n;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        at(xv, k * VEC + e) = in ? to_f32(xq.v[e]) : 0.f;
+        at(gv, k * VEC + e) = in ? to_f32(gq.v[e]) : 0.f;
       }
     }
     if constexpr (kRing) get = get + 1 == kDepth ? 0 : get + 1;
-    const float mu = mn, r = rn;
+    const float2 minus_mu = make_float2(-mn, -mn), r2 = make_float2(rn, rn);
     if constexpr (!kRing) fetch();
     if (t + step < N) {
       mn = mean[t + step];
       rn = rstd[t + step];
     }
-    float s1 = 0.f, s2 = 0.f;
+    float2 s1 = make_float2(0.f, 0.f), s2 = s1;
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
-      if (i + k * g < n) {
-        float wl[VEC];
-        if constexpr (!kKeep) load_params<VEC>(w, param_type, (i + k * g) * VEC, wl);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const float xh = (to_f32(xr[k].v[e]) - mu) * r, d = to_f32(gr[k].v[e]);
-          const float h = d * (kKeep ? wv[kKeep ? k : 0][e] : wl[e]);
-          s1 = fmaf(h, xh, s1);
-          s2 += h;
-          aw[k][e] = fmaf(d, xh, aw[k][e]);
-          ab[k][e] += d;
-        }
-      }
-    s1 = warp_sum(s1);
-    s2 = warp_sum(s2);
+    for (int j = 0; j < kPairs; ++j) {
+      const float2 xh = mul2(add2(xv[j], minus_mu), r2), h = mul2(gv[j], weight_of(j));
+      s1 = fma2(h, xh, s1);
+      s2 = add2(s2, h);
+      aw[j] = fma2(gv[j], xh, aw[j]);
+      ab[j] = add2(ab[j], gv[j]);
+    }
+    float t1 = warp_sum(s1.x + s1.y), t2 = warp_sum(s2.x + s2.y);
     if constexpr (kRing) fetch();   // into the slots just read, all of whose values are in the sums
     if (dx) {
       if (warps > 1) {
         const int w0 = grp * warps;
         if (lane == 0) {
-          red[flip][0][threadIdx.x >> 5] = s1;
-          red[flip][1][threadIdx.x >> 5] = s2;
+          red[flip][0][threadIdx.x >> 5] = t1;
+          red[flip][1][threadIdx.x >> 5] = t2;
         }
         named_bar_sync(1 + grp, g);
-        s1 = warp_sum(lane < warps ? red[flip][0][w0 + lane] : 0.f);
-        s2 = warp_sum(lane < warps ? red[flip][1][w0 + lane] : 0.f);
+        t1 = warp_sum(lane < warps ? red[flip][0][w0 + lane] : 0.f);
+        t2 = warp_sum(lane < warps ? red[flip][1][w0 + lane] : 0.f);
       }
-      const float c1 = s1 * inv, c2 = s2 * inv;
+      const float2 minus_c1 = make_float2(-t1 * inv, -t1 * inv), minus_c2 = make_float2(-t2 * inv, -t2 * inv);
 #pragma unroll
-      for (int k = 0; k < NV; ++k)
-        if (i + k * g < n) {
-          const int c = (i + k * g) * VEC;
-          float wl[VEC];
-          if constexpr (!kKeep) load_params<VEC>(w, param_type, c, wl);
-          Pack<X, VEC> o;
+      for (int j = 0; j < kPairs; ++j) {
+        const float2 xh = mul2(add2(xv[j], minus_mu), r2), h = mul2(gv[j], weight_of(j));
+        gv[j] = mul2(fma2(xh, minus_c1, add2(h, minus_c2)), r2);
+      }
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            const float xh = (to_f32(xr[k].v[e]) - mu) * r;
-            const float h = to_f32(gr[k].v[e]) * (kKeep ? wv[kKeep ? k : 0][e] : wl[e]);
-            o.v[e] = from_f32<X>((h - c2 - xh * c1) * r);
-          }
-          *reinterpret_cast<Pack<X, VEC>*>(dx + t * dx_ld + c) = o;
-        }
+      for (int k = 0; k < NV; ++k) {
+        if (i + k * g >= n) continue;
+        Pack<X, VEC> o;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) o.v[e] = from_f32<X>(at(gv, k * VEC + e));
+        *reinterpret_cast<Pack<X, VEC>*>(dx + t * dx_ld + (i + k * g) * VEC) = o;
+      }
     }
   }
   if constexpr (kRing) copy_async_wait<0>();
@@ -469,8 +488,9 @@ __global__ void __launch_bounds__(kBwdThreads)
           }
 #pragma unroll
           for (int j = 0; j < N; ++j) {
-            a.v[j] = q > 0 ? a.v[j] + aw[k][e + j] : aw[k][e + j];
-            b.v[j] = q > 0 ? b.v[j] + ab[k][e + j] : ab[k][e + j];
+            const float own_w = at(aw, k * VEC + e + j), own_b = at(ab, k * VEC + e + j);
+            a.v[j] = q > 0 ? a.v[j] + own_w : own_w;
+            b.v[j] = q > 0 ? b.v[j] + own_b : own_b;
           }
           *reinterpret_cast<Some*>(to_w + c + e) = a;
           *reinterpret_cast<Some*>(to_b + c + e) = b;
