@@ -11,6 +11,7 @@ missing or cannot load, every call raises.
 workspace with torch and raise ``LmheadError`` on a non-zero status.
 """
 import ctypes
+import functools
 import os
 
 __all__ = [
@@ -190,14 +191,15 @@ def _check_tensor(t, name, dtype, shape, allow_none=False):
         if allow_none:
             return
         raise ValueError("%s is required" % name)
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return
     if t.dtype is not dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
-    if t.shape != shape:
-        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
 
 
 def _on_device(tensors, stream, fn):
@@ -601,6 +603,7 @@ def lmhead_distill_logits_bwd(logits, top_ids, top_logits, teacher_lse, loss_mas
                  d_logits.data_ptr(), d_ld)
 
 
+@functools.lru_cache(maxsize=None)
 def lmhead_layernorm_workspace_size(N, H):
     return int(library().lmhead_layernorm_workspace_size(N, H))
 
@@ -642,9 +645,8 @@ def lmhead_layernorm_fwd(x, weight, bias, eps, y, mean, rstd, stream=None):
     return _layernorm_fwd(x, weight, bias, eps, (y, mean, rstd), None, stream)[0]
 
 
-def lmhead_layernorm_bwd(dy, x, weight, mean, rstd, dx, d_weight, d_bias, accumulate, workspace,
-                         stream=None):
-    """C ``lmhead_layernorm_bwd`` on torch tensors; returns the status code."""
+def _layernorm_bwd(dy, x, weight, mean, rstd, out, with_bias, accumulate, workspace, stream):
+    """out: (dx, d_weight, d_bias), or None for new ones; then workspace may be None too."""
     N, H = x.shape
     x_type, x_ld = _check_rows(x, "x", (N, H))
     f32 = _torch.float32
@@ -653,17 +655,38 @@ def lmhead_layernorm_bwd(dy, x, weight, mean, rstd, dx, d_weight, d_bias, accumu
     param_type = _check_norm_params(x, weight, None, H)
     _check_tensor(mean, "mean", f32, (N,))
     _check_tensor(rstd, "rstd", f32, (N,))
-    dx_ld = 0 if dx is None else _check_rows(dx, "dx", (N, H), (x.dtype,))[1]
-    _check_tensor(d_weight, "d_weight", f32, (H,), allow_none=True)
-    _check_tensor(d_bias, "d_bias", f32, (H,), allow_none=True)
-    if workspace is not None or d_weight is not None or d_bias is not None:
-        _check_workspace(workspace)
-    dev = _one_device(x, dy, weight, mean, rstd, dx, d_weight, d_bias, workspace)
-    return _call(library().lmhead_layernorm_bwd, dev, stream, dy.data_ptr(), dy_type, dy_ld,
-                 x.data_ptr(), x_type, x_ld, weight.data_ptr(), param_type, mean.data_ptr(),
-                 rstd.data_ptr(), N, H, _ptr(dx), dx_ld, _ptr(d_weight), _ptr(d_bias),
-                 1 if accumulate else 0, _ptr(workspace),
-                 0 if workspace is None else workspace.nbytes)
+    if out is None:
+        empty, where = _torch.empty, x.device
+        dx, dx_ld = empty((N, H), dtype=x.dtype, device=where), H
+        d_weight = empty(H, dtype=f32, device=where)
+        d_bias = empty(H, dtype=f32, device=where) if with_bias else None
+        if workspace is None:
+            workspace = empty(lmhead_layernorm_workspace_size(N, H), dtype=_torch.uint8,
+                              device=where)
+        else:
+            _check_workspace(workspace)
+        dev = _one_device(x, dy, weight, mean, rstd, workspace)
+    else:
+        dx, d_weight, d_bias = out
+        dx_ld = 0 if dx is None else _check_rows(dx, "dx", (N, H), (x.dtype,))[1]
+        _check_tensor(d_weight, "d_weight", f32, (H,), allow_none=True)
+        _check_tensor(d_bias, "d_bias", f32, (H,), allow_none=True)
+        if workspace is not None or d_weight is not None or d_bias is not None:
+            _check_workspace(workspace)
+        dev = _one_device(x, dy, weight, mean, rstd, dx, d_weight, d_bias, workspace)
+    rc = _call(library().lmhead_layernorm_bwd, dev, stream, dy.data_ptr(), dy_type, dy_ld,
+               x.data_ptr(), x_type, x_ld, weight.data_ptr(), param_type, mean.data_ptr(),
+               rstd.data_ptr(), N, H, _ptr(dx), dx_ld, _ptr(d_weight), _ptr(d_bias),
+               1 if accumulate else 0, _ptr(workspace),
+               0 if workspace is None else workspace.nbytes)
+    return rc, (dx, d_weight, d_bias)
+
+
+def lmhead_layernorm_bwd(dy, x, weight, mean, rstd, dx, d_weight, d_bias, accumulate, workspace,
+                         stream=None):
+    """C ``lmhead_layernorm_bwd`` on torch tensors; returns the status code."""
+    return _layernorm_bwd(dy, x, weight, mean, rstd, (dx, d_weight, d_bias), True, accumulate,
+                          workspace, stream)[0]
 
 
 def _check_rules(R, V, tokens, spans, repetition, frequency, presence, allowed, allowed_rows):
@@ -864,7 +887,8 @@ def distill_backward(hidden, weight, top_ids, top_logits, loss_mask, temperature
     dev = hidden.device
     d_hidden = torch.empty((T, H), dtype=torch.float32, device=dev)
     if d_weight is None:
-        d_weight = torch.empty((V, H), dtype=torch.float32, device=dev)
+        make = torch.zeros if accumulate_dweight else torch.empty
+        d_weight = make((V, H), dtype=torch.float32, device=dev)
     if workspace is None:
         workspace = _distill_workspace(LMHEAD_OP_BWD, T, H, V, top_ids.shape[1], chunk_size, dev)
     rc = lmhead_distill_bwd(hidden, weight, top_ids, top_logits, teacher_lse, loss_mask,
@@ -923,25 +947,25 @@ def layernorm_forward(x, weight, bias=None, eps=1e-5, out_dtype=None, stream=Non
 def layernorm_backward(dy, x, weight, mean, rstd, with_bias=True, d_weight=None, d_bias=None,
                        accumulate=False, dx=None, workspace=None, stream=None):
     """Returns (dx [N, H] of x's type, d_weight [H] fp32, d_bias [H] fp32 or None)."""
-    if _torch is None:
-        _bind_torch()
-    torch = _torch
-    N, H = x.shape
-    dev = x.device
-    if dx is None:
-        dx = torch.empty((N, H), dtype=x.dtype, device=dev)
-    if d_weight is None:
-        d_weight = torch.empty(H, dtype=torch.float32, device=dev)
-    if d_bias is None and with_bias:
-        d_bias = torch.empty(H, dtype=torch.float32, device=dev)
-    if workspace is None:
-        workspace = torch.empty(lmhead_layernorm_workspace_size(N, H), dtype=torch.uint8,
-                                device=dev)
-    rc = lmhead_layernorm_bwd(dy, x, weight, mean, rstd, dx, d_weight, d_bias, accumulate,
-                              workspace, stream)
+    if dx is None and d_weight is None and d_bias is None and not accumulate:
+        out = None
+    else:
+        import torch
+        N, H = x.shape
+        new = dict(dtype=torch.float32, device=x.device)
+        dx = torch.empty((N, H), dtype=x.dtype, device=x.device) if dx is None else dx
+        make = torch.zeros if accumulate else torch.empty
+        d_weight = make(H, **new) if d_weight is None else d_weight
+        d_bias = make(H, **new) if d_bias is None and with_bias else d_bias
+        out = dx, d_weight, d_bias
+        if workspace is None:
+            workspace = torch.empty(lmhead_layernorm_workspace_size(N, H), dtype=torch.uint8,
+                                    device=x.device)
+    rc, out = _layernorm_bwd(dy, x, weight, mean, rstd, out, with_bias, accumulate, workspace,
+                             stream)
     if rc:
         raise LmheadError(rc, "lmhead_layernorm_bwd")
-    return dx, d_weight, d_bias
+    return out
 
 
 def process_logits(logits, tokens=None, spans=None, repetition=None, frequency=None,
