@@ -29,6 +29,7 @@ __all__ = [
     "forward", "backward",
     "LMHEAD_F32", "LMHEAD_BF16", "LMHEAD_F16",
     "lmhead_distill_workspace_size", "lmhead_distill_fwd", "lmhead_distill_bwd",
+    "lmhead_distill_narrow_dweight",
     "lmhead_distill_logits_fwd", "lmhead_distill_logits_bwd",
     "lmhead_layernorm_workspace_size", "lmhead_layernorm_fwd", "lmhead_layernorm_bwd",
     "lmhead_process_logits_fwd", "lmhead_process_logits_bwd",
@@ -104,7 +105,8 @@ _SIGNATURES = {
                                           _VP, _SZ, _VP]),
     "lmhead_distill_bwd": (ctypes.c_int, [_VP, _VP, _VP, _VP, _VP, _VP, _I64, _I32, _I32, _I32,
                                           ctypes.c_float, ctypes.c_float, _I32, _VP, _VP, _VP,
-                                          _VP, _VP, ctypes.c_int, _VP, _SZ, _VP]),
+                                          _VP, _VP, ctypes.c_int, ctypes.c_int, _VP, _SZ, _VP]),
+    "lmhead_distill_narrow_dweight": (ctypes.c_int, [_I64, _I32, _I32, _I32]),
     "lmhead_distill_logits_fwd": (ctypes.c_int, [_VP, ctypes.c_int, _I64, _VP, _VP, _VP, _VP, _I64,
                                                  _I32, _I32, ctypes.c_float, ctypes.c_float, _VP,
                                                  _VP, _VP]),
@@ -287,6 +289,8 @@ def _check_rows(t, name, shape, dtypes=None):
 
 
 def _check_teacher(top_ids, top_logits, teacher_lse, loss_mask, T):
+    if _torch is None:
+        _bind_torch()
     torch = _torch
     K = top_ids.shape[1] if top_ids.dim() == 2 else -1
     _check_tensor(top_ids, "top_ids", torch.int32, (T, K))
@@ -513,6 +517,11 @@ def lmhead_distill_workspace_size(op, T, H, V, K, chunk_size):
     return int(library().lmhead_distill_workspace_size(op, T, H, V, K, chunk_size))
 
 
+def lmhead_distill_narrow_dweight(T, H, V, chunk_size):
+    """Whether ``lmhead_distill_bwd`` can write d_weight in bf16 for these sizes."""
+    return bool(library().lmhead_distill_narrow_dweight(T, H, V, chunk_size))
+
+
 def lmhead_distill_fwd(hidden, weight, top_ids, top_logits, teacher_lse, loss_mask, temperature,
                        teacher_temperature, chunk_size, loss, lse, z_top, workspace, stream=None):
     """C ``lmhead_distill_fwd`` on torch tensors; returns the status code."""
@@ -538,7 +547,8 @@ def lmhead_distill_fwd(hidden, weight, top_ids, top_logits, teacher_lse, loss_ma
 def lmhead_distill_bwd(hidden, weight, top_ids, top_logits, teacher_lse, loss_mask, temperature,
                        teacher_temperature, chunk_size, grad_loss, lse, z_top, d_hidden, d_weight,
                        accumulate_dweight, workspace, stream=None):
-    """C ``lmhead_distill_bwd`` on torch tensors; returns the status code."""
+    """C ``lmhead_distill_bwd`` on torch tensors (d_weight fp32, or bf16 where
+    ``lmhead_distill_narrow_dweight``); returns the status code."""
     import torch
     T, H = hidden.shape
     V = weight.shape[0]
@@ -549,7 +559,8 @@ def lmhead_distill_bwd(hidden, weight, top_ids, top_logits, teacher_lse, loss_ma
     _check_tensor(lse, "lse", torch.float32, (T,))
     _check_tensor(z_top, "z_top", torch.float32, (T, K))
     _check_tensor(d_hidden, "d_hidden", torch.float32, (T, H))
-    _check_tensor(d_weight, "d_weight", torch.float32, (V, H))
+    kind = LMHEAD_BF16 if d_weight is not None and d_weight.dtype is torch.bfloat16 else LMHEAD_F32
+    _check_tensor(d_weight, "d_weight", torch.bfloat16 if kind else torch.float32, (V, H))
     _check_workspace(workspace)
     tensors = [hidden, weight, top_ids, top_logits, teacher_lse, loss_mask, grad_loss, lse, z_top,
                d_hidden, d_weight, workspace]
@@ -557,7 +568,7 @@ def lmhead_distill_bwd(hidden, weight, top_ids, top_logits, teacher_lse, loss_ma
         _ptr(hidden), _ptr(weight), _ptr(top_ids), _ptr(top_logits), _ptr(teacher_lse),
         _ptr(loss_mask), T, H, V, K, float(temperature), float(teacher_temperature),
         int(chunk_size), _ptr(grad_loss), _ptr(lse), _ptr(z_top), _ptr(d_hidden),
-        _ptr(d_weight), int(bool(accumulate_dweight)), _ptr(workspace),
+        _ptr(d_weight), kind, int(bool(accumulate_dweight)), _ptr(workspace),
         workspace.numel() * workspace.element_size(), _stream(stream))))
 
 

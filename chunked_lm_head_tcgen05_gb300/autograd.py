@@ -23,7 +23,8 @@ import torch
 
 from . import LMHEAD_OP_BWD, LMHEAD_OP_FWD, LmheadError, distill_logits_backward, \
     distill_logits_forward, layernorm_backward, layernorm_forward, lmhead_distill_bwd, \
-    lmhead_distill_fwd, lmhead_distill_workspace_size, lmhead_layernorm_workspace_size, \
+    lmhead_distill_narrow_dweight, lmhead_distill_fwd, lmhead_distill_workspace_size, \
+    lmhead_layernorm_workspace_size, \
     lmhead_logps_bwd, lmhead_logps_fwd, lmhead_workspace_size, process_logits_backward
 from . import process_logits as _process_logits
 
@@ -179,8 +180,12 @@ class LMHeadDistill(torch.autograd.Function):
         V = weight.shape[0]
         dev = hidden.device
         d_hidden = torch.empty((T, H), dtype=torch.float32, device=dev)
-        d_weight = main if main is not None else torch.empty((V, H), dtype=torch.float32,
-                                                             device=dev)
+        if main is not None:
+            d_weight = main
+        else:   # autograd hands the parameter its own type: bf16 at once where the library can
+            kind = torch.bfloat16 if lmhead_distill_narrow_dweight(T, H, V, ctx.chunk_size) \
+                else torch.float32
+            d_weight = torch.empty((V, H), dtype=kind, device=dev)
         ws = _stream_workspace(ctx.workspace_bytes, dev)
         rc = lmhead_distill_bwd(hidden, weight, top_ids, top_logits, teacher_lse, loss_mask,
                                 *ctx.temperatures, ctx.chunk_size,

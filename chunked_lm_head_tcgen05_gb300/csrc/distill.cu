@@ -11,6 +11,8 @@
 #include "operators.h"
 #include "ptx.cuh"
 
+#include <climits>
+
 namespace lmh {
 namespace {
 
@@ -24,22 +26,14 @@ constexpr int kBwdLeast = 16384;   // least (shorter rows aside)
 constexpr int kFwdThreads = 256;   // forward on held logits
 constexpr int kFwdDepth = 8;       // its packs in flight per thread (even)
 constexpr int kMaxCluster = 8;
+constexpr int kRowThreads = 128;   // lists of one row, through the head
+constexpr int kLossWarps = 4;      // rows per CTA of the loss, through the head
 
 // Row of the student's table that an entry names: negative ids wrap; -1 for
 // an id outside [-V, V).
 __device__ __forceinline__ int wrap_id(int id, int V) {
   if (id < 0) id += V;
   return (id >= 0 && id < V) ? id : -1;
-}
-
-__device__ __forceinline__ float block_sum(float v, float* red) {
-  v = warp_sum(v);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  float t = 0.f;
-  for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) t += red[w];
-  return t;
 }
 
 // The teacher's distribution of one token, formed by one warp: p[k] and the
@@ -386,90 +380,140 @@ __global__ void __launch_bounds__(kThreads, 5) logits_bwd_kernel(DistillLogits a
 }
 
 // ------------------------------------------------------------------ through the head
-// One CTA per token: z_k = hidden . weight[id_k] / tau for the K entries (one
-// warp per entry), then the loss with the statistics of the whole vocabulary.
-// The loss takes z_k - max in the statistics' own units, u = (h . w) scale
-// with the scale the GEMM used: the rounding of log2(e) / tau then cancels
-// (loss error against 64 bits 1.3e-6 with z_k = (h . w) / tau there instead).
-__global__ void __launch_bounds__(kThreads)
-    head_loss_kernel(const uint16_t* __restrict__ hidden, const uint16_t* __restrict__ weight,
-                     int H, int V, Teacher te, const uint8_t* __restrict__ mask, int T, float tau,
-                     const float4* __restrict__ stats, DeviceState* st, float* loss, float* lse,
-                     float* z_top) {
-  pdl_wait_prerequisites();
-  pdl_launch_dependents();
-  __shared__ float red[kWarps], total;
-  __shared__ float p[kMaxTeacher], logp[kMaxTeacher], z[kMaxTeacher];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int K = te.K;
-  const float scale = kLog2e / tau;
-  for (int t = blockIdx.x; t < T; t += gridDim.x) {
-    float* zt = z_top + static_cast<int64_t>(t) * K;
-    if (mask && !mask[t]) {
-      for (int k = threadIdx.x; k < K; k += kThreads) zt[k] = 0.f;
-      if (threadIdx.x == 0) {
-        loss[t] = 0.f;
-        lse[t] = 0.f;
-      }
-      continue;
+// A row's K ids in ascending order: position of entry k among them.  Entries
+// without an id (absent, or outside [-V, V)) have key INT_MAX and come last, in
+// entry order.  Ranks by counting: K compares per entry, all from shared memory.
+__device__ __forceinline__ int id_key(const Teacher& te, int64_t at, int V) {
+  if (te.logits[at] == -INFINITY) return INT_MAX;
+  const int v = wrap_id(te.ids[at], V);
+  return v < 0 ? INT_MAX : v;
+}
+
+__device__ __forceinline__ int rank_of(const int* key, int K, int k) {
+  const int mine = key[k];
+  int rank = 0;
+  for (int j = 0; j < K; ++j) rank += key[j] < mine || (key[j] == mine && j < k);
+  return rank;
+}
+
+// start[n] = entries whose id lies before 256-column tile n.
+__device__ __forceinline__ void tile_starts(const int* sorted, int K, int n_tiles, uint16_t* start) {
+  for (int n = threadIdx.x; n <= n_tiles; n += kRowThreads) {
+    int lo = 0, hi = K;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (sorted[mid] < n * BN)
+        lo = mid + 1;
+      else
+        hi = mid;
     }
-    if (warp == 0) {
-      const float sum = teacher_row(te, t, p, logp);
-      if (lane == 0) total = sum;
-    }
-    __syncthreads();
-    const float P = total;
-    const uint4* h = reinterpret_cast<const uint4*>(hidden + static_cast<int64_t>(t) * H);
-    bool bad = false;
-    for (int k = warp; k < K; k += kWarps) {
-      const bool absent = logp[k] == -INFINITY;
-      const int v = absent ? -1 : wrap_id(te.ids[static_cast<int64_t>(t) * K + k], V);
-      float acc = 0.f;
-      if (v >= 0) {
-        const uint4* wr = reinterpret_cast<const uint4*>(weight + static_cast<int64_t>(v) * H);
-        for (int i = lane; i < H / 8; i += 32) {
-          const Pack<__nv_bfloat16, 8> x = *reinterpret_cast<const Pack<__nv_bfloat16, 8>*>(h + i);
-          const Pack<__nv_bfloat16, 8> y = *reinterpret_cast<const Pack<__nv_bfloat16, 8>*>(wr + i);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) acc = fmaf(to_f32(x.v[j]), to_f32(y.v[j]), acc);
-        }
-      } else if (!absent) {
-        bad = true;
-      }
-      acc = warp_sum(acc);
-      if (lane == 0) {
-        const float none = absent ? 0.f : __int_as_float(0x7fc00000);
-        z[k] = v >= 0 ? acc * scale : none;
-        zt[k] = v >= 0 ? acc / tau : none;
-      }
-    }
-    if (bad && lane == 0) atomicCAS(&st->status, 0, STATUS_BAD_TARGET);
-    __syncthreads();
-    const float4 q = stats[t];
-    const float ln_s = logf(q.y);
-    float term = 0.f;
-    for (int k = threadIdx.x; k < K; k += kThreads)
-      term += loss_term(p[k], logp[k], (z[k] - q.x) * kLn2);
-    const float A = block_sum(term, red);
-    if (threadIdx.x == 0) {
-      lse[t] = fmaf(q.x, kLn2, ln_s);
-      loss[t] = P == 0.f ? 0.f : fmaf(P, ln_s, A);
-    }
-    __syncthreads();
+    start[n] = static_cast<uint16_t>(lo);
   }
 }
 
-// One CTA per compacted row.
-__global__ void __launch_bounds__(kThreads)
+// Lists of the forward, one CTA per compacted row: ids ascending, the entry each
+// came from, and where each tile's begin.
+__global__ void __launch_bounds__(kRowThreads)
+    distill_lists_kernel(Teacher te, int V, const int* __restrict__ idx, const DeviceState* st,
+                         int T_alloc, RowIds lists, int32_t* out_ids, uint16_t* out_start,
+                         uint16_t* order) {
+  pdl_wait_prerequisites();
+  pdl_launch_dependents();
+  __shared__ int key[kMaxTeacher], sorted[kMaxTeacher];
+  const int K = te.K, rows = min(st->rows, T_alloc);
+  for (int r = blockIdx.x; r < rows; r += gridDim.x) {
+    const int64_t t = idx ? idx[r] : r;
+    for (int k = threadIdx.x; k < K; k += kRowThreads) key[k] = id_key(te, t * K + k, V);
+    __syncthreads();
+    for (int k = threadIdx.x; k < K; k += kRowThreads) {
+      const int at = rank_of(key, K, k);
+      sorted[at] = key[k];
+      out_ids[static_cast<int64_t>(r) * K + at] = key[k];
+      order[static_cast<int64_t>(r) * K + at] = static_cast<uint16_t>(k);
+    }
+    __syncthreads();
+    tile_starts(sorted, K, lists.start_ld - 1, out_start + static_cast<int64_t>(r) * lists.start_ld);
+  }
+}
+
+// The loss, one warp per compacted row: the vocabulary splits' statistics joined,
+// the picked logits put back in entry order.  z - max is taken in the statistics'
+// own units, u = (h . w) scale with the scale the GEMM used, so that the rounding
+// of log2(e) / tau cancels.
+__global__ void __launch_bounds__(32 * kLossWarps)
+    distill_loss_kernel(Teacher te, int V, float tau, const int* __restrict__ idx, DeviceState* st,
+                        int T_alloc, const float4* __restrict__ partials, int n_splits, int part_ld,
+                        const int32_t* __restrict__ sorted, const uint16_t* __restrict__ order,
+                        const float* __restrict__ picked, float* loss, float* lse, float* z_top) {
+  extern __shared__ float teacher[];   // per warp: p, log p, u [K]
+  pdl_wait_prerequisites();
+  pdl_launch_dependents();
+  const int K = te.K, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float* const p = teacher + 3 * K * warp;
+  float* const logp = p + K;
+  float* const u = logp + K;
+  const float scale = kLog2e / tau;
+  const int rows = min(st->rows, T_alloc);
+  for (int r = blockIdx.x * kLossWarps + warp; r < rows; r += gridDim.x * kLossWarps) {
+    const int64_t t = idx ? idx[r] : r, at = static_cast<int64_t>(r) * K;
+    const float4 q = lane < n_splits ? partials[static_cast<int64_t>(lane) * part_ld + r]
+                                     : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+    const float P = teacher_row(te, t, p, logp);
+    bool bad = false;
+    for (int j = lane; j < K; j += 32) {
+      const int k = order[at + j];
+      float z = 0.f, own = 0.f;
+      if (sorted[at + j] != INT_MAX) {
+        own = picked[at + j];
+        z = own / tau;
+      } else if (te.logits[t * K + k] != -INFINITY) {   // present, but no id of the vocabulary
+        z = own = __int_as_float(0x7fc00000);
+        bad = true;
+      }
+      u[k] = own * scale;
+      z_top[t * K + k] = z;
+    }
+    if (bad) atomicCAS(&st->status, 0, STATUS_BAD_TARGET);
+    __syncwarp();
+    const float M = warp_max(q.x);
+    const float ln_s = logf(warp_sum(q.y * exp2f(q.x - M)));
+    float term = 0.f;
+    for (int k = lane; k < K; k += 32)
+      if (logp[k] != -INFINITY) term += loss_term(p[k], logp[k], (u[k] - M) * kLn2);
+    const float A = warp_sum(term);
+    if (lane == 0) {
+      lse[t] = fmaf(M, kLn2, ln_s);
+      loss[t] = P == 0.f ? 0.f : fmaf(P, ln_s, A);
+    }
+    __syncwarp();
+  }
+}
+
+__global__ void distill_zero_kernel(const uint8_t* __restrict__ mask, int T, int K, float* loss,
+                                    float* lse, float* z_top) {
+  pdl_wait_prerequisites();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  for (int t = (blockIdx.x * blockDim.x + threadIdx.x) >> 5; t < T; t += (gridDim.x * blockDim.x) >> 5) {
+    if (mask[t]) continue;
+    for (int k = lane; k < K; k += 32) z_top[static_cast<int64_t>(t) * K + k] = 0.f;
+    if (lane == 0) loss[t] = lse[t] = 0.f;
+  }
+}
+
+// The backward's side of a row, one CTA per compacted row: the GEMM epilogue's
+// coefficients (dz = g P softmax(z) for every id) and, in ascending order of the
+// teacher's ids, the cotangents that replace the dense ones there.
+__global__ void __launch_bounds__(kRowThreads)
     distill_prep_kernel(Teacher te, int V, float tau, const int* __restrict__ idx, int T_alloc,
                         const float* __restrict__ grad_loss, const float* __restrict__ lse,
                         const float* __restrict__ z_top, DeviceState* st, float4* coef,
-                        int32_t* patch_ids, uint16_t* patch_values) {
+                        RowIds lists, int32_t* out_ids, uint16_t* out_start, float* out_values) {
   pdl_wait_prerequisites();
   pdl_launch_dependents();
   __shared__ float total;
   __shared__ float p[kMaxTeacher], logp[kMaxTeacher];
-  __shared__ int id[kMaxTeacher];
+  __shared__ int key[kMaxTeacher], sorted[kMaxTeacher];
   const int K = te.K;
   const int rows = st->rows;
   for (int r = blockIdx.x; r < T_alloc; r += gridDim.x) {
@@ -477,42 +521,43 @@ __global__ void __launch_bounds__(kThreads)
       if (threadIdx.x == 0) coef[r] = make_float4(0.f, 0.f, 0.f, 0.f);
       continue;
     }
-    const int t = idx ? idx[r] : r;
+    const int64_t t = idx ? idx[r] : r;
     if (threadIdx.x < 32) {
       const float sum = teacher_row(te, t, p, logp);
       if (threadIdx.x == 0) total = sum;
     }
-    __syncthreads();
-    const float P = total;
     bool bad = false;
-    for (int k = threadIdx.x; k < K; k += kThreads) {
-      const bool absent = logp[k] == -INFINITY;
-      id[k] = absent ? -1 : wrap_id(te.ids[static_cast<int64_t>(t) * K + k], V);
-      bad |= id[k] < 0 && !absent;
+    for (int k = threadIdx.x; k < K; k += kRowThreads) {
+      key[k] = id_key(te, t * K + k, V);
+      bad |= key[k] == INT_MAX && te.logits[t * K + k] != -INFINITY;
     }
     if (bad) atomicCAS(&st->status, 0, STATUS_BAD_TARGET);
     __syncthreads();
-    const float g = grad_loss[t] / tau, L = lse[t];
-    const float gP = P == 0.f ? 0.f : g * P;
+    const float P = total, g = grad_loss[t] / tau, L = lse[t];
+    const float gP = P == 0.f ? 0.f : g * P;   // a row without a teacher has no gradient
     if (threadIdx.x == 0) coef[r] = make_float4(L * kLog2e, 0.f, -gP, 0.f);
-    for (int k = threadIdx.x; k < K; k += kThreads) {
-      const int64_t at = static_cast<int64_t>(r) * K + k;
-      patch_ids[at] = id[k];
-      if (id[k] < 0) continue;
-      float taken = 0.f;
-      for (int i = 0; i < K; ++i) taken += id[i] == id[k] ? p[i] : 0.f;
-      const float q = ex2_approx((z_top[static_cast<int64_t>(t) * K + k] - L) * kLog2e);
-      const __nv_bfloat16 v = __float2bfloat16_rn(fmaf(gP, q, -g * taken));
-      patch_values[at] = __bfloat16_as_ushort(v);
+    for (int k = threadIdx.x; k < K; k += kRowThreads) {
+      const int at = rank_of(key, K, k);
+      float taken = 0.f;   // repeated ids add up, and each writes the same value
+      for (int i = 0; i < K; ++i) taken += key[i] == key[k] ? p[i] : 0.f;
+      const float q = ex2_approx((z_top[t * K + k] - L) * kLog2e);
+      const float value = P == 0.f || key[k] == INT_MAX ? 0.f : fmaf(gP, q, -g * taken);
+      sorted[at] = key[k];
+      out_ids[static_cast<int64_t>(r) * K + at] = key[k];
+      out_values[static_cast<int64_t>(r) * K + at] = value;
     }
+    __syncthreads();
+    tile_starts(sorted, K, lists.start_ld - 1, out_start + static_cast<int64_t>(r) * lists.start_ld);
     __syncthreads();
   }
 }
 
+// Two launches per block: the dz GEMM has stored the dense cotangents of rows
+// [t0, t0 + rows_cap), vocabulary rows [v0, v0 + cols).
 __global__ void __launch_bounds__(kThreads)
-    distill_patch_kernel(const int32_t* __restrict__ patch_ids,
-                         const uint16_t* __restrict__ patch_values, int K, const DeviceState* st,
-                         int t0, int rows_cap, int v0, int cols, uint16_t* dz, int64_t dz_ld) {
+    distill_patch_kernel(const int32_t* __restrict__ ids, const float* __restrict__ values, int K,
+                         const DeviceState* st, int t0, int rows_cap, int v0, int cols, uint16_t* dz,
+                         int64_t dz_ld) {
   pdl_wait_prerequisites();
   pdl_launch_dependents();
   const int rows = min(st->rows - t0, rows_cap);
@@ -520,9 +565,9 @@ __global__ void __launch_bounds__(kThreads)
   for (int64_t i = blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x; i < n;
        i += static_cast<int64_t>(gridDim.x) * kThreads) {
     const int64_t at = static_cast<int64_t>(t0) * K + i;
-    const int v = patch_ids[at];
+    const int v = ids[at];
     if (v < v0 || v - v0 >= cols) continue;
-    dz[(i / K) * dz_ld + (v - v0)] = patch_values[at];
+    dz[(i / K) * dz_ld + (v - v0)] = __bfloat16_as_ushort(__float2bfloat16_rn(values[at]));
   }
 }
 
@@ -576,33 +621,55 @@ cudaError_t launch_distill_logits_bwd(const DistillLogits& a, cudaStream_t s) {
   return logits_bwd<__half>(a, s);
 }
 
-cudaError_t launch_distill_head_loss(const uint16_t* hidden, const uint16_t* weight, int H, int V,
-                                     const Teacher& teacher, const uint8_t* mask, int T, float tau,
-                                     const float4* stats, DeviceState* st, float* loss, float* lse,
-                                     float* z_top, cudaStream_t s) {
-  const int cap = sm_count() * 8;
-  return launch_dependent(head_loss_kernel, dim3(T < cap ? T : cap), kThreads, 0, 1, s, hidden,
-                          weight, H, V, teacher, mask, T, tau, stats, st, loss, lse, z_top);
+cudaError_t launch_distill_lists(const Teacher& teacher, int V, const int* idx, int T_alloc,
+                                 const DeviceState* st, const RowIds& lists, int32_t* ids,
+                                 uint16_t* start, uint16_t* order, cudaStream_t s) {
+  const int cap = sm_count() * 16;
+  return launch_dependent(distill_lists_kernel, dim3(T_alloc < cap ? T_alloc : cap), kRowThreads, 0,
+                          1, s, teacher, V, idx, st, T_alloc, lists, ids, start, order);
+}
+
+cudaError_t launch_distill_loss(const Teacher& teacher, int V, float tau, const int* idx,
+                                int T_alloc, DeviceState* st, const float4* partials, int n_splits,
+                                int part_ld, const RowIds& lists, const uint16_t* order,
+                                const float* picked, float* loss, float* lse, float* z_top,
+                                cudaStream_t s) {
+  static std::atomic<int> ready[64];
+  const cudaError_t e = allow_shared(ready, reinterpret_cast<const void*>(distill_loss_kernel),
+                                     3 * sizeof(float) * kMaxTeacher * kLossWarps);
+  if (e != cudaSuccess) return e;
+  const int ctas = (T_alloc + kLossWarps - 1) / kLossWarps, cap = sm_count() * 16;
+  return launch_dependent(distill_loss_kernel, dim3(ctas < cap ? ctas : cap), 32 * kLossWarps,
+                          3 * sizeof(float) * teacher.K * kLossWarps, 1, s, teacher, V, tau, idx, st,
+                          T_alloc, partials, n_splits, part_ld, lists.ids, order, picked, loss, lse,
+                          z_top);
+}
+
+cudaError_t launch_distill_zero(const uint8_t* mask, int T, int K, float* loss, float* lse,
+                                float* z_top, cudaStream_t s) {
+  const int64_t ctas = (static_cast<int64_t>(T) * 32 + 255) / 256, cap = sm_count() * 16;
+  return launch_dependent(distill_zero_kernel, dim3(static_cast<unsigned>(ctas < cap ? ctas : cap)),
+                          256, 0, 1, s, mask, T, K, loss, lse, z_top);
 }
 
 cudaError_t launch_distill_prep(const Teacher& teacher, int V, float tau, const int* idx,
                                 int T_alloc, const float* grad_loss, const float* lse,
                                 const float* z_top, DeviceState* st, float4* coef,
-                                int32_t* patch_ids, uint16_t* patch_values, cudaStream_t s) {
-  const int cap = sm_count() * 8;
-  return launch_dependent(distill_prep_kernel, dim3(T_alloc < cap ? T_alloc : cap), kThreads, 0, 1,
-                          s, teacher, V, tau, idx, T_alloc, grad_loss, lse, z_top, st, coef,
-                          patch_ids, patch_values);
+                                const RowIds& lists, int32_t* ids, uint16_t* start, float* values,
+                                cudaStream_t s) {
+  const int cap = sm_count() * 16;
+  return launch_dependent(distill_prep_kernel, dim3(T_alloc < cap ? T_alloc : cap), kRowThreads, 0,
+                          1, s, teacher, V, tau, idx, T_alloc, grad_loss, lse, z_top, st, coef, lists,
+                          ids, start, values);
 }
 
-cudaError_t launch_distill_patch(const int32_t* patch_ids, const uint16_t* patch_values, int K,
+cudaError_t launch_distill_patch(const int32_t* ids, const float* values, int K,
                                  const DeviceState* st, int t0, int rows_cap, int v0, int cols,
                                  uint16_t* dz, int64_t dz_ld, cudaStream_t s) {
   const int64_t blocks = (static_cast<int64_t>(rows_cap) * K + kThreads - 1) / kThreads;
   const int64_t cap = static_cast<int64_t>(sm_count()) * 8;
   return launch_dependent(distill_patch_kernel, dim3(static_cast<int>(blocks < cap ? blocks : cap)),
-                          kThreads, 0, 1, s, patch_ids, patch_values, K, st, t0, rows_cap, v0,
-                          cols, dz, dz_ld);
+                          kThreads, 0, 1, s, ids, values, K, st, t0, rows_cap, v0, cols, dz, dz_ld);
 }
 
 }  // namespace lmh

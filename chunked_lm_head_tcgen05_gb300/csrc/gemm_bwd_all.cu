@@ -185,6 +185,9 @@ __device__ __forceinline__ bool wait_flag(const int* f, int target, volatile int
   }
 }
 
+// PATCH: the distillation backward, whose cotangents at each row's listed ids
+// replace the dense ones, and whose d_weight may be bf16.
+template <bool PATCH>
 __global__ void __launch_bounds__(GEMM_THREADS, 1)
     bwd_all_kernel(const __grid_constant__ BwdAllArgs A) {
   using C = TileCfg<true>;
@@ -535,9 +538,15 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
         // a dW tile of a token block without scored tokens: zeros unless it adds
         const int col0 = x.n * BN;
         if (x.k.tb == 0 && !A.accumulate_dweight && rloc < x.k.vact) {
-          float* dst = A.d_weight + static_cast<int64_t>(x.k.v0 + rloc) * A.H + col0;
+          const int64_t at = static_cast<int64_t>(x.k.v0 + rloc) * A.H + col0;
           const int lim = min(BN, A.H - col0);
-          for (int j = 0; j < lim; ++j) dst[j] = 0.f;
+          if (PATCH && A.dweight_bf16) {
+            uint16_t* dst = reinterpret_cast<uint16_t*>(A.d_weight) + at;
+            for (int j = 0; j < lim; ++j) dst[j] = 0;
+          } else {
+            float* dst = A.d_weight + at;
+            for (int j = 0; j < lim; ++j) dst[j] = 0.f;
+          }
         }
         signal(F.dw_col(x.b, x.m), nullptr, false);
         continue;
@@ -591,6 +600,23 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
             y = A.y_c[x.k.t0 + rloc];
           }
           const int yt = y - x.k.v0 - col0;
+          // distillation: this row's ids in this tile, and the cotangents there
+          const int32_t* ids = nullptr;
+          const float* values = nullptr;
+          int next_id = INT_MAX, left = 0;
+          if constexpr (PATCH) {
+            if (rloc < x.k.rows) {
+              const int64_t r = x.k.t0 + rloc;
+              const uint16_t* start = A.patch.start + r * A.patch.start_ld + (x.k.v0 + col0) / BN;
+              const int first = start[0];
+              left = start[1] - first;
+              if (left > 0) {
+                ids = A.patch.ids + r * A.patch.k + first;
+                values = A.patch_value + r * A.patch.k + first;
+                next_id = *ids - x.k.v0 - col0;
+              }
+            }
+          }
   #pragma unroll 1
           for (int cc = 0; cc < BN / 64; ++cc) {
             uint32_t pk[32];
@@ -611,6 +637,15 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
   #pragma unroll
                 for (int j = 0; j < 32; ++j)
                   if (j == yt - cb) g[j] += cf.w;
+              }
+              if constexpr (PATCH) {
+                while (static_cast<unsigned>(next_id - cb) < 32u) {
+                  const float value = *values++;
+  #pragma unroll
+                  for (int j = 0; j < 32; ++j)
+                    if (j == next_id - cb) g[j] = value;
+                  next_id = --left > 0 ? *++ids - x.k.v0 - col0 : INT_MAX;
+                }
               }
               // columns past the vocabulary block hold zeros: the dh and dW
               // tiles read whole 64-wide K steps of the scratch
@@ -672,6 +707,22 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
           signal(F.dh_row(x.b, x.m), nullptr, !scatter);
         } else {
           const int mode = (x.k.tb > 0 || A.accumulate_dweight) ? 2 : 1;
+          if (PATCH && A.dweight_bf16) {
+  #pragma unroll 1
+            for (int cc = 0; cc < BN / 64; ++cc) {
+              uint32_t pk[32];
+  #pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                float v[32];
+                tmem_load_32(tcol + cc * 64 + h * 32, v);
+                if (cc == BN / 64 - 1 && h == 1) release_acc();
+  #pragma unroll
+                for (int k = 0; k < 16; ++k) pk[h * 16 + k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
+              }
+              stage_out(pk, stg0, nstore++, lrow, issuer, &A.dw_out, 1, col0 + cc * 64,
+                        x.k.v0 + x.m * PAIR_M + r128, &st->status);
+            }
+          } else
   #pragma unroll 1
           for (int c = 0; c < BN / 32; ++c) {
             float v[32];
@@ -704,13 +755,16 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
 
 }  // namespace
 
-cudaError_t launch_gemm_bwd_all(const BwdAllArgs& a, int grid, cudaStream_t s) {
+namespace {
+
+template <bool PATCH>
+cudaError_t launch_bwd_all(const BwdAllArgs& a, int grid, cudaStream_t s) {
   if (a.n_tb < 1 || a.n_tb > BWD_ALL_MAX_TOKEN_BLOCKS || a.n_vb < 1 || a.T_b % (2 * BM) != 0 ||
       a.V_b % BN != 0 || a.H % BK != 0)
     return cudaErrorInvalidValue;
   static std::atomic<int> ready[64];   // per device
   int pairs_max = 0;
-  const cudaError_t e = prepare_kernel(ready, reinterpret_cast<const void*>(bwd_all_kernel),
+  const cudaError_t e = prepare_kernel(ready, reinterpret_cast<const void*>(bwd_all_kernel<PATCH>),
                                        BWD_ALL_SMEM_BYTES, true, &pairs_max);
   if (e != cudaSuccess) return e;
   int pairs = (grid + 1) / 2;
@@ -730,7 +784,13 @@ cudaError_t launch_gemm_bwd_all(const BwdAllArgs& a, int grid, cudaStream_t s) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, bwd_all_kernel, a);
+  return cudaLaunchKernelEx(&cfg, bwd_all_kernel<PATCH>, a);
+}
+
+}  // namespace
+
+cudaError_t launch_gemm_bwd_all(const BwdAllArgs& a, int grid, cudaStream_t s) {
+  return a.patch.ids ? launch_bwd_all<true>(a, grid, s) : launch_bwd_all<false>(a, grid, s);
 }
 
 }  // namespace lmh

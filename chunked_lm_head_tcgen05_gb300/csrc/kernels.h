@@ -46,6 +46,18 @@ enum EpiKind : int {
   EPI_STORE_F32 = 2,   // plain fp32 tile store or read-modify-write (dh, dW)
   EPI_FWD_Z = 3,       // EPI_FWD_STATS, and also keep the logits: fp16 (u - m_tile) tiles
                        // through map_out plus the per-(row, tile) reference m_tile
+  EPI_FWD_PICK = 4,    // online max / exp-sum per vocab split, and the raw logits at each
+                       // row's own list of ids
+};
+
+// Per-row lists of vocabulary ids (a teacher's top entries): `k` ids per row,
+// ascending, those that are no id at the end as INT_MAX.  start[row][n] is the
+// first position whose id lies in 256-column tile n or after it (n_tiles + 1
+// values per row, start_ld apart).
+struct RowIds {
+  const int32_t* ids;
+  const uint16_t* start;
+  int k, start_ld;
 };
 
 struct GemmArgs {
@@ -77,6 +89,8 @@ struct GemmArgs {
   int zero_if_empty;     // EPI_STORE_F32: K == 0 and !accumulate writes zeros
   float* m_tile;         // EPI_FWD_Z: [rows][m_tile_ld] reference max of each 256-column tile
   int m_tile_ld;
+  RowIds pick;           // EPI_FWD_PICK: lists by row_base + row
+  float* pick_z;         // EPI_FWD_PICK: [rows][pick.k] accumulators at those ids
   int n_fastest;         // unit order: 1 = N tiles of one M block consecutively (one tile per unit)
   int m_group;           // unit order otherwise: M blocks fastest, taken in groups of m_group
                          // blocks that run through every N split before the next group
@@ -136,6 +150,10 @@ struct BwdAllArgs {
   float* d_hidden;
   float* d_weight;
   int accumulate_dweight;
+  int dweight_bf16;    // d_weight is bf16 (one token block, not accumulating); dw_out then
+                       // has boxes 64 x 128
+  RowIds patch;        // distillation: dz at these ids (by t0 + row) is patch_value instead
+  const float* patch_value;
   int* unit_counter;   // zeroed; one per launch
   int* flags;          // per block: all dz [1], dz columns [NT], dh rows [MT], dW columns [NT]
   // -1: every unit in one launch.  w in [0, blocks]: launch w of a sequence of
@@ -156,6 +174,7 @@ cudaError_t launch_gemm_fwd_stats(const LaunchArgs& a, int grid, bool pair, cuda
 cudaError_t launch_gemm_bwd_dz(const LaunchArgs& a, int grid, bool pair, cudaStream_t s);
 cudaError_t launch_gemm_bwd_grad(const LaunchArgs& a, int grid, bool pair, cudaStream_t s);
 cudaError_t launch_gemm_fwd_z(const LaunchArgs& a, int grid, bool pair, cudaStream_t s);
+cudaError_t launch_gemm_fwd_pick(const LaunchArgs& a, int grid, bool pair, cudaStream_t s);
 
 // Auxiliary kernels (aux.cu).
 // Mask compaction works on chunks of this many tokens; `counts` holds one

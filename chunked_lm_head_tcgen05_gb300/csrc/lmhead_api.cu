@@ -322,6 +322,14 @@ BwdPlan plan_bwd(int64_t T, int64_t H, int64_t V, int64_t chunk) {
   return p;
 }
 
+// How the backward launches its blocks: 0 two launches per block, 1 one persistent
+// launch, 2 one launch per block window.
+int bwd_launch_mode(const BwdPlan& bp, int64_t H) {
+  int mode = bwd_mode();
+  if (mode < 0) mode = persistent_pays(bp.Tb, bp.Vb, H) ? 1 : 0;
+  return use_pair() && bp.n_tb <= BWD_ALL_MAX_TOKEN_BLOCKS ? mode : 0;
+}
+
 // Forward unit order.  The forward's units (token block, vocabulary split)
 // are handed out token-block fastest, so the CTAs running at one time sweep
 // the same split's W tiles together (one DRAM read, the rest L2 hits) while
@@ -564,20 +572,34 @@ lmhead_status lmhead_plan_info(int64_t T, int32_t H, int32_t V, int32_t chunk_si
 
 namespace {
 
+// The distillation forward's side: lists before the GEMM, the loss after it.
+struct DistillForward {
+  Teacher teacher;
+  RowIds lists;        // workspace, as the next pointers
+  int32_t* ids;
+  uint16_t* start;
+  uint16_t* order;
+  float* picked;
+  float* loss;
+  float* z_top;
+};
+
 // Forward over vocabulary rows [v0, v0 + V) of a vocabulary of Vt ids.  With
-// shard_part == NULL (the whole vocabulary: v0 = 0, Vt = V) it writes logp /
+// `distill` (whole vocabulary, no targets) it writes the distillation's loss, lse
+// and z_top.  With shard_part == NULL (the whole vocabulary: v0 = 0, Vt = V) it writes logp /
 // entropy / lse; otherwise the token's statistics over these rows go to
 // shard_part, for lmhead_combine_shards.
 lmhead_status fwd_impl(const uint16_t* hidden, const uint16_t* weight, const int32_t* targets,
                        const uint8_t* loss_mask, int64_t T, int32_t H, int32_t V, int32_t v0,
                        int32_t Vt, float temperature, int32_t chunk_size, float* logp,
-                       float* entropy, float* lse, float4* shard_part, void* workspace,
-                       size_t workspace_bytes, lmhead_stream_t stream) {
+                       float* entropy, float* lse, float4* shard_part,
+                       const DistillForward* distill, void* workspace, size_t workspace_bytes,
+                       lmhead_stream_t stream) {
   lmhead_status rc = check_sizes(T, H, V, temperature, chunk_size);
   if (rc != LMHEAD_OK) return rc;
   if (T == 0) return LMHEAD_OK;
-  // targets may be NULL when only the statistics are wanted (distillation)
-  if (!hidden || !weight || !workspace || (!shard_part && (!targets || !logp || !lse)))
+  if (!hidden || !weight || !workspace || (!distill && !targets) ||
+      (!distill && !shard_part && (!logp || !lse)))
     return LMHEAD_ERR_INVALID_ARG;
   if (!aligned16(hidden) || !aligned16(weight) || (reinterpret_cast<uintptr_t>(workspace) & 255))
     return LMHEAD_ERR_UNSUPPORTED;
@@ -618,6 +640,28 @@ lmhead_status fwd_impl(const uint16_t* hidden, const uint16_t* weight, const int
   la.n_problems = 1;
   la.counter = f.counters;
   const int grid = static_cast<int>(std::min<int64_t>(m_tiles * splits * (pair ? 2 : 1), sms));
+  if (distill) {
+    const DistillForward& d = *distill;
+    const int T_alloc = static_cast<int>(f.T_alloc);
+    LMH_TRY(launch("distill_lists", s, [&] {
+      return launch_distill_lists(d.teacher, V, f.idx, T_alloc, f.st, d.lists, d.ids, d.start,
+                                  d.order, s);
+    }));
+    p.pick = d.lists;
+    p.pick_z = d.picked;
+    LMH_TRY(launch("fwd_pick_gemm", s, [&] { return launch_gemm_fwd_pick(la, grid, pair, s); }));
+    LMH_TRY(launch("distill_loss", s, [&] {
+      return launch_distill_loss(d.teacher, V, temperature, f.idx, T_alloc, f.st, part, splits,
+                                 T_alloc, d.lists, d.order, d.picked, d.loss, lse, d.z_top, s);
+    }));
+    if (loss_mask) {
+      LMH_TRY(launch("distill_zero", s, [&] {
+        return launch_distill_zero(loss_mask, static_cast<int>(T), d.teacher.K, d.loss, lse,
+                                   d.z_top, s);
+      }));
+    }
+    return LMHEAD_OK;
+  }
   LMH_TRY(launch("fwd_stats_gemm", s, [&] { return launch_gemm_fwd_stats(la, grid, pair, s); }));
   LMH_TRY(launch("fwd_merge", s, [&] {
     return launch_fwd_merge(part, splits, static_cast<int>(f.T_alloc), f.idx, f.y_c, f.st, 0,
@@ -633,15 +677,18 @@ lmhead_status fwd_impl(const uint16_t* hidden, const uint16_t* weight, const int
 }
 
 // What the distillation backward puts in place of the log-prob / entropy
-// cotangent: the row coefficients come from launch_distill_prep, and each dz
-// block gets the exact cotangents at the teacher's ids before the gradient
-// contractions read it.
-struct DistillCotangent {
+// cotangent: the row coefficients come from launch_distill_prep, and the exact
+// cotangents at the teacher's ids replace the dense ones, in the persistent
+// launch's epilogue or, with two launches per block, in the stored dz block.
+struct DistillBackward {
   Teacher teacher;
   const float* grad_loss;
   const float* z_top;
-  int32_t* patch_ids;       // workspace [T_alloc, K]
-  uint16_t* patch_values;   // workspace [T_alloc, K]
+  RowIds lists;        // workspace, as the next pointers
+  int32_t* ids;
+  uint16_t* start;
+  float* values;
+  bool dweight_bf16;   // d_weight is bf16 (only where bf16_dweight_fits)
 };
 
 // Backward over vocabulary rows [v0, v0 + V) of a vocabulary of Vt ids, given
@@ -654,7 +701,7 @@ lmhead_status bwd_impl(const uint16_t* hidden, const uint16_t* weight, const int
                        int32_t Vt, float temperature, int32_t chunk_size,
                        const float* grad_logp, const float* grad_entropy, const float* lse,
                        const float* entropy, float* d_hidden, float* d_weight,
-                       int accumulate_dweight, const DistillCotangent* distill, void* workspace,
+                       int accumulate_dweight, const DistillBackward* distill, void* workspace,
                        size_t workspace_bytes, lmhead_stream_t stream) {
   lmhead_status rc = check_sizes(T, H, V, temperature, chunk_size);
   if (rc != LMHEAD_OK) return rc;
@@ -688,8 +735,8 @@ lmhead_status bwd_impl(const uint16_t* hidden, const uint16_t* weight, const int
     LMH_TRY(launch("distill_prep", s, [&] {
       return launch_distill_prep(distill->teacher, V, temperature, f.idx,
                                  static_cast<int>(f.T_alloc), distill->grad_loss, lse,
-                                 distill->z_top, f.st, coef, distill->patch_ids,
-                                 distill->patch_values, s);
+                                 distill->z_top, f.st, coef, distill->lists, distill->ids,
+                                 distill->start, distill->values, s);
     }));
   } else {
     LMH_TRY(launch("bwd_prep", s, [&] {
@@ -709,10 +756,8 @@ lmhead_status bwd_impl(const uint16_t* hidden, const uint16_t* weight, const int
   const int64_t um = unit_rows();
   const int64_t ctas = pair ? 2 : 1;
 
-  int mode = bwd_mode();
-  if (mode < 0) mode = persistent_pays(bp.Tb, bp.Vb, H) ? 1 : 0;
-  if (distill) mode = 0;   // its dz blocks are completed between the launches
-  if (pair && mode != 0 && bp.n_tb <= BWD_ALL_MAX_TOKEN_BLOCKS) {
+  const int mode = bwd_launch_mode(bp, H);
+  if (mode != 0) {
     // every block's dz, dh and dW tiles in one launch, ordered by tile flags
     BwdAllArgs a;
     std::memset(&a, 0, sizeof(a));
@@ -724,8 +769,15 @@ lmhead_status bwd_impl(const uint16_t* hidden, const uint16_t* weight, const int
         !make_map_mn(&a.dz_mn, dz, Vb, Tb, 2ull * Vb, 2) ||
         !make_map_mn(&a.h_mn, f.h_src, H, f.rows_avail, 2ull * H, 2) ||
         (!f.idx && !make_out_map_f32(&a.dh_out, d_hidden, H, T, H)) ||
-        !make_out_map_f32(&a.dw_out, d_weight, H, V, H))
+        !(distill && distill->dweight_bf16
+              ? make_map(&a.dw_out, d_weight, H, V, 2ull * H, 64, BM)
+              : make_out_map_f32(&a.dw_out, d_weight, H, V, H)))
       return LMHEAD_ERR_CUDA;
+    if (distill) {
+      a.patch = distill->lists;
+      a.patch_value = distill->values;
+      a.dweight_bf16 = distill->dweight_bf16 ? 1 : 0;
+    }
     a.T_b = static_cast<int>(bp.Tb);
     a.V_b = static_cast<int>(bp.Vb);
     a.n_tb = static_cast<int>(bp.n_tb);
@@ -802,8 +854,7 @@ lmhead_status bwd_impl(const uint16_t* hidden, const uint16_t* weight, const int
       LMH_TRY(launch("bwd_dz_gemm", s, [&] { return launch_gemm_bwd_dz(lz, gz, pair, s); }));
       if (distill) {
         LMH_TRY(launch("distill_patch", s, [&] {
-          return launch_distill_patch(distill->patch_ids, distill->patch_values,
-                                      distill->teacher.K, f.st, static_cast<int>(t0),
+          return launch_distill_patch(distill->ids, distill->values, distill->teacher.K, f.st, static_cast<int>(t0),
                                       static_cast<int>(m_cap), static_cast<int>(v0),
                                       static_cast<int>(vact), dz, bp.Vb, s);
         }));
@@ -888,7 +939,7 @@ lmhead_status lmhead_logps_fwd(const uint16_t* hidden, const uint16_t* weight,
                                float* logp, float* entropy, float* lse, void* workspace,
                                size_t workspace_bytes, lmhead_stream_t stream) {
   return fwd_impl(hidden, weight, targets, loss_mask, T, H, V, 0, V, temperature, chunk_size,
-                  logp, entropy, lse, nullptr, workspace, workspace_bytes, stream);
+                  logp, entropy, lse, nullptr, nullptr, workspace, workspace_bytes, stream);
 }
 
 lmhead_status lmhead_logps_bwd(const uint16_t* hidden, const uint16_t* weight,
@@ -915,7 +966,7 @@ lmhead_status lmhead_logps_fwd_shard(const uint16_t* hidden, const uint16_t* wei
   if (!aligned16(partials)) return LMHEAD_ERR_UNSUPPORTED;
   return fwd_impl(hidden, weight_shard, targets, loss_mask, T, H, V_shard, vocab_offset,
                   vocab_total, temperature, chunk_size, nullptr, nullptr, nullptr,
-                  reinterpret_cast<float4*>(partials), workspace, workspace_bytes, stream);
+                  reinterpret_cast<float4*>(partials), nullptr, workspace, workspace_bytes, stream);
 }
 
 lmhead_status lmhead_logps_bwd_shard(const uint16_t* hidden, const uint16_t* weight_shard,
@@ -1133,21 +1184,30 @@ lmhead_status lmhead_logps_fwd_bwd(const uint16_t* hidden, const uint16_t* weigh
 namespace {
 
 // Workspace of the distillation calls: that of the head's forward or backward
-// (256-byte multiples), then the statistics of the forward, or the ids and
-// cotangents of the teacher's entries.
-bool distill_extra(int op, int64_t T, int32_t K, size_t* first, size_t* second) {
+// (256-byte multiples), then the rows' lists of the teacher's ids with what belongs
+// to them.
+struct DistillLayout {
+  size_t ids, start, order, values, total;   // offsets past the head's workspace
+  int start_ld;
+};
+
+bool distill_layout(int64_t T, int64_t V, int32_t K, DistillLayout* L) {
   if (K <= 0 || K > kMaxTeacher) return false;
-  const int64_t T_alloc = round_up(T, BM);
-  *second = 0;
-  if (op == LMHEAD_OP_FWD) {
-    *first = align256(16 * static_cast<size_t>(T));
-  } else if (op == LMHEAD_OP_BWD) {
-    *first = align256(4 * static_cast<size_t>(T_alloc) * static_cast<size_t>(K));
-    *second = align256(2 * static_cast<size_t>(T_alloc) * static_cast<size_t>(K));
-  } else {
-    return false;
-  }
+  const size_t rows = static_cast<size_t>(round_up(T, BM)), n = rows * static_cast<size_t>(K);
+  L->start_ld = static_cast<int>(ceil_div(V, BN)) + 1;
+  L->ids = 0;
+  L->values = align256(4 * n);                       // picked logits, or cotangents
+  L->order = L->values + align256(4 * n);
+  L->start = L->order + align256(2 * n);
+  L->total = L->start + align256(2 * rows * static_cast<size_t>(L->start_ld));
   return true;
+}
+
+// Whether the distillation backward can write d_weight in bf16: every tile is
+// then complete when it is stored (one token block, one persistent launch).
+bool bf16_dweight_fits(int64_t T, int64_t H, int64_t V, int64_t chunk) {
+  const BwdPlan bp = plan_bwd(T, H, V, chunk);
+  return bp.n_tb == 1 && bwd_launch_mode(bp, H) == 1;
 }
 
 // The planner keeps small host tables; out of host memory there must not leave
@@ -1172,10 +1232,16 @@ extern "C" {
 
 size_t lmhead_distill_workspace_size(int op, int64_t T, int32_t H, int32_t V, int32_t K,
                                      int32_t chunk_size) {
-  size_t a = 0, b = 0;
-  if (check_sizes(T, H, V, 1.0f, chunk_size) != LMHEAD_OK || !distill_extra(op, T, K, &a, &b))
+  DistillLayout dl;
+  if ((op != LMHEAD_OP_FWD && op != LMHEAD_OP_BWD) ||
+      check_sizes(T, H, V, 1.0f, chunk_size) != LMHEAD_OK || !distill_layout(T, V, K, &dl))
     return 0;
-  return layout(op, T, H, V, chunk_size).total + a + b;
+  return layout(op, T, H, V, chunk_size).total + dl.total;
+}
+
+int lmhead_distill_narrow_dweight(int64_t T, int32_t H, int32_t V, int32_t chunk_size) {
+  return check_sizes(T, H, V, 1.0f, chunk_size) == LMHEAD_OK && T > 0 &&
+         bf16_dweight_fits(T, H, V, chunk_size);
 }
 
 lmhead_status lmhead_distill_fwd(const uint16_t* hidden, const uint16_t* weight,
@@ -1193,24 +1259,24 @@ lmhead_status lmhead_distill_fwd(const uint16_t* hidden, const uint16_t* weight,
     return LMHEAD_ERR_INVALID_ARG;
   if (!aligned16(hidden) || !aligned16(weight) || (reinterpret_cast<uintptr_t>(workspace) & 255))
     return LMHEAD_ERR_UNSUPPORTED;
-  size_t extra = 0, none = 0;
-  distill_extra(LMHEAD_OP_FWD, T, K, &extra, &none);
+  DistillLayout dl;
+  distill_layout(T, V, K, &dl);
   const size_t base = layout(LMHEAD_OP_FWD, T, H, V, chunk_size).total;
-  if (workspace_bytes < base + extra) return LMHEAD_ERR_WORKSPACE_TOO_SMALL;
-  float4* stats = reinterpret_cast<float4*>(static_cast<char*>(workspace) + base);
-  rc = no_throw([&] {
+  if (workspace_bytes < base + dl.total) return LMHEAD_ERR_WORKSPACE_TOO_SMALL;
+  char* ws = static_cast<char*>(workspace) + base;
+  DistillForward d;
+  d.teacher = {top_ids, top_logits, teacher_lse, K, teacher_temperature};
+  d.ids = reinterpret_cast<int32_t*>(ws + dl.ids);
+  d.start = reinterpret_cast<uint16_t*>(ws + dl.start);
+  d.order = reinterpret_cast<uint16_t*>(ws + dl.order);
+  d.picked = reinterpret_cast<float*>(ws + dl.values);
+  d.lists = {d.ids, d.start, K, dl.start_ld};
+  d.loss = loss;
+  d.z_top = z_top;
+  return no_throw([&] {
     return fwd_impl(hidden, weight, nullptr, loss_mask, T, H, V, 0, V, temperature, chunk_size,
-                    nullptr, nullptr, nullptr, stats, workspace, base, stream);
+                    nullptr, nullptr, lse, nullptr, &d, workspace, base, stream);
   });
-  if (rc != LMHEAD_OK) return rc;
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const Teacher teacher{top_ids, top_logits, teacher_lse, K, teacher_temperature};
-  LMH_TRY(launch("distill_head_loss", s, [&] {
-    return launch_distill_head_loss(hidden, weight, H, V, teacher, loss_mask, static_cast<int>(T),
-                                    temperature, stats, static_cast<DeviceState*>(workspace), loss,
-                                    lse, z_top, s);
-  }));
-  return LMHEAD_OK;
 }
 
 lmhead_status lmhead_distill_bwd(const uint16_t* hidden, const uint16_t* weight,
@@ -1219,35 +1285,43 @@ lmhead_status lmhead_distill_bwd(const uint16_t* hidden, const uint16_t* weight,
                                  int32_t H, int32_t V, int32_t K, float temperature,
                                  float teacher_temperature, int32_t chunk_size,
                                  const float* grad_loss, const float* lse, const float* z_top,
-                                 float* d_hidden, float* d_weight, int accumulate_dweight,
-                                 void* workspace, size_t workspace_bytes, lmhead_stream_t stream) {
+                                 float* d_hidden, void* d_weight, int d_weight_type,
+                                 int accumulate_dweight, void* workspace, size_t workspace_bytes,
+                                 lmhead_stream_t stream) {
   lmhead_status rc = check_sizes(T, H, V, temperature, chunk_size);
   if (rc == LMHEAD_OK) rc = check_teacher(K, teacher_temperature);
   if (rc != LMHEAD_OK) return rc;
-  size_t base = 0, ids = 0, values = 0;
-  DistillCotangent d{};
+  if (d_weight_type != LMHEAD_F32 && d_weight_type != LMHEAD_BF16) return LMHEAD_ERR_INVALID_ARG;
+  const bool bf16 = d_weight_type == LMHEAD_BF16;
+  if (bf16 && (accumulate_dweight || T == 0 || !bf16_dweight_fits(T, H, V, chunk_size)))
+    return LMHEAD_ERR_UNSUPPORTED;
+  size_t base = 0;
+  DistillBackward d{};
   if (T > 0) {
-    if (!top_ids || !top_logits || !grad_loss || !lse || !z_top || !workspace)
+    if (!top_ids || !top_logits || !grad_loss || !lse || !z_top || !workspace || !weight ||
+        !d_weight || !hidden || !d_hidden)
       return LMHEAD_ERR_INVALID_ARG;
-    base = layout(LMHEAD_OP_BWD, T, H, V, chunk_size).total;
-    distill_extra(LMHEAD_OP_BWD, T, K, &ids, &values);
-    // pointers and alignment come before the size, as in lmhead_logps_bwd
-    if (!weight || !d_weight || !hidden || !d_hidden) return LMHEAD_ERR_INVALID_ARG;
     if (!aligned16(weight) || !aligned16(d_weight) || !aligned16(hidden) || !aligned16(d_hidden) ||
         (reinterpret_cast<uintptr_t>(workspace) & 255))
       return LMHEAD_ERR_UNSUPPORTED;
-    if (workspace_bytes < base + ids + values) return LMHEAD_ERR_WORKSPACE_TOO_SMALL;
+    DistillLayout dl;
+    distill_layout(T, V, K, &dl);
+    base = layout(LMHEAD_OP_BWD, T, H, V, chunk_size).total;
+    if (workspace_bytes < base + dl.total) return LMHEAD_ERR_WORKSPACE_TOO_SMALL;
     char* ws = static_cast<char*>(workspace) + base;
-    d = {{top_ids, top_logits, teacher_lse, K, teacher_temperature},
-         grad_loss,
-         z_top,
-         reinterpret_cast<int32_t*>(ws),
-         reinterpret_cast<uint16_t*>(ws + ids)};
+    d.teacher = {top_ids, top_logits, teacher_lse, K, teacher_temperature};
+    d.grad_loss = grad_loss;
+    d.z_top = z_top;
+    d.ids = reinterpret_cast<int32_t*>(ws + dl.ids);
+    d.start = reinterpret_cast<uint16_t*>(ws + dl.start);
+    d.values = reinterpret_cast<float*>(ws + dl.values);
+    d.lists = {d.ids, d.start, K, dl.start_ld};
+    d.dweight_bf16 = bf16;
   }
   return no_throw([&] {
     return bwd_impl(hidden, weight, nullptr, loss_mask, T, H, V, 0, V, temperature, chunk_size,
-                    nullptr, nullptr, lse, nullptr, d_hidden, d_weight, accumulate_dweight, &d,
-                    workspace, base, stream);
+                    nullptr, nullptr, lse, nullptr, d_hidden, static_cast<float*>(d_weight),
+                    accumulate_dweight, &d, workspace, base, stream);
   });
 }
 

@@ -89,25 +89,32 @@ struct DistillLogits {
 cudaError_t launch_distill_logits_fwd(const DistillLogits& a, cudaStream_t s);
 cudaError_t launch_distill_logits_bwd(const DistillLogits& a, cudaStream_t s);
 
-// Forward through the head, after the statistics GEMM: stats[t] = {m, s, ..}
-// in log2 units as launch_fwd_merge leaves them; writes loss, lse and the
-// student's scaled logits at the teacher's ids.
-cudaError_t launch_distill_head_loss(const uint16_t* hidden, const uint16_t* weight, int H, int V,
-                                     const Teacher& teacher, const uint8_t* mask, int T, float tau,
-                                     const float4* stats, DeviceState* st, float* loss, float* lse,
-                                     float* z_top, cudaStream_t s);
-
-// Backward through the head: the GEMM epilogue's row coefficients (whose
-// target term stays unused) and, per scored row and teacher entry, the
-// vocabulary row (or -1) and the bf16 cotangent that replaces the dense one
-// there.
+// Through the head.  The teacher's ids of each scored (compacted) row go to the
+// GEMMs as ascending lists (RowIds: ids [T_alloc, K], start [T_alloc, tiles + 1]).
+// Forward, before the GEMM: the lists, and the entry each id came from.
+cudaError_t launch_distill_lists(const Teacher& teacher, int V, const int* idx, int T_alloc,
+                                 const DeviceState* st, const RowIds& lists, int32_t* ids,
+                                 uint16_t* start, uint16_t* order, cudaStream_t s);
+// Forward, after it: loss, lse and z_top of the scored tokens from the vocabulary
+// splits' statistics (as launch_fwd_merge reads them) and the picked accumulators.
+cudaError_t launch_distill_loss(const Teacher& teacher, int V, float tau, const int* idx,
+                                int T_alloc, DeviceState* st, const float4* partials, int n_splits,
+                                int part_ld, const RowIds& lists, const uint16_t* order,
+                                const float* picked, float* loss, float* lse, float* z_top,
+                                cudaStream_t s);
+// Unscored tokens' outputs.
+cudaError_t launch_distill_zero(const uint8_t* mask, int T, int K, float* loss, float* lse,
+                                float* z_top, cudaStream_t s);
+// Backward: the epilogue's row coefficients (whose target term stays unused), the
+// lists, and the cotangents that replace the dense ones at their ids.
 cudaError_t launch_distill_prep(const Teacher& teacher, int V, float tau, const int* idx,
                                 int T_alloc, const float* grad_loss, const float* lse,
                                 const float* z_top, DeviceState* st, float4* coef,
-                                int32_t* patch_ids, uint16_t* patch_values, cudaStream_t s);
-// Writes those cotangents into a dz block: rows [t0, t0 + rows_cap) of the
+                                const RowIds& lists, int32_t* ids, uint16_t* start, float* values,
+                                cudaStream_t s);
+// Writes those cotangents into a stored dz block: rows [t0, t0 + rows_cap) of the
 // compacted order, vocabulary rows [v0, v0 + cols).
-cudaError_t launch_distill_patch(const int32_t* patch_ids, const uint16_t* patch_values, int K,
+cudaError_t launch_distill_patch(const int32_t* ids, const float* values, int K,
                                  const DeviceState* st, int t0, int rows_cap, int v0, int cols,
                                  uint16_t* dz, int64_t dz_ld, cudaStream_t s);
 

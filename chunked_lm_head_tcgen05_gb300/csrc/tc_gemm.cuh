@@ -564,7 +564,20 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
       int y = -1;
       bool row_ok = false;
       int64_t orow = 0;
-      if constexpr (EPI == EPI_FWD_STATS || EPI == EPI_FWD_Z) {
+      const int32_t* ids = nullptr;   // EPI_FWD_PICK: this row's list, from the unit's first id on
+      float* picked = nullptr;
+      int next_id = INT_MAX, left = 0;
+      if constexpr (EPI == EPI_FWD_PICK) {
+        row_ok = row < s.M;
+        if (row_ok) {
+          const int64_t r = p.row_base + row;
+          const int first = p.pick.start[r * p.pick.start_ld + nb];
+          ids = p.pick.ids + r * p.pick.k + first;
+          picked = p.pick_z + r * p.pick.k + first;
+          left = p.pick.k - first;
+          if (left > 0) next_id = *ids;
+        }
+      } else if constexpr (EPI == EPI_FWD_STATS || EPI == EPI_FWD_Z) {
         row_ok = row < s.M;
         if (row_ok) y = p.y_c[p.row_base + row];
       } else if constexpr (EPI == EPI_BWD_DZ) {
@@ -655,6 +668,48 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
               for (int j = 0; j < 32; ++j)
                 if (j == yt - cb) zy = v[j] * p.scale;
             }
+          }
+        } else if constexpr (EPI == EPI_FWD_PICK) {
+          // As EPI_FWD_STATS without the entropy's sum; a chunk's exponentials
+          // are summed on their own before they join the row's, which keeps a
+          // vocabulary's sum within a few units of its last place.
+          const float2 scale2 = make_float2(p.scale, p.scale);
+#pragma unroll 1
+          for (int c = 0; c < BN / 32; ++c) {
+            float v[32];
+            tmem_load_32(tcol + c * 32, v);
+            if (c == BN / 32 - 1) release_acc();
+            const int cb = c * 32;
+            const int lim = p.n_extent - col0 - cb;   // valid columns in this chunk
+            while (static_cast<unsigned>(next_id - col0 - cb) < 32u) {
+              float z = 0.f;
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (j == next_id - col0 - cb) z = v[j];
+              *picked++ = z;
+              next_id = --left > 0 ? *++ids : INT_MAX;
+            }
+            if (lim < 32) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (j >= lim) v[j] = -INFINITY;
+            }
+            float cmax = v[0];
+#pragma unroll
+            for (int j = 1; j < 32; ++j) cmax = fmaxf(cmax, v[j]);
+            const float cm = cmax * p.scale;
+            if (cm > mrun) {
+              ssum *= ex2_approx(mrun - cm);
+              mrun = cm;
+            }
+            const float2 shift = make_float2(-mrun, -mrun);
+            float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              const float2 d = fma2(make_float2(v[j], v[j + 1]), scale2, shift);
+              sum = add2(sum, make_float2(ex2_approx(d.x), ex2_approx(d.y)));
+            }
+            ssum += sum.x + sum.y;
           }
         } else if constexpr (EPI == EPI_FWD_Z) {
           // pass 1: the tile's maximum sets this tile's reference m' (>= every
@@ -813,7 +868,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
         if (acc == 0) acc_phase ^= 1;
       }
       if (!ok) break;
-      if constexpr (EPI == EPI_FWD_STATS || EPI == EPI_FWD_Z) {
+      if constexpr (EPI == EPI_FWD_STATS || EPI == EPI_FWD_Z || EPI == EPI_FWD_PICK) {
         if (row_ok)
           p.partials[static_cast<int64_t>(split) * p.part_ld + p.row_base + row] =
               make_float4(mrun, ssum, s1, zy);

@@ -366,11 +366,12 @@ enum { LMHEAD_F32 = 0, LMHEAD_BF16 = 1, LMHEAD_F16 = 2 };
  *  z_top  [T, K] fp32 out: z at the teacher's ids (0 at absent entries and
  *         unscored tokens, NaN at an invalid id); keep it for the backward
  *  grad_loss [T] fp32: the loss's cotangent
+ *  d_weight  [V, H] of d_weight_type: LMHEAD_F32, or LMHEAD_BF16 where
+ *         lmhead_distill_narrow_dweight allows it
  *  workspace  lmhead_distill_workspace_size(LMHEAD_OP_FWD or LMHEAD_OP_BWD, ...)
- * The forward is the head's statistics GEMM and one pass that forms the K
- * products per token; the backward forms the dense part of the cotangent in the
- * recompute GEMM's epilogue and replaces it at the K ids before both gradient
- * contractions read it.
+ * The forward's GEMM keeps the K logits of each row as it passes their columns;
+ * the backward forms the dense part of the cotangent in the recompute GEMM's
+ * epilogue and replaces it at the K ids before both gradient contractions read it.
  */
 size_t lmhead_distill_workspace_size(int op, int64_t T, int32_t H, int32_t V, int32_t K,
                                      int32_t chunk_size);
@@ -389,8 +390,17 @@ lmhead_status lmhead_distill_bwd(const uint16_t* hidden, const uint16_t* weight,
                                  int32_t H, int32_t V, int32_t K, float temperature,
                                  float teacher_temperature, int32_t chunk_size,
                                  const float* grad_loss, const float* lse, const float* z_top,
-                                 float* d_hidden, float* d_weight, int accumulate_dweight,
-                                 void* workspace, size_t workspace_bytes, lmhead_stream_t stream);
+                                 float* d_hidden, void* d_weight, int d_weight_type,
+                                 int accumulate_dweight, void* workspace, size_t workspace_bytes,
+                                 lmhead_stream_t stream);
+
+/*
+ * 1 where lmhead_distill_bwd can write d_weight in bf16 (LMHEAD_BF16, without
+ * accumulation): the tokens fit one backward block and the backward runs as one
+ * persistent launch, so every tile is complete when it is stored and is rounded
+ * once.  Elsewhere LMHEAD_BF16 returns LMHEAD_ERR_UNSUPPORTED.
+ */
+int lmhead_distill_narrow_dweight(int64_t T, int32_t H, int32_t V, int32_t chunk_size);
 
 /*
  * Distillation on logits the caller holds: logits [T, V] of element type `type`,

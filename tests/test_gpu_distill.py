@@ -8,6 +8,8 @@ enters sum p (log p - z + lse).  Gradient: g P q and g p, q off by 2^-21 and 8 u
 of its exponent's operands, then one rounding to the output type.  Through the
 head the tolerances are the head's own: 1e-3 on lse, 2e-3 on the loss (times
 P), 1e-2 relative Frobenius on gradients (bf16 cotangents)."""
+import os
+
 import numpy as np
 import pytest
 import torch
@@ -258,10 +260,37 @@ def test_through_the_head(T, H, V, K, chunk, mask, own_lse, tau):
             assert rel_fro(ref.f64(got), want) <= LIMITS["d_hidden"]
     if M is not None:
         assert (dh[m == 0] == 0).all()
+    # bf16 d_weight: the fp32 tiles, rounded once
+    if lm.lmhead_distill_narrow_dweight(T, H, V, chunk):
+        narrow = torch.empty(V, H, dtype=torch.bfloat16, device="cuda")
+        assert torch.equal(lm.distill_backward(hidden, weight, ids, a, m, tau, 1.2, chunk, grad, lse,
+                                               zt, tlse, d_weight=narrow, workspace=ws)[0], dh)
+        assert torch.equal(narrow, dw.to(torch.bfloat16))
     again = lm.distill_backward(hidden, weight, ids, a, m, tau, 1.2, chunk, grad, lse, zt, tlse,
                                 d_weight=start, accumulate_dweight=True, workspace=ws)
     assert torch.equal(again[0], dh)
     assert torch.allclose(start, dw + 1.0, rtol=1e-5, atol=1e-6)
+
+
+@pytest.mark.parametrize("form", ["0", "2"])
+def test_head_backward_forms_agree(form):
+    """Two launches per block, and windows, against the persistent launch: the same bits."""
+    ensure_built()
+    T, H, V, K, chunk = 333, 192, 3001, 40, 64
+    hidden, weight, ids, a, m, grad = head_inputs(T, H, V, K, 3, True)
+    _, lse, zt = lm.distill_forward(hidden, weight, ids, a, m, 1.0, 1.0, chunk)
+    want = lm.distill_backward(hidden, weight, ids, a, m, 1.0, 1.0, chunk, grad, lse, zt)
+    old = os.environ.get("LMHEAD_BWD_PERSISTENT")
+    try:
+        os.environ["LMHEAD_BWD_PERSISTENT"] = form
+        assert not lm.lmhead_distill_narrow_dweight(T, H, V, chunk)
+        got = lm.distill_backward(hidden, weight, ids, a, m, 1.0, 1.0, chunk, grad, lse, zt)
+    finally:
+        if old is None:
+            del os.environ["LMHEAD_BWD_PERSISTENT"]
+        else:
+            os.environ["LMHEAD_BWD_PERSISTENT"] = old
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
 def test_head_every_token_unscored_or_without_a_teacher():

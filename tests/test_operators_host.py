@@ -40,7 +40,8 @@ HEAD_FWD = dict(hidden=P(), weight=P(), ids=P(), top=P(), teacher_lse=None, mask
                 workspace=P(), bytes=1 << 30, stream=None)
 HEAD_BWD = dict(hidden=P(), weight=P(), ids=P(), top=P(), teacher_lse=None, mask=None, T=8, H=64,
                 V=100, K=4, tau=1.0, teacher_tau=1.0, chunk=4, grad=P(), lse=P(), z_top=P(),
-                d_hidden=P(), d_weight=P(), accumulate=0, workspace=P(), bytes=1 << 30, stream=None)
+                d_hidden=P(), d_weight=P(), d_weight_type=0, accumulate=0, workspace=P(),
+                bytes=1 << 30, stream=None)
 PROCESS_FWD = dict(logits=P(), type=0, ld=100, R=8, V=100, tokens=P(), n_tokens=50, spans=P(),
                    repetition=P(), frequency=P(), presence=P(), offsets=P(), ids=P(), values=P(),
                    n_bias=3, allowed=P(), n_allowed=8, allowed_rows=None, out=P(), out_ld=100,
@@ -89,6 +90,8 @@ CASES = [
         (dict(hidden=None), INVALID), (dict(grad=None), INVALID), (dict(lse=None), INVALID),
         (dict(z_top=None), INVALID), (dict(d_hidden=None), INVALID), (dict(d_weight=None), INVALID),
         (dict(K=1025), UNSUPPORTED), (dict(d_weight=P((1 << 20) + 4)), UNSUPPORTED),
+        (dict(d_weight_type=2), INVALID), (dict(d_weight_type=1, accumulate=1), UNSUPPORTED),
+        (dict(d_weight_type=1, T=100000, H=4096, chunk=4096, V=151936), UNSUPPORTED),
         (dict(bytes=256), SMALL), (dict(T=0, accumulate=1), OK)]),
     ("lmhead_process_logits_fwd", PROCESS_FWD, [
         (dict(logits=None), INVALID), (dict(out=None), INVALID), (dict(R=-1), INVALID),
