@@ -120,6 +120,13 @@ struct PackRing {
       copy_async<kUnit>(static_cast<uint32_t>(__cvta_generic_to_shared(mine + (slot * kParts + q) * stride)),
                         reinterpret_cast<const char*>(src) + q * kUnit);
   }
+  __device__ __forceinline__ void clear(int slot) const {
+#pragma unroll
+    for (int q = 0; q < kParts; ++q)
+#pragma unroll
+      for (int b = 0; b < kUnit; b += 4)
+        *reinterpret_cast<uint32_t*>(mine + (slot * kParts + q) * stride + b) = 0;
+  }
   __device__ __forceinline__ Pack<T, VEC> read(int slot) const {
     constexpr int N = VEC / kParts;
     Pack<T, VEC> out;

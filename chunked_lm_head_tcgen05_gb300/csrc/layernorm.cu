@@ -59,6 +59,17 @@ __device__ __forceinline__ float& at(float2 (&v)[N], int e) {
   return e & 1 ? v[e >> 1].y : v[e >> 1].x;
 }
 
+// Sums of two values over a warp in one tree: lanes 0..15 return the first, lanes
+// 16..31 the second.
+__device__ __forceinline__ float warp_sum_halves(float a, float b) {
+  const bool upper = threadIdx.x & 16;
+  const float other = __shfl_xor_sync(0xffffffffu, upper ? a : b, 16);
+  float v = (upper ? b : a) + other;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
 // Sum over the CTA, returned to every thread.
 __device__ __forceinline__ float block_sum(float v, float* red) {
   v = warp_sum(v);
@@ -193,46 +204,56 @@ __global__ void __launch_bounds__(kPerWarp ? 32 * kFwdWarpRows : kFwdMaxThreads)
 //   mean = ref + sum n_j (m_j - ref) / n,  M2 = sum M2_j + n_j (m_j - ref)^2 - n (mean - ref)^2
 // over threads and then warps, with one part's own mean as ref: both sums at once,
 // and what cancels is no larger than that part's share of M2 times the parts.
-template <typename X, typename Y, int VEC, int NV, int kDepth>
+template <typename X, typename Y, int VEC, int NV, int kDepth, bool kFull>
 __global__ void __launch_bounds__(kStreamThreads)
     norm_fwd_stream_kernel(const X* __restrict__ x, int64_t x_ld, const void* __restrict__ w,
                            const void* __restrict__ b, int param_type, int64_t N, int H, float eps,
                            Y* __restrict__ y, int64_t y_ld, float* mean, float* rstd, int g) {
   extern __shared__ __align__(16) char ring_bytes[];
-  __shared__ float red[2][2][kStreamThreads / 32];
+  __shared__ float red[2][3][kStreamThreads / 32];
   pdl_wait_prerequisites();
   pdl_launch_dependents();
   const int groups = blockDim.x / g;
   const int grp = threadIdx.x / g, i = threadIdx.x - grp * g;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = g >> 5, w0 = grp * warps;
   const int n = H / VEC;
+  auto in = [&](int k) { return kFull || i + k * g < n; };   // kFull: n = NV g
   const PackRing<X, VEC> ring(ring_bytes, blockDim.x, threadIdx.x);
-  float wv[NV][VEC], bv[NV][VEC];
+  float2 wv[NV * VEC / 2], bv[NV * VEC / 2];
   int cnt = 0;
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
+    float one[VEC] = {}, two[VEC] = {};
+    if (in(k)) {
+      cnt += VEC;
+      load_params<VEC>(w, param_type, (i + k * g) * VEC, one);
+      if (b) load_params<VEC>(b, param_type, (i + k * g) * VEC, two);
+    } else {   // slots that are never filled read as zeros
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) wv[k][e] = bv[k][e] = 0.f;
-    if (i + k * g >= n) continue;
-    cnt += VEC;
-    load_params<VEC>(w, param_type, (i + k * g) * VEC, wv[k]);
-    if (b) load_params<VEC>(b, param_type, (i + k * g) * VEC, bv[k]);
+      for (int d = 0; d < kDepth; ++d) ring.clear(d * NV + k);
+    }
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      at(wv, k * VEC + e) = one[e];
+      at(bv, k * VEC + e) = two[e];
+    }
   }
   const float own_cnt = static_cast<float>(cnt), own_inv = cnt ? 1.f / own_cnt : 0.f;
-  cnt = __reduce_add_sync(0xffffffffu, cnt);   // columns of this warp
-  const float inv = cnt ? 1.f / static_cast<float>(cnt) : 0.f, inv_H = 1.f / static_cast<float>(H);
-  // columns of the group's lane-th warp: the warp fills NV rounds of 32 packs, cut off at n
-  float lane_share = 0.f;
+  const float inv_H = 1.f / static_cast<float>(H);
+  // columns of the group's (lane % 16)-th warp, which fills NV rounds of 32 packs
+  float share = 0.f;
   for (int k = 0; k < NV; ++k)
-    lane_share += static_cast<float>(VEC * min(max(n - (lane * 32 + k * g), 0), 32));
+    share += static_cast<float>(VEC * min(max(n - ((lane & 15) * 32 + k * g), 0), 32));
+  const float share_inv = share > 0.f ? 1.f / share : 0.f;
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
   int64_t t = static_cast<int64_t>(blockIdx.x) * groups + grp, next = t;
   int put = 0, get = 0;
   auto fetch = [&] {
     if (next < N) {
+      const X* from = x + next * x_ld + i * VEC;
 #pragma unroll
       for (int k = 0; k < NV; ++k)
-        if (i + k * g < n) ring.fetch(put * NV + k, x + next * x_ld + (i + k * g) * VEC);
+        if (in(k)) ring.fetch(put * NV + k, from + k * g * VEC);
     }
     copy_async_commit();
     next += step;
@@ -243,69 +264,66 @@ __global__ void __launch_bounds__(kStreamThreads)
   for (int flip = 0; t < N; t += step, flip ^= 1) {
     copy_async_wait<kDepth - 1>();
     // the thread's mean and squared deviations about it
-    float2 v[NV][VEC / 2];
+    float2 v[NV * VEC / 2];
     float2 s2 = make_float2(0.f, 0.f), q2 = make_float2(0.f, 0.f);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const bool in = i + k * g < n;
       const Pack<X, VEC> q = ring.read(get * NV + k);
 #pragma unroll
       for (int e = 0; e < VEC / 2; ++e) {
-        v[k][e] = in ? pair_of(q, e) : make_float2(0.f, 0.f);
-        s2 = add2(s2, v[k][e]);
+        v[k * VEC / 2 + e] = pair_of(q, e);
+        s2 = add2(s2, v[k * VEC / 2 + e]);
       }
     }
     get = get + 1 == kDepth ? 0 : get + 1;
     const float own = (s2.x + s2.y) * own_inv;
+    const float2 minus_own = make_float2(-own, -own);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      if (i + k * g >= n) continue;
+      if (!in(k)) continue;
 #pragma unroll
       for (int e = 0; e < VEC / 2; ++e) {
-        const float2 d = add2(v[k][e], make_float2(-own, -own));
+        const float2 d = add2(v[k * VEC / 2 + e], minus_own);
         q2 = fma2(d, d, q2);
       }
     }
-    // the warp's, about lane 0's mean
-    float ref = __shfl_sync(0xffffffffu, own, 0);
-    float d = own - ref, d1 = own_cnt * d, d2 = fmaf(d1, d, q2.x + q2.y);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      d1 += __shfl_xor_sync(0xffffffffu, d1, o);
-      d2 += __shfl_xor_sync(0xffffffffu, d2, o);
-    }
-    fetch();   // into the slots just read, all of whose values are in d1 and d2
-    if (warps > 1) {   // the group's, about its first warp's mean
-      if (lane == 0) {
-        red[flip][0][warp] = fmaf(d1, inv, ref);
-        red[flip][1][warp] = fmaf(-d1 * inv, d1, d2);
-      }
+    // the warp's, about lane 0's mean: its two sums go to shared memory
+    const float first = __shfl_sync(0xffffffffu, own, 0);
+    const float d0 = own - first, d1 = own_cnt * d0;
+    const float half = warp_sum_halves(d1, fmaf(d1, d0, q2.x + q2.y));
+    fetch();   // into the slots just read, all of whose values are in the sums
+    if ((lane & 15) == 0) red[flip][lane >> 4][warp] = half;
+    if (lane == 1) red[flip][2][warp] = first;
+    if (warps > 1)
       named_bar_sync(1 + grp, g);
-      const bool have = lane < warps;
-      ref = red[flip][0][w0];
-      d = have ? red[flip][0][w0 + lane] - ref : 0.f;
-      d1 = lane_share * d;
-      d2 = have ? fmaf(d1, d, red[flip][1][w0 + lane]) : 0.f;
+    else
+      __syncwarp();
+    // the group's, about its first warp's mean
+    const int wl = w0 + min(lane & 15, warps - 1);
+    const bool have = (lane & 15) < warps;
+    const float s1w = red[flip][0][wl], q1w = red[flip][1][wl], fw = red[flip][2][wl];
+    const float mw = fmaf(s1w, share_inv, fw);
+    const float ref = __shfl_sync(0xffffffffu, mw, 0);
+    const float dw = mw - ref, nd = share * dw;
+    const float part = lane < 16 ? nd : fmaf(nd, dw, fmaf(-s1w * share_inv, s1w, q1w));
+    float sum = have ? part : 0.f;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        d1 += __shfl_xor_sync(0xffffffffu, d1, o);
-        d2 += __shfl_xor_sync(0xffffffffu, d2, o);
-      }
-    }
-    const float mu = fmaf(d1, inv_H, ref);
-    const float r = rsqrtf(fmaf(fmaf(-d1 * inv_H, d1, d2), inv_H, eps));
-    Y* out = y + t * y_ld;
+    for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const float e1 = __shfl_sync(0xffffffffu, sum, 0), e2 = __shfl_sync(0xffffffffu, sum, 16);
+    const float mu = fmaf(e1, inv_H, ref);
+    const float r = rsqrtf(fmaf(fmaf(-e1 * inv_H, e1, e2), inv_H, eps));
+    const float2 minus_mu = make_float2(-mu, -mu), r2 = make_float2(r, r);
+    Y* out = y + t * y_ld + i * VEC;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      if (i + k * g >= n) continue;
+      if (!in(k)) continue;
       Pack<Y, VEC> o;
 #pragma unroll
       for (int e = 0; e < VEC / 2; ++e) {
-        const float2 xh = mul2(add2(v[k][e], make_float2(-mu, -mu)), make_float2(r, r));
-        set_pair(o, e, fma2(xh, make_float2(wv[k][2 * e], wv[k][2 * e + 1]),
-                            make_float2(bv[k][2 * e], bv[k][2 * e + 1])));
+        const int j = k * VEC / 2 + e;
+        set_pair(o, e, fma2(mul2(add2(v[j], minus_mu), r2), wv[j], bv[j]));
       }
-      *reinterpret_cast<Pack<Y, VEC>*>(out + (i + k * g) * VEC) = o;
+      *reinterpret_cast<Pack<Y, VEC>*>(out + k * g * VEC) = o;
     }
     if (i == 0) {
       if (mean) mean[t] = mu;
@@ -321,7 +339,7 @@ __global__ void __launch_bounds__(kStreamThreads)
 // at the end, and the CTA writes one partial row.  Rows arrive through a ring of
 // asynchronous copies kDepth rows deep (kDepth = 0: units too small for such
 // copies; a row's loads are then issued before the previous row's sums).
-template <typename X, typename D, int VEC, int NV, int kDepth>
+template <typename X, typename D, int VEC, int NV, int kDepth, bool kFull>
 __global__ void __launch_bounds__(kBwdThreads)
     norm_bwd_kernel(const D* __restrict__ dy, int64_t dy_ld, const X* x, int64_t x_ld,
                     const void* __restrict__ w, int param_type, const float* __restrict__ mean,
@@ -338,6 +356,7 @@ __global__ void __launch_bounds__(kBwdThreads)
   const int grp = threadIdx.x / g, i = threadIdx.x - grp * g;
   const int lane = threadIdx.x & 31, warps = g >> 5;
   const int n = H / VEC;
+  auto in = [&](int k) { return kFull || i + k * g < n; };   // kFull: n = NV g
   const float inv = 1.f / static_cast<float>(H);
   const PackRing<X, VEC> x_ring(ring_bytes, blockDim.x, threadIdx.x);
   const PackRing<D, VEC> g_ring(ring_bytes + kDepth * NV * sizeof(X) * VEC * blockDim.x, blockDim.x,
@@ -349,7 +368,7 @@ __global__ void __launch_bounds__(kBwdThreads)
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       float one[VEC] = {};
-      if (i + k * g < n) load_params<VEC>(w, param_type, (i + k * g) * VEC, one);
+      if (in(k)) load_params<VEC>(w, param_type, (i + k * g) * VEC, one);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) at(wv, k * VEC + e) = one[e];
     }
@@ -374,7 +393,7 @@ __global__ void __launch_bounds__(kBwdThreads)
     if (next < N) {
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
-        if (i + k * g >= n) continue;
+        if (!in(k)) continue;
         const X* xs = x + next * x_ld + (i + k * g) * VEC;
         const D* gs = dy + next * dy_ld + (i + k * g) * VEC;
         if constexpr (kRing) {
@@ -412,11 +431,10 @@ __global__ void __launch_bounds__(kBwdThreads)
         xq = xn[k];
         gq = gn[k];
       }
-      const bool in = i + k * g < n;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        at(xv, k * VEC + e) = in ? to_f32(xq.v[e]) : 0.f;
-        at(gv, k * VEC + e) = in ? to_f32(gq.v[e]) : 0.f;
+        at(xv, k * VEC + e) = in(k) ? to_f32(xq.v[e]) : 0.f;
+        at(gv, k * VEC + e) = in(k) ? to_f32(gq.v[e]) : 0.f;
       }
     }
     if constexpr (kRing) get = get + 1 == kDepth ? 0 : get + 1;
@@ -435,19 +453,18 @@ __global__ void __launch_bounds__(kBwdThreads)
       aw[j] = fma2(gv[j], xh, aw[j]);
       ab[j] = add2(ab[j], gv[j]);
     }
-    float t1 = warp_sum(s1.x + s1.y), t2 = warp_sum(s2.x + s2.y);
+    float half = warp_sum_halves(s1.x + s1.y, s2.x + s2.y);
     if constexpr (kRing) fetch();   // into the slots just read, all of whose values are in the sums
     if (dx) {
       if (warps > 1) {
-        const int w0 = grp * warps;
-        if (lane == 0) {
-          red[flip][0][threadIdx.x >> 5] = t1;
-          red[flip][1][threadIdx.x >> 5] = t2;
-        }
+        const int w0 = grp * warps, wl = lane & 15;
+        if (wl == 0) red[flip][lane >> 4][threadIdx.x >> 5] = half;
         named_bar_sync(1 + grp, g);
-        t1 = warp_sum(lane < warps ? red[flip][0][w0 + lane] : 0.f);
-        t2 = warp_sum(lane < warps ? red[flip][1][w0 + lane] : 0.f);
+        half = wl < warps ? red[flip][lane >> 4][w0 + wl] : 0.f;
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) half += __shfl_xor_sync(0xffffffffu, half, o);
       }
+      const float t1 = __shfl_sync(0xffffffffu, half, 0), t2 = __shfl_sync(0xffffffffu, half, 16);
       const float2 minus_c1 = make_float2(-t1 * inv, -t1 * inv), minus_c2 = make_float2(-t2 * inv, -t2 * inv);
 #pragma unroll
       for (int j = 0; j < kPairs; ++j) {
@@ -456,7 +473,7 @@ __global__ void __launch_bounds__(kBwdThreads)
       }
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
-        if (i + k * g >= n) continue;
+        if (!in(k)) continue;
         Pack<X, VEC> o;
 #pragma unroll
         for (int e = 0; e < VEC; ++e) o.v[e] = from_f32<X>(at(gv, k * VEC + e));
@@ -473,7 +490,7 @@ __global__ void __launch_bounds__(kBwdThreads)
     if (grp != q) continue;
 #pragma unroll
     for (int k = 0; k < NV; ++k)
-      if (i + k * g < n) {
+      if (in(k)) {
         const int c = (i + k * g) * VEC;
         constexpr int N = VEC < 4 ? VEC : 4;
         using Some = Pack<float, N>;
@@ -607,13 +624,17 @@ cudaError_t fwd_rows(const NormFwd& a, cudaStream_t s) {
 
 template <typename X, typename Y, int VEC, int NV, int kDepth>
 cudaError_t fwd_stream(const NormFwd& a, cudaStream_t s) {
-  static std::atomic<int> ready[64];
-  auto* kern = norm_fwd_stream_kernel<X, Y, VEC, NV, kDepth>;
+  static std::atomic<int> ready_full[64], ready_part[64];
+  const int n = a.H / VEC;
+  const bool full = n % (32 * NV) == 0;
+  auto* kern = full ? norm_fwd_stream_kernel<X, Y, VEC, NV, kDepth, true>
+                    : norm_fwd_stream_kernel<X, Y, VEC, NV, kDepth, false>;
   constexpr size_t kPerThread = static_cast<size_t>(kDepth) * NV * sizeof(X) * VEC;
-  const cudaError_t e = allow_shared(ready, reinterpret_cast<const void*>(kern),
+  const cudaError_t e = allow_shared(full ? ready_full : ready_part,
+                                     reinterpret_cast<const void*>(kern),
                                      kPerThread * kStreamThreads);
   if (e != cudaSuccess) return e;
-  const int g = round32((a.H / VEC + NV - 1) / NV), groups = kStreamThreads / g;
+  const int g = round32((n + NV - 1) / NV), groups = kStreamThreads / g;
   const int64_t ctas = (a.N + groups - 1) / groups, sms = sm_count();
   return launch_dependent(kern, dim3(static_cast<unsigned>(ctas < sms ? ctas : sms)), g * groups,
                           kPerThread * g * groups, 1, s, static_cast<const X*>(a.x), a.x_ld,
@@ -668,11 +689,13 @@ cudaError_t bwd_rows(const NormBwd& a, cudaStream_t s) {
   const int64_t ctas = (a.N + groups - 1) / groups;
   const int P = static_cast<int>(ctas < sms ? ctas : sms);
   const bool params = a.d_weight || a.d_bias;
-  static std::atomic<int> ready[64];
-  auto* kern = norm_bwd_kernel<X, D, VEC, NV, kDepth>;
+  static std::atomic<int> ready_full[64], ready_part[64];
+  const bool full = n % (32 * NV) == 0;
+  auto* kern = full ? norm_bwd_kernel<X, D, VEC, NV, kDepth, true>
+                    : norm_bwd_kernel<X, D, VEC, NV, kDepth, false>;
   constexpr size_t kMostRing = kDepth * kRow * kBwdThreads;
   constexpr size_t kMostJoin = 2 * sizeof(float) * kBwdThreads / 2 * VEC * NV;   // two groups or more
-  cudaError_t e = allow_shared(ready, reinterpret_cast<const void*>(kern),
+  cudaError_t e = allow_shared(full ? ready_full : ready_part, reinterpret_cast<const void*>(kern),
                                kMostRing > kMostJoin ? kMostRing : kMostJoin);
   if (e != cudaSuccess) return e;
   const size_t ring = kDepth * kRow * g * groups;
