@@ -19,7 +19,6 @@ constexpr int kFwdWarpRows = 4;        // forward, one warp per row: rows per CT
 constexpr int kStreamThreads = 512;    // forward with many rows: most threads per CTA
 constexpr int kBwdThreads = 512;       // backward: most threads per CTA
 constexpr int kRowThreads = 256;
-constexpr int kColThreads = 256;   // 32 columns x 8 row lanes
 constexpr int kFinishRows = 16;
 
 __device__ __forceinline__ float load_param(const void* p, int type, int64_t i) {
@@ -336,26 +335,36 @@ __global__ void __launch_bounds__(kStreamThreads)
 // Both gradients in one pass over x and dy.  A group of g threads (a multiple of
 // 32) owns a row at a time and its threads fixed columns, so dw and db gather in
 // registers over the group's rows; the CTA's groups are joined in shared memory
-// at the end, and the CTA writes one partial row.  Rows arrive through a ring of
+// at the end, and the CTA writes one partial row.  Rows of more than `cols` columns
+// go in blocks of that many (blockIdx.y), their two sums having been formed before
+// (`sums`); narrower ones in one block that forms them itself.  Rows arrive through a ring of
 // asynchronous copies kDepth rows deep (kDepth = 0: units too small for such
 // copies; a row's loads are then issued before the previous row's sums).
 template <typename X, typename D, int VEC, int NV, int kDepth, bool kFull>
 __global__ void __launch_bounds__(kBwdThreads)
     norm_bwd_kernel(const D* __restrict__ dy, int64_t dy_ld, const X* x, int64_t x_ld,
                     const void* __restrict__ w, int param_type, const float* __restrict__ mean,
-                    const float* __restrict__ rstd, int64_t N, int H, X* dx, int64_t dx_ld,
+                    const float* __restrict__ rstd, int64_t N, int H, int cols,
+                    const float2* __restrict__ sums, X* dx, int64_t dx_ld,
                     float* __restrict__ part_w, float* __restrict__ part_b, int g) {
-  extern __shared__ __align__(16) char ring_bytes[];   // x and dy in flight; then [2][H] sums
+  extern __shared__ __align__(16) char ring_bytes[];   // x and dy in flight; then [2][W] sums
   __shared__ float red[2][2][kBwdThreads / 32];
   constexpr bool kRing = kDepth > 0;
   constexpr int kRegs = kRing ? 1 : NV;
-  constexpr bool kKeep = VEC * NV <= 16 && NV <= 8;   // room to keep w in registers
   pdl_wait_prerequisites();
   pdl_launch_dependents();
+  const int c_first = blockIdx.y * cols, W = min(cols, H - c_first);
+  x += c_first;
+  dy += c_first;
+  if (dx) dx += c_first;
+  if (part_w) {
+    part_w += c_first;
+    part_b += c_first;
+  }
   const int groups = blockDim.x / g;
   const int grp = threadIdx.x / g, i = threadIdx.x - grp * g;
   const int lane = threadIdx.x & 31, warps = g >> 5;
-  const int n = H / VEC;
+  const int n = W / VEC;
   auto in = [&](int k) { return kFull || i + k * g < n; };   // kFull: n = NV g
   const float inv = 1.f / static_cast<float>(H);
   const PackRing<X, VEC> x_ring(ring_bytes, blockDim.x, threadIdx.x);
@@ -363,26 +372,14 @@ __global__ void __launch_bounds__(kBwdThreads)
                                 threadIdx.x);
   // pairs of columns: within a pack, or of neighbouring packs of one element
   constexpr int kPairs = NV * VEC / 2;
-  float2 aw[kPairs] = {}, ab[kPairs] = {}, wv[kKeep ? kPairs : 1] = {};
-  if constexpr (kKeep) {
+  float2 aw[kPairs] = {}, ab[kPairs] = {}, wv[kPairs];
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      float one[VEC] = {};
-      if (in(k)) load_params<VEC>(w, param_type, (i + k * g) * VEC, one);
+  for (int k = 0; k < NV; ++k) {
+    float one[VEC] = {};
+    if (in(k)) load_params<VEC>(w, param_type, c_first + (i + k * g) * VEC, one);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) at(wv, k * VEC + e) = one[e];
-    }
+    for (int e = 0; e < VEC; ++e) at(wv, k * VEC + e) = one[e];
   }
-  auto weight_of = [&](int j) {
-    if constexpr (kKeep) {
-      return wv[j];
-    } else {   // no room: from L1 each time
-      const int e0 = 2 * j, e1 = 2 * j + 1;
-      const int c0 = (i + e0 / VEC * g) * VEC + e0 % VEC, c1 = (i + e1 / VEC * g) * VEC + e1 % VEC;
-      return make_float2(c0 < H ? load_param(w, param_type, c0) : 0.f,
-                         c1 < H ? load_param(w, param_type, c1) : 0.f);
-    }
-  };
   Pack<X, VEC> xn[kRegs];
   Pack<D, VEC> gn[kRegs];
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
@@ -447,16 +444,20 @@ __global__ void __launch_bounds__(kBwdThreads)
     float2 s1 = make_float2(0.f, 0.f), s2 = s1;
 #pragma unroll
     for (int j = 0; j < kPairs; ++j) {
-      const float2 xh = mul2(add2(xv[j], minus_mu), r2), h = mul2(gv[j], weight_of(j));
+      const float2 xh = mul2(add2(xv[j], minus_mu), r2), h = mul2(gv[j], wv[j]);
       s1 = fma2(h, xh, s1);
       s2 = add2(s2, h);
       aw[j] = fma2(gv[j], xh, aw[j]);
       ab[j] = add2(ab[j], gv[j]);
     }
-    float half = warp_sum_halves(s1.x + s1.y, s2.x + s2.y);
-    if constexpr (kRing) fetch();   // into the slots just read, all of whose values are in the sums
+    // into the slots just read, whose values are in the sums; fp32 dy, the longer rows,
+    // gain from asking first (16384 x 4096: 115 us against 124), 16-bit ones lose
+    // (65536 x 2560: 180 against 170)
+    if constexpr (kRing && sizeof(D) == 4) fetch();
+    float half = sums ? 0.f : warp_sum_halves(s1.x + s1.y, s2.x + s2.y);
+    if constexpr (kRing && sizeof(D) != 4) fetch();
     if (dx) {
-      if (warps > 1) {
+      if (!sums && warps > 1) {
         const int w0 = grp * warps, wl = lane & 15;
         if (wl == 0) red[flip][lane >> 4][threadIdx.x >> 5] = half;
         named_bar_sync(1 + grp, g);
@@ -464,11 +465,15 @@ __global__ void __launch_bounds__(kBwdThreads)
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) half += __shfl_xor_sync(0xffffffffu, half, o);
       }
-      const float t1 = __shfl_sync(0xffffffffu, half, 0), t2 = __shfl_sync(0xffffffffu, half, 16);
-      const float2 minus_c1 = make_float2(-t1 * inv, -t1 * inv), minus_c2 = make_float2(-t2 * inv, -t2 * inv);
+      float2 c;
+      if (sums)
+        c = sums[t];
+      else
+        c = make_float2(__shfl_sync(0xffffffffu, half, 0) * inv, __shfl_sync(0xffffffffu, half, 16) * inv);
+      const float2 minus_c1 = make_float2(-c.x, -c.x), minus_c2 = make_float2(-c.y, -c.y);
 #pragma unroll
       for (int j = 0; j < kPairs; ++j) {
-        const float2 xh = mul2(add2(xv[j], minus_mu), r2), h = mul2(gv[j], weight_of(j));
+        const float2 xh = mul2(add2(xv[j], minus_mu), r2), h = mul2(gv[j], wv[j]);
         gv[j] = mul2(fma2(xh, minus_c1, add2(h, minus_c2)), r2);
       }
 #pragma unroll
@@ -495,13 +500,13 @@ __global__ void __launch_bounds__(kBwdThreads)
         constexpr int N = VEC < 4 ? VEC : 4;
         using Some = Pack<float, N>;
         float* const to_w = q + 1 < groups ? joined : part_w + static_cast<int64_t>(blockIdx.x) * H;
-        float* const to_b = q + 1 < groups ? joined + H : part_b + static_cast<int64_t>(blockIdx.x) * H;
+        float* const to_b = q + 1 < groups ? joined + W : part_b + static_cast<int64_t>(blockIdx.x) * H;
 #pragma unroll
         for (int e = 0; e < VEC; e += N) {
           Some a, b;
           if (q > 0) {
             a = *reinterpret_cast<const Some*>(joined + c + e);
-            b = *reinterpret_cast<const Some*>(joined + H + c + e);
+            b = *reinterpret_cast<const Some*>(joined + W + c + e);
           }
 #pragma unroll
           for (int j = 0; j < N; ++j) {
@@ -546,38 +551,38 @@ __global__ void __launch_bounds__(kRowThreads)
   }
 }
 
-// Partial column sums: CTA (c, p) adds rows p, p + P, ... of columns
-// [32 c, 32 c + 32) and writes row p of part_w / part_b [P][H].
-template <typename X, typename D>
-__global__ void __launch_bounds__(kColThreads)
-    norm_columns_any_kernel(const D* __restrict__ dy, int64_t dy_ld, const X* __restrict__ x,
-                            int64_t x_ld, const float* __restrict__ mean,
-                            const float* __restrict__ rstd, int64_t N, int H,
-                            float* __restrict__ part_w, float* __restrict__ part_b) {
+// The two sums of a row's gradient, for rows wider than a CTA keeps:
+// sums[t] = (mean(h xh), mean(h)).
+template <typename X, typename D, int VEC>
+__global__ void __launch_bounds__(kRowThreads)
+    norm_sums_kernel(const D* __restrict__ dy, int64_t dy_ld, const X* __restrict__ x, int64_t x_ld,
+                     const void* __restrict__ w, int param_type, const float* __restrict__ mean,
+                     const float* __restrict__ rstd, int64_t N, int H, float2* __restrict__ sums) {
   pdl_wait_prerequisites();
   pdl_launch_dependents();
-  __shared__ float sw[8][33], sb[8][33];
-  const int lane = threadIdx.x & 31, sub = threadIdx.x >> 5;
-  const int P = gridDim.y, p = blockIdx.y;
-  const int c = blockIdx.x * 32 + lane;
-  float aw = 0.f, ab = 0.f;
-  if (c < H) {
-    for (int64_t t = p + static_cast<int64_t>(sub) * P; t < N; t += 8ll * P) {
-      const float g = to_f32(dy[t * dy_ld + c]);
-      aw = fmaf(g, (to_f32(x[t * x_ld + c]) - mean[t]) * rstd[t], aw);
-      ab += g;
+  __shared__ float red[kRowThreads / 32];
+  for (int64_t t = blockIdx.x; t < N; t += gridDim.x) {
+    const X* xr = x + t * x_ld;
+    const D* gr = dy + t * dy_ld;
+    const float mu = mean[t], r = rstd[t];
+    float s1 = 0.f, s2 = 0.f;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < H / VEC; i += kRowThreads) {
+      const Pack<X, VEC> xq = *reinterpret_cast<const Pack<X, VEC>*>(xr + i * VEC);
+      const Pack<D, VEC> gq = *reinterpret_cast<const Pack<D, VEC>*>(gr + i * VEC);
+      float wl[VEC];
+      load_params<VEC>(w, param_type, i * VEC, wl);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float h = to_f32(gq.v[e]) * wl[e];
+        s1 = fmaf(h, (to_f32(xq.v[e]) - mu) * r, s1);
+        s2 += h;
+      }
     }
-  }
-  sw[sub][lane] = aw;
-  sb[sub][lane] = ab;
-  __syncthreads();
-  if (sub == 0 && c < H) {
-    for (int k = 1; k < 8; ++k) {
-      aw += sw[k][lane];
-      ab += sb[k][lane];
-    }
-    part_w[static_cast<int64_t>(p) * H + c] = aw;
-    part_b[static_cast<int64_t>(p) * H + c] = ab;
+    s1 = block_sum(s1, red);
+    s2 = block_sum(s2, red);
+    if (threadIdx.x == 0)
+      sums[t] = make_float2(s1 / static_cast<float>(H), s2 / static_cast<float>(H));
   }
 }
 
@@ -679,18 +684,29 @@ template <typename X, typename D, int VEC, int NV>
 cudaError_t bwd_rows(const NormBwd& a, cudaStream_t s) {
   constexpr bool kRing = PackRing<X, VEC>::kAsync && PackRing<D, VEC>::kAsync;
   constexpr size_t kRow = NV * VEC * (sizeof(X) + sizeof(D));   // a thread's bytes of one row
-  constexpr int kDepth = !kRing ? 0 : kRow <= 96 ? 4 : kRow <= 128 ? 3 : kRow <= 192 ? 2 : 1;
-  const int n = a.H / VEC;
-  const int g = round32((n + NV - 1) / NV);
+  constexpr int kDepth = !kRing ? 0 : kRow <= 96 ? 4 : 3;
+  constexpr int kCols = kBwdThreads * VEC * NV;
   const int sms = sm_count();
+  const int blocks = (a.H + kCols - 1) / kCols;
+  const int n = ((a.H + blocks - 1) / blocks + VEC - 1) / VEC;   // packs of a block
+  const bool params = a.d_weight || a.d_bias;
+  if (blocks > 1 && a.dx) {
+    const int64_t cap = static_cast<int64_t>(sms) * 8;
+    const cudaError_t e = launch_dependent(
+        norm_sums_kernel<X, D, VEC>, dim3(static_cast<unsigned>(a.N < cap ? a.N : cap)), kRowThreads,
+        0, 1, s, static_cast<const D*>(a.dy), a.dy_ld, static_cast<const X*>(a.x), a.x_ld, a.weight,
+        a.param_type, a.mean, a.rstd, a.N, a.H, a.sums);
+    if (e != cudaSuccess) return e;
+  }
+  const bool full = blocks == 1 && n % (32 * NV) == 0;
+  const int g = round32((n + NV - 1) / NV);
+  const int64_t most = sms / blocks > 1 ? sms / blocks : 1;   // CTAs per block of columns
   int groups = kBwdThreads / g;
-  const int64_t per_cta = (a.N + sms - 1) / sms;
+  const int64_t per_cta = (a.N + most - 1) / most;
   if (groups > per_cta) groups = static_cast<int>(per_cta);
   const int64_t ctas = (a.N + groups - 1) / groups;
-  const int P = static_cast<int>(ctas < sms ? ctas : sms);
-  const bool params = a.d_weight || a.d_bias;
+  const int P = static_cast<int>(ctas < most ? ctas : most);
   static std::atomic<int> ready_full[64], ready_part[64];
-  const bool full = n % (32 * NV) == 0;
   auto* kern = full ? norm_bwd_kernel<X, D, VEC, NV, kDepth, true>
                     : norm_bwd_kernel<X, D, VEC, NV, kDepth, false>;
   constexpr size_t kMostRing = kDepth * kRow * kBwdThreads;
@@ -699,13 +715,14 @@ cudaError_t bwd_rows(const NormBwd& a, cudaStream_t s) {
                                kMostRing > kMostJoin ? kMostRing : kMostJoin);
   if (e != cudaSuccess) return e;
   const size_t ring = kDepth * kRow * g * groups;
-  const size_t join = groups > 1 && params ? 2 * sizeof(float) * static_cast<size_t>(a.H) : 0;
+  const size_t join = groups > 1 && params ? 2 * sizeof(float) * static_cast<size_t>(n) * VEC : 0;
   float* part_w = params ? a.partials : nullptr;
   float* part_b = params ? a.partials + static_cast<int64_t>(P) * a.H : nullptr;
-  e = launch_dependent(kern, dim3(P), g * groups, ring > join ? ring : join, 1, s,
+  e = launch_dependent(kern, dim3(P, blocks), g * groups, ring > join ? ring : join, 1, s,
                        static_cast<const D*>(a.dy), a.dy_ld, static_cast<const X*>(a.x), a.x_ld,
-                       a.weight, a.param_type, a.mean, a.rstd, a.N, a.H, static_cast<X*>(a.dx),
-                       a.dx_ld, part_w, part_b, g);
+                       a.weight, a.param_type, a.mean, a.rstd, a.N, a.H, n * VEC,
+                       static_cast<const float2*>(blocks > 1 ? a.sums : nullptr),
+                       static_cast<X*>(a.dx), a.dx_ld, part_w, part_b, g);
   if (e != cudaSuccess || !params) return e;
   return finish(a, P, s);
 }
@@ -713,41 +730,18 @@ cudaError_t bwd_rows(const NormBwd& a, cudaStream_t s) {
 template <typename X, typename D>
 cudaError_t bwd_typed(const NormBwd& a, cudaStream_t s) {
   constexpr int VEC = kVec<X>;
+  if (!a.sums && a.H > kNormWide) {   // dx alone, without a workspace for a wide row's sums
+    const int64_t cap = static_cast<int64_t>(sm_count()) * 8;
+    return launch_dependent(norm_dx_any_kernel<X, D>, dim3(static_cast<unsigned>(a.N < cap ? a.N : cap)),
+                            kRowThreads, 0, 1, s, static_cast<const D*>(a.dy), a.dy_ld,
+                            static_cast<const X*>(a.x), a.x_ld, a.weight, a.param_type, a.mean,
+                            a.rstd, a.N, a.H, static_cast<X*>(a.dx), a.dx_ld);
+  }
   const bool packs = a.H % VEC == 0 && a.x_ld % VEC == 0 && a.dy_ld % VEC == 0 &&
                      a.dx_ld % VEC == 0 && aligned(a.x, 16) && aligned(a.dx, 16) &&
                      aligned(a.dy, sizeof(D) * VEC > 16 ? 16 : sizeof(D) * VEC) &&
                      aligned(a.weight, 16);
-  if (packs) {
-    if (a.H <= kBwdThreads * 16) return bwd_rows<X, D, VEC, 16 / VEC>(a, s);
-    if (a.H <= kBwdThreads * 32) return bwd_rows<X, D, VEC, 32 / VEC>(a, s);
-  }
-  if (a.H <= kBwdThreads * 8) return bwd_rows<X, D, 1, 8>(a, s);
-  if (a.H <= kBwdThreads * 16) return bwd_rows<X, D, 1, 16>(a, s);
-  const X* x = static_cast<const X*>(a.x);
-  const D* dy = static_cast<const D*>(a.dy);
-  cudaError_t e = cudaSuccess;
-  // the column sums first: dx may overwrite x or dy
-  if (a.d_weight || a.d_bias) {
-  const int P = static_cast<int>(a.N < 32 ? 1 : (a.N / 32 < kNormPartials ? a.N / 32 : kNormPartials));
-  float* part_w = a.partials;
-  float* part_b = a.partials + static_cast<int64_t>(P) * a.H;
-  const int cols = (a.H + 31) / 32;
-  e = launch_dependent(norm_columns_any_kernel<X, D>, dim3(cols, P), kColThreads, 0, 1,
-                                   s, dy, a.dy_ld, x, a.x_ld, a.mean, a.rstd, a.N, a.H, part_w,
-                                   part_b);
-  if (e != cudaSuccess) return e;
-  e = finish(a, P, s);
-  if (e != cudaSuccess) return e;
-  }
-  if (a.dx) {
-    const int64_t cap = static_cast<int64_t>(sm_count()) * 8;
-    const int grid = static_cast<int>(a.N < cap ? a.N : cap);
-    e = launch_dependent(norm_dx_any_kernel<X, D>, dim3(grid), kRowThreads, 0, 1,
-                                           s, dy, a.dy_ld, x, a.x_ld, a.weight, a.param_type,
-                                           a.mean, a.rstd, a.N, a.H, static_cast<X*>(a.dx),
-                                           a.dx_ld);
-  }
-  return e;
+  return packs ? bwd_rows<X, D, VEC, 16 / VEC>(a, s) : bwd_rows<X, D, 1, 8>(a, s);
 }
 
 }  // namespace

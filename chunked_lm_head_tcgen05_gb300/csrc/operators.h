@@ -16,6 +16,8 @@ constexpr int kF16 = 2;
 // ------------------------------------------------------------------ layer norm
 // Most partial rows of the weight gradient's column sums (workspace bound).
 constexpr int kNormPartials = 304;
+// Rows wider than this may need their two sums (mean(h xh), mean(h)) beforehand.
+constexpr int kNormWide = 4096;
 
 struct NormFwd {
   const void* x;
@@ -53,6 +55,7 @@ struct NormBwd {
   float* d_bias;         // or NULL
   int accumulate;
   float* partials;       // workspace: 2 * kNormPartials * H floats at most
+  float2* sums;          // workspace [N], or NULL without one or at H <= kNormWide
 };
 
 cudaError_t launch_norm_fwd(const NormFwd& a, cudaStream_t s);

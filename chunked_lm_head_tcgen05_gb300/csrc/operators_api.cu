@@ -29,7 +29,14 @@ bool positive(float v) { return std::isfinite(v) && v > 0.f; }
 
 lmhead_status status_of(cudaError_t e) { return e == cudaSuccess ? LMHEAD_OK : LMHEAD_ERR_CUDA; }
 
-size_t norm_workspace(int64_t H) { return 2 * sizeof(float) * kNormPartials * static_cast<size_t>(H); }
+// Partial column sums, then (wide rows) the rows' own sums.
+size_t norm_partials(int64_t H) {
+  return (2 * sizeof(float) * kNormPartials * static_cast<size_t>(H) + 255) / 256 * 256;
+}
+
+size_t norm_workspace(int64_t N, int64_t H) {
+  return norm_partials(H) + (H > kNormWide ? sizeof(float2) * static_cast<size_t>(N) : 0);
+}
 
 lmhead_status check_norm(int64_t N, int32_t H, int x_type, int other_type, int param_type,
                          int64_t x_ld, int64_t other_ld) {
@@ -77,7 +84,7 @@ lmhead_status check_process(const ProcessLogits& a) {
 extern "C" {
 
 size_t lmhead_layernorm_workspace_size(int64_t N, int32_t H) {
-  return N < 0 || N >= kMaxRows || H <= 0 ? 0 : norm_workspace(H);
+  return N < 0 || N >= kMaxRows || H <= 0 ? 0 : norm_workspace(N, H);
 }
 
 lmhead_status lmhead_layernorm_fwd(const void* x, int x_type, int64_t x_ld, const void* weight,
@@ -122,10 +129,15 @@ lmhead_status lmhead_layernorm_bwd(const void* dy, int dy_type, int64_t dy_ld, c
   if (!aligned_to(dy, dy_type) || !aligned_to(x, x_type) || !aligned_to(dx, x_type) ||
       !aligned_to(weight, param_type) || (reinterpret_cast<uintptr_t>(workspace) & 255))
     return LMHEAD_ERR_UNSUPPORTED;
-  if ((d_weight || d_bias) && workspace_bytes < norm_workspace(H))
+  if ((d_weight || d_bias) && workspace_bytes < norm_workspace(N, H))
     return LMHEAD_ERR_WORKSPACE_TOO_SMALL;
+  // a workspace given for dx alone is used if it is large enough
+  const bool room = workspace && workspace_bytes >= norm_workspace(N, H);
+  float2* sums = room && H > kNormWide
+                     ? reinterpret_cast<float2*>(static_cast<char*>(workspace) + norm_partials(H))
+                     : nullptr;
   const NormBwd a{dy, dy_type, dy_ld, x, x_type, x_ld, weight, param_type, mean, rstd, N, H,
-                  dx, dx_ld, d_weight, d_bias, accumulate ? 1 : 0, static_cast<float*>(workspace)};
+                  dx, dx_ld, d_weight, d_bias, accumulate ? 1 : 0, static_cast<float*>(workspace), sums};
   return status_of(traced_launch("layernorm_bwd", s, [&] { return launch_norm_bwd(a, s); }));
 }
 

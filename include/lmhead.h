@@ -447,7 +447,8 @@ lmhead_status lmhead_distill_logits_bwd(const void* logits, int type, int64_t ld
  *  d_weight, d_bias  [H] fp32, each may be NULL; overwritten, or added to when
  *                  accumulate != 0
  *  workspace       lmhead_layernorm_workspace_size(N, H) bytes, 256-byte aligned;
- *                  needed with d_weight or d_bias
+ *                  needed with d_weight or d_bias (for dx alone it may be NULL; rows
+ *                  wider than 4096 then take a slower path)
  * Statistics and sums are fp32, the variance is taken about the mean, and column
  * sums are added in a fixed order: same inputs, same bits.  N == 0 is a no-op
  * (the backward still zeroes d_weight / d_bias unless accumulate is set).

@@ -130,7 +130,7 @@ def test_strides_and_alignment(pad, shift, x_type, g_type, h):
     check_bwd(dy, x, w, mean, rstd, dx, dw, db)
 
 
-@pytest.mark.parametrize("h", [512, 999])
+@pytest.mark.parametrize("h", [512, 999, 9001, 12288])
 def test_accumulate_in_place_and_partial_outputs(h):
     ensure_built()
     n = 200
