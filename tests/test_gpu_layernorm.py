@@ -147,7 +147,9 @@ def test_accumulate_in_place_and_partial_outputs(h):
     check_bwd(dy, x, w, mean, rstd, x2, dw, None)
     only = torch.empty_like(dx)
     assert lm.lmhead_layernorm_bwd(dy, x, w, mean, rstd, only, None, None, False, None) == 0
-    assert torch.equal(only, dx)
+    check_bwd(dy, x, w, mean, rstd, only, None, None)
+    if h <= 4096:          # wider rows without a workspace form their sums in another order
+        assert torch.equal(only, dx)
     assert lm.lmhead_layernorm_bwd(dy, x, w, mean, rstd, None, None, db, False, ws) == 0
     check_bwd(dy, x, w, mean, rstd, None, None, db)
 
