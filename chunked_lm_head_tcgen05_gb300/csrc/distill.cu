@@ -20,7 +20,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kUnroll = 4;         // backward: 16-byte accesses in flight per thread
+constexpr int kUnroll = 2;         // backward: 16-byte accesses in flight per thread
 constexpr int kBwdMost = 65536;    // backward: bytes of logits per CTA, most and
 constexpr int kBwdLeast = 16384;   // least (shorter rows aside)
 constexpr int kFwdThreads = 256;   // forward on held logits
@@ -278,7 +278,7 @@ struct Dense {
 // the entries of this range and read their logits (d_logits may be the logits
 // buffer); the dense pass follows, and the few exact cotangents are written last.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 5) logits_bwd_kernel(DistillLogits a, int range) {
+__global__ void __launch_bounds__(kThreads, 8) logits_bwd_kernel(DistillLogits a, int range) {
   extern __shared__ float teacher[];   // p, log p, id, entries of the range, their cotangents [K]
   __shared__ float total;
   __shared__ int entries;
