@@ -16,8 +16,10 @@ namespace {
 
 constexpr int kFwdMaxThreads = 1024;   // forward, one CTA per row
 constexpr int kFwdWarpRows = 4;        // forward, one warp per row: rows per CTA
-constexpr int kStreamThreads = 512;    // forward with many rows: most threads per CTA
+constexpr int kStreamThreads = 768;    // forward with many rows: most threads per CTA (85 registers each)
 constexpr int kBwdThreads = 512;       // backward: most threads per CTA
+constexpr int kGroupThreads = 512;     // most threads of a row: 16 warps, half a warp reads their sums
+static_assert(kBwdThreads <= kGroupThreads, "a row's warps");
 constexpr int kRowThreads = 256;
 constexpr int kFinishRows = 16;
 
@@ -659,7 +661,7 @@ cudaError_t fwd_typed(const NormFwd& a, cudaStream_t s) {
       if (n <= 32 * 2) return fwd_rows<X, Y, VEC, 2, true>(a, s);
       if (n <= 32 * 4) return fwd_rows<X, Y, VEC, 4, true>(a, s);
       constexpr int NV = 16 / VEC;
-      if (n <= kStreamThreads * NV) return fwd_stream<X, Y, VEC, NV, NV == 2 ? 6 : 4>(a, s);
+      if (n <= kGroupThreads * NV) return fwd_stream<X, Y, VEC, NV, NV == 2 ? 4 : 3>(a, s);
     }
     if (n <= kFwdMaxThreads) return fwd_rows<X, Y, VEC, 1, false>(a, s);
     if (n <= 4 * kFwdMaxThreads) return fwd_rows<X, Y, VEC, 4, false>(a, s);

@@ -88,7 +88,7 @@ def check_bwd(dy, x, w, mean, rstd, dx, dw, db, dw0=None, db0=None):
 
 
 SHAPES = [(1, 1), (1, 2560), (3, 7), (5, 1111), (33, 64), (300, 1000), (1500, 2560), (700, 4096),
-          (9, 8192), (7, 20000), (2, 70001), (1, 70008)]
+          (9, 8192), (640, 8192), (640, 8200), (615, 12288), (7, 20000), (2, 70001), (1, 70008)]
 TYPES = [("float32", "float32", "float32"), ("bfloat16", "bfloat16", "float32"),
          ("bfloat16", "float32", "bfloat16"), ("float16", "float16", "float16"),
          ("float32", "float32", "bfloat16"), ("float16", "float32", "float32")]
