@@ -200,8 +200,9 @@ __global__ void __launch_bounds__(kPerWarp ? 32 * kFwdWarpRows : kFwdMaxThreads)
 
 // Many rows: a group of g threads (a multiple of 32) takes row after row, each
 // thread always the same columns, so that weight and bias stay in registers and
-// rows arrive through a ring of asynchronous copies kDepth rows deep.  One barrier
-// per row and group.  The statistics join by
+// rows arrive through a ring of asynchronous copies kDepth rows deep (kDepth = 0:
+// units too small for such copies; a row's loads are issued a row ahead).  One
+// barrier per row and group.  The statistics join by
 //   mean = ref + sum n_j (m_j - ref) / n,  M2 = sum M2_j + n_j (m_j - ref)^2 - n (mean - ref)^2
 // over threads and then warps, with one part's own mean as ref: both sums at once,
 // and what cancels is no larger than that part's share of M2 times the parts.
@@ -217,6 +218,7 @@ __global__ void __launch_bounds__(kStreamThreads)
   const int groups = blockDim.x / g;
   const int grp = threadIdx.x / g, i = threadIdx.x - grp * g;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = g >> 5, w0 = grp * warps;
+  constexpr bool kRing = kDepth > 0;
   const int n = H / VEC;
   auto in = [&](int k) { return kFull || i + k * g < n; };   // kFull: n = NV g
   const PackRing<X, VEC> ring(ring_bytes, blockDim.x, threadIdx.x);
@@ -229,7 +231,7 @@ __global__ void __launch_bounds__(kStreamThreads)
       cnt += VEC;
       load_params<VEC>(w, param_type, (i + k * g) * VEC, one);
       if (b) load_params<VEC>(b, param_type, (i + k * g) * VEC, two);
-    } else {   // slots that are never filled read as zeros
+    } else if constexpr (kRing) {   // slots that are never filled read as zeros
 #pragma unroll
       for (int d = 0; d < kDepth; ++d) ring.clear(d * NV + k);
     }
@@ -249,50 +251,78 @@ __global__ void __launch_bounds__(kStreamThreads)
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
   int64_t t = static_cast<int64_t>(blockIdx.x) * groups + grp, next = t;
   int put = 0, get = 0;
+  Pack<X, VEC> ahead[kRing ? 1 : NV];
   auto fetch = [&] {
     if (next < N) {
       const X* from = x + next * x_ld + i * VEC;
 #pragma unroll
-      for (int k = 0; k < NV; ++k)
-        if (in(k)) ring.fetch(put * NV + k, from + k * g * VEC);
+      for (int k = 0; k < NV; ++k) {
+        if (!in(k)) continue;
+        if constexpr (kRing)
+          ring.fetch(put * NV + k, from + k * g * VEC);
+        else
+          ahead[k] = *reinterpret_cast<const Pack<X, VEC>*>(from + k * g * VEC);
+      }
     }
-    copy_async_commit();
+    if constexpr (kRing) {
+      copy_async_commit();
+      put = put + 1 == kDepth ? 0 : put + 1;
+    }
     next += step;
-    put = put + 1 == kDepth ? 0 : put + 1;
   };
 #pragma unroll
-  for (int d = 0; d < kDepth; ++d) fetch();
+  for (int d = 0; d < (kRing ? kDepth : 1); ++d) fetch();
   for (int flip = 0; t < N; t += step, flip ^= 1) {
-    copy_async_wait<kDepth - 1>();
-    // the thread's mean and squared deviations about it
-    float2 v[NV * VEC / 2];
+    if constexpr (kRing) copy_async_wait<kRing ? kDepth - 1 : 0>();
+    // the thread's mean and squared deviations about it (pairs of columns: within a
+    // pack, or of neighbouring packs of one element)
+    constexpr int kPairs = NV * VEC / 2;
+    float2 v[kPairs];
     float2 s2 = make_float2(0.f, 0.f), q2 = make_float2(0.f, 0.f);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const Pack<X, VEC> q = ring.read(get * NV + k);
+      Pack<X, VEC> q;
+      if constexpr (kRing)
+        q = ring.read(get * NV + k);
+      else
+        q = ahead[k];
+      if constexpr (VEC > 1) {
 #pragma unroll
-      for (int e = 0; e < VEC / 2; ++e) {
-        v[k * VEC / 2 + e] = pair_of(q, e);
-        s2 = add2(s2, v[k * VEC / 2 + e]);
+        for (int e = 0; e < VEC / 2; ++e) v[k * VEC / 2 + e] = pair_of(q, e);
+      } else {
+        at(v, k) = in(k) ? to_f32(q.v[0]) : 0.f;
       }
     }
-    get = get + 1 == kDepth ? 0 : get + 1;
+    if constexpr (kRing)
+      get = get + 1 == kDepth ? 0 : get + 1;
+    else
+      fetch();
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j) s2 = add2(s2, v[j]);
     const float own = (s2.x + s2.y) * own_inv;
     const float2 minus_own = make_float2(-own, -own);
+    if constexpr (VEC > 1) {
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      if (!in(k)) continue;
+      for (int k = 0; k < NV; ++k) {
+        if (!in(k)) continue;
 #pragma unroll
-      for (int e = 0; e < VEC / 2; ++e) {
-        const float2 d = add2(v[k * VEC / 2 + e], minus_own);
-        q2 = fma2(d, d, q2);
+        for (int e = 0; e < VEC / 2; ++e) {
+          const float2 d = add2(v[k * VEC / 2 + e], minus_own);
+          q2 = fma2(d, d, q2);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const float d = in(k) ? at(v, k) - own : 0.f;
+        q2.x = fmaf(d, d, q2.x);
       }
     }
     // the warp's, about lane 0's mean: its two sums go to shared memory
     const float first = __shfl_sync(0xffffffffu, own, 0);
     const float d0 = own - first, d1 = own_cnt * d0;
     const float half = warp_sum_halves(d1, fmaf(d1, d0, q2.x + q2.y));
-    fetch();   // into the slots just read, all of whose values are in the sums
+    if constexpr (kRing) fetch();   // into the slots just read, all of whose values are in the sums
     if ((lane & 15) == 0) red[flip][lane >> 4][warp] = half;
     if (lane == 1) red[flip][2][warp] = first;
     if (warps > 1)
@@ -316,13 +346,16 @@ __global__ void __launch_bounds__(kStreamThreads)
     const float2 minus_mu = make_float2(-mu, -mu), r2 = make_float2(r, r);
     Y* out = y + t * y_ld + i * VEC;
 #pragma unroll
+    for (int j = 0; j < kPairs; ++j) v[j] = fma2(mul2(add2(v[j], minus_mu), r2), wv[j], bv[j]);
+#pragma unroll
     for (int k = 0; k < NV; ++k) {
       if (!in(k)) continue;
       Pack<Y, VEC> o;
+      if constexpr (VEC > 1) {
 #pragma unroll
-      for (int e = 0; e < VEC / 2; ++e) {
-        const int j = k * VEC / 2 + e;
-        set_pair(o, e, fma2(mul2(add2(v[j], minus_mu), r2), wv[j], bv[j]));
+        for (int e = 0; e < VEC / 2; ++e) set_pair(o, e, v[k * VEC / 2 + e]);
+      } else {
+        o.v[0] = from_f32<Y>(at(v, k));
       }
       *reinterpret_cast<Pack<Y, VEC>*>(out + k * g * VEC) = o;
     }
@@ -331,7 +364,7 @@ __global__ void __launch_bounds__(kStreamThreads)
       if (rstd) rstd[t] = r;
     }
   }
-  copy_async_wait<0>();
+  if constexpr (kRing) copy_async_wait<0>();
 }
 
 // Both gradients in one pass over x and dy.  A group of g threads (a multiple of
@@ -666,6 +699,8 @@ cudaError_t fwd_typed(const NormFwd& a, cudaStream_t s) {
     if (n <= kFwdMaxThreads) return fwd_rows<X, Y, VEC, 1, false>(a, s);
     if (n <= 4 * kFwdMaxThreads) return fwd_rows<X, Y, VEC, 4, false>(a, s);
   }
+  if (a.N >= 4ll * sm_count() && a.H <= kGroupThreads * 8)
+    return fwd_stream<X, Y, 1, 8, sizeof(X) == 4 ? 4 : 0>(a, s);
   if (a.H <= kFwdMaxThreads) return fwd_rows<X, Y, 1, 4, false>(a, s);
   if (a.H <= 8 * kFwdMaxThreads) return fwd_rows<X, Y, 1, 8, false>(a, s);
   const int64_t cap = static_cast<int64_t>(sm_count()) * 8;
