@@ -15,6 +15,7 @@ namespace {
 static_assert(kF32 == LMHEAD_F32 && kBF16 == LMHEAD_BF16 && kF16 == LMHEAD_F16, "element types");
 
 constexpr int64_t kMaxRows = (int64_t{1} << 31) - 256;
+constexpr int32_t kMaxWidth = 1 << 20;   // of a layer norm's rows
 
 bool known_type(int type) { return type == kF32 || type == kBF16 || type == kF16; }
 
@@ -43,7 +44,7 @@ lmhead_status check_norm(int64_t N, int32_t H, int x_type, int other_type, int p
   if (N < 0 || H <= 0 || !known_type(x_type) || !known_type(other_type) || !known_type(param_type))
     return LMHEAD_ERR_INVALID_ARG;
   if (x_ld < H || other_ld < H) return LMHEAD_ERR_INVALID_ARG;
-  if (N >= kMaxRows || (param_type != kF32 && param_type != x_type)) return LMHEAD_ERR_UNSUPPORTED;
+  if (N >= kMaxRows || H > kMaxWidth || (param_type != kF32 && param_type != x_type)) return LMHEAD_ERR_UNSUPPORTED;
   return LMHEAD_OK;
 }
 
@@ -84,7 +85,7 @@ lmhead_status check_process(const ProcessLogits& a) {
 extern "C" {
 
 size_t lmhead_layernorm_workspace_size(int64_t N, int32_t H) {
-  return N < 0 || N >= kMaxRows || H <= 0 ? 0 : norm_workspace(N, H);
+  return N < 0 || N >= kMaxRows || H <= 0 || H > kMaxWidth ? 0 : norm_workspace(N, H);
 }
 
 lmhead_status lmhead_layernorm_fwd(const void* x, int x_type, int64_t x_ld, const void* weight,

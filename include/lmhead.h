@@ -450,7 +450,8 @@ lmhead_status lmhead_distill_logits_bwd(const void* logits, int type, int64_t ld
  *                  needed with d_weight or d_bias (for dx alone it may be NULL; rows
  *                  wider than 4096 then take a slower path)
  * Statistics and sums are fp32, the variance is taken about the mean, and column
- * sums are added in a fixed order: same inputs, same bits.  N == 0 is a no-op
+ * sums are added in a fixed order: same inputs, same bits.  H <= 2^20 and
+ * N < 2^31 - 256 (LMHEAD_ERR_UNSUPPORTED beyond).  N == 0 is a no-op
  * (the backward still zeroes d_weight / d_bias unless accumulate is set).
  */
 size_t lmhead_layernorm_workspace_size(int64_t N, int32_t H);

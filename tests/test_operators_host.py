@@ -57,6 +57,7 @@ CASES = [
         (dict(y_ld=63), INVALID), (dict(x_type=3), INVALID), (dict(y_type=-1), INVALID),
         (dict(param_type=9), INVALID), (dict(eps=-1e-6), INVALID), (dict(eps=float("nan")), INVALID),
         (dict(N=(1 << 31) - 256), UNSUPPORTED), (dict(param_type=2), UNSUPPORTED),
+        (dict(H=(1 << 20) + 1, x_ld=1 << 21, y_ld=1 << 21), UNSUPPORTED),
         (dict(y_type=0), UNSUPPORTED), (dict(x_type=2, y_type=1, param_type=0), UNSUPPORTED),
         (dict(x=P((1 << 20) + 1)), UNSUPPORTED), (dict(bias=P((1 << 20) + 1)), UNSUPPORTED),
         (dict(N=0, x=None, y=None), OK)]),
