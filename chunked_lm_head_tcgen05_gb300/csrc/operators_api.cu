@@ -69,12 +69,13 @@ lmhead_status check_process(const ProcessLogits& a) {
   if (a.R >= kMaxRows) return LMHEAD_ERR_UNSUPPORTED;
   if (a.R == 0) return LMHEAD_OK;
   if (!a.logits || !a.out) return LMHEAD_ERR_INVALID_ARG;
-  if ((a.tokens == nullptr) != (a.spans == nullptr)) return LMHEAD_ERR_INVALID_ARG;
-  if (!a.tokens && (a.repetition || a.frequency || a.presence)) return LMHEAD_ERR_INVALID_ARG;
+  // an empty list may have no address
+  if (a.tokens ? !a.spans : a.spans && a.n_tokens > 0) return LMHEAD_ERR_INVALID_ARG;
+  if (!a.spans && (a.repetition || a.frequency || a.presence)) return LMHEAD_ERR_INVALID_ARG;
   if (a.bias_offsets && a.n_bias > 0 && (!a.bias_ids || !a.bias_values))
     return LMHEAD_ERR_INVALID_ARG;
   if (!a.bias_offsets && (a.bias_ids || a.bias_values)) return LMHEAD_ERR_INVALID_ARG;
-  if (!a.allowed && a.allowed_rows) return LMHEAD_ERR_INVALID_ARG;
+  if (!a.allowed && a.allowed_rows && a.M > 0) return LMHEAD_ERR_INVALID_ARG;
   if (a.allowed && !a.allowed_rows && a.M < a.R) return LMHEAD_ERR_INVALID_ARG;
   if (!aligned_to(a.logits, a.type) || !aligned_to(a.out, a.type)) return LMHEAD_ERR_UNSUPPORTED;
   return LMHEAD_OK;

@@ -483,7 +483,8 @@ lmhead_status lmhead_layernorm_bwd(const void* dy, int dy_type, int64_t dy_ld, c
  *                positions of one sequence are rows whose spans end one token later
  *                each.  Ends are cut to [0, n_tokens] and to be in order; ids
  *                outside [0, V) (padding) are skipped.  Both NULL: no history
- *                (then the three penalties must be NULL too).
+ *                (then the three penalties must be NULL too).  tokens, bias_ids,
+ *                bias_values and allowed may be NULL where their count is 0.
  *  repetition, frequency, presence  [R] fp32, each may be NULL (1, 0, 0)
  *  bias_offsets  [R + 1] int64: row r's biases are entries
  *                [bias_offsets[r], bias_offsets[r + 1]) of bias_ids int32 and

@@ -215,3 +215,24 @@ def test_processed_logits_are_scored():
     ok = ~none & torch.isfinite(want)
     assert (logp[ok].double() - want[ok]).abs().max() < 1e-4
     assert torch.isneginf(logp[~none & torch.isneginf(want)]).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_empty_lists(dtype):
+    """Lists without an entry (torch gives them no address) are lists all the same."""
+    ensure_built()
+    R, V = 3, 1000
+    x = torch.randn(R, V, device="cuda", generator=torch.Generator("cuda").manual_seed(3)).to(dtype)
+    none = dict(dtype=torch.int32, device="cuda")
+    two = torch.full((R,), 2.0, device="cuda")
+    history = dict(tokens=torch.empty(0, **none),
+                   spans=torch.zeros(R, 3, dtype=torch.int64, device="cuda"), repetition=two)
+    grammar = dict(allowed=torch.empty(0, (V + 31) // 32, **none),
+                   allowed_rows=torch.full((R,), -1, **none))
+    bias = dict(bias_offsets=torch.zeros(R + 1, dtype=torch.int64, device="cuda"),
+                bias_ids=torch.empty(0, **none), bias_values=torch.empty(0, device="cuda"))
+    penalties = dict(frequency=two, presence=two)
+    for k in (history, grammar, bias, dict(history, **grammar, **bias, **penalties)):
+        assert torch.equal(lm.process_logits(x, **k), x)
+    for k in (history, grammar, dict(history, **grammar)):
+        assert torch.equal(lm.process_logits_backward(x, x, **k), x)
