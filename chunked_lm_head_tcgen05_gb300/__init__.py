@@ -857,6 +857,22 @@ def backward(hidden, weight, targets, loss_mask, temperature, chunk_size, grad_l
     return d_hidden, d_weight
 
 
+def _made_on(stream, first, fn, *args):
+    """fn(*args) with `stream` current, so that what it allocates belongs to that stream: memory
+    of another one could still be in use there, or be handed out again before the call is done."""
+    if _torch is None:
+        _bind_torch()
+    cuda = _torch.cuda
+    if isinstance(stream, int):
+        stream = (cuda.ExternalStream(stream, device=first.device) if stream
+                  else cuda.default_stream(first.device))
+    if first.device != stream.device:
+        raise ValueError("all tensors and the stream of one call must be on one CUDA device, "
+                         "got %s" % sorted({str(first.device), str(stream.device)}))
+    with cuda.stream(stream):
+        return fn(*args)
+
+
 def _distill_workspace(op, T, H, V, K, chunk_size, device):
     import torch
     n = lmhead_distill_workspace_size(op, T, H, V, K, chunk_size)
@@ -870,6 +886,10 @@ def distill_forward(hidden, weight, top_ids, top_logits, loss_mask=None, tempera
                     stream=None):
     """Distillation loss through the head.  Returns (loss [T], lse [T], z_top [T, K]), fp32;
     keep lse and z_top for ``distill_backward``."""
+    if stream is not None:
+        return _made_on(stream, hidden, distill_forward, hidden, weight, top_ids, top_logits,
+                        loss_mask, temperature, teacher_temperature, chunk_size, teacher_lse,
+                        workspace)
     import torch
     T, H = hidden.shape
     V = weight.shape[0]
@@ -882,7 +902,7 @@ def distill_forward(hidden, weight, top_ids, top_logits, loss_mask=None, tempera
         workspace = _distill_workspace(LMHEAD_OP_FWD, T, H, V, K, chunk_size, dev)
     rc = lmhead_distill_fwd(hidden, weight, top_ids, top_logits, teacher_lse, loss_mask,
                             temperature, teacher_temperature, chunk_size, loss, lse, z_top,
-                            workspace, stream)
+                            workspace)
     if rc:
         raise LmheadError(rc, "lmhead_distill_fwd")
     return loss, lse, z_top
@@ -892,6 +912,10 @@ def distill_backward(hidden, weight, top_ids, top_logits, loss_mask, temperature
                      teacher_temperature, chunk_size, grad_loss, lse, z_top, teacher_lse=None,
                      d_weight=None, accumulate_dweight=False, workspace=None, stream=None):
     """Returns (d_hidden [T, H] fp32, d_weight [V, H] fp32)."""
+    if stream is not None:
+        return _made_on(stream, hidden, distill_backward, hidden, weight, top_ids, top_logits,
+                        loss_mask, temperature, teacher_temperature, chunk_size, grad_loss, lse,
+                        z_top, teacher_lse, d_weight, accumulate_dweight, workspace)
     import torch
     T, H = hidden.shape
     V = weight.shape[0]
@@ -904,7 +928,7 @@ def distill_backward(hidden, weight, top_ids, top_logits, loss_mask, temperature
         workspace = _distill_workspace(LMHEAD_OP_BWD, T, H, V, top_ids.shape[1], chunk_size, dev)
     rc = lmhead_distill_bwd(hidden, weight, top_ids, top_logits, teacher_lse, loss_mask,
                             temperature, teacher_temperature, chunk_size, grad_loss, lse, z_top,
-                            d_hidden, d_weight, accumulate_dweight, workspace, stream)
+                            d_hidden, d_weight, accumulate_dweight, workspace)
     if rc:
         raise LmheadError(rc, "lmhead_distill_bwd")
     return d_hidden, d_weight
@@ -924,8 +948,11 @@ def distill_logits_forward(logits, top_ids, top_logits, loss_mask=None, temperat
                            teacher_temperature=1.0, teacher_lse=None, stream=None):
     """Distillation loss on held logits [T, V] (fp32, bf16 or fp16, rows may be padded).
     Returns (loss [T], lse [T]), fp32."""
+    if stream is not None:
+        return _made_on(stream, logits, distill_logits_forward, logits, top_ids, top_logits,
+                        loss_mask, temperature, teacher_temperature, teacher_lse)
     rc, out = _distill_logits_fwd(logits, top_ids, top_logits, teacher_lse, loss_mask, temperature,
-                                  teacher_temperature, None, stream)
+                                  teacher_temperature, None, None)
     if rc:
         raise LmheadError(rc, "lmhead_distill_logits_fwd")
     return out
@@ -936,11 +963,14 @@ def distill_logits_backward(logits, top_ids, top_logits, loss_mask, temperature,
                             stream=None):
     """Returns d_logits [T, V] of the logits' type, laid out like the logits
     (``d_logits=logits`` overwrites them)."""
+    if stream is not None:
+        return _made_on(stream, logits, distill_logits_backward, logits, top_ids, top_logits,
+                        loss_mask, temperature, teacher_temperature, grad_loss, lse, teacher_lse,
+                        d_logits)
     if d_logits is None:
         d_logits = _rows_like(logits)
     rc = lmhead_distill_logits_bwd(logits, top_ids, top_logits, teacher_lse, loss_mask,
-                                   temperature, teacher_temperature, grad_loss, lse, d_logits,
-                                   stream)
+                                   temperature, teacher_temperature, grad_loss, lse, d_logits)
     if rc:
         raise LmheadError(rc, "lmhead_distill_logits_bwd")
     return d_logits
@@ -949,7 +979,9 @@ def distill_logits_backward(logits, top_ids, top_logits, loss_mask, temperature,
 def layernorm_forward(x, weight, bias=None, eps=1e-5, out_dtype=None, stream=None):
     """Layer norm of x [N, H].  Returns (y [N, H] of x's type or out_dtype, mean [N] fp32,
     rstd [N] fp32)."""
-    rc, out = _layernorm_fwd(x, weight, bias, eps, None, out_dtype, stream)
+    if stream is not None:
+        return _made_on(stream, x, layernorm_forward, x, weight, bias, eps, out_dtype)
+    rc, out = _layernorm_fwd(x, weight, bias, eps, None, out_dtype, None)
     if rc:
         raise LmheadError(rc, "lmhead_layernorm_fwd")
     return out
@@ -958,6 +990,9 @@ def layernorm_forward(x, weight, bias=None, eps=1e-5, out_dtype=None, stream=Non
 def layernorm_backward(dy, x, weight, mean, rstd, with_bias=True, d_weight=None, d_bias=None,
                        accumulate=False, dx=None, workspace=None, stream=None):
     """Returns (dx [N, H] of x's type, d_weight [H] fp32, d_bias [H] fp32 or None)."""
+    if stream is not None:
+        return _made_on(stream, dy, layernorm_backward, dy, x, weight, mean, rstd, with_bias,
+                        d_weight, d_bias, accumulate, dx, workspace)
     if dx is None and d_weight is None and d_bias is None and not accumulate:
         out = None
     else:
@@ -973,7 +1008,7 @@ def layernorm_backward(dy, x, weight, mean, rstd, with_bias=True, d_weight=None,
             workspace = torch.empty(lmhead_layernorm_workspace_size(N, H), dtype=torch.uint8,
                                     device=x.device)
     rc, out = _layernorm_bwd(dy, x, weight, mean, rstd, out, with_bias, accumulate, workspace,
-                             stream)
+                             None)
     if rc:
         raise LmheadError(rc, "lmhead_layernorm_bwd")
     return out
@@ -984,11 +1019,15 @@ def process_logits(logits, tokens=None, spans=None, repetition=None, frequency=N
                    allowed=None, allowed_rows=None, out=None, stream=None):
     """Penalties, biases and a grammar mask on logits [R, V]; returns the processed logits, laid
     out like the logits (``out=logits`` processes them in place)."""
+    if stream is not None:
+        return _made_on(stream, logits, process_logits, logits, tokens, spans, repetition,
+                        frequency, presence, bias_offsets, bias_ids, bias_values, allowed,
+                        allowed_rows, out)
     if out is None:
         out = _rows_like(logits)
     rc = lmhead_process_logits_fwd(logits, tokens, spans, repetition, frequency, presence,
                                    bias_offsets, bias_ids, bias_values, allowed, allowed_rows,
-                                   out, stream)
+                                   out)
     if rc:
         raise LmheadError(rc, "lmhead_process_logits_fwd")
     return out
@@ -998,10 +1037,13 @@ def process_logits_backward(grad_out, logits, tokens=None, spans=None, repetitio
                             allowed=None, allowed_rows=None, d_logits=None, stream=None):
     """Cotangent of the original logits, laid out like grad_out (``d_logits=grad_out``
     overwrites it)."""
+    if stream is not None:
+        return _made_on(stream, grad_out, process_logits_backward, grad_out, logits, tokens, spans,
+                        repetition, allowed, allowed_rows, d_logits)
     if d_logits is None:
         d_logits = _rows_like(grad_out)
     rc = lmhead_process_logits_bwd(grad_out, logits, tokens, spans, repetition, allowed,
-                                   allowed_rows, d_logits, stream)
+                                   allowed_rows, d_logits)
     if rc:
         raise LmheadError(rc, "lmhead_process_logits_bwd")
     return d_logits
