@@ -123,11 +123,12 @@ __global__ void __launch_bounds__(kFwdThreads) logits_fwd_kernel(DistillLogits a
   extern __shared__ __align__(16) float teacher[];   // ring of packs; p, log p, logits [K]
   __shared__ float red[2][kFwdThreads / 32];
   __shared__ float joined[2][2 * kMaxCluster];       // by row parity: maxima, sums
+  uint32_t size;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(size));
+  if (size > 1) cluster_sync();   // every CTA runs before one writes to rank 0's memory
   pdl_wait_prerequisites();
   pdl_launch_dependents();
   constexpr int VEC = kVec<T>;
-  uint32_t size;
-  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(size));
   const uint32_t rank = cluster_cta_rank();
   const int K = a.teacher.K, threads = blockDim.x;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -229,6 +230,7 @@ __global__ void __launch_bounds__(kFwdThreads) logits_fwd_kernel(DistillLogits a
         st_shared_remote(to, __float_as_int(M));
         st_shared_remote(to + 4 * kMaxCluster, __float_as_int(S));
       }
+      __syncwarp();
     }
     if (size > 1) cluster_sync();
     if (!lead) continue;

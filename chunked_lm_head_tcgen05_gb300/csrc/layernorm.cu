@@ -733,7 +733,7 @@ cudaError_t bwd_rows(const NormBwd& a, cudaStream_t s) {
   constexpr size_t kRow = NV * VEC * (sizeof(X) + sizeof(D));   // a thread's bytes of one row
   constexpr int kDepth = !kRing ? 0 : kRow <= 96 ? 4 : 3;
   constexpr int kCols = kBwdThreads * VEC * NV;
-  const int sms = sm_count();
+  const int sms = std::min(sm_count(), kNormPartials);
   const int blocks = (a.H + kCols - 1) / kCols;
   const int n = ((a.H + blocks - 1) / blocks + VEC - 1) / VEC;   // packs of a block
   const bool params = a.d_weight || a.d_bias;
