@@ -11,6 +11,8 @@
 #include "operators.h"
 #include "ptx.cuh"
 
+#include <algorithm>
+
 namespace lmh {
 namespace {
 
