@@ -499,8 +499,8 @@ lmhead_status lmhead_layernorm_bwd(const void* dy, int dy_type, int64_t dy_ld, c
  * The backward takes the ORIGINAL logits and grad_out (the cotangent of out):
  *   d_logits = v allowed ? (met ? (x > 0 ? 1 / repetition_r : repetition_r) : 1)
  *              * grad_out : 0
- * d_logits may be grad_out itself, with the same ld.  Masked logits are not
- * read, nor, in the backward, logits of ids that were never met.
+ * d_logits may be grad_out itself, with the same ld.  Masked logits have no
+ * effect, whatever they are, nor, in the backward, logits of ids never met.
  */
 lmhead_status lmhead_process_logits_fwd(const void* logits, int type, int64_t ld, int64_t R,
                                         int32_t V, const int32_t* tokens, int64_t n_tokens,
