@@ -236,3 +236,20 @@ def test_empty_lists(dtype):
         assert torch.equal(lm.process_logits(x, **k), x)
     for k in (history, grammar, dict(history, **grammar)):
         assert torch.equal(lm.process_logits_backward(x, x, **k), x)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_many_rows(dtype):
+    """More rows than several rounds of CTAs take at once, with histories that overlap."""
+    ensure_built()
+    R, V, n = 1500, 517, 120
+    x = (np.random.default_rng(8).normal(size=(R, V)) * 3).astype(np.float32)
+    z = padded(x, 3, 1, DT[dtype])
+    k = rules(R, V, n, 6)
+    w = wide(k)
+    xz = ref.f64(z)
+    check(lm.process_logits(z, **cu(k)), ref.process_fwd(xz, **w), sizes(xz, w), dtype)
+    g = padded(np.random.default_rng(9).normal(size=(R, V)).astype(np.float32), 0, 0, DT[dtype])
+    kb = {n: v for n, v in k.items() if n in ("tokens", "spans", "repetition", "allowed", "allowed_rows")}
+    want = ref.process_bwd(ref.f64(g), xz, **wide(kb))
+    check(lm.process_logits_backward(g, z, **cu(kb)), want, 2 * np.abs(ref.f64(g)), dtype)
