@@ -285,12 +285,14 @@ struct Dense {
 // HBM-bound: 2048 x 151936 bf16, a quarter unscored, 172 us (6.3 TB/s).  Many warps with
 // few loads each do best: eight CTAs per SM with two packs in flight per thread; five
 // with four packs: 207 us.  K compares per entry by one thread instead of a warp, for
-// repeated ids, cost as many instructions as the dense pass (285 us).
-template <typename T>
+// repeated ids, cost as many instructions as the dense pass (285 us); with kBitmap a row
+// without repeated ids makes none.
+template <typename T, bool kBitmap>
 __global__ void __launch_bounds__(kThreads, 8) logits_bwd_kernel(DistillLogits a, int range) {
   extern __shared__ float teacher[];   // p, log p, id, entries of the range, their cotangents [K]
+  __shared__ uint32_t named[kBitmap ? kBwdMost / 2 / 32 : 1];   // a bit per column of the range
   __shared__ float total;
-  __shared__ int entries;
+  __shared__ int entries, repeated;
   pdl_wait_prerequisites();
   pdl_launch_dependents();
   constexpr int VEC = kVec<T>;
@@ -301,6 +303,8 @@ __global__ void __launch_bounds__(kThreads, 8) logits_bwd_kernel(DistillLogits a
   int* const entry = id + K;
   float* const value = reinterpret_cast<float*>(entry + K);
   const int c0 = blockIdx.x * range, n = min(range, a.V - c0);
+  if constexpr (kBitmap)
+    for (int i = threadIdx.x; i < range / 32; i += kThreads) named[i] = 0;   // and again after use
   for (int64_t t = blockIdx.y; t < a.T; t += gridDim.y) {
     const T* const src = static_cast<const T*>(a.logits) + t * a.ld + c0;
     T* const dst = static_cast<T*>(a.d_logits) + t * a.d_ld + c0;
@@ -315,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 8) logits_bwd_kernel(DistillLogits a
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u)
         if (threadIdx.x + u * kThreads < packs) q[u] = from[threadIdx.x + u * kThreads];
-      if (threadIdx.x == 0) entries = 0;
+      if (threadIdx.x == 0) entries = repeated = 0;
       __syncthreads();   // also: the previous row's readers are done
       if (warp == 0) {
         const float sum = teacher_row(a.teacher, t, p, logp);
@@ -328,8 +332,12 @@ __global__ void __launch_bounds__(kThreads, 8) logits_bwd_kernel(DistillLogits a
           id[k] = here ? v - c0 : -1;
           if (here) {
             const int e = atomicAdd(&entries, 1);
-            entry[e] = v - c0;
+            entry[e] = kBitmap ? v - c0 | k << 16 : v - c0;   // range <= 2^15 columns, K <= 2^10
             value[e] = to_f32(src[v - c0]);
+            if constexpr (kBitmap) {
+              const uint32_t bit = 1u << ((v - c0) & 31);
+              if (atomicOr(&named[(v - c0) >> 5], bit) & bit) repeated = 1;
+            }
           }
         }
       }
@@ -343,20 +351,30 @@ __global__ void __launch_bounds__(kThreads, 8) logits_bwd_kernel(DistillLogits a
       for (int i = threadIdx.x; i < head; i += kThreads) dst[i] = from_f32<T>(0.f);
       for (int i = tail + threadIdx.x; i < n; i += kThreads) dst[i] = from_f32<T>(0.f);
       for (int k = threadIdx.x; k < packs; k += kThreads) to[k] = zero;
+      if (kBitmap && scored) {
+        for (int e = threadIdx.x; e < entries; e += kThreads) named[(entry[e] & 0xffff) >> 5] = 0;
+        __syncthreads();   // `entries` is read before the next row's is written
+      }
       continue;
     }
     const float g = a.grad[t] / a.tau;
     const Dense<T> dense(a.tau, a.lse[t], g * P);
-    // a warp per entry: repeated ids add up, and each writes the same value
     const int here = entries;
-    for (int e = warp; e < here; e += kWarps) {
-      const int v = entry[e];
-      float taken = 0.f;
-      for (int i = lane; i < K; i += 32) taken += id[i] == v ? p[i] : 0.f;
-      taken = warp_sum(taken);
-      if (lane == 0) {
+    if (kBitmap && !repeated) {
+      for (int e = threadIdx.x; e < here; e += kThreads) {
         const float x = value[e];
-        value[e] = fabsf(x) < INFINITY ? fmaf(-g, taken, dense(x)) : 0.f;
+        value[e] = fabsf(x) < INFINITY ? fmaf(-g, p[entry[e] >> 16], dense(x)) : 0.f;
+      }
+    } else {   // a warp per entry: repeated ids add up, and each writes the same value
+      for (int e = warp; e < here; e += kWarps) {
+        const int v = kBitmap ? entry[e] & 0xffff : entry[e];
+        float taken = 0.f;
+        for (int i = lane; i < K; i += 32) taken += id[i] == v ? p[i] : 0.f;
+        taken = warp_sum(taken);
+        if (lane == 0) {
+          const float x = value[e];
+          value[e] = fabsf(x) < INFINITY ? fmaf(-g, taken, dense(x)) : 0.f;
+        }
       }
     }
 #pragma unroll 4
@@ -384,7 +402,11 @@ __global__ void __launch_bounds__(kThreads, 8) logits_bwd_kernel(DistillLogits a
       }
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < here; e += kThreads) dst[entry[e]] = from_f32<T>(value[e]);
+    for (int e = threadIdx.x; e < here; e += kThreads) {
+      const int v = kBitmap ? entry[e] & 0xffff : entry[e];
+      dst[v] = from_f32<T>(value[e]);
+      if constexpr (kBitmap) named[v >> 5] = 0;
+    }
   }
 }
 
@@ -611,7 +633,14 @@ cudaError_t logits_bwd(const DistillLogits& a, cudaStream_t s) {
   ranges = ranges < least ? least : ranges > most ? most : ranges;
   const int range = static_cast<int>(((a.V + ranges - 1) / ranges + 63) / 64 * 64);
   const unsigned rows = static_cast<unsigned>(a.T < 32768 ? a.T : 32768);
-  return launch_dependent(logits_bwd_kernel<T>,
+  // Comparing ids takes K compares for each of a range's about K range / V entries: with
+  // many, a bitmap that shows whether a row repeats an id at all is faster (6,171 rows of
+  // 2,491 fp16, K 213: 35 us against 146; 3,193 of 48,721 fp16, K 126: 115 against 126), with
+  // few it is slower (2,048 of 151,936 bf16, K 128: 178 against 168).
+  const int64_t K = a.teacher.K;
+  auto* const kern = K * K * range >= 5000ll * a.V ? logits_bwd_kernel<T, true>
+                                                   : logits_bwd_kernel<T, false>;
+  return launch_dependent(kern,
                           dim3(static_cast<unsigned>((static_cast<int64_t>(a.V) + range - 1) / range), rows),
                           kThreads, 5 * sizeof(float) * a.teacher.K, 1, s, a, range);
 }

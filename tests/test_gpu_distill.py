@@ -134,6 +134,30 @@ def test_held_logits(T, V, K, dtype, own_lse):
     assert torch.equal(z, d)
 
 
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_held_logits_more_rows_than_the_grid(dtype):
+    """CTAs that take a second row, with many entries: distinct, repeated, absent, and (rows whose
+    own log-sum-exp is far above) present without any mass."""
+    ensure_built()
+    T, V, K = 33500, 100, 80
+    r = np.random.default_rng(12)
+    ids = np.argsort(r.random((T, V)), axis=1)[:, :K].astype(np.int32)
+    a = (r.normal(size=(T, K)) * 2 + 5).astype(np.float32)
+    tlse = (9.0 + r.random(T)).astype(np.float32)
+    ids[::3, 5] = ids[::3, 9]
+    a[1::5] = -np.inf
+    tlse[2::5] = 3000.0
+    z = padded((r.normal(size=(T, V)) * 2).astype(np.float32), 4, 0, DT[dtype])
+    grad = r.normal(size=T).astype(np.float32)
+    cu = lambda v: torch.from_numpy(v).cuda()   # noqa: E731
+    loss, lse = lm.distill_logits_forward(z, cu(ids), cu(a), None, 0.7, 1.0, cu(tlse))
+    d = lm.distill_logits_backward(z, cu(ids), cu(a), None, 0.7, 1.0, cu(grad), lse, cu(tlse))
+    for rows in (slice(0, 150), slice(32700, 33500)):
+        check_logits(z[rows], ids[rows], a[rows].astype(np.float64), 0.7, 1.0,
+                     tlse[rows].astype(np.float64), None, grad[rows].astype(np.float64),
+                     loss[rows], lse[rows], d[rows], dtype)
+
+
 @pytest.mark.parametrize("V", [3001, 3000, 40000])
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
 def test_held_logits_not_finite(V, dtype):
