@@ -282,7 +282,7 @@ struct Dense {
 // CTA (column range, row).  Warp 0 forms the teacher's side while the others find
 // the entries of this range and read their logits (d_logits may be the logits
 // buffer); the dense pass follows, and the few exact cotangents are written last.
-// HBM-bound: 2048 x 151936 bf16, a quarter unscored, 172 us (6.3 TB/s).  Many warps with
+// HBM-bound: 2048 x 151936 bf16, a quarter unscored, 168 us (6.5 TB/s).  Many warps with
 // few loads each do best: eight CTAs per SM with two packs in flight per thread; five
 // with four packs: 207 us.  K compares per entry by one thread instead of a warp, for
 // repeated ids, cost as many instructions as the dense pass (285 us); with kBitmap a row
