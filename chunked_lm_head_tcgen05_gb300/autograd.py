@@ -264,19 +264,21 @@ def layer_norm(x, weight, bias=None, eps=1e-5, out_dtype=None):
 class ProcessLogits(torch.autograd.Function):
     """(logits [R,V], rules as keyword arguments of ``process_logits``) -> processed [R,V]."""
 
+    _BACKWARD = "tokens", "spans", "repetition", "allowed", "allowed_rows"   # rules it needs
+
     @staticmethod
     def forward(ctx, logits, rules):
-        ctx.save_for_backward(logits)
-        ctx.rules = {k: rules.get(k) for k in ("tokens", "spans", "repetition", "allowed",
-                                               "allowed_rows")}
+        # saved, so that a buffer the sampler has rewritten by the time of the backward is refused
+        ctx.save_for_backward(logits, *(rules.get(k) for k in ProcessLogits._BACKWARD))
         return _process_logits(logits, **rules)
 
     @staticmethod
     def backward(ctx, g):
-        logits, = ctx.saved_tensors
+        logits, *rules = ctx.saved_tensors
         if g.stride(1) != 1 or (g.shape[0] > 1 and g.stride(0) < g.shape[1]):
             g = g.contiguous()
-        return process_logits_backward(g, logits, **ctx.rules), None
+        rules = dict(zip(ProcessLogits._BACKWARD, rules))
+        return process_logits_backward(g, logits, **rules), None
 
 
 def process_logits(logits, **rules):
