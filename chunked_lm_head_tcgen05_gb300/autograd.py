@@ -261,6 +261,10 @@ def layer_norm(x, weight, bias=None, eps=1e-5, out_dtype=None):
     return LayerNorm.apply(x, weight, bias, float(eps), out_dtype)
 
 
+_RULES = {"tokens", "spans", "repetition", "frequency", "presence", "bias_offsets", "bias_ids",
+          "bias_values", "allowed", "allowed_rows"}
+
+
 class ProcessLogits(torch.autograd.Function):
     """(logits [R,V], rules as keyword arguments of ``process_logits``) -> processed [R,V]."""
 
@@ -284,4 +288,7 @@ class ProcessLogits(torch.autograd.Function):
 def process_logits(logits, **rules):
     """``chunked_lm_head_tcgen05_gb300.process_logits`` (the same keyword arguments, without
     ``out`` and ``stream``), differentiable in the logits."""
+    unknown = sorted(rules.keys() - _RULES)
+    if unknown:
+        raise TypeError("process_logits takes no %s here" % ", ".join(unknown))
     return ProcessLogits.apply(logits, rules)

@@ -53,3 +53,13 @@ def test_rules_pass_through_saved_tensor_hooks(processing):
     with torch.autograd.graph.saved_tensors_hooks(lambda t: seen.append(t.shape) or t, lambda t: t):
         autograd.process_logits(z, **processing)
     assert len(seen) == 1 + len(processing)
+
+
+@pytest.mark.parametrize("name", ["out", "stream"])
+def test_processing_refuses_what_it_has_no_form_for(processing, name):
+    """An output of the caller's could be the logits, which the backward reads."""
+    z = torch.randn(R, V, requires_grad=True)
+    with pytest.raises(TypeError, match=name):
+        autograd.process_logits(z, **processing, **{name: z.detach() if name == "out" else 0})
+    with pytest.raises(TypeError, match="no_such_rule"):
+        autograd.process_logits(z, no_such_rule=None)
