@@ -19,6 +19,8 @@ fp32 (``accumulate_dweight = 1``) instead; ``weight.grad`` is then left
 untouched, as in trainers that keep fp32 main gradients beside bf16
 parameters.
 """
+import contextlib
+
 import torch
 
 from . import LMHEAD_OP_BWD, LMHEAD_OP_FWD, LmheadError, distill_logits_backward, \
@@ -42,16 +44,30 @@ def _workspace(T, H, V, chunk_size, device):
     return _stream_workspace(n, device)
 
 
+@contextlib.contextmanager
 def _stream_workspace(n, device):
+    """The current stream's workspace, for the time a call enqueues its work.
+
+    It leaves the cache meanwhile: a call is several launches that pass data through
+    its workspace, and another thread's call on the same stream could come between
+    them.  A call under graph capture gets memory of the graph's own pool, since
+    replays go on using it."""
+    if torch.cuda.is_current_stream_capturing():
+        yield torch.empty(n, dtype=torch.uint8, device=device)
+        return
     key = (device.index, torch.cuda.current_stream(device).cuda_stream)
-    buf = _workspaces.get(key)
+    buf = _workspaces.pop(key, None)
     if buf is None or buf.numel() < n:
         # A smaller buffer replaced here may still be read by work queued on this
         # stream; torch's caching allocator gives its memory only to later work on
         # the same stream, so dropping the reference is safe.
         buf = torch.empty(n, dtype=torch.uint8, device=device)
-        _workspaces[key] = buf
-    return buf
+    try:
+        yield buf
+    finally:
+        kept = _workspaces.setdefault(key, buf)
+        if kept.numel() < buf.numel():   # another thread's, a smaller one, came back first
+            _workspaces[key] = buf
 
 
 def release_workspaces():
@@ -72,9 +88,9 @@ class LMHeadLogps(torch.autograd.Function):
         logp = torch.empty(T, dtype=torch.float32, device=dev)
         ent = torch.empty(T, dtype=torch.float32, device=dev)
         lse = torch.empty(T, dtype=torch.float32, device=dev)
-        ws = _workspace(T, H, V, chunk_size, dev)
-        rc = lmhead_logps_fwd(hidden, weight, targets, loss_mask, temperature, chunk_size, logp,
-                              ent, lse, ws)
+        with _workspace(T, H, V, chunk_size, dev) as ws:
+            rc = lmhead_logps_fwd(hidden, weight, targets, loss_mask, temperature, chunk_size,
+                                  logp, ent, lse, ws)
         if rc:
             raise LmheadError(rc, "lmhead_logps_fwd")
         ctx.save_for_backward(hidden, weight, targets, loss_mask, lse, ent)
@@ -102,10 +118,10 @@ class LMHeadLogps(torch.autograd.Function):
             d_weight, accumulate = main, 1
         else:
             d_weight, accumulate = torch.empty((V, H), dtype=torch.float32, device=dev), 0
-        ws = _workspace(T, H, V, ctx.chunk_size, dev)
-        rc = lmhead_logps_bwd(hidden, weight, targets, loss_mask, ctx.temperature, ctx.chunk_size,
-                              gl, ge, lse, ent if ge is not None else None, d_hidden, d_weight,
-                              accumulate, ws)
+        with _workspace(T, H, V, ctx.chunk_size, dev) as ws:
+            rc = lmhead_logps_bwd(hidden, weight, targets, loss_mask, ctx.temperature,
+                                  ctx.chunk_size, gl, ge, lse, ent if ge is not None else None,
+                                  d_hidden, d_weight, accumulate, ws)
         if rc:
             raise LmheadError(rc, "lmhead_logps_bwd")
         d_w = d_weight if (need_w and main is None) else None
@@ -156,9 +172,10 @@ class LMHeadDistill(torch.autograd.Function):
                  for op in (LMHEAD_OP_FWD, LMHEAD_OP_BWD)]
         if 0 in sizes:
             raise LmheadError(1, "lmhead_distill_workspace_size")
-        ws = _stream_workspace(max(sizes), dev)
-        rc = lmhead_distill_fwd(hidden, weight, top_ids, top_logits, teacher_lse, loss_mask,
-                                temperature, teacher_temperature, chunk_size, loss, lse, z_top, ws)
+        with _stream_workspace(max(sizes), dev) as ws:
+            rc = lmhead_distill_fwd(hidden, weight, top_ids, top_logits, teacher_lse, loss_mask,
+                                    temperature, teacher_temperature, chunk_size, loss, lse,
+                                    z_top, ws)
         if rc:
             raise LmheadError(rc, "lmhead_distill_fwd")
         ctx.save_for_backward(hidden, weight, top_ids, top_logits, loss_mask, teacher_lse, lse,
@@ -186,11 +203,11 @@ class LMHeadDistill(torch.autograd.Function):
             kind = torch.bfloat16 if lmhead_distill_narrow_dweight(T, H, V, ctx.chunk_size) \
                 else torch.float32
             d_weight = torch.empty((V, H), dtype=kind, device=dev)
-        ws = _stream_workspace(ctx.workspace_bytes, dev)
-        rc = lmhead_distill_bwd(hidden, weight, top_ids, top_logits, teacher_lse, loss_mask,
-                                *ctx.temperatures, ctx.chunk_size,
-                                g_loss.to(torch.float32).contiguous(), lse, z_top, d_hidden,
-                                d_weight, main is not None, ws)
+        g_loss = g_loss.to(torch.float32).contiguous()
+        with _stream_workspace(ctx.workspace_bytes, dev) as ws:
+            rc = lmhead_distill_bwd(hidden, weight, top_ids, top_logits, teacher_lse, loss_mask,
+                                    *ctx.temperatures, ctx.chunk_size, g_loss, lse, z_top,
+                                    d_hidden, d_weight, main is not None, ws)
         if rc:
             raise LmheadError(rc, "lmhead_distill_bwd")
         return (d_hidden if need_h else None, d_weight if need_w and main is None else None,
@@ -250,8 +267,9 @@ class LayerNorm(torch.autograd.Function):
         if dy.stride(1) != 1 or (dy.shape[0] > 1 and dy.stride(0) < dy.shape[1]):
             dy = dy.contiguous()
         need_b = ctx.needs_input_grad[2]
-        ws = _stream_workspace(lmhead_layernorm_workspace_size(*x.shape), x.device)
-        dx, dw, db = layernorm_backward(dy, x, weight, mean, rstd, with_bias=need_b, workspace=ws)
+        with _stream_workspace(lmhead_layernorm_workspace_size(*x.shape), x.device) as ws:
+            dx, dw, db = layernorm_backward(dy, x, weight, mean, rstd, with_bias=need_b,
+                                            workspace=ws)
         return (dx, dw, db, None, None)
 
 

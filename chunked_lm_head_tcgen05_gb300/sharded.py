@@ -24,6 +24,8 @@ d_weight.
 tensors' GPU.  Collectives run on the default stream of torch.distributed's
 backend after the library's work on the current stream.
 """
+import contextlib
+
 import torch
 import torch.distributed as dist
 
@@ -48,16 +50,16 @@ class LibraryOps:
     @staticmethod
     def _ws(T, H, V, chunk_size, device, workspace):
         if workspace is not None:
-            return workspace
+            return contextlib.nullcontext(workspace)
         return _workspace(T, H, V, chunk_size, device)
 
     def shard_forward(self, hidden, weight_shard, targets, loss_mask, vocab_offset, vocab_total,
                       temperature, chunk_size, workspace=None):
         T, H = hidden.shape
         part = torch.empty((T, 4), dtype=torch.float32, device=hidden.device)
-        ws = self._ws(T, H, weight_shard.shape[0], chunk_size, hidden.device, workspace)
-        rc = lmhead_logps_fwd_shard(hidden, weight_shard, targets, loss_mask, vocab_offset,
-                                    vocab_total, temperature, chunk_size, part, ws)
+        with self._ws(T, H, weight_shard.shape[0], chunk_size, hidden.device, workspace) as ws:
+            rc = lmhead_logps_fwd_shard(hidden, weight_shard, targets, loss_mask, vocab_offset,
+                                        vocab_total, temperature, chunk_size, part, ws)
         if rc:
             raise LmheadError(rc, "lmhead_logps_fwd_shard")
         return part
@@ -76,11 +78,12 @@ class LibraryOps:
                        d_weight_shard, accumulate, workspace=None):
         T, H = hidden.shape
         d_hidden = torch.empty((T, H), dtype=torch.float32, device=hidden.device)
-        ws = self._ws(T, H, weight_shard.shape[0], chunk_size, hidden.device, workspace)
-        rc = lmhead_logps_bwd_shard(hidden, weight_shard, targets, loss_mask, vocab_offset,
-                                    vocab_total, temperature, chunk_size, grad_logp, grad_entropy,
-                                    lse, entropy if grad_entropy is not None else None, d_hidden,
-                                    d_weight_shard, accumulate, ws)
+        with self._ws(T, H, weight_shard.shape[0], chunk_size, hidden.device, workspace) as ws:
+            rc = lmhead_logps_bwd_shard(hidden, weight_shard, targets, loss_mask, vocab_offset,
+                                        vocab_total, temperature, chunk_size, grad_logp,
+                                        grad_entropy, lse,
+                                        entropy if grad_entropy is not None else None, d_hidden,
+                                        d_weight_shard, accumulate, ws)
         if rc:
             raise LmheadError(rc, "lmhead_logps_bwd_shard")
         return d_hidden
@@ -90,9 +93,9 @@ class LibraryOps:
         T, H = hidden.shape
         dev = hidden.device
         logp, ent, lse = (torch.empty(T, dtype=torch.float32, device=dev) for _ in range(3))
-        ws = self._ws(T, H, weight.shape[0], chunk_size, dev, workspace)
-        rc = lmhead_logps_fwd(hidden, weight, targets, loss_mask, temperature, chunk_size, logp,
-                              ent, lse, ws)
+        with self._ws(T, H, weight.shape[0], chunk_size, dev, workspace) as ws:
+            rc = lmhead_logps_fwd(hidden, weight, targets, loss_mask, temperature, chunk_size,
+                                  logp, ent, lse, ws)
         if rc:
             raise LmheadError(rc, "lmhead_logps_fwd")
         return logp, ent, lse
@@ -102,11 +105,11 @@ class LibraryOps:
         T, H = hidden.shape
         dev = hidden.device
         d_hidden = torch.empty((T, H), dtype=torch.float32, device=dev)
-        ws = self._ws(T, H, weight.shape[0], chunk_size, dev, workspace)
-        rc = lmhead_logps_bwd(hidden, weight, targets, loss_mask, temperature, chunk_size,
-                              grad_logp, grad_entropy, lse,
-                              entropy if grad_entropy is not None else None, d_hidden, d_weight,
-                              accumulate, ws)
+        with self._ws(T, H, weight.shape[0], chunk_size, dev, workspace) as ws:
+            rc = lmhead_logps_bwd(hidden, weight, targets, loss_mask, temperature, chunk_size,
+                                  grad_logp, grad_entropy, lse,
+                                  entropy if grad_entropy is not None else None, d_hidden,
+                                  d_weight, accumulate, ws)
         if rc:
             raise LmheadError(rc, "lmhead_logps_bwd")
         return d_hidden

@@ -1,5 +1,8 @@
 """What the autograd functions of layer norm, distillation and logit processing keep between
 forward and backward, with stand-ins for the library's calls (no GPU)."""
+import threading
+from types import SimpleNamespace
+
 import pytest
 import torch
 
@@ -63,3 +66,88 @@ def test_processing_refuses_what_it_has_no_form_for(processing, name):
         autograd.process_logits(z, **processing, **{name: z.detach() if name == "out" else 0})
     with pytest.raises(TypeError, match="no_such_rule"):
         autograd.process_logits(z, no_such_rule=None)
+
+
+class Meeting:
+    """A stand-in for a library call that several threads are in at once; notes the workspaces."""
+
+    def __init__(self, threads):
+        self.barrier = threading.Barrier(threads, timeout=20)
+        self.workspaces = []
+
+    def __call__(self, workspace):
+        self.workspaces.append(workspace)
+        self.barrier.wait()
+
+
+@pytest.fixture
+def cached(monkeypatch):
+    """The workspace cache without a GPU: every call is on one stream, capturing as told."""
+    state = SimpleNamespace(capturing=False)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: SimpleNamespace(cuda_stream=7))
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: state.capturing)
+    monkeypatch.setattr(autograd, "lmhead_layernorm_workspace_size", lambda n, h: 64 * n)
+    monkeypatch.setattr(autograd, "layernorm_forward",
+                        lambda x, w, b, eps, kind: (x * w, x.mean(1), x.mean(1)))
+    autograd.release_workspaces()
+    yield state
+    autograd.release_workspaces()
+
+
+def norm_backward(monkeypatch, call, rows=4):
+    def backward(dy, x, w, mean, rstd, with_bias=True, workspace=None):
+        call(workspace)
+        return dy, torch.zeros_like(w), None
+    monkeypatch.setattr(autograd, "layernorm_backward", backward)
+    x, w = torch.randn(rows, 8, requires_grad=True), torch.ones(8)
+    return lambda: autograd.layer_norm(x, w).backward(torch.ones(rows, 8))
+
+
+def test_threads_in_one_streams_calls_do_not_share_a_workspace(cached, monkeypatch):
+    """A call is several launches that pass data through its workspace, and another thread's may
+    come between them on the same stream."""
+    meeting = Meeting(2)
+    step = norm_backward(monkeypatch, meeting)
+    step_too = norm_backward(monkeypatch, meeting)
+    threads = [threading.Thread(target=f) for f in (step, step_too)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(meeting.workspaces) == 2
+    assert len({w.data_ptr() for w in meeting.workspaces}) == 2
+    assert len(autograd._workspaces) == 1          # and one of them stays
+
+
+def test_workspace_stays_between_calls_and_grows(cached, monkeypatch):
+    seen = []
+    for rows in (4, 4, 2, 9, 4):
+        norm_backward(monkeypatch, lambda w: seen.append((w.data_ptr(), w.numel())), rows)()
+    assert [n for _, n in seen] == [256, 256, 256, 576, 576]
+    assert seen[0] == seen[1] == seen[2] and seen[3] == seen[4]
+
+
+def test_a_captured_call_has_a_workspace_of_its_own(cached, monkeypatch):
+    """A graph replays into the address it was captured with, so that memory belongs to the graph's
+    pool and not to a cache that may drop it."""
+    seen = []
+    step = norm_backward(monkeypatch, seen.append)
+    step()
+    before = {k: v.data_ptr() for k, v in autograd._workspaces.items()}
+    cached.capturing = True
+    step()
+    cached.capturing = False
+    assert seen[1].data_ptr() != seen[0].data_ptr()
+    assert {k: v.data_ptr() for k, v in autograd._workspaces.items()} == before
+
+
+def test_a_refused_call_does_not_lose_the_workspace(cached, monkeypatch):
+    seen = []
+
+    def refuse(w):
+        seen.append(w.data_ptr())
+        raise ValueError("refused")
+    for _ in range(2):
+        with pytest.raises(ValueError, match="refused"):
+            norm_backward(monkeypatch, refuse)()
+    assert seen[0] == seen[1]
