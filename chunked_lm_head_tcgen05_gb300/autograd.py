@@ -20,6 +20,7 @@ untouched, as in trainers that keep fp32 main gradients beside bf16
 parameters.
 """
 import contextlib
+import functools
 
 import torch
 
@@ -153,6 +154,35 @@ def _main_grad(weight, main_grad):
     return main_grad
 
 
+class _Once(torch.autograd.Function):
+    """(n, n gradients, what they were formed from) -> the gradients, whose own backward raises."""
+
+    @staticmethod
+    def forward(ctx, n, *tensors):
+        return tuple(t.view_as(t) for t in tensors[:n])
+
+    @staticmethod
+    def backward(ctx, *cotangents):
+        raise RuntimeError("this function is differentiable once: its gradient comes from the "
+                           "library's kernels, whose own derivative torch does not know")
+
+
+def _differentiable_once(backward):
+    """A backward whose gradients refuse to be differentiated again (create_graph=True) instead of
+    passing for constants.  torch's own once_differentiable looks at the cotangents only; these
+    gradients depend on the saved tensors too."""
+    @functools.wraps(backward)
+    def first(ctx, *cotangents):
+        with torch.no_grad():
+            grads = backward(ctx, *cotangents)
+        if not torch.is_grad_enabled():
+            return grads
+        at = [i for i, t in enumerate(grads) if t is not None]
+        marked = _Once.apply(len(at), *(grads[i] for i in at), *cotangents, *ctx.saved_tensors)
+        return tuple(marked[at.index(i)] if i in at else None for i in range(len(grads)))
+    return first
+
+
 class LMHeadDistill(torch.autograd.Function):
     """(hidden [T,H] bf16, weight [V,H] bf16, top_ids [T,K] int32, top_logits [T,K] fp32,
     loss_mask, temperature, teacher_temperature, chunk_size, teacher_lse [T] fp32 or None,
@@ -187,6 +217,7 @@ class LMHeadDistill(torch.autograd.Function):
         return loss
 
     @staticmethod
+    @_differentiable_once
     def backward(ctx, g_loss):
         hidden, weight, top_ids, top_logits, loss_mask, teacher_lse, lse, z_top = ctx.saved_tensors
         need_h, need_w = ctx.needs_input_grad[0], ctx.needs_input_grad[1]
@@ -238,6 +269,7 @@ class DistillLogits(torch.autograd.Function):
         return loss
 
     @staticmethod
+    @_differentiable_once
     def backward(ctx, g_loss):
         logits, top_ids, top_logits, loss_mask, teacher_lse, lse = ctx.saved_tensors
         d = distill_logits_backward(logits, top_ids, top_logits, loss_mask, *ctx.temperatures,
@@ -262,6 +294,7 @@ class LayerNorm(torch.autograd.Function):
         return y
 
     @staticmethod
+    @_differentiable_once
     def backward(ctx, dy):
         x, weight, mean, rstd = ctx.saved_tensors
         if dy.stride(1) != 1 or (dy.shape[0] > 1 and dy.stride(0) < dy.shape[1]):
@@ -295,6 +328,7 @@ class ProcessLogits(torch.autograd.Function):
         return _process_logits(logits, **rules)
 
     @staticmethod
+    @_differentiable_once
     def backward(ctx, g):
         logits, *rules = ctx.saved_tensors
         if g.stride(1) != 1 or (g.shape[0] > 1 and g.stride(0) < g.shape[1]):

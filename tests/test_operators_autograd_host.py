@@ -1,5 +1,6 @@
 """What the autograd functions of layer norm, distillation and logit processing keep between
 forward and backward, with stand-ins for the library's calls (no GPU)."""
+import contextlib
 import threading
 from types import SimpleNamespace
 
@@ -151,3 +152,46 @@ def test_a_refused_call_does_not_lose_the_workspace(cached, monkeypatch):
         with pytest.raises(ValueError, match="refused"):
             norm_backward(monkeypatch, refuse)()
     assert seen[0] == seen[1]
+
+
+def first_gradients(monkeypatch):
+    """(name, loss, leaf) of the four functions, by stand-ins."""
+    @contextlib.contextmanager
+    def no_workspace(n, device):
+        yield None
+    zero = torch.zeros(4)
+    monkeypatch.setattr(autograd, "_stream_workspace", no_workspace)
+    monkeypatch.setattr(autograd, "lmhead_layernorm_workspace_size", lambda n, h: 1)
+    monkeypatch.setattr(autograd, "layernorm_forward", lambda x, w, b, eps, kind: (x * x, zero, zero))
+    monkeypatch.setattr(autograd, "layernorm_backward",
+                        lambda dy, x, w, *a, **k: (2 * dy * x, torch.zeros_like(w), None))
+    monkeypatch.setattr(autograd, "distill_logits_forward", lambda z, *a: ((z * z).sum(1), zero))
+    monkeypatch.setattr(autograd, "distill_logits_backward",
+                        lambda z, ids, top, mask, t, tt, g, *a: 2 * z * g[:, None])
+    monkeypatch.setattr(autograd, "lmhead_distill_workspace_size", lambda *a: 1)
+    monkeypatch.setattr(autograd, "lmhead_distill_narrow_dweight", lambda *a: False)
+    monkeypatch.setattr(autograd, "lmhead_distill_fwd", lambda *a: 0)
+    monkeypatch.setattr(autograd, "lmhead_distill_bwd", lambda *a: 0)
+    monkeypatch.setattr(autograd, "_process_logits", lambda z: z * z)
+    monkeypatch.setattr(autograd, "process_logits_backward", lambda g, z, **rules: 2 * g * z)
+    x = torch.randn(4, 8, requires_grad=True)
+    ids, top = torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2)
+    yield "layer_norm", autograd.layer_norm(x, torch.ones(8)), x
+    yield "distill_logits", autograd.distill_logits(x, ids, top), x
+    yield "lmhead_distill", autograd.lmhead_distill(x, torch.ones(5, 8), ids, top), x
+    yield "process_logits", autograd.process_logits(x), x
+
+
+def test_a_second_derivative_is_refused(monkeypatch):
+    """The backward's calls are no graph of torch's: a term that needs their derivative must raise,
+    not drop out of a sum in which another path carries one."""
+    for name, out, x in first_gradients(monkeypatch):
+        plain, = torch.autograd.grad(out.sum(), x, retain_graph=True)
+        assert not plain.requires_grad
+        d, = torch.autograd.grad(out.sum(), x, create_graph=True)
+        if name != "lmhead_distill":           # (its stand-in writes nothing)
+            assert torch.equal(d.detach(), plain), name
+        (x ** 3).sum().backward()              # other paths are not concerned
+        for second in (lambda p: torch.autograd.grad(p, x, retain_graph=True), torch.Tensor.backward):
+            with pytest.raises(RuntimeError, match="differentiable once"):
+                second(d.sum() + (x ** 3).sum())
