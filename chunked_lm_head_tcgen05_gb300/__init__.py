@@ -934,14 +934,20 @@ def distill_backward(hidden, weight, top_ids, top_logits, loss_mask, temperature
     return d_hidden, d_weight
 
 
+_MOST_PADDING = 256   # elements between rows that a new result repeats
+
+
 def _rows_like(t):
-    """A new matrix with t's rows as far apart as t's are (so both sides of a call have the
-    same alignment, padded rows included)."""
+    """A new matrix for a result beside t: its rows as far apart as t's where those are padded (a
+    table rounded up), else just far enough to have the same 16-byte alignment as t's (rows taken
+    out of a larger tensor must not cost its size again)."""
     if _torch is None:
         _bind_torch()
     rows, cols = t.shape
-    return _torch.empty_strided((rows, cols), (max(t.stride(0), cols), 1), dtype=t.dtype,
-                                device=t.device)
+    gap = max(t.stride(0) - cols, 0)
+    if gap > _MOST_PADDING:
+        gap %= 16 // t.element_size()
+    return _torch.empty_strided((rows, cols), (cols + gap, 1), dtype=t.dtype, device=t.device)
 
 
 def distill_logits_forward(logits, top_ids, top_logits, loss_mask=None, temperature=1.0,
@@ -961,7 +967,7 @@ def distill_logits_forward(logits, top_ids, top_logits, loss_mask=None, temperat
 def distill_logits_backward(logits, top_ids, top_logits, loss_mask, temperature,
                             teacher_temperature, grad_loss, lse, teacher_lse=None, d_logits=None,
                             stream=None):
-    """Returns d_logits [T, V] of the logits' type, laid out like the logits
+    """Returns d_logits [T, V] of the logits' type, padded like the logits
     (``d_logits=logits`` overwrites them)."""
     if stream is not None:
         return _made_on(stream, logits, distill_logits_backward, logits, top_ids, top_logits,
@@ -1017,8 +1023,8 @@ def layernorm_backward(dy, x, weight, mean, rstd, with_bias=True, d_weight=None,
 def process_logits(logits, tokens=None, spans=None, repetition=None, frequency=None,
                    presence=None, bias_offsets=None, bias_ids=None, bias_values=None,
                    allowed=None, allowed_rows=None, out=None, stream=None):
-    """Penalties, biases and a grammar mask on logits [R, V]; returns the processed logits, laid
-    out like the logits (``out=logits`` processes them in place)."""
+    """Penalties, biases and a grammar mask on logits [R, V]; returns the processed logits, padded
+    like the logits (``out=logits`` processes them in place)."""
     if stream is not None:
         return _made_on(stream, logits, process_logits, logits, tokens, spans, repetition,
                         frequency, presence, bias_offsets, bias_ids, bias_values, allowed,
@@ -1035,7 +1041,7 @@ def process_logits(logits, tokens=None, spans=None, repetition=None, frequency=N
 
 def process_logits_backward(grad_out, logits, tokens=None, spans=None, repetition=None,
                             allowed=None, allowed_rows=None, d_logits=None, stream=None):
-    """Cotangent of the original logits, laid out like grad_out (``d_logits=grad_out``
+    """Cotangent of the original logits, padded like grad_out (``d_logits=grad_out``
     overwrites it)."""
     if stream is not None:
         return _made_on(stream, grad_out, process_logits_backward, grad_out, logits, tokens, spans,
