@@ -26,6 +26,12 @@ bool aligned_to(const void* p, int type) {
   return (reinterpret_cast<uintptr_t>(p) & (element_bytes(type) - 1)) == 0;
 }
 
+// A result over one of the call's inputs needs that input's layout: a CTA writes its
+// rows while others still read theirs.
+bool clash(const void* in, int64_t in_ld, const void* out, int64_t out_ld, int64_t rows) {
+  return in && in == out && rows > 1 && in_ld != out_ld;
+}
+
 bool positive(float v) { return std::isfinite(v) && v > 0.f; }
 
 lmhead_status status_of(cudaError_t e) { return e == cudaSuccess ? LMHEAD_OK : LMHEAD_ERR_CUDA; }
@@ -78,6 +84,7 @@ lmhead_status check_process(const ProcessLogits& a) {
   if (!a.allowed && a.allowed_rows && a.M > 0) return LMHEAD_ERR_INVALID_ARG;
   if (a.allowed && !a.allowed_rows && a.M < a.R) return LMHEAD_ERR_INVALID_ARG;
   if (!aligned_to(a.logits, a.type) || !aligned_to(a.out, a.type)) return LMHEAD_ERR_UNSUPPORTED;
+  if (clash(a.logits, a.ld, a.out, a.out_ld, a.R)) return LMHEAD_ERR_INVALID_ARG;
   return LMHEAD_OK;
 }
 
@@ -102,6 +109,7 @@ lmhead_status lmhead_layernorm_fwd(const void* x, int x_type, int64_t x_ld, cons
   if (!aligned_to(x, x_type) || !aligned_to(y, y_type) || !aligned_to(weight, param_type) ||
       !aligned_to(bias, param_type))
     return LMHEAD_ERR_UNSUPPORTED;
+  if (clash(x, x_ld, y, y_ld, N) || (x == y && x_type != y_type)) return LMHEAD_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const NormFwd a{x, x_type, x_ld, weight, bias, param_type, N, H, eps, y, y_type, y_ld, mean, rstd};
   return status_of(traced_launch("layernorm_fwd", s, [&] { return launch_norm_fwd(a, s); }));
@@ -133,6 +141,8 @@ lmhead_status lmhead_layernorm_bwd(const void* dy, int dy_type, int64_t dy_ld, c
     return LMHEAD_ERR_UNSUPPORTED;
   if ((d_weight || d_bias) && workspace_bytes < norm_workspace(N, H))
     return LMHEAD_ERR_WORKSPACE_TOO_SMALL;
+  if (clash(x, x_ld, dx, dx_ld, N) || clash(dy, dy_ld, dx, dx_ld, N) || (dx == dy && dy_type != x_type))
+    return LMHEAD_ERR_INVALID_ARG;
   // a workspace given for dx alone is used if it is large enough
   const bool room = workspace && workspace_bytes >= norm_workspace(N, H);
   float2* sums = room && H > kNormWide
@@ -183,6 +193,7 @@ lmhead_status lmhead_distill_logits_bwd(const void* logits, int type, int64_t ld
   if (T == 0) return LMHEAD_OK;
   if (!grad_loss || !lse || !d_logits) return LMHEAD_ERR_INVALID_ARG;
   if (!aligned_to(d_logits, type)) return LMHEAD_ERR_UNSUPPORTED;
+  if (clash(logits, ld, d_logits, d_ld, T)) return LMHEAD_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   DistillLogits a{};
   a.logits = logits;
@@ -234,6 +245,7 @@ lmhead_status lmhead_process_logits_bwd(const void* grad_out, int64_t grad_ld, c
   if (R == 0) return LMHEAD_OK;
   if (!grad_out) return LMHEAD_ERR_INVALID_ARG;
   if (!aligned_to(grad_out, type)) return LMHEAD_ERR_UNSUPPORTED;
+  if (clash(grad_out, grad_ld, d_logits, d_ld, R)) return LMHEAD_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return status_of(traced_launch("process_logits_bwd", s, [&] { return launch_process_logits(a, s); }));
 }

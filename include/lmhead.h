@@ -406,7 +406,7 @@ int lmhead_distill_narrow_dweight(int64_t T, int32_t H, int32_t V, int32_t chunk
  * Distillation on logits the caller holds: logits [T, V] of element type `type`,
  * rows `ld` >= V elements apart (a table padded past V keeps its padding out of
  * the softmax).  d_logits (type, rows d_ld apart) is overwritten and may be the
- * logits buffer itself, with the same ld.  Sums are fp32; d_logits is rounded
+ * logits buffer itself, with the same ld (another: LMHEAD_ERR_INVALID_ARG).  Sums are fp32; d_logits is rounded
  * once.  Non-finite student logits as in lmhead_score_logits_fwd: -inf has
  * probability 0 (and makes the loss +inf where p_k > 0), NaN or +inf makes the
  * row's lse and loss NaN, a row with no finite logit has lse = -inf and a NaN
@@ -442,8 +442,8 @@ lmhead_status lmhead_distill_logits_bwd(const void* logits, int type, int64_t ld
  *   dx = rstd_t (h - mean(h) - xh mean(h xh))
  *   d_weight (+)= sum_t dy xh,  d_bias (+)= sum_t dy
  *  dy_type         x_type or LMHEAD_F32 (the head's d_hidden), or bf16 for fp32 rows
- *  dx              [N, H] of x_type, rows dx_ld apart; may be NULL, and may be x or
- *                  (same type and ld) dy itself
+ *  dx              [N, H] of x_type, rows dx_ld apart; may be NULL, and may be x or dy
+ *                  itself with the same type and ld (others: LMHEAD_ERR_INVALID_ARG)
  *  d_weight, d_bias  [H] fp32, each may be NULL; overwritten, or added to when
  *                  accumulate != 0
  *  workspace       lmhead_layernorm_workspace_size(N, H) bytes, 256-byte aligned;
@@ -495,12 +495,13 @@ lmhead_status lmhead_layernorm_bwd(const void* dy, int dy_type, int64_t dy_ld, c
  *                r when allowed_rows is NULL; an index outside [0, n_allowed) (-1)
  *                leaves the row unmasked.  A mask with no bit set gives a row of -inf.
  *  out           [R, V] of the same type, rows out_ld apart; may be the logits
- *                buffer itself, with the same ld
+ *                buffer itself, with the same ld (another: LMHEAD_ERR_INVALID_ARG)
  * The backward takes the ORIGINAL logits and grad_out (the cotangent of out):
  *   d_logits = v allowed ? (met ? (x > 0 ? 1 / repetition_r : repetition_r) : 1)
  *              * grad_out : 0
- * d_logits may be grad_out itself, with the same ld.  Masked logits have no
- * effect, whatever they are, nor, in the backward, logits of ids never met.
+ * d_logits may be grad_out itself, with the same ld (another: LMHEAD_ERR_INVALID_ARG).
+ * Masked logits have no effect, whatever they are, nor, in the backward, logits of ids
+ * never met.
  */
 lmhead_status lmhead_process_logits_fwd(const void* logits, int type, int64_t ld, int64_t R,
                                         int32_t V, const int32_t* tokens, int64_t n_tokens,
