@@ -378,7 +378,8 @@ __global__ void __launch_bounds__(kStreamThreads)
 
 // Both gradients in one pass over x and dy.  A group of g threads (a multiple of
 // 32) owns a row at a time and its threads fixed columns, so dw and db gather in
-// registers over the group's rows; the CTA's groups are joined in shared memory
+// registers over the group's rows; dx may be x or dy (each thread writes what it alone
+// has read).  The CTA's groups are joined in shared memory
 // at the end, and the CTA writes one partial row.  Rows of more than `cols` columns
 // go in blocks of that many (blockIdx.y), their two sums having been formed before
 // (`sums`); narrower ones in one block that forms them itself.  Rows arrive through a ring of
@@ -389,7 +390,7 @@ __global__ void __launch_bounds__(kStreamThreads)
 // are too few to hide the first loads and the join.
 template <typename X, typename D, int VEC, int NV, int kDepth, bool kFull>
 __global__ void __launch_bounds__(kBwdThreads)
-    norm_bwd_kernel(const D* __restrict__ dy, int64_t dy_ld, const X* x, int64_t x_ld,
+    norm_bwd_kernel(const D* dy, int64_t dy_ld, const X* x, int64_t x_ld,
                     const void* __restrict__ w, int param_type, const float* __restrict__ mean,
                     const float* __restrict__ rstd, int64_t N, int H, int cols,
                     const float2* __restrict__ sums, X* dx, int64_t dx_ld,
@@ -568,12 +569,13 @@ __global__ void __launch_bounds__(kBwdThreads)
   }
 }
 
+// dx of wide rows without a workspace for their sums; dx may be x or dy.
 template <typename X, typename D>
 __global__ void __launch_bounds__(kRowThreads)
-    norm_dx_any_kernel(const D* __restrict__ dy, int64_t dy_ld, const X* __restrict__ x,
+    norm_dx_any_kernel(const D* dy, int64_t dy_ld, const X* x,
                        int64_t x_ld, const void* __restrict__ w, int param_type,
                        const float* __restrict__ mean, const float* __restrict__ rstd, int64_t N,
-                       int H, X* __restrict__ dx, int64_t dx_ld) {
+                       int H, X* dx, int64_t dx_ld) {
   pdl_wait_prerequisites();
   pdl_launch_dependents();
   __shared__ float red[kRowThreads / 32];

@@ -40,3 +40,26 @@ def test_last_position_of_a_batch(B, S, V, dtype):
         # (odd widths lie at another alignment packed, where a row's sums take another order)
         assert torch.equal(a, b) if V % 8 == 0 else torch.allclose(a, b, rtol=1e-2, atol=1e-6), name
         assert a.untyped_storage().nbytes() <= B * (V + 256) * a.element_size(), name
+
+
+@pytest.mark.parametrize("N,H", [(40, 1001), (700, 999), (700, 1024), (9, 4500), (50, 5000), (20, 9001)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("params", [False, True])
+def test_layernorm_gradient_over_its_inputs(N, H, dtype, params):
+    """dx over dy and over x, alone (wide rows then have no workspace for their sums) and with the
+    weight's gradients."""
+    ensure_built()
+    x, dy = randn(N, H, seed=5, dtype=dtype), randn(N, H, seed=6, dtype=dtype)
+    w = 1 + 0.1 * randn(H, seed=7)
+    _, mean, rstd = lm.layernorm_forward(x, w)
+    ws = torch.empty(lm.lmhead_layernorm_workspace_size(N, H), dtype=torch.uint8, device="cuda") \
+        if params else None
+
+    def call(dy, x, dx):
+        dw, db = [torch.empty(H, device="cuda") if params else None for _ in range(2)]
+        assert lm.lmhead_layernorm_bwd(dy, x, w, mean, rstd, dx, dw, db, False, ws) == 0
+        return [dx] + ([dw, db] if params else [])
+    want = call(dy, x, torch.empty_like(x))
+    over_dy, over_x = dy.clone(), x.clone()
+    for got in (call(over_dy, x, over_dy), call(dy, over_x, over_x)):
+        assert all(torch.equal(p, q) for p, q in zip(got, want))
