@@ -16,6 +16,7 @@ static_assert(kF32 == LMHEAD_F32 && kBF16 == LMHEAD_BF16 && kF16 == LMHEAD_F16, 
 
 constexpr int64_t kMaxRows = (int64_t{1} << 31) - 256;
 constexpr int32_t kMaxWidth = 1 << 20;   // of a layer norm's rows
+constexpr int32_t kMaxVocab = INT32_MAX - 1024;   // columns, tails and mask words are counted in 32 bits
 
 bool known_type(int type) { return type == kF32 || type == kBF16 || type == kF16; }
 
@@ -60,7 +61,7 @@ lmhead_status check_distill(const void* logits, int type, int64_t ld, const int3
   if (T < 0 || V <= 0 || K <= 0 || !known_type(type) || ld < V || !positive(tau) ||
       !positive(teacher_tau))
     return LMHEAD_ERR_INVALID_ARG;
-  if (T >= kMaxRows || K > kMaxTeacher) return LMHEAD_ERR_UNSUPPORTED;
+  if (T >= kMaxRows || V > kMaxVocab || K > kMaxTeacher) return LMHEAD_ERR_UNSUPPORTED;
   if (T == 0) return LMHEAD_OK;
   if (!logits || !top_ids || !top_logits) return LMHEAD_ERR_INVALID_ARG;
   if (!aligned_to(logits, type)) return LMHEAD_ERR_UNSUPPORTED;
@@ -72,7 +73,7 @@ lmhead_status check_process(const ProcessLogits& a) {
   if (a.R < 0 || a.V <= 0 || !known_type(a.type) || a.ld < a.V || a.out_ld < a.V ||
       a.n_tokens < 0 || a.n_bias < 0 || a.M < 0)
     return LMHEAD_ERR_INVALID_ARG;
-  if (a.R >= kMaxRows) return LMHEAD_ERR_UNSUPPORTED;
+  if (a.R >= kMaxRows || a.V > kMaxVocab) return LMHEAD_ERR_UNSUPPORTED;
   if (a.R == 0) return LMHEAD_OK;
   if (!a.logits || !a.out) return LMHEAD_ERR_INVALID_ARG;
   // an empty list may have no address

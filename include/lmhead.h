@@ -413,6 +413,7 @@ int lmhead_distill_narrow_dweight(int64_t T, int32_t H, int32_t V, int32_t chunk
  * loss; non-finite logits get a zero cotangent.  HBM-bound: one read of the
  * logits; one read and one write backward.  A pointer that is not aligned to
  * its element returns LMHEAD_ERR_UNSUPPORTED; any other alignment works.
+ * T >= 2^31 - 256 and V >= 2^31 - 1024 return it too.
  */
 lmhead_status lmhead_distill_logits_fwd(const void* logits, int type, int64_t ld,
                                         const int32_t* top_ids, const float* top_logits,
@@ -501,7 +502,7 @@ lmhead_status lmhead_layernorm_bwd(const void* dy, int dy_type, int64_t dy_ld, c
  *              * grad_out : 0
  * d_logits may be grad_out itself, with the same ld (another: LMHEAD_ERR_INVALID_ARG).
  * Masked logits have no effect, whatever they are, nor, in the backward, logits of ids
- * never met.
+ * never met.  R >= 2^31 - 256 or V >= 2^31 - 1024 returns LMHEAD_ERR_UNSUPPORTED.
  */
 lmhead_status lmhead_process_logits_fwd(const void* logits, int type, int64_t ld, int64_t R,
                                         int32_t V, const int32_t* tokens, int64_t n_tokens,
