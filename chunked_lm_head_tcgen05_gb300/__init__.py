@@ -614,7 +614,7 @@ def lmhead_distill_logits_bwd(logits, top_ids, top_logits, teacher_lse, loss_mas
                  d_logits.data_ptr(), d_ld)
 
 
-@functools.lru_cache(maxsize=None)
+@functools.lru_cache(maxsize=128)   # a model has few sizes; packed rows have one per length
 def lmhead_layernorm_workspace_size(N, H):
     return int(library().lmhead_layernorm_workspace_size(N, H))
 

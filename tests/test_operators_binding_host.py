@@ -21,3 +21,13 @@ def test_results_keep_a_padded_tables_layout():
     for pad in (0, 1, 64, 256):
         logits = torch.empty(7, 1000 + pad, dtype=torch.bfloat16)[:, :1000]
         assert lm._rows_like(logits).stride() == logits.stride()
+
+
+def test_workspace_sizes_are_not_remembered_without_end():
+    """A trainer with packed rows asks for another length every step."""
+    lm.build()
+    ask = lm.lmhead_layernorm_workspace_size
+    want = [ask(n, 64) for n in range(1, 3001)]
+    kept = ask.cache_info().currsize if hasattr(ask, "cache_info") else 0
+    assert kept <= 256
+    assert want == [ask(n, 64) for n in range(1, 3001)]
