@@ -112,7 +112,8 @@ __device__ __forceinline__ void fold(float& m, float2& s, const float2 (&x)[N], 
 
 // A cluster of CTAs per row (one CTA when there are rows enough), each with a
 // range of its columns; ranks above 0 hand their maximum and sum to rank 0 in
-// distributed shared memory.  Packs come through a ring of asynchronous copies in
+// distributed shared memory.  Only single CTAs take further rows: a cluster has one
+// (see the launch), so nothing guards the handed values against a next row's.  Packs come through a ring of asynchronous copies in
 // shared memory.  Warp 0 of rank 0 forms the teacher's side while its first
 // packs arrive, and the loss at the end.
 // HBM-bound: 512 x 151936 fp32 55 us (5.6 TB/s), 2048 x 151936 bf16 6.1 TB/s.  Packs
@@ -122,7 +123,7 @@ template <typename T>
 __global__ void __launch_bounds__(kFwdThreads) logits_fwd_kernel(DistillLogits a) {
   extern __shared__ __align__(16) float teacher[];   // ring of packs; p, log p, logits [K]
   __shared__ float red[2][kFwdThreads / 32];
-  __shared__ float joined[2][2 * kMaxCluster];       // by row parity: maxima, sums
+  __shared__ float joined[2 * kMaxCluster];          // maxima, sums
   uint32_t size;
   asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(size));
   if (size > 1) cluster_sync();   // every CTA runs before one writes to rank 0's memory
@@ -140,8 +141,7 @@ __global__ void __launch_bounds__(kFwdThreads) logits_fwd_kernel(DistillLogits a
   float* const logp = p + K;
   float* const at_id = logp + K;
   const float c = kLog2e / a.tau;
-  int flip = 0;
-  for (int64_t t = blockIdx.x / size; t < a.T; t += gridDim.x / size, flip ^= 1) {
+  for (int64_t t = blockIdx.x / size; t < a.T; t += gridDim.x / size) {
     if (a.mask && !a.mask[t]) {
       if (rank == 0 && threadIdx.x == 0) {
         a.loss[t] = 0.f;
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kFwdThreads) logits_fwd_kernel(DistillLogits a
       const float base = M == -INFINITY ? 0.f : M;
       S = warp_sum(have ? red[1][lane] * ex2_approx((mw - base) * c) : 0.f);
       if (size > 1 && lane == 0) {
-        const uint32_t to = map_to_cta(smem_addr(&joined[flip][rank]), 0);
+        const uint32_t to = map_to_cta(smem_addr(&joined[rank]), 0);
         st_shared_remote(to, __float_as_int(M));
         st_shared_remote(to + 4 * kMaxCluster, __float_as_int(S));
       }
@@ -236,10 +236,10 @@ __global__ void __launch_bounds__(kFwdThreads) logits_fwd_kernel(DistillLogits a
     if (!lead) continue;
     if (size > 1) {
       const bool have = lane < size;
-      const float mw = have ? joined[flip][lane] : -INFINITY;
+      const float mw = have ? joined[lane] : -INFINITY;
       M = warp_max(mw);
       const float base = M == -INFINITY ? 0.f : M;
-      S = warp_sum(have ? joined[flip][kMaxCluster + lane] * ex2_approx((mw - base) * c) : 0.f);
+      S = warp_sum(have ? joined[kMaxCluster + lane] * ex2_approx((mw - base) * c) : 0.f);
     }
     // loss relative to the maximum, so that large logits do not cancel
     const float ln_s = logf(S);
@@ -617,6 +617,7 @@ cudaError_t logits_fwd(const DistillLogits& a, cudaStream_t s) {
     size *= 2;
   int threads = kFwdThreads;
   while (threads > 64 && packs / size < threads * kFwdDepth) threads /= 2;
+  // every row a CTA or cluster of its own, up to far more rows than are ever split
   const int64_t rows = a.T < (1 << 20) ? a.T : (1 << 20);
   return launch_dependent(logits_fwd_kernel<T>, dim3(static_cast<unsigned>(rows * size)), threads,
                           16 * static_cast<size_t>(kFwdDepth) * threads + 3 * sizeof(float) * a.teacher.K,
