@@ -1063,7 +1063,36 @@ def run_ours(args, rank, world, local):
         line["workloads"] = wl
     clocks.stop()
     if rank == 0:
-        print(json.dumps(line), flush=True)
+        print("full record:", json.dumps(line), file=sys.stderr, flush=True)
+        print(json.dumps(short_line(line), separators=(",", ":")), flush=True)
+
+
+# What each configuration's entry keeps on standard output (None: all of it).
+WORKLOAD_KEYS = {
+    "ms_per_step": None, "tokens_per_s": None, "tflops_counted": None, "frac_peak_counted": None,
+    "peak_kind": None, "tokens_per_s_per_mhz": None, "fwd": ("ms",),
+    "single_call_fwd_bwd": ("strategy", "ms_per_step"),
+    "roofline": ("kernel", "achieved", "peak", "frac"),
+    "clocks": ("sm_mhz", "reasons"),
+    "oracle": ("value", "cores", "kind", "scaled", "parity_on_sample"),
+}
+
+
+def short_line(line):
+    """The line as printed: without notes, and each configuration's entry without its details.
+    The full record is about 20 KB, more than a reader that keeps the end of a log gets whole;
+    it goes to standard error."""
+    def bare(v):
+        if not isinstance(v, dict):
+            return v
+        return {k: bare(x) for k, x in v.items() if not k.endswith("note")}
+    out = bare(line)
+    for name, w in out.get("workloads", {}).items():
+        out["workloads"][name] = {
+            k: w[k] if inner is None or not isinstance(w[k], dict)
+            else {i: w[k][i] for i in inner if i in w[k]}
+            for k, inner in WORKLOAD_KEYS.items() if k in w}
+    return out
 
 
 def run_score_logits(args, rank, world, local):
