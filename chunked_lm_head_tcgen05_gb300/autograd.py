@@ -19,7 +19,6 @@ fp32 (``accumulate_dweight = 1``) instead; ``weight.grad`` is then left
 untouched, as in trainers that keep fp32 main gradients beside bf16
 parameters.
 """
-import contextlib
 import functools
 
 import torch
@@ -45,30 +44,47 @@ def _workspace(T, H, V, chunk_size, device):
     return _stream_workspace(n, device)
 
 
-@contextlib.contextmanager
-def _stream_workspace(n, device):
-    """The current stream's workspace, for the time a call enqueues its work.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_handle(device):
+    """The current stream's, without a Stream object around it where torch can say it so."""
+    if _raw_stream is not None:
+        return _raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+class _stream_workspace:
+    """The current stream's workspace (at least n bytes), for the time a call enqueues its work.
 
     It leaves the cache meanwhile: a call is several launches that pass data through
     its workspace, and another thread's call on the same stream could come between
     them.  A call under graph capture gets memory of the graph's own pool, since
     replays go on using it."""
-    if torch.cuda.is_current_stream_capturing():
-        yield torch.empty(n, dtype=torch.uint8, device=device)
-        return
-    key = (device.index, torch.cuda.current_stream(device).cuda_stream)
-    buf = _workspaces.pop(key, None)
-    if buf is None or buf.numel() < n:
-        # A smaller buffer replaced here may still be read by work queued on this
-        # stream; torch's caching allocator gives its memory only to later work on
-        # the same stream, so dropping the reference is safe.
-        buf = torch.empty(n, dtype=torch.uint8, device=device)
-    try:
-        yield buf
-    finally:
-        kept = _workspaces.setdefault(key, buf)
-        if kept.numel() < buf.numel():   # another thread's, a smaller one, came back first
-            _workspaces[key] = buf
+
+    __slots__ = "key", "buf"
+
+    def __init__(self, n, device):
+        if torch.cuda.is_current_stream_capturing():
+            self.key, buf = None, None
+        else:
+            self.key = (device.index, _stream_handle(device))
+            buf = _workspaces.pop(self.key, None)
+        if buf is None or buf.numel() < n:
+            # A smaller buffer replaced here may still be read by work queued on this
+            # stream; torch's caching allocator gives its memory only to later work on
+            # the same stream, so dropping the reference is safe.
+            buf = torch.empty(n, dtype=torch.uint8, device=device)
+        self.buf = buf
+
+    def __enter__(self):
+        return self.buf
+
+    def __exit__(self, *error):
+        if self.key is not None:
+            kept = _workspaces.setdefault(self.key, self.buf)
+            if kept is not self.buf and kept.numel() < self.buf.numel():
+                _workspaces[self.key] = self.buf   # another thread's, a smaller one, came first
 
 
 def release_workspaces():

@@ -85,7 +85,7 @@ class Meeting:
 def cached(monkeypatch):
     """The workspace cache without a GPU: every call is on one stream, capturing as told."""
     state = SimpleNamespace(capturing=False)
-    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: SimpleNamespace(cuda_stream=7))
+    monkeypatch.setattr(autograd, "_stream_handle", lambda device: 7)
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: state.capturing)
     monkeypatch.setattr(autograd, "lmhead_layernorm_workspace_size", lambda n, h: 64 * n)
     monkeypatch.setattr(autograd, "layernorm_forward",
