@@ -3,7 +3,7 @@
 //   y = xh w + b
 //   dx = r (h - mean(h) - xh mean(h xh)),  h = dy w
 //   dw = sum over rows of dy xh,  db = sum over rows of dy
-// All sums are fp32; the variance is the mean square of x - mu (never
+// All sums and statistics are fp32; the variance is the mean square of x - mu (never
 // mean(x^2) - mu^2, which cancels when |mu| is large).  Column sums go through
 // per-CTA partial rows that are added in a fixed order (no atomics: the same
 // inputs give the same bits).
@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(kStreamThreads)
     const float mu = fmaf(e1, inv_H, ref);
     float var = fmaf(-e1 * inv_H, e1, e2) * inv_H;
     var = var < 0.f ? 0.f : var;   // rounding, where a row has no spread
-    const float r = rsqrtf(var + eps);
+    const float r = rsqrtf(var + eps);   // 2 units of the last place off at most; one value per row
     const float2 minus_mu = make_float2(-mu, -mu), r2 = make_float2(r, r);
     Y* out = y + t * y_ld + i * VEC;
 #pragma unroll
@@ -379,8 +379,8 @@ __global__ void __launch_bounds__(kStreamThreads)
 // Both gradients in one pass over x and dy.  A group of g threads (a multiple of
 // 32) owns a row at a time and its threads fixed columns, so dw and db gather in
 // registers over the group's rows; dx may be x or dy (each thread writes what it alone
-// has read).  The CTA's groups are joined in shared memory
-// at the end, and the CTA writes one partial row.  Rows of more than `cols` columns
+// has read).  The CTA's groups are joined in shared memory at the end, and the CTA writes
+// one partial row.  Rows of more than `cols` columns
 // go in blocks of that many (blockIdx.y), their two sums having been formed before
 // (`sums`); narrower ones in one block that forms them itself.  Rows arrive through a ring of
 // asynchronous copies kDepth rows deep (kDepth = 0: units too small for such

@@ -371,7 +371,9 @@ enum { LMHEAD_F32 = 0, LMHEAD_BF16 = 1, LMHEAD_F16 = 2 };
  *  workspace  lmhead_distill_workspace_size(LMHEAD_OP_FWD or LMHEAD_OP_BWD, ...)
  * The forward's GEMM keeps the K logits of each row as it passes their columns;
  * the backward forms the dense part of the cotangent in the recompute GEMM's
- * epilogue and replaces it at the K ids before both gradient contractions read it.
+ * epilogue and replaces it at the K ids before both gradient contractions read it
+ * (as bf16, like the log-prob backward's).  weight is the whole table: there is no
+ * form over a vocabulary shard.
  */
 size_t lmhead_distill_workspace_size(int op, int64_t T, int32_t H, int32_t V, int32_t K,
                                      int32_t chunk_size);
