@@ -35,6 +35,8 @@ __all__ = [
     "lmhead_process_logits_fwd", "lmhead_process_logits_bwd",
     "distill_forward", "distill_backward", "distill_logits_forward", "distill_logits_backward",
     "layernorm_forward", "layernorm_backward", "process_logits", "process_logits_backward",
+    "NO_PADDING", "lmhead_embedding_workspace_size", "lmhead_embedding_fwd",
+    "lmhead_embedding_bwd", "embedding_forward", "embedding_backward",
 ]
 
 LMHEAD_OP_FWD = 0
@@ -46,6 +48,7 @@ LMHEAD_STRATEGY_KEEP_LOGITS = 2
 LMHEAD_F32 = 0
 LMHEAD_BF16 = 1
 LMHEAD_F16 = 2
+NO_PADDING = -2 ** 31   # LMHEAD_NO_PADDING
 NOALLOC_SCRATCH_BYTES = 64 << 20   # LMHEAD_NOALLOC_SCRATCH_BYTES in include/lmhead.h
 STATUS_NAMES = {
     0: "LMHEAD_OK", 1: "LMHEAD_ERR_INVALID_ARG", 2: "LMHEAD_ERR_UNSUPPORTED",
@@ -126,6 +129,12 @@ _SIGNATURES = {
     "lmhead_process_logits_bwd": (ctypes.c_int, [_VP, _I64, _VP, ctypes.c_int, _I64, _I64, _I32,
                                                  _VP, _I64, _VP, _VP, _VP, _I64, _VP, _VP, _I64,
                                                  _VP]),
+    "lmhead_embedding_workspace_size": (_SZ, [_I64, _I32]),
+    "lmhead_embedding_fwd": (ctypes.c_int, [_VP, _I64, _VP, ctypes.c_int, _I64, _I32, _I32,
+                                            ctypes.c_float, _VP, ctypes.c_int, _I64, _VP]),
+    "lmhead_embedding_bwd": (ctypes.c_int, [_VP, ctypes.c_int, _I64, _VP, _I64, _I32, _I32,
+                                            ctypes.c_float, _I32, _VP, ctypes.c_int, ctypes.c_int,
+                                            _VP, _SZ, _VP]),
 }
 
 
@@ -752,6 +761,53 @@ def lmhead_process_logits_bwd(grad_out, logits, tokens, spans, repetition, allow
                  d_logits.data_ptr(), d_ld)
 
 
+def lmhead_embedding_workspace_size(N, H):
+    return int(library().lmhead_embedding_workspace_size(N, H))
+
+
+def _check_ids(ids):
+    if _torch is None:
+        _bind_torch()
+    if ids is None or ids.dim() != 1:
+        raise ValueError("ids must be a list of token ids [N]")
+    _check_tensor(ids, "ids", _torch.int32, ids.shape)
+    return ids.shape[0]
+
+
+def _embedding_types(dtype):
+    """What a table of this type can give."""
+    f32, bf16 = _torch.float32, _torch.bfloat16
+    return (f32, bf16) if dtype is f32 else (dtype, f32)
+
+
+def lmhead_embedding_fwd(ids, weight, scale, y, stream=None):
+    """C ``lmhead_embedding_fwd`` on torch tensors; returns the status code."""
+    N = _check_ids(ids)
+    V, H = weight.shape
+    kind, w_ld = _check_rows(weight, "weight", (V, H))
+    y_type, y_ld = _check_rows(y, "y", (N, H), _embedding_types(weight.dtype))
+    dev = _one_device(weight, ids, y)
+    return _call(library().lmhead_embedding_fwd, dev, stream, ids.data_ptr(), N, weight.data_ptr(),
+                 kind, w_ld, V, H, scale, y.data_ptr(), y_type, y_ld)
+
+
+def lmhead_embedding_bwd(dy, ids, scale, padding_id, d_weight, accumulate, workspace, stream=None):
+    """C ``lmhead_embedding_bwd`` on torch tensors (padding_id None: no padding); returns the
+    status code."""
+    N = _check_ids(ids)
+    V, H = d_weight.shape
+    kind, ld = _check_rows(dy, "dy", (N, H))
+    torch = _torch
+    narrow = d_weight.dtype is torch.bfloat16
+    _check_tensor(d_weight, "d_weight", torch.bfloat16 if narrow else torch.float32, (V, H))
+    _check_workspace(workspace)
+    dev = _one_device(dy, ids, d_weight, workspace)
+    return _call(library().lmhead_embedding_bwd, dev, stream, dy.data_ptr(), kind, ld,
+                 ids.data_ptr(), N, V, H, scale, NO_PADDING if padding_id is None else padding_id,
+                 d_weight.data_ptr(), LMHEAD_BF16 if narrow else LMHEAD_F32,
+                 1 if accumulate else 0, workspace.data_ptr(), workspace.nbytes)
+
+
 def lmhead_selftest_bounded_wait(workspace, limit_ms, stream=None):
     """C ``lmhead_selftest_bounded_wait``; returns the status code of the launch."""
     _check_workspace(workspace)
@@ -1053,3 +1109,46 @@ def process_logits_backward(grad_out, logits, tokens=None, spans=None, repetitio
     if rc:
         raise LmheadError(rc, "lmhead_process_logits_bwd")
     return d_logits
+
+
+def embedding_forward(ids, weight, scale=1.0, out_dtype=None, out=None, stream=None):
+    """scale * weight[ids] for ids [N] int32 and weight [V, H]; returns [N, H] of the table's type
+    or out_dtype (bf16 for an fp32 table, fp32 for a 16-bit one)."""
+    if stream is not None:
+        return _made_on(stream, weight, embedding_forward, ids, weight, scale, out_dtype, out)
+    if out is None:
+        if _torch is None:
+            _bind_torch()
+        out = _torch.empty((ids.shape[0], weight.shape[1]), device=weight.device,
+                           dtype=weight.dtype if out_dtype is None else out_dtype)
+    rc = lmhead_embedding_fwd(ids, weight, scale, out)
+    if rc:
+        raise LmheadError(rc, "lmhead_embedding_fwd")
+    return out
+
+
+def embedding_backward(dy, ids, vocab, scale=1.0, padding_id=None, dtype=None, d_weight=None,
+                       accumulate=False, workspace=None, stream=None):
+    """Gradient [vocab, H] of the table: fp32, or bf16 with dtype.  ``d_weight`` is overwritten, or
+    added to with ``accumulate`` (fp32)."""
+    if stream is not None:
+        return _made_on(stream, dy, embedding_backward, dy, ids, vocab, scale, padding_id, dtype,
+                        d_weight, accumulate, workspace)
+    if _torch is None:
+        _bind_torch()
+    torch = _torch
+    N, H = dy.shape
+    if d_weight is None:
+        make = torch.zeros if accumulate else torch.empty
+        d_weight = make((vocab, H), dtype=torch.float32 if dtype is None else dtype,
+                        device=dy.device)
+    elif d_weight.shape[0] != vocab or dtype not in (None, d_weight.dtype):
+        raise ValueError("d_weight is %s %s, expected %d rows of %s"
+                         % (d_weight.dtype, tuple(d_weight.shape), vocab, dtype))
+    if workspace is None:
+        workspace = torch.empty(lmhead_embedding_workspace_size(N, H), dtype=torch.uint8,
+                                device=dy.device)
+    rc = lmhead_embedding_bwd(dy, ids, scale, padding_id, d_weight, accumulate, workspace)
+    if rc:
+        raise LmheadError(rc, "lmhead_embedding_bwd")
+    return d_weight

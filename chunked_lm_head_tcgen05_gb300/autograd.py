@@ -24,8 +24,10 @@ import functools
 import torch
 
 from . import LMHEAD_OP_BWD, LMHEAD_OP_FWD, LmheadError, distill_logits_backward, \
-    distill_logits_forward, layernorm_backward, layernorm_forward, lmhead_distill_bwd, \
+    distill_logits_forward, embedding_backward, embedding_forward, layernorm_backward, \
+    layernorm_forward, lmhead_distill_bwd, \
     lmhead_distill_narrow_dweight, lmhead_distill_fwd, lmhead_distill_workspace_size, \
+    lmhead_embedding_workspace_size, \
     lmhead_layernorm_workspace_size, \
     lmhead_logps_bwd, lmhead_logps_fwd, lmhead_workspace_size, process_logits_backward
 from . import process_logits as _process_logits
@@ -360,3 +362,42 @@ def process_logits(logits, **rules):
     if unknown:
         raise TypeError("process_logits takes no %s here" % ", ".join(unknown))
     return ProcessLogits.apply(logits, rules)
+
+
+class Embedding(torch.autograd.Function):
+    """(ids [N] int32, weight [V,H], scale, padding_id, out_dtype, main_grad) -> y [N,H]."""
+
+    @staticmethod
+    def forward(ctx, ids, weight, scale, padding_id, out_dtype, main_grad):
+        ctx.save_for_backward(ids)
+        ctx.table = weight.shape, weight.dtype
+        ctx.scale, ctx.padding_id, ctx.main_grad = scale, padding_id, main_grad
+        return embedding_forward(ids, weight, scale, out_dtype)
+
+    @staticmethod
+    @_differentiable_once
+    def backward(ctx, dy):
+        if not ctx.needs_input_grad[1]:
+            return (None,) * 6
+        ids, = ctx.saved_tensors
+        (V, H), dtype = ctx.table
+        main = ctx.main_grad
+        if dy.stride(1) != 1 or (dy.shape[0] > 1 and dy.stride(0) < H):
+            dy = dy.contiguous()
+        # autograd hands the table its own type: bf16 at once where the library can
+        kind = torch.bfloat16 if dtype is torch.bfloat16 and dy.shape[0] <= _SORT_MOST \
+            else torch.float32
+        with _stream_workspace(lmhead_embedding_workspace_size(*dy.shape), dy.device) as ws:
+            d = embedding_backward(dy, ids, V, ctx.scale, ctx.padding_id,
+                                   kind if main is None else None, main, main is not None, ws)
+        return (None, d if main is None else None, *(None,) * 4)
+
+
+_SORT_MOST = 131072   # tokens whose gradient can be written in bf16 (lmhead_embedding_bwd)
+
+
+def embedding(ids, weight, scale=1.0, padding_id=None, out_dtype=None, main_grad=None):
+    """scale * weight[ids], differentiable in the table; tokens with padding_id give no gradient.
+    main_grad as in ``lmhead_logps``: a table tied to the head gets both gradients in it."""
+    return Embedding.apply(ids, weight, float(scale), padding_id, out_dtype,
+                           _main_grad(weight, main_grad))

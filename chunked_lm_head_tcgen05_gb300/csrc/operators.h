@@ -149,4 +149,48 @@ struct ProcessLogits {
 
 cudaError_t launch_process_logits(const ProcessLogits& a, cudaStream_t s);
 
+// ------------------------------------------------------------------ ids in order
+// Most ids of one sort.
+constexpr int kSortMost = 131072;
+// Stable sort of n <= kSortMost ids: keys ascending, pos their places in `ids`.  Ids
+// outside [0, bound) and `skip` (-1: none) count as `bound` and come last; with `wrap`,
+// ids in [-bound, 0) first become id + bound.  *live: how many are inside.
+cudaError_t launch_sort_ids(const int32_t* ids, int n, int bound, bool wrap, int skip, int32_t* keys,
+                            int32_t* pos, int* live, cudaStream_t s);
+
+// ------------------------------------------------------------------ embedding
+struct EmbedFwd {
+  const int32_t* ids;    // [N]
+  int64_t N;
+  const void* weight;    // [V, H]
+  int type;
+  int64_t w_ld;
+  int V;
+  int H;
+  float scale;
+  void* y;               // [N, H]
+  int y_type;
+  int64_t y_ld;
+};
+
+struct EmbedBwd {
+  const void* dy;        // [N, H]
+  int dy_type;
+  int64_t dy_ld;
+  const int32_t* ids;    // [N]
+  int64_t N;
+  int V;
+  int H;
+  float scale;
+  int skip;              // wrapped padding id, or -1
+  void* d_weight;        // [V, H]
+  int d_type;            // fp32, or bf16 without accumulate and N <= kSortMost
+  int accumulate;
+  void* workspace;       // embed_workspace(N, H) bytes
+};
+
+size_t embed_workspace(int64_t N, int H);
+cudaError_t launch_embed_fwd(const EmbedFwd& a, cudaStream_t s);
+cudaError_t launch_embed_bwd(const EmbedBwd& a, cudaStream_t s);
+
 }  // namespace lmh

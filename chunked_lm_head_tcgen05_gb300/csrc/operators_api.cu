@@ -1,5 +1,5 @@
-// Host side of the C ABI of layer norm, distillation on held logits and logit
-// processing: argument checks and the stream-ordered launches.  No device
+// Host side of the C ABI of layer norm, distillation on held logits, logit
+// processing and embedding: argument checks and the stream-ordered launches.  No device
 // memory is allocated and nothing synchronises.
 #include "lmhead.h"
 
@@ -86,6 +86,16 @@ lmhead_status check_process(const ProcessLogits& a) {
   if (a.allowed && !a.allowed_rows && a.M < a.R) return LMHEAD_ERR_INVALID_ARG;
   if (!aligned_to(a.logits, a.type) || !aligned_to(a.out, a.type)) return LMHEAD_ERR_UNSUPPORTED;
   if (clash(a.logits, a.ld, a.out, a.out_ld, a.R)) return LMHEAD_ERR_INVALID_ARG;
+  return LMHEAD_OK;
+}
+
+// Arguments that both directions of the embedding share; `in` and `out` are its matrices.
+lmhead_status check_embedding(int64_t N, int32_t V, int32_t H, float scale, int in_type, int64_t in_ld,
+                              int out_type, int64_t out_ld) {
+  if (N < 0 || V <= 0 || H <= 0 || !known_type(in_type) || !known_type(out_type) || in_ld < H || out_ld < H ||
+      !std::isfinite(scale))
+    return LMHEAD_ERR_INVALID_ARG;
+  if (N >= kMaxRows || V > kMaxVocab || H > kMaxWidth) return LMHEAD_ERR_UNSUPPORTED;
   return LMHEAD_OK;
 }
 
@@ -249,6 +259,55 @@ lmhead_status lmhead_process_logits_bwd(const void* grad_out, int64_t grad_ld, c
   if (clash(grad_out, grad_ld, d_logits, d_ld, R)) return LMHEAD_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return status_of(traced_launch("process_logits_bwd", s, [&] { return launch_process_logits(a, s); }));
+}
+
+size_t lmhead_embedding_workspace_size(int64_t N, int32_t H) {
+  return N < 0 || N >= kMaxRows || H <= 0 || H > kMaxWidth ? 0 : embed_workspace(N, H);
+}
+
+lmhead_status lmhead_embedding_fwd(const int32_t* ids, int64_t N, const void* weight, int type,
+                                   int64_t w_ld, int32_t V, int32_t H, float scale, void* y,
+                                   int y_type, int64_t y_ld, lmhead_stream_t stream) {
+  const lmhead_status rc = check_embedding(N, V, H, scale, type, w_ld, y_type, y_ld);
+  if (rc != LMHEAD_OK) return rc;
+  if (y_type != type && !(type == kF32 && y_type == kBF16) && y_type != kF32) return LMHEAD_ERR_UNSUPPORTED;
+  if (N == 0) return LMHEAD_OK;
+  if (!ids || !weight || !y || weight == y) return LMHEAD_ERR_INVALID_ARG;
+  if (!aligned_to(weight, type) || !aligned_to(y, y_type) || !aligned_to(ids, kF32)) return LMHEAD_ERR_UNSUPPORTED;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const EmbedFwd a{ids, N, weight, type, w_ld, V, H, scale, y, y_type, y_ld};
+  return status_of(traced_launch("embedding_fwd", s, [&] { return launch_embed_fwd(a, s); }));
+}
+
+lmhead_status lmhead_embedding_bwd(const void* dy, int dy_type, int64_t dy_ld, const int32_t* ids,
+                                   int64_t N, int32_t V, int32_t H, float scale,
+                                   int32_t padding_id, void* d_weight, int d_weight_type,
+                                   int accumulate, void* workspace, size_t workspace_bytes,
+                                   lmhead_stream_t stream) {
+  const lmhead_status rc = check_embedding(N, V, H, scale, dy_type, dy_ld, d_weight_type, H);
+  if (rc != LMHEAD_OK) return rc;
+  int skip = -1;
+  if (padding_id != LMHEAD_NO_PADDING) {
+    if (padding_id < -V || padding_id >= V) return LMHEAD_ERR_INVALID_ARG;
+    skip = padding_id < 0 ? padding_id + V : padding_id;
+  }
+  if (d_weight_type != kF32 && (d_weight_type != kBF16 || accumulate || N > kSortMost))
+    return LMHEAD_ERR_UNSUPPORTED;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (N == 0 && accumulate) return LMHEAD_OK;
+  if (!d_weight) return LMHEAD_ERR_INVALID_ARG;
+  if (!aligned_to(d_weight, d_weight_type)) return LMHEAD_ERR_UNSUPPORTED;
+  if (N == 0) {
+    const size_t bytes = element_bytes(d_weight_type) * static_cast<size_t>(V) * static_cast<size_t>(H);
+    return status_of(cudaMemsetAsync(d_weight, 0, bytes, s));
+  }
+  if (!dy || !ids || !workspace || dy == d_weight) return LMHEAD_ERR_INVALID_ARG;
+  if (!aligned_to(dy, dy_type) || !aligned_to(ids, kF32) || (reinterpret_cast<uintptr_t>(workspace) & 255))
+    return LMHEAD_ERR_UNSUPPORTED;
+  if (workspace_bytes < embed_workspace(N, H)) return LMHEAD_ERR_WORKSPACE_TOO_SMALL;
+  const EmbedBwd a{dy, dy_type, dy_ld, ids, N, V, H, scale, skip, d_weight, d_weight_type,
+                   accumulate ? 1 : 0, workspace};
+  return status_of(launch_embed_bwd(a, s));
 }
 
 }  // extern "C"

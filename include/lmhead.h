@@ -525,6 +525,44 @@ lmhead_status lmhead_process_logits_bwd(const void* grad_out, int64_t grad_ld, c
                                         lmhead_stream_t stream);
 
 /*
+ * Embedding: rows of the vocabulary table by token id, scaled (the table read at the
+ * model's other end), and their gradient.
+ *   y_t = scale weight[id_t]
+ *   d_weight_v (+)= scale sum_{t : id_t = v} dy_t
+ *  ids           [N] int32; ids in [-V, 0) wrap to id + V.  An id outside [-V, V) gives a
+ *                row of NaN and takes no part in the gradient.
+ *  weight        [V, H] of `type`, rows w_ld elements apart
+ *  y             [N, H], rows y_ld apart: of the table's type, or bf16 for an fp32 table,
+ *                or fp32 for a 16-bit one (an fp32 residual stream); not over weight
+ *  scale         finite; products are formed in fp32 and rounded once
+ *  dy            [N, H] of dy_type, rows dy_ld apart
+ *  padding_id    tokens with this id (after wrapping) take no part in the gradient;
+ *                LMHEAD_NO_PADDING: none.  The forward does not look at it.
+ *  d_weight      [V, H] of d_weight_type: LMHEAD_F32, overwritten (ids that do not occur
+ *                get zeros) or added to when accumulate != 0 -- for instance the buffer
+ *                that lmhead_logps_bwd accumulates into, where the table is tied; or
+ *                LMHEAD_BF16, each sum rounded once, without accumulate and for
+ *                N <= 131072 (LMHEAD_ERR_UNSUPPORTED otherwise)
+ *  workspace     lmhead_embedding_workspace_size(N, H) bytes, 256-byte aligned
+ * The gradient sums an id's tokens in fp32 in a fixed order: same inputs, same bits.
+ * H <= 2^20, N < 2^31 - 256 and V < 2^31 - 1024 (LMHEAD_ERR_UNSUPPORTED beyond).
+ * N == 0 is a no-op (the backward still zeroes d_weight unless accumulate is set).
+ */
+#define LMHEAD_NO_PADDING INT32_MIN
+
+size_t lmhead_embedding_workspace_size(int64_t N, int32_t H);
+
+lmhead_status lmhead_embedding_fwd(const int32_t* ids, int64_t N, const void* weight, int type,
+                                   int64_t w_ld, int32_t V, int32_t H, float scale, void* y,
+                                   int y_type, int64_t y_ld, lmhead_stream_t stream);
+
+lmhead_status lmhead_embedding_bwd(const void* dy, int dy_type, int64_t dy_ld, const int32_t* ids,
+                                   int64_t N, int32_t V, int32_t H, float scale,
+                                   int32_t padding_id, void* d_weight, int d_weight_type,
+                                   int accumulate, void* workspace, size_t workspace_bytes,
+                                   lmhead_stream_t stream);
+
+/*
  * Self-test of failure detection (the pages have no counterpart; the
  * kernels need it on shared GPUs): launches one CTA that allocates tensor
  * memory and waits, with the same bounded mbarrier wait every GEMM pipeline
