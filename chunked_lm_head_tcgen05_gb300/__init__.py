@@ -37,6 +37,8 @@ __all__ = [
     "layernorm_forward", "layernorm_backward", "process_logits", "process_logits_backward",
     "NO_PADDING", "lmhead_embedding_workspace_size", "lmhead_embedding_fwd",
     "lmhead_embedding_bwd", "embedding_forward", "embedding_backward",
+    "lmhead_beam_workspace_size", "lmhead_beam_select", "lmhead_beam_reorder", "beam_select",
+    "beam_reorder",
 ]
 
 LMHEAD_OP_FWD = 0
@@ -135,6 +137,12 @@ _SIGNATURES = {
     "lmhead_embedding_bwd": (ctypes.c_int, [_VP, ctypes.c_int, _I64, _VP, _I64, _I32, _I32,
                                             ctypes.c_float, _I32, _VP, ctypes.c_int, ctypes.c_int,
                                             _VP, _SZ, _VP]),
+    "lmhead_beam_workspace_size": (_SZ, [_I64, _I32, _I32]),
+    "lmhead_beam_select": (ctypes.c_int, [_VP, ctypes.c_int, _I64, _I64, _I32, _I32, _I32, _VP, _VP,
+                                          _I32, ctypes.c_float, _VP, _VP, _VP, _VP, _VP, _VP, _SZ,
+                                          _VP]),
+    "lmhead_beam_reorder": (ctypes.c_int, [_VP, _I64, _I64, _I64, _I64, _VP, _I64, _I64, _I64, _VP,
+                                           _I64, _I32, _I64, _I64, _I64, ctypes.c_int, _VP]),
 }
 
 
@@ -808,6 +816,97 @@ def lmhead_embedding_bwd(dy, ids, scale, padding_id, d_weight, accumulate, works
                  1 if accumulate else 0, workspace.data_ptr(), workspace.nbytes)
 
 
+def lmhead_beam_workspace_size(R, V, take):
+    return int(library().lmhead_beam_workspace_size(R, V, take))
+
+
+def lmhead_beam_select(logits, beams, take, scores, finished, eos_id, temperature, out_scores,
+                       parents, tokens, next_finished, lse, workspace, stream=None):
+    """C ``lmhead_beam_select`` on torch tensors; returns the status code."""
+    R, V = logits.shape
+    kind, ld = _check_rows(logits, "logits", (R, V))
+    torch = _torch
+    _check_tensor(scores, "scores", torch.float32, (R,))
+    _check_tensor(finished, "finished", torch.uint8, (R,), allow_none=True)
+    if beams <= 0 or R % beams:
+        raise ValueError("logits must have the rows of whole groups of beams: got %d rows of %d "
+                         "beams" % (R, beams))
+    shape = (R // beams, take)
+    _check_tensor(out_scores, "out_scores", torch.float32, shape)
+    _check_tensor(parents, "parents", torch.int32, shape)
+    _check_tensor(tokens, "tokens", torch.int32, shape)
+    _check_tensor(next_finished, "next_finished", torch.uint8, shape, allow_none=True)
+    _check_tensor(lse, "lse", torch.float32, (R,), allow_none=True)
+    _check_workspace(workspace)
+    dev = _one_device(logits, scores, finished, out_scores, parents, tokens, next_finished, lse,
+                      workspace)
+    return _call(library().lmhead_beam_select, dev, stream, logits.data_ptr(), kind, ld, R, V,
+                 beams, take, scores.data_ptr(), _ptr(finished), eos_id, temperature,
+                 out_scores.data_ptr(), parents.data_ptr(), tokens.data_ptr(), _ptr(next_finished),
+                 _ptr(lse), workspace.data_ptr(), workspace.nbytes)
+
+
+def _state_layout(state, out, dim):
+    """(outer, mid, inner_bytes, (outer, row, mid) strides in bytes of state and of out): the
+    dimensions before `dim` as one, those behind it as one and a contiguous rest."""
+    size = state.element_size()
+    a, b = state.stride(), out.stride()
+
+    def merged(dims):
+        got = []      # [size, stride, stride], inner dimensions last
+        for i in dims:
+            n = state.shape[i]
+            if n == 1:
+                continue
+            if got and got[-1][1] == n * a[i] and got[-1][2] == n * b[i]:
+                got[-1] = [got[-1][0] * n, a[i], b[i]]
+            else:
+                got.append([n, a[i], b[i]])
+        return got
+
+    before, behind = merged(range(dim)), merged(range(dim + 1, state.dim()))
+    inner = 1
+    if behind and behind[-1][1] == 1 and behind[-1][2] == 1:
+        inner = behind.pop()[0]
+    if len(before) > 1 or len(behind) > 1:
+        raise ValueError("state must be one block of rows, repeated at most once outside `dim` and "
+                         "once inside it: got shape %s, strides %s and %s"
+                         % (tuple(state.shape), a, b))
+    outer = before[0] if before else (1, 0, 0)
+    mid = behind[0] if behind else (1, 0, 0)
+    return outer[0], mid[0], inner * size, \
+        (outer[1] * size, a[dim] * size, mid[1] * size), \
+        (outer[2] * size, b[dim] * size, mid[2] * size)
+
+
+def lmhead_beam_reorder(state, out, parents, dim, beams=0, clear_missing=False, stream=None):
+    """C ``lmhead_beam_reorder`` on torch tensors of any element type whose rows lie along `dim`;
+    in place where out is the state.  Returns the status code."""
+    if _torch is None:
+        _bind_torch()
+    if parents is None or parents.dim() != 1:
+        raise ValueError("parents must be a list of rows")
+    rows = parents.shape[0]
+    _check_tensor(parents, "parents", _torch.int32, (rows,))
+    for t, name in ((state, "state"), (out, "out")):
+        if not t.is_cuda:
+            raise ValueError("%s must be a CUDA tensor" % name)
+    if not 0 <= dim < state.dim():
+        raise ValueError("state has no dimension %d" % dim)
+    shape = state.shape[:dim] + (rows,) + state.shape[dim + 1:]
+    if out.dtype is not state.dtype:
+        raise TypeError("out must be %s, got %s" % (state.dtype, out.dtype))
+    if out.shape != shape:
+        raise ValueError("out has shape %s, expected %s" % (tuple(out.shape), tuple(shape)))
+    dev = _one_device(state, out, parents)
+    if out.numel() == 0:
+        return 0
+    outer, mid, inner, (so, sr, sm), (do, dr, dm) = _state_layout(state, out, dim)
+    return _call(library().lmhead_beam_reorder, dev, stream, state.data_ptr(), so, sr, sm,
+                 state.shape[dim], out.data_ptr(), do, dr, dm, parents.data_ptr(), rows, beams,
+                 outer, mid, inner, 1 if clear_missing else 0)
+
+
 def lmhead_selftest_bounded_wait(workspace, limit_ms, stream=None):
     """C ``lmhead_selftest_bounded_wait``; returns the status code of the launch."""
     _check_workspace(workspace)
@@ -1152,3 +1251,54 @@ def embedding_backward(dy, ids, vocab, scale=1.0, padding_id=None, dtype=None, d
     if rc:
         raise LmheadError(rc, "lmhead_embedding_bwd")
     return d_weight
+
+
+def beam_select(logits, scores, beams, take=None, temperature=1.0, finished=None, eos_id=-1,
+                next_finished=None, workspace=None, stream=None):
+    """The `take` (default: beams) best continuations of each group of `beams` rows of logits [R, V],
+    whose sequences have scores [R].  Returns (scores, parents, tokens), each [R / beams, take], and
+    lse [R]; next_finished, if given, is filled beside them."""
+    if stream is not None:
+        return _made_on(stream, logits, beam_select, logits, scores, beams, take, temperature,
+                        finished, eos_id, next_finished, workspace)
+    if _torch is None:
+        _bind_torch()
+    torch = _torch
+    R, V = logits.shape
+    take = beams if take is None else take
+    if beams <= 0 or take <= 0:
+        raise ValueError("beams and take must be positive, got %d and %d" % (beams, take))
+    where = logits.device
+    empty, shape = torch.empty, (R // beams, take)
+    out_scores = empty(shape, dtype=torch.float32, device=where)
+    parents = empty(shape, dtype=torch.int32, device=where)
+    tokens = empty(shape, dtype=torch.int32, device=where)
+    lse = empty(R, dtype=torch.float32, device=where)
+    if workspace is None:
+        workspace = empty(lmhead_beam_workspace_size(R, V, take), dtype=torch.uint8, device=where)
+    rc = lmhead_beam_select(logits, beams, take, scores, finished, eos_id, temperature, out_scores,
+                            parents, tokens, next_finished, lse, workspace)
+    if rc:
+        raise LmheadError(rc, "lmhead_beam_select")
+    return out_scores, parents, tokens, lse
+
+
+def beam_reorder(state, parents, dim=0, out=None, beams=0, stream=None):
+    """state with row parents[r] in the place of row r along `dim` (any element type); parents [rows]
+    int32.  ``out=state`` moves the rows in place, `beams` rows at a time, parents within their
+    group.  A parent of -1 leaves the row of `out` as it is; in a new tensor it is zero."""
+    if stream is not None:
+        return _made_on(stream, state, beam_reorder, state, parents, dim, out, beams)
+    if dim < 0:
+        dim += state.dim()
+    new = out is None
+    if new:
+        if _torch is None:
+            _bind_torch()
+        shape = list(state.shape)
+        shape[dim] = parents.shape[0]
+        out = _torch.empty(shape, dtype=state.dtype, device=state.device)
+    rc = lmhead_beam_reorder(state, out, parents, dim, beams, new)
+    if rc:
+        raise LmheadError(rc, "lmhead_beam_reorder")
+    return out

@@ -1,0 +1,594 @@
+// One step of beam search.  Row r = group * beams + j of the logits belongs to
+// beam j of its group, with score_r so far.  With z = x / tau,
+//   lse_r = log sum_v exp(z_v),   candidate (j, v): score_r + z_v - lse_r,
+// and a group's best `take` candidates go on, ties to the lowest j V + v.
+// HBM-bound: one read of the logits, two kernels.
+//  1. scan_kernel, one CTA per piece of a row, held in registers: maximum and
+//     exponential sum of the piece, and its best `take` logits.  At least `take`
+//     groups of threads have a largest element, so the least of these is at most
+//     the piece's take-th largest element: what is not below it (some
+//     take * ln(take) of the elements) goes to shared memory and is ranked there.
+//     When more elements qualify than fit (equal logits), the take-th largest is
+//     found by halving intervals instead.
+//  2. best_kernel, one CTA per group, joins the pieces: lse, then the candidates.
+//     An fp32 score with its error bound on either side sorts out most of them;
+//     the rest are compared in 64 bits, where fp32 could confuse two that are
+//     close (and 64-bit arithmetic for all of them would take longer than the
+//     scan: a few operations per clock and SM).
+// Order among one row's logits is by the logit itself, as an integer that grows
+// with it, then by the id.
+//
+// beam_reorder moves states to the beams that go on: row r takes over row
+// parents[r].  In place a thread holds one column of a group's rows, reads what
+// other rows need and then writes, so rows that keep their place cost nothing.
+#include "element.cuh"
+#include "operators.h"
+#include "ptx.cuh"
+
+namespace lmh {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kManyElements = 32;    // per thread, of many rows: pieces of 8,192
+constexpr int kFewElements = 8;      // of few rows: pieces of 2,048
+constexpr int64_t kManyPieces = 304; // CTAs of the long pieces that fill the GPU
+constexpr int kRoom = 1024;          // elements ranked in shared memory
+constexpr int kBestThreads = 512;
+constexpr int kBestWarps = kBestThreads / 32;
+
+// An integer that grows with x (no NaN); 0 is below every number's.
+__device__ __forceinline__ uint32_t order_of(float x) {
+  const uint32_t u = __float_as_uint(x + 0.f);   // one zero
+  return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float from_order(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+constexpr uint32_t kMinusInf = 0x007fffffu;      // order_of(-inf)
+
+// Larger logit first, then the lower id.
+__device__ __forceinline__ uint64_t entry_of(uint32_t order, int v) {
+  return static_cast<uint64_t>(order) << 32 | static_cast<uint32_t>(~v);
+}
+
+// log2(e) / tau, finite for every tau
+__device__ __forceinline__ float steps(float tau) { return fminf(1.4426950408889634f / tau, 3.0e38f); }
+
+struct Pieces {
+  float2* stats;      // [R][pieces] maximum of x, sum of exp((x - maximum) / tau)
+  uint64_t* best;     // [R][pieces][take] descending, 0 behind the last
+  int pieces;
+  int length;         // packs of a row per piece
+};
+
+// The number of `on` in the CTA.
+__device__ __forceinline__ int count_all(int on, int* scratch) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int w = __reduce_add_sync(0xffffffffu, on);
+  __syncthreads();
+  if (lane == 0) scratch[warp] = w;
+  __syncthreads();
+  int sum = 0;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) sum += scratch[i];
+  return sum;
+}
+
+template <typename T, int ELEMS>
+__global__ void __launch_bounds__(kThreads, 4) scan_kernel(BeamSelect a, Pieces z, int span) {
+  constexpr int VEC = kVec<T>, PACKS = ELEMS / VEC;
+  __shared__ uint64_t found[kRoom];
+  __shared__ uint32_t warp_max[kWarps], warp_min[kWarps];
+  __shared__ float warp_sums[kWarps];
+  __shared__ int scratch[kWarps], n_found, bad;
+  pdl_wait_prerequisites();
+  pdl_launch_dependents();
+  const int64_t r = blockIdx.x / z.pieces;
+  const int piece = static_cast<int>(blockIdx.x % z.pieces);
+  if (a.finished && a.finished[r]) return;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) n_found = 0, bad = 0;
+  // packs are counted from the 16-byte boundary at or before the row's start
+  const T* const row = static_cast<const T*>(a.logits) + r * a.ld;
+  const int skip = static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
+  const int p0 = piece * z.length, p1 = min(p0 + z.length, (a.V + skip + VEC - 1) / VEC);
+  Pack<T, VEC> q[PACKS];
+#pragma unroll
+  for (int i = 0; i < PACKS; ++i) {
+    const int p = p0 + i * kThreads + tid, v = p * VEC - skip;
+    if (p < p1 && v >= 0 && v + VEC <= a.V) {
+      const uint4 w = __ldcs(reinterpret_cast<const uint4*>(row + v));
+      q[i] = *reinterpret_cast<const Pack<T, VEC>*>(&w);
+    } else {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+        q[i].v[e] = p < p1 && v + e >= 0 && v + e < a.V ? row[v + e] : from_f32<T>(-INFINITY);
+    }
+  }
+  float top = -INFINITY;
+  bool nan = false;
+#pragma unroll
+  for (int i = 0; i < PACKS; ++i)
+#pragma unroll
+    for (int e = 0; e < VEC / 2; ++e) {
+      const float2 x = pair_of(q[i], e);
+      nan |= !(x.x < INFINITY) || !(x.y < INFINITY);
+      top = fmaxf(top, fmaxf(x.x, x.y));
+    }
+  // the least of the largest elements of kThreads / span groups of threads
+  uint32_t high = order_of(top), low = high;
+  for (int o = 1; o < span; o <<= 1) low = max(low, __shfl_xor_sync(0xffffffffu, low, o));
+  high = __reduce_max_sync(0xffffffffu, high);
+  low = __reduce_min_sync(0xffffffffu, low);
+  if (lane == 0) warp_max[warp] = high, warp_min[warp] = low;
+  __syncthreads();
+  if (nan) bad = 1;      // NaN or +inf
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) high = max(high, warp_max[w]), low = min(low, warp_min[w]);
+  low = max(low, kMinusInf + 1);      // -inf is no candidate
+  const float m = from_order(high), at_least = from_order(low);
+  // exp((x - m) / tau) = 2^((x - m) k); all of a piece of -inf count as 0
+  const float k = steps(a.tau), mm = m == -INFINITY ? 0.f : m;
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < PACKS; ++i) {
+    const int v = (p0 + i * kThreads + tid) * VEC - skip;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      const float x = to_f32(q[i].v[e]);
+      sum += ex2_approx((x - mm) * k);
+      if (x >= at_least) {
+        const int n = atomicAdd(&n_found, 1);
+        if (n < kRoom) found[n] = entry_of(order_of(x), v + e);
+      }
+    }
+  }
+  sum = warp_sum(sum);
+  if (lane == 0) warp_sums[warp] = sum;
+  __syncthreads();
+  const int64_t slot = r * z.pieces + piece;
+  if (tid == 0) {
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) s += warp_sums[w];
+    z.stats[slot] = bad ? make_float2(NAN, NAN) : make_float2(m, s);
+  }
+  uint64_t* const out = z.best + slot * a.take;
+  int n = n_found;
+  if (bad) n = 0;        // the row offers nothing
+  if (n > kRoom) {
+    // more than fit: the take-th largest order `lo`, then how many equals of it are taken
+    auto count_from = [&](uint32_t least) {
+      int c = 0;
+#pragma unroll
+      for (int i = 0; i < PACKS; ++i)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) c += order_of(to_f32(q[i].v[e])) >= least;
+      return count_all(c, scratch);
+    };
+    uint32_t lo = low, hi = high;      // at least take from lo on; the answer is at most hi
+    while (lo < hi) {
+      const uint32_t mid = lo + (hi - lo + 1) / 2;
+      if (count_from(mid) >= a.take) lo = mid; else hi = mid - 1;
+    }
+    const int above = lo == 0xffffffffu ? 0 : count_from(lo + 1);
+    int first = 0, last = a.V - 1;     // ids up to `first` hold enough equals
+    while (first < last) {
+      const int mid = first + (last - first) / 2;
+      int c = 0;
+#pragma unroll
+      for (int i = 0; i < PACKS; ++i)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+          c += order_of(to_f32(q[i].v[e])) == lo && (p0 + i * kThreads + tid) * VEC - skip + e <= mid;
+      if (count_all(c, scratch) >= a.take - above) last = mid; else first = mid + 1;
+    }
+    __syncthreads();
+    if (tid == 0) n_found = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < PACKS; ++i) {
+      const int v = (p0 + i * kThreads + tid) * VEC - skip;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const uint32_t o = order_of(to_f32(q[i].v[e]));
+        if (o > lo || (o == lo && v + e <= first)) found[atomicAdd(&n_found, 1)] = entry_of(o, v + e);
+      }
+    }
+    __syncthreads();
+    n = n_found;         // take of them
+  }
+  for (int i = tid; i < n; i += kThreads) {
+    const uint64_t me = found[i];
+    int rank = 0;
+    for (int j = 0; j < n; ++j) rank += found[j] > me;
+    if (rank < a.take) out[rank] = me;
+  }
+  for (int i = n + tid; i < a.take; i += kThreads) out[i] = 0;
+}
+
+// ------------------------------------------------------------------ the group's best
+enum : uint8_t { kLive, kEnded, kNone };   // a beam; kNone offers nothing
+
+struct Ranked {
+  double score;
+  int64_t at;      // j V + v
+};
+
+__device__ __forceinline__ bool ahead(const Ranked& x, const Ranked& y) {
+  return x.score > y.score || (x.score == y.score && x.at < y.at);
+}
+
+__global__ void __launch_bounds__(kBestThreads) best_kernel(BeamSelect a, Pieces z, int span) {
+  __shared__ Ranked found[kRoom];
+  // lse = top / tau + log s, so score(j, v) = (score_j - log s) + (x_v - top) / tau: a row
+  // whose logits are all near the type's lowest value keeps its differences
+  __shared__ double bias[kMaxBeams];       // score - log s of each beam
+  __shared__ float rough[kMaxBeams];       // the same in fp32
+  __shared__ float tops[kMaxBeams];
+  __shared__ uint8_t kind[kMaxBeams];
+  __shared__ float warp_low[kBestWarps];
+  __shared__ int n_found;
+  __shared__ Ranked warp_best[kBestWarps], last;
+  pdl_wait_prerequisites();
+  pdl_launch_dependents();
+  const int64_t g = blockIdx.x, r0 = g * a.beams;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) n_found = 0;
+  const double inv = 1.0 / static_cast<double>(a.tau);
+  for (int j = warp; j < a.beams; j += kBestWarps) {
+    const int64_t r = r0 + j;
+    const float score = a.scores[r];
+    const bool ended = a.finished && a.finished[r];
+    double log_s = 0.0;
+    float m = -INFINITY;
+    bool bad = false;
+    if (!ended) {
+      const float2* const st = z.stats + r * z.pieces;
+      for (int i = lane; i < z.pieces; i += 32) {
+        const float x = st[i].x;
+        bad |= x != x;
+        m = fmaxf(m, x);
+      }
+      m = warp_max(m);
+      bad = __any_sync(0xffffffffu, bad);
+      double s = 0.0;
+      const float k = steps(a.tau);
+      if (m > -INFINITY)
+        for (int i = lane; i < z.pieces; i += 32) s += st[i].y * ex2_approx((st[i].x - m) * k);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      // log s = e log 2 + log f with f in [1, 2): only the small part in fp32
+      int e;
+      const float near = static_cast<float>(s), f = 2.f * frexpf(near, &e);
+      const float rest = static_cast<float>(s - static_cast<double>(near)) / near;
+      log_s = (e - 1) * 0.6931471805599453 + static_cast<double>(logf(f) + rest);
+    }
+    if (lane == 0) {
+      const bool none = !ended && (bad || m == -INFINITY);
+      if (a.lse) {
+        const double lse = ended ? 0.0 : bad ? static_cast<double>(NAN)
+                                             : m == -INFINITY ? static_cast<double>(m) : static_cast<double>(m) * inv + log_s;
+        a.lse[r] = static_cast<float>(lse);
+      }
+      bias[j] = static_cast<double>(score) - log_s;
+      rough[j] = static_cast<float>(bias[j]);
+      tops[j] = m;
+      kind[j] = none || !isfinite(score) ? kNone : ended ? kEnded : kLive;
+    }
+  }
+  __syncthreads();
+  const int per_beam = z.pieces * a.take, total = a.beams * per_beam;
+  const float inv_f = static_cast<float>(inv);
+  // an entry's score in fp32 and a bound of its error: a rounding of the difference, of
+  // 1 / tau, of the product, of the beam's part and of the sums
+  auto estimate = [&](int j, uint32_t order, float& err) {
+    const float x = (from_order(order) - tops[j]) * inv_f, b = rough[j], f = x + b;
+    err = 4.0e-7f * (fabsf(x) + fabsf(b)) + 1e-37f;   // 6.7 roundings; six are met
+    return f;
+  };
+  auto each = [&](auto&& f) {
+    for (int i = tid; i < total; i += kBestThreads) {
+      const int j = i / per_beam;
+      if (kind[j] != kLive) continue;
+      const uint64_t e = z.best[(r0 + j) * per_beam + (i - j * per_beam)];
+      if (e) f(j, static_cast<uint32_t>(e >> 32), static_cast<int>(~static_cast<uint32_t>(e)));
+    }
+  };
+  auto exact = [&](int j, uint32_t order, int v) {
+    const double x = static_cast<double>(from_order(order)) - static_cast<double>(tops[j]);
+    return Ranked{bias[j] + x * inv, static_cast<int64_t>(j) * a.V + v};
+  };
+  float low = -INFINITY;
+  each([&](int j, uint32_t order, int) {
+    float err;
+    const float f = estimate(j, order, err);
+    low = fmaxf(low, f - err);       // NaN (an overflow) is passed over
+  });
+  for (int o = 1; o < span; o <<= 1) low = fmaxf(low, __shfl_xor_sync(0xffffffffu, low, o));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
+  if (lane == 0) warp_low[warp] = low;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kBestWarps; ++w) low = fminf(low, warp_low[w]);
+  each([&](int j, uint32_t order, int v) {
+    float err;
+    const float f = estimate(j, order, err);
+    if (f + err < low) return;       // not so where one is NaN
+    const int n = atomicAdd(&n_found, 1);
+    if (n < kRoom) found[n] = exact(j, order, v);
+  });
+  if (tid < a.beams && kind[tid] == kEnded) {
+    const int n = atomicAdd(&n_found, 1);
+    if (n < kRoom) found[n] = Ranked{bias[tid], static_cast<int64_t>(tid) * a.V + a.eos};
+  }
+  __syncthreads();
+  auto put = [&](int n, const Ranked& x) {
+    const int j = static_cast<int>(x.at / a.V), v = static_cast<int>(x.at % a.V);
+    const int64_t o = g * a.take + n;
+    a.out_scores[o] = static_cast<float>(x.score);
+    a.parents[o] = static_cast<int32_t>(r0 + j);
+    a.tokens[o] = v;
+    if (a.next_finished) a.next_finished[o] = kind[j] == kEnded || v == a.eos;
+  };
+  int n = n_found;
+  if (n <= kRoom) {
+    for (int i = tid; i < n; i += kBestThreads) {
+      const Ranked me = found[i];
+      int rank = 0;
+      for (int j = 0; j < n; ++j) rank += ahead(found[j], me);
+      if (rank < a.take) put(rank, me);
+    }
+  } else {
+    // more than fit (equal scores): one after the other, the first behind the last one put
+    n = a.take;
+    if (tid == 0) last = Ranked{static_cast<double>(INFINITY), -1};
+    for (int t = 0; t < a.take; ++t) {
+      __syncthreads();
+      const Ranked before = last;
+      Ranked mine{-static_cast<double>(INFINITY), INT64_MAX};
+      auto offer = [&](const Ranked& x) {
+        if (ahead(before, x) && ahead(x, mine)) mine = x;
+      };
+      each([&](int j, uint32_t order, int v) { offer(exact(j, order, v)); });
+      if (tid < a.beams && kind[tid] == kEnded)
+        offer(Ranked{bias[tid], static_cast<int64_t>(tid) * a.V + a.eos});
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const Ranked x{__shfl_xor_sync(0xffffffffu, mine.score, o), __shfl_xor_sync(0xffffffffu, mine.at, o)};
+        if (ahead(x, mine)) mine = x;
+      }
+      if (lane == 0) warp_best[warp] = mine;
+      __syncthreads();
+      if (tid == 0) {
+        for (int w = 0; w < kBestWarps; ++w)
+          if (ahead(warp_best[w], mine)) mine = warp_best[w];
+        last = mine;
+        put(t, mine);
+      }
+    }
+  }
+  for (int i = n + tid; i < a.take; i += kBestThreads) {
+    const int64_t o = g * a.take + i;
+    a.out_scores[o] = -INFINITY;
+    a.parents[o] = -1;
+    a.tokens[o] = -1;
+    if (a.next_finished) a.next_finished[o] = 0;
+  }
+}
+
+// ------------------------------------------------------------------ states
+constexpr int kMoveThreads = 256;
+constexpr int kMoveUnroll = 4;
+
+// Threads along the contiguous bytes (a power of two) and along `mid`.
+struct Tile {
+  int across;           // threads along inner
+  int64_t parts;        // CTAs along inner
+  int64_t mids;         // CTAs along mid
+};
+
+template <typename U>
+__global__ void __launch_bounds__(kMoveThreads) gather_kernel(BeamReorder a, Tile t) {
+  pdl_wait_prerequisites();
+  pdl_launch_dependents();
+  int64_t b = blockIdx.x;
+  const int64_t part = b % t.parts;
+  b /= t.parts;
+  const int64_t mids = b % t.mids;
+  b /= t.mids;
+  const int64_t r = b % a.rows, o = b / a.rows;
+  const int from = a.parents[r];
+  const bool none = from < 0 || from >= a.src_rows;
+  if (none && !a.clear) return;
+  const int x = threadIdx.x % t.across, y = threadIdx.x / t.across;
+  const int64_t m = mids * (kMoveThreads / t.across) + y;
+  if (m >= a.mid) return;
+  const U* const src = reinterpret_cast<const U*>(a.src + o * a.src_outer + from * a.src_row + m * a.src_mid);
+  U* const dst = reinterpret_cast<U*>(a.dst + o * a.dst_outer + r * a.dst_row + m * a.dst_mid);
+  const int64_t n = a.inner / static_cast<int64_t>(sizeof(U));
+  const int64_t i0 = part * t.across * kMoveUnroll + x;
+  U q[kMoveUnroll] = {};
+#pragma unroll
+  for (int u = 0; u < kMoveUnroll; ++u)
+    if (!none && i0 + u * t.across < n) q[u] = src[i0 + u * t.across];
+#pragma unroll
+  for (int u = 0; u < kMoveUnroll; ++u)
+    if (i0 + u * t.across < n) dst[i0 + u * t.across] = q[u];
+}
+
+// BEAMS >= a.beams rows of a group, one unit of each per thread.
+template <typename U, int BEAMS>
+__global__ void __launch_bounds__(kMoveThreads) in_place_kernel(BeamReorder a, Tile t) {
+  __shared__ int from[BEAMS];
+  __shared__ int moving;
+  pdl_wait_prerequisites();
+  pdl_launch_dependents();
+  int64_t b = blockIdx.x;
+  const int64_t part = b % t.parts;
+  b /= t.parts;
+  const int64_t mids = b % t.mids;
+  b /= t.mids;
+  const int64_t groups = a.rows / a.beams, r0 = b % groups * a.beams, o = b / groups;
+  if (threadIdx.x == 0) moving = 0;
+  __syncthreads();
+  if (threadIdx.x < BEAMS) {
+    int f = -1;              // stays
+    if (threadIdx.x < a.beams) {
+      const int64_t p = a.parents[r0 + threadIdx.x] - r0;
+      if (p >= 0 && p < a.beams && p != threadIdx.x) f = static_cast<int>(p);
+    }
+    from[threadIdx.x] = f;
+    if (f >= 0) moving = 1;
+  }
+  __syncthreads();
+  if (!moving) return;
+  const int x = threadIdx.x % t.across, y = threadIdx.x / t.across;
+  const int64_t m = mids * (kMoveThreads / t.across) + y;
+  const int64_t n = a.inner / static_cast<int64_t>(sizeof(U)), i = part * t.across + x;
+  if (m >= a.mid || i >= n) return;
+  char* const base = a.dst + o * a.dst_outer + r0 * a.dst_row + m * a.dst_mid + i * static_cast<int64_t>(sizeof(U));
+  U q[BEAMS];
+#pragma unroll
+  for (int j = 0; j < BEAMS; ++j)
+    if (from[j] >= 0) q[j] = *reinterpret_cast<const U*>(base + from[j] * a.dst_row);
+#pragma unroll
+  for (int j = 0; j < BEAMS; ++j)
+    if (from[j] >= 0) *reinterpret_cast<U*>(base + j * a.dst_row) = q[j];
+}
+
+// The widest unit in bytes that every address is a multiple of; 17 to 64 rows in
+// registers take units of 4 bytes at most.
+int unit_of(const BeamReorder& a) {
+  const uint64_t bits = reinterpret_cast<uintptr_t>(a.src) | reinterpret_cast<uintptr_t>(a.dst) |
+                        static_cast<uint64_t>(a.inner | a.src_outer | a.dst_outer | a.src_row | a.dst_row |
+                                              a.src_mid | a.dst_mid);
+  int unit = a.src == a.dst && a.beams > 16 ? 4 : 16;
+  while (bits & static_cast<uint64_t>(unit - 1)) unit /= 2;
+  return unit;
+}
+
+// The tile and the number of CTAs.
+Tile tile_of(const BeamReorder& a, int unit, double& ctas) {
+  const bool in_place = a.src == a.dst;
+  const int64_t n = a.inner / unit;
+  const int each = in_place ? 1 : kMoveUnroll;
+  Tile t;
+  t.across = 1;
+  while (t.across < kMoveThreads && static_cast<int64_t>(t.across) * each < n) t.across *= 2;
+  t.parts = (n + static_cast<int64_t>(t.across) * each - 1) / (static_cast<int64_t>(t.across) * each);
+  const int down = kMoveThreads / t.across;
+  t.mids = (a.mid + down - 1) / down;
+  ctas = static_cast<double>(t.parts) * static_cast<double>(t.mids) * static_cast<double>(a.outer) *
+         static_cast<double>(in_place ? a.rows / a.beams : a.rows);
+  return t;
+}
+
+template <typename U>
+cudaError_t move(const BeamReorder& a, cudaStream_t s) {
+  double ctas = 0;
+  const Tile t = tile_of(a, sizeof(U), ctas);
+  const dim3 grid(static_cast<unsigned>(ctas));
+  if (a.src != a.dst) return launch_dependent(gather_kernel<U>, grid, kMoveThreads, 0, 1, s, a, t);
+  if (a.beams <= 4) return launch_dependent(in_place_kernel<U, 4>, grid, kMoveThreads, 0, 1, s, a, t);
+  if (a.beams <= 8) return launch_dependent(in_place_kernel<U, 8>, grid, kMoveThreads, 0, 1, s, a, t);
+  if (a.beams <= 16) return launch_dependent(in_place_kernel<U, 16>, grid, kMoveThreads, 0, 1, s, a, t);
+  if constexpr (sizeof(U) <= 4) {
+    return launch_dependent(in_place_kernel<U, kMaxBeams>, grid, kMoveThreads, 0, 1, s, a, t);
+  } else {
+    return cudaErrorInvalidValue;   // unit_of gives none
+  }
+}
+
+size_t round_up(size_t n) { return (n + 255) / 256 * 256; }
+
+// Pieces of a row: long ones where they fill the GPU.  A row that starts off a 16-byte
+// boundary spreads over up to one pack more.
+template <typename T>
+Pieces plan(int64_t R, int V, int& elements) {
+  constexpr int VEC = kVec<T>;
+  const int64_t packs = (static_cast<int64_t>(V) + 2 * VEC - 2) / VEC;
+  auto cut = [&](int elems) { return (packs * VEC + kThreads * elems - 1) / (static_cast<int64_t>(kThreads) * elems); };
+  elements = R * cut(kManyElements) >= kManyPieces ? kManyElements : kFewElements;
+  const int64_t pieces = cut(elements);
+  Pieces z{};
+  z.pieces = static_cast<int>(pieces);
+  z.length = static_cast<int>((packs + pieces - 1) / pieces);
+  return z;
+}
+
+template <typename F>
+auto by_type(int type, F&& f) {
+  switch (type) {
+    case kF32: return f(float{});
+    case kBF16: return f(__nv_bfloat16{});
+    default: return f(__half{});
+  }
+}
+
+}  // namespace
+
+size_t beam_workspace(int64_t R, int V, int take) {
+  size_t most = 0;
+  for (const int type : {kF32, kBF16}) {
+    const size_t n = by_type(type, [&](auto t) {
+      int elements;
+      const size_t slots = static_cast<size_t>(R) * plan<decltype(t)>(R, V, elements).pieces;
+      return round_up(slots * sizeof(float2)) + slots * sizeof(uint64_t) * take;
+    });
+    most = n > most ? n : most;
+  }
+  return most > 256 ? most : 256;
+}
+
+bool beam_select_fits(int type, int64_t R, int V) {
+  int elements = 0;
+  return by_type(type, [&](auto t) { return R * plan<decltype(t)>(R, V, elements).pieces; }) <= 0x7fffffff;
+}
+
+cudaError_t launch_beam_select(const BeamSelect& a, cudaStream_t s) {
+  int elements = 0;
+  Pieces z = by_type(a.type, [&](auto t) { return plan<decltype(t)>(a.R, a.V, elements); });
+  const size_t slots = static_cast<size_t>(a.R) * z.pieces;
+  z.stats = static_cast<float2*>(a.workspace);
+  z.best = reinterpret_cast<uint64_t*>(static_cast<char*>(a.workspace) + round_up(slots * sizeof(float2)));
+  // groups of threads, at least `take` of them (whole warps at most)
+  int groups = kWarps;
+  while (groups < a.take) groups *= 2;
+  cudaError_t e = traced_launch("beam_select_scan", s, [&] {
+    return by_type(a.type, [&](auto t) {
+      using T = decltype(t);
+      auto kern = elements == kManyElements ? scan_kernel<T, kManyElements> : scan_kernel<T, kFewElements>;
+      return launch_dependent(kern, dim3(static_cast<unsigned>(slots)), kThreads, 0, 1, s, a, z, kThreads / groups);
+    });
+  });
+  if (e != cudaSuccess) return e;
+  groups = kBestWarps;
+  while (groups < a.take) groups *= 2;
+  return traced_launch("beam_select_best", s, [&] {
+    return launch_dependent(best_kernel, dim3(static_cast<unsigned>(a.R / a.beams)), kBestThreads, 0, 1, s, a, z,
+                            kBestThreads / groups);
+  });
+}
+
+bool beam_reorder_fits(const BeamReorder& a) {
+  double ctas = 0;
+  tile_of(a, unit_of(a), ctas);
+  return ctas <= 2147483647.0;
+}
+
+cudaError_t launch_beam_reorder(const BeamReorder& a, cudaStream_t s) {
+  return traced_launch("beam_reorder", s, [&] {
+    switch (unit_of(a)) {
+      case 16: return move<uint4>(a, s);
+      case 8: return move<uint2>(a, s);
+      case 4: return move<uint32_t>(a, s);
+      case 2: return move<uint16_t>(a, s);
+      default: return move<uint8_t>(a, s);
+    }
+  });
+}
+
+}  // namespace lmh

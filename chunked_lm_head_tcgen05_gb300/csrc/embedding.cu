@@ -33,26 +33,6 @@ constexpr int kJoinSegments = 32;
 int segment_of(int64_t n) { return n < kFew ? kShort : kLong; }
 
 // ------------------------------------------------------------------ forward
-// The 16 bytes at p, which is aligned to its element only, from the two aligned
-// blocks they lie in.
-template <typename T>
-__device__ __forceinline__ uint4 load_across(const T* p) {
-  const unsigned off = static_cast<unsigned>(reinterpret_cast<uintptr_t>(p)) & 15u;
-  const uint4* const q = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(p) - off);
-  const uint4 lo = q[0];
-  if (off == 0) return lo;
-  const uint4 hi = q[1];
-  const unsigned words = off >> 2, bits = (off & 3u) * 8u;
-  // words of lo : hi from `words` on, five of them
-  const bool two = words & 2u, one = words & 1u;
-  const uint32_t a0 = two ? lo.z : lo.x, a1 = two ? lo.w : lo.y, a2 = two ? hi.x : lo.z,
-                 a3 = two ? hi.y : lo.w, a4 = two ? hi.z : hi.x, a5 = two ? hi.w : hi.y;
-  const uint32_t b0 = one ? a1 : a0, b1 = one ? a2 : a1, b2 = one ? a3 : a2, b3 = one ? a4 : a3,
-                 b4 = one ? a5 : a4;
-  return make_uint4(__funnelshift_r(b0, b1, bits), __funnelshift_r(b1, b2, bits),
-                    __funnelshift_r(b2, b3, bits), __funnelshift_r(b3, b4, bits));
-}
-
 // VEC elements of W become VEC of y.
 template <typename W, typename Y, int VEC>
 __device__ __forceinline__ Pack<Y, VEC> scaled(const Pack<W, VEC>& q, float scale) {

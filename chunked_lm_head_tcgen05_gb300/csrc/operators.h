@@ -152,7 +152,7 @@ cudaError_t launch_process_logits(const ProcessLogits& a, cudaStream_t s);
 // ------------------------------------------------------------------ ids in order
 // Most ids of one sort.
 constexpr int kSortMost = 131072;
-// Stable sort of n <= kSortMost ids: keys ascending, pos their places in `ids`.  Ids
+// Stable sort of n <= kSortMost ids (NULL: all 0): keys ascending, pos their places in `ids`.  Ids
 // outside [0, bound) and `skip` (-1: none) count as `bound` and come last; with `wrap`,
 // ids in [-bound, 0) first become id + bound.  *live: how many are inside.
 cudaError_t launch_sort_ids(const int32_t* ids, int n, int bound, bool wrap, int skip, int32_t* keys,
@@ -192,5 +192,51 @@ struct EmbedBwd {
 size_t embed_workspace(int64_t N, int H);
 cudaError_t launch_embed_fwd(const EmbedFwd& a, cudaStream_t s);
 cudaError_t launch_embed_bwd(const EmbedBwd& a, cudaStream_t s);
+
+// ------------------------------------------------------------------ beam search
+constexpr int kMaxBeams = 64;
+constexpr int kMaxTake = 128;
+
+struct BeamSelect {
+  const void* logits;    // [R, V], rows ld elements apart
+  int type;
+  int64_t ld;
+  int64_t R;             // groups * beams
+  int V;
+  int beams;
+  int take;
+  const float* scores;   // [R]
+  const uint8_t* finished;   // [R] or NULL
+  int eos;               // the id that ends a sequence, or -1
+  float tau;
+  float* out_scores;     // [R / beams, take], as the next two
+  int32_t* parents;
+  int32_t* tokens;
+  uint8_t* next_finished;    // or NULL
+  float* lse;            // [R] or NULL
+  void* workspace;       // beam_workspace(R, V, take) bytes
+};
+
+size_t beam_workspace(int64_t R, int V, int take);
+bool beam_select_fits(int type, int64_t R, int V);   // the grid
+cudaError_t launch_beam_select(const BeamSelect& a, cudaStream_t s);
+
+// dst[o][r][m] = src[o][parents[r]][m], `inner` contiguous bytes each; strides in bytes.
+// In place (src == dst): `beams` rows at a time, parents within their own group.
+struct BeamReorder {
+  const char* src;
+  char* dst;
+  const int32_t* parents;    // [rows]
+  int64_t rows;
+  int64_t src_rows;
+  int beams;
+  int64_t outer, mid, inner;
+  int64_t src_outer, src_row, src_mid;
+  int64_t dst_outer, dst_row, dst_mid;
+  int clear;                 // rows without a parent: zeros, else left
+};
+
+bool beam_reorder_fits(const BeamReorder& a);   // the grid
+cudaError_t launch_beam_reorder(const BeamReorder& a, cudaStream_t s);
 
 }  // namespace lmh

@@ -1,8 +1,9 @@
 // Host side of the C ABI of layer norm, distillation on held logits, logit
-// processing and embedding: argument checks and the stream-ordered launches.  No device
+// processing, embedding and beam search: argument checks and the stream-ordered launches.  No device
 // memory is allocated and nothing synchronises.
 #include "lmhead.h"
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -97,6 +98,39 @@ lmhead_status check_embedding(int64_t N, int32_t V, int32_t H, float scale, int 
     return LMHEAD_ERR_INVALID_ARG;
   if (N >= kMaxRows || V > kMaxVocab || H > kMaxWidth) return LMHEAD_ERR_UNSUPPORTED;
   return LMHEAD_OK;
+}
+
+constexpr int32_t kMaxBeamVocab = 1 << 30;   // columns of the pieces past a row's end are counted too
+
+// A strided block of bytes: up to three dimensions of `inner` contiguous bytes.
+struct Block {
+  int64_t size[3], stride[3], inner;
+};
+
+// The bytes from its first to its last, or -1 where that cannot be: sizes are small
+// enough for memory, strides may be anything.
+int64_t extent_of(const Block& b) {
+  double end = static_cast<double>(b.inner);
+  for (int i = 0; i < 3; ++i)
+    if (b.size[i] > 1) end += static_cast<double>(b.size[i] - 1) * static_cast<double>(b.stride[i]);
+  if (end > 9.0e18) return -1;
+  int64_t n = b.inner;
+  for (int i = 0; i < 3; ++i)
+    if (b.size[i] > 1) n += (b.size[i] - 1) * b.stride[i];
+  return n;
+}
+
+// Whether no two elements share a byte, judged from the strides in ascending order.
+bool apart(Block b) {
+  int order[3] = {0, 1, 2};
+  std::sort(order, order + 3, [&](int x, int y) { return b.stride[x] < b.stride[y]; });
+  int64_t within = b.inner;
+  for (const int i : order) {
+    if (b.size[i] <= 1) continue;
+    if (b.stride[i] < within) return false;
+    within += (b.size[i] - 1) * b.stride[i];
+  }
+  return true;
 }
 
 }  // namespace
@@ -308,6 +342,75 @@ lmhead_status lmhead_embedding_bwd(const void* dy, int dy_type, int64_t dy_ld, c
   const EmbedBwd a{dy, dy_type, dy_ld, ids, N, V, H, scale, skip, d_weight, d_weight_type,
                    accumulate ? 1 : 0, workspace};
   return status_of(launch_embed_bwd(a, s));
+}
+
+size_t lmhead_beam_workspace_size(int64_t R, int32_t V, int32_t take) {
+  return R < 0 || R >= kMaxRows || V <= 0 || V > kMaxBeamVocab || take <= 0 || take > kMaxTake
+             ? 0 : beam_workspace(R, V, take);
+}
+
+lmhead_status lmhead_beam_select(const void* logits, int type, int64_t ld, int64_t R, int32_t V,
+                                 int32_t beams, int32_t take, const float* scores,
+                                 const uint8_t* finished, int32_t eos_id, float temperature,
+                                 float* out_scores, int32_t* parents, int32_t* tokens,
+                                 uint8_t* next_finished, float* lse, void* workspace,
+                                 size_t workspace_bytes, lmhead_stream_t stream) {
+  if (R < 0 || V <= 0 || beams <= 0 || take <= 0 || !known_type(type) || ld < V || !positive(temperature) ||
+      R % beams != 0 || eos_id < -1 || eos_id >= V || (finished && eos_id < 0))
+    return LMHEAD_ERR_INVALID_ARG;
+  if (R >= kMaxRows || V > kMaxBeamVocab || beams > kMaxBeams || take > kMaxTake) return LMHEAD_ERR_UNSUPPORTED;
+  if (R == 0) return LMHEAD_OK;
+  if (!logits || !scores || !out_scores || !parents || !tokens || !workspace) return LMHEAD_ERR_INVALID_ARG;
+  for (const void* p : {static_cast<const void*>(scores), static_cast<const void*>(out_scores),
+                        static_cast<const void*>(parents), static_cast<const void*>(tokens),
+                        static_cast<const void*>(lse)})
+    if (!aligned_to(p, kF32)) return LMHEAD_ERR_UNSUPPORTED;
+  if (!aligned_to(logits, type) || (reinterpret_cast<uintptr_t>(workspace) & 255)) return LMHEAD_ERR_UNSUPPORTED;
+  if (!beam_select_fits(type, R, V)) return LMHEAD_ERR_UNSUPPORTED;
+  if (workspace_bytes < beam_workspace(R, V, take)) return LMHEAD_ERR_WORKSPACE_TOO_SMALL;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const BeamSelect a{logits, type, ld, R, V, beams, take, scores, finished, eos_id, temperature,
+                     out_scores, parents, tokens, next_finished, lse, workspace};
+  return status_of(launch_beam_select(a, s));
+}
+
+lmhead_status lmhead_beam_reorder(const void* src, int64_t src_outer, int64_t src_row,
+                                  int64_t src_mid, int64_t src_rows, void* dst,
+                                  int64_t dst_outer, int64_t dst_row, int64_t dst_mid,
+                                  const int32_t* parents, int64_t rows, int32_t beams,
+                                  int64_t outer, int64_t mid, int64_t inner_bytes,
+                                  int clear_missing, lmhead_stream_t stream) {
+  if (rows < 0 || src_rows < 0 || outer < 0 || mid < 0 || inner_bytes < 0) return LMHEAD_ERR_INVALID_ARG;
+  if (rows >= kMaxRows || src_rows >= kMaxRows) return LMHEAD_ERR_UNSUPPORTED;
+  if (rows == 0 || outer == 0 || mid == 0 || inner_bytes == 0) return LMHEAD_OK;
+  if (!src || !dst || !parents) return LMHEAD_ERR_INVALID_ARG;
+  // strides of dimensions of size 1 say nothing
+  if (outer == 1) src_outer = dst_outer = 0;
+  if (mid == 1) src_mid = dst_mid = 0;
+  if (rows == 1) dst_row = 0;
+  if (src_rows <= 1) src_row = 0;
+  if (src_outer < 0 || src_row < 0 || src_mid < 0 || dst_outer < 0 || dst_row < 0 || dst_mid < 0)
+    return LMHEAD_ERR_INVALID_ARG;
+  const Block from{{outer, src_rows, mid}, {src_outer, src_row, src_mid}, inner_bytes};
+  const Block to{{outer, rows, mid}, {dst_outer, dst_row, dst_mid}, inner_bytes};
+  const int64_t from_bytes = extent_of(from), to_bytes = extent_of(to);
+  if (from_bytes < 0 || to_bytes < 0 || !apart(to)) return LMHEAD_ERR_INVALID_ARG;
+  if (src == dst) {
+    if (src_rows != rows || src_outer != dst_outer || src_row != dst_row || src_mid != dst_mid || beams <= 0 ||
+        rows % beams != 0)
+      return LMHEAD_ERR_INVALID_ARG;
+    if (beams > kMaxBeams) return LMHEAD_ERR_UNSUPPORTED;
+  } else {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(src), q = reinterpret_cast<uintptr_t>(dst);
+    if (src_rows > 0 && p < q + static_cast<uintptr_t>(to_bytes) && q < p + static_cast<uintptr_t>(from_bytes))
+      return LMHEAD_ERR_INVALID_ARG;
+  }
+  if (!aligned_to(parents, kF32)) return LMHEAD_ERR_UNSUPPORTED;
+  const BeamReorder a{static_cast<const char*>(src), static_cast<char*>(dst), parents, rows, src_rows, beams,
+                      outer, mid, inner_bytes, src_outer, src_row, src_mid, dst_outer, dst_row, dst_mid,
+                      clear_missing};
+  if (!beam_reorder_fits(a)) return LMHEAD_ERR_UNSUPPORTED;
+  return status_of(launch_beam_reorder(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

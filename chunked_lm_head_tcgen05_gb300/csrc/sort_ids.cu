@@ -22,7 +22,7 @@ constexpr int kMaxDigits = 512;
 constexpr int kCluster = 8;
 
 struct SortArgs {
-  const int32_t* ids;
+  const int32_t* ids;   // NULL: all 0
   int n;
   int bound;       // ids outside [0, bound) sort last, as `bound`
   int wrap;        // ids in [-bound, 0) mean id + bound
@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(kThreads) sort_kernel(SortArgs a) {
     const int g = rank * P + first + j * 32;
     uint32_t key = last;               // places past the end sort behind everything
     if (g < a.n) {
-      int id = a.ids[g];
+      int id = a.ids ? a.ids[g] : 0;
       if (a.wrap && id < 0) id += a.bound;
       const bool in = id >= 0 && id < a.bound && id != a.skip;
       key = static_cast<uint32_t>(in ? id : a.bound);

@@ -563,6 +563,63 @@ lmhead_status lmhead_embedding_bwd(const void* dy, int dy_type, int64_t dy_ld, c
                                    lmhead_stream_t stream);
 
 /*
+ * One step of beam search: a group's best continuations.  Row r = group * beams + j of
+ * logits [R, V] (element type `type`, rows ld apart) belongs to beam j of its group, whose
+ * sequence has scores[r] so far.  With z = logits / temperature,
+ *   lse_r = log sum_v exp(z_v)
+ *   score(j, v) = scores[r] + z_v - lse_r
+ * and each group gets the `take` best of its beams * V candidates in falling order, ties
+ * to the lowest j V + v.  Scores are compared in 64 bits.
+ *  finished      [R] uint8 or NULL: nonzero for a sequence that has ended.  Its logits are
+ *                not read; its one candidate is the id eos_id with its score unchanged.
+ *  eos_id        the id that ends a sequence, in [0, V); -1 for none (then finished must
+ *                be NULL)
+ *  out_scores    [R / beams, take] fp32; parents: the candidate's row r (int32); tokens:
+ *                its id v (int32)
+ *  next_finished [R / beams, take] uint8 or NULL: the parent has ended or v is eos_id
+ *  lse           [R] fp32 or NULL; +0.0 for finished rows
+ * -inf logits (masks) are no candidates; a row without a finite logit has lse = -inf, a
+ * NaN or +inf logit makes the row's lse NaN, and a row whose lse or score is not finite
+ * offers nothing: give beams that do not exist yet the score -inf.  Where a group has
+ * fewer than `take` candidates the rest have score -inf, parent -1 and id -1 (and
+ * next_finished 0).
+ *  workspace     lmhead_beam_workspace_size(R, V, take) bytes, 256-byte aligned
+ * R must be a multiple of beams.  beams <= 64, take <= 128, V <= 2^30, R < 2^31 - 256 and
+ * pieces of rows within the launch limits (LMHEAD_ERR_UNSUPPORTED beyond).  HBM-bound: one
+ * read of the logits.  R == 0 is a no-op.
+ */
+size_t lmhead_beam_workspace_size(int64_t R, int32_t V, int32_t take);
+
+lmhead_status lmhead_beam_select(const void* logits, int type, int64_t ld, int64_t R, int32_t V,
+                                 int32_t beams, int32_t take, const float* scores,
+                                 const uint8_t* finished, int32_t eos_id, float temperature,
+                                 float* out_scores, int32_t* parents, int32_t* tokens,
+                                 uint8_t* next_finished, float* lse, void* workspace,
+                                 size_t workspace_bytes, lmhead_stream_t stream);
+
+/*
+ * States that follow their beams: dst[o][r][m] = src[o][parents[r]][m] for o < outer,
+ * r < rows, m < mid, `inner_bytes` contiguous bytes each (a cache's layers, rows, heads
+ * and used positions; token histories).  All strides are in bytes; those of dimensions
+ * of size 1 are not looked at.
+ *  src != dst    src has src_rows rows and does not overlap dst (LMHEAD_ERR_INVALID_ARG
+ *                where their extents do); a parent outside [0, src_rows) (-1) leaves the
+ *                row of dst as it is, or clears it to zero bytes where clear_missing != 0
+ *  src == dst    in place, with the same strides and src_rows == rows: rows are taken in
+ *                groups of `beams` (1 to 64, a divisor of rows), and a parent outside its
+ *                own group leaves the row as it is.  Rows that keep their place are neither
+ *                read nor written.
+ * dst's rows must not overlap one another.  beams is not looked at where src != dst, nor
+ * clear_missing in place.
+ */
+lmhead_status lmhead_beam_reorder(const void* src, int64_t src_outer, int64_t src_row,
+                                  int64_t src_mid, int64_t src_rows, void* dst,
+                                  int64_t dst_outer, int64_t dst_row, int64_t dst_mid,
+                                  const int32_t* parents, int64_t rows, int32_t beams,
+                                  int64_t outer, int64_t mid, int64_t inner_bytes,
+                                  int clear_missing, lmhead_stream_t stream);
+
+/*
  * Self-test of failure detection (the pages have no counterpart; the
  * kernels need it on shared GPUs): launches one CTA that allocates tensor
  * memory and waits, with the same bounded mbarrier wait every GEMM pipeline
