@@ -38,7 +38,8 @@ __all__ = [
     "NO_PADDING", "lmhead_embedding_workspace_size", "lmhead_embedding_fwd",
     "lmhead_embedding_bwd", "embedding_forward", "embedding_backward",
     "lmhead_beam_workspace_size", "lmhead_beam_select", "lmhead_beam_reorder", "beam_select",
-    "beam_reorder",
+    "beam_reorder", "lmhead_adapters_workspace_size", "lmhead_adapters_fwd", "lmhead_adapters_bwd",
+    "adapters_forward", "adapters_backward",
 ]
 
 LMHEAD_OP_FWD = 0
@@ -137,6 +138,12 @@ _SIGNATURES = {
     "lmhead_embedding_bwd": (ctypes.c_int, [_VP, ctypes.c_int, _I64, _VP, _I64, _I32, _I32,
                                             ctypes.c_float, _I32, _VP, ctypes.c_int, ctypes.c_int,
                                             _VP, _SZ, _VP]),
+    "lmhead_adapters_workspace_size": (_SZ, [_I64, _I32, _I32, _I32, _I32]),
+    "lmhead_adapters_fwd": (ctypes.c_int, [_VP, ctypes.c_int, _I64, _VP, _I64, _VP, _VP, _VP, _VP,
+                                           _I64, _I32, _I32, _I32, _I32, _VP, _I64, _VP, _SZ, _VP]),
+    "lmhead_adapters_bwd": (ctypes.c_int, [_VP, ctypes.c_int, _I64, _VP, _I64, _VP, _VP, _VP, _VP,
+                                           _I64, _I32, _I32, _I32, _I32, _VP, _I64, ctypes.c_int,
+                                           _VP, _VP, ctypes.c_int, _VP, _SZ, _VP]),
     "lmhead_beam_workspace_size": (_SZ, [_I64, _I32, _I32]),
     "lmhead_beam_select": (ctypes.c_int, [_VP, ctypes.c_int, _I64, _I64, _I32, _I32, _I32, _VP, _VP,
                                           _I32, ctypes.c_float, _VP, _VP, _VP, _VP, _VP, _VP, _SZ,
@@ -816,6 +823,54 @@ def lmhead_embedding_bwd(dy, ids, scale, padding_id, d_weight, accumulate, works
                  1 if accumulate else 0, workspace.data_ptr(), workspace.nbytes)
 
 
+def lmhead_adapters_workspace_size(T, H, V, rank, n_adapters):
+    return int(library().lmhead_adapters_workspace_size(T, H, V, rank, n_adapters))
+
+
+def _check_adapters(x, down, up, adapter_ids, scale):
+    """(T, H, V, rank, n_adapters, elements between x's rows)"""
+    if _torch is None:
+        _bind_torch()
+    torch = _torch
+    T, H = x.shape
+    _, x_ld = _check_rows(x, "x", (T, H), (torch.bfloat16,))
+    n, rank, V = up.shape
+    _check_tensor(down, "down", torch.bfloat16, (n, rank, H))
+    _check_tensor(up, "up", torch.bfloat16, (n, rank, V))
+    _check_tensor(adapter_ids, "adapter_ids", torch.int32, (T,), allow_none=True)
+    _check_tensor(scale, "scale", torch.float32, (n,), allow_none=True)
+    return T, H, V, rank, n, x_ld
+
+
+def lmhead_adapters_fwd(base, x, down, up, adapter_ids, scale, out, workspace, stream=None):
+    """C ``lmhead_adapters_fwd`` on torch tensors; returns the status code."""
+    T, H, V, rank, n, x_ld = _check_adapters(x, down, up, adapter_ids, scale)
+    kind, ld = _check_rows(base, "base", (T, V))
+    _, out_ld = _check_rows(out, "out", (T, V), (base.dtype,))
+    _check_workspace(workspace)
+    dev = _one_device(base, x, down, up, adapter_ids, scale, out, workspace)
+    return _call(library().lmhead_adapters_fwd, dev, stream, base.data_ptr(), kind, ld,
+                 x.data_ptr(), x_ld, down.data_ptr(), up.data_ptr(), _ptr(adapter_ids), _ptr(scale),
+                 T, H, V, rank, n, out.data_ptr(), out_ld, workspace.data_ptr(), workspace.nbytes)
+
+
+def lmhead_adapters_bwd(grad_out, x, down, up, adapter_ids, scale, dx, accumulate_dx, d_down, d_up,
+                        accumulate, workspace, stream=None):
+    """C ``lmhead_adapters_bwd`` on torch tensors; returns the status code."""
+    T, H, V, rank, n, x_ld = _check_adapters(x, down, up, adapter_ids, scale)
+    kind, ld = _check_rows(grad_out, "grad_out", (T, V))
+    f32 = _torch.float32
+    dx_ld = 0 if dx is None else _check_rows(dx, "dx", (T, H), (f32,))[1]
+    _check_tensor(d_down, "d_down", f32, (n, rank, H), allow_none=True)
+    _check_tensor(d_up, "d_up", f32, (n, rank, V), allow_none=True)
+    _check_workspace(workspace)
+    dev = _one_device(grad_out, x, down, up, adapter_ids, scale, dx, d_down, d_up, workspace)
+    return _call(library().lmhead_adapters_bwd, dev, stream, grad_out.data_ptr(), kind, ld,
+                 x.data_ptr(), x_ld, down.data_ptr(), up.data_ptr(), _ptr(adapter_ids), _ptr(scale),
+                 T, H, V, rank, n, _ptr(dx), dx_ld, 1 if accumulate_dx else 0, _ptr(d_down),
+                 _ptr(d_up), 1 if accumulate else 0, workspace.data_ptr(), workspace.nbytes)
+
+
 def lmhead_beam_workspace_size(R, V, take):
     return int(library().lmhead_beam_workspace_size(R, V, take))
 
@@ -1302,3 +1357,58 @@ def beam_reorder(state, parents, dim=0, out=None, beams=0, stream=None):
     if rc:
         raise LmheadError(rc, "lmhead_beam_reorder")
     return out
+
+
+def _adapters_workspace(x, up):
+    n, rank, V = up.shape
+    size = lmhead_adapters_workspace_size(*x.shape, V, rank, n)
+    if size == 0:
+        raise LmheadError(2 if rank > 128 or n > 65535 else 1, "lmhead_adapters_workspace_size")
+    return _torch.empty(size, dtype=_torch.uint8, device=x.device)
+
+
+def adapters_forward(base, x, down, up, adapter_ids=None, scale=None, out=None, workspace=None,
+                     stream=None):
+    """base [T, V] plus each row's low-rank adapter of x [T, H]: down [n, rank, H] and up
+    [n, rank, V] bf16, adapter_ids [T] int32 (-1: none), scale [n].  Returns a new matrix, padded
+    like base, or out (``out=base`` adds in place)."""
+    if stream is not None:
+        return _made_on(stream, base, adapters_forward, base, x, down, up, adapter_ids, scale, out,
+                        workspace)
+    if out is None:
+        out = _rows_like(base)
+    elif _torch is None:
+        _bind_torch()
+    if workspace is None:
+        workspace = _adapters_workspace(x, up)
+    rc = lmhead_adapters_fwd(base, x, down, up, adapter_ids, scale, out, workspace)
+    if rc:
+        raise LmheadError(rc, "lmhead_adapters_fwd")
+    return out
+
+
+def adapters_backward(grad_out, x, down, up, adapter_ids=None, scale=None, dx=None,
+                      accumulate_dx=False, d_down=None, d_up=None, accumulate=False,
+                      workspace=None, stream=None):
+    """Returns (dx [T, H], d_down, d_up), fp32; base's gradient is grad_out itself."""
+    if stream is not None:
+        return _made_on(stream, grad_out, adapters_backward, grad_out, x, down, up, adapter_ids,
+                        scale, dx, accumulate_dx, d_down, d_up, accumulate, workspace)
+    if _torch is None:
+        _bind_torch()
+    torch = _torch
+    f32, where = torch.float32, grad_out.device
+    if dx is None:
+        dx = (torch.zeros if accumulate_dx else torch.empty)(x.shape, dtype=f32, device=where)
+    make = torch.zeros if accumulate else torch.empty
+    if d_down is None:
+        d_down = make(down.shape, dtype=f32, device=where)
+    if d_up is None:
+        d_up = make(up.shape, dtype=f32, device=where)
+    if workspace is None:
+        workspace = _adapters_workspace(x, up)
+    rc = lmhead_adapters_bwd(grad_out, x, down, up, adapter_ids, scale, dx, accumulate_dx, d_down,
+                             d_up, accumulate, workspace)
+    if rc:
+        raise LmheadError(rc, "lmhead_adapters_bwd")
+    return dx, d_down, d_up

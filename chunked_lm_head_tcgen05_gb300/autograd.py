@@ -23,9 +23,10 @@ import functools
 
 import torch
 
-from . import LMHEAD_OP_BWD, LMHEAD_OP_FWD, LmheadError, distill_logits_backward, \
+from . import LMHEAD_OP_BWD, LMHEAD_OP_FWD, LmheadError, adapters_forward, \
+    distill_logits_backward, \
     distill_logits_forward, embedding_backward, embedding_forward, layernorm_backward, \
-    layernorm_forward, lmhead_distill_bwd, \
+    layernorm_forward, lmhead_adapters_bwd, lmhead_adapters_workspace_size, lmhead_distill_bwd, \
     lmhead_distill_narrow_dweight, lmhead_distill_fwd, lmhead_distill_workspace_size, \
     lmhead_embedding_workspace_size, \
     lmhead_layernorm_workspace_size, \
@@ -401,3 +402,50 @@ def embedding(ids, weight, scale=1.0, padding_id=None, out_dtype=None, main_grad
     main_grad as in ``lmhead_logps``: a table tied to the head gets both gradients in it."""
     return Embedding.apply(ids, weight, float(scale), padding_id, out_dtype,
                            _main_grad(weight, main_grad))
+
+
+class Adapters(torch.autograd.Function):
+    """(base [T,V], x [T,H] bf16, down [n,rank,H] bf16, up [n,rank,V] bf16, adapter_ids [T] int32 or
+    None, scale [n] fp32 or None) -> base plus the adapters' share [T,V]."""
+
+    @staticmethod
+    def forward(ctx, base, x, down, up, adapter_ids, scale):
+        with _stream_workspace(_adapters_bytes(x, up), x.device) as ws:
+            out = adapters_forward(base, x, down, up, adapter_ids, scale, workspace=ws)
+        ctx.save_for_backward(x, down, up, adapter_ids, scale)
+        return out
+
+    @staticmethod
+    @_differentiable_once
+    def backward(ctx, g):
+        x, down, up, adapter_ids, scale = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        grads = [torch.empty(t.shape, dtype=torch.float32, device=t.device) if n else None
+                 for t, n in zip((x, down, up), need[1:4])]
+        if any(need[1:4]):
+            rows = g
+            if g.stride(1) != 1 or (g.shape[0] > 1 and g.stride(0) < g.shape[1]):
+                rows = g.contiguous()
+            dx, d_down, d_up = grads
+            with _stream_workspace(_adapters_bytes(x, up), x.device) as ws:
+                rc = lmhead_adapters_bwd(rows, x, down, up, adapter_ids, scale, dx, False, d_down,
+                                         d_up, False, ws)
+            if rc:
+                raise LmheadError(rc, "lmhead_adapters_bwd")
+        return (g if need[0] else None, *grads, None, None)
+
+
+def _adapters_bytes(x, up):
+    n, rank, V = up.shape
+    size = lmhead_adapters_workspace_size(*x.shape, V, rank, n)
+    if size == 0:
+        raise LmheadError(1, "lmhead_adapters_workspace_size")
+    return size
+
+
+def adapters(base, x, down, up, adapter_ids=None, scale=None):
+    """``chunked_lm_head_tcgen05_gb300.adapters_forward`` into a new matrix, differentiable in base,
+    x and both factors (not in scale)."""
+    if scale is not None and scale.requires_grad:
+        raise ValueError("adapters has no gradient for scale")
+    return Adapters.apply(base, x, down, up, adapter_ids, scale)

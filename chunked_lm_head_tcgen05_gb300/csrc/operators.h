@@ -239,4 +239,47 @@ struct BeamReorder {
 bool beam_reorder_fits(const BeamReorder& a);   // the grid
 cudaError_t launch_beam_reorder(const BeamReorder& a, cudaStream_t s);
 
+// ------------------------------------------------------------------ low-rank adapters
+constexpr int kMaxRank = 128;
+constexpr int kMaxAdapters = 65535;
+
+struct Adapters {
+  const void* x;         // [T, H] bf16
+  int64_t x_ld;
+  const void* down;      // [n, rank, H] bf16
+  const void* up;        // [n, rank, V] bf16
+  const int32_t* ids;    // [T], outside [0, n): no adapter; NULL: all 0
+  const float* scale;    // [n] or NULL (1)
+  int64_t T;
+  int H, V, rank, n;
+  void* workspace;       // adapters_workspace(...) bytes
+};
+
+struct AdaptersFwd {
+  Adapters a;
+  const void* base;      // [T, V]
+  int type;
+  int64_t base_ld;
+  void* out;             // [T, V], may be base
+  int64_t out_ld;
+};
+
+struct AdaptersBwd {
+  Adapters a;
+  const void* grad;      // [T, V]
+  int type;
+  int64_t grad_ld;
+  float* dx;             // [T, H] or NULL
+  int64_t dx_ld;
+  int accumulate_dx;
+  float* d_down;         // [n, rank, H] or NULL
+  float* d_up;           // [n, rank, V] or NULL
+  int accumulate;        // of d_down and d_up
+};
+
+size_t adapters_workspace(int64_t T, int H, int V, int rank, int n);
+bool adapters_fit(int64_t T, int width, int n);   // the grid of the widest product
+cudaError_t launch_adapters_fwd(const AdaptersFwd& a, cudaStream_t s);
+cudaError_t launch_adapters_bwd(const AdaptersBwd& a, cudaStream_t s);
+
 }  // namespace lmh

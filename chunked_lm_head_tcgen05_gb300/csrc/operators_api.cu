@@ -1,5 +1,5 @@
 // Host side of the C ABI of layer norm, distillation on held logits, logit
-// processing, embedding and beam search: argument checks and the stream-ordered launches.  No device
+// processing, embedding, low-rank adapters and beam search: argument checks and the stream-ordered launches.  No device
 // memory is allocated and nothing synchronises.
 #include "lmhead.h"
 
@@ -98,6 +98,25 @@ lmhead_status check_embedding(int64_t N, int32_t V, int32_t H, float scale, int 
     return LMHEAD_ERR_INVALID_ARG;
   if (N >= kMaxRows || V > kMaxVocab || H > kMaxWidth) return LMHEAD_ERR_UNSUPPORTED;
   return LMHEAD_OK;
+}
+
+// Sizes, types and operands that both directions of the adapters share.
+lmhead_status check_adapters(const Adapters& a, int type, int64_t ld) {
+  if (a.T < 0 || a.H <= 0 || a.V <= 0 || a.rank <= 0 || a.n <= 0 || !known_type(type) || ld < a.V || a.x_ld < a.H)
+    return LMHEAD_ERR_INVALID_ARG;
+  if (a.T >= kMaxRows || a.H > kMaxVocab || a.V > kMaxVocab || a.rank > kMaxRank || a.n > kMaxAdapters ||
+      !adapters_fit(a.T, a.H > a.V ? a.H : a.V, a.n))
+    return LMHEAD_ERR_UNSUPPORTED;
+  return LMHEAD_OK;
+}
+
+lmhead_status check_adapter_operands(const Adapters& a, size_t workspace_bytes) {
+  if (!a.x || !a.down || !a.up || !a.workspace) return LMHEAD_ERR_INVALID_ARG;
+  for (const void* p : {a.x, a.down, a.up})
+    if (!aligned_to(p, kBF16)) return LMHEAD_ERR_UNSUPPORTED;
+  if (!aligned_to(a.ids, kF32) || !aligned_to(a.scale, kF32) || (reinterpret_cast<uintptr_t>(a.workspace) & 255))
+    return LMHEAD_ERR_UNSUPPORTED;
+  return workspace_bytes < adapters_workspace(a.T, a.H, a.V, a.rank, a.n) ? LMHEAD_ERR_WORKSPACE_TOO_SMALL : LMHEAD_OK;
 }
 
 constexpr int32_t kMaxBeamVocab = 1 << 30;   // columns of the pieces past a row's end are counted too
@@ -342,6 +361,65 @@ lmhead_status lmhead_embedding_bwd(const void* dy, int dy_type, int64_t dy_ld, c
   const EmbedBwd a{dy, dy_type, dy_ld, ids, N, V, H, scale, skip, d_weight, d_weight_type,
                    accumulate ? 1 : 0, workspace};
   return status_of(launch_embed_bwd(a, s));
+}
+
+size_t lmhead_adapters_workspace_size(int64_t T, int32_t H, int32_t V, int32_t rank, int32_t n_adapters) {
+  const Adapters a{nullptr, H, nullptr, nullptr, nullptr, nullptr, T, H, V, rank, n_adapters, nullptr};
+  return check_adapters(a, kF32, V) == LMHEAD_OK ? adapters_workspace(T, H, V, rank, n_adapters) : 0;
+}
+
+lmhead_status lmhead_adapters_fwd(const void* base, int type, int64_t base_ld, const uint16_t* x,
+                                  int64_t x_ld, const uint16_t* down, const uint16_t* up,
+                                  const int32_t* adapter_ids, const float* scale, int64_t T,
+                                  int32_t H, int32_t V, int32_t rank, int32_t n_adapters,
+                                  void* out, int64_t out_ld, void* workspace,
+                                  size_t workspace_bytes, lmhead_stream_t stream) {
+  const Adapters a{x, x_ld, down, up, adapter_ids, scale, T, H, V, rank, n_adapters, workspace};
+  lmhead_status rc = check_adapters(a, type, base_ld);
+  if (rc != LMHEAD_OK) return rc;
+  if (out_ld < V) return LMHEAD_ERR_INVALID_ARG;
+  if (T == 0) return LMHEAD_OK;
+  if (!base || !out) return LMHEAD_ERR_INVALID_ARG;
+  if (!aligned_to(base, type) || !aligned_to(out, type)) return LMHEAD_ERR_UNSUPPORTED;
+  if (clash(base, base_ld, out, out_ld, T) || out == x || out == down || out == up) return LMHEAD_ERR_INVALID_ARG;
+  rc = check_adapter_operands(a, workspace_bytes);
+  if (rc != LMHEAD_OK) return rc;
+  const AdaptersFwd f{a, base, type, base_ld, out, out_ld};
+  return status_of(launch_adapters_fwd(f, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+lmhead_status lmhead_adapters_bwd(const void* grad_out, int type, int64_t grad_ld,
+                                  const uint16_t* x, int64_t x_ld, const uint16_t* down,
+                                  const uint16_t* up, const int32_t* adapter_ids,
+                                  const float* scale, int64_t T, int32_t H, int32_t V,
+                                  int32_t rank, int32_t n_adapters, float* dx, int64_t dx_ld,
+                                  int accumulate_dx, float* d_down, float* d_up, int accumulate,
+                                  void* workspace, size_t workspace_bytes,
+                                  lmhead_stream_t stream) {
+  const Adapters a{x, x_ld, down, up, adapter_ids, scale, T, H, V, rank, n_adapters, workspace};
+  lmhead_status rc = check_adapters(a, type, grad_ld);
+  if (rc != LMHEAD_OK) return rc;
+  if (dx && dx_ld < H) return LMHEAD_ERR_INVALID_ARG;
+  for (const float* p : {dx, d_down, d_up})
+    if (!aligned_to(p, kF32)) return LMHEAD_ERR_UNSUPPORTED;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (T == 0) {
+    const size_t factor = sizeof(float) * static_cast<size_t>(n_adapters) * static_cast<size_t>(rank);
+    if (d_down && !accumulate && cudaMemsetAsync(d_down, 0, factor * static_cast<size_t>(H), s) != cudaSuccess)
+      return LMHEAD_ERR_CUDA;
+    if (d_up && !accumulate && cudaMemsetAsync(d_up, 0, factor * static_cast<size_t>(V), s) != cudaSuccess)
+      return LMHEAD_ERR_CUDA;
+    return LMHEAD_OK;
+  }
+  if (!grad_out || (!dx && !d_down && !d_up)) return LMHEAD_ERR_INVALID_ARG;
+  if (!aligned_to(grad_out, type)) return LMHEAD_ERR_UNSUPPORTED;
+  for (const void* p : {static_cast<const void*>(dx), static_cast<const void*>(d_down), static_cast<const void*>(d_up)})
+    if (p && (p == grad_out || p == x || p == down || p == up)) return LMHEAD_ERR_INVALID_ARG;
+  if ((d_down && d_down == d_up) || (dx && (dx == d_down || dx == d_up))) return LMHEAD_ERR_INVALID_ARG;
+  rc = check_adapter_operands(a, workspace_bytes);
+  if (rc != LMHEAD_OK) return rc;
+  const AdaptersBwd b{a, grad_out, type, grad_ld, dx, dx_ld, accumulate_dx ? 1 : 0, d_down, d_up, accumulate ? 1 : 0};
+  return status_of(launch_adapters_bwd(b, s));
 }
 
 size_t lmhead_beam_workspace_size(int64_t R, int32_t V, int32_t take) {

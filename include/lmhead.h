@@ -563,6 +563,57 @@ lmhead_status lmhead_embedding_bwd(const void* dy, int dy_type, int64_t dy_ld, c
                                    lmhead_stream_t stream);
 
 /*
+ * Low-rank adapters of many requests at once, beside a shared projection whose result the
+ * caller holds (the head's logits, or any other product with x).  Row t with adapter
+ * a = adapter_ids[t]:
+ *   u_t   = scale_a x_t down_a^T              (rank numbers, fp32)
+ *   out_t = base_t + u_t up_a
+ * Backward, for the cotangent g of out (base's own cotangent is g itself):
+ *   du_t = scale_a g_t up_a^T,  dx_t (+)= du_t down_a
+ *   d_up_a (+)= sum_t u_t^T g_t,  d_down_a (+)= sum_t du_t^T x_t
+ *  x             [T, H] bf16, rows x_ld apart
+ *  down          [n_adapters, rank, H] bf16, up [n_adapters, rank, V] bf16: both with the
+ *                long side contiguous
+ *  adapter_ids   [T] int32, in any order; a row whose id is outside [0, n_adapters) (-1)
+ *                has no adapter: out = base, dx = 0.  NULL: every row has adapter 0.
+ *  scale         [n_adapters] fp32, or NULL (1)
+ *  base, out     [T, V] of element type `type`, rows base_ld / out_ld apart; out may be
+ *                base itself with the same ld (another: LMHEAD_ERR_INVALID_ARG), which
+ *                leaves rows without an adapter untouched
+ *  grad_out      [T, V] of `type`, rows grad_ld apart
+ *  dx            [T, H] fp32, rows dx_ld apart, or NULL; overwritten, or added to when
+ *                accumulate_dx != 0 (the head's d_hidden)
+ *  d_down, d_up  fp32, shaped as down and up, each may be NULL; overwritten (adapters
+ *                without rows get zeros), or added to when accumulate != 0
+ *  workspace     lmhead_adapters_workspace_size(T, H, V, rank, n_adapters) bytes, 256-byte
+ *                aligned
+ * Sums are fp32 in a fixed order (same inputs, same bits); u and du are used with all
+ * their bits, in sums for 16-bit results with 16 of them; results are rounded once.  The
+ * factors are taken to be finite.  1 <= rank <= 128, n_adapters <= 65535, T < 2^31 - 256,
+ * H and V < 2^31 - 1024, and at most 2^31 - 1 tiles of 256 columns and 64 rows of one
+ * adapter (LMHEAD_ERR_UNSUPPORTED beyond).  T == 0 is a no-op (the backward still zeroes
+ * d_down and d_up unless accumulate is set).
+ */
+size_t lmhead_adapters_workspace_size(int64_t T, int32_t H, int32_t V, int32_t rank,
+                                      int32_t n_adapters);
+
+lmhead_status lmhead_adapters_fwd(const void* base, int type, int64_t base_ld, const uint16_t* x,
+                                  int64_t x_ld, const uint16_t* down, const uint16_t* up,
+                                  const int32_t* adapter_ids, const float* scale, int64_t T,
+                                  int32_t H, int32_t V, int32_t rank, int32_t n_adapters,
+                                  void* out, int64_t out_ld, void* workspace,
+                                  size_t workspace_bytes, lmhead_stream_t stream);
+
+lmhead_status lmhead_adapters_bwd(const void* grad_out, int type, int64_t grad_ld,
+                                  const uint16_t* x, int64_t x_ld, const uint16_t* down,
+                                  const uint16_t* up, const int32_t* adapter_ids,
+                                  const float* scale, int64_t T, int32_t H, int32_t V,
+                                  int32_t rank, int32_t n_adapters, float* dx, int64_t dx_ld,
+                                  int accumulate_dx, float* d_down, float* d_up, int accumulate,
+                                  void* workspace, size_t workspace_bytes,
+                                  lmhead_stream_t stream);
+
+/*
  * One step of beam search: a group's best continuations.  Row r = group * beams + j of
  * logits [R, V] (element type `type`, rows ld apart) belongs to beam j of its group, whose
  * sequence has scores[r] so far.  With z = logits / temperature,
