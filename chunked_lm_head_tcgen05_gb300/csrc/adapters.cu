@@ -21,6 +21,8 @@
 // bf16 parts, which together hold the 24 bits of fp32; products of parts whose
 // result lies below 2^-24 of the whole are left out.  16-bit results take two
 // parts of u (2^-17 of the adapter's share, against their own 2^-9 or 2^-12).
+#include <type_traits>
+
 #include "element.cuh"
 #include "operators.h"
 #include "ptx.cuh"
@@ -37,6 +39,8 @@ constexpr int kBlock = 256;      // columns of the wide side per CTA (widen, out
 constexpr int kPad = 8;          // elements between rows in shared memory: no bank conflicts
 constexpr int kParts = 3;        // bf16 parts of u
 constexpr int kOuterRows = 32;   // rows of a step of outer_kernel
+constexpr int kManyCtas = 608;   // four per SM
+constexpr int kFewCtas = 304;    // two
 
 __host__ __device__ constexpr int round_rank(int r) { return (r + 15) / 16 * 16; }
 
@@ -93,28 +97,6 @@ __device__ __forceinline__ void split(float x, float (&part)[N]) {
   if (!isfinite(part[0])) {
 #pragma unroll
     for (int i = 1; i < N; ++i) part[i] = 0.f;
-  }
-}
-
-// Eight elements as bf16 pairs, part by part.
-template <typename T>
-__device__ __forceinline__ void to_parts(const Pack<T, 8>& q, uint4 (&part)[kPartsOf<T>]) {
-  if constexpr (kPartsOf<T> == 1) {
-    part[0] = *reinterpret_cast<const uint4*>(&q);
-  } else {
-    constexpr int N = kPartsOf<T>;
-    uint32_t w[N][4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 x = pair_of(q, e);
-      float lo[N], hi[N];
-      split(x.x, lo);
-      split(x.y, hi);
-#pragma unroll
-      for (int i = 0; i < N; ++i) w[i][e] = pack_bf16x2(lo[i], hi[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i) part[i] = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
   }
 }
 
@@ -178,107 +160,204 @@ __global__ void __launch_bounds__(1024) plan_kernel(Plan p) {
   if (tid == 0) *p.n_items = total;
 }
 
+// ------------------------------------------------------------------ tiles in shared memory
+// A tile's rows lie kPad elements apart more than they are long, so that the eight
+// 16-byte rows of a matrix load fall into different banks.  fp32 tiles are read as
+// pairs along their rows (narrow) or their columns (outer): 8 and 4 floats of padding.
+template <typename X>
+__device__ __forceinline__ void copy_chunk(X* dst, const X* src, bool on) {   // 16 bytes, or zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(on ? 16 : 0)
+               : "memory");
+}
+
+// Eight elements of a row (or zeros) into a tile: asynchronously, where both are aligned, or by
+// way of `q`.  `any`: an address that may be named where nothing is read.
+template <typename X, bool kAsync>
+__device__ __forceinline__ void fetch8(Pack<X, 8>& q, X* dst, const X* row, int c, int width, const X* any) {
+  const bool on = row != nullptr && c < width;
+  if constexpr (kAsync) {
+    constexpr int n = 16 / sizeof(X);
+#pragma unroll
+    for (int h = 0; h < 8; h += n) {
+      const bool part = on && c + h < width;      // width is a multiple of n
+      copy_chunk(dst + h, part ? row + c + h : any, part);
+    }
+  } else {
+    q = on ? load8(row, c, width) : Pack<X, 8>{};
+  }
+}
+template <typename X>
+__device__ __forceinline__ void put8(X* dst, const Pack<X, 8>& q) {
+  reinterpret_cast<uint4*>(dst)[0] = reinterpret_cast<const uint4*>(&q)[0];
+  if constexpr (sizeof(X) == 4) reinterpret_cast<uint4*>(dst)[1] = reinterpret_cast<const uint4*>(&q)[1];
+}
+
+// A pair of numbers as bf16 pairs, part by part.
+template <int N>
+__device__ __forceinline__ void pair_parts(float2 x, uint32_t (&w)[N]) {
+  float lo[N], hi[N];
+  split(x.x, lo);
+  split(x.y, hi);
+#pragma unroll
+  for (int i = 0; i < N; ++i) w[i] = pack_bf16x2(lo[i], hi[i]);
+}
+
 // ------------------------------------------------------------------ u = wide F^T
-// Grid (items, splits of the wide side, blocks of 8 NT ranks).  A warp holds 32 rows;
-// a thread reads 8 consecutive elements of its rows and of its ranks, so fragments
-// need no shared memory: any order of the summed index serves, if it is the same on
-// both sides.
+// Grid (items, splits of the wide side).  Both operands come tile by tile (kRows and
+// 8 NT rows of kTile columns) through a ring of asynchronous copies.  Warp = (16 rows,
+// half of the tile's columns); the halves meet at the end.  A first form that read
+// fragments straight from global memory, 64 bytes of each of 8 rows at a time, took 915 us
+// for 2,048 rows of 151,936 bf16 columns and 32 ranks.
+constexpr int kTile = 128;
+
 template <typename X, int NT>
+struct NarrowShape {
+  static constexpr int kStages = 3;
+  static constexpr int xs = kTile + kPad, fs = kTile + kPad;
+  static constexpr size_t stage = sizeof(X) * kRows * xs + 2 * size_t{8} * NT * fs;
+  static constexpr size_t bytes(bool async) { return async ? kStages * stage : stage; }
+  static_assert(sizeof(float) * 4 * 32 * NT * 4 <= stage, "the halves meet in one stage");
+};
+
+template <typename X, int NT, bool kAsync>
 __global__ void __launch_bounds__(kThreads) narrow_kernel(const X* wide, int64_t ld, const bf16* factor, int width,
                                                           int rank, Plan p, float* part, int per_split) {
-  constexpr int N = kPartsOf<X>;
-  constexpr int kUnroll = N > 1 || NT > 4 ? 1 : 2;
-  extern __shared__ float sums[];      // [warps][32][8 NT + 1]
+  using S = NarrowShape<X, NT>;
+  constexpr int N = kPartsOf<X>, kStages = kAsync ? S::kStages : 1;
+  constexpr int kX = kRows * kTile / 8 / kThreads, kF = NT * kTile / kThreads;
+  static_assert(kF >= 1, "chunks per thread");
+  extern __shared__ __align__(16) char shared[];
+  __shared__ int64_t offset[kRows];
   pdl_wait_prerequisites();
   pdl_launch_dependents();
   if (static_cast<int>(blockIdx.x) >= *p.n_items) return;
   const Item it = p.items[blockIdx.x];
   if (it.adapter >= p.n) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const int halves = it.count > 32 ? 2 : 1, slices = kWarps / halves, half = warp % halves, slice = warp / halves;
-  const int rank0 = blockIdx.z * 8 * NT;
-  const X* row[4];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  if (tid < it.count) offset[tid] = p.pos[it.first + tid] * ld;
+  __syncthreads();
+  auto x_tile = [&](int s) { return reinterpret_cast<X*>(shared + s * S::stage); };
+  auto f_tile = [&](int s) { return reinterpret_cast<bf16*>(shared + s * S::stage + sizeof(X) * kRows * S::xs); };
+  const int begin = blockIdx.y * per_split;
+  const int end = static_cast<int>(min(static_cast<int64_t>(begin) + per_split, static_cast<int64_t>(width)));
+  const bf16* const f0 = factor + static_cast<int64_t>(it.adapter) * rank * width;
+  Pack<X, 8> xq[kX];
+  Pack<bf16, 8> fq[kF];
+  // chunk i of a thread: row (i kThreads + tid) / 16, columns 8 (tid % 16)
+  const int row0 = tid / 16, col = tid % 16 * 8;
+  auto fetch = [&](int c0, int s) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int local = half * 32 + i * 8 + g;
-    row[i] = local < it.count ? wide + p.pos[it.first + local] * ld : nullptr;
-  }
-  const bf16* f[NT];
-#pragma unroll
-  for (int j = 0; j < NT; ++j)
-    f[j] = rank0 + 8 * j + g < rank
-               ? factor + (static_cast<int64_t>(it.adapter) * rank + rank0 + 8 * j + g) * width : nullptr;
-  float acc[2][NT][4] = {};
-  const int end = static_cast<int>(min(static_cast<int64_t>(blockIdx.y + 1) * per_split, static_cast<int64_t>(width)));
-  for (int c0 = blockIdx.y * per_split + slice * 32 * kUnroll; c0 < end; c0 += slices * 32 * kUnroll) {
-    Pack<X, 8> q[kUnroll][4];
-    uint4 b[kUnroll][NT];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int c = c0 + u * 32 + t * 8;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (row[i] && c < end)
-          q[u][i] = load8(row[i], c, end);
-        else
-          q[u][i] = Pack<X, 8>{};
-      }
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        b[u][j] = make_uint4(0u, 0u, 0u, 0u);
-        if (f[j] && c < end) {
-          const Pack<bf16, 8> v = load8(f[j], c, width);
-          b[u][j] = *reinterpret_cast<const uint4*>(&v);
-        }
-      }
+    for (int i = 0; i < kX; ++i) {
+      const int r = row0 + i * 16;
+      fetch8<X, kAsync>(xq[i], x_tile(s) + r * S::xs + col, r < it.count ? wide + offset[r] : nullptr, c0 + col, end,
+                        wide);
     }
-    // the sum of each stretch starts from zero, so that its small terms are not cut to
-    // the last bit of a long sum
-    float sum[2][NT][4] = {};
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      uint4 a[4][N];
+    for (int i = 0; i < kF; ++i) {
+      const int r = row0 + i * 16;
+      fetch8<bf16, kAsync>(fq[i], f_tile(s) + r * S::fs + col, r < rank ? f0 + static_cast<int64_t>(r) * width : nullptr,
+                           c0 + col, width, factor);
+    }
+  };
+  const int m0 = (warp & 3) * 16, k0 = (warp >> 2) * (kTile / 2);
+  const bool busy = m0 < it.count;
+  float acc[NT][4] = {};
+  if constexpr (kAsync) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) to_parts(q[u][i], a[i]);
+    for (int s = 0; s < kStages - 1; ++s) {
+      if (begin + s * kTile < end) fetch(begin + s * kTile, s);
+      copy_async_commit();
+    }
+  } else {
+    fetch(begin, 0);
+  }
+  int stage = 0;
+  for (int c0 = begin; c0 < end; c0 += kTile) {
+    if constexpr (kAsync) {
+      copy_async_wait<kStages - 2>();
+      __syncthreads();
+      const int ahead = c0 + (kStages - 1) * kTile;
+      if (ahead < end) fetch(ahead, (stage + kStages - 1) % kStages);
+      copy_async_commit();
+    } else {
+      __syncthreads();
 #pragma unroll
-      for (int s = N - 1; s >= 0; --s)
+      for (int i = 0; i < kX; ++i) put8(x_tile(0) + (row0 + i * 16) * S::xs + col, xq[i]);
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          const uint4 lo = a[2 * m][s], hi = a[2 * m + 1][s];
-          const uint32_t first[4] = {lo.x, hi.x, lo.y, hi.y}, second[4] = {lo.z, hi.z, lo.w, hi.w};
+      for (int i = 0; i < kF; ++i) put8(f_tile(0) + (row0 + i * 16) * S::fs + col, fq[i]);
+      __syncthreads();
+      if (c0 + kTile < end) fetch(c0 + kTile, 0);
+    }
+    if (busy) {
+      const X* const xt = x_tile(stage);
+      const bf16* const ft = f_tile(stage);
+      // a tile's sum starts from zero, so that its terms are not cut to the last bit of a long sum
+      float sum[NT][4] = {};
 #pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            mma(sum[m][j], first, b[u][j].x, b[u][j].y);
-            mma(sum[m][j], second, b[u][j].z, b[u][j].w);
+      for (int k = k0; k < k0 + kTile / 2; k += 16) {
+        uint32_t a[N][4];
+        if constexpr (sizeof(X) == 4) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t w[N];
+            pair_parts(*reinterpret_cast<const float2*>(xt + (m0 + (i & 1) * 8 + g) * S::xs + k + (i >> 1) * 8 + 2 * t), w);
+#pragma unroll
+            for (int s = 0; s < N; ++s) a[s][i] = w[s];
+          }
+        } else {
+          uint32_t raw[4];
+          load_matrices(raw, xt + (m0 + (lane >> 3 & 1) * 8 + (lane & 7)) * S::xs + k + (lane >> 4) * 8);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if constexpr (N == 1) {
+              a[0][i] = raw[i];
+            } else {
+              uint32_t w[N];
+              pair_parts(__half22float2(*reinterpret_cast<const __half2*>(&raw[i])), w);
+#pragma unroll
+              for (int s = 0; s < N; ++s) a[s][i] = w[s];
+            }
           }
         }
-    }
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+        for (int j = 0; j < NT; j += 2) {
+          uint32_t b[4];   // two blocks of 8 ranks
+          load_matrices(b, ft + (j * 8 + (lane >> 4) * 8 + (lane & 7)) * S::fs + k + (lane >> 3 & 1) * 8);
+#pragma unroll
+          for (int s = N - 1; s >= 0; --s) {
+            mma(sum[j], a[s], b[0], b[1]);
+            mma(sum[j + 1], a[s], b[2], b[3]);
+          }
+        }
+      }
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[m][j][e] += sum[m][j][e];
+        for (int e = 0; e < 4; ++e) acc[j][e] += sum[j][e];
+    }
+    stage = (stage + 1) % kStages;
   }
-  constexpr int kStride = 8 * NT + 1;
-  float* const own = sums + warp * 32 * kStride;
-#pragma unroll
-  for (int m = 0; m < 2; ++m)
+  if constexpr (kAsync) copy_async_wait<0>();
+  __syncthreads();
+  float* const meet = reinterpret_cast<float*>(shared) + ((warp & 3) * 32 + lane);   // [NT * 4][4 * 32]
+  if (warp >= 4) {
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        own[(m * 16 + (e >> 1) * 8 + g) * kStride + 8 * j + 2 * t + (e & 1)] = acc[m][j][e];
-  __syncthreads();
-  const int wide_rank = round_rank(rank);
-  for (int i = threadIdx.x; i < it.count * 8 * NT; i += kThreads) {
-    const int local = i / (8 * NT), c = i % (8 * NT);
-    if (rank0 + c >= rank) continue;
-    float s = 0.f;
-    for (int k = 0; k < slices; ++k)
-      s += sums[((k * halves + local / 32) * 32 + local % 32) * kStride + c];
-    part[(static_cast<int64_t>(blockIdx.y) * p.rows + it.first + local) * wide_rank + rank0 + c] = s;
+      for (int e = 0; e < 4; ++e) meet[(j * 4 + e) * 128] = acc[j][e];
   }
+  __syncthreads();
+  if (warp >= 4) return;
+  const int wide_rank = round_rank(rank);
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int r = m0 + (e >> 1) * 8 + g, c = j * 8 + 2 * t + (e & 1);
+      if (r < it.count && c < rank)
+        part[(static_cast<int64_t>(blockIdx.y) * p.rows + it.first + r) * wide_rank + c] =
+            acc[j][e] + meet[(j * 4 + e) * 128];
+    }
 }
 
 // u = scale * the sum of its splits, as bf16 parts [rows][kParts][round_rank(rank)].
@@ -304,64 +383,155 @@ __global__ void __launch_bounds__(kThreads) join_kernel(Plan p, const float* par
 }
 
 // ------------------------------------------------------------------ y = base + u F
-// Shared memory: F's block [wide_rank][kBlock + kPad], u [parts][kRows][wide_rank + kPad],
-// both bf16, and the share of 16 rows [16][kBlock + 4] in fp32.
-size_t widen_shared(int wide_rank, int parts) {
+// CTA = (block of columns, item), items of one block next to each other: they share F.
+// A warp has 32 columns.  Their order in shared memory is such that a thread's
+// results in four 8-column tiles are 8 consecutive columns: word w (two columns) of
+// the group of 32 lies at (w % 4) * 4 + w / 4.  So rows of y move 16 bytes a thread
+// straight between global memory and registers, all of an item's rows in flight.
+// Rows off 16-byte boundaries go column by column instead, their share by way of
+// the warp's own corner of shared memory.
+// Items of few rows (one token per request) have nothing to share: each thread
+// multiplies its 8 columns of F, read once from global memory, by the rows' u.
+constexpr int kFewRows = 8;
+constexpr int kFewAtOnce = 4;                // rows' sums in registers
+constexpr int kFewBlock = kThreads * 8;      // columns per CTA of such an item
+
+size_t widen_shared(int wide_rank, int parts, bool packs) {
   return 2 * (static_cast<size_t>(wide_rank) * (kBlock + kPad) + static_cast<size_t>(parts) * kRows * (wide_rank + kPad)) +
-         4 * 16 * (kBlock + 4);
+         (packs ? 0 : 4 * kWarps * 16 * 33);
 }
 
-// CTA = (block of columns, item), items of one block next to each other: they share F.
-template <typename Y, int VEC>
-__global__ void __launch_bounds__(kThreads) widen_kernel(const Y* base, int64_t base_ld, Y* out, int64_t out_ld,
+// Rows of one item times F, a thread per 8 columns.
+template <typename Y, bool kPacks>
+__device__ __forceinline__ void widen_few(const Y* base, int64_t base_ld, Y* out, int64_t out_ld, const bf16* f, int width,
+                                          int rank, const bf16* u, const Plan& p, const Item& it, float* us, int c0) {
+  const int wide_rank = round_rank(rank);
+  for (int i = threadIdx.x; i < it.count * rank; i += kThreads) {
+    const bf16* const q = u + static_cast<int64_t>(it.first + i / rank) * kParts * wide_rank + i % rank;
+    us[i / rank * kMaxRank + i % rank] =
+        __bfloat162float(q[0]) + (__bfloat162float(q[wide_rank]) + __bfloat162float(q[2 * wide_rank]));
+  }
+  __syncthreads();
+  const int c = c0 + threadIdx.x * 8;
+  if (c >= width) return;
+  for (int r0 = 0; r0 < it.count; r0 += kFewAtOnce) {
+    float2 acc[kFewAtOnce][4] = {};
+    constexpr int kAhead = 8;
+    for (int k0 = 0; k0 < rank; k0 += kAhead) {
+      Pack<bf16, 8> q[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (k0 + k < rank) q[k] = load8(f + static_cast<int64_t>(k0 + k) * width, c, width);
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        if (k0 + k >= rank) continue;
+#pragma unroll
+        for (int r = 0; r < kFewAtOnce; ++r) {
+          if (r0 + r >= it.count) continue;
+          const float w = us[(r0 + r) * kMaxRank + k0 + k];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[r][e] = fma2(pair_of(q[k], e), make_float2(w, w), acc[r][e]);
+        }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < kFewAtOnce; ++r) {
+      if (r0 + r >= it.count) continue;
+      const int64_t row = p.pos[it.first + r0 + r];
+      const Y* const src = base ? base + row * base_ld + c : nullptr;
+      Y* const dst = out + row * out_ld + c;
+      if (kPacks && c + 8 <= width) {
+        Pack<Y, 8> q{};
+        if (src) q = *reinterpret_cast<const Pack<Y, 8>*>(src);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) set_pair(q, e, add2(pair_of(q, e), acc[r][e]));
+        *reinterpret_cast<Pack<Y, 8>*>(dst) = q;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (c + e < width)
+            dst[e] = from_f32<Y>((src ? to_f32(src[e]) : 0.f) + (e & 1 ? acc[r][e / 2].y : acc[r][e / 2].x));
+      }
+    }
+  }
+}
+
+template <typename Y, bool kPacks>
+__global__ void __launch_bounds__(kThreads, 3) widen_kernel(const Y* base, int64_t base_ld, Y* out, int64_t out_ld,
                                                          const bf16* factor, int width, int rank, const bf16* u,
                                                          int parts, Plan p, bool factor_wide) {
-  constexpr int kEach = 16 * kBlock / kThreads / VEC;      // packs of 16 rows per thread
   extern __shared__ __align__(16) char shared[];
   pdl_wait_prerequisites();
   pdl_launch_dependents();
-  const int item = blockIdx.x % p.most;
+  const int item = blockIdx.x % p.most, block = blockIdx.x / p.most;
   if (item >= *p.n_items) return;
   const Item it = p.items[item];
   const bool bare = it.adapter >= p.n;
   if (bare && base == out) return;
+  const bf16* const f = factor + static_cast<int64_t>(it.adapter) * rank * width;
+  if (!bare && it.count <= kFewRows) {
+    __shared__ float us[kFewRows * kMaxRank];
+    if (block % (kFewBlock / kBlock) == 0)
+      widen_few<Y, kPacks>(base, base_ld, out, out_ld, f, width, rank, u, p, it, us, block * kBlock);
+    return;
+  }
   const int wide_rank = round_rank(rank), fs = kBlock + kPad, us = wide_rank + kPad;
   bf16* const F = reinterpret_cast<bf16*>(shared);
   bf16* const U = F + wide_rank * fs;
-  float* const share = reinterpret_cast<float*>(U + parts * kRows * us);
-  const int c0 = blockIdx.x / p.most * kBlock;
+  const int c0 = block * kBlock;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  const int my_row = tid / 16, my_col = tid % 16 * VEC;
-  Pack<Y, VEC> q[kEach];
+  float* const corner = reinterpret_cast<float*>(U + parts * kRows * us) + warp * 16 * 33;   // without kPacks
+  constexpr int kAhead = !kPacks ? 1 : sizeof(Y) == 4 ? 2 : 4;     // 16-row tiles in flight
+  const int mine = c0 + warp * 32 + (kPacks ? 8 * t : lane);       // this thread's columns
+  Pack<Y, 8> q[kAhead][2];
+  Y single[16];
+  auto row_of = [&](int r) { return static_cast<int64_t>(p.pos[it.first + r]); };
   auto fetch = [&](int r0) {
-    if (r0 + my_row >= it.count) return;
-    const Y* const src = base ? base + p.pos[it.first + r0 + my_row] * base_ld : nullptr;
+    if constexpr (kPacks) {
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int c = c0 + my_col + i * 16 * VEC;
-      if (!src)
-        q[i] = Pack<Y, VEC>{};
-      else if (c + VEC <= width)
-        q[i] = *reinterpret_cast<const Pack<Y, VEC>*>(src + c);
-      else
-        for (int e = 0; e < VEC; ++e)
-          if (c + e < width) q[i].v[e] = src[c + e];
+      for (int m = 0; m < kAhead; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = r0 + m * 16 + h * 8 + g;
+          q[m][h] = Pack<Y, 8>{};
+          if (r >= it.count || !base) continue;
+          const Y* const src = base + row_of(r) * base_ld + mine;
+          if (mine + 8 <= width) {
+            q[m][h] = *reinterpret_cast<const Pack<Y, 8>*>(src);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (mine + e < width) q[m][h].v[e] = src[e];
+          }
+        }
+    } else {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        single[r] = from_f32<Y>(0.f);
+        if (r0 + r < it.count && base && mine < width) single[r] = base[row_of(r0 + r) * base_ld + mine];
+      }
     }
   };
   fetch(0);
   if (!bare) {
-    const bf16* const f = factor + static_cast<int64_t>(it.adapter) * rank * width;
-    if (factor_wide) {
-      for (int i = tid; i < wide_rank * (kBlock / 8); i += kThreads) {
-        const int k = i / (kBlock / 8), c = i % (kBlock / 8) * 8;
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (k < rank && c0 + c < width) v = *reinterpret_cast<const uint4*>(f + static_cast<int64_t>(k) * width + c0 + c);
-        *reinterpret_cast<uint4*>(F + k * fs + c) = v;
+    for (int i = tid; i < wide_rank * (kBlock / 8); i += kThreads) {
+      const int k = i / (kBlock / 8), c = i % (kBlock / 8) * 8;
+      Pack<bf16, 8> v{};
+      if (k < rank && c0 + c < width) {
+        if (factor_wide)
+          *reinterpret_cast<uint4*>(&v) = *reinterpret_cast<const uint4*>(f + static_cast<int64_t>(k) * width + c0 + c);
+        else
+          v = load8(f + static_cast<int64_t>(k) * width, c0 + c, width);
       }
-    } else {
-      for (int i = tid; i < wide_rank * kBlock; i += kThreads) {
-        const int k = i / kBlock, c = i % kBlock;
-        F[k * fs + c] = k < rank && c0 + c < width ? f[static_cast<int64_t>(k) * width + c0 + c] : __float2bfloat16_rn(0.f);
+      if constexpr (kPacks) {
+        uint32_t* const dst = reinterpret_cast<uint32_t*>(F + k * fs + c / 32 * 32) + c % 32 / 8;
+        const uint4 w = *reinterpret_cast<const uint4*>(&v);
+        dst[0] = w.x;
+        dst[4] = w.y;
+        dst[8] = w.z;
+        dst[12] = w.w;
+      } else {
+        *reinterpret_cast<uint4*>(F + k * fs + c) = *reinterpret_cast<const uint4*>(&v);
       }
     }
     const int packs = wide_rank / 8;
@@ -372,135 +542,202 @@ __global__ void __launch_bounds__(kThreads) widen_kernel(const Y* base, int64_t 
         v = *reinterpret_cast<const uint4*>(u + (static_cast<int64_t>(it.first + r) * kParts + k) * wide_rank + c);
       *reinterpret_cast<uint4*>(U + (k * kRows + r) * us + c) = v;
     }
+    __syncthreads();
   }
-  __syncthreads();
-  for (int r0 = 0; r0 < it.count; r0 += 16) {
-    if (!bare) {
+  for (int r0 = 0; r0 < it.count; r0 += 16 * kAhead) {
+    if (r0) fetch(r0);
+#pragma unroll
+    for (int m = 0; m < kAhead; ++m) {
+      if (r0 + m * 16 >= it.count) break;
       float acc[4][4] = {};
-      for (int k = 0; k < wide_rank; k += 16) {
-        uint32_t b[2][4];
+      if (!bare) {
+        for (int k = 0; k < wide_rank; k += 16) {
+          uint32_t b[2][4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          load_matrices_turned(b[h], F + (k + (lane >> 3 & 1) * 8 + (lane & 7)) * fs + warp * 32 + h * 16 + (lane >> 4) * 8);
-        for (int s = parts - 1; s >= 0; --s) {
-          uint32_t a[4];
-          load_matrices(a, U + (s * kRows + r0 + (lane >> 3 & 1) * 8 + (lane & 7)) * us + k + (lane >> 4) * 8);
+          for (int h = 0; h < 2; ++h)
+            load_matrices_turned(b[h], F + (k + (lane >> 3 & 1) * 8 + (lane & 7)) * fs + warp * 32 + h * 16 + (lane >> 4) * 8);
+          for (int s = parts - 1; s >= 0; --s) {
+            uint32_t a[4];
+            load_matrices(a, U + (s * kRows + r0 + m * 16 + (lane >> 3 & 1) * 8 + (lane & 7)) * us + k + (lane >> 4) * 8);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) mma(acc[j], a, b[j >> 1][(j & 1) * 2], b[j >> 1][(j & 1) * 2 + 1]);
+            for (int j = 0; j < 4; ++j) mma(acc[j], a, b[j >> 1][(j & 1) * 2], b[j >> 1][(j & 1) * 2 + 1]);
+          }
         }
       }
+      if constexpr (kPacks) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+        for (int h = 0; h < 2; ++h) {
+          const int r = r0 + m * 16 + h * 8 + g;
+          if (r >= it.count) continue;
+          Pack<Y, 8> y;
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          *reinterpret_cast<float2*>(share + (h * 8 + g) * (kBlock + 4) + warp * 32 + j * 8 + 2 * t) =
-              make_float2(acc[j][2 * h], acc[j][2 * h + 1]);
-    }
-    __syncthreads();
-    if (r0 + my_row < it.count) {
-      Y* const dst = out + p.pos[it.first + r0 + my_row] * out_ld;
+          for (int j = 0; j < 4; ++j) {
+            const float2 old = pair_of(q[m][h], j);
+            set_pair(y, j, make_float2(old.x + acc[j][2 * h], old.y + acc[j][2 * h + 1]));
+          }
+          Y* const dst = out + row_of(r) * out_ld + mine;
+          if (mine + 8 <= width) {
+            *reinterpret_cast<Pack<Y, 8>*>(dst) = y;
+          } else {
 #pragma unroll
-      for (int i = 0; i < kEach; ++i) {
-        const int at = my_col + i * 16 * VEC, c = c0 + at;
-        if (!bare) {
-#pragma unroll
-          for (int e = 0; e < VEC; ++e)
-            q[i].v[e] = from_f32<Y>(to_f32(q[i].v[e]) + share[my_row * (kBlock + 4) + at + e]);
+            for (int e = 0; e < 8; ++e)
+              if (mine + e < width) dst[e] = y.v[e];
+          }
         }
-        if (c + VEC <= width)
-          *reinterpret_cast<Pack<Y, VEC>*>(dst + c) = q[i];
-        else
-          for (int e = 0; e < VEC; ++e)
-            if (c + e < width) dst[c + e] = q[i].v[e];
+      } else {
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) corner[((e >> 1) * 8 + g) * 33 + j * 8 + 2 * t + (e & 1)] = acc[j][e];
+        __syncwarp();
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (r0 + r < it.count && mine < width)
+            out[row_of(r0 + r) * out_ld + mine] = from_f32<Y>(to_f32(single[r]) + corner[r * 33 + lane]);
       }
     }
-    fetch(r0 + 16);
-    __syncthreads();
   }
 }
 
 // ------------------------------------------------------------------ dF = sum u^T wide
-// CTA = (block of columns, adapter, block of 16 RT ranks).  Steps of kOuterRows rows;
-// the next step's rows are fetched while the matrix instructions run.
+// CTA = (block of columns, adapter and part of its rows, block of 16 RT ranks).  Steps of
+// kOuterRows rows come through a ring of asynchronous copies; the rows' places are read a
+// step ahead.  A warp has 32 columns of the block.
 template <typename X, int RT>
-constexpr size_t outer_shared() {
-  return 2 * (static_cast<size_t>(kPartsOf<X>) * kOuterRows * (kBlock + kPad) +
-              static_cast<size_t>(kParts) * kOuterRows * (16 * RT + kPad));
-}
+struct OuterShape {
+  static constexpr int kStages = sizeof(X) == 4 ? 3 : 4;
+  static constexpr int fs = kBlock + (sizeof(X) == 4 ? 4 : kPad), us = 16 * RT + kPad;
+  static constexpr size_t x_bytes = sizeof(X) * kOuterRows * fs;
+  static constexpr size_t stage = x_bytes + 2 * size_t{kParts} * kOuterRows * us;
+  static constexpr size_t bytes(bool async) { return async ? kStages * stage : stage; }
+};
 
-template <typename X, int RT>
+template <typename X, int RT, bool kAsync>
 __global__ void __launch_bounds__(kThreads) outer_kernel(const X* wide, int64_t ld, int width, int rank, const bf16* u,
-                                                         Plan p, float* grad, int accumulate) {
-  constexpr int N = kPartsOf<X>, fs = kBlock + kPad, us = 16 * RT + kPad, kRowsEach = kOuterRows / kWarps;
+                                                         Plan p, float* grad, int accumulate, int row_splits,
+                                                         int64_t split_size) {
+  using S = OuterShape<X, RT>;
+  constexpr int N = kPartsOf<X>, kStages = kAsync ? S::kStages : 1, kRowsEach = kOuterRows / kWarps;
   constexpr int kPacks = (kOuterRows * kParts * RT * 2 + kThreads - 1) / kThreads;   // of u per thread
   extern __shared__ __align__(16) char shared[];
-  bf16* const W = reinterpret_cast<bf16*>(shared);     // [N][kOuterRows][fs]
-  bf16* const U = W + N * kOuterRows * fs;             // [kParts][kOuterRows][us]
   pdl_wait_prerequisites();
   pdl_launch_dependents();
-  const int c0 = blockIdx.x * kBlock, adapter = blockIdx.y, rank0 = blockIdx.z * 16 * RT;
+  const int c0 = blockIdx.x * kBlock, adapter = blockIdx.y / row_splits, part = blockIdx.y % row_splits;
+  const int rank0 = blockIdx.z * 16 * RT;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  const int from = p.starts[adapter], to = p.starts[adapter + 1], wide_rank = round_rank(rank);
-  Pack<X, 8> q[kRowsEach];
-  uint4 uq[kPacks];
-  auto fetch = [&](int r0) {
+  const int wide_rank = round_rank(rank);
+  const int all_from = p.starts[adapter], all_to = p.starts[adapter + 1];
+  const int each = ((all_to - all_from + row_splits - 1) / row_splits + kOuterRows - 1) / kOuterRows * kOuterRows;
+  const int from = min(all_from + part * each, all_to), to = min(from + each, all_to);
+  auto x_tile = [&](int s) { return reinterpret_cast<X*>(shared + s * S::stage); };
+  auto u_tile = [&](int s) { return reinterpret_cast<bf16*>(shared + s * S::stage + S::x_bytes); };
+  Pack<X, 8> xq[kRowsEach];
+  Pack<bf16, 8> uq[kPacks];
+  int place[kRowsEach];        // of the next step's rows
+  auto look = [&](int r0) {
 #pragma unroll
     for (int i = 0; i < kRowsEach; ++i) {
-      const int r = r0 + i * kWarps + warp, c = c0 + lane * 8;
-      q[i] = Pack<X, 8>{};
-      if (r < to && c < width) q[i] = load8(wide + p.pos[r] * ld, c, width);
-    }
-#pragma unroll
-    for (int i = 0; i < kPacks; ++i) {
-      const int at = i * kThreads + tid, k = at / (kOuterRows * RT * 2), r = at / (RT * 2) % kOuterRows,
-                c = rank0 + at % (RT * 2) * 8;
-      uq[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (k < kParts && r0 + r < to && c < wide_rank)
-        uq[i] = *reinterpret_cast<const uint4*>(u + (static_cast<int64_t>(r0 + r) * kParts + k) * wide_rank + c);
+      const int r = r0 + i * kWarps + warp;
+      place[i] = r < to ? p.pos[r] : -1;
     }
   };
-  float acc[RT][4][4] = {};
-  fetch(from);
-  for (int r0 = from; r0 < to; r0 += kOuterRows) {
-    __syncthreads();
+  auto fetch = [&](int r0, int s) {
 #pragma unroll
-    for (int i = 0; i < kRowsEach; ++i) {
-      uint4 part[N];
-      to_parts(q[i], part);
-#pragma unroll
-      for (int s = 0; s < N; ++s)
-        *reinterpret_cast<uint4*>(W + (s * kOuterRows + i * kWarps + warp) * fs + lane * 8) = part[s];
-    }
+    for (int i = 0; i < kRowsEach; ++i)
+      fetch8<X, kAsync>(xq[i], x_tile(s) + (i * kWarps + warp) * S::fs + lane * 8,
+                        place[i] >= 0 ? wide + place[i] * ld : nullptr, c0 + lane * 8, width, wide);
 #pragma unroll
     for (int i = 0; i < kPacks; ++i) {
       const int at = i * kThreads + tid, k = at / (kOuterRows * RT * 2), r = at / (RT * 2) % kOuterRows,
                 c = at % (RT * 2) * 8;
-      if (k < kParts) *reinterpret_cast<uint4*>(U + (k * kOuterRows + r) * us + c) = uq[i];
+      if (k < kParts)
+        fetch8<bf16, kAsync>(uq[i], u_tile(s) + (k * kOuterRows + r) * S::us + c,
+                             r0 + r < to ? u + (static_cast<int64_t>(r0 + r) * kParts + k) * wide_rank : nullptr,
+                             rank0 + c, wide_rank, u);
     }
-    __syncthreads();
-    fetch(r0 + kOuterRows);
+    look(r0 + kOuterRows);
+  };
+  float acc[RT][4][4] = {};
+  look(from);
+  if constexpr (kAsync) {
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) {
+      if (from + s * kOuterRows < to) fetch(from + s * kOuterRows, s);
+      copy_async_commit();
+    }
+  } else {
+    fetch(from, 0);
+  }
+  int stage = 0;
+  for (int r0 = from; r0 < to; r0 += kOuterRows) {
+    if constexpr (kAsync) {
+      copy_async_wait<kStages - 2>();
+      __syncthreads();
+      const int ahead = r0 + (kStages - 1) * kOuterRows;
+      if (ahead < to) fetch(ahead, (stage + kStages - 1) % kStages);
+      copy_async_commit();
+    } else {
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kRowsEach; ++i) put8(x_tile(0) + (i * kWarps + warp) * S::fs + lane * 8, xq[i]);
+#pragma unroll
+      for (int i = 0; i < kPacks; ++i) {
+        const int at = i * kThreads + tid, k = at / (kOuterRows * RT * 2), r = at / (RT * 2) % kOuterRows,
+                  c = at % (RT * 2) * 8;
+        if (k < kParts) put8(u_tile(0) + (k * kOuterRows + r) * S::us + c, uq[i]);
+      }
+      __syncthreads();
+      fetch(r0 + kOuterRows, 0);
+    }
+    const X* const W = x_tile(stage);
+    const bf16* const U = u_tile(stage);
+    // a step's sum starts from zero, so that its terms are not cut to the last bit of a long sum
     float sum[RT][4][4] = {};
 #pragma unroll
     for (int k = 0; k < kOuterRows; k += 16) {
-      uint32_t b[N][2][4];
+      uint32_t b[N][4][2];
+      if constexpr (sizeof(X) == 4) {
 #pragma unroll
-      for (int s = 0; s < N; ++s)
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          load_matrices_turned(b[s][h], W + (s * kOuterRows + k + (lane >> 3 & 1) * 8 + (lane & 7)) * fs + warp * 32 +
-                                            h * 16 + (lane >> 4) * 8);
+          for (int h = 0; h < 2; ++h) {
+            const X* const at = W + (k + h * 8 + 2 * t) * S::fs + warp * 32 + j * 8 + g;
+            uint32_t w[N];
+            pair_parts(make_float2(at[0], at[S::fs]), w);
+#pragma unroll
+            for (int s = 0; s < N; ++s) b[s][j][h] = w[s];
+          }
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t raw[4];
+          load_matrices_turned(raw, W + (k + (lane >> 3 & 1) * 8 + (lane & 7)) * S::fs + warp * 32 + h * 16 + (lane >> 4) * 8);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if constexpr (N == 1) {
+              b[0][2 * h + (i >> 1)][i & 1] = raw[i];
+            } else {
+              uint32_t w[N];
+              pair_parts(__half22float2(*reinterpret_cast<const __half2*>(&raw[i])), w);
+#pragma unroll
+              for (int s = 0; s < N; ++s) b[s][2 * h + (i >> 1)][i & 1] = w[s];
+            }
+          }
+        }
+      }
 #pragma unroll
       for (int v = kParts - 1; v >= 0; --v)
 #pragma unroll
         for (int m = 0; m < RT; ++m) {
           uint32_t a[4];
-          load_matrices_turned(a, U + (v * kOuterRows + k + (lane >> 4) * 8 + (lane & 7)) * us + m * 16 +
+          load_matrices_turned(a, U + (v * kOuterRows + k + (lane >> 4) * 8 + (lane & 7)) * S::us + m * 16 +
                                       (lane >> 3 & 1) * 8);
 #pragma unroll
           for (int s = N - 1; s >= 0; --s)
             if (s + v < kParts) {
 #pragma unroll
-              for (int j = 0; j < 4; ++j) mma(sum[m][j], a, b[s][j >> 1][(j & 1) * 2], b[s][j >> 1][(j & 1) * 2 + 1]);
+              for (int j = 0; j < 4; ++j) mma(sum[m][j], a, b[s][j][0], b[s][j][1]);
             }
         }
     }
@@ -510,15 +747,18 @@ __global__ void __launch_bounds__(kThreads) outer_kernel(const X* wide, int64_t 
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[m][j][e] += sum[m][j][e];
+    stage = (stage + 1) % kStages;
   }
-  if (accumulate && from == to) return;
+  if constexpr (kAsync) copy_async_wait<0>();
+  if (accumulate && all_from == all_to) return;
+  float* const result = grad + part * split_size;
 #pragma unroll
   for (int m = 0; m < RT; ++m)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int r = rank0 + m * 16 + h * 8 + g;
       if (r >= rank) continue;
-      float* const dst = grad + (static_cast<int64_t>(adapter) * rank + r) * width;
+      float* const dst = result + (static_cast<int64_t>(adapter) * rank + r) * width;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -527,6 +767,19 @@ __global__ void __launch_bounds__(kThreads) outer_kernel(const X* wide, int64_t 
           if (c < width) dst[c] = accumulate ? dst[c] + acc[m][j][2 * h + e] : acc[m][j][2 * h + e];
         }
     }
+}
+
+// dF = the sum of its row splits.
+__global__ void __launch_bounds__(kThreads) add_splits_kernel(const float* part, int splits, int64_t size, float* grad,
+                                                              int accumulate) {
+  pdl_wait_prerequisites();
+  pdl_launch_dependents();
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  if (i >= size) return;
+  float s = 0.f;
+#pragma unroll 4
+  for (int k = 0; k < splits; ++k) s += part[k * size + i];
+  grad[i] = accumulate ? grad[i] + s : s;
 }
 
 // ------------------------------------------------------------------ host
@@ -543,20 +796,29 @@ auto by_type(int type, F&& f) {
 
 int64_t most_items(int64_t rows, int n) { return rows / kRows + (n + 1 < rows ? n + 1 : rows) + 1; }
 
-// Splits of the wide side: CTAs enough for the GPU, at least 1,024 columns each.
+// Splits of the wide side: CTAs enough for the GPU, at least 512 columns each.
 int splits_of(int64_t rows, int width, int& per_split) {
   const int64_t items = (rows + kRows - 1) / kRows;
-  int64_t splits = (608 + items - 1) / items;
-  const int64_t most = (width + 1023) / 1024;
+  int64_t splits = (kManyCtas + items - 1) / items;
+  const int64_t most = (width + 511) / 512;
   if (splits > most) splits = most;
-  per_split = static_cast<int>(((width + splits - 1) / splits + 255) / 256 * 256);
+  per_split = static_cast<int>(((width + splits - 1) / splits + kTile - 1) / kTile * kTile);
   return (width - 1) / per_split + 1;
+}
+
+// Splits of an adapter's rows, where columns and adapters alone leave SMs idle.
+int row_splits_of(int64_t rows, int width, int n) {
+  const int64_t ctas = (static_cast<int64_t>(width) + kBlock - 1) / kBlock * n;
+  int64_t splits = kFewCtas / ctas;
+  const int64_t most = (rows / n + 4 * kOuterRows - 1) / (4 * kOuterRows);   // four steps each at least
+  if (splits > most) splits = most;
+  return splits < 1 ? 1 : static_cast<int>(splits);
 }
 
 struct Space {
   Plan plan;
   bf16 *u, *du;
-  float* part;
+  float* part;       // splits of u, or of dF
   size_t bytes;
 };
 
@@ -581,23 +843,39 @@ Space lay_out(void* workspace, int64_t T, int H, int V, int rank, int n) {
   const size_t wide_rank = static_cast<size_t>(round_rank(rank));
   s.u = reinterpret_cast<bf16*>(take(2 * kParts * wide_rank * rows));
   s.du = reinterpret_cast<bf16*>(take(2 * kParts * wide_rank * rows));
-  int per;
-  const int a = splits_of(rows > 0 ? rows : 1, H, per), b = splits_of(rows > 0 ? rows : 1, V, per);
-  s.part = reinterpret_cast<float*>(take(4 * wide_rank * rows * static_cast<size_t>(a > b ? a : b)));
-  // (a last part of fewer rows has more splits, of at most 64 * (608 + 607) rows in all)
+  // a last part of fewer rows has more splits, of at most kRows (kManyCtas + items) rows in
+  // all where there are fewer than kManyCtas items: below kSortMost
+  size_t most = 0;
+  for (const int width : {H, V}) {
+    int per;
+    const size_t narrow = wide_rank * rows * static_cast<size_t>(splits_of(rows > 0 ? rows : 1, width, per));
+    // row splits fill kFewCtas blocks at most, whatever the rows
+    const int splits = row_splits_of(kSortMost, width, n);
+    const size_t outer = splits > 1 ? static_cast<size_t>(splits) * n * rank * width : 0;
+    most = narrow > most ? narrow : most;
+    most = outer > most ? outer : most;
+  }
+  s.part = reinterpret_cast<float*>(take(sizeof(float) * most));
   s.bytes = at;
   return s;
 }
 
-template <typename X, int NT>
+// Whether rows can be copied 16 bytes at a time.
+template <typename X>
+bool whole_chunks(const X* p, int64_t ld, int width) {
+  constexpr int n = kVec<X>;
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % n == 0 && width % n == 0;
+}
+
+template <typename X, int NT, bool kAsync>
 cudaError_t narrow_of(const X* wide, int64_t ld, const bf16* factor, int width, int rank, const Plan& p, float* part,
                       int splits, int per_split, cudaStream_t s) {
   static std::atomic<int> ready[64];
-  constexpr size_t smem = 4 * kWarps * 32 * (8 * NT + 1);
-  const cudaError_t e = allow_shared(ready, reinterpret_cast<const void*>(narrow_kernel<X, NT>), smem);
+  constexpr size_t smem = NarrowShape<X, NT>::bytes(kAsync);
+  const cudaError_t e = allow_shared(ready, reinterpret_cast<const void*>(narrow_kernel<X, NT, kAsync>), smem);
   if (e != cudaSuccess) return e;
-  return launch_dependent(narrow_kernel<X, NT>, dim3(p.most, splits, (rank + 8 * NT - 1) / (8 * NT)), kThreads, smem, 1,
-                          s, wide, ld, factor, width, rank, p, part, per_split);
+  return launch_dependent(narrow_kernel<X, NT, kAsync>, dim3(p.most, splits), kThreads, smem, 1, s, wide, ld, factor,
+                          width, rank, p, part, per_split);
 }
 
 // u (as parts) of every row with an adapter.
@@ -607,11 +885,17 @@ cudaError_t narrow(const char* name, const X* wide, int64_t ld, const void* fact
   int per_split;
   const int splits = splits_of(z.plan.rows, width, per_split);
   const bf16* const f = static_cast<const bf16*>(factor);
+  const bool async = whole_chunks(wide, ld, width) && whole_chunks(f, width, width);
+  auto run = [&](auto nt) {
+    constexpr int NT = decltype(nt)::value;
+    return async ? narrow_of<X, NT, true>(wide, ld, f, width, a.rank, z.plan, z.part, splits, per_split, s)
+                 : narrow_of<X, NT, false>(wide, ld, f, width, a.rank, z.plan, z.part, splits, per_split, s);
+  };
   cudaError_t e = traced_launch(name, s, [&] {
-    if (a.rank <= 8) return narrow_of<X, 1>(wide, ld, f, width, a.rank, z.plan, z.part, splits, per_split, s);
-    if (a.rank <= 16) return narrow_of<X, 2>(wide, ld, f, width, a.rank, z.plan, z.part, splits, per_split, s);
-    if (a.rank <= 32) return narrow_of<X, 4>(wide, ld, f, width, a.rank, z.plan, z.part, splits, per_split, s);
-    return narrow_of<X, 8>(wide, ld, f, width, a.rank, z.plan, z.part, splits, per_split, s);
+    if (a.rank <= 16) return run(std::integral_constant<int, 2>{});
+    if (a.rank <= 32) return run(std::integral_constant<int, 4>{});
+    if (a.rank <= 64) return run(std::integral_constant<int, 8>{});
+    return run(std::integral_constant<int, 16>{});
   });
   if (e != cudaSuccess) return e;
   const int64_t n = static_cast<int64_t>(z.plan.rows) * round_rank(a.rank);
@@ -621,18 +905,17 @@ cudaError_t narrow(const char* name, const X* wide, int64_t ld, const void* fact
   });
 }
 
-template <typename Y, int VEC>
+template <typename Y, bool kPacks>
 cudaError_t widen_of(const Y* base, int64_t base_ld, Y* out, int64_t out_ld, const bf16* factor, int width, int rank,
                      const bf16* u, int parts, const Plan& p, cudaStream_t s) {
   static std::atomic<int> ready[64];
-  const cudaError_t e = allow_shared(ready, reinterpret_cast<const void*>(widen_kernel<Y, VEC>),
-                                     widen_shared(round_rank(kMaxRank), kParts));
+  const cudaError_t e = allow_shared(ready, reinterpret_cast<const void*>(widen_kernel<Y, kPacks>),
+                                     widen_shared(round_rank(kMaxRank), kParts, kPacks));
   if (e != cudaSuccess) return e;
   const int64_t blocks = (static_cast<int64_t>(width) + kBlock - 1) / kBlock;
-  const bool factor_wide = reinterpret_cast<uintptr_t>(factor) % 16 == 0 && width % 8 == 0;
-  return launch_dependent(widen_kernel<Y, VEC>, dim3(static_cast<unsigned>(blocks * p.most)), kThreads,
-                          widen_shared(round_rank(rank), parts), 1, s, base, base_ld, out, out_ld, factor, width, rank, u,
-                          parts, p, factor_wide);
+  return launch_dependent(widen_kernel<Y, kPacks>, dim3(static_cast<unsigned>(blocks * p.most)), kThreads,
+                          widen_shared(round_rank(rank), parts, kPacks), 1, s, base, base_ld, out, out_ld, factor, width,
+                          rank, u, parts, p, whole_chunks(factor, width, width));
 }
 
 template <typename Y>
@@ -644,30 +927,45 @@ cudaError_t widen(const char* name, const Y* base, int64_t base_ld, Y* out, int6
                      base_ld % VEC == 0 && out_ld % VEC == 0;
   const int parts = sizeof(Y) == 4 ? kParts : 2;
   return traced_launch(name, s, [&] {
-    return packs ? widen_of<Y, VEC>(base, base_ld, out, out_ld, f, width, rank, u, parts, p, s)
-                 : widen_of<Y, 1>(base, base_ld, out, out_ld, f, width, rank, u, parts, p, s);
+    return packs ? widen_of<Y, true>(base, base_ld, out, out_ld, f, width, rank, u, parts, p, s)
+                 : widen_of<Y, false>(base, base_ld, out, out_ld, f, width, rank, u, parts, p, s);
   });
 }
 
-template <typename X, int RT>
-cudaError_t outer_of(const X* wide, int64_t ld, int width, int rank, const bf16* u, const Plan& p, float* grad,
+template <typename X, int RT, bool kAsync>
+cudaError_t outer_of(const char* name, const X* wide, int64_t ld, int width, int rank, const bf16* u, const Space& z, float* grad,
                      int accumulate, cudaStream_t s) {
   static std::atomic<int> ready[64];
-  constexpr size_t smem = outer_shared<X, RT>();
-  const cudaError_t e = allow_shared(ready, reinterpret_cast<const void*>(outer_kernel<X, RT>), smem);
+  constexpr size_t smem = OuterShape<X, RT>::bytes(kAsync);
+  const cudaError_t e = allow_shared(ready, reinterpret_cast<const void*>(outer_kernel<X, RT, kAsync>), smem);
   if (e != cudaSuccess) return e;
-  return launch_dependent(outer_kernel<X, RT>, dim3((width + kBlock - 1) / kBlock, p.n, (rank + 16 * RT - 1) / (16 * RT)),
-                          kThreads, smem, 1, s, wide, ld, width, rank, u, p, grad, accumulate);
+  const int splits = row_splits_of(z.plan.rows, width, z.plan.n);
+  const int64_t size = static_cast<int64_t>(z.plan.n) * rank * width;
+  const dim3 grid((width + kBlock - 1) / kBlock, z.plan.n * splits, (rank + 16 * RT - 1) / (16 * RT));
+  const bool whole = splits == 1;
+  const cudaError_t r = traced_launch(name, s, [&] {
+    return launch_dependent(outer_kernel<X, RT, kAsync>, grid, kThreads, smem, 1, s, wide, ld, width, rank, u, z.plan,
+                            whole ? grad : z.part, whole ? accumulate : 0, splits, size);
+  });
+  if (r != cudaSuccess || whole) return r;
+  return traced_launch("adapters_add_splits", s, [&] {
+    return launch_dependent(add_splits_kernel, dim3(static_cast<unsigned>((size + kThreads - 1) / kThreads)), kThreads,
+                            0, 1, s, static_cast<const float*>(z.part), splits, size, grad, accumulate);
+  });
 }
 
 template <typename X>
-cudaError_t outer(const char* name, const X* wide, int64_t ld, int width, int rank, const bf16* u, const Plan& p,
+cudaError_t outer(const char* name, const X* wide, int64_t ld, int width, int rank, const bf16* u, const Space& z,
                   float* grad, int accumulate, cudaStream_t s) {
-  return traced_launch(name, s, [&] {
-    if (rank <= 16) return outer_of<X, 1>(wide, ld, width, rank, u, p, grad, accumulate, s);
-    if (rank <= 32) return outer_of<X, 2>(wide, ld, width, rank, u, p, grad, accumulate, s);
-    return outer_of<X, 4>(wide, ld, width, rank, u, p, grad, accumulate, s);
-  });
+  const bool async = whole_chunks(wide, ld, width);
+  auto run = [&](auto rt) {
+    constexpr int RT = decltype(rt)::value;
+    return async ? outer_of<X, RT, true>(name, wide, ld, width, rank, u, z, grad, accumulate, s)
+                 : outer_of<X, RT, false>(name, wide, ld, width, rank, u, z, grad, accumulate, s);
+  };
+  if (rank <= 16) return run(std::integral_constant<int, 1>{});
+  if (rank <= 32) return run(std::integral_constant<int, 2>{});
+  return run(std::integral_constant<int, 4>{});
 }
 
 cudaError_t plan_rows(const Adapters& a, int64_t first, Space& z, cudaStream_t s) {
@@ -729,11 +1027,11 @@ cudaError_t launch_adapters_bwd(const AdaptersBwd& b, cudaStream_t s) {
       cudaError_t r = cudaSuccess;
       if (b.dx || b.d_down) r = narrow("adapters_narrow_grad", g, b.grad_ld, a.up, a.V, a, z, z.du, s);
       if (r == cudaSuccess && b.d_up)
-        r = outer("adapters_d_up", g, b.grad_ld, a.V, a.rank, z.u, z.plan, b.d_up, accumulate, s);
+        r = outer("adapters_d_up", g, b.grad_ld, a.V, a.rank, z.u, z, b.d_up, accumulate, s);
       return r;
     });
     if (e == cudaSuccess && b.d_down)
-      e = outer("adapters_d_down", x, a.x_ld, a.H, a.rank, z.du, z.plan, b.d_down, accumulate, s);
+      e = outer("adapters_d_down", x, a.x_ld, a.H, a.rank, z.du, z, b.d_down, accumulate, s);
     if (e == cudaSuccess && b.dx) {
       float* const dx = b.dx + first * b.dx_ld;
       e = widen("adapters_dx", b.accumulate_dx ? static_cast<const float*>(dx) : nullptr, b.dx_ld, dx, b.dx_ld, a.down,
