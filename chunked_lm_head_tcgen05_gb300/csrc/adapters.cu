@@ -38,6 +38,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kBlock = 256;      // columns of the wide side per CTA (widen, outer)
 constexpr int kPad = 8;          // elements between rows in shared memory: no bank conflicts
 constexpr int kParts = 3;        // bf16 parts of u
+constexpr int kFewRows = 8;      // of a run whose factor is not shared
 constexpr int kOuterRows = 32;   // rows of a step of outer_kernel
 constexpr int kManyCtas = 608;   // four per SM
 constexpr int kFewCtas = 304;    // two
@@ -59,12 +60,15 @@ struct Item {
 
 struct Plan {
   int* live;         // rows with an adapter
-  int* n_items;
+  int* counts;       // of items, runs and few
   int32_t* keys;     // [rows] adapters in order
   int32_t* pos;      // [rows] their rows
   int* starts;       // [n + 2] first sorted place of each adapter, of the rows without, and the end
-  Item* items;
-  int most;          // items at most
+  Item* items;       // up to kRows rows of one adapter each
+  Item* runs;        // up to run_rows rows each, those of at most kFewRows rows apart, in few
+  Item* few;
+  int most;          // items at most, so also of the other lists
+  int run_rows;
   int rows;
   int n;
 };
@@ -127,7 +131,7 @@ __device__ __forceinline__ Pack<T, 8> load8(const T* row, int c, int width) {
 
 // ------------------------------------------------------------------ items
 __global__ void __launch_bounds__(1024) plan_kernel(Plan p) {
-  __shared__ int sums[32], total;
+  __shared__ int sums[3][32], total[3];
   pdl_wait_prerequisites();
   pdl_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -135,29 +139,45 @@ __global__ void __launch_bounds__(1024) plan_kernel(Plan p) {
     const int before = g == 0 ? -1 : p.keys[g - 1], here = g == p.rows ? p.n + 1 : p.keys[g];
     for (int a = before + 1; a <= here; ++a) p.starts[a] = g;
   }
-  if (tid == 0) total = 0;
+  if (tid < 3) total[tid] = 0;
   __syncthreads();
   for (int a0 = 0; a0 <= p.n; a0 += 1024) {
     const int a = a0 + tid;
     const int first = a <= p.n ? p.starts[a] : 0, count = a <= p.n ? p.starts[a + 1] - first : 0;
-    const int mine = (count + kRows - 1) / kRows;
-    int scan = mine;
+    // a last run of few rows is listed with the few, if its rows have an adapter
+    const int rest = count % p.run_rows, is_few = rest > 0 && rest <= kFewRows && a < p.n;
+    const int mine[3] = {(count + kRows - 1) / kRows, (count + p.run_rows - 1) / p.run_rows - is_few, is_few};
+    int scan[3];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, scan, o);
-      if (lane >= o) scan += v;
+    for (int l = 0; l < 3; ++l) {
+      scan[l] = mine[l];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, scan[l], o);
+        if (lane >= o) scan[l] += v;
+      }
+      if (lane == 31) sums[l][warp] = scan[l];
     }
-    if (lane == 31) sums[warp] = scan;
     __syncthreads();
-    int at = total + scan - mine;
-    for (int w = 0; w < warp; ++w) at += sums[w];
-    for (int i = 0; i < mine; ++i)
-      p.items[at + i] = Item{a, first + i * kRows, min(kRows, count - i * kRows), 0};
+    int at[3];
+#pragma unroll
+    for (int l = 0; l < 3; ++l) {
+      at[l] = total[l] + scan[l] - mine[l];
+      for (int w = 0; w < warp; ++w) at[l] += sums[l][w];
+    }
+    for (int i = 0; i < mine[0]; ++i)
+      p.items[at[0] + i] = Item{a, first + i * kRows, min(kRows, count - i * kRows), 0};
+    for (int i = 0; i < mine[1]; ++i)
+      p.runs[at[1] + i] = Item{a, first + i * p.run_rows, min(p.run_rows, count - i * p.run_rows), 0};
+    if (is_few) p.few[at[2]] = Item{a, first + count - rest, rest, 0};
     __syncthreads();
-    if (tid == 1023) total = at + mine;
+    if (tid == 1023) {
+#pragma unroll
+      for (int l = 0; l < 3; ++l) total[l] = at[l] + mine[l];
+    }
     __syncthreads();
   }
-  if (tid == 0) *p.n_items = total;
+  if (tid < 3) p.counts[tid] = total[tid];
 }
 
 // ------------------------------------------------------------------ tiles in shared memory
@@ -230,7 +250,7 @@ __global__ void __launch_bounds__(kThreads) narrow_kernel(const X* wide, int64_t
   __shared__ int64_t offset[kRows];
   pdl_wait_prerequisites();
   pdl_launch_dependents();
-  if (static_cast<int>(blockIdx.x) >= *p.n_items) return;
+  if (static_cast<int>(blockIdx.x) >= p.counts[0]) return;
   const Item it = p.items[blockIdx.x];
   if (it.adapter >= p.n) return;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
@@ -383,199 +403,212 @@ __global__ void __launch_bounds__(kThreads) join_kernel(Plan p, const float* par
 }
 
 // ------------------------------------------------------------------ y = base + u F
-// CTA = (block of columns, item), items of one block next to each other: they share F.
+// Persistent grids over units of work.  widen_kernel: (block of columns, run of up to
+// `run_rows` rows of one adapter), runs of one block next to each other, so that they find F
+// in the L2.  F's block stays in registers (ranks up to 64) or shared memory for the
+// run, u comes 64 rows at a time, and y moves 16 rows at a time through a ring of
+// asynchronous copies in which each thread reads back what it copied itself: no
+// barrier but one per 64 rows.
 // A warp has 32 columns.  Their order in shared memory is such that a thread's
 // results in four 8-column tiles are 8 consecutive columns: word w (two columns) of
-// the group of 32 lies at (w % 4) * 4 + w / 4.  So rows of y move 16 bytes a thread
-// straight between global memory and registers, all of an item's rows in flight.
+// the group of 32 lies at (w % 4) * 4 + w / 4.  So rows of y move 16 bytes a thread.
 // Rows off 16-byte boundaries go column by column instead, their share by way of
 // the warp's own corner of shared memory.
-// Items of few rows (one token per request) have nothing to share: each thread
-// multiplies its 8 columns of F, read once from global memory, by the rows' u.
-constexpr int kFewRows = 8;
+// few_kernel takes the runs of few rows (one token per request), which have nothing to
+// share: each thread multiplies its 8 columns of F, read once, by the rows' u.
 constexpr int kFewAtOnce = 4;                // rows' sums in registers
-constexpr int kFewBlock = kThreads * 8;      // columns per CTA of such an item
+constexpr int kFewBlock = kThreads * 8;      // columns of such a unit
+constexpr int kMostRun = 512;
 
-size_t widen_shared(int wide_rank, int parts, bool packs) {
-  return 2 * (static_cast<size_t>(wide_rank) * (kBlock + kPad) + static_cast<size_t>(parts) * kRows * (wide_rank + kPad)) +
-         (packs ? 0 : 4 * kWarps * 16 * 33);
-}
+template <typename Y>
+constexpr int kPartsFor = sizeof(Y) == 4 ? kParts : 2;     // of u in a result of type Y
 
-// Rows of one item times F, a thread per 8 columns.
-template <typename Y, bool kPacks>
-__device__ __forceinline__ void widen_few(const Y* base, int64_t base_ld, Y* out, int64_t out_ld, const bf16* f, int width,
-                                          int rank, const bf16* u, const Plan& p, const Item& it, float* us, int c0) {
-  const int wide_rank = round_rank(rank);
-  for (int i = threadIdx.x; i < it.count * rank; i += kThreads) {
-    const bf16* const q = u + static_cast<int64_t>(it.first + i / rank) * kParts * wide_rank + i % rank;
-    us[i / rank * kMaxRank + i % rank] =
-        __bfloat162float(q[0]) + (__bfloat162float(q[wide_rank]) + __bfloat162float(q[2 * wide_rank]));
+template <typename Y, int KT>
+struct WidenShape {
+  static constexpr int kStages = sizeof(Y) == 4 ? 3 : 4;
+  static constexpr int kChunks = sizeof(Y) / 2;            // of 16 bytes: 8 columns of a row
+  static constexpr int fs = kBlock + kPad, us = 16 * KT + kPad, u_size = kPartsFor<Y> * kRows * us;
+  // F, two buffers of u, and the ring or the warps' corners
+  static constexpr size_t bytes(bool packs) {
+    return 2 * (size_t{16} * KT * fs + 2 * u_size) +
+           (packs ? size_t{16} * 2 * kChunks * kThreads * kStages : sizeof(float) * kWarps * 16 * 33);
   }
-  __syncthreads();
-  const int c = c0 + threadIdx.x * 8;
-  if (c >= width) return;
-  for (int r0 = 0; r0 < it.count; r0 += kFewAtOnce) {
-    float2 acc[kFewAtOnce][4] = {};
-    constexpr int kAhead = 8;
-    for (int k0 = 0; k0 < rank; k0 += kAhead) {
-      Pack<bf16, 8> q[kAhead];
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k)
-        if (k0 + k < rank) q[k] = load8(f + static_cast<int64_t>(k0 + k) * width, c, width);
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        if (k0 + k >= rank) continue;
-#pragma unroll
-        for (int r = 0; r < kFewAtOnce; ++r) {
-          if (r0 + r >= it.count) continue;
-          const float w = us[(r0 + r) * kMaxRank + k0 + k];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[r][e] = fma2(pair_of(q[k], e), make_float2(w, w), acc[r][e]);
-        }
-      }
-    }
-#pragma unroll
-    for (int r = 0; r < kFewAtOnce; ++r) {
-      if (r0 + r >= it.count) continue;
-      const int64_t row = p.pos[it.first + r0 + r];
-      const Y* const src = base ? base + row * base_ld + c : nullptr;
-      Y* const dst = out + row * out_ld + c;
-      if (kPacks && c + 8 <= width) {
-        Pack<Y, 8> q{};
-        if (src) q = *reinterpret_cast<const Pack<Y, 8>*>(src);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) set_pair(q, e, add2(pair_of(q, e), acc[r][e]));
-        *reinterpret_cast<Pack<Y, 8>*>(dst) = q;
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (c + e < width)
-            dst[e] = from_f32<Y>((src ? to_f32(src[e]) : 0.f) + (e & 1 ? acc[r][e / 2].y : acc[r][e / 2].x));
-      }
-    }
-  }
-}
+};
 
-template <typename Y, bool kPacks>
-__global__ void __launch_bounds__(kThreads, 3) widen_kernel(const Y* base, int64_t base_ld, Y* out, int64_t out_ld,
-                                                         const bf16* factor, int width, int rank, const bf16* u,
-                                                         int parts, Plan p, bool factor_wide) {
+template <typename Y, int KT, bool kPacks>
+__global__ void __launch_bounds__(kThreads, KT <= 2 ? 3 : KT <= 4 ? 2 : 1)
+widen_kernel(const Y* base, int64_t base_ld, Y* out, int64_t out_ld, const bf16* factor, int width, int rank,
+             const bf16* u, Plan p) {
+  using S = WidenShape<Y, KT>;
+  constexpr int kStages = S::kStages, P = kPartsFor<Y>;
+  constexpr bool kHold = KT <= 4;
   extern __shared__ __align__(16) char shared[];
+  __shared__ int places[kMostRun];
   pdl_wait_prerequisites();
   pdl_launch_dependents();
-  const int item = blockIdx.x % p.most, block = blockIdx.x / p.most;
-  if (item >= *p.n_items) return;
-  const Item it = p.items[item];
-  const bool bare = it.adapter >= p.n;
-  if (bare && base == out) return;
-  const bf16* const f = factor + static_cast<int64_t>(it.adapter) * rank * width;
-  if (!bare && it.count <= kFewRows) {
-    __shared__ float us[kFewRows * kMaxRank];
-    if (block % (kFewBlock / kBlock) == 0)
-      widen_few<Y, kPacks>(base, base_ld, out, out_ld, f, width, rank, u, p, it, us, block * kBlock);
-    return;
-  }
-  const int wide_rank = round_rank(rank), fs = kBlock + kPad, us = wide_rank + kPad;
+  const int n_runs = p.counts[1];
+  const int blocks = (width - 1) / kBlock + 1;
+  // a narrow product takes its runs in pieces of kRows rows, to have enough units
+  const int pieces = static_cast<int64_t>(n_runs) * blocks < 2 * static_cast<int64_t>(gridDim.x) ? p.run_rows / kRows : 1;
+  const int64_t units = static_cast<int64_t>(n_runs) * blocks * pieces;
+  const int wide_rank = round_rank(rank);
   bf16* const F = reinterpret_cast<bf16*>(shared);
-  bf16* const U = F + wide_rank * fs;
-  const int c0 = block * kBlock;
+  bf16* const U = F + 16 * KT * S::fs;                   // two buffers
+  char* const ring = reinterpret_cast<char*>(U + 2 * S::u_size);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  float* const corner = reinterpret_cast<float*>(U + parts * kRows * us) + warp * 16 * 33;   // without kPacks
-  constexpr int kAhead = !kPacks ? 1 : sizeof(Y) == 4 ? 2 : 4;     // 16-row tiles in flight
-  const int mine = c0 + warp * 32 + (kPacks ? 8 * t : lane);       // this thread's columns
-  Pack<Y, 8> q[kAhead][2];
-  Y single[16];
-  auto row_of = [&](int r) { return static_cast<int64_t>(p.pos[it.first + r]); };
-  auto fetch = [&](int r0) {
-    if constexpr (kPacks) {
-#pragma unroll
-      for (int m = 0; m < kAhead; ++m)
+  float* const corner = reinterpret_cast<float*>(ring) + warp * 16 * 33;   // without kPacks
+  char* const slots = ring + tid * 16;
+  const int row8 = (lane >> 3 & 1) * 8 + (lane & 7), col8 = (lane >> 4) * 8;   // of a matrix load
+  for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
+    const int64_t piece = unit / n_runs;
+    Item it = p.runs[unit % n_runs];
+    const int c0 = static_cast<int>(piece / pieces) * kBlock;
+    if (pieces > 1) {
+      const int skip = static_cast<int>(piece % pieces) * kRows;
+      it.first += skip;
+      it.count = min(it.count - skip, kRows);
+      if (it.count <= 0) continue;
+    }
+    const bool bare = it.adapter >= p.n;
+    if (bare && base == out) continue;
+    const bf16* const f = factor + static_cast<int64_t>(it.adapter) * rank * width;
+    const int mine = c0 + warp * 32 + (kPacks ? 8 * t : lane);       // this thread's columns
+    __syncthreads();     // the unit before has read its places, F and u
+    for (int i = tid; i < it.count; i += kThreads) places[i] = p.pos[it.first + i];
+    __syncthreads();
+    const Y* const from = base ? base + mine : nullptr;
+    Y* const to = out + mine;
+    // stage s of the ring: 16 rows, this thread's chunk of two of them
+    auto fetch = [&](int r0, int s) {
+      if constexpr (kPacks) {
+        if (!base || mine >= width) return;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int r = r0 + m * 16 + h * 8 + g;
-          q[m][h] = Pack<Y, 8>{};
-          if (r >= it.count || !base) continue;
-          const Y* const src = base + row_of(r) * base_ld + mine;
+          const int r = r0 + h * 8 + g;
+          if (r >= it.count) continue;
+          const Y* const src = from + places[r] * base_ld;
+          const uint32_t dst = smem_addr(slots) + static_cast<uint32_t>((s * 2 + h) * S::kChunks * kThreads * 16);
           if (mine + 8 <= width) {
-            q[m][h] = *reinterpret_cast<const Pack<Y, 8>*>(src);
+#pragma unroll
+            for (int q = 0; q < S::kChunks; ++q)
+              copy_async<16>(dst + q * kThreads * 16, src + q * kVec<Y>);
           } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (mine + e < width) q[m][h].v[e] = src[e];
+            for (int q = 0; q < S::kChunks; ++q) {
+              constexpr int n = kVec<Y>;
+              const int left = max(0, min(width - mine - q * n, n)) * static_cast<int>(sizeof(Y));
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + q * kThreads * 16),
+                           "l"(left ? src + q * n : base), "r"(left)
+                           : "memory");
+            }
           }
         }
-    } else {
+      }
+    };
+    auto fetch_u = [&](int r0, int buffer) {
+      constexpr int packs = 2 * KT;
+      bf16* const dst = U + buffer * S::u_size;
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        single[r] = from_f32<Y>(0.f);
-        if (r0 + r < it.count && base && mine < width) single[r] = base[row_of(r0 + r) * base_ld + mine];
+      for (int i0 = 0; i0 < P * kRows * packs; i0 += kThreads) {
+        const int i = i0 + tid, k = i / (kRows * packs), r = i / packs % kRows, c = i % packs * 8;
+        if (P * kRows * packs % kThreads && i >= P * kRows * packs) break;
+        const bool on = r0 + r < it.count && c < wide_rank;
+        copy_chunk(dst + (k * kRows + r) * S::us + c,
+                   on ? u + (static_cast<int64_t>(it.first + r0 + r) * kParts + k) * wide_rank + c : u, on);
       }
+    };
+    if (!bare) fetch_u(0, 0);
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) {
+      if (s * 16 < it.count) fetch(s * 16, s);
+      copy_async_commit();
     }
-  };
-  fetch(0);
-  if (!bare) {
-    for (int i = tid; i < wide_rank * (kBlock / 8); i += kThreads) {
-      const int k = i / (kBlock / 8), c = i % (kBlock / 8) * 8;
-      Pack<bf16, 8> v{};
-      if (k < rank && c0 + c < width) {
-        if (factor_wide)
-          *reinterpret_cast<uint4*>(&v) = *reinterpret_cast<const uint4*>(f + static_cast<int64_t>(k) * width + c0 + c);
-        else
-          v = load8(f + static_cast<int64_t>(k) * width, c0 + c, width);
-      }
-      if constexpr (kPacks) {
-        uint32_t* const dst = reinterpret_cast<uint32_t*>(F + k * fs + c / 32 * 32) + c % 32 / 8;
+    uint32_t held[kHold ? KT : 1][2][4];
+    if (!bare) {
+#pragma unroll 4
+      for (int i = tid; i < 16 * KT * (kBlock / 8); i += kThreads) {
+        const int k = i / (kBlock / 8), c = i % (kBlock / 8) * 8;
+        Pack<bf16, 8> v{};
+        if (k < rank && c0 + c < width) v = load8(f + static_cast<int64_t>(k) * width, c0 + c, width);
         const uint4 w = *reinterpret_cast<const uint4*>(&v);
-        dst[0] = w.x;
-        dst[4] = w.y;
-        dst[8] = w.z;
-        dst[12] = w.w;
-      } else {
-        *reinterpret_cast<uint4*>(F + k * fs + c) = *reinterpret_cast<const uint4*>(&v);
+        if constexpr (kPacks) {
+          uint32_t* const dst = reinterpret_cast<uint32_t*>(F + k * S::fs + c / 32 * 32) + c % 32 / 8;
+          dst[0] = w.x;
+          dst[4] = w.y;
+          dst[8] = w.z;
+          dst[12] = w.w;
+        } else {
+          *reinterpret_cast<uint4*>(F + k * S::fs + c) = w;
+        }
       }
-    }
-    const int packs = wide_rank / 8;
-    for (int i = tid; i < parts * kRows * packs; i += kThreads) {
-      const int k = i / (kRows * packs), r = i / packs % kRows, c = i % packs * 8;
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (r < it.count)
-        v = *reinterpret_cast<const uint4*>(u + (static_cast<int64_t>(it.first + r) * kParts + k) * wide_rank + c);
-      *reinterpret_cast<uint4*>(U + (k * kRows + r) * us + c) = v;
-    }
-    __syncthreads();
-  }
-  for (int r0 = 0; r0 < it.count; r0 += 16 * kAhead) {
-    if (r0) fetch(r0);
+      if constexpr (kHold) {
+        __syncthreads();
 #pragma unroll
-    for (int m = 0; m < kAhead; ++m) {
-      if (r0 + m * 16 >= it.count) break;
-      float acc[4][4] = {};
-      if (!bare) {
-        for (int k = 0; k < wide_rank; k += 16) {
-          uint32_t b[2][4];
+        for (int k = 0; k < KT; ++k)
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            load_matrices_turned(b[h], F + (k + (lane >> 3 & 1) * 8 + (lane & 7)) * fs + warp * 32 + h * 16 + (lane >> 4) * 8);
-          for (int s = parts - 1; s >= 0; --s) {
-            uint32_t a[4];
-            load_matrices(a, U + (s * kRows + r0 + m * 16 + (lane >> 3 & 1) * 8 + (lane & 7)) * us + k + (lane >> 4) * 8);
+            load_matrices_turned(held[k][h], F + (k * 16 + row8) * S::fs + warp * 32 + h * 16 + col8);
+      }
+    }
+    int stage = 0;
+    for (int r0 = 0; r0 < it.count; r0 += 16) {
+      // all but the last kStages - 2 groups are here: this stage, and u of these rows before it
+      copy_async_wait<kStages - 2>();
+      if (r0 % kRows == 0 && !bare) {
+        __syncthreads();
+        if (r0 + kRows < it.count) fetch_u(r0 + kRows, (r0 / kRows + 1) & 1);
+      }
+      const int ahead = r0 + (kStages - 1) * 16;
+      if (ahead < it.count) fetch(ahead, stage == 0 ? kStages - 1 : stage - 1);
+      copy_async_commit();
+      Y single[16];
+      if constexpr (!kPacks) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) mma(acc[j], a, b[j >> 1][(j & 1) * 2], b[j >> 1][(j & 1) * 2 + 1]);
+        for (int r = 0; r < 16; ++r) {
+          single[r] = from_f32<Y>(0.f);
+          if (r0 + r < it.count && base && mine < width) single[r] = from[places[r0 + r] * base_ld];
+        }
+      }
+      float acc[4][4] = {};
+      if (!bare) {
+        const bf16* const own = U + (r0 / kRows & 1) * S::u_size + (r0 % kRows + row8) * S::us + col8;
+#pragma unroll
+        for (int k = 0; k < KT; ++k) {
+          uint32_t b[2][4];
+          if constexpr (!kHold) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              load_matrices_turned(b[h], F + (k * 16 + row8) * S::fs + warp * 32 + h * 16 + col8);
+          }
+#pragma unroll
+          for (int s = P - 1; s >= 0; --s) {
+            uint32_t a[4];
+            load_matrices(a, own + s * kRows * S::us + k * 16);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if constexpr (kHold)
+                mma(acc[j], a, held[k][j >> 1][(j & 1) * 2], held[k][j >> 1][(j & 1) * 2 + 1]);
+              else
+                mma(acc[j], a, b[j >> 1][(j & 1) * 2], b[j >> 1][(j & 1) * 2 + 1]);
+            }
           }
         }
       }
       if constexpr (kPacks) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int r = r0 + m * 16 + h * 8 + g;
+          const int r = r0 + h * 8 + g;
           if (r >= it.count) continue;
-          Pack<Y, 8> y;
+          Pack<Y, 8> y{};
+          if (base) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 old = pair_of(q[m][h], j);
-            set_pair(y, j, make_float2(old.x + acc[j][2 * h], old.y + acc[j][2 * h + 1]));
+            for (int q = 0; q < S::kChunks; ++q)
+              reinterpret_cast<uint4*>(&y)[q] =
+                  *reinterpret_cast<const uint4*>(slots + ((stage * 2 + h) * S::kChunks + q) * kThreads * 16);
           }
-          Y* const dst = out + row_of(r) * out_ld + mine;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) set_pair(y, j, add2(pair_of(y, j), make_float2(acc[j][2 * h], acc[j][2 * h + 1])));
+          Y* const dst = to + places[r] * out_ld;
           if (mine + 8 <= width) {
             *reinterpret_cast<Pack<Y, 8>*>(dst) = y;
           } else {
@@ -594,7 +627,90 @@ __global__ void __launch_bounds__(kThreads, 3) widen_kernel(const Y* base, int64
 #pragma unroll
         for (int r = 0; r < 16; ++r)
           if (r0 + r < it.count && mine < width)
-            out[row_of(r0 + r) * out_ld + mine] = from_f32<Y>(to_f32(single[r]) + corner[r * 33 + lane]);
+            to[places[r0 + r] * out_ld] = from_f32<Y>(to_f32(single[r]) + corner[r * 33 + lane]);
+      }
+      stage = stage == kStages - 1 ? 0 : stage + 1;
+    }
+    copy_async_wait<0>();
+  }
+}
+
+template <typename Y, bool kPacks>
+__global__ void __launch_bounds__(kThreads, 2) few_kernel(const Y* base, int64_t base_ld, Y* out, int64_t out_ld,
+                                                          const bf16* factor, int width, int rank, const bf16* u, Plan p) {
+  constexpr int kAhead = 8;      // ranks in flight
+  __shared__ float4 us[kMaxRank];      // of four rows
+  pdl_wait_prerequisites();
+  pdl_launch_dependents();
+  const int n_few = p.counts[2], blocks = (width - 1) / kFewBlock + 1, wide_rank = round_rank(rank);
+  constexpr int kTurns = kFewRows / kFewAtOnce;
+  const int64_t units = static_cast<int64_t>(n_few) * kTurns * blocks;
+  for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
+    // the turns of one run's columns next to each other: the second finds F in the L2
+    const int turn = static_cast<int>(unit % kTurns);
+    const int64_t rest = unit / kTurns;
+    Item it = p.few[rest / blocks];
+    it.first += turn * kFewAtOnce;
+    it.count = min(it.count - turn * kFewAtOnce, kFewAtOnce);
+    if (it.count <= 0) continue;
+    const int c = static_cast<int>(rest % blocks) * kFewBlock + threadIdx.x * 8;
+    const bf16* const f = factor + static_cast<int64_t>(it.adapter) * rank * width;
+    Pack<Y, 8> y[kFewAtOnce];
+    Y* dst[kFewAtOnce];
+#pragma unroll
+    for (int r = 0; r < kFewAtOnce; ++r) {
+      if (r >= it.count || c >= width) continue;
+      const int64_t row = p.pos[it.first + r];
+      dst[r] = out + row * out_ld + c;
+      y[r] = Pack<Y, 8>{};
+      if (!base) continue;
+      const Y* const src = base + row * base_ld + c;
+      if (kPacks && c + 8 <= width) {
+        y[r] = *reinterpret_cast<const Pack<Y, 8>*>(src);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (c + e < width) y[r].v[e] = src[e];
+      }
+    }
+    __syncthreads();     // the unit before has read its u
+    for (int i = threadIdx.x; i < kFewAtOnce * wide_rank; i += kThreads) {
+      const int r = i / wide_rank, k = i % wide_rank;      // 0 behind the rank
+      const bf16* const q = u + static_cast<int64_t>(it.first + r) * kParts * wide_rank + k;
+      reinterpret_cast<float*>(us)[k * 4 + r] =
+          r < it.count ? __bfloat162float(q[0]) + (__bfloat162float(q[wide_rank]) + __bfloat162float(q[2 * wide_rank])) : 0.f;
+    }
+    __syncthreads();
+    if (c >= width) continue;
+    float2 acc[kFewAtOnce][4] = {};
+    for (int k0 = 0; k0 < rank; k0 += kAhead) {
+      Pack<bf16, 8> q[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        q[k] = k0 + k < rank ? load8(f + static_cast<int64_t>(k0 + k) * width, c, width) : Pack<bf16, 8>{};
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const float4 w = us[k0 + k];
+        const float each[kFewAtOnce] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 x = pair_of(q[k], e);
+#pragma unroll
+          for (int r = 0; r < kFewAtOnce; ++r) acc[r][e] = fma2(x, make_float2(each[r], each[r]), acc[r][e]);
+        }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < kFewAtOnce; ++r) {
+      if (r >= it.count) continue;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) set_pair(y[r], e, add2(pair_of(y[r], e), acc[r][e]));
+      if (kPacks && c + 8 <= width) {
+        *reinterpret_cast<Pack<Y, 8>*>(dst[r]) = y[r];
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (c + e < width) dst[r][e] = y[r].v[e];
       }
     }
   }
@@ -833,12 +949,14 @@ Space lay_out(void* workspace, int64_t T, int H, int V, int rank, int n) {
   };
   Space s{};
   s.plan.live = reinterpret_cast<int*>(take(256));
-  s.plan.n_items = s.plan.live + 1;
+  s.plan.counts = s.plan.live + 1;
   s.plan.keys = reinterpret_cast<int32_t*>(take(4 * static_cast<size_t>(rows)));
   s.plan.pos = reinterpret_cast<int32_t*>(take(4 * static_cast<size_t>(rows)));
   s.plan.starts = reinterpret_cast<int*>(take(4 * (static_cast<size_t>(n) + 2)));
   s.plan.most = static_cast<int>(most_items(rows, n));
   s.plan.items = reinterpret_cast<Item*>(take(sizeof(Item) * static_cast<size_t>(s.plan.most)));
+  s.plan.runs = reinterpret_cast<Item*>(take(sizeof(Item) * static_cast<size_t>(s.plan.most)));
+  s.plan.few = reinterpret_cast<Item*>(take(sizeof(Item) * static_cast<size_t>(s.plan.most)));
   s.plan.n = n;
   const size_t wide_rank = static_cast<size_t>(round_rank(rank));
   s.u = reinterpret_cast<bf16*>(take(2 * kParts * wide_rank * rows));
@@ -905,17 +1023,19 @@ cudaError_t narrow(const char* name, const X* wide, int64_t ld, const void* fact
   });
 }
 
-template <typename Y, bool kPacks>
+template <typename Y, int KT, bool kPacks>
 cudaError_t widen_of(const Y* base, int64_t base_ld, Y* out, int64_t out_ld, const bf16* factor, int width, int rank,
-                     const bf16* u, int parts, const Plan& p, cudaStream_t s) {
+                     const bf16* u, const Plan& p, int sms, cudaStream_t s) {
   static std::atomic<int> ready[64];
-  const cudaError_t e = allow_shared(ready, reinterpret_cast<const void*>(widen_kernel<Y, kPacks>),
-                                     widen_shared(round_rank(kMaxRank), kParts, kPacks));
+  constexpr size_t smem = WidenShape<Y, KT>::bytes(kPacks);
+  const cudaError_t e = allow_shared(ready, reinterpret_cast<const void*>(widen_kernel<Y, KT, kPacks>), smem);
   if (e != cudaSuccess) return e;
-  const int64_t blocks = (static_cast<int64_t>(width) + kBlock - 1) / kBlock;
-  return launch_dependent(widen_kernel<Y, kPacks>, dim3(static_cast<unsigned>(blocks * p.most)), kThreads,
-                          widen_shared(round_rank(rank), parts, kPacks), 1, s, base, base_ld, out, out_ld, factor, width,
-                          rank, u, parts, p, whole_chunks(factor, width, width));
+  constexpr int by_shared = static_cast<int>(size_t{220} * 1024 / (smem + 4096)), by_registers = KT <= 2 ? 3 : KT <= 4 ? 2 : 1;
+  constexpr int fit = by_shared < 1 ? 1 : by_shared < by_registers ? by_shared : by_registers;
+  const int64_t units = (static_cast<int64_t>(width - 1) / kBlock + 1) * p.most * (p.run_rows / kRows);
+  const int64_t resident = static_cast<int64_t>(sms) * fit;
+  return launch_dependent(widen_kernel<Y, KT, kPacks>, dim3(static_cast<unsigned>(units < resident ? units : resident)),
+                          kThreads, smem, 1, s, base, base_ld, out, out_ld, factor, width, rank, u, p);
 }
 
 template <typename Y>
@@ -925,10 +1045,27 @@ cudaError_t widen(const char* name, const Y* base, int64_t base_ld, Y* out, int6
   const bf16* const f = static_cast<const bf16*>(factor);
   const bool packs = ((reinterpret_cast<uintptr_t>(base) | reinterpret_cast<uintptr_t>(out)) & 15u) == 0 &&
                      base_ld % VEC == 0 && out_ld % VEC == 0;
-  const int parts = sizeof(Y) == 4 ? kParts : 2;
-  return traced_launch(name, s, [&] {
-    return packs ? widen_of<Y, true>(base, base_ld, out, out_ld, f, width, rank, u, parts, p, s)
-                 : widen_of<Y, false>(base, base_ld, out, out_ld, f, width, rank, u, parts, p, s);
+  const int sms = sm_count();
+  if (sms <= 0) return cudaErrorUnknown;
+  auto run = [&](auto kt) {
+    constexpr int KT = decltype(kt)::value;
+    return packs ? widen_of<Y, KT, true>(base, base_ld, out, out_ld, f, width, rank, u, p, sms, s)
+                 : widen_of<Y, KT, false>(base, base_ld, out, out_ld, f, width, rank, u, p, sms, s);
+  };
+  const cudaError_t e = traced_launch(name, s, [&] {
+    if (rank <= 16) return run(std::integral_constant<int, 1>{});
+    if (rank <= 32) return run(std::integral_constant<int, 2>{});
+    if (rank <= 64) return run(std::integral_constant<int, 4>{});
+    return run(std::integral_constant<int, 8>{});
+  });
+  if (e != cudaSuccess) return e;
+  return traced_launch("adapters_few", s, [&] {
+    auto kern = packs ? few_kernel<Y, true> : few_kernel<Y, false>;
+    const int64_t runs = p.n < p.rows ? p.n : p.rows;
+    const int64_t units = runs * (kFewRows / kFewAtOnce) * ((static_cast<int64_t>(width) - 1) / kFewBlock + 1);
+    const int64_t resident = 2 * static_cast<int64_t>(sms);
+    return launch_dependent(kern, dim3(static_cast<unsigned>(units < resident ? units : resident)), kThreads, 0, 1, s,
+                            base, base_ld, out, out_ld, f, width, rank, u, p);
   });
 }
 
@@ -971,6 +1108,10 @@ cudaError_t outer(const char* name, const X* wide, int64_t ld, int width, int ra
 cudaError_t plan_rows(const Adapters& a, int64_t first, Space& z, cudaStream_t s) {
   z.plan.rows = static_cast<int>(a.T - first < kSortMost ? a.T - first : kSortMost);
   z.plan.most = static_cast<int>(most_items(z.plan.rows, a.n));
+  // runs as long as keeps some eight units per CTA of the widest product
+  const int64_t units = static_cast<int64_t>(a.V > a.H ? a.V : a.H) / kBlock * ((z.plan.rows + kRows - 1) / kRows);
+  const int64_t run = units / (8 * kManyCtas);
+  z.plan.run_rows = kRows * static_cast<int>(run < 1 ? 1 : run > kMostRun / kRows ? kMostRun / kRows : run);
   const cudaError_t e = traced_launch("adapters_sort", s, [&] {
     return launch_sort_ids(a.ids ? a.ids + first : nullptr, z.plan.rows, a.n, false, -1, z.plan.keys, z.plan.pos,
                            z.plan.live, s);
