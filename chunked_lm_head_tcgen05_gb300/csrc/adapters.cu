@@ -104,29 +104,42 @@ __device__ __forceinline__ void split(float x, float (&part)[N]) {
   }
 }
 
-// Elements [c, c + 8) of a row of `width`, zero behind its end; c >= 0.
-template <typename T>
+// Elements [c, c + 8) of a row.  A thread that knows which of these fits all of its loads
+// has several of them in flight: a choice per load would make each wait for the one before.
+enum class At {
+  kAligned,    // on a 16-byte boundary, inside the row
+  kInside,     // anywhere, with 8 elements of the row on either side
+  kEdge        // anywhere, zeros behind the row's end
+};
+template <At kAt, typename T>
 __device__ __forceinline__ Pack<T, 8> load8(const T* row, int c, int width) {
   Pack<T, 8> q;
   const T* const p = row + c;
-  if (c + 8 <= width && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
-    if constexpr (sizeof(T) == 4) {
-      reinterpret_cast<uint4*>(&q)[0] = reinterpret_cast<const uint4*>(p)[0];
-      reinterpret_cast<uint4*>(&q)[1] = reinterpret_cast<const uint4*>(p)[1];
-    } else {
-      *reinterpret_cast<uint4*>(&q) = *reinterpret_cast<const uint4*>(p);
-    }
-    return q;
-  }
-  if constexpr (sizeof(T) == 2) {
-    if (c >= 8 && c + 16 <= width) {     // both blocks lie inside the row
-      *reinterpret_cast<uint4*>(&q) = load_across(p);
-      return q;
-    }
-  }
+  if constexpr (kAt == At::kAligned) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) q.v[e] = c + e < width ? p[e] : from_f32<T>(0.f);
+    for (int h = 0; h < static_cast<int>(sizeof(T)) / 2; ++h)
+      reinterpret_cast<uint4*>(&q)[h] = reinterpret_cast<const uint4*>(p)[h];
+  } else if constexpr (kAt == At::kInside && sizeof(T) == 2) {
+    *reinterpret_cast<uint4*>(&q) = load_across(p);
+  } else if constexpr (kAt == At::kInside) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) q.v[e] = p[e];
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) q.v[e] = c + e < width ? p[e] : from_f32<T>(0.f);
+  }
   return q;
+}
+
+// f(std::integral_constant<At, ...>) for loads of columns [c, c + 8).
+template <typename F>
+__device__ __forceinline__ void at_columns(bool aligned, int c, int width, F&& f) {
+  if (aligned)
+    f(std::integral_constant<At, At::kAligned>{});
+  else if (c >= 8 && c + 16 <= width)
+    f(std::integral_constant<At, At::kInside>{});
+  else
+    f(std::integral_constant<At, At::kEdge>{});
 }
 
 // ------------------------------------------------------------------ items
@@ -190,20 +203,15 @@ __device__ __forceinline__ void copy_chunk(X* dst, const X* src, bool on) {   //
                : "memory");
 }
 
-// Eight elements of a row (or zeros) into a tile: asynchronously, where both are aligned, or by
-// way of `q`.  `any`: an address that may be named where nothing is read.
-template <typename X, bool kAsync>
-__device__ __forceinline__ void fetch8(Pack<X, 8>& q, X* dst, const X* row, int c, int width, const X* any) {
-  const bool on = row != nullptr && c < width;
-  if constexpr (kAsync) {
-    constexpr int n = 16 / sizeof(X);
+// Eight elements of a row (or zeros) into a tile by an asynchronous copy, both being
+// aligned; `any`: an address that may be named where nothing is read.
+template <typename X>
+__device__ __forceinline__ void copy8(X* dst, const X* row, int c, int width, const X* any) {
+  constexpr int n = 16 / sizeof(X);
 #pragma unroll
-    for (int h = 0; h < 8; h += n) {
-      const bool part = on && c + h < width;      // width is a multiple of n
-      copy_chunk(dst + h, part ? row + c + h : any, part);
-    }
-  } else {
-    q = on ? load8(row, c, width) : Pack<X, 8>{};
+  for (int h = 0; h < 8; h += n) {
+    const bool on = row != nullptr && c + h < width;      // width is a multiple of n
+    copy_chunk(dst + h, on ? row + c + h : any, on);
   }
 }
 template <typename X>
@@ -266,17 +274,33 @@ __global__ void __launch_bounds__(kThreads) narrow_kernel(const X* wide, int64_t
   // chunk i of a thread: row (i kThreads + tid) / 16, columns 8 (tid % 16)
   const int row0 = tid / 16, col = tid % 16 * 8;
   auto fetch = [&](int c0, int s) {
+    if constexpr (kAsync) {
 #pragma unroll
-    for (int i = 0; i < kX; ++i) {
-      const int r = row0 + i * 16;
-      fetch8<X, kAsync>(xq[i], x_tile(s) + r * S::xs + col, r < it.count ? wide + offset[r] : nullptr, c0 + col, end,
-                        wide);
-    }
+      for (int i = 0; i < kX; ++i) {
+        const int r = row0 + i * 16;
+        copy8(x_tile(s) + r * S::xs + col, r < it.count ? wide + offset[r] : nullptr, c0 + col, end, wide);
+      }
 #pragma unroll
-    for (int i = 0; i < kF; ++i) {
-      const int r = row0 + i * 16;
-      fetch8<bf16, kAsync>(fq[i], f_tile(s) + r * S::fs + col, r < rank ? f0 + static_cast<int64_t>(r) * width : nullptr,
-                           c0 + col, width, factor);
+      for (int i = 0; i < kF; ++i) {
+        const int r = row0 + i * 16;
+        copy8(f_tile(s) + r * S::fs + col, r < rank ? f0 + static_cast<int64_t>(r) * width : nullptr, c0 + col, width,
+              factor);
+      }
+    } else {
+      const int c = c0 + col;
+      at_columns(false, c, end, [&](auto at) {
+#pragma unroll
+        for (int i = 0; i < kX; ++i) {
+          const int r = row0 + i * 16;
+          xq[i] = r < it.count && c < end ? load8<decltype(at)::value>(wide + offset[r], c, end) : Pack<X, 8>{};
+        }
+#pragma unroll
+        for (int i = 0; i < kF; ++i) {
+          const int r = row0 + i * 16;
+          fq[i] = r < rank && c < end ? load8<decltype(at)::value>(f0 + static_cast<int64_t>(r) * width, c, end)
+                                      : Pack<bf16, 8>{};
+        }
+      });
     }
   };
   const int m0 = (warp & 3) * 16, k0 = (warp >> 2) * (kTile / 2);
@@ -438,7 +462,7 @@ struct WidenShape {
 template <typename Y, int KT, bool kPacks>
 __global__ void __launch_bounds__(kThreads, KT <= 2 ? 3 : KT <= 4 ? 2 : 1)
 widen_kernel(const Y* base, int64_t base_ld, Y* out, int64_t out_ld, const bf16* factor, int width, int rank,
-             const bf16* u, Plan p) {
+             const bf16* u, Plan p, bool factor_wide) {
   using S = WidenShape<Y, KT>;
   constexpr int kStages = S::kStages, P = kPartsFor<Y>;
   constexpr bool kHold = KT <= 4;
@@ -525,22 +549,35 @@ widen_kernel(const Y* base, int64_t base_ld, Y* out, int64_t out_ld, const bf16*
     }
     uint32_t held[kHold ? KT : 1][2][4];
     if (!bare) {
-#pragma unroll 4
-      for (int i = tid; i < 16 * KT * (kBlock / 8); i += kThreads) {
-        const int k = i / (kBlock / 8), c = i % (kBlock / 8) * 8;
-        Pack<bf16, 8> v{};
-        if (k < rank && c0 + c < width) v = load8(f + static_cast<int64_t>(k) * width, c0 + c, width);
-        const uint4 w = *reinterpret_cast<const uint4*>(&v);
-        if constexpr (kPacks) {
-          uint32_t* const dst = reinterpret_cast<uint32_t*>(F + k * S::fs + c / 32 * 32) + c % 32 / 8;
-          dst[0] = w.x;
-          dst[4] = w.y;
-          dst[8] = w.z;
-          dst[12] = w.w;
-        } else {
-          *reinterpret_cast<uint4*>(F + k * S::fs + c) = w;
+      // this thread's 8 columns of every eighth rank
+      const int c = tid % (kBlock / 8) * 8, first = tid / (kBlock / 8);
+      constexpr int kAtOnce = KT <= 2 ? 2 * KT : 4;
+      at_columns(factor_wide, c0 + c, width, [&](auto at) {
+#pragma unroll
+        for (int k0 = 0; k0 < 16 * KT; k0 += 8 * kAtOnce) {
+          Pack<bf16, 8> v[kAtOnce];
+#pragma unroll
+          for (int i = 0; i < kAtOnce; ++i) {
+            const int k = k0 + i * 8 + first;
+            v[i] = k < rank && c0 + c < width ? load8<decltype(at)::value>(f + static_cast<int64_t>(k) * width, c0 + c, width)
+                                              : Pack<bf16, 8>{};
+          }
+#pragma unroll
+          for (int i = 0; i < kAtOnce; ++i) {
+            const int k = k0 + i * 8 + first;
+            const uint4 w = *reinterpret_cast<const uint4*>(&v[i]);
+            if constexpr (kPacks) {
+              uint32_t* const dst = reinterpret_cast<uint32_t*>(F + k * S::fs + c / 32 * 32) + c % 32 / 8;
+              dst[0] = w.x;
+              dst[4] = w.y;
+              dst[8] = w.z;
+              dst[12] = w.w;
+            } else {
+              *reinterpret_cast<uint4*>(F + k * S::fs + c) = w;
+            }
+          }
         }
-      }
+      });
       if constexpr (kHold) {
         __syncthreads();
 #pragma unroll
@@ -637,7 +674,8 @@ widen_kernel(const Y* base, int64_t base_ld, Y* out, int64_t out_ld, const bf16*
 
 template <typename Y, bool kPacks>
 __global__ void __launch_bounds__(kThreads, 2) few_kernel(const Y* base, int64_t base_ld, Y* out, int64_t out_ld,
-                                                          const bf16* factor, int width, int rank, const bf16* u, Plan p) {
+                                                          const bf16* factor, int width, int rank, const bf16* u, Plan p,
+                                                          bool factor_wide) {
   constexpr int kAhead = 8;      // ranks in flight
   __shared__ float4 us[kMaxRank];      // of four rows
   pdl_wait_prerequisites();
@@ -683,23 +721,27 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const Y* base, int64_t
     __syncthreads();
     if (c >= width) continue;
     float2 acc[kFewAtOnce][4] = {};
-    for (int k0 = 0; k0 < rank; k0 += kAhead) {
-      Pack<bf16, 8> q[kAhead];
+    at_columns(factor_wide, c, width, [&](auto at) {
+      for (int k0 = 0; k0 < rank; k0 += kAhead) {
+        Pack<bf16, 8> q[kAhead];
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k)
-        q[k] = k0 + k < rank ? load8(f + static_cast<int64_t>(k0 + k) * width, c, width) : Pack<bf16, 8>{};
+        for (int k = 0; k < kAhead; ++k) {
+          q[k] = Pack<bf16, 8>{};
+          if (k0 + k < rank) q[k] = load8<decltype(at)::value>(f + static_cast<int64_t>(k0 + k) * width, c, width);
+        }
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        const float4 w = us[k0 + k];
-        const float each[kFewAtOnce] = {w.x, w.y, w.z, w.w};
+        for (int k = 0; k < kAhead; ++k) {
+          const float4 w = us[k0 + k];
+          const float each[kFewAtOnce] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 x = pair_of(q[k], e);
+          for (int e = 0; e < 4; ++e) {
+            const float2 x = pair_of(q[k], e);
 #pragma unroll
-          for (int r = 0; r < kFewAtOnce; ++r) acc[r][e] = fma2(x, make_float2(each[r], each[r]), acc[r][e]);
+            for (int r = 0; r < kFewAtOnce; ++r) acc[r][e] = fma2(x, make_float2(each[r], each[r]), acc[r][e]);
+          }
         }
       }
-    }
+    });
 #pragma unroll
     for (int r = 0; r < kFewAtOnce; ++r) {
       if (r >= it.count) continue;
@@ -759,18 +801,30 @@ __global__ void __launch_bounds__(kThreads) outer_kernel(const X* wide, int64_t 
     }
   };
   auto fetch = [&](int r0, int s) {
+    const int c = c0 + lane * 8;
+    if constexpr (kAsync) {
 #pragma unroll
-    for (int i = 0; i < kRowsEach; ++i)
-      fetch8<X, kAsync>(xq[i], x_tile(s) + (i * kWarps + warp) * S::fs + lane * 8,
-                        place[i] >= 0 ? wide + place[i] * ld : nullptr, c0 + lane * 8, width, wide);
+      for (int i = 0; i < kRowsEach; ++i)
+        copy8(x_tile(s) + (i * kWarps + warp) * S::fs + lane * 8, place[i] >= 0 ? wide + place[i] * ld : nullptr, c, width,
+              wide);
+    } else {
+      at_columns(false, c, width, [&](auto at) {
+#pragma unroll
+        for (int i = 0; i < kRowsEach; ++i)
+          xq[i] = place[i] >= 0 && c < width ? load8<decltype(at)::value>(wide + place[i] * ld, c, width) : Pack<X, 8>{};
+      });
+    }
 #pragma unroll
     for (int i = 0; i < kPacks; ++i) {
       const int at = i * kThreads + tid, k = at / (kOuterRows * RT * 2), r = at / (RT * 2) % kOuterRows,
-                c = at % (RT * 2) * 8;
-      if (k < kParts)
-        fetch8<bf16, kAsync>(uq[i], u_tile(s) + (k * kOuterRows + r) * S::us + c,
-                             r0 + r < to ? u + (static_cast<int64_t>(r0 + r) * kParts + k) * wide_rank : nullptr,
-                             rank0 + c, wide_rank, u);
+                cu = at % (RT * 2) * 8;
+      if (k >= kParts) continue;
+      const bool on = r0 + r < to && rank0 + cu < wide_rank;
+      const bf16* const src = on ? u + (static_cast<int64_t>(r0 + r) * kParts + k) * wide_rank + rank0 + cu : u;
+      if constexpr (kAsync)
+        copy_chunk(u_tile(s) + (k * kOuterRows + r) * S::us + cu, src, on);
+      else
+        uq[i] = on ? load8<At::kAligned>(src, 0, 8) : Pack<bf16, 8>{};
     }
     look(r0 + kOuterRows);
   };
@@ -1035,7 +1089,8 @@ cudaError_t widen_of(const Y* base, int64_t base_ld, Y* out, int64_t out_ld, con
   const int64_t units = (static_cast<int64_t>(width - 1) / kBlock + 1) * p.most * (p.run_rows / kRows);
   const int64_t resident = static_cast<int64_t>(sms) * fit;
   return launch_dependent(widen_kernel<Y, KT, kPacks>, dim3(static_cast<unsigned>(units < resident ? units : resident)),
-                          kThreads, smem, 1, s, base, base_ld, out, out_ld, factor, width, rank, u, p);
+                          kThreads, smem, 1, s, base, base_ld, out, out_ld, factor, width, rank, u, p,
+                          whole_chunks(factor, width, width));
 }
 
 template <typename Y>
@@ -1065,7 +1120,7 @@ cudaError_t widen(const char* name, const Y* base, int64_t base_ld, Y* out, int6
     const int64_t units = runs * (kFewRows / kFewAtOnce) * ((static_cast<int64_t>(width) - 1) / kFewBlock + 1);
     const int64_t resident = 2 * static_cast<int64_t>(sms);
     return launch_dependent(kern, dim3(static_cast<unsigned>(units < resident ? units : resident)), kThreads, 0, 1, s,
-                            base, base_ld, out, out_ld, f, width, rank, u, p);
+                            base, base_ld, out, out_ld, f, width, rank, u, p, whole_chunks(f, width, width));
   });
 }
 

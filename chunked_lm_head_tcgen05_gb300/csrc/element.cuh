@@ -84,14 +84,12 @@ __device__ __forceinline__ void set_pair(Pack<__half, VEC>& q, int i, float2 x) 
 }
 
 // The 16 bytes at p, which is aligned to its element only, from the two aligned
-// blocks they lie in.
+// blocks they lie in; both are read.
 template <typename T>
 __device__ __forceinline__ uint4 load_across(const T* p) {
   const unsigned off = static_cast<unsigned>(reinterpret_cast<uintptr_t>(p)) & 15u;
   const uint4* const q = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(p) - off);
-  const uint4 lo = q[0];
-  if (off == 0) return lo;
-  const uint4 hi = q[1];
+  const uint4 lo = q[0], hi = q[1];     // no branch, so that several of these are in flight
   const unsigned words = off >> 2, bits = (off & 3u) * 8u;
   // words of lo : hi from `words` on, five of them
   const bool two = words & 2u, one = words & 1u;
