@@ -3,13 +3,14 @@
 //   lse_r = log sum_v exp(z_v),   candidate (j, v): score_r + z_v - lse_r,
 // and a group's best `take` candidates go on, ties to the lowest j V + v.
 // HBM-bound: one read of the logits, two kernels.
-//  1. scan_kernel, one CTA per piece of a row, held in registers: maximum and
-//     exponential sum of the piece, and its best `take` logits.  At least `take`
-//     groups of threads have a largest element, so the least of these is at most
-//     the piece's take-th largest element: what is not below it (some
-//     take * ln(take) of the elements) goes to shared memory and is ranked there.
-//     When more elements qualify than fit (equal logits), the take-th largest is
-//     found by halving intervals instead.
+//  1. scan_kernel, one CTA per piece of a row, tile by tile with the next one in flight:
+//     maximum and exponential sum of the piece, and its best `take` logits.  In the first
+//     tile, at least `take` groups of threads have a largest element, so the least of these
+//     is at most the tile's take-th largest element: what is not below it (some
+//     take * ln(take) of the elements) goes to shared memory and is ranked there.  From
+//     then on only elements above the take-th best so far go there, and are ranked again
+//     when they are many.  When a tile has more than fit (equal or ascending logits), its
+//     take-th largest is found by halving intervals instead.
 //  2. best_kernel, one CTA per group, joins the pieces: lse, then the candidates.
 //     An fp32 score with its error bound on either side sorts out most of them;
 //     the rest are compared in 64 bits, where fp32 could confuse two that are
@@ -30,9 +31,10 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kManyElements = 32;    // per thread, of many rows: pieces of 8,192
-constexpr int kFewElements = 8;      // of few rows: pieces of 2,048
-constexpr int64_t kManyPieces = 304; // CTAs of the long pieces that fill the GPU
+constexpr int kManyElements = 16;    // per thread and tile, of many rows: tiles of 4,096
+constexpr int kFewElements = 8;      // of few rows: pieces of one tile of 2,048
+constexpr int64_t kManyTiles = 304;  // the long tiles from which on they fill the GPU
+constexpr int64_t kManyPieces = 608; // CTAs that many rows are cut into
 constexpr int kRoom = 1024;          // elements ranked in shared memory
 constexpr int kBestThreads = 512;
 constexpr int kBestWarps = kBestThreads / 32;
@@ -46,6 +48,7 @@ __device__ __forceinline__ float from_order(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 constexpr uint32_t kMinusInf = 0x007fffffu;      // order_of(-inf)
+constexpr uint32_t kMinusZero = 0x7fffffffu;     // no number's: zero's is the next
 
 // Larger logit first, then the lower id.
 __device__ __forceinline__ uint64_t entry_of(uint32_t order, int v) {
@@ -75,152 +78,214 @@ __device__ __forceinline__ int count_all(int on, int* scratch) {
   return sum;
 }
 
+// The `take` best of found[0, n), n <= kRoom, in falling order; every thread gets their number.
+__device__ __noinline__ int keep_best(uint64_t* found, int n, int take) {
+  constexpr int kEach = kRoom / kThreads;
+  uint64_t me[kEach];
+  int rank[kEach];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int at = i * kThreads + threadIdx.x;
+    rank[i] = take;
+    if (at >= n) continue;
+    me[i] = found[at];
+    int above = 0;
+    for (int j = 0; j < n; ++j) above += found[j] > me[i];
+    rank[i] = above;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kEach; ++i)
+    if (rank[i] < take) found[rank[i]] = me[i];
+  __syncthreads();
+  return min(n, take);
+}
+
+// The best `take` of a tile's elements above `low` (there are more than that), added to found:
+// their take-th largest order, by halving intervals, then the ids up to which its equals are
+// taken.  Reads the tile again each time: this is rare, and its registers are needed elsewhere.
+template <typename T, int PACKS>
+__device__ __noinline__ void add_best_of_tile(uint64_t* found, int* n_found, int* scratch, const T* row, int from, int p1,
+                                              int skip, int V, uint32_t low, int take) {
+  constexpr int VEC = kVec<T>;
+  auto each = [&](auto&& f) {
+    for (int i = 0; i < PACKS * VEC; ++i) {
+      const int p = from + i / VEC * kThreads + threadIdx.x, v = p * VEC - skip + i % VEC;
+      if (p >= p1 || v < 0 || v >= V) continue;
+      const float x = to_f32(row[v]);
+      if (x == x) f(order_of(x), v);       // a row with a NaN offers nothing in the end
+    }
+  };
+  auto count = [&](auto&& f) {
+    int c = 0;
+    each([&](uint32_t o, int v) { c += f(o, v); });
+    return count_all(c, scratch);
+  };
+  uint32_t lo = low + 1, hi = 0xff800000u;      // order_of(inf): no number is above it
+  while (lo < hi) {
+    const uint32_t mid = lo + (hi - lo + 1) / 2;
+    if (count([&](uint32_t o, int) { return o >= mid; }) >= take) lo = mid; else hi = mid - 1;
+  }
+  const int larger = count([&](uint32_t o, int) { return o > lo; });
+  int first = 0, last = V - 1;
+  while (first < last) {
+    const int mid = first + (last - first) / 2;
+    if (count([&](uint32_t o, int v) { return o == lo && v <= mid; }) >= take - larger) last = mid; else first = mid + 1;
+  }
+  each([&](uint32_t o, int v) {
+    if (o > lo || (o == lo && v <= first)) {
+      const int n = atomicAdd(n_found, 1);
+      if (n < kRoom) found[n] = entry_of(o, v);
+    }
+  });
+  __syncthreads();
+}
+
 template <typename T, int ELEMS>
 __global__ void __launch_bounds__(kThreads, 4) scan_kernel(BeamSelect a, Pieces z, int span) {
   constexpr int VEC = kVec<T>, PACKS = ELEMS / VEC;
   __shared__ uint64_t found[kRoom];
-  __shared__ uint32_t warp_max[kWarps], warp_min[kWarps];
-  __shared__ float warp_sums[kWarps];
-  __shared__ int scratch[kWarps], n_found, bad;
+  __shared__ uint32_t warp_min[kWarps];
+  __shared__ float2 warp_sums[kWarps];
+  __shared__ int scratch[kWarps], n_found;
   pdl_wait_prerequisites();
   pdl_launch_dependents();
   const int64_t r = blockIdx.x / z.pieces;
   const int piece = static_cast<int>(blockIdx.x % z.pieces);
   if (a.finished && a.finished[r]) return;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) n_found = 0, bad = 0;
+  if (tid == 0) n_found = 0;
   // packs are counted from the 16-byte boundary at or before the row's start
   const T* const row = static_cast<const T*>(a.logits) + r * a.ld;
   const int skip = static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
   const int p0 = piece * z.length, p1 = min(p0 + z.length, (a.V + skip + VEC - 1) / VEC);
-  Pack<T, VEC> q[PACKS];
-#pragma unroll
-  for (int i = 0; i < PACKS; ++i) {
-    const int p = p0 + i * kThreads + tid, v = p * VEC - skip;
-    if (p < p1 && v >= 0 && v + VEC <= a.V) {
-      const uint4 w = __ldcs(reinterpret_cast<const uint4*>(row + v));
-      q[i] = *reinterpret_cast<const Pack<T, VEC>*>(&w);
-    } else {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e)
-        q[i].v[e] = p < p1 && v + e >= 0 && v + e < a.V ? row[v + e] : from_f32<T>(-INFINITY);
-    }
-  }
-  float top = -INFINITY;
-  bool nan = false;
-#pragma unroll
-  for (int i = 0; i < PACKS; ++i)
-#pragma unroll
-    for (int e = 0; e < VEC / 2; ++e) {
-      const float2 x = pair_of(q[i], e);
-      nan |= !(x.x < INFINITY) || !(x.y < INFINITY);
-      top = fmaxf(top, fmaxf(x.x, x.y));
-    }
-  // the least of the largest elements of kThreads / span groups of threads
-  uint32_t high = order_of(top), low = high;
-  for (int o = 1; o < span; o <<= 1) low = max(low, __shfl_xor_sync(0xffffffffu, low, o));
-  high = __reduce_max_sync(0xffffffffu, high);
-  low = __reduce_min_sync(0xffffffffu, low);
-  if (lane == 0) warp_max[warp] = high, warp_min[warp] = low;
-  __syncthreads();
-  if (nan) bad = 1;      // NaN or +inf
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) high = max(high, warp_max[w]), low = min(low, warp_min[w]);
-  low = max(low, kMinusInf + 1);      // -inf is no candidate
-  const float m = from_order(high), at_least = from_order(low);
-  // exp((x - m) / tau) = 2^((x - m) k); all of a piece of -inf count as 0
-  const float k = steps(a.tau), mm = m == -INFINITY ? 0.f : m;
-  float sum = 0.f;
-#pragma unroll
-  for (int i = 0; i < PACKS; ++i) {
-    const int v = (p0 + i * kThreads + tid) * VEC - skip;
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      const float x = to_f32(q[i].v[e]);
-      sum += ex2_approx((x - mm) * k);
-      if (x >= at_least) {
-        const int n = atomicAdd(&n_found, 1);
-        if (n < kRoom) found[n] = entry_of(order_of(x), v + e);
-      }
-    }
-  }
-  sum = warp_sum(sum);
-  if (lane == 0) warp_sums[warp] = sum;
-  __syncthreads();
-  const int64_t slot = r * z.pieces + piece;
-  if (tid == 0) {
-    float s = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) s += warp_sums[w];
-    z.stats[slot] = bad ? make_float2(NAN, NAN) : make_float2(m, s);
-  }
-  uint64_t* const out = z.best + slot * a.take;
-  int n = n_found;
-  if (bad) n = 0;        // the row offers nothing
-  if (n > kRoom) {
-    // more than fit: the take-th largest order `lo`, then how many equals of it are taken
-    auto count_from = [&](uint32_t least) {
-      int c = 0;
-#pragma unroll
-      for (int i = 0; i < PACKS; ++i)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) c += order_of(to_f32(q[i].v[e])) >= least;
-      return count_all(c, scratch);
-    };
-    uint32_t lo = low, hi = high;      // at least take from lo on; the answer is at most hi
-    while (lo < hi) {
-      const uint32_t mid = lo + (hi - lo + 1) / 2;
-      if (count_from(mid) >= a.take) lo = mid; else hi = mid - 1;
-    }
-    const int above = lo == 0xffffffffu ? 0 : count_from(lo + 1);
-    int first = 0, last = a.V - 1;     // ids up to `first` hold enough equals
-    while (first < last) {
-      const int mid = first + (last - first) / 2;
-      int c = 0;
-#pragma unroll
-      for (int i = 0; i < PACKS; ++i)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e)
-          c += order_of(to_f32(q[i].v[e])) == lo && (p0 + i * kThreads + tid) * VEC - skip + e <= mid;
-      if (count_all(c, scratch) >= a.take - above) last = mid; else first = mid + 1;
-    }
-    __syncthreads();
-    if (tid == 0) n_found = 0;
-    __syncthreads();
+  auto fetch = [&](Pack<T, VEC> (&q)[PACKS], int from) {
 #pragma unroll
     for (int i = 0; i < PACKS; ++i) {
-      const int v = (p0 + i * kThreads + tid) * VEC - skip;
+      const int p = from + i * kThreads + tid, v = p * VEC - skip;
+      if (p < p1 && v >= 0 && v + VEC <= a.V) {
+        const uint4 w = __ldcs(reinterpret_cast<const uint4*>(row + v));
+        q[i] = *reinterpret_cast<const Pack<T, VEC>*>(&w);
+      } else {
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const uint32_t o = order_of(to_f32(q[i].v[e]));
-        if (o > lo || (o == lo && v + e <= first)) found[atomicAdd(&n_found, 1)] = entry_of(o, v + e);
+        for (int e = 0; e < VEC; ++e)
+          q[i].v[e] = p < p1 && v + e >= 0 && v + e < a.V ? row[v + e] : from_f32<T>(-INFINITY);
+      }
+    }
+  };
+  Pack<T, VEC> q[PACKS], next[PACKS];
+  fetch(q, p0);
+  const float k = steps(a.tau);
+  float m = -INFINITY, sum = 0.f;      // of this thread's elements: sum of 2^((x - m) k)
+  uint32_t low = kMinusInf;            // what is found lies above it
+  int before = 0;                      // found in earlier tiles
+  for (int from = p0; from < p1; from += kThreads * PACKS) {
+    if (from + kThreads * PACKS < p1) fetch(next, from + kThreads * PACKS);
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < PACKS; ++i)
+#pragma unroll
+      for (int e = 0; e < VEC / 2; ++e) {
+        const float2 x = pair_of(q[i], e);
+        top = fmaxf(top, fmaxf(x.x, x.y));
+      }
+    if (from == p0) {
+      // the least of the largest elements of kThreads / span groups of threads
+      uint32_t least = order_of(top);
+      for (int o = 1; o < span; o <<= 1) least = max(least, __shfl_xor_sync(0xffffffffu, least, o));
+      least = __reduce_min_sync(0xffffffffu, least);
+      if (lane == 0) warp_min[warp] = least;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) least = min(least, warp_min[w]);
+      low = max(least - 1, kMinusInf);
+      low -= low == kMinusZero;      // not below zero, as a number
+    }
+    const float above = from_order(low);
+    const float to = fmaxf(m, top), base = to == -INFINITY ? 0.f : to;
+    sum *= ex2_approx((m - base) * k);
+    m = to;
+#pragma unroll
+    for (int i = 0; i < PACKS; ++i)
+#pragma unroll
+      for (int e = 0; e < VEC / 2; ++e) {
+        const float2 x = pair_of(q[i], e);
+        sum += ex2_approx((x.x - base) * k) + ex2_approx((x.y - base) * k);
+      }
+    if (top > above) {
+#pragma unroll
+      for (int i = 0; i < PACKS; ++i) {
+        const int v = (from + i * kThreads + tid) * VEC - skip;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float x = to_f32(q[i].v[e]);
+          if (x > above) {
+            const int n = atomicAdd(&n_found, 1);
+            if (n < kRoom) found[n] = entry_of(order_of(x), v + e);
+          }
+        }
       }
     }
     __syncthreads();
-    n = n_found;         // take of them
+    int n = n_found;
+    if (n > kRoom) {
+      n = keep_best(found, before, a.take);
+      if (tid == 0) n_found = n;
+      __syncthreads();
+      add_best_of_tile<T, PACKS>(found, &n_found, scratch, row, from, p1, skip, a.V, low, a.take);
+      n = n_found;       // 2 take at most
+    }
+    if (from == p0 || n > kRoom / 2) {
+      n = keep_best(found, n, a.take);
+      // later elements have higher ids: those equal to the last one kept come behind it
+      if (n == a.take) low = static_cast<uint32_t>(found[n - 1] >> 32);
+      if (tid == 0) n_found = n;
+      __syncthreads();
+    }
+    before = n;
+#pragma unroll
+    for (int i = 0; i < PACKS; ++i) q[i] = next[i];
   }
-  for (int i = tid; i < n; i += kThreads) {
-    const uint64_t me = found[i];
-    int rank = 0;
-    for (int j = 0; j < n; ++j) rank += found[j] > me;
-    if (rank < a.take) out[rank] = me;
+  const float most = warp_max(m), at = most == -INFINITY ? 0.f : most;
+  sum = warp_sum(sum * ex2_approx((m - at) * k));
+  if (lane == 0) warp_sums[warp] = make_float2(most, sum);
+  const int n = keep_best(found, before, a.take);
+  const int64_t slot = r * z.pieces + piece;
+  uint64_t* const out = z.best + slot * a.take;
+  for (int i = tid; i < a.take; i += kThreads) out[i] = i < n ? found[i] : 0;
+  if (tid == 0) {
+    float top = -INFINITY, s = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, warp_sums[w].x);
+    const float from = top == -INFINITY ? 0.f : top;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) s += warp_sums[w].y * ex2_approx((warp_sums[w].x - from) * k);
+    // a NaN is in the sum, and an infinity minus itself is one
+    z.stats[slot] = s != s ? make_float2(NAN, NAN) : make_float2(top, s);
   }
-  for (int i = n + tid; i < a.take; i += kThreads) out[i] = 0;
 }
 
 // ------------------------------------------------------------------ the group's best
 enum : uint8_t { kLive, kEnded, kNone };   // a beam; kNone offers nothing
 
 struct Ranked {
-  double score;
-  int64_t at;      // j V + v
+  uint64_t score;  // an integer that grows with the 64-bit score (comparing those themselves
+  int64_t at;      // is slow here: 600 candidates took 190 us); j V + v
 };
+
+__device__ __forceinline__ uint64_t order_of(double x) {
+  const int64_t u = __double_as_longlong(x + 0.0);
+  return static_cast<uint64_t>(u ^ ((u >> 63) | static_cast<int64_t>(uint64_t{1} << 63)));
+}
+__device__ __forceinline__ double from_order(uint64_t k) {
+  return __longlong_as_double(static_cast<int64_t>(k >> 63 ? k ^ (uint64_t{1} << 63) : ~k));
+}
 
 __device__ __forceinline__ bool ahead(const Ranked& x, const Ranked& y) {
   return x.score > y.score || (x.score == y.score && x.at < y.at);
 }
 
-__global__ void __launch_bounds__(kBestThreads) best_kernel(BeamSelect a, Pieces z, int span) {
+__global__ void __launch_bounds__(kBestThreads) best_kernel(BeamSelect a, Pieces z) {
   __shared__ Ranked found[kRoom];
   // lse = top / tau + log s, so score(j, v) = (score_j - log s) + (x_v - top) / tau: a row
   // whose logits are all near the type's lowest value keeps its differences
@@ -228,7 +293,6 @@ __global__ void __launch_bounds__(kBestThreads) best_kernel(BeamSelect a, Pieces
   __shared__ float rough[kMaxBeams];       // the same in fp32
   __shared__ float tops[kMaxBeams];
   __shared__ uint8_t kind[kMaxBeams];
-  __shared__ float warp_low[kBestWarps];
   __shared__ int n_found;
   __shared__ Ranked warp_best[kBestWarps], last;
   pdl_wait_prerequisites();
@@ -298,7 +362,7 @@ __global__ void __launch_bounds__(kBestThreads) best_kernel(BeamSelect a, Pieces
   };
   auto exact = [&](int j, uint32_t order, int v) {
     const double x = static_cast<double>(from_order(order)) - static_cast<double>(tops[j]);
-    return Ranked{bias[j] + x * inv, static_cast<int64_t>(j) * a.V + v};
+    return Ranked{order_of(bias[j] + x * inv), static_cast<int64_t>(j) * a.V + v};
   };
   float low = -INFINITY;
   each([&](int j, uint32_t order, int) {
@@ -306,13 +370,16 @@ __global__ void __launch_bounds__(kBestThreads) best_kernel(BeamSelect a, Pieces
     const float f = estimate(j, order, err);
     low = fmaxf(low, f - err);       // NaN (an overflow) is passed over
   });
-  for (int o = 1; o < span; o <<= 1) low = fmaxf(low, __shfl_xor_sync(0xffffffffu, low, o));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
-  if (lane == 0) warp_low[warp] = low;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kBestWarps; ++w) low = fminf(low, warp_low[w]);
+  // the take-th largest of the threads' largest lower bounds, bit by bit (0 where fewer
+  // threads than that have one)
+  const uint32_t key = low > -INFINITY ? order_of(low) : 0;
+  uint32_t at_least = 0;
+#pragma unroll 1
+  for (int bit = 31; bit >= 0; --bit) {
+    const uint32_t more = at_least | 1u << bit;
+    if (__syncthreads_count(key >= more) >= a.take) at_least = more;
+  }
+  low = at_least ? from_order(at_least) : -INFINITY;
   each([&](int j, uint32_t order, int v) {
     float err;
     const float f = estimate(j, order, err);
@@ -322,13 +389,13 @@ __global__ void __launch_bounds__(kBestThreads) best_kernel(BeamSelect a, Pieces
   });
   if (tid < a.beams && kind[tid] == kEnded) {
     const int n = atomicAdd(&n_found, 1);
-    if (n < kRoom) found[n] = Ranked{bias[tid], static_cast<int64_t>(tid) * a.V + a.eos};
+    if (n < kRoom) found[n] = Ranked{order_of(bias[tid]), static_cast<int64_t>(tid) * a.V + a.eos};
   }
   __syncthreads();
   auto put = [&](int n, const Ranked& x) {
     const int j = static_cast<int>(x.at / a.V), v = static_cast<int>(x.at % a.V);
     const int64_t o = g * a.take + n;
-    a.out_scores[o] = static_cast<float>(x.score);
+    a.out_scores[o] = static_cast<float>(from_order(x.score));
     a.parents[o] = static_cast<int32_t>(r0 + j);
     a.tokens[o] = v;
     if (a.next_finished) a.next_finished[o] = kind[j] == kEnded || v == a.eos;
@@ -344,17 +411,17 @@ __global__ void __launch_bounds__(kBestThreads) best_kernel(BeamSelect a, Pieces
   } else {
     // more than fit (equal scores): one after the other, the first behind the last one put
     n = a.take;
-    if (tid == 0) last = Ranked{static_cast<double>(INFINITY), -1};
+    if (tid == 0) last = Ranked{~uint64_t{0}, -1};
     for (int t = 0; t < a.take; ++t) {
       __syncthreads();
       const Ranked before = last;
-      Ranked mine{-static_cast<double>(INFINITY), INT64_MAX};
+      Ranked mine{0, INT64_MAX};
       auto offer = [&](const Ranked& x) {
         if (ahead(before, x) && ahead(x, mine)) mine = x;
       };
       each([&](int j, uint32_t order, int v) { offer(exact(j, order, v)); });
       if (tid < a.beams && kind[tid] == kEnded)
-        offer(Ranked{bias[tid], static_cast<int64_t>(tid) * a.V + a.eos});
+        offer(Ranked{order_of(bias[tid]), static_cast<int64_t>(tid) * a.V + a.eos});
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
         const Ranked x{__shfl_xor_sync(0xffffffffu, mine.score, o), __shfl_xor_sync(0xffffffffu, mine.at, o)};
@@ -504,18 +571,23 @@ cudaError_t move(const BeamReorder& a, cudaStream_t s) {
 
 size_t round_up(size_t n) { return (n + 255) / 256 * 256; }
 
-// Pieces of a row: long ones where they fill the GPU.  A row that starts off a 16-byte
-// boundary spreads over up to one pack more.
+// Pieces of a row: several tiles each where rows alone nearly fill the GPU, one short tile
+// each where they do not.  A row that starts off a 16-byte boundary spreads over up to one
+// pack more.
 template <typename T>
 Pieces plan(int64_t R, int V, int& elements) {
   constexpr int VEC = kVec<T>;
   const int64_t packs = (static_cast<int64_t>(V) + 2 * VEC - 2) / VEC;
-  auto cut = [&](int elems) { return (packs * VEC + kThreads * elems - 1) / (static_cast<int64_t>(kThreads) * elems); };
-  elements = R * cut(kManyElements) >= kManyPieces ? kManyElements : kFewElements;
-  const int64_t pieces = cut(elements);
+  auto tiles = [&](int elems) { return (packs * VEC + kThreads * elems - 1) / (static_cast<int64_t>(kThreads) * elems); };
+  elements = R * tiles(kManyElements) >= kManyTiles ? kManyElements : kFewElements;
+  int64_t pieces = tiles(elements);
+  if (elements == kManyElements) {
+    const int64_t most = (kManyPieces + R - 1) / R;
+    pieces = pieces < most ? pieces : most;
+  }
   Pieces z{};
-  z.pieces = static_cast<int>(pieces);
   z.length = static_cast<int>((packs + pieces - 1) / pieces);
+  z.pieces = static_cast<int>((packs + z.length - 1) / z.length);
   return z;
 }
 
@@ -565,11 +637,8 @@ cudaError_t launch_beam_select(const BeamSelect& a, cudaStream_t s) {
     });
   });
   if (e != cudaSuccess) return e;
-  groups = kBestWarps;
-  while (groups < a.take) groups *= 2;
   return traced_launch("beam_select_best", s, [&] {
-    return launch_dependent(best_kernel, dim3(static_cast<unsigned>(a.R / a.beams)), kBestThreads, 0, 1, s, a, z,
-                            kBestThreads / groups);
+    return launch_dependent(best_kernel, dim3(static_cast<unsigned>(a.R / a.beams)), kBestThreads, 0, 1, s, a, z);
   });
 }
 

@@ -56,10 +56,9 @@ def test_workspace_sizes(lib):  # noqa: F811
     assert size(-1, 100, 4) == size(4, 0, 4) == size(4, 100, 0) == size(4, 100, 129) == 0
     assert size(4, (1 << 30) + 1, 4) == size((1 << 31) - 256, 100, 4) == 0
     assert size(0, 100, 4) > 0
-    # every piece's statistics and candidates: at most 2,048 columns of few rows, 8,192 of many
+    # every row's statistics and candidates, of one piece at least
     for rows, v, take in ((1, 1, 1), (4, 151936, 8), (256, 151936, 16), (64, 5000, 128), (1000, 2048, 2)):
-        pieces = -(-v // (2048 if rows * -(-v // 8192) < 304 else 8192))
-        assert size(rows, v, take) >= rows * pieces * 8 * (1 + take)
+        assert size(rows, v, take) >= rows * 8 * (1 + take)
 
 
 def test_layout_of_states():

@@ -151,6 +151,17 @@ def test_select_among_equals(dtype, R, K, V, N):
     check(z, s, K, N, exactly=True)
 
 
+@pytest.mark.parametrize("R,V,N", [(2, 40000, 100), (400, 9000, 8), (200, 40000, 3)])
+def test_select_of_ascending_and_descending_logits(R, V, N):
+    """Every tile's elements are above what was found before, or none is."""
+    ramp = torch.arange(V, device="cuda", dtype=torch.float32) / 1000
+    z = torch.stack([ramp, ramp.flip(0)]).repeat(R // 2, 1)
+    z[:, V // 2] = torch.where(torch.arange(R, device="cuda") % 4 == 0, float("nan"), z[:, V // 2])
+    s = -torch.rand(R, device="cuda")
+    check(z, s, 2, N)
+    check((z * 16).floor() / 16, s, 1, N)      # steps of equal logits
+
+
 def test_select_with_extreme_logits_and_temperatures():
     gen = torch.Generator("cuda").manual_seed(2)
     z = logits_of(8, 5000, F32, gen)
