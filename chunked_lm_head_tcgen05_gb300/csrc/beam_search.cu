@@ -22,6 +22,8 @@
 // beam_reorder moves states to the beams that go on: row r takes over row
 // parents[r].  In place a thread holds one column of a group's rows, reads what
 // other rows need and then writes, so rows that keep their place cost nothing.
+#include <type_traits>
+
 #include "element.cuh"
 #include "operators.h"
 #include "ptx.cuh"
@@ -57,6 +59,12 @@ __device__ __forceinline__ uint64_t entry_of(uint32_t order, int v) {
 
 // log2(e) / tau, finite for every tau
 __device__ __forceinline__ float steps(float tau) { return fminf(1.4426950408889634f / tau, 3.0e38f); }
+
+// Tiles in flight; a short piece is one tile.
+template <int ELEMS>
+constexpr int kStagesOf = ELEMS == kManyElements ? 4 : 2;
+template <typename T, int ELEMS>
+constexpr size_t kRingBytes = sizeof(T) * ELEMS * kThreads * kStagesOf<ELEMS>;
 
 struct Pieces {
   float2* stats;      // [R][pieces] maximum of x, sum of exp((x - maximum) / tau)
@@ -141,9 +149,31 @@ __device__ __noinline__ void add_best_of_tile(uint64_t* found, int* n_found, int
   __syncthreads();
 }
 
+// The largest of a thread's elements; NaN is passed over.
+template <typename T, int PACKS, int VEC>
+__device__ __forceinline__ float largest(const Pack<T, VEC> (&q)[PACKS]) {
+  if constexpr (sizeof(T) == 4) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < PACKS; ++i)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) top = fmaxf(top, q[i].v[e]);
+    return top;
+  } else {
+    using T2 = std::conditional_t<std::is_same_v<T, __half>, __half2, __nv_bfloat162>;
+    const T2* const v = reinterpret_cast<const T2*>(&q[0]);
+    T2 top = v[0];
+#pragma unroll
+    for (int e = 1; e < PACKS * VEC / 2; ++e) top = __hmax2(top, v[e]);
+    const float lo = to_f32(top.x), hi = to_f32(top.y);
+    return fmaxf(fmaxf(lo, hi), -INFINITY);       // of NaN alone: -inf
+  }
+}
+
 template <typename T, int ELEMS>
 __global__ void __launch_bounds__(kThreads, 4) scan_kernel(BeamSelect a, Pieces z, int span) {
-  constexpr int VEC = kVec<T>, PACKS = ELEMS / VEC;
+  constexpr int VEC = kVec<T>, PACKS = ELEMS / VEC, kStages = kStagesOf<ELEMS>;
+  extern __shared__ __align__(16) char ring_memory[];
   __shared__ uint64_t found[kRoom];
   __shared__ uint32_t warp_min[kWarps];
   __shared__ float2 warp_sums[kWarps];
@@ -159,36 +189,52 @@ __global__ void __launch_bounds__(kThreads, 4) scan_kernel(BeamSelect a, Pieces 
   const T* const row = static_cast<const T*>(a.logits) + r * a.ld;
   const int skip = static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
   const int p0 = piece * z.length, p1 = min(p0 + z.length, (a.V + skip + VEC - 1) / VEC);
-  auto fetch = [&](Pack<T, VEC> (&q)[PACKS], int from) {
+  // Whole packs come through a ring of asynchronous copies, each thread reading what it copied
+  // itself; packs that reach over the row's ends are read element by element.
+  const PackRing<T, VEC> ring(ring_memory, kThreads, tid);
+  const int whole0 = skip ? 1 : 0, whole1 = min(p1, (a.V + skip) / VEC);
+  constexpr int kTile = kThreads * PACKS;
+  auto fetch = [&](int from, int stage) {
+    const T* const src = row + (static_cast<int64_t>(from) + tid) * VEC - skip;
+    if (from >= whole0 && from + kTile <= whole1) {
 #pragma unroll
-    for (int i = 0; i < PACKS; ++i) {
-      const int p = from + i * kThreads + tid, v = p * VEC - skip;
-      if (p < p1 && v >= 0 && v + VEC <= a.V) {
-        const uint4 w = __ldcs(reinterpret_cast<const uint4*>(row + v));
-        q[i] = *reinterpret_cast<const Pack<T, VEC>*>(&w);
-      } else {
+      for (int i = 0; i < PACKS; ++i) ring.fetch(stage * PACKS + i, src + i * kThreads * VEC);
+    } else {
+#pragma unroll
+      for (int i = 0; i < PACKS; ++i) {
+        const int p = from + i * kThreads + tid;
+        if (p >= whole0 && p < whole1) ring.fetch(stage * PACKS + i, src + i * kThreads * VEC);
+      }
+    }
+  };
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) {
+    if (p0 + s * kTile < p1) fetch(p0 + s * kTile, s);
+    copy_async_commit();
+  }
+  const float k = steps(a.tau);
+  float m = -INFINITY, sum = 0.f;      // of this thread's elements: sum of 2^((x - m) k)
+  uint32_t low = kMinusInf;            // what is found lies above it
+  int before = 0, stage = 0;           // found in earlier tiles
+  for (int from = p0; from < p1; from += kTile) {
+    copy_async_wait<kStages - 2>();
+    Pack<T, VEC> q[PACKS];
+#pragma unroll
+    for (int i = 0; i < PACKS; ++i) q[i] = ring.read(stage * PACKS + i);
+    if (from < whole0 || from + kTile > whole1) {
+#pragma unroll
+      for (int i = 0; i < PACKS; ++i) {
+        const int p = from + i * kThreads + tid, v = p * VEC - skip;
+        if (p >= whole0 && p < whole1) continue;
 #pragma unroll
         for (int e = 0; e < VEC; ++e)
           q[i].v[e] = p < p1 && v + e >= 0 && v + e < a.V ? row[v + e] : from_f32<T>(-INFINITY);
       }
     }
-  };
-  Pack<T, VEC> q[PACKS], next[PACKS];
-  fetch(q, p0);
-  const float k = steps(a.tau);
-  float m = -INFINITY, sum = 0.f;      // of this thread's elements: sum of 2^((x - m) k)
-  uint32_t low = kMinusInf;            // what is found lies above it
-  int before = 0;                      // found in earlier tiles
-  for (int from = p0; from < p1; from += kThreads * PACKS) {
-    if (from + kThreads * PACKS < p1) fetch(next, from + kThreads * PACKS);
-    float top = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < PACKS; ++i)
-#pragma unroll
-      for (int e = 0; e < VEC / 2; ++e) {
-        const float2 x = pair_of(q[i], e);
-        top = fmaxf(top, fmaxf(x.x, x.y));
-      }
+    const int ahead = from + (kStages - 1) * kTile;
+    if (ahead < p1) fetch(ahead, stage == 0 ? kStages - 1 : stage - 1);
+    copy_async_commit();
+    const float top = largest<T, PACKS, VEC>(q);
     if (from == p0) {
       // the least of the largest elements of kThreads / span groups of threads
       uint32_t least = order_of(top);
@@ -203,15 +249,18 @@ __global__ void __launch_bounds__(kThreads, 4) scan_kernel(BeamSelect a, Pieces 
     }
     const float above = from_order(low);
     const float to = fmaxf(m, top), base = to == -INFINITY ? 0.f : to;
-    sum *= ex2_approx((m - base) * k);
+    const float shrink = ex2_approx((m - base) * k);
+    float2 sums = make_float2(sum * shrink, 0.f);
     m = to;
+    const float2 down = make_float2(-base, -base), kk = make_float2(k, k);
 #pragma unroll
     for (int i = 0; i < PACKS; ++i)
 #pragma unroll
       for (int e = 0; e < VEC / 2; ++e) {
-        const float2 x = pair_of(q[i], e);
-        sum += ex2_approx((x.x - base) * k) + ex2_approx((x.y - base) * k);
+        const float2 d = mul2(add2(pair_of(q[i], e), down), kk);
+        sums = add2(sums, make_float2(ex2_approx(d.x), ex2_approx(d.y)));
       }
+    sum = sums.x + sums.y;
     if (top > above) {
 #pragma unroll
       for (int i = 0; i < PACKS; ++i) {
@@ -235,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 4) scan_kernel(BeamSelect a, Pieces 
       add_best_of_tile<T, PACKS>(found, &n_found, scratch, row, from, p1, skip, a.V, low, a.take);
       n = n_found;       // 2 take at most
     }
-    if (from == p0 || n > kRoom / 2) {
+    if (from == p0 || n > 2 * a.take + 16) {
       n = keep_best(found, n, a.take);
       // later elements have higher ids: those equal to the last one kept come behind it
       if (n == a.take) low = static_cast<uint32_t>(found[n - 1] >> 32);
@@ -243,9 +292,9 @@ __global__ void __launch_bounds__(kThreads, 4) scan_kernel(BeamSelect a, Pieces 
       __syncthreads();
     }
     before = n;
-#pragma unroll
-    for (int i = 0; i < PACKS; ++i) q[i] = next[i];
+    stage = stage == kStages - 1 ? 0 : stage + 1;
   }
+  copy_async_wait<0>();
   const float most = warp_max(m), at = most == -INFINITY ? 0.f : most;
   sum = warp_sum(sum * ex2_approx((m - at) * k));
   if (lane == 0) warp_sums[warp] = make_float2(most, sum);
@@ -632,8 +681,15 @@ cudaError_t launch_beam_select(const BeamSelect& a, cudaStream_t s) {
   cudaError_t e = traced_launch("beam_select_scan", s, [&] {
     return by_type(a.type, [&](auto t) {
       using T = decltype(t);
-      auto kern = elements == kManyElements ? scan_kernel<T, kManyElements> : scan_kernel<T, kFewElements>;
-      return launch_dependent(kern, dim3(static_cast<unsigned>(slots)), kThreads, 0, 1, s, a, z, kThreads / groups);
+      if (elements == kFewElements)
+        return launch_dependent(scan_kernel<T, kFewElements>, dim3(static_cast<unsigned>(slots)), kThreads,
+                                kRingBytes<T, kFewElements>, 1, s, a, z, kThreads / groups);
+      static std::atomic<int> ready[64];
+      constexpr size_t ring = kRingBytes<T, kManyElements>;
+      const cudaError_t r = allow_shared(ready, reinterpret_cast<const void*>(scan_kernel<T, kManyElements>), ring);
+      if (r != cudaSuccess) return r;
+      return launch_dependent(scan_kernel<T, kManyElements>, dim3(static_cast<unsigned>(slots)), kThreads, ring, 1, s, a,
+                              z, kThreads / groups);
     });
   });
   if (e != cudaSuccess) return e;
