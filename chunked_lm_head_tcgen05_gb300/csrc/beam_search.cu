@@ -33,7 +33,9 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kManyElements = 16;    // per thread and tile, of many rows: tiles of 4,096
+// Elements per thread and tile of many rows: 64 bytes, so tiles of 8,192 16-bit elements.
+template <typename T>
+constexpr int kManyElements = 64 / static_cast<int>(sizeof(T));
 constexpr int kFewElements = 8;      // of few rows: pieces of one tile of 2,048
 constexpr int64_t kManyTiles = 304;  // the long tiles from which on they fill the GPU
 constexpr int64_t kManyPieces = 608; // CTAs that many rows are cut into
@@ -62,7 +64,7 @@ __device__ __forceinline__ float steps(float tau) { return fminf(1.4426950408889
 
 // Tiles in flight; a short piece is one tile.
 template <int ELEMS>
-constexpr int kStagesOf = ELEMS == kManyElements ? 4 : 2;
+constexpr int kStagesOf = ELEMS == kFewElements ? 2 : 3;
 template <typename T, int ELEMS>
 constexpr size_t kRingBytes = sizeof(T) * ELEMS * kThreads * kStagesOf<ELEMS>;
 
@@ -628,10 +630,10 @@ Pieces plan(int64_t R, int V, int& elements) {
   constexpr int VEC = kVec<T>;
   const int64_t packs = (static_cast<int64_t>(V) + 2 * VEC - 2) / VEC;
   auto tiles = [&](int elems) { return (packs * VEC + kThreads * elems - 1) / (static_cast<int64_t>(kThreads) * elems); };
-  elements = R * tiles(kManyElements) >= kManyTiles ? kManyElements : kFewElements;
+  elements = R * tiles(kManyElements<T>) >= kManyTiles ? kManyElements<T> : kFewElements;
   int64_t pieces = tiles(elements);
-  if (elements == kManyElements) {
-    const int64_t most = (kManyPieces + R - 1) / R;
+  if (elements != kFewElements) {
+    const int64_t most = R < kManyPieces ? kManyPieces / R : 1;    // no second wave of CTAs
     pieces = pieces < most ? pieces : most;
   }
   Pieces z{};
@@ -685,10 +687,10 @@ cudaError_t launch_beam_select(const BeamSelect& a, cudaStream_t s) {
         return launch_dependent(scan_kernel<T, kFewElements>, dim3(static_cast<unsigned>(slots)), kThreads,
                                 kRingBytes<T, kFewElements>, 1, s, a, z, kThreads / groups);
       static std::atomic<int> ready[64];
-      constexpr size_t ring = kRingBytes<T, kManyElements>;
-      const cudaError_t r = allow_shared(ready, reinterpret_cast<const void*>(scan_kernel<T, kManyElements>), ring);
+      constexpr size_t ring = kRingBytes<T, kManyElements<T>>;
+      const cudaError_t r = allow_shared(ready, reinterpret_cast<const void*>(scan_kernel<T, kManyElements<T>>), ring);
       if (r != cudaSuccess) return r;
-      return launch_dependent(scan_kernel<T, kManyElements>, dim3(static_cast<unsigned>(slots)), kThreads, ring, 1, s, a,
+      return launch_dependent(scan_kernel<T, kManyElements<T>>, dim3(static_cast<unsigned>(slots)), kThreads, ring, 1, s, a,
                               z, kThreads / groups);
     });
   });
