@@ -901,16 +901,12 @@ def lmhead_beam_select(logits, beams, take, scores, finished, eos_id, temperatur
                  _ptr(lse), workspace.data_ptr(), workspace.nbytes)
 
 
-def _state_layout(state, out, dim):
-    """(outer, mid, inner_bytes, (outer, row, mid) strides in bytes of state and of out): the
-    dimensions before `dim` as one, those behind it as one and a contiguous rest."""
-    size = state.element_size()
-    a, b = state.stride(), out.stride()
-
+@functools.lru_cache(maxsize=128)
+def _layout(shape, a, b, dim, size):
     def merged(dims):
         got = []      # [size, stride, stride], inner dimensions last
         for i in dims:
-            n = state.shape[i]
+            n = shape[i]
             if n == 1:
                 continue
             if got and got[-1][1] == n * a[i] and got[-1][2] == n * b[i]:
@@ -919,19 +915,24 @@ def _state_layout(state, out, dim):
                 got.append([n, a[i], b[i]])
         return got
 
-    before, behind = merged(range(dim)), merged(range(dim + 1, state.dim()))
+    before, behind = merged(range(dim)), merged(range(dim + 1, len(shape)))
     inner = 1
     if behind and behind[-1][1] == 1 and behind[-1][2] == 1:
         inner = behind.pop()[0]
     if len(before) > 1 or len(behind) > 1:
         raise ValueError("state must be one block of rows, repeated at most once outside `dim` and "
-                         "once inside it: got shape %s, strides %s and %s"
-                         % (tuple(state.shape), a, b))
+                         "once inside it: got shape %s, strides %s and %s" % (shape, a, b))
     outer = before[0] if before else (1, 0, 0)
     mid = behind[0] if behind else (1, 0, 0)
     return outer[0], mid[0], inner * size, \
         (outer[1] * size, a[dim] * size, mid[1] * size), \
         (outer[2] * size, b[dim] * size, mid[2] * size)
+
+
+def _state_layout(state, out, dim):
+    """(outer, mid, inner_bytes, (outer, row, mid) strides in bytes of state and of out): the
+    dimensions before `dim` as one, those behind it as one and a contiguous rest."""
+    return _layout(tuple(state.shape), state.stride(), out.stride(), dim, state.element_size())
 
 
 def lmhead_beam_reorder(state, out, parents, dim, beams=0, clear_missing=False, stream=None):

@@ -666,15 +666,10 @@ size_t beam_workspace(int64_t R, int V, int take) {
   return most > 256 ? most : 256;
 }
 
-bool beam_select_fits(int type, int64_t R, int V) {
-  int elements = 0;
-  return by_type(type, [&](auto t) { return R * plan<decltype(t)>(R, V, elements).pieces; }) <= 0x7fffffff;
-}
-
 cudaError_t launch_beam_select(const BeamSelect& a, cudaStream_t s) {
   int elements = 0;
   Pieces z = by_type(a.type, [&](auto t) { return plan<decltype(t)>(a.R, a.V, elements); });
-  const size_t slots = static_cast<size_t>(a.R) * z.pieces;
+  const size_t slots = static_cast<size_t>(a.R) * z.pieces;      // below 2^31: see plan
   z.stats = static_cast<float2*>(a.workspace);
   z.best = reinterpret_cast<uint64_t*>(static_cast<char*>(a.workspace) + round_up(slots * sizeof(float2)));
   // groups of threads, at least `take` of them (whole warps at most)

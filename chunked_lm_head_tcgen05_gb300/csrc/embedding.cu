@@ -8,8 +8,8 @@
 // fp32 registers, writing an id's sum when the id ends.  An id whose tokens cross
 // from one such segment into the next leaves partial sums, which join_kernel adds
 // in order: no atomics, same inputs, same bits.  A dense gradient also needs
-// zeros in the rows of ids that do not occur; CTAs of the same launch write them,
-// so every row of d_weight is written once.
+// zeros in the rows of ids that do not occur: the SMs that do not sort write the first
+// rows meanwhile, and CTAs of the summing launch the rest of them.
 // Sums are rounded once, where d_weight is bf16.
 #include "element.cuh"
 #include "operators.h"
@@ -29,6 +29,7 @@ constexpr int kFillRows = 16;   // table rows per CTA that writes zeros
 constexpr int kJoinThreads = 256;
 constexpr int kJoinColumns = 128;
 constexpr int kJoinSegments = 32;
+constexpr int kJoinShort = 16;
 
 int segment_of(int64_t n) { return n < kFew ? kShort : kLong; }
 
@@ -114,9 +115,11 @@ struct Sorted {
   float* part;      // [segments][2][H]: sums that began before the segment, and that go on after it
   int n;            // sorted ids, `live` of them inside the table
   int segments;
+  int filled;       // rows of d_weight that are zero already, a multiple of kFillRows
 };
 
-// Zeros in the rows [v0, v0 + kFillRows) of ids that do not occur.
+// Zeros in the rows [v0, v0 + kFillRows) of ids that do not occur; the rows before
+// z.filled got theirs beside the sort.
 template <typename O>
 __device__ void fill_zeros(const EmbedBwd& a, const Sorted& z, int64_t v0) {
   __shared__ int absent[kFillRows];
@@ -176,7 +179,7 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(EmbedBwd a, Sorted z, 
   pdl_launch_dependents();
   const unsigned summing = static_cast<unsigned>(z.segments) * chunks;
   if (blockIdx.x >= summing) {
-    fill_zeros<O>(a, z, static_cast<int64_t>(blockIdx.x - summing) * kFillRows);
+    fill_zeros<O>(a, z, z.filled + static_cast<int64_t>(blockIdx.x - summing) * kFillRows);
     return;
   }
   const int sgm = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
@@ -233,52 +236,79 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(EmbedBwd a, Sorted z, 
     put<O, VEC>(out + static_cast<int64_t>(key[n - 1]) * a.H, sum, a.scale, a.accumulate);
 }
 
-// Ids that cross segments: the segment where such an id begins holds its first
-// sum, the following ones the rest.  Grid (kJoinSegments segments, kJoinColumns
-// columns); a CTA's warps take consecutive parts of a long id's segments.
+// Ids that cross segments: the segment where such an id begins holds its first sum, the
+// following ones the rest.  Grid (kJoinSegments segments, kJoinColumns columns).  A warp
+// adds an id of up to kJoinShort segments more; longer ones take the whole CTA, its warps
+// consecutive parts of the id's segments, whose sums are then added in order.
+// One id after the other by the whole CTA, its end found by bisection, took 70 us for
+// 65,536 tokens of 2,560 columns, most of them waiting for a few rows.
 template <typename O>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(EmbedBwd a, Sorted z, int seg) {
   constexpr int kWarps = kJoinThreads / 32, kEach = kJoinColumns / 32;
   __shared__ uint32_t todo;
+  __shared__ int rests[kJoinSegments];
   __shared__ float sums[kWarps][kJoinColumns];
   pdl_wait_prerequisites();
   pdl_launch_dependents();
   const int live = *z.live, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int seg0 = blockIdx.x * kJoinSegments;
   if (warp == 0) {
-    const int64_t at = (static_cast<int64_t>(blockIdx.x) * kJoinSegments + lane) * seg, next = at + seg;
+    const int64_t at = static_cast<int64_t>(seg0 + lane) * seg, next = at + seg;
     bool owns = false;
     if (next < live) {
-      const int key = z.keys[next - 1];
-      owns = z.keys[next] == key && !(z.keys[at] == key && at > 0 && z.keys[at - 1] == key);
+      const int before = at > 0 ? z.keys[at - 1] : -1, first = z.keys[at], key = z.keys[next - 1], after = z.keys[next];
+      owns = after == key && !(first == key && before == key);
     }
     const uint32_t b = __ballot_sync(0xffffffffu, owns);
     if (lane == 0) todo = b;
   }
   __syncthreads();
-  const int c0 = blockIdx.y * kJoinColumns + lane;
-  for (uint32_t left = todo; left; left &= left - 1) {
-    const int sgm = blockIdx.x * kJoinSegments + __ffs(static_cast<int>(left)) - 1;
+  if (todo == 0) return;
+  const int last_segment = (live - 1) / seg, c0 = blockIdx.y * kJoinColumns + lane;
+  auto partial = [&](int sgm, int which, float (&sum)[kEach]) {
+#pragma unroll
+    for (int e = 0; e < kEach; ++e)
+      if (c0 + 32 * e < a.H) sum[e] += z.part[(static_cast<int64_t>(sgm) * 2 + which) * a.H + c0 + 32 * e];
+  };
+  int turn = 0;
+  for (uint32_t left = todo; left; left &= left - 1, ++turn) {
+    if (turn % kWarps != warp) continue;
+    const int bit = __ffs(static_cast<int>(left)) - 1, sgm = seg0 + bit;
     const int key = z.keys[(sgm + 1) * seg - 1];
-    // last segment that begins with this id
-    int lo = sgm + 1, hi = (live - 1) / seg;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (z.keys[mid * seg] == key) lo = mid; else hi = mid - 1;
+    // segments behind this one that begin with the id
+    int rest = 0;
+    for (int from = sgm + 1;; from += 32) {
+      const int s = from + lane;
+      const bool same = s <= last_segment && z.keys[static_cast<int64_t>(s) * seg] == key;
+      const uint32_t b = __ballot_sync(0xffffffffu, same);
+      rest += b == 0xffffffffu ? 32 : __ffs(static_cast<int>(~b)) - 1;
+      if (b != 0xffffffffu) break;
     }
-    const int rest = lo - sgm, each = (rest + kWarps - 1) / kWarps;
-    const int from = sgm + 1 + warp * each, to = min(from + each, lo + 1);
+    if (lane == 0) rests[bit] = rest;
+    if (rest > kJoinShort) continue;
     float sum[kEach] = {};
-    if (warp == 0) {
+    partial(sgm, 1, sum);
+#pragma unroll 4
+    for (int i = 1; i <= rest; ++i) partial(sgm + i, 0, sum);
 #pragma unroll
-      for (int e = 0; e < kEach; ++e)
-        if (c0 + 32 * e < a.H) sum[e] = z.part[(static_cast<int64_t>(sgm) * 2 + 1) * a.H + c0 + 32 * e];
-    }
+    for (int e = 0; e < kEach; ++e)
+      if (c0 + 32 * e < a.H) {
+        const float total[1] = {sum[e]};
+        put<O, 1>(static_cast<O*>(a.d_weight) + static_cast<int64_t>(key) * a.H + c0 + 32 * e, total, a.scale,
+                  a.accumulate);
+      }
+  }
+  __syncthreads();
+  for (uint32_t left = todo; left; left &= left - 1) {
+    const int bit = __ffs(static_cast<int>(left)) - 1, sgm = seg0 + bit, rest = rests[bit];
+    if (rest <= kJoinShort) continue;
+    const int key = z.keys[(sgm + 1) * seg - 1];
+    const int each = (rest + kWarps - 1) / kWarps;
+    const int from = sgm + 1 + warp * each, to = min(from + each, sgm + rest + 1);
+    float sum[kEach] = {};
+    if (warp == 0) partial(sgm, 1, sum);
 #pragma unroll 8
-    for (int i = from; i < to; ++i) {
-#pragma unroll
-      for (int e = 0; e < kEach; ++e)
-        if (c0 + 32 * e < a.H) sum[e] += z.part[static_cast<int64_t>(i) * 2 * a.H + c0 + 32 * e];
-    }
+    for (int i = from; i < to; ++i) partial(i, 0, sum);
 #pragma unroll
     for (int e = 0; e < kEach; ++e) sums[warp][lane + 32 * e] = sum[e];
     __syncthreads();
@@ -313,7 +343,7 @@ cudaError_t launch_sums(const EmbedBwd& a, const Sorted& z, int64_t first, int s
                     reinterpret_cast<uintptr_t>(a.d_weight) % 16 == 0;
   const int per_cta = kSumThreads * (wide ? VEC : 1);
   const int chunks = (a.H + per_cta - 1) / per_cta;
-  const int64_t grid = static_cast<int64_t>(z.segments) * chunks + (fill ? (a.V + kFillRows - 1) / kFillRows : 0);
+  const int64_t grid = static_cast<int64_t>(z.segments) * chunks + (fill ? (a.V - z.filled + kFillRows - 1) / kFillRows : 0);
   auto kern = wide ? sum_kernel<D, O, VEC> : sum_kernel<D, O, 1>;
   return launch_dependent(kern, dim3(static_cast<unsigned>(grid)), kSumThreads, 0, 1, s, a, z, first, seg, chunks);
 }
@@ -321,6 +351,10 @@ cudaError_t launch_sums(const EmbedBwd& a, const Sorted& z, int64_t first, int s
 size_t round_up(size_t n) { return (n + 255) / 256 * 256; }
 
 }  // namespace
+
+// Bytes that the SMs beside the sort can write in its time (measured: 10 us for 4,096
+// ids, 37 for 65,536), at some 5 TB/s.
+size_t sort_time_bytes(int n) { return n <= 1024 ? 0 : (size_t{25} << 20) + static_cast<size_t>(n) * 2300; }
 
 // Count, sorted ids and positions, partial sums of the segments of one sort.
 size_t embed_workspace(int64_t N, int H) {
@@ -364,8 +398,14 @@ cudaError_t launch_embed_bwd(const EmbedBwd& call, cudaStream_t s) {
     z.part = reinterpret_cast<float*>(p + 256 + 2 * round_up(4 * static_cast<size_t>(n)));
     z.n = n;
     z.segments = (n + seg - 1) / seg;
+    // what the GPU writes while one cluster sorts
+    const size_t row = (a.d_type == kF32 ? 4 : 2) * static_cast<size_t>(a.H);
+    const bool beside = !a.accumulate && reinterpret_cast<uintptr_t>(a.d_weight) % 16 == 0;
+    size_t rows = beside ? sort_time_bytes(n) / row / kFillRows * kFillRows : 0;
+    if (rows > static_cast<size_t>(a.V)) rows = a.V / kFillRows * kFillRows;
+    z.filled = static_cast<int>(rows);
     cudaError_t e = traced_launch("embedding_bwd_sort", s, [&] {
-      return launch_sort_ids(a.ids + first, n, a.V, true, a.skip, z.keys, z.pos, z.live, s);
+      return launch_sort_ids(a.ids + first, n, a.V, true, a.skip, z.keys, z.pos, z.live, s, a.d_weight, rows * row);
     });
     if (e != cudaSuccess) return e;
     e = traced_launch("embedding_bwd", s, [&] {

@@ -154,9 +154,10 @@ cudaError_t launch_process_logits(const ProcessLogits& a, cudaStream_t s);
 constexpr int kSortMost = 131072;
 // Stable sort of n <= kSortMost ids (NULL: all 0): keys ascending, pos their places in `ids`.  Ids
 // outside [0, bound) and `skip` (-1: none) count as `bound` and come last; with `wrap`,
-// ids in [-bound, 0) first become id + bound.  *live: how many are inside.
+// ids in [-bound, 0) first become id + bound.  *live: how many are inside.  Meanwhile the
+// other SMs clear zero_bytes (a multiple of 16) at `zeros`, which is aligned to 16.
 cudaError_t launch_sort_ids(const int32_t* ids, int n, int bound, bool wrap, int skip, int32_t* keys,
-                            int32_t* pos, int* live, cudaStream_t s);
+                            int32_t* pos, int* live, cudaStream_t s, void* zeros = nullptr, size_t zero_bytes = 0);
 
 // ------------------------------------------------------------------ embedding
 struct EmbedFwd {
@@ -218,7 +219,6 @@ struct BeamSelect {
 };
 
 size_t beam_workspace(int64_t R, int V, int take);
-bool beam_select_fits(int type, int64_t R, int V);   // the grid
 cudaError_t launch_beam_select(const BeamSelect& a, cudaStream_t s);
 
 // dst[o][r][m] = src[o][parents[r]][m], `inner` contiguous bytes each; strides in bytes.

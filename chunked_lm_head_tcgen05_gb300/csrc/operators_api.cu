@@ -444,7 +444,6 @@ lmhead_status lmhead_beam_select(const void* logits, int type, int64_t ld, int64
                         static_cast<const void*>(lse)})
     if (!aligned_to(p, kF32)) return LMHEAD_ERR_UNSUPPORTED;
   if (!aligned_to(logits, type) || (reinterpret_cast<uintptr_t>(workspace) & 255)) return LMHEAD_ERR_UNSUPPORTED;
-  if (!beam_select_fits(type, R, V)) return LMHEAD_ERR_UNSUPPORTED;
   if (workspace_bytes < beam_workspace(R, V, take)) return LMHEAD_ERR_WORKSPACE_TOO_SMALL;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const BeamSelect a{logits, type, ld, R, V, beams, take, scores, finished, eos_id, temperature,

@@ -29,9 +29,12 @@ struct SortArgs {
   int skip;        // an id (after wrapping) that counts as outside; -1: none
   int bits;        // of a digit
   int passes;
+  int ctas;        // of the cluster
   int32_t* keys;   // [n] ascending
   int32_t* pos;    // [n]
   int* live;       // ids inside
+  uint4* zeros;    // cleared by the clusters behind the first
+  size_t n_zeros;  // 16-byte units
 };
 
 __device__ __forceinline__ uint64_t pair_of_key(uint32_t key, uint32_t pos) {
@@ -49,9 +52,15 @@ __global__ void __launch_bounds__(kThreads) sort_kernel(SortArgs a) {
   int* const mine = part + kWarps;                                             // ids inside, this CTA
   constexpr int P = kThreads * ITEMS;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rank = static_cast<int>(blockIdx.x), ctas = static_cast<int>(gridDim.x);   // one cluster
+  const int rank = static_cast<int>(blockIdx.x), ctas = a.ctas;   // the first cluster sorts
   pdl_wait_prerequisites();
   pdl_launch_dependents();
+  if (static_cast<int>(blockIdx.x) >= ctas) {
+    const size_t stride = static_cast<size_t>(gridDim.x - ctas) * kThreads;
+    for (size_t i = static_cast<size_t>(blockIdx.x - ctas) * kThreads + tid; i < a.n_zeros; i += stride)
+      a.zeros[i] = make_uint4(0u, 0u, 0u, 0u);
+    return;
+  }
   const int first = warp * 32 * ITEMS + lane;
   const int digits = 1 << a.bits;
   const uint32_t last = a.passes * a.bits >= 32 ? 0xffffffffu : (1u << (a.passes * a.bits)) - 1u;
@@ -161,31 +170,34 @@ __global__ void __launch_bounds__(kThreads) sort_kernel(SortArgs a) {
 }
 
 template <int ITEMS>
-cudaError_t launch(const SortArgs& a, int ctas, cudaStream_t s) {
+cudaError_t launch(const SortArgs& a, int grid, cudaStream_t s) {
   static std::atomic<int> ready[64];
   constexpr size_t smem = size_t{8} * kThreads * ITEMS + 2 * kWarps * kMaxDigits + 4 * (2 * kMaxDigits + kWarps + 1);
   const cudaError_t e = allow_shared(ready, reinterpret_cast<const void*>(sort_kernel<ITEMS>), smem);
   if (e != cudaSuccess) return e;
-  return launch_dependent(sort_kernel<ITEMS>, dim3(ctas), kThreads, smem, ctas, s, a);
+  return launch_dependent(sort_kernel<ITEMS>, dim3(grid), kThreads, smem, a.ctas, s, a);
 }
 
 }  // namespace
 
 cudaError_t launch_sort_ids(const int32_t* ids, int n, int bound, bool wrap, int skip, int32_t* keys,
-                            int32_t* pos, int* live, cudaStream_t s) {
+                            int32_t* pos, int* live, cudaStream_t s, void* zeros, size_t zero_bytes) {
   if (n <= 0 || n > kSortMost) return cudaErrorInvalidValue;
   // keys run from 0 to `bound`
   int width = 1;
   while (width < 31 && (bound >> width) != 0) ++width;
-  const int passes = (width + 8) / 9;
-  const SortArgs a{ids, n, bound, wrap ? 1 : 0, skip, (width + passes - 1) / passes, passes, keys, pos, live};
-  if (n <= kThreads) return launch<1>(a, 1, s);
-  const int items = (n + kCluster * kThreads - 1) / (kCluster * kThreads);
-  if (items <= 1) return launch<1>(a, kCluster, s);
-  if (items <= 2) return launch<2>(a, kCluster, s);
-  if (items <= 4) return launch<4>(a, kCluster, s);
-  if (items <= 8) return launch<8>(a, kCluster, s);
-  return launch<16>(a, kCluster, s);
+  const int passes = (width + 8) / 9, ctas = n <= kThreads ? 1 : kCluster;
+  const SortArgs a{ids, n, bound, wrap ? 1 : 0, skip, (width + passes - 1) / passes, passes, ctas, keys, pos, live,
+                   static_cast<uint4*>(zeros), zero_bytes / 16};
+  // one CTA per SM; the sorting cluster's are taken
+  const int sms = zero_bytes ? sm_count() : 0;
+  const int grid = sms > 2 * ctas ? sms / ctas * ctas : zero_bytes ? 2 * ctas : ctas;
+  const int items = ctas == 1 ? 1 : (n + kCluster * kThreads - 1) / (kCluster * kThreads);
+  if (items <= 1) return launch<1>(a, grid, s);
+  if (items <= 2) return launch<2>(a, grid, s);
+  if (items <= 4) return launch<4>(a, grid, s);
+  if (items <= 8) return launch<8>(a, grid, s);
+  return launch<16>(a, grid, s);
 }
 
 }  // namespace lmh

@@ -635,9 +635,8 @@ lmhead_status lmhead_adapters_bwd(const void* grad_out, int type, int64_t grad_l
  * fewer than `take` candidates the rest have score -inf, parent -1 and id -1 (and
  * next_finished 0).
  *  workspace     lmhead_beam_workspace_size(R, V, take) bytes, 256-byte aligned
- * R must be a multiple of beams.  beams <= 64, take <= 128, V <= 2^30, R < 2^31 - 256 and
- * pieces of rows within the launch limits (LMHEAD_ERR_UNSUPPORTED beyond).  HBM-bound: one
- * read of the logits.  R == 0 is a no-op.
+ * R must be a multiple of beams.  beams <= 64, take <= 128, V <= 2^30 and R < 2^31 - 256
+ * (LMHEAD_ERR_UNSUPPORTED beyond).  HBM-bound: one read of the logits.  R == 0 is a no-op.
  */
 size_t lmhead_beam_workspace_size(int64_t R, int32_t V, int32_t take);
 

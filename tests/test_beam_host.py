@@ -23,7 +23,6 @@ CASES = [
         (dict(eos=100), INVALID), (dict(eos=-2, finished=None), INVALID),
         (dict(beams=65, R=65), UNSUPPORTED), (dict(take=129), UNSUPPORTED),
         (dict(R=(1 << 31) - 256), UNSUPPORTED), (dict(V=(1 << 30) + 1, ld=1 << 31), UNSUPPORTED),
-        (dict(V=1 << 30, ld=1 << 30, R=1 << 28), UNSUPPORTED),
         (dict(logits=P((1 << 20) + 2)), UNSUPPORTED), (dict(workspace=P((1 << 20) + 16)), UNSUPPORTED),
         (dict(scores=P((1 << 20) + 2)), UNSUPPORTED), (dict(lse=P((1 << 20) + 1)), UNSUPPORTED),
         (dict(bytes=128), SMALL), (dict(R=0, logits=None), OK)]),
