@@ -69,6 +69,7 @@ struct Plan {
   Item* few;
   int most;          // items at most, so also of the other lists
   int run_rows;
+  int use_few;
   int rows;
   int n;
 };
@@ -143,14 +144,64 @@ __device__ __forceinline__ void at_columns(bool aligned, int c, int width, F&& f
 }
 
 // ------------------------------------------------------------------ items
-__global__ void __launch_bounds__(1024) plan_kernel(Plan p) {
+constexpr int kSmallRows = 1024, kSmallKeys = 512;
+
+// kSmall: up to kSmallRows rows of fewer than kSmallKeys - 1 adapters, sorted here in one pass
+// of sort_ids.cu's kind, whose digit is the adapter: a launch less.
+template <bool kSmall>
+__global__ void __launch_bounds__(1024) plan_kernel(Plan p, const int32_t* ids) {
   __shared__ int sums[3][32], total[3];
   pdl_wait_prerequisites();
   pdl_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (int g = tid; g <= p.rows; g += 1024) {
-    const int before = g == 0 ? -1 : p.keys[g - 1], here = g == p.rows ? p.n + 1 : p.keys[g];
-    for (int a = before + 1; a <= here; ++a) p.starts[a] = g;
+  if constexpr (kSmall) {
+    __shared__ uint16_t counts[32][kSmallKeys];
+    __shared__ int base[kSmallKeys];
+    int key = p.n + 1;         // places past the end
+    if (tid < p.rows) {
+      key = ids ? ids[tid] : 0;
+      if (key < 0 || key >= p.n) key = p.n;
+    }
+    for (int k = lane; k < p.n + 2; k += 32) counts[warp][k] = 0;
+    __syncwarp();
+    const uint32_t peers = __match_any_sync(0xffffffffu, key);
+    if (lane == __ffs(static_cast<int>(peers)) - 1) counts[warp][key] = static_cast<uint16_t>(__popc(peers));
+    __syncthreads();
+    int all = 0;
+    if (tid < p.n + 2) {
+#pragma unroll 8
+      for (int w = 0; w < 32; ++w) {
+        const int c = counts[w][tid];
+        counts[w][tid] = static_cast<uint16_t>(all);
+        all += c;
+      }
+    }
+    int scan = all;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, scan, o);
+      if (lane >= o) scan += v;
+    }
+    if (lane == 31) sums[0][warp] = scan;
+    __syncthreads();
+    if (tid < p.n + 2) {
+      int first = scan - all;
+      for (int w = 0; w < warp; ++w) first += sums[0][w];
+      base[tid] = first;
+      p.starts[tid] = first;
+      if (tid == p.n) *p.live = first;
+    }
+    __syncthreads();
+    if (tid < p.rows) {
+      const int to = base[key] + counts[warp][key] + __popc(peers & ((1u << lane) - 1u));
+      p.keys[to] = key;
+      p.pos[to] = tid;
+    }
+  } else {
+    for (int g = tid; g <= p.rows; g += 1024) {
+      const int before = g == 0 ? -1 : p.keys[g - 1], here = g == p.rows ? p.n + 1 : p.keys[g];
+      for (int a = before + 1; a <= here; ++a) p.starts[a] = g;
+    }
   }
   if (tid < 3) total[tid] = 0;
   __syncthreads();
@@ -158,7 +209,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(Plan p) {
     const int a = a0 + tid;
     const int first = a <= p.n ? p.starts[a] : 0, count = a <= p.n ? p.starts[a + 1] - first : 0;
     // a last run of few rows is listed with the few, if its rows have an adapter
-    const int rest = count % p.run_rows, is_few = rest > 0 && rest <= kFewRows && a < p.n;
+    const int rest = count % p.run_rows, is_few = p.use_few && rest > 0 && rest <= kFewRows && a < p.n;
     const int mine[3] = {(count + kRows - 1) / kRows, (count + p.run_rows - 1) / p.run_rows - is_few, is_few};
     int scan[3];
 #pragma unroll
@@ -405,10 +456,18 @@ __global__ void __launch_bounds__(kThreads) narrow_kernel(const X* wide, int64_t
 }
 
 // u = scale * the sum of its splits, as bf16 parts [rows][kParts][round_rank(rank)].
-__global__ void __launch_bounds__(kThreads) join_kernel(Plan p, const float* part, int splits, const float* scale,
-                                                        int rank, bf16* u) {
+struct Join {
+  const float* part;
+  int splits;
+  bf16* u;
+};
+
+__global__ void __launch_bounds__(kThreads) join_kernel(Plan p, Join first, Join second, const float* scale, int rank) {
   pdl_wait_prerequisites();
   pdl_launch_dependents();
+  const float* const part = blockIdx.y ? second.part : first.part;
+  const int splits = blockIdx.y ? second.splits : first.splits;
+  bf16* const u = blockIdx.y ? second.u : first.u;
   const int wide_rank = round_rank(rank);
   const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
   const int64_t row = i / wide_rank;
@@ -684,33 +743,15 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const Y* base, int64_t
   constexpr int kTurns = kFewRows / kFewAtOnce;
   const int64_t units = static_cast<int64_t>(n_few) * kTurns * blocks;
   for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
-    // the turns of one run's columns next to each other: the second finds F in the L2
-    const int turn = static_cast<int>(unit % kTurns);
-    const int64_t rest = unit / kTurns;
+    // second turns, of which there are few, come last: every CTA gets its share of them
+    const int64_t each = static_cast<int64_t>(n_few) * blocks, rest = unit % each;
+    const int turn = static_cast<int>(unit / each);
     Item it = p.few[rest / blocks];
     it.first += turn * kFewAtOnce;
     it.count = min(it.count - turn * kFewAtOnce, kFewAtOnce);
     if (it.count <= 0) continue;
     const int c = static_cast<int>(rest % blocks) * kFewBlock + threadIdx.x * 8;
     const bf16* const f = factor + static_cast<int64_t>(it.adapter) * rank * width;
-    Pack<Y, 8> y[kFewAtOnce];
-    Y* dst[kFewAtOnce];
-#pragma unroll
-    for (int r = 0; r < kFewAtOnce; ++r) {
-      if (r >= it.count || c >= width) continue;
-      const int64_t row = p.pos[it.first + r];
-      dst[r] = out + row * out_ld + c;
-      y[r] = Pack<Y, 8>{};
-      if (!base) continue;
-      const Y* const src = base + row * base_ld + c;
-      if (kPacks && c + 8 <= width) {
-        y[r] = *reinterpret_cast<const Pack<Y, 8>*>(src);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (c + e < width) y[r].v[e] = src[e];
-      }
-    }
     __syncthreads();     // the unit before has read its u
     for (int i = threadIdx.x; i < kFewAtOnce * wide_rank; i += kThreads) {
       const int r = i / wide_rank, k = i % wide_rank;      // 0 behind the rank
@@ -719,16 +760,37 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const Y* base, int64_t
           r < it.count ? __bfloat162float(q[0]) + (__bfloat162float(q[wide_rank]) + __bfloat162float(q[2 * wide_rank])) : 0.f;
     }
     __syncthreads();
-    if (c >= width) continue;
+    Pack<Y, 8> y[kFewAtOnce];
+    Y* dst[kFewAtOnce];
     float2 acc[kFewAtOnce][4] = {};
-    at_columns(factor_wide, c, width, [&](auto at) {
-      for (int k0 = 0; k0 < rank; k0 += kAhead) {
-        Pack<bf16, 8> q[kAhead];
+    at_columns(factor_wide && c < width, c, width, [&](auto at) {
+      Pack<bf16, 8> q[kAhead];
+      auto fetch = [&](int k0) {
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
           q[k] = Pack<bf16, 8>{};
-          if (k0 + k < rank) q[k] = load8<decltype(at)::value>(f + static_cast<int64_t>(k0 + k) * width, c, width);
+          if (k0 + k < rank && c < width) q[k] = load8<decltype(at)::value>(f + static_cast<int64_t>(k0 + k) * width, c, width);
         }
+      };
+      fetch(0);      // before all that waits for the rows' places
+#pragma unroll
+      for (int r = 0; r < kFewAtOnce; ++r) {
+        if (r >= it.count || c >= width) continue;
+        const int64_t row = p.pos[it.first + r];
+        dst[r] = out + row * out_ld + c;
+        y[r] = Pack<Y, 8>{};
+        if (!base) continue;
+        const Y* const src = base + row * base_ld + c;
+        if (kPacks && c + 8 <= width) {
+          y[r] = *reinterpret_cast<const Pack<Y, 8>*>(src);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (c + e < width) y[r].v[e] = src[e];
+        }
+      }
+      for (int k0 = 0; k0 < rank; k0 += kAhead) {
+        if (k0) fetch(k0);
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
           const float4 w = us[k0 + k];
@@ -742,6 +804,7 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const Y* base, int64_t
         }
       }
     });
+    if (c >= width) continue;
 #pragma unroll
     for (int r = 0; r < kFewAtOnce; ++r) {
       if (r >= it.count) continue;
@@ -980,15 +1043,19 @@ int splits_of(int64_t rows, int width, int& per_split) {
 int row_splits_of(int64_t rows, int width, int n) {
   const int64_t ctas = (static_cast<int64_t>(width) + kBlock - 1) / kBlock * n;
   int64_t splits = kFewCtas / ctas;
-  const int64_t most = (rows / n + 4 * kOuterRows - 1) / (4 * kOuterRows);   // four steps each at least
+  const int64_t most = rows / n / (8 * kOuterRows);   // 8 steps each: the splits cost a launch to join
   if (splits > most) splits = most;
   return splits < 1 ? 1 : static_cast<int>(splits);
 }
 
+// Runs of few rows are worth a launch of their own where adapters have few on average
+// (64 requests of 16 adapters: 55 us a pass, 94 without).
+bool use_few(int64_t rows, int n) { return rows <= int64_t{kRows} * n; }
+
 struct Space {
   Plan plan;
   bf16 *u, *du;
-  float* part;       // splits of u, or of dF
+  float* part;       // splits of u and du, or of dF
   size_t bytes;
 };
 
@@ -1017,10 +1084,10 @@ Space lay_out(void* workspace, int64_t T, int H, int V, int rank, int n) {
   s.du = reinterpret_cast<bf16*>(take(2 * kParts * wide_rank * rows));
   // a last part of fewer rows has more splits, of at most kRows (kManyCtas + items) rows in
   // all where there are fewer than kManyCtas items: below kSortMost
-  size_t most = 0;
+  size_t most = 0, narrow = 0;
   for (const int width : {H, V}) {
     int per;
-    const size_t narrow = wide_rank * rows * static_cast<size_t>(splits_of(rows > 0 ? rows : 1, width, per));
+    narrow += wide_rank * rows * static_cast<size_t>(splits_of(rows > 0 ? rows : 1, width, per));
     // row splits fill kFewCtas blocks at most, whatever the rows
     const int splits = row_splits_of(kSortMost, width, n);
     const size_t outer = splits > 1 ? static_cast<size_t>(splits) * n * rank * width : 0;
@@ -1050,30 +1117,37 @@ cudaError_t narrow_of(const X* wide, int64_t ld, const bf16* factor, int width, 
                           width, rank, p, part, per_split);
 }
 
-// u (as parts) of every row with an adapter.
+// The splits of u of every row with an adapter, at `at` of the workspace's part, which moves on.
 template <typename X>
 cudaError_t narrow(const char* name, const X* wide, int64_t ld, const void* factor, int width, const Adapters& a,
-                   const Space& z, bf16* u, cudaStream_t s) {
+                   const Space& z, float*& at, Join& join, cudaStream_t s) {
   int per_split;
   const int splits = splits_of(z.plan.rows, width, per_split);
   const bf16* const f = static_cast<const bf16*>(factor);
   const bool async = whole_chunks(wide, ld, width) && whole_chunks(f, width, width);
+  float* const part = at;
+  at += static_cast<size_t>(splits) * z.plan.rows * round_rank(a.rank);
+  join.part = part;
+  join.splits = splits;
   auto run = [&](auto nt) {
     constexpr int NT = decltype(nt)::value;
-    return async ? narrow_of<X, NT, true>(wide, ld, f, width, a.rank, z.plan, z.part, splits, per_split, s)
-                 : narrow_of<X, NT, false>(wide, ld, f, width, a.rank, z.plan, z.part, splits, per_split, s);
+    return async ? narrow_of<X, NT, true>(wide, ld, f, width, a.rank, z.plan, part, splits, per_split, s)
+                 : narrow_of<X, NT, false>(wide, ld, f, width, a.rank, z.plan, part, splits, per_split, s);
   };
-  cudaError_t e = traced_launch(name, s, [&] {
+  return traced_launch(name, s, [&] {
     if (a.rank <= 16) return run(std::integral_constant<int, 2>{});
     if (a.rank <= 32) return run(std::integral_constant<int, 4>{});
     if (a.rank <= 64) return run(std::integral_constant<int, 8>{});
     return run(std::integral_constant<int, 16>{});
   });
-  if (e != cudaSuccess) return e;
-  const int64_t n = static_cast<int64_t>(z.plan.rows) * round_rank(a.rank);
+}
+
+// u, or u and du, from their splits.
+cudaError_t join(const Join* joins, int n, const Adapters& a, const Plan& p, cudaStream_t s) {
+  const int64_t size = static_cast<int64_t>(p.rows) * round_rank(a.rank);
   return traced_launch("adapters_join", s, [&] {
-    return launch_dependent(join_kernel, dim3(static_cast<unsigned>((n + kThreads - 1) / kThreads)), kThreads, 0, 1, s,
-                            z.plan, z.part, splits, a.scale, a.rank, u);
+    return launch_dependent(join_kernel, dim3(static_cast<unsigned>((size + kThreads - 1) / kThreads), n), kThreads, 0, 1,
+                            s, p, joins[0], joins[n - 1], a.scale, a.rank);
   });
 }
 
@@ -1113,7 +1187,7 @@ cudaError_t widen(const char* name, const Y* base, int64_t base_ld, Y* out, int6
     if (rank <= 64) return run(std::integral_constant<int, 4>{});
     return run(std::integral_constant<int, 8>{});
   });
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || !p.use_few) return e;
   return traced_launch("adapters_few", s, [&] {
     auto kern = packs ? few_kernel<Y, true> : few_kernel<Y, false>;
     const int64_t runs = p.n < p.rows ? p.n : p.rows;
@@ -1167,12 +1241,18 @@ cudaError_t plan_rows(const Adapters& a, int64_t first, Space& z, cudaStream_t s
   const int64_t units = static_cast<int64_t>(a.V > a.H ? a.V : a.H) / kBlock * ((z.plan.rows + kRows - 1) / kRows);
   const int64_t run = units / (8 * kManyCtas);
   z.plan.run_rows = kRows * static_cast<int>(run < 1 ? 1 : run > kMostRun / kRows ? kMostRun / kRows : run);
-  const cudaError_t e = traced_launch("adapters_sort", s, [&] {
-    return launch_sort_ids(a.ids ? a.ids + first : nullptr, z.plan.rows, a.n, false, -1, z.plan.keys, z.plan.pos,
-                           z.plan.live, s);
+  z.plan.use_few = use_few(z.plan.rows, a.n);
+  const int32_t* const ids = a.ids ? a.ids + first : nullptr;
+  const bool small = z.plan.rows <= kSmallRows && a.n + 2 <= kSmallKeys;
+  if (!small) {
+    const cudaError_t e = traced_launch("adapters_sort", s, [&] {
+      return launch_sort_ids(ids, z.plan.rows, a.n, false, -1, z.plan.keys, z.plan.pos, z.plan.live, s);
+    });
+    if (e != cudaSuccess) return e;
+  }
+  return traced_launch("adapters_plan", s, [&] {
+    return launch_dependent(small ? plan_kernel<true> : plan_kernel<false>, dim3(1), 1024, 0, 1, s, z.plan, ids);
   });
-  if (e != cudaSuccess) return e;
-  return traced_launch("adapters_plan", s, [&] { return launch_dependent(plan_kernel, dim3(1), 1024, 0, 1, s, z.plan); });
 }
 
 }  // namespace
@@ -1193,7 +1273,10 @@ cudaError_t launch_adapters_fwd(const AdaptersFwd& f, cudaStream_t s) {
   for (int64_t first = 0; first < a.T; first += kSortMost) {
     cudaError_t e = plan_rows(a, first, z, s);
     if (e != cudaSuccess) return e;
-    e = narrow("adapters_narrow", static_cast<const bf16*>(a.x) + first * a.x_ld, a.x_ld, a.down, a.H, a, z, z.u, s);
+    float* at = z.part;
+    Join u{nullptr, 0, z.u};
+    e = narrow("adapters_narrow", static_cast<const bf16*>(a.x) + first * a.x_ld, a.x_ld, a.down, a.H, a, z, at, u, s);
+    if (e == cudaSuccess) e = join(&u, 1, a, z.plan, s);
     if (e != cudaSuccess) return e;
     e = by_type(f.type, [&](auto t) {
       using Y = decltype(t);
@@ -1213,15 +1296,23 @@ cudaError_t launch_adapters_bwd(const AdaptersBwd& b, cudaStream_t s) {
     const bf16* const x = static_cast<const bf16*>(a.x) + first * a.x_ld;
     cudaError_t e = plan_rows(a, first, z, s);
     if (e != cudaSuccess) return e;
+    float* at = z.part;
+    Join joins[2];
+    int n = 0;
     if (b.d_up) {
-      e = narrow("adapters_narrow", x, a.x_ld, a.down, a.H, a, z, z.u, s);
+      joins[n] = Join{nullptr, 0, z.u};
+      e = narrow("adapters_narrow", x, a.x_ld, a.down, a.H, a, z, at, joins[n++], s);
       if (e != cudaSuccess) return e;
     }
     e = by_type(b.type, [&](auto t) {
       using G = decltype(t);
       const G* const g = static_cast<const G*>(b.grad) + first * b.grad_ld;
       cudaError_t r = cudaSuccess;
-      if (b.dx || b.d_down) r = narrow("adapters_narrow_grad", g, b.grad_ld, a.up, a.V, a, z, z.du, s);
+      if (b.dx || b.d_down) {
+        joins[n] = Join{nullptr, 0, z.du};
+        r = narrow("adapters_narrow_grad", g, b.grad_ld, a.up, a.V, a, z, at, joins[n++], s);
+      }
+      if (r == cudaSuccess) r = join(joins, n, a, z.plan, s);
       if (r == cudaSuccess && b.d_up)
         r = outer("adapters_d_up", g, b.grad_ld, a.V, a.rank, z.u, z, b.d_up, accumulate, s);
       return r;
