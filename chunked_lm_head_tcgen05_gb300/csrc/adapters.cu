@@ -827,7 +827,7 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const Y* base, int64_t
 // step ahead.  A warp has 32 columns of the block.
 template <typename X, int RT>
 struct OuterShape {
-  static constexpr int kStages = sizeof(X) == 4 ? 3 : 4;
+  static constexpr int kStages = 3;
   static constexpr int fs = kBlock + (sizeof(X) == 4 ? 4 : kPad), us = 16 * RT + kPad;
   static constexpr size_t x_bytes = sizeof(X) * kOuterRows * fs;
   static constexpr size_t stage = x_bytes + 2 * size_t{kParts} * kOuterRows * us;
@@ -835,7 +835,7 @@ struct OuterShape {
 };
 
 template <typename X, int RT, bool kAsync>
-__global__ void __launch_bounds__(kThreads) outer_kernel(const X* wide, int64_t ld, int width, int rank, const bf16* u,
+__global__ void __launch_bounds__(kThreads, kAsync && sizeof(X) == 2 && RT <= 2 ? 3 : 1) outer_kernel(const X* wide, int64_t ld, int width, int rank, const bf16* u,
                                                          Plan p, float* grad, int accumulate, int row_splits,
                                                          int64_t split_size) {
   using S = OuterShape<X, RT>;
@@ -1029,12 +1029,14 @@ auto by_type(int type, F&& f) {
 
 int64_t most_items(int64_t rows, int n) { return rows / kRows + (n + 1 < rows ? n + 1 : rows) + 1; }
 
-// Splits of the wide side: CTAs enough for the GPU, at least 512 columns each.
-int splits_of(int64_t rows, int width, int& per_split) {
-  const int64_t items = (rows + kRows - 1) / kRows;
-  int64_t splits = (kManyCtas + items - 1) / items;
+// Splits of the wide side: one wave of two CTAs per SM (at 2,048 x 151,936 bf16 and rank 32
+// 2.4 waves took 155 us, one takes 130), at least 512 columns each.  Adapters' last items are part full.
+int splits_of(int64_t rows, int width, int n, int& per_split) {
+  const int64_t items = (rows + kRows - 1) / kRows, partial = (n + 1) / 2;
+  int64_t splits = kFewCtas / (items + (partial < items ? partial : items));
   const int64_t most = (width + 511) / 512;
   if (splits > most) splits = most;
+  if (splits < 1) splits = 1;
   per_split = static_cast<int>(((width + splits - 1) / splits + kTile - 1) / kTile * kTile);
   return (width - 1) / per_split + 1;
 }
@@ -1082,12 +1084,11 @@ Space lay_out(void* workspace, int64_t T, int H, int V, int rank, int n) {
   const size_t wide_rank = static_cast<size_t>(round_rank(rank));
   s.u = reinterpret_cast<bf16*>(take(2 * kParts * wide_rank * rows));
   s.du = reinterpret_cast<bf16*>(take(2 * kParts * wide_rank * rows));
-  // a last part of fewer rows has more splits, of at most kRows (kManyCtas + items) rows in
-  // all where there are fewer than kManyCtas items: below kSortMost
+  // (a last part of fewer rows has more splits: those of at most kRows kFewCtas rows in all)
   size_t most = 0, narrow = 0;
   for (const int width : {H, V}) {
     int per;
-    narrow += wide_rank * rows * static_cast<size_t>(splits_of(rows > 0 ? rows : 1, width, per));
+    narrow += wide_rank * rows * static_cast<size_t>(splits_of(rows > 0 ? rows : 1, width, n, per));
     // row splits fill kFewCtas blocks at most, whatever the rows
     const int splits = row_splits_of(kSortMost, width, n);
     const size_t outer = splits > 1 ? static_cast<size_t>(splits) * n * rank * width : 0;
@@ -1122,7 +1123,7 @@ template <typename X>
 cudaError_t narrow(const char* name, const X* wide, int64_t ld, const void* factor, int width, const Adapters& a,
                    const Space& z, float*& at, Join& join, cudaStream_t s) {
   int per_split;
-  const int splits = splits_of(z.plan.rows, width, per_split);
+  const int splits = splits_of(z.plan.rows, width, a.n, per_split);
   const bf16* const f = static_cast<const bf16*>(factor);
   const bool async = whole_chunks(wide, ld, width) && whole_chunks(f, width, width);
   float* const part = at;
@@ -1237,9 +1238,9 @@ cudaError_t outer(const char* name, const X* wide, int64_t ld, int width, int ra
 cudaError_t plan_rows(const Adapters& a, int64_t first, Space& z, cudaStream_t s) {
   z.plan.rows = static_cast<int>(a.T - first < kSortMost ? a.T - first : kSortMost);
   z.plan.most = static_cast<int>(most_items(z.plan.rows, a.n));
-  // runs as long as keeps some eight units per CTA of the widest product
+  // runs as long as keeps some units per CTA of the widest product
   const int64_t units = static_cast<int64_t>(a.V > a.H ? a.V : a.H) / kBlock * ((z.plan.rows + kRows - 1) / kRows);
-  const int64_t run = units / (8 * kManyCtas);
+  const int64_t run = units / (7 * kManyCtas);
   z.plan.run_rows = kRows * static_cast<int>(run < 1 ? 1 : run > kMostRun / kRows ? kMostRun / kRows : run);
   z.plan.use_few = use_few(z.plan.rows, a.n);
   const int32_t* const ids = a.ids ? a.ids + first : nullptr;
