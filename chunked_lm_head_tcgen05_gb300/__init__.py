@@ -789,6 +789,11 @@ def _check_ids(ids):
     return ids.shape[0]
 
 
+def _check_padding(padding_id, V):
+    if padding_id is not None and not -V <= padding_id < V:
+        raise ValueError("padding_id %d is no id of a vocabulary of %d" % (padding_id, V))
+
+
 def _embedding_types(dtype):
     """What a table of this type can give."""
     f32, bf16 = _torch.float32, _torch.bfloat16
@@ -816,6 +821,7 @@ def lmhead_embedding_bwd(dy, ids, scale, padding_id, d_weight, accumulate, works
     narrow = d_weight.dtype is torch.bfloat16
     _check_tensor(d_weight, "d_weight", torch.bfloat16 if narrow else torch.float32, (V, H))
     _check_workspace(workspace)
+    _check_padding(padding_id, V)
     dev = _one_device(dy, ids, d_weight, workspace)
     return _call(library().lmhead_embedding_bwd, dev, stream, dy.data_ptr(), kind, ld,
                  ids.data_ptr(), N, V, H, scale, NO_PADDING if padding_id is None else padding_id,
@@ -886,6 +892,8 @@ def lmhead_beam_select(logits, beams, take, scores, finished, eos_id, temperatur
     if beams <= 0 or R % beams:
         raise ValueError("logits must have the rows of whole groups of beams: got %d rows of %d "
                          "beams" % (R, beams))
+    if not -1 <= eos_id < V:
+        raise ValueError("eos_id %d is no id of a vocabulary of %d" % (eos_id, V))
     shape = (R // beams, take)
     _check_tensor(out_scores, "out_scores", torch.float32, shape)
     _check_tensor(parents, "parents", torch.int32, shape)
@@ -954,6 +962,8 @@ def lmhead_beam_reorder(state, out, parents, dim, beams=0, clear_missing=False, 
         raise TypeError("out must be %s, got %s" % (state.dtype, out.dtype))
     if out.shape != shape:
         raise ValueError("out has shape %s, expected %s" % (tuple(out.shape), tuple(shape)))
+    if not 0 <= beams < 2 ** 31:
+        raise ValueError("beams must be the rows of a group, got %d" % beams)
     dev = _one_device(state, out, parents)
     if out.numel() == 0:
         return 0

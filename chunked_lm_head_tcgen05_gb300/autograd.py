@@ -31,6 +31,7 @@ from . import LMHEAD_OP_BWD, LMHEAD_OP_FWD, LmheadError, adapters_forward, \
     lmhead_embedding_workspace_size, \
     lmhead_layernorm_workspace_size, \
     lmhead_logps_bwd, lmhead_logps_fwd, lmhead_workspace_size, process_logits_backward
+from . import _check_padding
 from . import process_logits as _process_logits
 
 # (device index, stream handle) -> uint8 workspace, grown on demand.  Work on one
@@ -400,6 +401,7 @@ _SORT_MOST = 131072   # tokens whose gradient can be written in bf16 (lmhead_emb
 def embedding(ids, weight, scale=1.0, padding_id=None, out_dtype=None, main_grad=None):
     """scale * weight[ids], differentiable in the table; tokens with padding_id give no gradient.
     main_grad as in ``lmhead_logps``: a table tied to the head gets both gradients in it."""
+    _check_padding(padding_id, weight.shape[0])
     return Embedding.apply(ids, weight, float(scale), padding_id, out_dtype,
                            _main_grad(weight, main_grad))
 

@@ -404,11 +404,22 @@ __global__ void __launch_bounds__(kBestThreads) best_kernel(BeamSelect a, Pieces
     return f;
   };
   auto each = [&](auto&& f) {
-    for (int i = tid; i < total; i += kBestThreads) {
-      const int j = i / per_beam;
-      if (kind[j] != kLive) continue;
-      const uint64_t e = z.best[(r0 + j) * per_beam + (i - j * per_beam)];
-      if (e) f(j, static_cast<uint32_t>(e >> 32), static_cast<int>(~static_cast<uint32_t>(e)));
+    constexpr int kAhead = 8;        // entries in flight per thread
+    const uint64_t* const entries = z.best + r0 * per_beam;
+    for (int i0 = tid; i0 < total; i0 += kAhead * kBestThreads) {
+      uint64_t e[kAhead];
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q) {
+        const int i = i0 + q * kBestThreads;
+        e[q] = i < total ? entries[i] : 0;
+      }
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q) {
+        if (e[q] == 0) continue;
+        const int j = (i0 + q * kBestThreads) / per_beam;
+        // an ended beam's entries were not written
+        if (kind[j] == kLive) f(j, static_cast<uint32_t>(e[q] >> 32), static_cast<int>(~static_cast<uint32_t>(e[q])));
+      }
     }
   };
   auto exact = [&](int j, uint32_t order, int v) {
@@ -428,7 +439,9 @@ __global__ void __launch_bounds__(kBestThreads) best_kernel(BeamSelect a, Pieces
 #pragma unroll 1
   for (int bit = 31; bit >= 0; --bit) {
     const uint32_t more = at_least | 1u << bit;
-    if (__syncthreads_count(key >= more) >= a.take) at_least = more;
+    const int n = __syncthreads_count(key >= more);
+    if (n >= a.take) at_least = more;
+    if (n == a.take) break;          // no tighter than this
   }
   low = at_least ? from_order(at_least) : -INFINITY;
   each([&](int j, uint32_t order, int v) {

@@ -121,6 +121,12 @@ lmhead_status check_adapter_operands(const Adapters& a, size_t workspace_bytes) 
 
 constexpr int32_t kMaxBeamVocab = 1 << 30;   // columns of the pieces past a row's end are counted too
 
+// Whether n bytes at p and m bytes at q share any; NULL shares none.
+bool overlap(const void* p, size_t n, const void* q, size_t m) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return p && q && a < b + m && b < a + n;
+}
+
 // A strided block of bytes: up to three dimensions of `inner` contiguous bytes.
 struct Block {
   int64_t size[3], stride[3], inner;
@@ -444,6 +450,12 @@ lmhead_status lmhead_beam_select(const void* logits, int type, int64_t ld, int64
                         static_cast<const void*>(lse)})
     if (!aligned_to(p, kF32)) return LMHEAD_ERR_UNSUPPORTED;
   if (!aligned_to(logits, type) || (reinterpret_cast<uintptr_t>(workspace) & 255)) return LMHEAD_ERR_UNSUPPORTED;
+  // one group's results may lie over its own inputs, which it has read by then, not over another's
+  const size_t rows = static_cast<size_t>(R), results = rows / beams * take;
+  const bool own = take == beams;
+  if ((overlap(scores, 4 * rows, out_scores, 4 * results) && !(own && scores == out_scores)) ||
+      (overlap(finished, rows, next_finished, results) && !(own && finished == next_finished)))
+    return LMHEAD_ERR_INVALID_ARG;
   if (workspace_bytes < beam_workspace(R, V, take)) return LMHEAD_ERR_WORKSPACE_TOO_SMALL;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const BeamSelect a{logits, type, ld, R, V, beams, take, scores, finished, eos_id, temperature,

@@ -6,7 +6,7 @@ import chunked_lm_head_tcgen05_gb300 as lm
 from test_operators_host import INVALID, OK, P, SMALL, UNSUPPORTED, call, lib  # noqa: F401
 
 SELECT = dict(logits=P(), type=0, ld=100, R=8, V=100, beams=4, take=8, scores=P(), finished=P(), eos=2,
-              tau=1.0, out=P(), parents=P(), tokens=P(), next=P(), lse=P(), workspace=P(),
+              tau=1.0, out=P(1 << 22), parents=P(), tokens=P(), next=P(1 << 23), lse=P(), workspace=P(),
               bytes=1 << 30, stream=None)
 A, B = 1 << 20, 1 << 24
 REORDER = dict(src=P(A), so=8 * 640, sr=640, sm=320, src_rows=8, dst=P(B), do=8 * 640, dr=640, dm=320,
@@ -25,6 +25,9 @@ CASES = [
         (dict(R=(1 << 31) - 256), UNSUPPORTED), (dict(V=(1 << 30) + 1, ld=1 << 31), UNSUPPORTED),
         (dict(logits=P((1 << 20) + 2)), UNSUPPORTED), (dict(workspace=P((1 << 20) + 16)), UNSUPPORTED),
         (dict(scores=P((1 << 20) + 2)), UNSUPPORTED), (dict(lse=P((1 << 20) + 1)), UNSUPPORTED),
+        (dict(out=P()), INVALID), (dict(out=P((1 << 20) + 28)), INVALID), (dict(next=P()), INVALID),
+        (dict(out=P(), take=4, next=P((1 << 20) + 7)), INVALID),
+        (dict(out=P(), next=P(), take=4, bytes=128), SMALL),
         (dict(bytes=128), SMALL), (dict(R=0, logits=None), OK)]),
     ("lmhead_beam_reorder", REORDER, [
         (dict(src=None), INVALID), (dict(dst=None), INVALID), (dict(parents=None), INVALID),
@@ -87,5 +90,7 @@ def test_binding():
         lm.beam_select(z, s, 0)
     with pytest.raises(ValueError):
         lm.beam_select(z, s, 4, 0)
+    with pytest.raises(ValueError):
+        lm.beam_select(z, s, 4, eos_id=2 ** 32 + 2)
     with pytest.raises(ValueError):
         lm.beam_reorder(z, torch.zeros(8, dtype=torch.int32))

@@ -68,3 +68,6 @@ def test_binding():
                               workspace=torch.zeros(256, dtype=torch.uint8))
     with pytest.raises(ValueError):
         autograd.embedding(ids, w, main_grad=torch.zeros(9, 8))
+    for padding in (10, -11, 2 ** 32 + 3):
+        with pytest.raises(ValueError):
+            autograd.embedding(ids, w, padding_id=padding)

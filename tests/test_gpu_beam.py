@@ -225,6 +225,21 @@ def test_select_writes_stay_inside(R, K, V, N, dtype):
     _check(gin, out, "select")
 
 
+def test_select_into_its_own_inputs():
+    """A loop that keeps its scores and flags in one place."""
+    gen = torch.Generator("cuda").manual_seed(21)
+    z = logits_of(512, 3000, F32, gen)
+    s = -torch.rand(512, generator=gen, device="cuda")
+    f = (torch.rand(512, generator=gen, device="cuda") < 0.3).to(torch.uint8)
+    nxt = torch.empty(128, 4, dtype=torch.uint8, device="cuda")
+    want = lm.beam_select(z, s, 4, 4, 1.0, f, 5, nxt)
+    ws = torch.empty(lm.lmhead_beam_workspace_size(512, 3000, 4), dtype=torch.uint8, device="cuda")
+    p, t = torch.empty_like(want[1]), torch.empty_like(want[2])
+    assert lm.lmhead_beam_select(z, 4, 4, s, f, 5, 1.0, s.view(128, 4), p, t, f.view(128, 4), None, ws) == 0
+    assert torch.equal(s.view(128, 4), want[0]) and torch.equal(p, want[1]) and torch.equal(t, want[2])
+    assert torch.equal(f.view(128, 4), nxt)
+
+
 def test_select_past_32_bits():
     z = torch.zeros(17000, 151936, dtype=BF16, device="cuda")      # 2.58e9 elements
     z[-1, -1] = 5.0
