@@ -173,11 +173,11 @@ __device__ __forceinline__ float largest(const Pack<T, VEC> (&q)[PACKS]) {
 }
 
 template <typename T, int ELEMS>
-__global__ void __launch_bounds__(kThreads, 4) scan_kernel(BeamSelect a, Pieces z, int span) {
+__global__ void __launch_bounds__(kThreads, 4) scan_kernel(BeamSelect a, Pieces z, int groups) {
   constexpr int VEC = kVec<T>, PACKS = ELEMS / VEC, kStages = kStagesOf<ELEMS>;
   extern __shared__ __align__(16) char ring_memory[];
   __shared__ uint64_t found[kRoom];
-  __shared__ uint32_t warp_min[kWarps];
+  __shared__ uint32_t group_max[kMaxTake];
   __shared__ float2 warp_sums[kWarps];
   __shared__ int scratch[kWarps], n_found;
   pdl_wait_prerequisites();
@@ -187,6 +187,8 @@ __global__ void __launch_bounds__(kThreads, 4) scan_kernel(BeamSelect a, Pieces 
   if (a.finished && a.finished[r]) return;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) n_found = 0;
+  if (tid < kMaxTake) group_max[tid] = 0;
+  __syncthreads();
   // packs are counted from the 16-byte boundary at or before the row's start
   const T* const row = static_cast<const T*>(a.logits) + r * a.ld;
   const int skip = static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
@@ -238,14 +240,15 @@ __global__ void __launch_bounds__(kThreads, 4) scan_kernel(BeamSelect a, Pieces 
     copy_async_commit();
     const float top = largest<T, PACKS, VEC>(q);
     if (from == p0) {
-      // the least of the largest elements of kThreads / span groups of threads
+      // the least of the largest elements of `groups` groups of threads: those with the same
+      // number modulo that, so that a short tile leaves none empty
       uint32_t least = order_of(top);
-      for (int o = 1; o < span; o <<= 1) least = max(least, __shfl_xor_sync(0xffffffffu, least, o));
-      least = __reduce_min_sync(0xffffffffu, least);
-      if (lane == 0) warp_min[warp] = least;
+      for (int o = 16; o >= groups; o >>= 1) least = max(least, __shfl_xor_sync(0xffffffffu, least, o));
+      if (lane < groups) atomicMax(&group_max[tid & (groups - 1)], least);
       __syncthreads();
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) least = min(least, warp_min[w]);
+      least = ~0u;
+      for (int g = lane; g < groups; g += 32) least = min(least, group_max[g]);
+      least = __reduce_min_sync(0xffffffffu, least);
       low = max(least - 1, kMinusInf);
       low -= low == kMinusZero;      // not below zero, as a number
     }
@@ -541,6 +544,11 @@ __global__ void __launch_bounds__(kMoveThreads) gather_kernel(BeamReorder a, Til
   U* const dst = reinterpret_cast<U*>(a.dst + o * a.dst_outer + r * a.dst_row + m * a.dst_mid);
   const int64_t n = a.inner / static_cast<int64_t>(sizeof(U));
   const int64_t i0 = part * t.across * kMoveUnroll + x;
+  const int tail = static_cast<int>(a.inner % static_cast<int64_t>(sizeof(U)));   // bytes behind the last unit
+  if (tail && i0 == 0) {
+    for (int e = 0; e < tail; ++e)
+      reinterpret_cast<char*>(dst + n)[e] = none ? 0 : reinterpret_cast<const char*>(src + n)[e];
+  }
   U q[kMoveUnroll] = {};
 #pragma unroll
   for (int u = 0; u < kMoveUnroll; ++u)
@@ -579,8 +587,22 @@ __global__ void __launch_bounds__(kMoveThreads) in_place_kernel(BeamReorder a, T
   const int x = threadIdx.x % t.across, y = threadIdx.x / t.across;
   const int64_t m = mids * (kMoveThreads / t.across) + y;
   const int64_t n = a.inner / static_cast<int64_t>(sizeof(U)), i = part * t.across + x;
-  if (m >= a.mid || i >= n) return;
-  char* const base = a.dst + o * a.dst_outer + r0 * a.dst_row + m * a.dst_mid + i * static_cast<int64_t>(sizeof(U));
+  if (m >= a.mid) return;
+  char* const row = a.dst + o * a.dst_outer + r0 * a.dst_row + m * a.dst_mid;
+  const int64_t tail = a.inner - n * static_cast<int64_t>(sizeof(U));
+  if (tail && i == 0) {      // bytes behind the last unit, one after the other
+    for (char* at = row + a.inner - tail; at < row + a.inner; ++at) {
+      char c[BEAMS];
+#pragma unroll
+      for (int j = 0; j < BEAMS; ++j)
+        if (from[j] >= 0) c[j] = at[from[j] * a.dst_row];
+#pragma unroll
+      for (int j = 0; j < BEAMS; ++j)
+        if (from[j] >= 0) at[j * a.dst_row] = c[j];
+    }
+  }
+  if (i >= n) return;
+  char* const base = row + i * static_cast<int64_t>(sizeof(U));
   U q[BEAMS];
 #pragma unroll
   for (int j = 0; j < BEAMS; ++j)
@@ -590,14 +612,14 @@ __global__ void __launch_bounds__(kMoveThreads) in_place_kernel(BeamReorder a, T
     if (from[j] >= 0) *reinterpret_cast<U*>(base + j * a.dst_row) = q[j];
 }
 
-// The widest unit in bytes that every address is a multiple of; 17 to 64 rows in
-// registers take units of 4 bytes at most.
+// The widest unit in bytes that every row's address is a multiple of (its length need not be);
+// 17 to 64 rows in registers take units of 4 bytes at most.
 int unit_of(const BeamReorder& a) {
   const uint64_t bits = reinterpret_cast<uintptr_t>(a.src) | reinterpret_cast<uintptr_t>(a.dst) |
-                        static_cast<uint64_t>(a.inner | a.src_outer | a.dst_outer | a.src_row | a.dst_row |
-                                              a.src_mid | a.dst_mid);
+                        static_cast<uint64_t>(a.src_outer | a.dst_outer | a.src_row | a.dst_row | a.src_mid |
+                                              a.dst_mid);
   int unit = a.src == a.dst && a.beams > 16 ? 4 : 16;
-  while (bits & static_cast<uint64_t>(unit - 1)) unit /= 2;
+  while ((bits & static_cast<uint64_t>(unit - 1)) || unit > a.inner) unit /= 2;
   return unit;
 }
 
@@ -685,21 +707,20 @@ cudaError_t launch_beam_select(const BeamSelect& a, cudaStream_t s) {
   const size_t slots = static_cast<size_t>(a.R) * z.pieces;      // below 2^31: see plan
   z.stats = static_cast<float2*>(a.workspace);
   z.best = reinterpret_cast<uint64_t*>(static_cast<char*>(a.workspace) + round_up(slots * sizeof(float2)));
-  // groups of threads, at least `take` of them (whole warps at most)
-  int groups = kWarps;
+  int groups = 8;      // of threads, a power of two and at least `take` of them
   while (groups < a.take) groups *= 2;
   cudaError_t e = traced_launch("beam_select_scan", s, [&] {
     return by_type(a.type, [&](auto t) {
       using T = decltype(t);
       if (elements == kFewElements)
         return launch_dependent(scan_kernel<T, kFewElements>, dim3(static_cast<unsigned>(slots)), kThreads,
-                                kRingBytes<T, kFewElements>, 1, s, a, z, kThreads / groups);
+                                kRingBytes<T, kFewElements>, 1, s, a, z, groups);
       static std::atomic<int> ready[64];
       constexpr size_t ring = kRingBytes<T, kManyElements<T>>;
       const cudaError_t r = allow_shared(ready, reinterpret_cast<const void*>(scan_kernel<T, kManyElements<T>>), ring);
       if (r != cudaSuccess) return r;
       return launch_dependent(scan_kernel<T, kManyElements<T>>, dim3(static_cast<unsigned>(slots)), kThreads, ring, 1, s, a,
-                              z, kThreads / groups);
+                              z, groups);
     });
   });
   if (e != cudaSuccess) return e;

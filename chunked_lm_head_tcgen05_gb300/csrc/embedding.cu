@@ -107,6 +107,39 @@ __global__ void __launch_bounds__(kFwdThreads) embed_kernel(EmbedFwd a, int part
   }
 }
 
+// Rows of whole 16-byte packs on both sides: the packs of all rows as one list, a thread every
+// kFwdThreads-th of a CTA's UNROLL * kFwdThreads, so that short rows fill it too.
+template <typename W, typename Y, int UNROLL>
+__global__ void __launch_bounds__(kFwdThreads) embed_packs_kernel(EmbedFwd a, unsigned packs) {
+  pdl_wait_prerequisites();
+  pdl_launch_dependents();
+  constexpr int VEC = kVec<W>;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * UNROLL * kFwdThreads;
+  const int64_t t0 = first / packs;
+  const unsigned p0 = static_cast<unsigned>(first - t0 * packs) + threadIdx.x;
+  Pack<W, VEC> q[UNROLL];
+  Y* dst[UNROLL];
+#pragma unroll
+  for (int u = 0; u < UNROLL; ++u) {
+    const unsigned f = p0 + u * kFwdThreads, down = f / packs, p = f - down * packs;
+    const int64_t t = t0 + down;
+    dst[u] = nullptr;
+    if (t >= a.N) continue;
+    int id = a.ids[t];
+    if (id < 0) id += a.V;
+    dst[u] = static_cast<Y*>(a.y) + t * a.y_ld + p * VEC;
+    if (id >= 0 && id < a.V) {
+      q[u] = *reinterpret_cast<const Pack<W, VEC>*>(static_cast<const W*>(a.weight) + id * a.w_ld + p * VEC);
+    } else {      // an id that the table does not have
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) q[u].v[e] = from_f32<W>(NAN);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < UNROLL; ++u)
+    if (dst[u]) *reinterpret_cast<Pack<Y, VEC>*>(dst[u]) = scaled<W, Y>(q[u], a.scale);
+}
+
 // ------------------------------------------------------------------ backward
 struct Sorted {
   int* live;
@@ -371,6 +404,14 @@ cudaError_t launch_embed_fwd(const EmbedFwd& a, cudaStream_t s) {
     using Y = decltype(y);
     constexpr int VEC = kVec<W>;
     const int packs = (a.H + VEC - 1) / VEC;
+    if (whole_packs(a.weight, a.w_ld, a.H, sizeof(W), VEC) && whole_packs(a.y, a.y_ld, a.H, sizeof(Y), VEC)) {
+      const int64_t all = a.N * packs;
+      const bool few = all < int64_t{304} * kFwdThreads * kFwdUnroll;
+      const int64_t each = kFwdThreads * (few ? 1 : kFwdUnroll), ctas = (all + each - 1) / each;
+      if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
+      auto kern = few ? embed_packs_kernel<W, Y, 1> : embed_packs_kernel<W, Y, kFwdUnroll>;
+      return launch_dependent(kern, dim3(static_cast<unsigned>(ctas)), kFwdThreads, 0, 1, s, a, static_cast<unsigned>(packs));
+    }
     const int parts = (packs + 32 * kFwdUnroll - 1) / (32 * kFwdUnroll);
     const int span = ((packs + parts - 1) / parts + 31) / 32 * 32;
     const int64_t grid = (a.N * parts + kFwdThreads / 32 - 1) / (kFwdThreads / 32);
@@ -402,7 +443,10 @@ cudaError_t launch_embed_bwd(const EmbedBwd& call, cudaStream_t s) {
     const size_t row = (a.d_type == kF32 ? 4 : 2) * static_cast<size_t>(a.H);
     const bool beside = !a.accumulate && reinterpret_cast<uintptr_t>(a.d_weight) % 16 == 0;
     size_t rows = beside ? sort_time_bytes(n) / row / kFillRows * kFillRows : 0;
+    // few tokens: everything, since hardly a row is written twice
+    if (beside && n <= a.V / 32) rows = a.V;
     if (rows > static_cast<size_t>(a.V)) rows = a.V / kFillRows * kFillRows;
+    if (rows * row % 16) rows = rows / kFillRows * kFillRows;
     z.filled = static_cast<int>(rows);
     cudaError_t e = traced_launch("embedding_bwd_sort", s, [&] {
       return launch_sort_ids(a.ids + first, n, a.V, true, a.skip, z.keys, z.pos, z.live, s, a.d_weight, rows * row);

@@ -46,8 +46,8 @@ __global__ void __launch_bounds__(kThreads) sort_kernel(SortArgs a) {
   extern __shared__ __align__(16) char smem[];
   uint64_t* const buf = reinterpret_cast<uint64_t*>(smem);                     // [kThreads * ITEMS]
   uint16_t* const cnt = reinterpret_cast<uint16_t*>(buf + kThreads * ITEMS);   // [kWarps][digits]
-  int* const tot = reinterpret_cast<int*>(cnt + kWarps * kMaxDigits);          // [digits]
-  int* const base = tot + kMaxDigits;                                          // [digits]
+  int* const tot = reinterpret_cast<int*>(cnt + kWarps * kMaxDigits);          // [kCluster][digits]
+  int* const base = tot + kCluster * kMaxDigits;                               // [digits]
   int* const part = base + kMaxDigits;                                         // [kWarps]
   int* const mine = part + kWarps;                                             // ids inside, this CTA
   constexpr int P = kThreads * ITEMS;
@@ -105,22 +105,26 @@ __global__ void __launch_bounds__(kThreads) sort_kernel(SortArgs a) {
     }
     __syncthreads();
     if (tid < digits) {
+      int c[kWarps];
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) c[w] = cnt[w * digits + tid];
       int sum = 0;
-#pragma unroll 8
+#pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const int c = cnt[w * digits + tid];
         cnt[w * digits + tid] = static_cast<uint16_t>(sum);
-        sum += c;
+        sum += c[w];
       }
-      tot[tid] = sum;
+      // to every CTA: a store does not wait, a load from each of eight CTAs would
+      const uint32_t at = smem_addr(tot + rank * kMaxDigits + tid);
+      for (int c = 0; c < ctas; ++c)
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_to_cta(at, c)), "r"(sum) : "memory");
     }
     cluster_sync();   // every CTA's totals, and every pair is in its thread's registers
     int before = 0, all = 0;
     if (tid < digits) {
-      const uint32_t at = smem_addr(tot + tid);
-      for (int c = 0; c < ctas; ++c) {
-        int v;
-        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(map_to_cta(at, c)) : "memory");
+#pragma unroll
+      for (int c = 0; c < kCluster; ++c) {
+        const int v = c < ctas ? tot[c * kMaxDigits + tid] : 0;
         before += c < rank ? v : 0;
         all += v;
       }
@@ -172,7 +176,7 @@ __global__ void __launch_bounds__(kThreads) sort_kernel(SortArgs a) {
 template <int ITEMS>
 cudaError_t launch(const SortArgs& a, int grid, cudaStream_t s) {
   static std::atomic<int> ready[64];
-  constexpr size_t smem = size_t{8} * kThreads * ITEMS + 2 * kWarps * kMaxDigits + 4 * (2 * kMaxDigits + kWarps + 1);
+  constexpr size_t smem = size_t{8} * kThreads * ITEMS + 2 * kWarps * kMaxDigits + 4 * ((kCluster + 1) * kMaxDigits + kWarps + 1);
   const cudaError_t e = allow_shared(ready, reinterpret_cast<const void*>(sort_kernel<ITEMS>), smem);
   if (e != cudaSuccess) return e;
   return launch_dependent(sort_kernel<ITEMS>, dim3(grid), kThreads, smem, a.ctas, s, a);
