@@ -19,9 +19,9 @@
 // Order among one row's logits is by the logit itself, as an integer that grows
 // with it, then by the id.
 //
-// beam_reorder moves states to the beams that go on: row r takes over row
-// parents[r].  In place a thread holds one column of a group's rows, reads what
-// other rows need and then writes, so rows that keep their place cost nothing.
+// beam_reorder moves states to the beams that go on: row r takes over row parents[r].  In
+// place a thread (or, for rows off 16-byte boundaries, a CTA) holds one stretch of a group's
+// rows, reads what other rows need and then writes; rows that keep their place cost nothing.
 #include <type_traits>
 
 #include "element.cuh"
@@ -151,24 +151,21 @@ __device__ __noinline__ void add_best_of_tile(uint64_t* found, int* n_found, int
   __syncthreads();
 }
 
-// The largest of a thread's elements; NaN is passed over.
-template <typename T, int PACKS, int VEC>
-__device__ __forceinline__ float largest(const Pack<T, VEC> (&q)[PACKS]) {
+// The largest of a pack; NaN is passed over.
+template <typename T, int VEC>
+__device__ __forceinline__ float largest(const Pack<T, VEC>& q) {
   if constexpr (sizeof(T) == 4) {
     float top = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < PACKS; ++i)
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) top = fmaxf(top, q[i].v[e]);
+    for (int e = 0; e < VEC; ++e) top = fmaxf(top, q.v[e]);
     return top;
   } else {
     using T2 = std::conditional_t<std::is_same_v<T, __half>, __half2, __nv_bfloat162>;
-    const T2* const v = reinterpret_cast<const T2*>(&q[0]);
+    const T2* const v = reinterpret_cast<const T2*>(&q);
     T2 top = v[0];
 #pragma unroll
-    for (int e = 1; e < PACKS * VEC / 2; ++e) top = __hmax2(top, v[e]);
-    const float lo = to_f32(top.x), hi = to_f32(top.y);
-    return fmaxf(fmaxf(lo, hi), -INFINITY);       // of NaN alone: -inf
+    for (int e = 1; e < VEC / 2; ++e) top = __hmax2(top, v[e]);
+    return fmaxf(fmaxf(to_f32(top.x), to_f32(top.y)), -INFINITY);       // of NaN alone: -inf
   }
 }
 
@@ -238,7 +235,12 @@ __global__ void __launch_bounds__(kThreads, 4) scan_kernel(BeamSelect a, Pieces 
     const int ahead = from + (kStages - 1) * kTile;
     if (ahead < p1) fetch(ahead, stage == 0 ? kStages - 1 : stage - 1);
     copy_async_commit();
-    const float top = largest<T, PACKS, VEC>(q);
+    float tops[PACKS], top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < PACKS; ++i) {
+      tops[i] = largest(q[i]);
+      top = fmaxf(top, tops[i]);
+    }
     if (from == p0) {
       // the least of the largest elements of `groups` groups of threads: those with the same
       // number modulo that, so that a short tile leaves none empty
@@ -269,6 +271,7 @@ __global__ void __launch_bounds__(kThreads, 4) scan_kernel(BeamSelect a, Pieces 
     if (top > above) {
 #pragma unroll
       for (int i = 0; i < PACKS; ++i) {
+        if (!(tops[i] > above)) continue;
         const int v = (from + i * kThreads + tid) * VEC - skip;
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
@@ -516,143 +519,190 @@ __global__ void __launch_bounds__(kBestThreads) best_kernel(BeamSelect a, Pieces
 // ------------------------------------------------------------------ states
 constexpr int kMoveThreads = 256;
 constexpr int kMoveUnroll = 4;
+constexpr int kMoveShared = 32768;    // bytes of a group's rows that a CTA of across_in_place_kernel holds
 
 // Threads along the contiguous bytes (a power of two) and along `mid`.
 struct Tile {
   int across;           // threads along inner
   int64_t parts;        // CTAs along inner
   int64_t mids;         // CTAs along mid
+  int bytes;            // of a row per CTA (across_in_place_kernel)
 };
 
-template <typename U>
+// What a CTA moves.
+struct Place {
+  int64_t part, m, r, o;
+};
+__device__ __forceinline__ Place place_of(const Tile& t, int64_t rows, int& x) {
+  int64_t b = blockIdx.x;
+  Place p;
+  p.part = b % t.parts;
+  b /= t.parts;
+  const int64_t mids = b % t.mids;
+  b /= t.mids;
+  p.r = b % rows;
+  p.o = b / rows;
+  x = threadIdx.x % t.across;
+  p.m = mids * (kMoveThreads / t.across) + threadIdx.x / t.across;
+  return p;
+}
+
+// kAligned: every row of both sides starts on a 16-byte boundary.  Otherwise 16-byte stores are
+// counted from the first boundary of dst's row, and what they store lies across two blocks of
+// src's; the bytes before, behind and beside the ends go one by one.
+template <bool kAligned>
 __global__ void __launch_bounds__(kMoveThreads) gather_kernel(BeamReorder a, Tile t) {
   pdl_wait_prerequisites();
   pdl_launch_dependents();
-  int64_t b = blockIdx.x;
-  const int64_t part = b % t.parts;
-  b /= t.parts;
-  const int64_t mids = b % t.mids;
-  b /= t.mids;
-  const int64_t r = b % a.rows, o = b / a.rows;
-  const int from = a.parents[r];
+  int x;
+  const Place at = place_of(t, a.rows, x);
+  const int from = a.parents[at.r];
   const bool none = from < 0 || from >= a.src_rows;
-  if (none && !a.clear) return;
-  const int x = threadIdx.x % t.across, y = threadIdx.x / t.across;
-  const int64_t m = mids * (kMoveThreads / t.across) + y;
-  if (m >= a.mid) return;
-  const U* const src = reinterpret_cast<const U*>(a.src + o * a.src_outer + from * a.src_row + m * a.src_mid);
-  U* const dst = reinterpret_cast<U*>(a.dst + o * a.dst_outer + r * a.dst_row + m * a.dst_mid);
-  const int64_t n = a.inner / static_cast<int64_t>(sizeof(U));
-  const int64_t i0 = part * t.across * kMoveUnroll + x;
-  const int tail = static_cast<int>(a.inner % static_cast<int64_t>(sizeof(U)));   // bytes behind the last unit
-  if (tail && i0 == 0) {
-    for (int e = 0; e < tail; ++e)
-      reinterpret_cast<char*>(dst + n)[e] = none ? 0 : reinterpret_cast<const char*>(src + n)[e];
+  if ((none && !a.clear) || at.m >= a.mid) return;
+  const char* const src = a.src + at.o * a.src_outer + (none ? 0 : from * a.src_row) + at.m * a.src_mid;
+  char* const dst = a.dst + at.o * a.dst_outer + at.r * a.dst_row + at.m * a.dst_mid;
+  const int64_t head = kAligned ? 0 : min(static_cast<int64_t>(-reinterpret_cast<intptr_t>(dst) & 15), a.inner);
+  const int64_t n = (a.inner - head) / 16, i0 = at.part * t.across * kMoveUnroll + x;
+  uint4 q[kMoveUnroll];
+#pragma unroll
+  for (int u = 0; u < kMoveUnroll; ++u) {
+    const int64_t i = i0 + u * t.across;
+    q[u] = make_uint4(0u, 0u, 0u, 0u);
+    if (none || i >= n) continue;
+    if (kAligned)
+      q[u] = reinterpret_cast<const uint4*>(src)[i];
+    else if (i > 0 && i + 2 <= n)
+      q[u] = load_across(src + head + i * 16);
+    else
+      for (int e = 0; e < 16; ++e) reinterpret_cast<char*>(&q[u])[e] = src[head + i * 16 + e];
   }
-  U q[kMoveUnroll] = {};
 #pragma unroll
   for (int u = 0; u < kMoveUnroll; ++u)
-    if (!none && i0 + u * t.across < n) q[u] = src[i0 + u * t.across];
-#pragma unroll
-  for (int u = 0; u < kMoveUnroll; ++u)
-    if (i0 + u * t.across < n) dst[i0 + u * t.across] = q[u];
+    if (i0 + u * t.across < n) reinterpret_cast<uint4*>(dst + head)[i0 + u * t.across] = q[u];
+  if (i0 == 0) {
+    for (int64_t e = 0; e < head; ++e) dst[e] = none ? 0 : src[e];
+    for (int64_t e = head + n * 16; e < a.inner; ++e) dst[e] = none ? 0 : src[e];
+  }
 }
 
-// BEAMS >= a.beams rows of a group, one unit of each per thread.
-template <typename U, int BEAMS>
-__global__ void __launch_bounds__(kMoveThreads) in_place_kernel(BeamReorder a, Tile t) {
-  __shared__ int from[BEAMS];
-  __shared__ int moving;
-  pdl_wait_prerequisites();
-  pdl_launch_dependents();
-  int64_t b = blockIdx.x;
-  const int64_t part = b % t.parts;
-  b /= t.parts;
-  const int64_t mids = b % t.mids;
-  b /= t.mids;
-  const int64_t groups = a.rows / a.beams, r0 = b % groups * a.beams, o = b / groups;
-  if (threadIdx.x == 0) moving = 0;
+// Group of `a.beams` rows: from[j] = the row that row j takes over, -1: it stays.
+__device__ __forceinline__ bool find_moves(const BeamReorder& a, int64_t r0, int* from, int* moving) {
+  if (threadIdx.x == 0) *moving = 0;
   __syncthreads();
-  if (threadIdx.x < BEAMS) {
-    int f = -1;              // stays
+  if (threadIdx.x < kMaxBeams) {
+    int f = -1;
     if (threadIdx.x < a.beams) {
       const int64_t p = a.parents[r0 + threadIdx.x] - r0;
       if (p >= 0 && p < a.beams && p != threadIdx.x) f = static_cast<int>(p);
     }
     from[threadIdx.x] = f;
-    if (f >= 0) moving = 1;
+    if (f >= 0) *moving = 1;
   }
   __syncthreads();
-  if (!moving) return;
-  const int x = threadIdx.x % t.across, y = threadIdx.x / t.across;
-  const int64_t m = mids * (kMoveThreads / t.across) + y;
-  const int64_t n = a.inner / static_cast<int64_t>(sizeof(U)), i = part * t.across + x;
-  if (m >= a.mid) return;
-  char* const row = a.dst + o * a.dst_outer + r0 * a.dst_row + m * a.dst_mid;
-  const int64_t tail = a.inner - n * static_cast<int64_t>(sizeof(U));
-  if (tail && i == 0) {      // bytes behind the last unit, one after the other
-    for (char* at = row + a.inner - tail; at < row + a.inner; ++at) {
+  return *moving != 0;
+}
+
+// Rows on 16-byte boundaries: BEAMS >= a.beams rows of a group, 16 bytes of each per thread.
+template <int BEAMS>
+__global__ void __launch_bounds__(kMoveThreads) in_place_kernel(BeamReorder a, Tile t) {
+  __shared__ int from[kMaxBeams], moving;
+  pdl_wait_prerequisites();
+  pdl_launch_dependents();
+  int x;
+  const Place at = place_of(t, a.rows / a.beams, x);
+  if (!find_moves(a, at.r * a.beams, from, &moving) || at.m >= a.mid) return;
+  char* const row = a.dst + at.o * a.dst_outer + at.r * a.beams * a.dst_row + at.m * a.dst_mid;
+  const int64_t n = a.inner / 16, i = at.part * t.across + x;
+  if (i == 0) {      // bytes behind the last unit, one after the other
+    for (char* p = row + n * 16; p < row + a.inner; ++p) {
       char c[BEAMS];
 #pragma unroll
       for (int j = 0; j < BEAMS; ++j)
-        if (from[j] >= 0) c[j] = at[from[j] * a.dst_row];
+        if (from[j] >= 0) c[j] = p[from[j] * a.dst_row];
 #pragma unroll
       for (int j = 0; j < BEAMS; ++j)
-        if (from[j] >= 0) at[j * a.dst_row] = c[j];
+        if (from[j] >= 0) p[j * a.dst_row] = c[j];
     }
   }
   if (i >= n) return;
-  char* const base = row + i * static_cast<int64_t>(sizeof(U));
-  U q[BEAMS];
+  uint4 q[BEAMS];
 #pragma unroll
   for (int j = 0; j < BEAMS; ++j)
-    if (from[j] >= 0) q[j] = *reinterpret_cast<const U*>(base + from[j] * a.dst_row);
+    if (from[j] >= 0) q[j] = *reinterpret_cast<const uint4*>(row + i * 16 + from[j] * a.dst_row);
 #pragma unroll
   for (int j = 0; j < BEAMS; ++j)
-    if (from[j] >= 0) *reinterpret_cast<U*>(base + j * a.dst_row) = q[j];
+    if (from[j] >= 0) *reinterpret_cast<uint4*>(row + i * 16 + j * a.dst_row) = q[j];
 }
 
-// The widest unit in bytes that every row's address is a multiple of (its length need not be);
-// 17 to 64 rows in registers take units of 4 bytes at most.
-int unit_of(const BeamReorder& a) {
+// Any alignment, or more rows than registers hold: `t.bytes` of each row that moves go to shared
+// memory, where a row keeps its source's place within 16 bytes, and from there to their
+// place, 16 bytes at a time from the destination's first boundary on.
+__global__ void __launch_bounds__(kMoveThreads) across_in_place_kernel(BeamReorder a, Tile t) {
+  extern __shared__ __align__(16) char held[];
+  __shared__ int from[kMaxBeams], moving;
+  pdl_wait_prerequisites();
+  pdl_launch_dependents();
+  int x;
+  const Place at = place_of(t, a.rows / a.beams, x);     // t.across is kMoveThreads
+  if (!find_moves(a, at.r * a.beams, from, &moving)) return;
+  char* const row = a.dst + at.o * a.dst_outer + at.r * a.beams * a.dst_row + at.m * a.dst_mid + at.part * t.bytes;
+  const int bytes = static_cast<int>(min(static_cast<int64_t>(t.bytes), a.inner - at.part * t.bytes));
+  const int room = t.bytes + 32, blocks = t.bytes / 16 + 2;
+  for (int f = threadIdx.x; f < a.beams * blocks; f += kMoveThreads) {
+    const int j = f / blocks, i = f % blocks;
+    if (from[j] < 0) continue;
+    const char* const src = row + from[j] * a.dst_row;
+    const int phase = static_cast<int>(reinterpret_cast<uintptr_t>(src) & 15u);
+    const int first = i * 16 - phase;       // of the row's bytes
+    char* const to = held + j * room + i * 16;
+    if (first >= 0 && first + 16 <= bytes)
+      *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(src + first);
+    else
+      for (int e = max(0, -first); e < 16 && first + e < bytes; ++e) to[e] = src[first + e];
+  }
+  __syncthreads();
+  for (int f = threadIdx.x; f < a.beams * blocks; f += kMoveThreads) {
+    const int j = f / blocks, i = f % blocks;
+    if (from[j] < 0) continue;
+    char* const dst = row + j * a.dst_row;
+    const int phase = static_cast<int>(reinterpret_cast<uintptr_t>(row + from[j] * a.dst_row) & 15u);
+    const int first = i * 16 - static_cast<int>(reinterpret_cast<uintptr_t>(dst) & 15u);
+    const char* const src = held + j * room + phase + first;
+    if (first >= 0 && first + 16 <= bytes)      // the second block read may lie behind the row's bytes, inside its room
+      *reinterpret_cast<uint4*>(dst + first) = load_across(src);
+    else
+      for (int e = max(0, -first); e < 16 && first + e < bytes; ++e) dst[first + e] = src[e];
+  }
+}
+
+bool aligned_rows(const BeamReorder& a) {
   const uint64_t bits = reinterpret_cast<uintptr_t>(a.src) | reinterpret_cast<uintptr_t>(a.dst) |
                         static_cast<uint64_t>(a.src_outer | a.dst_outer | a.src_row | a.dst_row | a.src_mid |
                                               a.dst_mid);
-  int unit = a.src == a.dst && a.beams > 16 ? 4 : 16;
-  while ((bits & static_cast<uint64_t>(unit - 1)) || unit > a.inner) unit /= 2;
-  return unit;
+  return (bits & 15) == 0;
 }
 
 // The tile and the number of CTAs.
-Tile tile_of(const BeamReorder& a, int unit, double& ctas) {
+Tile tile_of(const BeamReorder& a, double& ctas) {
   const bool in_place = a.src == a.dst;
-  const int64_t n = a.inner / unit;
-  const int each = in_place ? 1 : kMoveUnroll;
-  Tile t;
-  t.across = 1;
-  while (t.across < kMoveThreads && static_cast<int64_t>(t.across) * each < n) t.across *= 2;
-  t.parts = (n + static_cast<int64_t>(t.across) * each - 1) / (static_cast<int64_t>(t.across) * each);
-  const int down = kMoveThreads / t.across;
-  t.mids = (a.mid + down - 1) / down;
+  Tile t{};
+  if (in_place && (!aligned_rows(a) || a.beams > 16)) {
+    t.across = kMoveThreads;
+    t.bytes = kMoveShared / a.beams / 16 * 16 - 32;
+    if (t.bytes > 4096) t.bytes = 4096;
+    t.parts = (a.inner + t.bytes - 1) / t.bytes;
+    t.mids = a.mid;
+  } else {
+    const int64_t n = (a.inner + 15) / 16, each = in_place ? 1 : kMoveUnroll;
+    t.across = 1;
+    while (t.across < kMoveThreads && t.across * each < n) t.across *= 2;
+    t.parts = (n + t.across * each - 1) / (t.across * each);
+    const int down = kMoveThreads / t.across;
+    t.mids = (a.mid + down - 1) / down;
+  }
   ctas = static_cast<double>(t.parts) * static_cast<double>(t.mids) * static_cast<double>(a.outer) *
          static_cast<double>(in_place ? a.rows / a.beams : a.rows);
   return t;
-}
-
-template <typename U>
-cudaError_t move(const BeamReorder& a, cudaStream_t s) {
-  double ctas = 0;
-  const Tile t = tile_of(a, sizeof(U), ctas);
-  const dim3 grid(static_cast<unsigned>(ctas));
-  if (a.src != a.dst) return launch_dependent(gather_kernel<U>, grid, kMoveThreads, 0, 1, s, a, t);
-  if (a.beams <= 4) return launch_dependent(in_place_kernel<U, 4>, grid, kMoveThreads, 0, 1, s, a, t);
-  if (a.beams <= 8) return launch_dependent(in_place_kernel<U, 8>, grid, kMoveThreads, 0, 1, s, a, t);
-  if (a.beams <= 16) return launch_dependent(in_place_kernel<U, 16>, grid, kMoveThreads, 0, 1, s, a, t);
-  if constexpr (sizeof(U) <= 4) {
-    return launch_dependent(in_place_kernel<U, kMaxBeams>, grid, kMoveThreads, 0, 1, s, a, t);
-  } else {
-    return cudaErrorInvalidValue;   // unit_of gives none
-  }
 }
 
 size_t round_up(size_t n) { return (n + 255) / 256 * 256; }
@@ -731,19 +781,23 @@ cudaError_t launch_beam_select(const BeamSelect& a, cudaStream_t s) {
 
 bool beam_reorder_fits(const BeamReorder& a) {
   double ctas = 0;
-  tile_of(a, unit_of(a), ctas);
+  tile_of(a, ctas);
   return ctas <= 2147483647.0;
 }
 
 cudaError_t launch_beam_reorder(const BeamReorder& a, cudaStream_t s) {
+  double ctas = 0;
+  const Tile t = tile_of(a, ctas);
+  const dim3 grid(static_cast<unsigned>(ctas));
   return traced_launch("beam_reorder", s, [&] {
-    switch (unit_of(a)) {
-      case 16: return move<uint4>(a, s);
-      case 8: return move<uint2>(a, s);
-      case 4: return move<uint32_t>(a, s);
-      case 2: return move<uint16_t>(a, s);
-      default: return move<uint8_t>(a, s);
-    }
+    const bool aligned = aligned_rows(a);
+    if (a.src != a.dst)
+      return launch_dependent(aligned ? gather_kernel<true> : gather_kernel<false>, grid, kMoveThreads, 0, 1, s, a, t);
+    if (!aligned || a.beams > 16)
+      return launch_dependent(across_in_place_kernel, grid, kMoveThreads, static_cast<size_t>(a.beams) * (t.bytes + 32), 1,
+                              s, a, t);
+    auto kern = a.beams <= 4 ? in_place_kernel<4> : a.beams <= 8 ? in_place_kernel<8> : in_place_kernel<16>;
+    return launch_dependent(kern, grid, kMoveThreads, 0, 1, s, a, t);
   });
 }
 

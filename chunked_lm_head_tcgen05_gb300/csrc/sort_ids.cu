@@ -5,8 +5,8 @@
 // ranks them by one digit and writes each to its new place, in whichever CTA
 // that is.  Up to 131,072 ids (8 CTAs x 16,384 pairs); digits of up to 9 bits, so
 // a 151,936-id vocabulary takes two passes.
-// Rank of a pair among those with its digit: pairs before it in its warp (a
-// match over the warp's lanes, and the warp's own counts from earlier rounds), in
+// Rank of a pair among those with its digit: pairs before it in its warp (votes
+// over the warp's lanes, and the warp's own counts from earlier rounds), in
 // earlier warps and in earlier CTAs; counts are sums of integers, so the order is
 // the same in every run.
 // Bound by latency: a few thousand cycles per pass.
@@ -95,7 +95,14 @@ __global__ void __launch_bounds__(kThreads) sort_kernel(SortArgs a) {
 #pragma unroll
     for (int j = 0; j < ITEMS; ++j) {
       const uint32_t d = static_cast<uint32_t>(pr[j] >> shift) & mask;
-      const uint32_t peers = __match_any_sync(0xffffffffu, d);
+      // lanes with the same digit, bit by bit: a match instruction over 32 different values
+      // takes longer than nine votes
+      uint32_t peers = 0xffffffffu;
+      for (int b = 0; b < a.bits; ++b) {
+        const bool on = d >> b & 1u;
+        const uint32_t votes = __ballot_sync(0xffffffffu, on);
+        peers &= on ? votes : ~votes;
+      }
       const int before = own[d];
       rnk[j] = static_cast<uint16_t>(before + __popc(peers & ((1u << lane) - 1u)));
       __syncwarp();
