@@ -169,15 +169,23 @@ __device__ void fill_zeros(const EmbedBwd& a, const Sorted& z, int64_t v0) {
   }
   __syncthreads();
   constexpr int VEC = kVec<O>;
-  for (int r = 0; r < rows; ++r) {
-    if (!absent[r]) continue;
+  for (int r = 0; r < rows;) {
+    if (!absent[r]) {
+      ++r;
+      continue;
+    }
+    int end = r + 1;       // rows next to each other are one stretch of memory
+    while (end < rows && absent[end]) ++end;
     O* const dst = static_cast<O*>(a.d_weight) + (v0 + r) * a.H;
-    const int head = min(to_boundary(dst), a.H), packs = (a.H - head) / VEC;
+    const int64_t n = static_cast<int64_t>(end - r) * a.H;
+    const int64_t head = min(static_cast<int64_t>(to_boundary(dst)), n), packs = (n - head) / VEC;
     if (threadIdx.x < head) dst[threadIdx.x] = from_f32<O>(0.f);
-    for (int p = threadIdx.x; p < packs; p += kSumThreads)
+#pragma unroll 4
+    for (int64_t p = threadIdx.x; p < packs; p += kSumThreads)
       *reinterpret_cast<uint4*>(dst + head + p * VEC) = make_uint4(0u, 0u, 0u, 0u);
-    const int c = head + packs * VEC + threadIdx.x;
-    if (c < a.H) dst[c] = from_f32<O>(0.f);
+    const int64_t c = head + packs * VEC + threadIdx.x;
+    if (c < n) dst[c] = from_f32<O>(0.f);
+    r = end;
   }
 }
 
