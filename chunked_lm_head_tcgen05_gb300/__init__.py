@@ -776,6 +776,7 @@ def lmhead_process_logits_bwd(grad_out, logits, tokens, spans, repetition, allow
                  d_logits.data_ptr(), d_ld)
 
 
+@functools.lru_cache(maxsize=128)
 def lmhead_embedding_workspace_size(N, H):
     return int(library().lmhead_embedding_workspace_size(N, H))
 
@@ -800,15 +801,29 @@ def _embedding_types(dtype):
     return (f32, bf16) if dtype is f32 else (dtype, f32)
 
 
-def lmhead_embedding_fwd(ids, weight, scale, y, stream=None):
-    """C ``lmhead_embedding_fwd`` on torch tensors; returns the status code."""
+def _embedding_fwd(ids, weight, scale, y, out_dtype, stream):
+    """y None: a new one."""
     N = _check_ids(ids)
     V, H = weight.shape
     kind, w_ld = _check_rows(weight, "weight", (V, H))
-    y_type, y_ld = _check_rows(y, "y", (N, H), _embedding_types(weight.dtype))
-    dev = _one_device(weight, ids, y)
+    if y is None:
+        dtype = weight.dtype if out_dtype is None else out_dtype
+        if dtype not in _embedding_types(weight.dtype):
+            raise TypeError("a table of %s gives no %s" % (weight.dtype, dtype))
+        y, y_type, y_ld = _torch.empty((N, H), dtype=dtype, device=weight.device), _types[dtype], H
+        dev = _one_device(weight, ids)
+    else:
+        y_type, y_ld = _check_rows(y, "y", (N, H), _embedding_types(weight.dtype))
+        dev = _one_device(weight, ids, y)
     return _call(library().lmhead_embedding_fwd, dev, stream, ids.data_ptr(), N, weight.data_ptr(),
-                 kind, w_ld, V, H, scale, y.data_ptr(), y_type, y_ld)
+                 kind, w_ld, V, H, scale, y.data_ptr(), y_type, y_ld), y
+
+
+def lmhead_embedding_fwd(ids, weight, scale, y, stream=None):
+    """C ``lmhead_embedding_fwd`` on torch tensors; returns the status code."""
+    if y is None:
+        raise ValueError("y is required")
+    return _embedding_fwd(ids, weight, scale, y, None, stream)[0]
 
 
 def lmhead_embedding_bwd(dy, ids, scale, padding_id, d_weight, accumulate, workspace, stream=None):
@@ -829,6 +844,7 @@ def lmhead_embedding_bwd(dy, ids, scale, padding_id, d_weight, accumulate, works
                  1 if accumulate else 0, workspace.data_ptr(), workspace.nbytes)
 
 
+@functools.lru_cache(maxsize=128)
 def lmhead_adapters_workspace_size(T, H, V, rank, n_adapters):
     return int(library().lmhead_adapters_workspace_size(T, H, V, rank, n_adapters))
 
@@ -877,36 +893,57 @@ def lmhead_adapters_bwd(grad_out, x, down, up, adapter_ids, scale, dx, accumulat
                  _ptr(d_up), 1 if accumulate else 0, workspace.data_ptr(), workspace.nbytes)
 
 
+@functools.lru_cache(maxsize=128)
 def lmhead_beam_workspace_size(R, V, take):
     return int(library().lmhead_beam_workspace_size(R, V, take))
 
 
-def lmhead_beam_select(logits, beams, take, scores, finished, eos_id, temperature, out_scores,
-                       parents, tokens, next_finished, lse, workspace, stream=None):
-    """C ``lmhead_beam_select`` on torch tensors; returns the status code."""
+def _beam_select(logits, beams, take, scores, finished, eos_id, temperature, out, next_finished,
+                 lse, workspace, stream):
+    """out: (scores, parents, tokens), or None for new ones and a new lse, and workspace if None."""
     R, V = logits.shape
     kind, ld = _check_rows(logits, "logits", (R, V))
     torch = _torch
-    _check_tensor(scores, "scores", torch.float32, (R,))
-    _check_tensor(finished, "finished", torch.uint8, (R,), allow_none=True)
+    f32, i32, u8 = torch.float32, torch.int32, torch.uint8
+    _check_tensor(scores, "scores", f32, (R,))
+    _check_tensor(finished, "finished", u8, (R,), allow_none=True)
     if beams <= 0 or R % beams:
         raise ValueError("logits must have the rows of whole groups of beams: got %d rows of %d "
                          "beams" % (R, beams))
     if not -1 <= eos_id < V:
         raise ValueError("eos_id %d is no id of a vocabulary of %d" % (eos_id, V))
     shape = (R // beams, take)
-    _check_tensor(out_scores, "out_scores", torch.float32, shape)
-    _check_tensor(parents, "parents", torch.int32, shape)
-    _check_tensor(tokens, "tokens", torch.int32, shape)
-    _check_tensor(next_finished, "next_finished", torch.uint8, shape, allow_none=True)
-    _check_tensor(lse, "lse", torch.float32, (R,), allow_none=True)
-    _check_workspace(workspace)
-    dev = _one_device(logits, scores, finished, out_scores, parents, tokens, next_finished, lse,
-                      workspace)
-    return _call(library().lmhead_beam_select, dev, stream, logits.data_ptr(), kind, ld, R, V,
-                 beams, take, scores.data_ptr(), _ptr(finished), eos_id, temperature,
-                 out_scores.data_ptr(), parents.data_ptr(), tokens.data_ptr(), _ptr(next_finished),
-                 _ptr(lse), workspace.data_ptr(), workspace.nbytes)
+    _check_tensor(next_finished, "next_finished", u8, shape, allow_none=True)
+    if out is None:
+        empty, where = torch.empty, logits.device
+        out = empty(shape, dtype=f32, device=where), empty(shape, dtype=i32, device=where), \
+            empty(shape, dtype=i32, device=where)
+        lse = empty(R, dtype=f32, device=where)
+        dev = _one_device(logits, scores, finished, next_finished)
+        if workspace is None:
+            workspace = empty(lmhead_beam_workspace_size(R, V, take), dtype=u8, device=where)
+        else:
+            _check_workspace(workspace)
+            _one_device(logits, workspace)
+    else:
+        _check_tensor(out[0], "out_scores", f32, shape)
+        _check_tensor(out[1], "parents", i32, shape)
+        _check_tensor(out[2], "tokens", i32, shape)
+        _check_tensor(lse, "lse", f32, (R,), allow_none=True)
+        _check_workspace(workspace)
+        dev = _one_device(logits, scores, finished, *out, next_finished, lse, workspace)
+    rc = _call(library().lmhead_beam_select, dev, stream, logits.data_ptr(), kind, ld, R, V, beams,
+               take, scores.data_ptr(), _ptr(finished), eos_id, temperature, out[0].data_ptr(),
+               out[1].data_ptr(), out[2].data_ptr(), _ptr(next_finished), _ptr(lse),
+               workspace.data_ptr(), workspace.nbytes)
+    return rc, (*out, lse)
+
+
+def lmhead_beam_select(logits, beams, take, scores, finished, eos_id, temperature, out_scores,
+                       parents, tokens, next_finished, lse, workspace, stream=None):
+    """C ``lmhead_beam_select`` on torch tensors; returns the status code."""
+    return _beam_select(logits, beams, take, scores, finished, eos_id, temperature,
+                        (out_scores, parents, tokens), next_finished, lse, workspace, stream)[0]
 
 
 @functools.lru_cache(maxsize=128)
@@ -1281,12 +1318,7 @@ def embedding_forward(ids, weight, scale=1.0, out_dtype=None, out=None, stream=N
     or out_dtype (bf16 for an fp32 table, fp32 for a 16-bit one)."""
     if stream is not None:
         return _made_on(stream, weight, embedding_forward, ids, weight, scale, out_dtype, out)
-    if out is None:
-        if _torch is None:
-            _bind_torch()
-        out = _torch.empty((ids.shape[0], weight.shape[1]), device=weight.device,
-                           dtype=weight.dtype if out_dtype is None else out_dtype)
-    rc = lmhead_embedding_fwd(ids, weight, scale, out)
+    rc, out = _embedding_fwd(ids, weight, scale, out, out_dtype, None)
     if rc:
         raise LmheadError(rc, "lmhead_embedding_fwd")
     return out
@@ -1327,26 +1359,14 @@ def beam_select(logits, scores, beams, take=None, temperature=1.0, finished=None
     if stream is not None:
         return _made_on(stream, logits, beam_select, logits, scores, beams, take, temperature,
                         finished, eos_id, next_finished, workspace)
-    if _torch is None:
-        _bind_torch()
-    torch = _torch
-    R, V = logits.shape
     take = beams if take is None else take
     if beams <= 0 or take <= 0:
         raise ValueError("beams and take must be positive, got %d and %d" % (beams, take))
-    where = logits.device
-    empty, shape = torch.empty, (R // beams, take)
-    out_scores = empty(shape, dtype=torch.float32, device=where)
-    parents = empty(shape, dtype=torch.int32, device=where)
-    tokens = empty(shape, dtype=torch.int32, device=where)
-    lse = empty(R, dtype=torch.float32, device=where)
-    if workspace is None:
-        workspace = empty(lmhead_beam_workspace_size(R, V, take), dtype=torch.uint8, device=where)
-    rc = lmhead_beam_select(logits, beams, take, scores, finished, eos_id, temperature, out_scores,
-                            parents, tokens, next_finished, lse, workspace)
+    rc, out = _beam_select(logits, beams, take, scores, finished, eos_id, temperature, None,
+                           next_finished, None, workspace, None)
     if rc:
         raise LmheadError(rc, "lmhead_beam_select")
-    return out_scores, parents, tokens, lse
+    return out
 
 
 def beam_reorder(state, parents, dim=0, out=None, beams=0, stream=None):

@@ -602,9 +602,23 @@ __device__ __forceinline__ bool find_moves(const BeamReorder& a, int64_t r0, int
   return *moving != 0;
 }
 
+// Bytes [at, end) of a group's rows, one after the other.
+template <int BEAMS>
+__device__ __noinline__ void move_bytes(char* at, char* end, int64_t stride, const int* from) {
+  for (; at < end; ++at) {
+    char c[BEAMS];
+#pragma unroll
+    for (int j = 0; j < BEAMS; ++j)
+      if (from[j] >= 0) c[j] = at[from[j] * stride];
+#pragma unroll
+    for (int j = 0; j < BEAMS; ++j)
+      if (from[j] >= 0) at[j * stride] = c[j];
+  }
+}
+
 // Rows on 16-byte boundaries: BEAMS >= a.beams rows of a group, 16 bytes of each per thread.
 template <int BEAMS>
-__global__ void __launch_bounds__(kMoveThreads) in_place_kernel(BeamReorder a, Tile t) {
+__global__ void __launch_bounds__(kMoveThreads, BEAMS <= 4 ? 6 : BEAMS <= 8 ? 4 : 2) in_place_kernel(BeamReorder a, Tile t) {
   __shared__ int from[kMaxBeams], moving;
   pdl_wait_prerequisites();
   pdl_launch_dependents();
@@ -613,17 +627,7 @@ __global__ void __launch_bounds__(kMoveThreads) in_place_kernel(BeamReorder a, T
   if (!find_moves(a, at.r * a.beams, from, &moving) || at.m >= a.mid) return;
   char* const row = a.dst + at.o * a.dst_outer + at.r * a.beams * a.dst_row + at.m * a.dst_mid;
   const int64_t n = a.inner / 16, i = at.part * t.across + x;
-  if (i == 0) {      // bytes behind the last unit, one after the other
-    for (char* p = row + n * 16; p < row + a.inner; ++p) {
-      char c[BEAMS];
-#pragma unroll
-      for (int j = 0; j < BEAMS; ++j)
-        if (from[j] >= 0) c[j] = p[from[j] * a.dst_row];
-#pragma unroll
-      for (int j = 0; j < BEAMS; ++j)
-        if (from[j] >= 0) p[j * a.dst_row] = c[j];
-    }
-  }
+  if (i == 0 && n * 16 < a.inner) move_bytes<BEAMS>(row + n * 16, row + a.inner, a.dst_row, from);
   if (i >= n) return;
   uint4 q[BEAMS];
 #pragma unroll
