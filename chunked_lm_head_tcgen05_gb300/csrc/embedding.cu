@@ -212,7 +212,7 @@ __device__ __forceinline__ void put(O* dst, const float (&sum)[VEC], float scale
 
 // CTAs below segments * chunks: (segment, columns); those behind write zeros.
 template <typename D, typename O, int VEC>
-__global__ void __launch_bounds__(kSumThreads, 8) sum_kernel(EmbedBwd a, Sorted z, int64_t first, int seg,
+__global__ void __launch_bounds__(kSumThreads, VEC == 1 ? 12 : 8) sum_kernel(EmbedBwd a, Sorted z, int64_t first, int seg,
                                                           int chunks) {
   // rows in flight per thread: eight packs hold registers that more threads use better (170 us
   // where four take 149, 65,536 x 2,560 bf16)
