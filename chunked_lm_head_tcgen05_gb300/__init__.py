@@ -966,7 +966,7 @@ def _layout(shape, a, b, dim, size):
         inner = behind.pop()[0]
     if len(before) > 1 or len(behind) > 1:
         raise ValueError("state must be one block of rows, repeated at most once outside `dim` and "
-                         "once inside it: got shape %s, strides %s and %s" % (shape, a, b))
+                         "once inside it: got shape %s, strides %s and %s" % (tuple(shape), a, b))
     outer = before[0] if before else (1, 0, 0)
     mid = behind[0] if behind else (1, 0, 0)
     return outer[0], mid[0], inner * size, \
@@ -977,37 +977,53 @@ def _layout(shape, a, b, dim, size):
 def _state_layout(state, out, dim):
     """(outer, mid, inner_bytes, (outer, row, mid) strides in bytes of state and of out): the
     dimensions before `dim` as one, those behind it as one and a contiguous rest."""
-    return _layout(tuple(state.shape), state.stride(), out.stride(), dim, state.element_size())
+    a = state.stride()
+    return _layout(state.shape, a, a if out is state else out.stride(), dim, state.element_size())
 
 
-def lmhead_beam_reorder(state, out, parents, dim, beams=0, clear_missing=False, stream=None):
-    """C ``lmhead_beam_reorder`` on torch tensors of any element type whose rows lie along `dim`;
-    in place where out is the state.  Returns the status code."""
+def _beam_reorder(state, out, parents, dim, beams, clear_missing, stream):
+    """out None: a new one."""
     if _torch is None:
         _bind_torch()
     if parents is None or parents.dim() != 1:
         raise ValueError("parents must be a list of rows")
     rows = parents.shape[0]
     _check_tensor(parents, "parents", _torch.int32, (rows,))
-    for t, name in ((state, "state"), (out, "out")):
-        if not t.is_cuda:
-            raise ValueError("%s must be a CUDA tensor" % name)
-    if not 0 <= dim < state.dim():
+    if not state.is_cuda:
+        raise ValueError("state must be a CUDA tensor")
+    shape = state.shape
+    if not 0 <= dim < len(shape):
         raise ValueError("state has no dimension %d" % dim)
-    shape = state.shape[:dim] + (rows,) + state.shape[dim + 1:]
-    if out.dtype is not state.dtype:
-        raise TypeError("out must be %s, got %s" % (state.dtype, out.dtype))
-    if out.shape != shape:
-        raise ValueError("out has shape %s, expected %s" % (tuple(out.shape), tuple(shape)))
     if not 0 <= beams < 2 ** 31:
         raise ValueError("beams must be the rows of a group, got %d" % beams)
-    dev = _one_device(state, out, parents)
+    src_rows = shape[dim]
+    if src_rows != rows:
+        shape = shape[:dim] + (rows,) + shape[dim + 1:]
+    if out is None:
+        out = _torch.empty(shape, dtype=state.dtype, device=state.device)
+        dev = _one_device(state, parents)
+    else:
+        if not out.is_cuda:
+            raise ValueError("out must be a CUDA tensor")
+        if out.dtype is not state.dtype:
+            raise TypeError("out must be %s, got %s" % (state.dtype, out.dtype))
+        if out.shape != shape:
+            raise ValueError("out has shape %s, expected %s" % (tuple(out.shape), tuple(shape)))
+        dev = _one_device(state, out, parents)
     if out.numel() == 0:
-        return 0
+        return 0, out
     outer, mid, inner, (so, sr, sm), (do, dr, dm) = _state_layout(state, out, dim)
-    return _call(library().lmhead_beam_reorder, dev, stream, state.data_ptr(), so, sr, sm,
-                 state.shape[dim], out.data_ptr(), do, dr, dm, parents.data_ptr(), rows, beams,
-                 outer, mid, inner, 1 if clear_missing else 0)
+    return _call(library().lmhead_beam_reorder, dev, stream, state.data_ptr(), so, sr, sm, src_rows,
+                 out.data_ptr(), do, dr, dm, parents.data_ptr(), rows, beams, outer, mid, inner,
+                 1 if clear_missing else 0), out
+
+
+def lmhead_beam_reorder(state, out, parents, dim, beams=0, clear_missing=False, stream=None):
+    """C ``lmhead_beam_reorder`` on torch tensors of any element type whose rows lie along `dim`;
+    in place where out is the state.  Returns the status code."""
+    if out is None:
+        raise ValueError("out is required")
+    return _beam_reorder(state, out, parents, dim, beams, clear_missing, stream)[0]
 
 
 def lmhead_selftest_bounded_wait(workspace, limit_ms, stream=None):
@@ -1377,14 +1393,7 @@ def beam_reorder(state, parents, dim=0, out=None, beams=0, stream=None):
         return _made_on(stream, state, beam_reorder, state, parents, dim, out, beams)
     if dim < 0:
         dim += state.dim()
-    new = out is None
-    if new:
-        if _torch is None:
-            _bind_torch()
-        shape = list(state.shape)
-        shape[dim] = parents.shape[0]
-        out = _torch.empty(shape, dtype=state.dtype, device=state.device)
-    rc = lmhead_beam_reorder(state, out, parents, dim, beams, new)
+    rc, out = _beam_reorder(state, out, parents, dim, beams, out is None, None)
     if rc:
         raise LmheadError(rc, "lmhead_beam_reorder")
     return out
