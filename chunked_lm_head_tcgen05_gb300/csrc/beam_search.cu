@@ -344,7 +344,8 @@ __device__ __forceinline__ bool ahead(const Ranked& x, const Ranked& y) {
   return x.score > y.score || (x.score == y.score && x.at < y.at);
 }
 
-__global__ void __launch_bounds__(kBestThreads) best_kernel(BeamSelect a, Pieces z) {
+// inv = 1 / tau, formed by the host: a 64-bit division by every thread here takes 4 us.
+__global__ void __launch_bounds__(kBestThreads) best_kernel(BeamSelect a, Pieces z, double inv) {
   __shared__ Ranked found[kRoom];
   // lse = top / tau + log s, so score(j, v) = (score_j - log s) + (x_v - top) / tau: a row
   // whose logits are all near the type's lowest value keeps its differences
@@ -359,7 +360,6 @@ __global__ void __launch_bounds__(kBestThreads) best_kernel(BeamSelect a, Pieces
   const int64_t g = blockIdx.x, r0 = g * a.beams;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) n_found = 0;
-  const double inv = 1.0 / static_cast<double>(a.tau);
   for (int j = warp; j < a.beams; j += kBestWarps) {
     const int64_t r = r0 + j;
     const float score = a.scores[r];
@@ -531,21 +531,24 @@ struct Tile {
   int bytes;            // of a row per CTA (across_in_place_kernel)
 };
 
-// What a CTA moves.
+// What a CTA moves.  All counts are below 2^31, as the number of CTAs is; 64-bit divisions
+// would cost a thread more than its copy.
 struct Place {
   int64_t part, m, r, o;
 };
 __device__ __forceinline__ Place place_of(const Tile& t, int64_t rows, int& x) {
-  int64_t b = blockIdx.x;
+  const unsigned parts = static_cast<unsigned>(t.parts), mids = static_cast<unsigned>(t.mids),
+                 count = static_cast<unsigned>(rows), across = static_cast<unsigned>(t.across);
+  unsigned b = blockIdx.x;
   Place p;
-  p.part = b % t.parts;
-  b /= t.parts;
-  const int64_t mids = b % t.mids;
-  b /= t.mids;
-  p.r = b % rows;
-  p.o = b / rows;
-  x = threadIdx.x % t.across;
-  p.m = mids * (kMoveThreads / t.across) + threadIdx.x / t.across;
+  p.part = b % parts;
+  b /= parts;
+  const unsigned mid = b % mids;
+  b /= mids;
+  p.r = b % count;
+  p.o = b / count;
+  x = static_cast<int>(threadIdx.x & (across - 1));       // a power of two
+  p.m = static_cast<int64_t>(mid) * (kMoveThreads / across) + threadIdx.x / across;
   return p;
 }
 
@@ -781,7 +784,8 @@ cudaError_t launch_beam_select(const BeamSelect& a, cudaStream_t s) {
   });
   if (e != cudaSuccess) return e;
   return traced_launch("beam_select_best", s, [&] {
-    return launch_dependent(best_kernel, dim3(static_cast<unsigned>(a.R / a.beams)), kBestThreads, 0, 1, s, a, z);
+    return launch_dependent(best_kernel, dim3(static_cast<unsigned>(a.R / a.beams)), kBestThreads, 0, 1, s, a, z,
+                            1.0 / static_cast<double>(a.tau));
   });
 }
 
