@@ -38,7 +38,8 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kBlock = 256;      // columns of the wide side per CTA (widen, outer)
 constexpr int kPad = 8;          // elements between rows in shared memory: no bank conflicts
 constexpr int kParts = 3;        // bf16 parts of u
-constexpr int kFewRows = 8;      // of a run whose factor is not shared
+constexpr int kFewAtOnce = 4;    // rows of a run that few_kernel takes
+constexpr int kFewMean = 16;     // rows per adapter, up to which it takes all runs
 constexpr int kOuterRows = 32;   // rows of a step of outer_kernel
 constexpr int kManyCtas = 608;   // four per SM
 constexpr int kFewCtas = 304;    // two
@@ -60,16 +61,14 @@ struct Item {
 
 struct Plan {
   int* live;         // rows with an adapter
-  int* counts;       // of items, runs and few
+  int* counts;       // of items and of runs
   int32_t* keys;     // [rows] adapters in order
   int32_t* pos;      // [rows] their rows
   int* starts;       // [n + 2] first sorted place of each adapter, of the rows without, and the end
   Item* items;       // up to kRows rows of one adapter each
-  Item* runs;        // up to run_rows rows each, those of at most kFewRows rows apart, in few
-  Item* few;
-  int most;          // items at most, so also of the other lists
+  Item* runs;        // up to run_rows rows each
+  int most;          // items at most
   int run_rows;
-  int use_few;
   int rows;
   int n;
 };
@@ -150,7 +149,7 @@ constexpr int kSmallRows = 1024, kSmallKeys = 512;
 // of sort_ids.cu's kind, whose digit is the adapter: a launch less.
 template <bool kSmall>
 __global__ void __launch_bounds__(1024) plan_kernel(Plan p, const int32_t* ids) {
-  __shared__ int sums[3][32], total[3];
+  __shared__ int sums[2][32], total[2];
   pdl_wait_prerequisites();
   pdl_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -203,17 +202,15 @@ __global__ void __launch_bounds__(1024) plan_kernel(Plan p, const int32_t* ids) 
       for (int a = before + 1; a <= here; ++a) p.starts[a] = g;
     }
   }
-  if (tid < 3) total[tid] = 0;
+  if (tid < 2) total[tid] = 0;
   __syncthreads();
   for (int a0 = 0; a0 <= p.n; a0 += 1024) {
     const int a = a0 + tid;
     const int first = a <= p.n ? p.starts[a] : 0, count = a <= p.n ? p.starts[a + 1] - first : 0;
-    // a last run of few rows is listed with the few, if its rows have an adapter
-    const int rest = count % p.run_rows, is_few = p.use_few && rest > 0 && rest <= kFewRows && a < p.n;
-    const int mine[3] = {(count + kRows - 1) / kRows, (count + p.run_rows - 1) / p.run_rows - is_few, is_few};
-    int scan[3];
+    const int mine[2] = {(count + kRows - 1) / kRows, (count + p.run_rows - 1) / p.run_rows};
+    int scan[2];
 #pragma unroll
-    for (int l = 0; l < 3; ++l) {
+    for (int l = 0; l < 2; ++l) {
       scan[l] = mine[l];
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -223,9 +220,9 @@ __global__ void __launch_bounds__(1024) plan_kernel(Plan p, const int32_t* ids) 
       if (lane == 31) sums[l][warp] = scan[l];
     }
     __syncthreads();
-    int at[3];
+    int at[2];
 #pragma unroll
-    for (int l = 0; l < 3; ++l) {
+    for (int l = 0; l < 2; ++l) {
       at[l] = total[l] + scan[l] - mine[l];
       for (int w = 0; w < warp; ++w) at[l] += sums[l][w];
     }
@@ -233,15 +230,14 @@ __global__ void __launch_bounds__(1024) plan_kernel(Plan p, const int32_t* ids) 
       p.items[at[0] + i] = Item{a, first + i * kRows, min(kRows, count - i * kRows), 0};
     for (int i = 0; i < mine[1]; ++i)
       p.runs[at[1] + i] = Item{a, first + i * p.run_rows, min(p.run_rows, count - i * p.run_rows), 0};
-    if (is_few) p.few[at[2]] = Item{a, first + count - rest, rest, 0};
     __syncthreads();
     if (tid == 1023) {
 #pragma unroll
-      for (int l = 0; l < 3; ++l) total[l] = at[l] + mine[l];
+      for (int l = 0; l < 2; ++l) total[l] = at[l] + mine[l];
     }
     __syncthreads();
   }
-  if (tid < 3) p.counts[tid] = total[tid];
+  if (tid < 2) p.counts[tid] = total[tid];
 }
 
 // ------------------------------------------------------------------ tiles in shared memory
@@ -499,10 +495,9 @@ __global__ void __launch_bounds__(kThreads) join_kernel(Plan p, Join first, Join
 // the group of 32 lies at (w % 4) * 4 + w / 4.  So rows of y move 16 bytes a thread.
 // Rows off 16-byte boundaries go column by column instead, their share by way of
 // the warp's own corner of shared memory.
-// few_kernel takes the runs of few rows (one token per request), which have nothing to
-// share: each thread multiplies its 8 columns of F, read once, by the rows' u (64 rows of 16
+// few_kernel takes runs of up to four rows where adapters have few (one token per request),
+// which have little to share: each thread multiplies its 8 columns of F, read once, by the rows' u (64 rows of 16
 // adapters, rank 16, 151,936 columns: 31 us, 3.4 TB/s).
-constexpr int kFewAtOnce = 4;                // rows' sums in registers
 constexpr int kFewBlock = kThreads * 8;      // columns of such a unit
 constexpr int kMostRun = 512;
 
@@ -742,21 +737,17 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const Y* base, int64_t
   __shared__ float4 us[kMaxRank];      // of four rows
   pdl_wait_prerequisites();
   pdl_launch_dependents();
-  const int n_few = p.counts[2], blocks = (width - 1) / kFewBlock + 1, wide_rank = round_rank(rank);
-  constexpr int kTurns = kFewRows / kFewAtOnce;
-  const int64_t units = static_cast<int64_t>(n_few) * kTurns * blocks;
+  const int n_runs = p.counts[1], blocks = (width - 1) / kFewBlock + 1, wide_rank = round_rank(rank);
+  const int64_t units = static_cast<int64_t>(n_runs) * blocks;
   for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
-    // second turns, of which there are few, come last: every CTA gets its share of them
-    const int64_t each = static_cast<int64_t>(n_few) * blocks, rest = unit % each;
-    const int turn = static_cast<int>(unit / each);
-    Item it = p.few[rest / blocks];
-    it.first += turn * kFewAtOnce;
-    it.count = min(it.count - turn * kFewAtOnce, kFewAtOnce);
-    if (it.count <= 0) continue;
-    const int c = static_cast<int>(rest % blocks) * kFewBlock + threadIdx.x * 8;
+    const Item it = p.runs[unit / blocks];
+    const bool bare = it.adapter >= p.n;
+    if (bare && base == out) continue;
+    const int ranks = bare ? 0 : rank;
+    const int c = static_cast<int>(unit % blocks) * kFewBlock + threadIdx.x * 8;
     const bf16* const f = factor + static_cast<int64_t>(it.adapter) * rank * width;
     __syncthreads();     // the unit before has read its u
-    for (int i = threadIdx.x; i < kFewAtOnce * wide_rank; i += kThreads) {
+    for (int i = threadIdx.x; !bare && i < kFewAtOnce * wide_rank; i += kThreads) {
       const int r = i / wide_rank, k = i % wide_rank;      // 0 behind the rank
       const bf16* const q = u + static_cast<int64_t>(it.first + r) * kParts * wide_rank + k;
       reinterpret_cast<float*>(us)[k * 4 + r] =
@@ -772,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const Y* base, int64_t
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
           q[k] = Pack<bf16, 8>{};
-          if (k0 + k < rank && c < width) q[k] = load8<decltype(at)::value>(f + static_cast<int64_t>(k0 + k) * width, c, width);
+          if (k0 + k < ranks && c < width) q[k] = load8<decltype(at)::value>(f + static_cast<int64_t>(k0 + k) * width, c, width);
         }
       };
       fetch(0);      // before all that waits for the rows' places
@@ -792,7 +783,7 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const Y* base, int64_t
             if (c + e < width) y[r].v[e] = src[e];
         }
       }
-      for (int k0 = 0; k0 < rank; k0 += kAhead) {
+      for (int k0 = 0; k0 < ranks; k0 += kAhead) {
         if (k0) fetch(k0);
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
@@ -1031,7 +1022,8 @@ auto by_type(int type, F&& f) {
   }
 }
 
-int64_t most_items(int64_t rows, int n) { return rows / kRows + (n + 1 < rows ? n + 1 : rows) + 1; }
+// Items, or runs of `each` rows, that lists of rows of n adapters (and of none) are cut into.
+int64_t most_items(int64_t rows, int n, int each = kRows) { return rows / each + (n + 1 < rows ? n + 1 : rows) + 1; }
 
 // Splits of the wide side: one wave of two CTAs per SM (at 2,048 x 151,936 bf16 and rank 32
 // 2.4 waves took 155 us, one takes 130), at least 512 columns each.  Adapters' last items are part full.
@@ -1054,9 +1046,9 @@ int row_splits_of(int64_t rows, int width, int n) {
   return splits < 1 ? 1 : static_cast<int>(splits);
 }
 
-// Runs of few rows are worth a launch of their own where adapters have few on average
-// (64 requests of 16 adapters: 50 us a pass, 86 without).
-bool use_few(int64_t rows, int n) { return rows <= int64_t{kRows} * n; }
+// Whether few_kernel multiplies: where adapters have few rows on average (64 requests of 16
+// adapters: 40 us a pass, 86 by widen_kernel, which is the faster one for long runs).
+bool use_few(int64_t rows, int n) { return rows <= int64_t{kFewMean} * n; }
 
 struct Space {
   Plan plan;
@@ -1082,8 +1074,8 @@ Space lay_out(void* workspace, int64_t T, int H, int V, int rank, int n) {
   s.plan.starts = reinterpret_cast<int*>(take(4 * (static_cast<size_t>(n) + 2)));
   s.plan.most = static_cast<int>(most_items(rows, n));
   s.plan.items = reinterpret_cast<Item*>(take(sizeof(Item) * static_cast<size_t>(s.plan.most)));
-  s.plan.runs = reinterpret_cast<Item*>(take(sizeof(Item) * static_cast<size_t>(s.plan.most)));
-  s.plan.few = reinterpret_cast<Item*>(take(sizeof(Item) * static_cast<size_t>(s.plan.most)));
+  // the last part of a long list may have runs of few rows
+  s.plan.runs = reinterpret_cast<Item*>(take(sizeof(Item) * static_cast<size_t>(most_items(rows, n, kFewAtOnce))));
   s.plan.n = n;
   const size_t wide_rank = static_cast<size_t>(round_rank(rank));
   s.u = reinterpret_cast<bf16*>(take(2 * kParts * wide_rank * rows));
@@ -1186,20 +1178,19 @@ cudaError_t widen(const char* name, const Y* base, int64_t base_ld, Y* out, int6
     return packs ? widen_of<Y, KT, true>(base, base_ld, out, out_ld, f, width, rank, u, p, sms, s)
                  : widen_of<Y, KT, false>(base, base_ld, out, out_ld, f, width, rank, u, p, sms, s);
   };
-  const cudaError_t e = traced_launch(name, s, [&] {
+  if (use_few(p.rows, p.n))
+    return traced_launch("adapters_few", s, [&] {
+      auto kern = packs ? few_kernel<Y, true> : few_kernel<Y, false>;
+      const int64_t units = most_items(p.rows, p.n, kFewAtOnce) * ((static_cast<int64_t>(width) - 1) / kFewBlock + 1);
+      const int64_t resident = 2 * static_cast<int64_t>(sms);
+      return launch_dependent(kern, dim3(static_cast<unsigned>(units < resident ? units : resident)), kThreads, 0, 1, s,
+                              base, base_ld, out, out_ld, f, width, rank, u, p, whole_chunks(f, width, width));
+    });
+  return traced_launch(name, s, [&] {
     if (rank <= 16) return run(std::integral_constant<int, 1>{});
     if (rank <= 32) return run(std::integral_constant<int, 2>{});
     if (rank <= 64) return run(std::integral_constant<int, 4>{});
     return run(std::integral_constant<int, 8>{});
-  });
-  if (e != cudaSuccess || !p.use_few) return e;
-  return traced_launch("adapters_few", s, [&] {
-    auto kern = packs ? few_kernel<Y, true> : few_kernel<Y, false>;
-    const int64_t runs = p.n < p.rows ? p.n : p.rows;
-    const int64_t units = runs * (kFewRows / kFewAtOnce) * ((static_cast<int64_t>(width) - 1) / kFewBlock + 1);
-    const int64_t resident = 2 * static_cast<int64_t>(sms);
-    return launch_dependent(kern, dim3(static_cast<unsigned>(units < resident ? units : resident)), kThreads, 0, 1, s,
-                            base, base_ld, out, out_ld, f, width, rank, u, p, whole_chunks(f, width, width));
   });
 }
 
@@ -1246,7 +1237,7 @@ cudaError_t plan_rows(const Adapters& a, int64_t first, Space& z, cudaStream_t s
   const int64_t units = static_cast<int64_t>(a.V > a.H ? a.V : a.H) / kBlock * ((z.plan.rows + kRows - 1) / kRows);
   const int64_t run = units / (7 * kManyCtas);
   z.plan.run_rows = kRows * static_cast<int>(run < 1 ? 1 : run > kMostRun / kRows ? kMostRun / kRows : run);
-  z.plan.use_few = use_few(z.plan.rows, a.n);
+  if (use_few(z.plan.rows, a.n)) z.plan.run_rows = kFewAtOnce;
   const int32_t* const ids = a.ids ? a.ids + first : nullptr;
   const bool small = z.plan.rows <= kSmallRows && a.n + 2 <= kSmallKeys;
   if (!small) {
