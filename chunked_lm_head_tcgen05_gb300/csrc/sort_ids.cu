@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(kThreads) sort_kernel(SortArgs a) {
     pr[j] = pair_of_key(key, static_cast<uint32_t>(g));
   }
   if (tid == 0) *mine = 0;
-  __syncthreads();
+  cluster_sync();   // every CTA runs before one writes to its memory
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) inside += __shfl_xor_sync(0xffffffffu, inside, o);
   if (lane == 0 && inside) atomicAdd(mine, inside);
