@@ -178,14 +178,17 @@ __global__ void __launch_bounds__(kThreads, 4) scan_kernel(BeamSelect a, Pieces 
   __shared__ uint64_t found[kRoom];
   __shared__ uint32_t group_max[kMaxTake];
   __shared__ float2 warp_sums[kWarps];
-  __shared__ int scratch[kWarps], n_found;
+  // elements that tiles t, t + 1 and t + 2 find: a thread that is ahead counts its next tile's
+  // while others still read this one's, and the counter after that is cleared meanwhile
+  __shared__ int added[3];
+  __shared__ int scratch[kWarps], n_best;
   pdl_wait_prerequisites();
   pdl_launch_dependents();
   const int64_t r = blockIdx.x / z.pieces;
   const int piece = static_cast<int>(blockIdx.x % z.pieces);
   if (a.finished && a.finished[r]) return;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) n_found = 0;
+  if (tid < 3) added[tid] = 0;
   if (tid < kMaxTake) group_max[tid] = 0;
   __syncthreads();
   // packs are counted from the 16-byte boundary at or before the row's start
@@ -218,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 4) scan_kernel(BeamSelect a, Pieces 
   const float k = steps(a.tau);
   float m = -INFINITY, sum = 0.f;      // of this thread's elements: sum of 2^((x - m) k)
   uint32_t low = kMinusInf;            // what is found lies above it
-  int before = 0, stage = 0;           // found in earlier tiles
+  int before = 0, stage = 0, turn = 0;   // found in earlier tiles
   for (int from = p0; from < p1; from += kTile) {
     copy_async_wait<kStages - 2>();
     Pack<T, VEC> q[PACKS];
@@ -279,27 +282,27 @@ __global__ void __launch_bounds__(kThreads, 4) scan_kernel(BeamSelect a, Pieces 
         for (int e = 0; e < VEC; ++e) {
           const float x = to_f32(q[i].v[e]);
           if (x > above) {
-            const int n = atomicAdd(&n_found, 1);
+            const int n = before + atomicAdd(&added[turn], 1);
             if (n < kRoom) found[n] = entry_of(order_of(x), v + e);
           }
         }
       }
     }
     __syncthreads();
-    int n = n_found;
+    int n = before + added[turn];
+    if (tid == 0) added[turn == 0 ? 2 : turn - 1] = 0;
+    turn = turn == 2 ? 0 : turn + 1;
     if (n > kRoom) {
       n = keep_best(found, before, a.take);
-      if (tid == 0) n_found = n;
+      if (tid == 0) n_best = n;
       __syncthreads();
-      add_best_of_tile<T, PACKS>(found, &n_found, scratch, row, from, p1, skip, a.V, low, a.take);
-      n = n_found;       // 2 take at most
+      add_best_of_tile<T, PACKS>(found, &n_best, scratch, row, from, p1, skip, a.V, low, a.take);
+      n = n_best;       // 2 take at most
     }
     if (from == p0 || n > 2 * a.take + 16) {
       n = keep_best(found, n, a.take);
       // later elements have higher ids: those equal to the last one kept come behind it
       if (n == a.take) low = static_cast<uint32_t>(found[n - 1] >> 32);
-      if (tid == 0) n_found = n;
-      __syncthreads();
     }
     before = n;
     stage = stage == kStages - 1 ? 0 : stage + 1;

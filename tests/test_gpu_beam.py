@@ -372,3 +372,21 @@ def test_reorder_streams_and_graphs():
     want = state.index_select(1, parents.long())
     graph.replay()
     assert torch.equal(out, want) and torch.equal(state, want)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_select_where_tiles_differ(dtype):
+    """Tiles of a long piece that add nothing, a few, some that are ranked again and more than fit, in
+    turn: what one tile adds is counted before every thread has read the tile before."""
+    R, V, take = 608, 60000, 5
+    gen = torch.Generator("cuda").manual_seed(77)
+    z = logits_of(R, V, dtype, gen, 4)
+    step = torch.arange(V, device="cuda")
+    for r, (width, every) in enumerate(((8192, 2), (8192, 3), (4096, 2), (2048, 5))):
+        rise = (step // width + r) % every == 0          # ascending over these, and none elsewhere
+        z[r::4] = torch.where(rise, step / 512.0, z[r::4].float()).to(dtype)
+    s = -8 * torch.rand(R, generator=gen, device="cuda")
+    first = check(z, s, 4, take)
+    for _ in range(40):
+        for a, b in zip(lm.beam_select(z, s, 4, take), first):
+            assert torch.equal(a, b)
