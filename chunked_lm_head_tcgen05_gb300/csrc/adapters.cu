@@ -39,7 +39,9 @@ constexpr int kBlock = 256;      // columns of the wide side per CTA (widen, out
 constexpr int kPad = 8;          // elements between rows in shared memory: no bank conflicts
 constexpr int kParts = 3;        // bf16 parts of u
 constexpr int kFewAtOnce = 4;    // rows of a run that few_kernel takes
-constexpr int kFewMean = 16;     // rows per adapter, up to which it takes all runs
+constexpr int kFewMean = 8;      // rows per adapter on average, up to which it may multiply
+constexpr int kFewAlone = 128;   // rows up to which nothing else is launched then
+constexpr int kFewRuns = 3;      // its runs per item, up to which it multiplies more rows
 constexpr int kOuterRows = 32;   // rows of a step of outer_kernel
 constexpr int kManyCtas = 608;   // four per SM
 constexpr int kFewCtas = 304;    // two
@@ -61,7 +63,7 @@ struct Item {
 
 struct Plan {
   int* live;         // rows with an adapter
-  int* counts;       // of items and of runs
+  int* counts;       // of items, of runs and, where `choose`, of items that widen_kernel takes
   int32_t* keys;     // [rows] adapters in order
   int32_t* pos;      // [rows] their rows
   int* starts;       // [n + 2] first sorted place of each adapter, of the rows without, and the end
@@ -71,6 +73,7 @@ struct Plan {
   int run_rows;
   int rows;
   int n;
+  bool choose;       // few_kernel (all runs) or widen_kernel (all items), by their numbers
 };
 
 // ------------------------------------------------------------------ matrix instructions
@@ -237,7 +240,12 @@ __global__ void __launch_bounds__(1024) plan_kernel(Plan p, const int32_t* ids) 
     }
     __syncthreads();
   }
-  if (tid < 2) p.counts[tid] = total[tid];
+  if (tid == 0) {
+    const bool few = total[1] <= kFewRuns * total[0];
+    p.counts[0] = total[0];
+    p.counts[1] = p.choose && !few ? 0 : total[1];
+    p.counts[2] = few ? 0 : total[0];
+  }
 }
 
 // ------------------------------------------------------------------ tiles in shared memory
@@ -1046,8 +1054,11 @@ int row_splits_of(int64_t rows, int width, int n) {
   return splits < 1 ? 1 : static_cast<int>(splits);
 }
 
-// Whether few_kernel multiplies: where adapters have few rows on average (64 requests of 16
-// adapters: 40 us a pass, 86 by widen_kernel, which is the faster one for long runs).
+// Whether few_kernel may multiply: where adapters have few rows on average.  Forward passes of
+// rank 16 and 151,936 columns by few_kernel | widen_kernel: 64 rows of 16 adapters 49 | 72 us, 256
+// of 64 127 | 231, 512 of 64 189 | 248, 256 of 16 96 | 90, 1,024 of 64 323 | 288.  If all rows have
+// the same one of them, widen_kernel is faster: 64 rows 34 | 30, 256 86 | 53, 2,048 567 | 231.  So
+// for more than kFewAlone rows the plan chooses and both are launched, one of them without work.
 bool use_few(int64_t rows, int n) { return rows <= int64_t{kFewMean} * n; }
 
 struct Space {
@@ -1173,19 +1184,25 @@ cudaError_t widen(const char* name, const Y* base, int64_t base_ld, Y* out, int6
                      base_ld % VEC == 0 && out_ld % VEC == 0;
   const int sms = sm_count();
   if (sms <= 0) return cudaErrorUnknown;
+  Plan wide = p;
   auto run = [&](auto kt) {
     constexpr int KT = decltype(kt)::value;
-    return packs ? widen_of<Y, KT, true>(base, base_ld, out, out_ld, f, width, rank, u, p, sms, s)
-                 : widen_of<Y, KT, false>(base, base_ld, out, out_ld, f, width, rank, u, p, sms, s);
+    return packs ? widen_of<Y, KT, true>(base, base_ld, out, out_ld, f, width, rank, u, wide, sms, s)
+                 : widen_of<Y, KT, false>(base, base_ld, out, out_ld, f, width, rank, u, wide, sms, s);
   };
-  if (use_few(p.rows, p.n))
-    return traced_launch("adapters_few", s, [&] {
+  if (use_few(p.rows, p.n)) {
+    const cudaError_t e = traced_launch("adapters_few", s, [&] {
       auto kern = packs ? few_kernel<Y, true> : few_kernel<Y, false>;
       const int64_t units = most_items(p.rows, p.n, kFewAtOnce) * ((static_cast<int64_t>(width) - 1) / kFewBlock + 1);
       const int64_t resident = 2 * static_cast<int64_t>(sms);
       return launch_dependent(kern, dim3(static_cast<unsigned>(units < resident ? units : resident)), kThreads, 0, 1, s,
                               base, base_ld, out, out_ld, f, width, rank, u, p, whole_chunks(f, width, width));
     });
+    if (e != cudaSuccess || !p.choose) return e;
+    wide.runs = p.items;
+    wide.run_rows = kRows;
+    wide.counts = p.counts + 1;      // the third of them in the place of the second
+  }
   return traced_launch(name, s, [&] {
     if (rank <= 16) return run(std::integral_constant<int, 1>{});
     if (rank <= 32) return run(std::integral_constant<int, 2>{});
@@ -1237,7 +1254,11 @@ cudaError_t plan_rows(const Adapters& a, int64_t first, Space& z, cudaStream_t s
   const int64_t units = static_cast<int64_t>(a.V > a.H ? a.V : a.H) / kBlock * ((z.plan.rows + kRows - 1) / kRows);
   const int64_t run = units / (7 * kManyCtas);
   z.plan.run_rows = kRows * static_cast<int>(run < 1 ? 1 : run > kMostRun / kRows ? kMostRun / kRows : run);
-  if (use_few(z.plan.rows, a.n)) z.plan.run_rows = kFewAtOnce;
+  z.plan.choose = false;
+  if (use_few(z.plan.rows, a.n)) {
+    z.plan.run_rows = kFewAtOnce;
+    z.plan.choose = z.plan.rows > kFewAlone;
+  }
   const int32_t* const ids = a.ids ? a.ids + first : nullptr;
   const bool small = z.plan.rows <= kSmallRows && a.n + 2 <= kSmallKeys;
   if (!small) {

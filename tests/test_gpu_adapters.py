@@ -292,3 +292,37 @@ def test_streams_and_graphs():
     want = [call() for call in calls]
     for _, out in graphs:
         assert all(torch.equal(a, b) for x, y in zip(out, want) for a, b in zip(x, y))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shares", ["few", "one", "half", "none", "runs"])
+def test_many_adapters_whatever_their_shares(dtype, shares):
+    """Rows of far more adapters than most batches use: the multiplying kernel is chosen by what
+    the batch holds."""
+    for T, n, pad, skip in ((129, 17, 0, 0), (300, 64, 8, 8), (300, 200, 3, 1), (1500, 600, 0, 0)):
+        s = make(T, 96, 520, 12, n, dtype, T + n, pad, skip)
+        if shares == "one":
+            s["of"].fill_(n // 2)
+        elif shares == "half":
+            s["of"][::2] = n - 1
+        elif shares == "none":
+            s["of"][1:] = -1
+        elif shares == "runs":       # four and five rows each, around the bound of both choices
+            s["of"].copy_(torch.arange(T, device="cuda") // 4 % n)
+            s["of"][: T // 2] = torch.arange(T // 2, device="cuda", dtype=torch.int32) // 13 % n
+        args = [s[k] for k in ("x", "down", "up", "of", "scale")]
+        out = lm.adapters_forward(s["base"], *args)
+        check_forward(s, out)
+        bare = s["of"] < 0
+        assert torch.equal(out[bare], s["base"][bare])
+        grads = lm.adapters_backward(s["grad"], *args)
+        check_backward(s, *grads)
+        assert not grads[0][bare].any()
+        assert torch.equal(lm.adapters_forward(s["base"], *args, out=s["base"]), out)
+
+
+def test_more_rows_than_one_sort_of_many_adapters():
+    s = make(131072 + 300, 16, 40, 3, 20000, F32, 11)
+    s["of"][131072:] = 19999
+    args = [s[k] for k in ("x", "down", "up", "of", "scale")]
+    check_forward(s, lm.adapters_forward(s["base"], *args))
