@@ -229,10 +229,20 @@ __global__ void __launch_bounds__(1024) plan_kernel(Plan p, const int32_t* ids) 
       at[l] = total[l] + scan[l] - mine[l];
       for (int w = 0; w < warp; ++w) at[l] += sums[l][w];
     }
-    for (int i = 0; i < mine[0]; ++i)
-      p.items[at[0] + i] = Item{a, first + i * kRows, min(kRows, count - i * kRows), 0};
-    for (int i = 0; i < mine[1]; ++i)
-      p.runs[at[1] + i] = Item{a, first + i * p.run_rows, min(p.run_rows, count - i * p.run_rows), 0};
+#pragma unroll
+    for (int l = 0; l < 2; ++l) {
+      Item* const list = l ? p.runs : p.items;
+      const int each = l ? p.run_rows : kRows;
+      const bool alone = mine[l] <= 4;      // longer ones by the whole warp, one adapter after the other
+      for (int i = 0; alone && i < mine[l]; ++i) list[at[l] + i] = Item{a, first + i * each, min(each, count - i * each), 0};
+      for (uint32_t left = __ballot_sync(0xffffffffu, !alone); left; left &= left - 1) {
+        const int from = __ffs(static_cast<int>(left)) - 1;
+        const int n = __shfl_sync(0xffffffffu, mine[l], from), to = __shfl_sync(0xffffffffu, at[l], from),
+                  f = __shfl_sync(0xffffffffu, first, from), c = __shfl_sync(0xffffffffu, count, from);
+        for (int i = lane; i < n; i += 32)
+          list[to + i] = Item{a - lane + from, f + i * each, min(each, c - i * each), 0};
+      }
+    }
     __syncthreads();
     if (tid == 1023) {
 #pragma unroll
