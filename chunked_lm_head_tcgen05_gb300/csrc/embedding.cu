@@ -396,11 +396,11 @@ cudaError_t launch_sums(const EmbedBwd& a, const Sorted& z, int64_t first, int s
 
 size_t round_up(size_t n) { return (n + 255) / 256 * 256; }
 
-}  // namespace
-
 // Bytes that the SMs beside the sort can write in its time (measured: 10 us for 4,096
 // ids, 37 for 65,536), at some 5 TB/s.
 size_t sort_time_bytes(int n) { return n <= 1024 ? 0 : (size_t{25} << 20) + static_cast<size_t>(n) * 2300; }
+
+}  // namespace
 
 // Count, sorted ids and positions, partial sums of the segments of one sort.
 size_t embed_workspace(int64_t N, int H) {

@@ -627,7 +627,7 @@ lmhead_status lmhead_adapters_bwd(const void* grad_out, int type, int64_t grad_l
  *                be NULL)
  *  out_scores    [R / beams, take] fp32; parents: the candidate's row r (int32); tokens:
  *                its id v (int32)
- *  next_finished [R / beams, take] uint8 or NULL: the parent has ended or v is eos_id
+ *  next_finished [R / beams, take] uint8 or NULL: the parent has ended or v is eos_id.
  *                Where take == beams, out_scores may be scores itself and next_finished
  *                finished; any other overlap of these is LMHEAD_ERR_INVALID_ARG.
  *  lse           [R] fp32 or NULL; +0.0 for finished rows
