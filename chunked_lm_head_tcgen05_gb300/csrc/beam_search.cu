@@ -10,20 +10,20 @@
 //     take * ln(take) of the elements) goes to shared memory and is ranked there.  From
 //     then on only elements above the take-th best so far go there, and are ranked again
 //     when they are many.  When a tile has more than fit (equal or ascending logits), its
-//     take-th largest is found by halving intervals instead.  256 x 151,936 bf16: 27 us, 2.9
+//     take-th largest is found by halving intervals instead.  256 x 151,936 bf16: 25 us, 3.1
 //     TB/s, bound by instructions (12 per element) and the tiles' barriers.
 //  2. best_kernel, one CTA per group, joins the pieces: lse, then the candidates.
 //     An fp32 score with its error bound on either side sorts out most of them;
 //     the rest are compared in 64 bits, where fp32 could confuse two that are
 //     close (and 64-bit arithmetic for all of them would take longer than the
-//     scan: a few operations per clock and SM).  8 us, all of it latency.
+//     scan: a few operations per clock and SM).  7 us, all of it latency.
 // Order among one row's logits is by the logit itself, as an integer that grows
 // with it, then by the id.
 //
 // beam_reorder moves states to the beams that go on: row r takes over row parents[r].  In
 // place a thread (or, for rows off 16-byte boundaries, a CTA) holds one stretch of a group's
 // rows, reads what other rows need and then writes; rows that keep their place cost nothing
-// (393 MB of 16 x 4 beams, half of which move: 67 us, 5.9 TB/s).
+// (393 MB of 16 x 4 beams, half of which move: 62 us, 6.3 TB/s).
 #include <type_traits>
 
 #include "element.cuh"
