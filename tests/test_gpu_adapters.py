@@ -326,3 +326,23 @@ def test_more_rows_than_one_sort_of_many_adapters():
     s["of"][131072:] = 19999
     args = [s[k] for k in ("x", "down", "up", "of", "scale")]
     check_forward(s, lm.adapters_forward(s["base"], *args))
+
+
+def test_a_captured_call_replayed_with_other_rows():
+    """What multiplies is chosen on the device, so that a captured call holds for any ids."""
+    s = make(300, 96, 520, 12, 64, F32, 12)
+    args = [s[k] for k in ("x", "down", "up", "of", "scale")]
+    out = torch.empty_like(s["base"])
+    ws = torch.empty(lm.lmhead_adapters_workspace_size(300, 96, 520, 12, 64), dtype=torch.uint8, device="cuda")
+    lm.adapters_forward(s["base"], *args, out=out, workspace=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lm.adapters_forward(s["base"], *args, out=out, workspace=ws)
+    for ids in (s["of"].clone(), torch.full_like(s["of"], 5), torch.full_like(s["of"], -1),
+                torch.arange(300, device="cuda", dtype=torch.int32) // 9):
+        s["of"].copy_(ids)
+        out.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        check_forward(s, out)
