@@ -27,47 +27,47 @@ _BYTES = {"float32": 4, "bfloat16": 2, "float16": 2}
 def listed():
     return [
         # The next tokens of a small decoding batch.
-        {"name": "embed fwd 16 tokens", "op": "embed_fwd", "tokens": 16, "vocab": 151936,
+        {"name": "embed fwd, 16 tokens", "op": "embed_fwd", "tokens": 16, "vocab": 151936,
          "width": 2560, "dtype": "bfloat16", "scale": 1.0},
         # A training batch of sixteen 4,096-token rows, scaled by the square root of the width.
-        {"name": "embed fwd 65536 tokens", "op": "embed_fwd", "tokens": 65536, "vocab": 151936,
+        {"name": "embed fwd, 65536 tokens", "op": "embed_fwd", "tokens": 65536, "vocab": 151936,
          "width": 2560, "dtype": "bfloat16", "scale": 50.596},
         # The same batch's gradient of a bf16 table: frequent ids hold thousands of tokens.
-        {"name": "embed bwd 65536 tokens", "op": "embed_bwd", "tokens": 65536, "vocab": 151936,
+        {"name": "embed bwd, 65536 tokens", "op": "embed_bwd", "tokens": 65536, "vocab": 151936,
          "width": 2560, "dtype": "bfloat16", "grad_dtype": "bfloat16", "scale": 50.596,
          "padding": True},
         # A packed row of odd length and width, fp32 throughout.
-        {"name": "embed bwd odd fp32", "op": "embed_bwd", "tokens": 5431, "vocab": 50257,
+        {"name": "embed bwd, odd fp32", "op": "embed_bwd", "tokens": 5431, "vocab": 50257,
          "width": 1111, "dtype": "float32", "grad_dtype": "float32", "scale": 1.0,
          "padding": False},
         # One decoding step of 64 requests with 16 adapters on the vocabulary head.
-        {"name": "adapters fwd 64 requests", "op": "adapters_fwd", "rows": 64, "width": 2560,
+        {"name": "adapters fwd, 64 requests", "op": "adapters_fwd", "rows": 64, "width": 2560,
          "vocab": 151936, "rank": 16, "adapters": 16, "bare": 0.1, "runs": False,
          "dtype": "bfloat16"},
         # Four fine-tuned models trained at once on one 2,048-token chunk's logits.
-        {"name": "adapters fwd 2048 rows", "op": "adapters_fwd", "rows": 2048, "width": 2560,
+        {"name": "adapters fwd, 2048 rows", "op": "adapters_fwd", "rows": 2048, "width": 2560,
          "vocab": 151936, "rank": 32, "adapters": 4, "bare": 0.0, "runs": True,
          "dtype": "bfloat16"},
         # The gradients of that chunk.
-        {"name": "adapters bwd 2048 rows", "op": "adapters_bwd", "rows": 2048, "width": 2560,
+        {"name": "adapters bwd, 2048 rows", "op": "adapters_bwd", "rows": 2048, "width": 2560,
          "vocab": 151936, "rank": 32, "adapters": 4, "bare": 0.0, "runs": True,
          "dtype": "bfloat16"},
         # A square projection of ragged size with fp32 cotangents.
-        {"name": "adapters bwd ragged fp32", "op": "adapters_bwd", "rows": 777, "width": 1088,
+        {"name": "adapters bwd, ragged fp32", "op": "adapters_bwd", "rows": 777, "width": 1088,
          "vocab": 2491, "rank": 8, "adapters": 3, "bare": 0.2, "runs": True,
          "dtype": "float32"},
         # One request's step: four beams, twice as many continuations.
-        {"name": "beam select 4 beams", "op": "beam_select", "groups": 1, "beams": 4,
+        {"name": "beam select, 4 beams", "op": "beam_select", "groups": 1, "beams": 4,
          "vocab": 151936, "take": 8, "dtype": "float32", "tau": 1.0, "finished": 0.0},
         # 32 requests of eight beams, a few of which have ended.
-        {"name": "beam select 32 x 8 beams", "op": "beam_select", "groups": 32, "beams": 8,
+        {"name": "beam select, 32 x 8 beams", "op": "beam_select", "groups": 32, "beams": 8,
          "vocab": 151936, "take": 16, "dtype": "bfloat16", "tau": 0.7, "finished": 0.1},
         # One request's cache of a small layer after 300 tokens.
-        {"name": "beam reorder 4 beams", "op": "beam_reorder", "layers": 2, "groups": 1,
+        {"name": "beam reorder, 4 beams", "op": "beam_reorder", "layers": 2, "groups": 1,
          "beams": 4, "heads": 4, "room": 512, "used": 300, "dim": 64, "dtype": "bfloat16",
          "keep": 0.5, "in_place": True},
         # Keys and values of one layer of 16 requests, 1,501 tokens of 2,048 in use.
-        {"name": "beam reorder 16 x 4 beams", "op": "beam_reorder", "layers": 2, "groups": 16,
+        {"name": "beam reorder, 16 x 4 beams", "op": "beam_reorder", "layers": 2, "groups": 16,
          "beams": 4, "heads": 8, "room": 2048, "used": 1501, "dim": 128, "dtype": "bfloat16",
          "keep": 0.5, "in_place": True},
     ]
