@@ -847,6 +847,21 @@ struct OuterShape {
   static constexpr size_t bytes(bool async) { return async ? kStages * stage : stage; }
 };
 
+// One element of dF from whole numbers, for sums that are no finite number: a part of u or of g is not the
+// number itself where the other factor is infinite (it may be 0 or have the other sign, and 0 x inf or
+// inf - inf would make a NaN of an infinity).  Once the sum is NaN it stays so.
+template <typename X>
+__device__ __noinline__ float outer_element(const X* wide, int64_t ld, const bf16* u, int wide_rank, const int32_t* pos,
+                                            int from, int to) {
+  float s = 0.f;
+  for (int r = from; r < to && s == s; ++r) {
+    const bf16* const q = u + static_cast<int64_t>(r) * kParts * wide_rank;
+    const float all = to_f32(q[0]) + (to_f32(q[wide_rank]) + to_f32(q[2 * wide_rank]));
+    s = fmaf(all, to_f32(wide[pos[r] * ld]), s);
+  }
+  return s;
+}
+
 template <typename X, int RT, bool kAsync>
 __global__ void __launch_bounds__(kThreads, kAsync && sizeof(X) == 2 && RT <= 2 ? 3 : 1) outer_kernel(const X* wide, int64_t ld, int width, int rank, const bf16* u,
                                                          Plan p, float* grad, int accumulate, int row_splits,
@@ -1010,7 +1025,10 @@ __global__ void __launch_bounds__(kThreads, kAsync && sizeof(X) == 2 && RT <= 2 
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int c = c0 + warp * 32 + j * 8 + 2 * t + e;
-          if (c < width) dst[c] = accumulate ? dst[c] + acc[m][j][2 * h + e] : acc[m][j][2 * h + e];
+          if (c >= width) continue;
+          float sum = acc[m][j][2 * h + e];
+          if (!isfinite(sum)) sum = outer_element(wide + c, ld, u + r, wide_rank, p.pos, from, to);
+          dst[c] = accumulate ? dst[c] + sum : sum;
         }
     }
 }

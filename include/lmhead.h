@@ -588,8 +588,10 @@ lmhead_status lmhead_embedding_bwd(const void* dy, int dy_type, int64_t dy_ld, c
  *  workspace     lmhead_adapters_workspace_size(T, H, V, rank, n_adapters) bytes, 256-byte
  *                aligned
  * Sums are fp32 in a fixed order (same inputs, same bits); u and du are used with all
- * their bits, in sums for 16-bit results with 16 of them; results are rounded once.  The
- * factors are taken to be finite.  1 <= rank <= 128, n_adapters <= 65535, T < 2^31 - 256,
+ * their bits, in sums for 16-bit results with 16 of them; results are rounded once.
+ * Infinities and NaN in base, x, scale and grad_out go through as in the formulas, so those
+ * of one row change its own results and its adapter's gradients.  The factors are taken to
+ * be finite.  1 <= rank <= 128, n_adapters <= 65535, T < 2^31 - 256,
  * H and V < 2^31 - 1024, and at most 2^31 - 1 tiles of 256 columns and 64 rows of one
  * adapter (LMHEAD_ERR_UNSUPPORTED beyond).  T == 0 is a no-op (the backward still zeroes
  * d_down and d_up unless accumulate is set).
