@@ -92,18 +92,28 @@ __device__ __forceinline__ void load_matrices_turned(uint32_t (&r)[4], const voi
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(smem_addr(p)) : "memory");
 }
 
+// The nearest bf16 number, the largest one for what lies above it (fp32 numbers from 3.396e38 on
+// would become infinite).
+__device__ __forceinline__ float nearest_bf16(float x) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.bf16.f32 %0, %1;" : "=h"(r) : "f"(x));
+  return __uint_as_float(static_cast<uint32_t>(r) << 16);
+}
+
 // x = sum of its parts; the remainder of each rounding is exact.
 template <int N>
 __device__ __forceinline__ void split(float x, float (&part)[N]) {
+  part[0] = nearest_bf16(x);
+  x -= part[0];
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
+  for (int i = 1; i < N; ++i) {
     part[i] = __bfloat162float(__float2bfloat16_rn(x));
     x -= part[i];
   }
-  // an infinity or NaN is in the first part alone
-  if (!isfinite(part[0])) {
+  // an infinity is in the second part, beside the largest number; a NaN in the first two
+  if (N > 2 && !isfinite(part[1])) {
 #pragma unroll
-    for (int i = 1; i < N; ++i) part[i] = 0.f;
+    for (int i = 2; i < N; ++i) part[i] = 0.f;
   }
 }
 

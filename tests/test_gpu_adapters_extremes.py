@@ -1,11 +1,11 @@
-"""Adapters whose operands hold infinities and NaN."""
+"""Adapters whose operands hold infinities, NaN and the largest fp32 numbers."""
 import numpy as np
 import pytest
 import torch
 
 import chunked_lm_head_tcgen05_gb300 as lm
 from gpu_helpers import ensure_built
-from operators_reference import f64
+from operators_reference import U32, f64
 
 pytestmark = pytest.mark.gpu
 F32, BF16, F16 = torch.float32, torch.bfloat16, torch.float16
@@ -111,3 +111,42 @@ def test_infinite_rows_of_x_go_through_as_in_the_formula(T, H, V, rank, n, dtype
         check(s)
         s["grad"][6::29, ::7] = -INF
         check(s)
+
+
+@pytest.mark.parametrize("T", [1, 40, 200])
+@pytest.mark.parametrize("V", [96, 51])
+def test_numbers_next_to_the_largest(T, V):
+    """u and the cotangent above the largest bf16 number, which is not the largest fp32 number."""
+    most = torch.finfo(F32).max
+    s = make(T, 16, V, 4, 1, F32)
+    s["of"].zero_()
+    s["scale"].fill_(1.0)
+    s["x"].zero_()
+    s["x"][:, 0] = torch.finfo(BF16).max
+    s["x"][:, 1] = 1.0e36                    # u = 3.3995e38: bf16 would round it to infinity
+    s["down"].zero_()
+    s["down"][:, :, :2] = 1.0
+    s["down"][:, 1] *= -1.0
+    s["up"].fill_(2.0 ** -20)
+    s["base"].zero_()
+    s["grad"].zero_()
+    s["grad"][:, 0] = most
+    s["grad"][:, 1] = -3.398e38
+    s["up"][:, :, 1] = 2.0 ** -30
+    args = [s[k] for k in ("x", "down", "up", "of", "scale")]
+    u = f64(s["x"]) @ f64(s["down"])[0].T
+    assert (np.abs(u) > torch.finfo(BF16).max).all() and (np.abs(u) < most).all()
+    # u and du: two products of powers of two and one rounding; three parts; sums of four
+    out = f64(lm.adapters_forward(s["base"], *args))
+    want = u @ f64(s["up"])[0]
+    size = np.abs(u) @ np.abs(f64(s["up"])[0])
+    assert (np.abs(out - want) <= 16 * U32 * size).all()
+    dx, d_down, _ = lm.adapters_backward(s["grad"], *args)
+    du = f64(s["grad"]) @ f64(s["up"])[0].T
+    size = np.abs(f64(s["grad"])) @ np.abs(f64(s["up"])[0].T)
+    assert (np.abs(f64(dx) - du @ f64(s["down"])[0]) <= 16 * U32 * size @ np.abs(f64(s["down"])[0])).all()
+    s["x"].fill_(0.0)
+    s["x"][:, 0] = 2.0 ** -12
+    _, d_down, _ = lm.adapters_backward(s["grad"], *args)
+    want = du.T @ f64(s["x"])
+    assert (np.abs(f64(d_down)[0] - want) <= (16 + 2 * T) * U32 * (size.T @ np.abs(f64(s["x"])))).all()
