@@ -1,7 +1,8 @@
 // One step of beam search.  Row r = group * beams + j of the logits belongs to
 // beam j of its group, with score_r so far.  With z = x / tau,
 //   lse_r = log sum_v exp(z_v),   candidate (j, v): score_r + z_v - lse_r,
-// and a group's best `take` candidates go on, ties to the lowest j V + v.
+// and a group's best `take` candidates go on, ties to the lowest j, then to the larger logit,
+// then to the lowest v.
 // HBM-bound: one read of the logits, two kernels.
 //  1. scan_kernel, one CTA per piece of a row, tile by tile with the next one in flight:
 //     maximum and exponential sum of the piece, and its best `take` logits.  In the first
@@ -330,9 +331,13 @@ __global__ void __launch_bounds__(kThreads, 4) scan_kernel(BeamSelect a, Pieces 
 // ------------------------------------------------------------------ the group's best
 enum : uint8_t { kLive, kEnded, kNone };   // a beam; kNone offers nothing
 
+// Different logits may share a 64-bit score (a large temperature or score): one beam's then
+// stay in the order that chose the best of its pieces, so that the pieces do not matter.
 struct Ranked {
   uint64_t score;  // an integer that grows with the 64-bit score (comparing those themselves
-  int64_t at;      // is slow here: 600 candidates took 190 us); j V + v
+                   // is slow here: 600 candidates took 190 us)
+  uint64_t entry;  // entry_of the logit and its id v
+  int64_t beam;    // j
 };
 
 __device__ __forceinline__ uint64_t order_of(double x) {
@@ -344,7 +349,8 @@ __device__ __forceinline__ double from_order(uint64_t k) {
 }
 
 __device__ __forceinline__ bool ahead(const Ranked& x, const Ranked& y) {
-  return x.score > y.score || (x.score == y.score && x.at < y.at);
+  return x.score > y.score ||
+         (x.score == y.score && (x.beam < y.beam || (x.beam == y.beam && x.entry > y.entry)));
 }
 
 // inv = 1 / tau, formed by the host: a 64-bit division by every thread here takes 4 us.
@@ -435,8 +441,9 @@ __global__ void __launch_bounds__(kBestThreads) best_kernel(BeamSelect a, Pieces
   };
   auto exact = [&](int j, uint32_t order, int v) {
     const double x = static_cast<double>(from_order(order)) - static_cast<double>(tops[j]);
-    return Ranked{order_of(bias[j] + x * inv), static_cast<int64_t>(j) * a.V + v};
+    return Ranked{order_of(bias[j] + x * inv), entry_of(order, v), j};
   };
+  auto end_of = [&](int j) { return Ranked{order_of(bias[j]), entry_of(0, a.eos), j}; };   // its one candidate
   float low = -INFINITY;
   each([&](int j, uint32_t order, int) {
     float err;
@@ -464,11 +471,11 @@ __global__ void __launch_bounds__(kBestThreads) best_kernel(BeamSelect a, Pieces
   });
   if (tid < a.beams && kind[tid] == kEnded) {
     const int n = atomicAdd(&n_found, 1);
-    if (n < kRoom) found[n] = Ranked{order_of(bias[tid]), static_cast<int64_t>(tid) * a.V + a.eos};
+    if (n < kRoom) found[n] = end_of(tid);
   }
   __syncthreads();
   auto put = [&](int n, const Ranked& x) {
-    const int j = static_cast<int>(x.at / a.V), v = static_cast<int>(x.at % a.V);
+    const int j = static_cast<int>(x.beam), v = static_cast<int>(~static_cast<uint32_t>(x.entry));
     const int64_t o = g * a.take + n;
     a.out_scores[o] = static_cast<float>(from_order(x.score));
     a.parents[o] = static_cast<int32_t>(r0 + j);
@@ -486,20 +493,21 @@ __global__ void __launch_bounds__(kBestThreads) best_kernel(BeamSelect a, Pieces
   } else {
     // more than fit (equal scores): one after the other, the first behind the last one put
     n = a.take;
-    if (tid == 0) last = Ranked{~uint64_t{0}, -1};
+    if (tid == 0) last = Ranked{~uint64_t{0}, 0, -1};
     for (int t = 0; t < a.take; ++t) {
       __syncthreads();
       const Ranked before = last;
-      Ranked mine{0, INT64_MAX};
+      Ranked mine{0, 0, INT64_MAX};
       auto offer = [&](const Ranked& x) {
         if (ahead(before, x) && ahead(x, mine)) mine = x;
       };
       each([&](int j, uint32_t order, int v) { offer(exact(j, order, v)); });
       if (tid < a.beams && kind[tid] == kEnded)
-        offer(Ranked{order_of(bias[tid]), static_cast<int64_t>(tid) * a.V + a.eos});
+        offer(end_of(tid));
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
-        const Ranked x{__shfl_xor_sync(0xffffffffu, mine.score, o), __shfl_xor_sync(0xffffffffu, mine.at, o)};
+        const Ranked x{__shfl_xor_sync(0xffffffffu, mine.score, o), __shfl_xor_sync(0xffffffffu, mine.entry, o),
+                       __shfl_xor_sync(0xffffffffu, mine.beam, o)};
         if (ahead(x, mine)) mine = x;
       }
       if (lane == 0) warp_best[warp] = mine;
