@@ -6,6 +6,8 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
+#include <numeric>
 
 #include "operators.h"
 
@@ -88,6 +90,42 @@ lmhead_status check_process(const ProcessLogits& a) {
   if (!aligned_to(a.logits, a.type) || !aligned_to(a.out, a.type)) return LMHEAD_ERR_UNSUPPORTED;
   if (clash(a.logits, a.ld, a.out, a.out_ld, a.R)) return LMHEAD_ERR_INVALID_ARG;
   return LMHEAD_OK;
+}
+
+// An operand: `rows` rows of `width` bytes, ld bytes apart.
+struct Rows {
+  const void* p;
+  int64_t rows, ld, width;
+};
+Rows matrix(const void* p, int type, int64_t rows, int64_t ld, int64_t cols) {
+  const int64_t size = static_cast<int64_t>(element_bytes(type));
+  return Rows{p, rows, ld > INT64_MAX / size ? INT64_MAX : ld * size, cols * size};
+}
+Rows block(const void* p, size_t bytes) { return Rows{p, 1, 0, static_cast<int64_t>(bytes)}; }
+
+// Whether two operands share a byte; NULL shares none.  Columns of one tensor beside each
+// other do not: their rows' starts keep their distance, modulo the strides' common divisor,
+// outside both widths.  (Strides that differ may be found to share where they only might.)
+bool share(const Rows& a, const Rows& b) {
+  if (!a.p || !b.p || a.rows <= 0 || b.rows <= 0 || a.width <= 0 || b.width <= 0) return false;
+  using Wide = __int128;      // a stride may be anything
+  const Wide p = reinterpret_cast<uintptr_t>(a.p), q = reinterpret_cast<uintptr_t>(b.p);
+  if (p >= q + Wide{b.rows - 1} * b.ld + b.width || q >= p + Wide{a.rows - 1} * a.ld + a.width) return false;
+  const int64_t step = std::gcd(a.rows > 1 ? a.ld : 0, b.rows > 1 ? b.ld : 0);
+  if (step == 0) return true;      // a row each
+  const Wide rest = (q - p) % step, d = rest < 0 ? rest + step : rest;
+  return d < a.width || d + b.width > step;
+}
+
+// Whether what a call writes shares no byte with what it reads, nor with another of its results.
+bool disjoint(std::initializer_list<Rows> written, std::initializer_list<Rows> read) {
+  for (const Rows* w = written.begin(); w != written.end(); ++w) {
+    for (const Rows* other = written.begin(); other != w; ++other)
+      if (share(*w, *other)) return false;
+    for (const Rows& r : read)
+      if (share(*w, r)) return false;
+  }
+  return true;
 }
 
 // Arguments that both directions of the embedding share; `in` and `out` are its matrices.
@@ -331,8 +369,10 @@ lmhead_status lmhead_embedding_fwd(const int32_t* ids, int64_t N, const void* we
   if (rc != LMHEAD_OK) return rc;
   if (y_type != type && !(type == kF32 && y_type == kBF16) && y_type != kF32) return LMHEAD_ERR_UNSUPPORTED;
   if (N == 0) return LMHEAD_OK;
-  if (!ids || !weight || !y || weight == y) return LMHEAD_ERR_INVALID_ARG;
+  if (!ids || !weight || !y) return LMHEAD_ERR_INVALID_ARG;
   if (!aligned_to(weight, type) || !aligned_to(y, y_type) || !aligned_to(ids, kF32)) return LMHEAD_ERR_UNSUPPORTED;
+  if (!disjoint({matrix(y, y_type, N, y_ld, H)}, {matrix(weight, type, V, w_ld, H), matrix(ids, kF32, 1, 0, N)}))
+    return LMHEAD_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const EmbedFwd a{ids, N, weight, type, w_ld, V, H, scale, y, y_type, y_ld};
   return status_of(traced_launch("embedding_fwd", s, [&] { return launch_embed_fwd(a, s); }));
@@ -360,10 +400,14 @@ lmhead_status lmhead_embedding_bwd(const void* dy, int dy_type, int64_t dy_ld, c
     const size_t bytes = element_bytes(d_weight_type) * static_cast<size_t>(V) * static_cast<size_t>(H);
     return status_of(cudaMemsetAsync(d_weight, 0, bytes, s));
   }
-  if (!dy || !ids || !workspace || dy == d_weight) return LMHEAD_ERR_INVALID_ARG;
+  if (!dy || !ids || !workspace) return LMHEAD_ERR_INVALID_ARG;
   if (!aligned_to(dy, dy_type) || !aligned_to(ids, kF32) || (reinterpret_cast<uintptr_t>(workspace) & 255))
     return LMHEAD_ERR_UNSUPPORTED;
-  if (workspace_bytes < embed_workspace(N, H)) return LMHEAD_ERR_WORKSPACE_TOO_SMALL;
+  const size_t needed = embed_workspace(N, H);
+  if (workspace_bytes < needed) return LMHEAD_ERR_WORKSPACE_TOO_SMALL;
+  if (!disjoint({matrix(d_weight, d_weight_type, V, H, H), block(workspace, needed)},
+             {matrix(dy, dy_type, N, dy_ld, H), matrix(ids, kF32, 1, 0, N)}))
+    return LMHEAD_ERR_INVALID_ARG;
   const EmbedBwd a{dy, dy_type, dy_ld, ids, N, V, H, scale, skip, d_weight, d_weight_type,
                    accumulate ? 1 : 0, workspace};
   return status_of(launch_embed_bwd(a, s));

@@ -533,7 +533,7 @@ lmhead_status lmhead_process_logits_bwd(const void* grad_out, int64_t grad_ld, c
  *                row of NaN and takes no part in the gradient.
  *  weight        [V, H] of `type`, rows w_ld elements apart
  *  y             [N, H], rows y_ld apart: of the table's type, or bf16 for an fp32 table,
- *                or fp32 for a 16-bit one (an fp32 residual stream); not over weight
+ *                or fp32 for a 16-bit one (an fp32 residual stream)
  *  scale         finite; products are formed in fp32 and rounded once
  *  dy            [N, H] of dy_type, rows dy_ld apart
  *  padding_id    tokens with this id (after wrapping) take no part in the gradient;
@@ -544,6 +544,8 @@ lmhead_status lmhead_process_logits_bwd(const void* grad_out, int64_t grad_ld, c
  *                LMHEAD_BF16, each sum rounded once, without accumulate and for
  *                N <= 131072 (LMHEAD_ERR_UNSUPPORTED otherwise)
  *  workspace     lmhead_embedding_workspace_size(N, H) bytes, 256-byte aligned
+ * y, d_weight and the workspace must not share memory with what the call reads, nor with one
+ * another (LMHEAD_ERR_INVALID_ARG); columns of one tensor beside each other do not.
  * The gradient sums an id's tokens in fp32 in a fixed order: same inputs, same bits.
  * H <= 2^20, N < 2^31 - 256 and V < 2^31 - 1024 (LMHEAD_ERR_UNSUPPORTED beyond).
  * N == 0 is a no-op (the backward still zeroes d_weight unless accumulate is set).
