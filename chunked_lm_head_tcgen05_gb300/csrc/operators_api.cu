@@ -157,6 +157,16 @@ lmhead_status check_adapter_operands(const Adapters& a, size_t workspace_bytes) 
   return workspace_bytes < adapters_workspace(a.T, a.H, a.V, a.rank, a.n) ? LMHEAD_ERR_WORKSPACE_TOO_SMALL : LMHEAD_OK;
 }
 
+// Whether results (NULL: not asked for), the workspace and `shared`, a further input, lie apart from
+// each other and from what both directions read.
+bool adapters_disjoint(const Adapters& a, const Rows& shared, const Rows& first, const Rows& second, const Rows& third) {
+  const int64_t factor_rows = int64_t{a.n} * a.rank;
+  return disjoint({first, second, third, block(a.workspace, adapters_workspace(a.T, a.H, a.V, a.rank, a.n))},
+                  {shared, matrix(a.x, kBF16, a.T, a.x_ld, a.H), matrix(a.down, kBF16, factor_rows, a.H, a.H),
+                   matrix(a.up, kBF16, factor_rows, a.V, a.V), matrix(a.ids, kF32, 1, 0, a.T),
+                   matrix(a.scale, kF32, 1, 0, a.n)});
+}
+
 constexpr int32_t kMaxBeamVocab = 1 << 30;   // columns of the pieces past a row's end are counted too
 
 // Whether n bytes at p and m bytes at q share any; NULL shares none.
@@ -431,9 +441,13 @@ lmhead_status lmhead_adapters_fwd(const void* base, int type, int64_t base_ld, c
   if (T == 0) return LMHEAD_OK;
   if (!base || !out) return LMHEAD_ERR_INVALID_ARG;
   if (!aligned_to(base, type) || !aligned_to(out, type)) return LMHEAD_ERR_UNSUPPORTED;
-  if (clash(base, base_ld, out, out_ld, T) || out == x || out == down || out == up) return LMHEAD_ERR_INVALID_ARG;
+  if (clash(base, base_ld, out, out_ld, T)) return LMHEAD_ERR_INVALID_ARG;
   rc = check_adapter_operands(a, workspace_bytes);
   if (rc != LMHEAD_OK) return rc;
+  const Rows in_place{nullptr, 0, 0, 0};
+  if (!adapters_disjoint(a, base == out ? in_place : matrix(base, type, T, base_ld, V), matrix(out, type, T, out_ld, V),
+                         in_place, in_place))
+    return LMHEAD_ERR_INVALID_ARG;
   const AdaptersFwd f{a, base, type, base_ld, out, out_ld};
   return status_of(launch_adapters_fwd(f, reinterpret_cast<cudaStream_t>(stream)));
 }
@@ -463,11 +477,12 @@ lmhead_status lmhead_adapters_bwd(const void* grad_out, int type, int64_t grad_l
   }
   if (!grad_out || (!dx && !d_down && !d_up)) return LMHEAD_ERR_INVALID_ARG;
   if (!aligned_to(grad_out, type)) return LMHEAD_ERR_UNSUPPORTED;
-  for (const void* p : {static_cast<const void*>(dx), static_cast<const void*>(d_down), static_cast<const void*>(d_up)})
-    if (p && (p == grad_out || p == x || p == down || p == up)) return LMHEAD_ERR_INVALID_ARG;
-  if ((d_down && d_down == d_up) || (dx && (dx == d_down || dx == d_up))) return LMHEAD_ERR_INVALID_ARG;
   rc = check_adapter_operands(a, workspace_bytes);
   if (rc != LMHEAD_OK) return rc;
+  const int64_t factor_rows = int64_t{n_adapters} * rank;
+  if (!adapters_disjoint(a, matrix(grad_out, type, T, grad_ld, V), matrix(dx, kF32, T, dx_ld, H),
+                         matrix(d_down, kF32, factor_rows, H, H), matrix(d_up, kF32, factor_rows, V, V)))
+    return LMHEAD_ERR_INVALID_ARG;
   const AdaptersBwd b{a, grad_out, type, grad_ld, dx, dx_ld, accumulate_dx ? 1 : 0, d_down, d_up, accumulate ? 1 : 0};
   return status_of(launch_adapters_bwd(b, s));
 }

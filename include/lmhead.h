@@ -589,6 +589,9 @@ lmhead_status lmhead_embedding_bwd(const void* dy, int dy_type, int64_t dy_ld, c
  *                without rows get zeros), or added to when accumulate != 0
  *  workspace     lmhead_adapters_workspace_size(T, H, V, rank, n_adapters) bytes, 256-byte
  *                aligned
+ * Results and the workspace must not share memory with what the call reads (but for out over
+ * base), nor with one another (LMHEAD_ERR_INVALID_ARG); columns of one tensor beside each
+ * other do not.
  * Sums are fp32 in a fixed order (same inputs, same bits); u and du are used with all
  * their bits, in sums for 16-bit results with 16 of them; results are rounded once.
  * Infinities and NaN in base, x, scale and grad_out go through as in the formulas, so those

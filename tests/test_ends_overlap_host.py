@@ -40,3 +40,30 @@ def test_embedding(lib):  # noqa: F811
         dict(d_weight=at(1)), dict(dy=P(3 * M + 256)), dict(dy=P(3 * M + 25600 - 2)), dict(d_weight=P(2 * M + 28)),
         dict(workspace=at(1)), dict(workspace=at(2)), dict(workspace=P(3 * M + 25600 - 256 * 4)),
         dict(d_type=1, d_weight=P(M + 1022))])
+
+
+# x [8, 64] bf16: 1,024 bytes; down [3, 4, 64]: 1,536; up [3, 4, 100]: 2,400; base and cotangent
+# [8, 100] bf16: 1,600; dx [8, 64] fp32: 2,048; d_down 3,072, d_up 4,800
+ADAPTERS_FWD = dict(base=at(1), type=1, base_ld=100, x=at(2), x_ld=64, down=at(3), up=at(4), ids=at(5), scale=at(6),
+                    T=8, H=64, V=100, rank=4, n=3, out=at(7), out_ld=100, workspace=at(8), bytes=1 << 19, stream=None)
+ADAPTERS_BWD = dict(grad=at(1), type=1, ld=100, x=at(2), x_ld=64, down=at(3), up=at(4), ids=at(5), scale=at(6), T=8,
+                    H=64, V=100, rank=4, n=3, dx=at(7), dx_ld=64, accumulate_dx=0, d_down=at(8), d_up=at(9),
+                    accumulate=0, workspace=at(10), bytes=1 << 19, stream=None)
+
+
+def test_adapters(lib):  # noqa: F811
+    inside = [P(2 * M + 1022), P(3 * M + 512), P(3 * M + 1534), P(4 * M + 2398), P(5 * M + 30), P(6 * M + 10)]
+    before = [P(n * M - 1598) for n in (2, 3, 4, 5, 6)]
+    refused(lib, "lmhead_adapters_fwd", ADAPTERS_FWD, [dict(out=p) for p in inside + before] + [
+        dict(out=P(M + 200)), dict(out=P(M - 200)), dict(out=P(M + 1598)), dict(out=P(M + 2), T=1),
+        # rows of one tensor whose columns meet
+        dict(base_ld=256, out_ld=256, out=P(M + 198)), dict(base_ld=256, out_ld=256, out=P(M + 314)),
+        dict(base_ld=256, out_ld=256, out=P(M - 198)),
+        dict(workspace=at(1)), dict(workspace=at(2)), dict(workspace=at(3)), dict(workspace=at(4)),
+        dict(workspace=at(5)), dict(workspace=at(6)), dict(workspace=at(7)), dict(base=at(8), out=at(8))])
+    results = [P(M + 1596), P(2 * M + 1020), P(3 * M + 4), P(4 * M + 2396), P(5 * M + 28), P(6 * M + 8)]
+    refused(lib, "lmhead_adapters_bwd", ADAPTERS_BWD,
+            [{name: p} for name in ("dx", "d_down", "d_up") for p in results] + [
+        dict(dx=P(8 * M + 3068)), dict(dx=P(9 * M + 4796)), dict(d_up=P(8 * M + 3068)), dict(d_down=P(9 * M - 3068)),
+        dict(dx=P(8 * M - 2044)), dict(dx_ld=512, d_down=P(7 * M + 256 - 4)), dict(d_up=None, dx=P(8 * M + 4)),
+        dict(dx=at(10)), dict(workspace=at(7)), dict(workspace=at(8)), dict(workspace=at(9)), dict(workspace=at(1))])

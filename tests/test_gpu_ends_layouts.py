@@ -46,3 +46,35 @@ def test_embedding_gradient_end_to_end_with_its_cotangent(dtype):
         lm.embedding_backward(flat[:N * H].view(N, H), ids, V, d_weight=flat[(N - 1) * H:(N - 1 + V) * H].view(V, H))
     with pytest.raises(lm.LmheadError):
         lm.embedding_forward(ids[:5], flat[:V * H].view(V, H), out=flat[H:6 * H].view(5, H))
+
+
+@pytest.mark.parametrize("V", [128, 51])
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+def test_adapters_beside_their_base(V, dtype):
+    g = torch.Generator("cuda").manual_seed(V)
+    T, H, rank, n = 70, 40, 5, 3
+    both = torch.randn(T, 2 * V, generator=g, device="cuda").to(dtype)
+    x = torch.randn(T, H, generator=g, device="cuda").to(BF16)
+    down, up = (torch.randn(n, rank, w, generator=g, device="cuda").to(BF16) for w in (H, V))
+    of = torch.randint(-1, n, (T,), generator=g, device="cuda", dtype=torch.int32)
+    before = both.clone()
+    for base, out in ((both[:, :V], both[:, V:]), (both[:, V:], both[:, :V])):
+        want = lm.adapters_forward(base.contiguous(), x, down, up, of)
+        kept = base.clone()
+        assert lm.adapters_forward(base, x, down, up, of, out=out) is out
+        assert torch.equal(out, want) and torch.equal(base, kept)
+        both.copy_(before)
+    with pytest.raises(lm.LmheadError):
+        lm.adapters_forward(both[:-1, :V], x[:-1], down, up, of[:-1], out=both[1:, :V])
+    # every gradient and the cotangent end to end
+    flat = torch.zeros(T * V + T * H + n * rank * (H + V), device="cuda")
+    grad, dx, d_down, d_up = (t.view(s) for t, s in zip(flat.split([T * V, T * H, n * rank * H, n * rank * V]),
+                                                      ((T, V), (T, H), (n, rank, H), (n, rank, V))))
+    grad.copy_(torch.randn(T, V, generator=g, device="cuda"))
+    want = lm.adapters_backward(grad.clone(), x, down, up, of)
+    lm.adapters_backward(grad, x, down, up, of, dx=dx, d_down=d_down, d_up=d_up)
+    assert torch.equal(dx, want[0]) and torch.equal(d_down, want[1]) and torch.equal(d_up, want[2])
+    # dx beside another matrix
+    wide = torch.zeros(T, 2 * H, device="cuda")
+    lm.adapters_backward(grad, x, down, up, of, dx=wide[:, H:])
+    assert torch.equal(wide[:, H:], want[0]) and not wide[:, :H].any()
