@@ -169,12 +169,6 @@ bool adapters_disjoint(const Adapters& a, const Rows& shared, const Rows& first,
 
 constexpr int32_t kMaxBeamVocab = 1 << 30;   // columns of the pieces past a row's end are counted too
 
-// Whether n bytes at p and m bytes at q share any; NULL shares none.
-bool overlap(const void* p, size_t n, const void* q, size_t m) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  return p && q && a < b + m && b < a + n;
-}
-
 // A strided block of bytes: up to three dimensions of `inner` contiguous bytes.
 struct Block {
   int64_t size[3], stride[3], inner;
@@ -512,10 +506,16 @@ lmhead_status lmhead_beam_select(const void* logits, int type, int64_t ld, int64
   // one group's results may lie over its own inputs, which it has read by then, not over another's
   const size_t rows = static_cast<size_t>(R), results = rows / beams * take;
   const bool own = take == beams;
-  if ((overlap(scores, 4 * rows, out_scores, 4 * results) && !(own && scores == out_scores)) ||
-      (overlap(finished, rows, next_finished, results) && !(own && finished == next_finished)))
+  const Rows old_scores = block(own && scores == out_scores ? nullptr : scores, 4 * rows),
+             old_finished = block(own && finished == next_finished ? nullptr : finished, rows),
+             new_scores = block(out_scores, 4 * results), new_finished = block(next_finished, results);
+  if (!disjoint({new_scores}, {old_scores}) || !disjoint({new_finished}, {old_finished})) return LMHEAD_ERR_INVALID_ARG;
+  const size_t needed = beam_workspace(R, V, take);
+  if (workspace_bytes < needed) return LMHEAD_ERR_WORKSPACE_TOO_SMALL;
+  if (!disjoint({new_scores, new_finished, block(parents, 4 * results), block(tokens, 4 * results), block(lse, 4 * rows),
+                 block(workspace, needed)},
+                {matrix(logits, type, R, ld, V), old_scores, old_finished}))
     return LMHEAD_ERR_INVALID_ARG;
-  if (workspace_bytes < beam_workspace(R, V, take)) return LMHEAD_ERR_WORKSPACE_TOO_SMALL;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const BeamSelect a{logits, type, ld, R, V, beams, take, scores, finished, eos_id, temperature,
                      out_scores, parents, tokens, next_finished, lse, workspace};

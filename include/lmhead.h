@@ -641,7 +641,8 @@ lmhead_status lmhead_adapters_bwd(const void* grad_out, int type, int64_t grad_l
  *                its id v (int32)
  *  next_finished [R / beams, take] uint8 or NULL: the parent has ended or v is eos_id.
  *                Where take == beams, out_scores may be scores itself and next_finished
- *                finished; any other overlap of these is LMHEAD_ERR_INVALID_ARG.
+ *                finished; any other overlap of a result or the workspace with another or
+ *                with what the call reads is LMHEAD_ERR_INVALID_ARG.
  *  lse           [R] fp32 or NULL; +0.0 for finished rows
  * -inf logits (masks) are no candidates; a row without a finite logit has lse = -inf, a
  * NaN or +inf logit makes the row's lse NaN, and a row whose lse or score is not finite

@@ -67,3 +67,19 @@ def test_adapters(lib):  # noqa: F811
         dict(dx=P(8 * M + 3068)), dict(dx=P(9 * M + 4796)), dict(d_up=P(8 * M + 3068)), dict(d_down=P(9 * M - 3068)),
         dict(dx=P(8 * M - 2044)), dict(dx_ld=512, d_down=P(7 * M + 256 - 4)), dict(d_up=None, dx=P(8 * M + 4)),
         dict(dx=at(10)), dict(workspace=at(7)), dict(workspace=at(8)), dict(workspace=at(9)), dict(workspace=at(1))])
+
+
+# eight rows [8, 100] fp32: 3,200 bytes; scores and lse 32, finished 8; two groups of 4: 32 a result
+SELECT = dict(logits=at(1), type=0, ld=100, R=8, V=100, beams=4, take=4, scores=at(2), finished=at(3), eos=2, tau=1.0,
+              out=at(4), parents=at(5), tokens=at(6), next=at(7), lse=at(8), workspace=at(9), bytes=1 << 19, stream=None)
+
+
+def test_selection(lib):  # noqa: F811
+    inputs = [P(M + 3196), P(M + 400), P(2 * M + 4), P(3 * M + 4), P(M - 28)]
+    refused(lib, "lmhead_beam_select", SELECT,
+            [{name: p} for name in ("out", "parents", "tokens", "lse") for p in inputs] + [
+        dict(parents=at(2)), dict(tokens=at(2)), dict(lse=at(2)), dict(next=at(2)), dict(next=P(M + 7)),
+        dict(lse=at(4)), dict(parents=at(4)), dict(tokens=at(5)), dict(tokens=P(5 * M + 28)), dict(next=P(4 * M + 31)),
+        dict(next=P(8 * M + 3)), dict(lse=at(2), out=at(2)), dict(parents=at(2), out=at(2)),
+        dict(ld=200, out=P(M + 384)), dict(workspace=at(1)), dict(workspace=at(2)), dict(workspace=at(8)),
+        dict(workspace=at(3)), dict(workspace=at(7))])

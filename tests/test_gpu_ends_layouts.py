@@ -78,3 +78,27 @@ def test_adapters_beside_their_base(V, dtype):
     wide = torch.zeros(T, 2 * H, device="cuda")
     lm.adapters_backward(grad, x, down, up, of, dx=wide[:, H:])
     assert torch.equal(wide[:, H:], want[0]) and not wide[:, :H].any()
+
+
+def test_selection_out_of_one_buffer():
+    """Results end to end, scores and flags in place, and scores kept behind each row of logits."""
+    g = torch.Generator("cuda").manual_seed(9)
+    wide = torch.randn(8, 1000 + 8, generator=g, device="cuda")
+    z = wide[:, :1000]
+    s = -torch.rand(8, generator=g, device="cuda")
+    f = torch.tensor([0, 1, 0, 0, 0, 0, 1, 0], dtype=torch.uint8, device="cuda")
+    nxt = torch.empty(2, 4, dtype=torch.uint8, device="cuda")
+    want = lm.beam_select(z, s, 4, 4, 1.0, f, 5, nxt)
+    flat = torch.zeros(32, device="cuda")
+    mine, lse = flat[:8], flat[24:]
+    mine.copy_(s)
+    p, t = (flat[8 * i:8 * i + 8].view(torch.int32).view(2, 4) for i in (1, 2))
+    ws = torch.empty(lm.lmhead_beam_workspace_size(8, 1000, 4), dtype=torch.uint8, device="cuda")
+    assert lm.lmhead_beam_select(z, 4, 4, mine, f, 5, 1.0, mine.view(2, 4), p, t, f.view(2, 4), lse, ws) == 0
+    for a, b in zip((mine.view(2, 4), p, t, lse, f.view(2, 4)), (*want, nxt)):
+        assert torch.equal(a, b)
+    # a result in the columns behind the logits
+    out = wide[0, 1000:].view(2, 4)
+    f.copy_(torch.tensor([0, 1, 0, 0, 0, 0, 1, 0]))
+    assert lm.lmhead_beam_select(z, 4, 4, s, f, 5, 1.0, out, p, t, None, None, ws) == 0
+    assert torch.equal(out, want[0])
