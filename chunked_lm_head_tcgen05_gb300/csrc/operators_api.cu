@@ -553,6 +553,8 @@ lmhead_status lmhead_beam_reorder(const void* src, int64_t src_outer, int64_t sr
     if (src_rows > 0 && p < q + static_cast<uintptr_t>(to_bytes) && q < p + static_cast<uintptr_t>(from_bytes))
       return LMHEAD_ERR_INVALID_ARG;
   }
+  if (!disjoint({block(dst, static_cast<size_t>(to_bytes))}, {block(parents, 4 * static_cast<size_t>(rows))}))
+    return LMHEAD_ERR_INVALID_ARG;
   if (!aligned_to(parents, kF32)) return LMHEAD_ERR_UNSUPPORTED;
   const BeamReorder a{static_cast<const char*>(src), static_cast<char*>(dst), parents, rows, src_rows, beams,
                       outer, mid, inner_bytes, src_outer, src_row, src_mid, dst_outer, dst_row, dst_mid,

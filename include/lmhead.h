@@ -674,7 +674,8 @@ lmhead_status lmhead_beam_select(const void* logits, int type, int64_t ld, int64
  *                groups of `beams` (1 to 64, a divisor of rows), and a parent outside its
  *                own group leaves the row as it is.  Rows that keep their place are neither
  *                read nor written.
- * dst's rows must not overlap one another.  beams is not looked at where src != dst, nor
+ * dst's rows must not overlap one another, nor dst's extent the parents
+ * (LMHEAD_ERR_INVALID_ARG).  beams is not looked at where src != dst, nor
  * clear_missing in place.
  */
 lmhead_status lmhead_beam_reorder(const void* src, int64_t src_outer, int64_t src_row,

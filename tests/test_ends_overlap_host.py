@@ -83,3 +83,15 @@ def test_selection(lib):  # noqa: F811
         dict(next=P(8 * M + 3)), dict(lse=at(2), out=at(2)), dict(parents=at(2), out=at(2)),
         dict(ld=200, out=P(M + 384)), dict(workspace=at(1)), dict(workspace=at(2)), dict(workspace=at(8)),
         dict(workspace=at(3)), dict(workspace=at(7))])
+
+
+# two times eight rows of two stretches of 320 bytes
+REORDER = dict(src=at(1), so=8 * 640, sr=640, sm=320, src_rows=8, dst=at(2), do=8 * 640, dr=640, dm=320, parents=at(3),
+               rows=8, beams=4, outer=2, mid=2, inner=320, clear=0, stream=None)
+
+
+def test_reorder(lib):  # noqa: F811
+    cases = [dict(parents=at(2)), dict(parents=P(2 * M - 28)), dict(parents=P(2 * M + 16 * 640 - 4)),
+             dict(parents=P(2 * M + 5000))]
+    refused(lib, "lmhead_beam_reorder", REORDER, cases)
+    refused(lib, "lmhead_beam_reorder", dict(REORDER, src=at(2)), cases)     # in place
