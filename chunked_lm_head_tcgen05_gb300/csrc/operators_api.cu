@@ -531,7 +531,7 @@ lmhead_status lmhead_beam_reorder(const void* src, int64_t src_outer, int64_t sr
   if (rows < 0 || src_rows < 0 || outer < 0 || mid < 0 || inner_bytes < 0) return LMHEAD_ERR_INVALID_ARG;
   if (rows >= kMaxRows || src_rows >= kMaxRows) return LMHEAD_ERR_UNSUPPORTED;
   if (rows == 0 || outer == 0 || mid == 0 || inner_bytes == 0) return LMHEAD_OK;
-  if (!src || !dst || !parents) return LMHEAD_ERR_INVALID_ARG;
+  if ((!src && src_rows > 0) || !dst || !parents) return LMHEAD_ERR_INVALID_ARG;   // no rows may have no address
   // strides of dimensions of size 1 say nothing
   if (outer == 1) src_outer = dst_outer = 0;
   if (mid == 1) src_mid = dst_mid = 0;

@@ -669,7 +669,8 @@ lmhead_status lmhead_beam_select(const void* logits, int type, int64_t ld, int64
  * of size 1 are not looked at.
  *  src != dst    src has src_rows rows and does not overlap dst (LMHEAD_ERR_INVALID_ARG
  *                where their extents do); a parent outside [0, src_rows) (-1) leaves the
- *                row of dst as it is, or clears it to zero bytes where clear_missing != 0
+ *                row of dst as it is, or clears it to zero bytes where clear_missing != 0;
+ *                without rows src may be NULL
  *  src == dst    in place, with the same strides and src_rows == rows: rows are taken in
  *                groups of `beams` (1 to 64, a divisor of rows), and a parent outside its
  *                own group leaves the row as it is.  Rows that keep their place are neither

@@ -102,3 +102,15 @@ def test_selection_out_of_one_buffer():
     f.copy_(torch.tensor([0, 1, 0, 0, 0, 0, 1, 0]))
     assert lm.lmhead_beam_select(z, 4, 4, s, f, 5, 1.0, out, p, t, None, None, ws) == 0
     assert torch.equal(out, want[0])
+
+
+def test_reorder_of_a_state_without_rows():
+    parents = torch.tensor([-1, 0, -1], dtype=torch.int32, device="cuda")
+    for shape, dim in (((0, 5), 0), ((2, 0, 3, 4), 1), ((2, 0, 3, 7), 1)):
+        state = torch.empty(shape, device="cuda")
+        full = [*shape]
+        full[dim] = 3
+        got = lm.beam_reorder(state, parents, dim)
+        assert got.shape == tuple(full) and not got.any()
+        kept = torch.ones(full, device="cuda")
+        assert lm.beam_reorder(state, parents, dim, kept) is kept and (kept == 1).all()
