@@ -1399,12 +1399,18 @@ def beam_reorder(state, parents, dim=0, out=None, beams=0, stream=None):
     return out
 
 
-def _adapters_workspace(x, up):
+def _adapters_bytes(x, up):
+    """Of a workspace; sizes that have none are refused as the calls refuse them."""
+    T, H = x.shape
     n, rank, V = up.shape
-    size = lmhead_adapters_workspace_size(*x.shape, V, rank, n)
+    size = lmhead_adapters_workspace_size(T, H, V, rank, n)
     if size == 0:
-        raise LmheadError(2 if rank > 128 or n > 65535 else 1, "lmhead_adapters_workspace_size")
-    return _torch.empty(size, dtype=_torch.uint8, device=x.device)
+        raise LmheadError(2 if min(H, V, rank, n) > 0 else 1, "lmhead_adapters_workspace_size")
+    return size
+
+
+def _adapters_workspace(x, up):
+    return _torch.empty(_adapters_bytes(x, up), dtype=_torch.uint8, device=x.device)
 
 
 def adapters_forward(base, x, down, up, adapter_ids=None, scale=None, out=None, workspace=None,

@@ -26,12 +26,12 @@ import torch
 from . import LMHEAD_OP_BWD, LMHEAD_OP_FWD, LmheadError, adapters_forward, \
     distill_logits_backward, \
     distill_logits_forward, embedding_backward, embedding_forward, layernorm_backward, \
-    layernorm_forward, lmhead_adapters_bwd, lmhead_adapters_workspace_size, lmhead_distill_bwd, \
+    layernorm_forward, lmhead_adapters_bwd, lmhead_distill_bwd, \
     lmhead_distill_narrow_dweight, lmhead_distill_fwd, lmhead_distill_workspace_size, \
     lmhead_embedding_workspace_size, \
     lmhead_layernorm_workspace_size, \
     lmhead_logps_bwd, lmhead_logps_fwd, lmhead_workspace_size, process_logits_backward
-from . import _check_padding
+from . import _adapters_bytes, _check_padding
 from . import process_logits as _process_logits
 
 # (device index, stream handle) -> uint8 workspace, grown on demand.  Work on one
@@ -435,14 +435,6 @@ class Adapters(torch.autograd.Function):
             if rc:
                 raise LmheadError(rc, "lmhead_adapters_bwd")
         return (g if need[0] else None, *grads, None, None)
-
-
-def _adapters_bytes(x, up):
-    n, rank, V = up.shape
-    size = lmhead_adapters_workspace_size(*x.shape, V, rank, n)
-    if size == 0:
-        raise LmheadError(1, "lmhead_adapters_workspace_size")
-    return size
 
 
 def adapters(base, x, down, up, adapter_ids=None, scale=None):
