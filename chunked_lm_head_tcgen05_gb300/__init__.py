@@ -288,6 +288,14 @@ def _check_workspace(ws):
         raise ValueError("workspace must be a contiguous CUDA tensor")
 
 
+_WIDEST = 2 ** 31 - 1   # what the C ABI's int32_t sizes hold; ctypes would cut a larger one
+
+
+def _check_widths(*sizes):
+    if max(sizes) > _WIDEST:
+        raise LmheadError(2, "a size of %d" % max(sizes))
+
+
 def _check_rows(t, name, shape, dtypes=None):
     """A CUDA matrix whose rows are contiguous but may lie further apart than their
     length; returns (element type, elements between rows)."""
@@ -304,6 +312,8 @@ def _check_rows(t, name, shape, dtypes=None):
     if t.shape != shape:
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
     rows, cols = shape
+    if cols > _WIDEST:
+        _check_widths(cols)
     ld, step = t.stride()
     if rows <= 1:
         ld = max(cols, ld)
@@ -778,6 +788,7 @@ def lmhead_process_logits_bwd(grad_out, logits, tokens, spans, repetition, allow
 
 @functools.lru_cache(maxsize=128)
 def lmhead_embedding_workspace_size(N, H):
+    _check_widths(H)
     return int(library().lmhead_embedding_workspace_size(N, H))
 
 
@@ -805,6 +816,7 @@ def _embedding_fwd(ids, weight, scale, y, out_dtype, stream):
     """y None: a new one."""
     N = _check_ids(ids)
     V, H = weight.shape
+    _check_widths(V)
     kind, w_ld = _check_rows(weight, "weight", (V, H))
     if y is None:
         dtype = weight.dtype if out_dtype is None else out_dtype
@@ -831,6 +843,7 @@ def lmhead_embedding_bwd(dy, ids, scale, padding_id, d_weight, accumulate, works
     status code."""
     N = _check_ids(ids)
     V, H = d_weight.shape
+    _check_widths(V)
     kind, ld = _check_rows(dy, "dy", (N, H))
     torch = _torch
     narrow = d_weight.dtype is torch.bfloat16
@@ -846,6 +859,7 @@ def lmhead_embedding_bwd(dy, ids, scale, padding_id, d_weight, accumulate, works
 
 @functools.lru_cache(maxsize=128)
 def lmhead_adapters_workspace_size(T, H, V, rank, n_adapters):
+    _check_widths(H, V, rank, n_adapters)
     return int(library().lmhead_adapters_workspace_size(T, H, V, rank, n_adapters))
 
 
@@ -857,6 +871,7 @@ def _check_adapters(x, down, up, adapter_ids, scale):
     T, H = x.shape
     _, x_ld = _check_rows(x, "x", (T, H), (torch.bfloat16,))
     n, rank, V = up.shape
+    _check_widths(n, rank)
     _check_tensor(down, "down", torch.bfloat16, (n, rank, H))
     _check_tensor(up, "up", torch.bfloat16, (n, rank, V))
     _check_tensor(adapter_ids, "adapter_ids", torch.int32, (T,), allow_none=True)
@@ -895,6 +910,7 @@ def lmhead_adapters_bwd(grad_out, x, down, up, adapter_ids, scale, dx, accumulat
 
 @functools.lru_cache(maxsize=128)
 def lmhead_beam_workspace_size(R, V, take):
+    _check_widths(V, take)
     return int(library().lmhead_beam_workspace_size(R, V, take))
 
 
@@ -910,6 +926,7 @@ def _beam_select(logits, beams, take, scores, finished, eos_id, temperature, out
     if beams <= 0 or R % beams:
         raise ValueError("logits must have the rows of whole groups of beams: got %d rows of %d "
                          "beams" % (R, beams))
+    _check_widths(beams, take)
     if not -1 <= eos_id < V:
         raise ValueError("eos_id %d is no id of a vocabulary of %d" % (eos_id, V))
     shape = (R // beams, take)
