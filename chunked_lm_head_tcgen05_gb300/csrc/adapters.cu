@@ -1129,13 +1129,13 @@ Space lay_out(void* workspace, int64_t T, int H, int V, int rank, int n) {
   const size_t wide_rank = static_cast<size_t>(round_rank(rank));
   s.u = reinterpret_cast<bf16*>(take(2 * kParts * wide_rank * rows));
   s.du = reinterpret_cast<bf16*>(take(2 * kParts * wide_rank * rows));
-  // (a last part of fewer rows has more splits: those of at most kRows kFewCtas rows in all)
+  // a last part of fewer rows has more splits of the wide side (those of at most kRows kFewCtas
+  // rows in all) and no more of its rows
   size_t most = 0, narrow = 0;
   for (const int width : {H, V}) {
     int per;
     narrow += wide_rank * rows * static_cast<size_t>(splits_of(rows > 0 ? rows : 1, width, n, per));
-    // row splits fill kFewCtas blocks at most, whatever the rows
-    const int splits = row_splits_of(kSortMost, width, n);
+    const int splits = row_splits_of(rows, width, n);
     const size_t outer = splits > 1 ? static_cast<size_t>(splits) * n * rank * width : 0;
     most = narrow > most ? narrow : most;
     most = outer > most ? outer : most;

@@ -71,3 +71,15 @@ def test_sizes_past_32_bits(lib):  # noqa: F811
         with pytest.raises(lm.LmheadError) as e:
             call()
         assert e.value.status == 2, i
+
+
+def test_few_rows_need_a_small_workspace(lib):  # noqa: F811
+    """Sums of row splits, which only a gradient over many rows has, are not asked for."""
+    size = lm.lmhead_adapters_workspace_size
+    for T, n in ((1, 1), (16, 1), (64, 16), (200, 4)):
+        for H, V, rank in ((2560, 2560, 128), (64, 2560, 16), (2560, 10240, 64)):
+            r = -(-rank // 16) * 16
+            # places and lists of every row and adapter; u and du in three bf16 parts, and their sums of
+            # at most one per 512 columns
+            most = T * (8 + 32 + 2 * 6 * r + 4 * r * (-(-H // 512) + -(-V // 512))) + 36 * n + 64 + 10 * 256
+            assert size(T, H, V, rank, n) <= most, (T, H, V, rank, n, size(T, H, V, rank, n), most)
