@@ -24,6 +24,8 @@ constexpr int kSumThreads = 128;
 constexpr int kLong = 32;       // sorted tokens per segment
 constexpr int kShort = 8;       // of fewer than kFew tokens
 constexpr int kFew = 8192;
+constexpr int kFewIds = 1024;   // that one CTA sorts
+constexpr size_t kSmallTable = size_t{256} << 20;
 constexpr int kFillRows = 16;   // table rows per CTA that writes zeros
 constexpr int kJoinThreads = 256;
 constexpr int kJoinColumns = 128;
@@ -396,9 +398,17 @@ cudaError_t launch_sums(const EmbedBwd& a, const Sorted& z, int64_t first, int s
 
 size_t round_up(size_t n) { return (n + 255) / 256 * 256; }
 
-// Bytes that the SMs beside the sort can write in its time (measured: 10 us for 4,096
-// ids, 37 for 65,536), at some 5 TB/s.
-size_t sort_time_bytes(int n) { return n <= 1024 ? 0 : (size_t{25} << 20) + static_cast<size_t>(n) * 2300; }
+// Bytes of zeros that the SMs beside the sort write meanwhile, at some 5 TB/s.  That is a
+// little more than the sort's own time (12 us for 4,096 ids, 30 for 65,536; with these zeros
+// 39), which costs nothing as the sums would wait for HBM as well: 65,536 x 2,560 bf16 take
+// 207 us in all so, 208 with a third less, 219 without any beside the sort.
+size_t sort_time_bytes(int n) { return n <= kFewIds ? 0 : (size_t{25} << 20) + static_cast<size_t>(n) * 2300; }
+
+// Whether everything is cleared beside the sort, also the few rows that are written again: a
+// table of this size by one CTA's worth of ids.  1,024 tokens, all beside | by the summing
+// launch: 50,257 x 512 bf16 (51 MB) 22 | 32 us, 50,257 x 1,111 fp32 (223 MB) 51 | 56,
+// 151,936 x 2,560 bf16 (778 MB) 133 | 129, fp32 254 | 233; 4,096 tokens of the last 362 | 239.
+bool all_beside(int n, int V, size_t bytes) { return n <= kFewIds && n <= V / 32 && bytes <= kSmallTable; }
 
 }  // namespace
 
@@ -456,8 +466,7 @@ cudaError_t launch_embed_bwd(const EmbedBwd& call, cudaStream_t s) {
     const size_t row = (a.d_type == kF32 ? 4 : 2) * static_cast<size_t>(a.H);
     const bool beside = !a.accumulate && reinterpret_cast<uintptr_t>(a.d_weight) % 16 == 0;
     size_t rows = beside ? sort_time_bytes(n) / row / kFillRows * kFillRows : 0;
-    // few tokens: everything, since hardly a row is written twice
-    if (beside && n <= a.V / 32) rows = a.V;
+    if (beside && all_beside(n, a.V, row * static_cast<size_t>(a.V))) rows = a.V;
     if (rows > static_cast<size_t>(a.V)) rows = a.V / kFillRows * kFillRows;
     if (rows * row % 16) rows = rows / kFillRows * kFillRows;
     z.filled = static_cast<int>(rows);
