@@ -863,11 +863,20 @@ struct OuterShape {
 template <typename X>
 __device__ __noinline__ float outer_element(const X* wide, int64_t ld, const bf16* u, int wide_rank, const int32_t* pos,
                                             int from, int to) {
+  constexpr int kAtOnce = 4;      // more would make the kernels spill
   float s = 0.f;
-  for (int r = from; r < to && s == s; ++r) {
-    const bf16* const q = u + static_cast<int64_t>(r) * kParts * wide_rank;
-    const float all = to_f32(q[0]) + (to_f32(q[wide_rank]) + to_f32(q[2 * wide_rank]));
-    s = fmaf(all, to_f32(wide[pos[r] * ld]), s);
+  for (int r0 = from; r0 < to && s == s; r0 += kAtOnce) {
+    float all[kAtOnce], g[kAtOnce];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int r = min(r0 + i, to - 1);
+      const bf16* const q = u + static_cast<int64_t>(r) * kParts * wide_rank;
+      all[i] = to_f32(q[0]) + (to_f32(q[wide_rank]) + to_f32(q[2 * wide_rank]));
+      g[i] = to_f32(wide[pos[r] * ld]);
+    }
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i)
+      if (r0 + i < to) s = fmaf(all[i], g[i], s);
   }
   return s;
 }
