@@ -816,7 +816,8 @@ def _embedding_fwd(ids, weight, scale, y, out_dtype, stream):
     """y None: a new one."""
     N = _check_ids(ids)
     V, H = weight.shape
-    _check_widths(V)
+    if V > _WIDEST:
+        _check_widths(V)
     kind, w_ld = _check_rows(weight, "weight", (V, H))
     if y is None:
         dtype = weight.dtype if out_dtype is None else out_dtype
@@ -843,7 +844,8 @@ def lmhead_embedding_bwd(dy, ids, scale, padding_id, d_weight, accumulate, works
     status code."""
     N = _check_ids(ids)
     V, H = d_weight.shape
-    _check_widths(V)
+    if V > _WIDEST:
+        _check_widths(V)
     kind, ld = _check_rows(dy, "dy", (N, H))
     torch = _torch
     narrow = d_weight.dtype is torch.bfloat16
@@ -871,7 +873,8 @@ def _check_adapters(x, down, up, adapter_ids, scale):
     T, H = x.shape
     _, x_ld = _check_rows(x, "x", (T, H), (torch.bfloat16,))
     n, rank, V = up.shape
-    _check_widths(n, rank)
+    if n > _WIDEST or rank > _WIDEST:
+        _check_widths(n, rank)
     _check_tensor(down, "down", torch.bfloat16, (n, rank, H))
     _check_tensor(up, "up", torch.bfloat16, (n, rank, V))
     _check_tensor(adapter_ids, "adapter_ids", torch.int32, (T,), allow_none=True)
@@ -926,7 +929,8 @@ def _beam_select(logits, beams, take, scores, finished, eos_id, temperature, out
     if beams <= 0 or R % beams:
         raise ValueError("logits must have the rows of whole groups of beams: got %d rows of %d "
                          "beams" % (R, beams))
-    _check_widths(beams, take)
+    if beams > _WIDEST or take > _WIDEST:
+        _check_widths(beams, take)
     if not -1 <= eos_id < V:
         raise ValueError("eos_id %d is no id of a vocabulary of %d" % (eos_id, V))
     shape = (R // beams, take)

@@ -92,29 +92,39 @@ lmhead_status check_process(const ProcessLogits& a) {
   return LMHEAD_OK;
 }
 
-// An operand: `rows` rows of `width` bytes, ld bytes apart.
+// An operand: `rows` rows of `width` bytes, ld bytes apart, from `from` to `to`; empty where
+// there is none of it.
 struct Rows {
-  const void* p;
+  uintptr_t from, to;
   int64_t rows, ld, width;
 };
 Rows matrix(const void* p, int type, int64_t rows, int64_t ld, int64_t cols) {
-  const int64_t size = static_cast<int64_t>(element_bytes(type));
-  return Rows{p, rows, ld > INT64_MAX / size ? INT64_MAX : ld * size, cols * size};
+  const int64_t size = static_cast<int64_t>(element_bytes(type)), width = cols * size;
+  const uintptr_t from = reinterpret_cast<uintptr_t>(p);
+  if (!p || rows <= 0 || width <= 0) return Rows{from, from, 0, 0, 0};
+  int64_t stride, last;      // a stride may be anything
+  if (__builtin_mul_overflow(ld, size, &stride)) stride = INT64_MAX;
+  if (__builtin_mul_overflow(rows - 1, stride, &last)) last = INT64_MAX;
+  uintptr_t to;
+  if (__builtin_add_overflow(from, static_cast<uintptr_t>(last) + static_cast<uintptr_t>(width), &to)) to = UINTPTR_MAX;
+  return Rows{from, to, rows, stride, width};
 }
-Rows block(const void* p, size_t bytes) { return Rows{p, 1, 0, static_cast<int64_t>(bytes)}; }
+Rows block(const void* p, size_t bytes) {
+  const uintptr_t from = reinterpret_cast<uintptr_t>(p);
+  return Rows{from, p ? from + bytes : from, 1, 0, static_cast<int64_t>(bytes)};
+}
 
-// Whether two operands share a byte; NULL shares none.  Columns of one tensor beside each
-// other do not: their rows' starts keep their distance, modulo the strides' common divisor,
-// outside both widths.  (Strides that differ may be found to share where they only might.)
+// Whether two operands share a byte.  Columns of one tensor beside each other do not: their
+// rows' starts keep their distance, modulo the strides' common divisor, outside both widths.
+// (Strides that differ may be found to share where they only might.)
 bool share(const Rows& a, const Rows& b) {
-  if (!a.p || !b.p || a.rows <= 0 || b.rows <= 0 || a.width <= 0 || b.width <= 0) return false;
-  using Wide = __int128;      // a stride may be anything
-  const Wide p = reinterpret_cast<uintptr_t>(a.p), q = reinterpret_cast<uintptr_t>(b.p);
-  if (p >= q + Wide{b.rows - 1} * b.ld + b.width || q >= p + Wide{a.rows - 1} * a.ld + a.width) return false;
+  if (a.from >= b.to || b.from >= a.to || a.from == a.to || b.from == b.to) return false;
   const int64_t step = std::gcd(a.rows > 1 ? a.ld : 0, b.rows > 1 ? b.ld : 0);
   if (step == 0) return true;      // a row each
-  const Wide rest = (q - p) % step, d = rest < 0 ? rest + step : rest;
-  return d < a.width || d + b.width > step;
+  int64_t d = b.from >= a.from ? static_cast<int64_t>((b.from - a.from) % static_cast<uintptr_t>(step))
+                               : -static_cast<int64_t>((a.from - b.from) % static_cast<uintptr_t>(step));
+  if (d < 0) d += step;
+  return d < a.width || d > step - b.width;
 }
 
 // Whether what a call writes shares no byte with what it reads, nor with another of its results.
@@ -148,21 +158,22 @@ lmhead_status check_adapters(const Adapters& a, int type, int64_t ld) {
   return LMHEAD_OK;
 }
 
-lmhead_status check_adapter_operands(const Adapters& a, size_t workspace_bytes) {
+lmhead_status check_adapter_operands(const Adapters& a, size_t workspace_bytes, size_t needed) {
   if (!a.x || !a.down || !a.up || !a.workspace) return LMHEAD_ERR_INVALID_ARG;
   for (const void* p : {a.x, a.down, a.up})
     if (!aligned_to(p, kBF16)) return LMHEAD_ERR_UNSUPPORTED;
   if (!aligned_to(a.ids, kF32) || !aligned_to(a.scale, kF32) || (reinterpret_cast<uintptr_t>(a.workspace) & 255))
     return LMHEAD_ERR_UNSUPPORTED;
-  return workspace_bytes < adapters_workspace(a.T, a.H, a.V, a.rank, a.n) ? LMHEAD_ERR_WORKSPACE_TOO_SMALL : LMHEAD_OK;
+  return workspace_bytes < needed ? LMHEAD_ERR_WORKSPACE_TOO_SMALL : LMHEAD_OK;
 }
 
-// Whether results (NULL: not asked for), the workspace and `shared`, a further input, lie apart from
-// each other and from what both directions read.
-bool adapters_disjoint(const Adapters& a, const Rows& shared, const Rows& first, const Rows& second, const Rows& third) {
+// Whether the workspace and the results (NULL: not asked for) lie apart from each other and from
+// what a call reads: `own`, and what both directions do.
+bool adapters_disjoint(const Adapters& a, size_t needed, const Rows& own, const Rows& first, const Rows& second,
+                       const Rows& third) {
   const int64_t factor_rows = int64_t{a.n} * a.rank;
-  return disjoint({first, second, third, block(a.workspace, adapters_workspace(a.T, a.H, a.V, a.rank, a.n))},
-                  {shared, matrix(a.x, kBF16, a.T, a.x_ld, a.H), matrix(a.down, kBF16, factor_rows, a.H, a.H),
+  return disjoint({first, second, third, block(a.workspace, needed)},
+                  {own, matrix(a.x, kBF16, a.T, a.x_ld, a.H), matrix(a.down, kBF16, factor_rows, a.H, a.H),
                    matrix(a.up, kBF16, factor_rows, a.V, a.V), matrix(a.ids, kF32, 1, 0, a.T),
                    matrix(a.scale, kF32, 1, 0, a.n)});
 }
@@ -436,11 +447,12 @@ lmhead_status lmhead_adapters_fwd(const void* base, int type, int64_t base_ld, c
   if (!base || !out) return LMHEAD_ERR_INVALID_ARG;
   if (!aligned_to(base, type) || !aligned_to(out, type)) return LMHEAD_ERR_UNSUPPORTED;
   if (clash(base, base_ld, out, out_ld, T)) return LMHEAD_ERR_INVALID_ARG;
-  rc = check_adapter_operands(a, workspace_bytes);
+  const size_t needed = adapters_workspace(T, H, V, rank, n_adapters);
+  rc = check_adapter_operands(a, workspace_bytes, needed);
   if (rc != LMHEAD_OK) return rc;
-  const Rows in_place{nullptr, 0, 0, 0};
-  if (!adapters_disjoint(a, base == out ? in_place : matrix(base, type, T, base_ld, V), matrix(out, type, T, out_ld, V),
-                         in_place, in_place))
+  const Rows none = block(nullptr, 0);
+  if (!adapters_disjoint(a, needed, base == out ? none : matrix(base, type, T, base_ld, V),
+                         matrix(out, type, T, out_ld, V), none, none))
     return LMHEAD_ERR_INVALID_ARG;
   const AdaptersFwd f{a, base, type, base_ld, out, out_ld};
   return status_of(launch_adapters_fwd(f, reinterpret_cast<cudaStream_t>(stream)));
@@ -471,10 +483,11 @@ lmhead_status lmhead_adapters_bwd(const void* grad_out, int type, int64_t grad_l
   }
   if (!grad_out || (!dx && !d_down && !d_up)) return LMHEAD_ERR_INVALID_ARG;
   if (!aligned_to(grad_out, type)) return LMHEAD_ERR_UNSUPPORTED;
-  rc = check_adapter_operands(a, workspace_bytes);
+  const size_t needed = adapters_workspace(T, H, V, rank, n_adapters);
+  rc = check_adapter_operands(a, workspace_bytes, needed);
   if (rc != LMHEAD_OK) return rc;
   const int64_t factor_rows = int64_t{n_adapters} * rank;
-  if (!adapters_disjoint(a, matrix(grad_out, type, T, grad_ld, V), matrix(dx, kF32, T, dx_ld, H),
+  if (!adapters_disjoint(a, needed, matrix(grad_out, type, T, grad_ld, V), matrix(dx, kF32, T, dx_ld, H),
                          matrix(d_down, kF32, factor_rows, H, H), matrix(d_up, kF32, factor_rows, V, V)))
     return LMHEAD_ERR_INVALID_ARG;
   const AdaptersBwd b{a, grad_out, type, grad_ld, dx, dx_ld, accumulate_dx ? 1 : 0, d_down, d_up, accumulate ? 1 : 0};
