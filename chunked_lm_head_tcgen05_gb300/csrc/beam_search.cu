@@ -263,7 +263,9 @@ __global__ void __launch_bounds__(kThreads, 4) scan_kernel(BeamSelect a, Pieces 
     const float above = from_order(low);
     const float to = fmaxf(m, top), base = to == -INFINITY ? 0.f : to;
     const float shrink = ex2_approx((m - base) * k);
-    float2 sums = make_float2(sum * shrink, 0.f);
+    // a tile's sum starts from zero: equal terms added to one long sum would all be rounded the
+    // same way (1,000 rows of 151,936 equal logits below one: lse off by 1.6e-5)
+    float2 sums = make_float2(0.f, 0.f);
     m = to;
     const float2 down = make_float2(-base, -base), kk = make_float2(k, k);
 #pragma unroll
@@ -273,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 4) scan_kernel(BeamSelect a, Pieces 
         const float2 d = mul2(add2(pair_of(q[i], e), down), kk);
         sums = add2(sums, make_float2(ex2_approx(d.x), ex2_approx(d.y)));
       }
-    sum = sums.x + sums.y;
+    sum = sum * shrink + (sums.x + sums.y);
     if (top > above) {
 #pragma unroll
       for (int i = 0; i < PACKS; ++i) {

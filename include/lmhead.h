@@ -629,10 +629,10 @@ lmhead_status lmhead_adapters_bwd(const void* grad_out, int type, int64_t grad_l
  * and each group gets the `take` best of its beams * V candidates in falling order.  Scores
  * are compared in 64 bits, ties go to the lowest j, then to the larger logit (two logits may
  * share a score at a large temperature), then to the lowest v.  lse comes from fp32
- * exponentials and sums (as a rule within 1e-7, always within 1e-5 of the real one): it does
- * not touch the order within a beam, but candidates of different beams that are closer than
- * that may change places, those of equal rows too where the rows start at different
- * distances from a 16-byte boundary.
+ * exponentials and sums (as a rule within 1e-7 of the real one, within 1e-5 for V up to
+ * 2^20): it does not touch the order within a beam, but candidates of different beams that
+ * are closer than that may change places, those of equal rows too where the rows start at
+ * different distances from a 16-byte boundary.
  *  finished      [R] uint8 or NULL: nonzero for a sequence that has ended.  Its logits are
  *                not read; its one candidate is the id eos_id with its score unchanged.
  *  eos_id        the id that ends a sequence, in [0, V); -1 for none (then finished must
