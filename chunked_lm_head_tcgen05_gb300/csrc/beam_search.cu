@@ -12,7 +12,9 @@
 //     then on only elements above the take-th best so far go there, and are ranked again
 //     when they are many.  When a tile has more than fit (equal or ascending logits), its
 //     take-th largest is found by halving intervals instead.  256 x 151,936 bf16: 25 us, 3.1
-//     TB/s, bound by instructions (12 per element) and the tiles' barriers.
+//     TB/s.  Some 12 us of that are instructions (12 per element); the rest is the tiles'
+//     barriers and waits, which the three CTAs that fit on an SM (59,008 bytes of shared
+//     memory each) do not cover, and the last CTAs of two waves.
 //  2. best_kernel, one CTA per group, joins the pieces: lse, then the candidates.
 //     An fp32 score with its error bound on either side sorts out most of them;
 //     the rest are compared in 64 bits, where fp32 could confuse two that are
@@ -41,7 +43,7 @@ template <typename T>
 constexpr int kManyElements = 64 / static_cast<int>(sizeof(T));
 constexpr int kFewElements = 8;      // of few rows: pieces of one tile of 2,048
 constexpr int64_t kManyTiles = 304;  // the long tiles from which on they fill the GPU
-constexpr int64_t kManyPieces = 608; // CTAs that many rows are cut into
+constexpr int64_t kManyPieces = 608; // CTAs that many rows are cut into, at most (456 are resident)
 constexpr int kRoom = 1024;          // elements ranked in shared memory
 constexpr int kBestThreads = 512;
 constexpr int kBestWarps = kBestThreads / 32;
@@ -172,6 +174,8 @@ __device__ __forceinline__ float largest(const Pack<T, VEC>& q) {
   }
 }
 
+// 64 registers, though shared memory holds three CTAs of the long tiles, not four: the fp32
+// form spills 40 bytes for it.
 template <typename T, int ELEMS>
 __global__ void __launch_bounds__(kThreads, 4) scan_kernel(BeamSelect a, Pieces z, int groups) {
   constexpr int VEC = kVec<T>, PACKS = ELEMS / VEC, kStages = kStagesOf<ELEMS>;
@@ -350,9 +354,11 @@ __device__ __forceinline__ double from_order(uint64_t k) {
   return __longlong_as_double(static_cast<int64_t>(k >> 63 ? k ^ (uint64_t{1} << 63) : ~k));
 }
 
+__device__ __forceinline__ bool first_of_equals(const Ranked& x, const Ranked& y) {
+  return x.beam < y.beam || (x.beam == y.beam && x.entry > y.entry);
+}
 __device__ __forceinline__ bool ahead(const Ranked& x, const Ranked& y) {
-  return x.score > y.score ||
-         (x.score == y.score && (x.beam < y.beam || (x.beam == y.beam && x.entry > y.entry)));
+  return x.score > y.score || (x.score == y.score && first_of_equals(x, y));
 }
 
 // inv = 1 / tau, formed by the host: a 64-bit division by every thread here takes 4 us.
@@ -488,8 +494,15 @@ __global__ void __launch_bounds__(kBestThreads) best_kernel(BeamSelect a, Pieces
   if (n <= kRoom) {
     for (int i = tid; i < n; i += kBestThreads) {
       const Ranked me = found[i];
-      int rank = 0;
-      for (int j = 0; j < n; ++j) rank += ahead(found[j], me);
+      int rank = 0, equals = 0;
+#pragma unroll 8
+      for (int j = 0; j < n; ++j) {
+        const uint64_t s = found[j].score;
+        rank += s > me.score;
+        equals += s == me.score;
+      }
+      if (equals > 1)
+        for (int j = 0; j < n; ++j) rank += found[j].score == me.score && first_of_equals(found[j], me);
       if (rank < a.take) put(rank, me);
     }
   } else {
@@ -740,7 +753,7 @@ Pieces plan(int64_t R, int V, int& elements) {
   elements = R * tiles(kManyElements<T>) >= kManyTiles ? kManyElements<T> : kFewElements;
   int64_t pieces = tiles(elements);
   if (elements != kFewElements) {
-    const int64_t most = R < kManyPieces ? kManyPieces / R : 1;    // no second wave of CTAs
+    const int64_t most = R < kManyPieces ? kManyPieces / R : 1;
     pieces = pieces < most ? pieces : most;
   }
   Pieces z{};
