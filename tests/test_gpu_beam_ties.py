@@ -67,3 +67,17 @@ def test_large_scores_and_subnormal_temperatures_keep_the_order_of_the_logits():
     _, parents, tokens, _ = lm.beam_select(z, torch.zeros(8, device="cuda"), 1, 4, 1e-40)
     for r in range(8):
         assert tokens[r].tolist() == best(z[r], 4).tolist()
+
+
+@pytest.mark.parametrize("G,K,V,take", [(1, 64, 50257, 128), (3, 64, 4100, 64), (2, 16, 30011, 128), (1, 3, 151936, 100),
+                                        (1, 1, 2048, 128), (5, 61, 9000, 127)])
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+def test_many_continuations_of_many_beams(G, K, V, take, dtype):
+    from test_gpu_beam import check, logits_of
+    gen = torch.Generator("cuda").manual_seed(K + take)
+    z = logits_of(G * K, V, dtype, gen)
+    s = -torch.rand(G * K, generator=gen, device="cuda")
+    check(z, s, K, take)
+    f = (torch.rand(G * K, generator=gen, device="cuda") < 0.5).to(torch.uint8)
+    check(z, s, K, take, 0.7, f, 3)
+    check(z, torch.where(f != 0, -float("inf"), s), K, take)
