@@ -1392,7 +1392,7 @@ def beam_select(logits, scores, beams, take=None, temperature=1.0, finished=None
                 next_finished=None, workspace=None, stream=None):
     """The `take` (default: beams) best continuations of each group of `beams` rows of logits [R, V],
     whose sequences have scores [R].  Returns (scores, parents, tokens), each [R / beams, take], and
-    lse [R]; next_finished, if given, is filled beside them."""
+    lse [R]; next_finished, if given, is filled beside them (finished and next_finished: uint8)."""
     if stream is not None:
         return _made_on(stream, logits, beam_select, logits, scores, beams, take, temperature,
                         finished, eos_id, next_finished, workspace)

@@ -15,8 +15,9 @@
 // Rows are first sorted by adapter (sort_ids.cu) and cut into items of up to kRows
 // rows of one adapter (plan_kernel), so requests with the same adapter share its
 // factors, whatever their order.  Rows without an adapter come last.
-// Matrix instructions take bf16 (mma.sync: at these ranks tensor throughput is not
-// the bound, and fragments go straight to and from rows that lie apart).  Values
+// Matrix instructions take bf16 (mma.sync: at these ranks tensor throughput does not
+// bind the forward, and fragments go straight to and from rows that lie apart; the
+// two products with a cotangent keep the tensor pipe 27% and 53% busy).  Values
 // with more bits -- u, fp32 and fp16 cotangents -- enter as sums of up to three
 // bf16 parts, which together hold the 24 bits of fp32; products of parts whose
 // result lies below 2^-24 of the whole are left out.  16-bit results take two
@@ -1103,8 +1104,11 @@ int row_splits_of(int64_t rows, int width, int n) {
 
 // Whether few_kernel may multiply: where adapters have few rows on average.  Forward passes of
 // rank 16 and 151,936 columns by few_kernel | widen_kernel: 64 rows of 16 adapters 49 | 72 us, 256
-// of 64 127 | 231, 512 of 64 189 | 248, 256 of 16 96 | 90, 1,024 of 64 323 | 288.  If all rows have
-// the same one of them, widen_kernel is faster: 64 rows 34 | 30, 256 86 | 53, 2,048 567 | 231.  So
+// of 64 127 | 231, 512 of 64 189 | 248, 256 of 16 96 | 90, 1,024 of 64 323 | 288.  At 10,240 columns
+// 64 of 16 20 | 22, 256 of 64 28 | 35, 512 of 64 32 | 37, 1,024 of 64 45 | 41, 2,048 of 512 105 | 160; at
+// 4,096 22 | 20, 24 | 26, 24 | 27, 32 | 30, 72 | 93.  If all rows have
+// the same one of them, widen_kernel is faster: 64 rows 34 | 30, 256 86 | 53, 2,048 567 | 231 (10,240
+// columns: 20 | 20, 24 | 22, 66 | 48).  So
 // for more than kFewAlone rows the plan chooses and both are launched, one of them without work.
 bool use_few(int64_t rows, int n) { return rows <= int64_t{kFewMean} * n; }
 

@@ -149,7 +149,6 @@ struct Sorted {
   int32_t* keys;
   int32_t* pos;
   float* part;      // [segments][2][H]: sums that began before the segment, and that go on after it
-  int n;            // sorted ids, `live` of them inside the table
   int segments;
   int filled;       // rows of d_weight that are zero already, a multiple of kFillRows
 };
@@ -460,7 +459,6 @@ cudaError_t launch_embed_bwd(const EmbedBwd& call, cudaStream_t s) {
     z.keys = reinterpret_cast<int32_t*>(p + 256);
     z.pos = reinterpret_cast<int32_t*>(p + 256 + round_up(4 * static_cast<size_t>(n)));
     z.part = reinterpret_cast<float*>(p + 256 + 2 * round_up(4 * static_cast<size_t>(n)));
-    z.n = n;
     z.segments = (n + seg - 1) / seg;
     // what the GPU writes while one cluster sorts
     const size_t row = (a.d_type == kF32 ? 4 : 2) * static_cast<size_t>(a.H);

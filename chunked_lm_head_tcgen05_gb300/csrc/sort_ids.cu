@@ -9,8 +9,8 @@
 // over the warp's lanes, and the warp's own counts from earlier rounds), in
 // earlier warps and in earlier CTAs; counts are sums of integers, so the order is
 // the same in every run.
-// Bound by latency and by the stores into other CTAs: two passes take 28 us for 60,000
-// ids and 5 for 4,096.
+// Bound by latency and by the stores into other CTAs: two passes take 26 us for 60,000
+// ids and 12 for 4,096 that come from HBM, one pass over 2,048 ids 6.
 #include "operators.h"
 #include "ptx.cuh"
 

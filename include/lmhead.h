@@ -593,7 +593,8 @@ lmhead_status lmhead_embedding_bwd(const void* dy, int dy_type, int64_t dy_ld, c
  * base), nor with one another (LMHEAD_ERR_INVALID_ARG); columns of one tensor beside each
  * other do not.
  * Sums are fp32 in a fixed order (same inputs, same bits); u and du are used with all
- * their bits, in sums for 16-bit results with 16 of them; results are rounded once.
+ * their bits, in sums for 16-bit results with 16 of them or all (as the whole batch's ids
+ * have it, so that a row's last bit may depend on the other rows); results are rounded once.
  * Infinities and NaN in base, x, scale and grad_out go through as in the formulas, so those
  * of one row change its own results and its adapter's gradients.  The factors are taken to
  * be finite.  1 <= rank <= 128, n_adapters <= 65535, T < 2^31 - 256,
