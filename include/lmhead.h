@@ -631,7 +631,7 @@ lmhead_status lmhead_adapters_bwd(const void* grad_out, int type, int64_t grad_l
  * are compared in 64 bits, ties go to the lowest j, then to the larger logit (two logits may
  * share a score at a large temperature), then to the lowest v.  lse comes from fp32
  * exponentials and sums (as a rule within 1e-7 of the real one, within 1e-5 for V up to
- * 2^20): it does not touch the order within a beam, but candidates of different beams that
+ * 2^18): it does not touch the order within a beam, but candidates of different beams that
  * are closer than that may change places, those of equal rows too where the rows start at
  * different distances from a 16-byte boundary.
  *  finished      [R] uint8 or NULL: nonzero for a sequence that has ended.  Its logits are
